@@ -1,0 +1,337 @@
+// Append to a paged store: keys turned by RoPE at their positions and values into the pages of
+// their rows, queries turned beside them, and the key bounds of the pages kept.
+//
+// HBM-bound for prompts (each input read once, each output written once), latency-bound for a
+// decode step's few tokens.  A block takes one run: the new tokens of one row that fall into one
+// page, so the row, the page number and the bounds are dealt with once per page.  A lane owns two
+// 16-byte vectors of a token's row, D/2 apart in one head: both halves of the pairs (x[j],
+// x[j + D/2]), or two vectors of pairs (x[2j], x[2j+1]).  Warps of a block share its columns out
+// and take every kth token of the run, kUnroll tokens loaded before any is stored.  A run's keys,
+// after rounding, give the page's maximum and minimum in registers: no second pass, no atomics.
+#include "paged_internal.h"
+#include "paged_rope.h"
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnroll = 2;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float& y, float x) { y = x; }
+__device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn(x); }
+__device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ float pick_max(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ __half pick_max(__half a, __half b) { return __hmax(a, b); }
+__device__ __forceinline__ __nv_bfloat16 pick_max(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmax(a, b); }
+__device__ __forceinline__ float pick_min(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ __half pick_min(__half a, __half b) { return __hmin(a, b); }
+__device__ __forceinline__ __nv_bfloat16 pick_min(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmin(a, b); }
+
+template <typename T>
+union Vec {
+  static constexpr int N = 16 / sizeof(T);
+  uint4 u;
+  T e[16 / sizeof(T)];
+  __device__ Vec() {}
+};
+
+struct AppendArgs {
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* cu;
+  int32_t* err;
+  const float2* rope;
+  int rope_positions;
+  int B, n_tokens, ps_log2, n_pages, max_pages;
+  int runs, groups_y;         // run blocks (behind them: query blocks), column groups per block
+  int64_t kv_stride, q_stride;
+  int kv_cols, q_cols;        // vector pairs of a key / query row
+  int H, Hkv;
+  int half;
+};
+
+// Turns the two vectors x (elements c VL ..) and y (D/2 further) of a head by the row `cs` of the table.
+template <typename T, int D>
+__device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const float2* cs, int c, bool half) {
+  constexpr int VL = Vec<T>::N;
+  const T* type = nullptr;
+  if (half) {
+#pragma unroll
+    for (int i = 0; i < VL; ++i) {
+      const float2 t = __ldg(cs + c * VL + i);
+      const float a = to_f(x.e[i]), b = to_f(y.e[i]);
+      from_f(x.e[i], pg_rot(a, t.x, b, t.y, type));
+      from_f(y.e[i], pg_rot(a, t.y, b, -t.x, type));
+    }
+  } else {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      Vec<T>& z = w ? y : x;
+#pragma unroll
+      for (int i = 0; i < VL; i += 2) {
+        const float2 t = __ldg(cs + (w * (D / 2) + c * VL + i) / 2);
+        const float a = to_f(z.e[i]), b = to_f(z.e[i + 1]);
+        from_f(z.e[i], pg_rot(a, t.x, b, t.y, type));
+        from_f(z.e[i + 1], pg_rot(a, t.y, b, -t.x, type));
+      }
+    }
+  }
+}
+
+// Row b's tokens and length, checked (the error bits are set by the first block alone).
+struct Row {
+  int t0, n, len;
+  bool ok;
+};
+__device__ __forceinline__ Row row_of(const AppendArgs& a, int b) {
+  Row r;
+  if (a.cu == nullptr) {
+    r.n = a.n_tokens / a.B;
+    r.t0 = b * r.n;
+    r.ok = true;
+  } else {
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    r.t0 = lo;
+    r.n = hi - lo;
+    r.ok = lo >= 0 && hi >= lo && hi <= a.n_tokens;
+  }
+  r.len = a.kv_len[b];
+  const bool len_ok = r.len >= 0 && r.len <= (a.max_pages << a.ps_log2) && (!r.ok || r.len >= r.n);
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (!r.ok) atomicOr(a.err, KVC_DEV_BAD_CUSEQ);
+    if (!len_ok) atomicOr(a.err, KVC_DEV_BAD_KVLEN);
+  }
+  r.ok = r.ok && len_ok;
+  return r;
+}
+
+// The last b in [0, B) with f(b) <= x, by a whole warp: 32 probes a step.
+template <typename F>
+__device__ __forceinline__ int search(int B, long long x, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+#pragma unroll 1
+  for (int step = 0; step < 3 && n > 1; ++step) {
+    const int w = (n + 31) / 32;
+    const int b = lo + lane * w;
+    const unsigned hit = __ballot_sync(0xffffffffu, lane * w < n && f(b) <= x);
+    const int last = hit ? 31 - __clz(hit) : 0;
+    lo += last * w;
+    n = min(w, n - last * w);
+  }
+  return lo;
+}
+
+template <typename T, int D, bool kBounds>
+__global__ void __launch_bounds__(kThreads)
+k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
+               T* q_out, T* __restrict__ bounds, AppendArgs a) {
+  constexpr int VL = Vec<T>::N;
+  constexpr int PH = D / 2 / VL;          // vector pairs of a head
+  __shared__ uint4 s_red[kBounds ? kWarps : 1][4][32];
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ps = 1 << a.ps_log2;
+  if (blockIdx.x == 0 && blockIdx.y == 0)      // every row is checked once, whether or not a block comes to it
+    for (int b = threadIdx.x; b < a.B; b += kThreads) row_of(a, b);
+
+  if ((int)blockIdx.x >= a.runs) {
+    // ---- queries: one warp per token and 32 vector pairs ----
+    const int groups = (a.q_cols + 31) / 32;
+    const long long n_warps = (long long)(gridDim.x - a.runs) * gridDim.y * kWarps;
+    const long long first = ((long long)(blockIdx.x - a.runs) * gridDim.y + blockIdx.y) * kWarps + warp;
+    for (long long e = first; e < (long long)a.n_tokens * groups; e += n_warps) {
+      const int t = (int)(e / groups), col = (int)(e % groups) * 32 + lane;
+      const int b = a.cu == nullptr ? t / (a.n_tokens / a.B) : search(a.B, t, [&](int i) { return (long long)a.cu[i]; });
+      const Row r = row_of(a, b);
+      if (!r.ok || t < r.t0 || t >= r.t0 + r.n) continue;
+      const int pos = r.len - r.n + (t - r.t0);
+      if (pos >= a.rope_positions) {
+        if (lane == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
+        continue;
+      }
+      if (col >= a.q_cols) continue;
+      const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
+      const T* src = q + (int64_t)t * a.q_stride + off;
+      Vec<T> x, y;
+      x.u = *reinterpret_cast<const uint4*>(src);
+      y.u = *reinterpret_cast<const uint4*>(src + D / 2);
+      turn<T, D>(x, y, a.rope + (int64_t)pos * (D / 2), col % PH, a.half);
+      T* dst = q_out + (int64_t)t * a.H * D + off;
+      *reinterpret_cast<uint4*>(dst) = x.u;
+      *reinterpret_cast<uint4*>(dst + D / 2) = y.u;
+    }
+    return;
+  }
+
+  // ---- keys and values: the run of this block ----
+  // Runs are numbered with room to spare: row b's start at cu[b] / page_size + 2 b, which leaves each
+  // row at least as many numbers as its tokens can touch pages.
+  int b, j;
+  if (a.cu == nullptr) {
+    const int most = (a.n_tokens / a.B + ps - 2) / ps + 1;
+    b = blockIdx.x / most;
+    j = blockIdx.x % most;
+  } else {
+    auto start = [&](int i) { return (long long)(a.cu[i] >> a.ps_log2) + 2 * i; };
+    b = search(a.B, blockIdx.x, start);
+    const long long jj = (long long)blockIdx.x - start(b);
+    if (jj < 0 || jj > a.max_pages) return;
+    j = (int)jj;
+  }
+  const Row r = row_of(a, b);
+  if (!r.ok || r.n == 0) return;
+  const int p0 = r.len - r.n;                       // position of the row's first new token
+  const int column = (p0 >> a.ps_log2) + j;
+  const int lo = max(p0, column << a.ps_log2), hi = min(r.len, (column + 1) << a.ps_log2);
+  if (lo >= hi) return;
+  const int page = a.table[(int64_t)b * a.max_pages + column];
+  if (page < 0 || page >= a.n_pages) {
+    if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+    return;
+  }
+  const int end = a.rope != nullptr ? min(hi, a.rope_positions) : hi;
+  if (end < hi && threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
+  const int gw = a.groups_y;                        // column groups this block's warps divide into
+  const int col = ((int)blockIdx.y * gw + warp % gw) * 32 + lane;
+  const int stride = kWarps / gw;
+  const bool have = col < a.kv_cols;
+  const int head = have ? col / PH : 0, c = have ? col % PH : 0;
+  const int64_t src0 = (int64_t)head * D + c * VL;
+  const int64_t dst_row = (int64_t)a.Hkv * D;
+  Vec<T> mx0, mx1, mn0, mn1;
+  bool any = false;
+  if (have) {
+    for (int p = lo + warp / gw; p < end; p += stride * kUnroll) {
+      Vec<T> x[kUnroll], y[kUnroll], vx[kUnroll], vy[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int pp = p + u * stride;
+        if (pp >= end) continue;
+        const int64_t off = (int64_t)(r.t0 + pp - p0) * a.kv_stride + src0;
+        x[u].u = __ldg(reinterpret_cast<const uint4*>(k + off));
+        y[u].u = __ldg(reinterpret_cast<const uint4*>(k + off + D / 2));
+        vx[u].u = __ldg(reinterpret_cast<const uint4*>(v + off));
+        vy[u].u = __ldg(reinterpret_cast<const uint4*>(v + off + D / 2));
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int pp = p + u * stride;
+        if (pp >= end) continue;
+        const int64_t dst = (((int64_t)page << a.ps_log2) + (pp & (ps - 1))) * dst_row + src0;
+        *reinterpret_cast<uint4*>(vp + dst) = vx[u].u;
+        *reinterpret_cast<uint4*>(vp + dst + D / 2) = vy[u].u;
+        if (a.rope != nullptr) turn<T, D>(x[u], y[u], a.rope + (int64_t)pp * (D / 2), c, a.half);
+        *reinterpret_cast<uint4*>(kp + dst) = x[u].u;
+        *reinterpret_cast<uint4*>(kp + dst + D / 2) = y[u].u;
+        if (kBounds) {
+          if (!any) {
+            mx0.u = mn0.u = x[u].u;
+            mx1.u = mn1.u = y[u].u;
+            any = true;
+          } else {
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+              mx0.e[i] = pick_max(mx0.e[i], x[u].e[i]);
+              mn0.e[i] = pick_min(mn0.e[i], x[u].e[i]);
+              mx1.e[i] = pick_max(mx1.e[i], y[u].e[i]);
+              mn1.e[i] = pick_min(mn1.e[i], y[u].e[i]);
+            }
+          }
+        }
+      }
+    }
+  }
+  if (!kBounds || end <= lo) return;                // (uniform per block)
+  // warps of the same columns, then what the page held before
+  s_red[warp][0][lane] = mx0.u;
+  s_red[warp][1][lane] = mx1.u;
+  s_red[warp][2][lane] = mn0.u;
+  s_red[warp][3][lane] = mn1.u;
+  __syncthreads();
+  if (warp >= gw || !have) return;                  // the warp of the run's first token has one for sure
+  auto widen = [&](const uint4& a0, const uint4& a1, const uint4& i0, const uint4& i1) {
+    Vec<T> u0, u1, w0, w1;
+    u0.u = a0;
+    u1.u = a1;
+    w0.u = i0;
+    w1.u = i1;
+#pragma unroll
+    for (int i = 0; i < VL; ++i) {
+      mx0.e[i] = pick_max(mx0.e[i], u0.e[i]);
+      mx1.e[i] = pick_max(mx1.e[i], u1.e[i]);
+      mn0.e[i] = pick_min(mn0.e[i], w0.e[i]);
+      mn1.e[i] = pick_min(mn1.e[i], w1.e[i]);
+    }
+  };
+  for (int w = warp + gw, t = 1; t < stride; w += gw, ++t)
+    if (lo + t < end) widen(s_red[w][0][lane], s_red[w][1][lane], s_red[w][2][lane], s_red[w][3][lane]);
+  T* bd = bounds + (((int64_t)page * a.Hkv + head) * 2) * D + c * VL;
+  if (lo & (ps - 1))
+    widen(*reinterpret_cast<const uint4*>(bd), *reinterpret_cast<const uint4*>(bd + D / 2),
+          *reinterpret_cast<const uint4*>(bd + D), *reinterpret_cast<const uint4*>(bd + D + D / 2));
+  *reinterpret_cast<uint4*>(bd) = mx0.u;
+  *reinterpret_cast<uint4*>(bd + D / 2) = mx1.u;
+  *reinterpret_cast<uint4*>(bd + D) = mn0.u;
+  *reinterpret_cast<uint4*>(bd + D + D / 2) = mn1.u;
+}
+
+template <typename T, int D>
+cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, void* q_out, AppendArgs a,
+                   cudaStream_t s) {
+  constexpr int VL = Vec<T>::N;
+  a.kv_cols = a.Hkv * (D / 2 / VL);
+  a.q_cols = q != nullptr ? a.H * (D / 2 / VL) : 0;
+  // warps of a block over column groups of 32 vector pairs: 1, 2, 4 or 8 of them, the rest over tokens
+  const int groups = (a.kv_cols + 31) / 32;
+  a.groups_y = groups >= 8 ? 8 : groups >= 4 ? 4 : groups >= 2 ? 2 : 1;
+  const int gy = (groups + a.groups_y - 1) / a.groups_y;
+  const int ps = 1 << a.ps_log2;
+  const int64_t runs = a.cu == nullptr ? (int64_t)a.B * ((a.n_tokens / a.B + ps - 2) / ps + 1)
+                                       : (int64_t)a.n_tokens / ps + 2 * (int64_t)a.B;
+  const int64_t q_warps = (int64_t)a.n_tokens * ((a.q_cols + 31) / 32);
+  int64_t q_blocks = (q_warps + (int64_t)kWarps * gy - 1) / ((int64_t)kWarps * gy);
+  if (q_blocks > 16 * KVC_PG_GRID) q_blocks = 16 * KVC_PG_GRID;
+  a.runs = (int)runs;
+  const dim3 grid((unsigned)(runs + q_blocks), gy);
+  if (c->bounds != nullptr)
+    return kvc_launch_pdl(k_paged_append<T, D, true>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
+                          (T*)c->k, (T*)c->v, (T*)q_out, (T*)c->bounds, a);
+  return kvc_launch_pdl(k_paged_append<T, D, false>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
+                        (T*)c->k, (T*)c->v, (T*)q_out, (T*)nullptr, a);
+}
+
+}  // namespace
+
+cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stride, const void* q,
+                                 int64_t q_stride, void* q_out, int n_tokens, const int32_t* cu, const float* rope,
+                                 int rope_positions, bool half, cudaStream_t s) {
+  const kvc_paged_config& g = c->cfg;
+  AppendArgs a{};
+  a.table = c->table;
+  a.kv_len = c->kv_len;
+  a.cu = cu;
+  a.err = reinterpret_cast<int32_t*>(c->ws);
+  a.rope = reinterpret_cast<const float2*>(rope);
+  a.rope_positions = rope_positions;
+  a.B = g.batch;
+  a.n_tokens = n_tokens;
+  a.ps_log2 = c->ps_log2;
+  a.n_pages = g.n_pages;
+  a.max_pages = g.max_pages;
+  a.kv_stride = kv_stride;
+  a.q_stride = q_stride;
+  a.H = g.heads;
+  a.Hkv = g.kv_heads;
+  a.half = half;
+  const bool d64 = g.head_dim == 64;
+  switch (g.dtype) {
+    case KVC_F32: return d64 ? launch<float, 64>(c, k, v, q, q_out, a, s) : launch<float, 128>(c, k, v, q, q_out, a, s);
+    case KVC_F16: return d64 ? launch<__half, 64>(c, k, v, q, q_out, a, s) : launch<__half, 128>(c, k, v, q, q_out, a, s);
+    default:
+      return d64 ? launch<__nv_bfloat16, 64>(c, k, v, q, q_out, a, s) : launch<__nv_bfloat16, 128>(c, k, v, q, q_out, a, s);
+  }
+}

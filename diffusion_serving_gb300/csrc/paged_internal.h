@@ -1,0 +1,363 @@
+// Internal declarations of the paged cache: the handle, the rows of a call as the kernels
+// see them, and how the attention kernels share work among blocks.
+#pragma once
+
+#include "../../include/kvc_paged.h"
+#include "kvc_internal.h"
+
+// Blocks of the attention kernels' grids (one per SM of a 152-SM GB300; two for the FMA
+// kernel).  Constants, so that workspace sizes do not depend on the device queried; no
+// block waits for another, so a device with fewer SMs runs them in turn.
+#define KVC_PG_GRID 152
+#define KVC_PG_GRID_SIMT 304
+#define KVC_PG_MAX_BATCH 1024
+#define KVC_PG_MAX_SCORED 32768   // pages per row that kvc_paged_attend_sparse can rank
+
+struct kvc_paged {
+  kvc_paged_config cfg;
+  int ps_log2;
+  int sub;              // a kv head's group is taken as `sub` groups of Gv <= 16 heads
+  int Gv, Hv;           // heads per (virtual) group, groups: Gv * Hv = H, Hv = Hkv * sub
+  float scale;
+  void* k;
+  void* v;
+  void* bounds;
+  const int32_t* table;
+  const int32_t* kv_len;
+  uint8_t* ws;
+  int device;
+  uint64_t debug_stall_ns;
+  CUtensorMap tm_k, tm_v;   // pages as boxes of 64 dims x 1 head x min(page_size, 64) slots (16-bit stores)
+};
+
+// Workspace, in bytes from its start.
+struct kvc_pg_layout {
+  size_t tickets;       // int32 per block: blocks that have left their part of a split item
+  size_t score_max;     // fp32 per (row, kv head): bound of a score's terms
+  size_t zeroed;        // end of what has to start at zero (and is left at zero)
+  size_t parts;         // split partials
+  size_t prefix;        // partials of a shared prefix
+  size_t scores;        // fp32 [batch, Hkv, max_pages]
+  size_t total;
+};
+kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& cfg);
+
+// What a launch is told.  `phase`: 0 attends a row's slots; 1 the shared prefix (one row of all
+// tokens, partials only); 2 the slots behind the prefix, joined with phase 1's partials.
+struct kvc_pg_args {
+  int B, H, Hkv, Hv, Gv, sub;
+  int ps_log2, n_pages, max_pages;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* cu;
+  int n_tokens, max_q;
+  int causal, phase;
+  float scale_log2;
+  float* lse;
+  int32_t* err;
+  const int32_t* prefix_pages;
+  const int32_t* prefix_len;
+  int prefix_cap;             // pages of the shared list
+  const int32_t* sel;         // [B, Hkv, n_sel] table columns to attend, ascending, -1 behind the last
+  int n_sel;
+  float* part;                // [2 * grid][R][D + 2]: O (unnormalised), then (max, sum) per row
+  int* tickets;
+  float* pre;                 // phase 1's partials [items + blocks][pre_rows][D + 2]
+  int pre_rows, pre_tile, pre_grid;
+  uint64_t stall_ns;
+};
+
+kvc_pg_args kvc_pg_base_args(const kvc_paged* c);
+
+// ---- launchers ----------------------------------------------------------------------
+cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stride, const void* q,
+                                 int64_t q_stride, void* q_out, int n_tokens, const int32_t* cu, const float* rope,
+                                 int rope_positions, bool half, cudaStream_t s);
+cudaError_t kvc_pg_launch_simt(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
+cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int first, int recent, int32_t* sel,
+                                 cudaStream_t s);
+// partial rows per item and slots per tile of the FMA kernel
+#define KVC_PG_SIMT_ROWS 16
+#define KVC_PG_SIMT_TILE 64
+
+#ifdef __CUDACC__
+// ---- rows of a call -------------------------------------------------------------------
+// Row b: tokens [t0, t0 + n) of the call, keys at positions [lo, len) (`len` counts virtual slots
+// of the selected pages when pages are selected).  n = 0 for a row that is skipped.
+struct kvc_pg_row {
+  int t0, n, len, lo;
+};
+
+// The shared prefix's length; -1 (with the error bit) where it is not one.
+__device__ __forceinline__ int pg_prefix_len(const kvc_pg_args& a) {
+  const int p = *a.prefix_len;
+  if (p < 0 || (p & ((1 << a.ps_log2) - 1)) || (p >> a.ps_log2) > a.prefix_cap) {
+    atomicOr(a.err, KVC_DEV_BAD_KVLEN);
+    return -1;
+  }
+  return p;
+}
+
+// Tokens of row b, checked: false for a bad offset.
+__device__ __forceinline__ bool pg_tokens(const kvc_pg_args& a, int b, int* t0, int* n) {
+  if (a.cu == nullptr) {
+    *n = a.n_tokens / a.B;
+    *t0 = b * *n;
+    return true;
+  }
+  const int lo = a.cu[b], hi = a.cu[b + 1];
+  *t0 = lo;
+  *n = hi - lo;
+  if (lo < 0 || hi < lo || hi > a.n_tokens || hi - lo > a.max_q) {
+    atomicOr(a.err, KVC_DEV_BAD_CUSEQ);
+    return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ int pg_len(const kvc_pg_args& a, int b) {
+  const int len = a.kv_len[b];
+  if (len < 0 || len > (a.max_pages << a.ps_log2)) {
+    atomicOr(a.err, KVC_DEV_BAD_KVLEN);
+    return -1;
+  }
+  return len;
+}
+
+__device__ __forceinline__ kvc_pg_row pg_row(const kvc_pg_args& a, int b) {
+  kvc_pg_row r{0, 0, 0, 0};
+  if (a.phase == 1) {
+    const int p = pg_prefix_len(a);
+    if (p > 0) r = kvc_pg_row{0, a.n_tokens, p, 0};
+    return r;
+  }
+  int t0, n;
+  const bool ok = pg_tokens(a, b, &t0, &n);
+  const int len = pg_len(a, b);
+  if (!ok || len < 0) return r;
+  r = kvc_pg_row{t0, n, len, 0};
+  if (a.phase == 2) {
+    const int p = pg_prefix_len(a);
+    if (p < 0) return kvc_pg_row{0, 0, 0, 0};
+    r.lo = min(p, len);
+  } else if (a.sel != nullptr) {
+    const int pages = (len + (1 << a.ps_log2) - 1) >> a.ps_log2;
+    r.len = min(pages, a.n_sel) << a.ps_log2;
+  }
+  return r;
+}
+
+// Position behind the last one that token i of row b sees (plain rows; not phase 1).
+__device__ __forceinline__ int pg_limit(const kvc_pg_args& a, const kvc_pg_row& r, int i) {
+  return a.causal ? r.len - r.n + i + 1 : r.len;
+}
+
+// The row that token t of the call belongs to, or -1: binary search in cu, which need not be in
+// order for it to end.
+__device__ __forceinline__ int pg_row_of(const kvc_pg_args& a, int t) {
+  if (a.cu == nullptr) return t / (a.n_tokens / a.B);
+  int lo = 0, hi = a.B;   // the last b with cu[b] <= t
+#pragma unroll 1
+  for (int step = 0; step < 11 && hi - lo > 1; ++step) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return t >= a.cu[lo] && t < a.cu[lo + 1] ? lo : -1;
+}
+
+// Phase 1: how far into the prefix token t of the call sees (0 for a token of no valid row).
+__device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int prefix) {
+  const int b = pg_row_of(a, t);
+  if (b < 0) return 0;
+  int t0, n;
+  const bool ok = pg_tokens(a, b, &t0, &n);
+  const int len = pg_len(a, b);
+  if (!ok || len < 0) return 0;
+  return max(0, min(prefix, a.causal ? len - n + (t - t0) + 1 : len));
+}
+
+// ---- work ------------------------------------------------------------------------------
+// An item is the R query rows (T = R / Gv tokens x Gv heads) of one (row, group) and token tile;
+// it takes tiles of TS slots, at least one (an item without keys still writes its output).
+// All items' tiles stand in one line, rows outermost, then groups, then token tiles; block c
+// takes the tiles [c * per, (c + 1) * per) of that line, so every block streams the same amount
+// whatever the rows' lengths, and an item that spans several blocks is joined from their
+// partials.  Rows' totals are summed up in shared memory by every block.
+//
+// Tiles of token tile k of a row: ceil(min(a + (k + 1) T, len) - lo / TS), a = len - n, where
+// queries are causal; the same for every k otherwise.
+__device__ __forceinline__ int pg_item_tiles(const kvc_pg_row& r, int k, int T, int TS, bool causal) {
+  const int end = causal ? min(r.len, r.len - r.n + min((k + 1) * T, r.n)) : r.len;
+  const int keys = end - r.lo;
+  return keys > TS ? (keys + TS - 1) / TS : 1;
+}
+
+// sum over i in [0, n) of floor((A i + B) / M), A, B >= 0: the lattice points under a line, by the
+// Euclidean recursion (swap axes, reduce).
+__device__ __forceinline__ long long pg_floor_sum(long long n, long long M, long long A, long long B) {
+  long long s = 0;
+#pragma unroll 1
+  for (int step = 0; step < 64 && n > 0; ++step) {
+    s += (A / M) * (n * (n - 1) / 2) + (B / M) * n;
+    A %= M;
+    B %= M;
+    const long long y = A * n + B;
+    if (y < M) break;
+    n = y / M;
+    B = y % M;
+    const long long t = M;
+    M = A;
+    A = t;
+  }
+  return s;
+}
+
+// Tiles of the row's token tiles [0, m).
+__device__ __forceinline__ long long pg_row_tiles(const kvc_pg_row& r, int m, int T, int TS, bool causal) {
+  if (m <= 0) return 0;
+  if (!causal) return (long long)m * pg_item_tiles(r, 0, T, TS, false);
+  const int all = (r.n + T - 1) / T;
+  long long s = 0;
+  int last = m;
+  if (m == all) {                        // the last token tile may be cut short
+    s = pg_item_tiles(r, all - 1, T, TS, true);
+    last = all - 1;
+  }
+  // tile k ends at x_k = a + (k + 1) T; up to TS it takes one tile
+  const long long a = (long long)r.len - r.n - r.lo;
+  long long one = TS - a >= T ? (TS - a) / T : 0;
+  if (one > last) one = last;
+  return s + one + pg_floor_sum(last - one, TS, T, a + (one + 1) * T + TS - 1);
+}
+
+struct kvc_pg_item {
+  int b, vh, k;          // row, group, token tile
+  int tiles;
+  long long start;       // its first tile on the line
+  kvc_pg_row r;
+};
+
+// Shared memory of the sums: (rows + 1) x 8 bytes, then rows x 16.
+__host__ __device__ inline size_t pg_sched_bytes(int B) { return (((size_t)(B + 1) * 8 + 15) & ~(size_t)15) + (size_t)B * 16; }
+
+template <int R, int TS>
+struct kvc_pg_sched {
+  long long* base;       // [rows + 1] first tile of each row
+  kvc_pg_row* rows;
+  int n_rows, T;
+  bool causal;
+  long long total, per;
+
+  // Every thread of the block calls it (it holds barriers).
+  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles) {
+    n_rows = a.phase == 1 ? 1 : a.B;
+    T = R / a.Gv;
+    causal = a.causal && a.phase != 1 && a.sel == nullptr;
+    base = reinterpret_cast<long long*>(smem);
+    rows = reinterpret_cast<kvc_pg_row*>(reinterpret_cast<uint8_t*>(smem) + (((size_t)(n_rows + 1) * 8 + 15) & ~(size_t)15));
+    for (int b = threadIdx.x; b < n_rows; b += blockDim.x) {
+      const kvc_pg_row r = pg_row(a, b);
+      rows[b] = r;
+      base[b + 1] = a.Hv * pg_row_tiles(r, (r.n + T - 1) / T, T, TS, causal);
+    }
+    if (threadIdx.x == 0) base[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      long long carry = 0;
+      for (int b0 = 0; b0 < n_rows; b0 += 32) {
+        const int b = b0 + threadIdx.x;
+        long long x = b < n_rows ? base[b + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if ((int)threadIdx.x >= o) x += y;
+        }
+        if (b < n_rows) base[b + 1] = carry + x;
+        carry += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    __syncthreads();
+    total = base[n_rows];
+    per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < min_tiles) per = min_tiles;
+  }
+
+  // The item that holds tile p of the line (p < total).
+  __device__ __forceinline__ kvc_pg_item at(const kvc_pg_args& a, long long p) const {
+    kvc_pg_item it;
+    int lo = 0, hi = n_rows;
+#pragma unroll 1
+    for (int step = 0; step < 11 && hi - lo > 1; ++step) {
+      const int mid = (lo + hi) >> 1;
+      if (base[mid] <= p) lo = mid;
+      else hi = mid;
+    }
+    it.b = lo;
+    it.r = rows[lo];
+    const long long per_group = (base[lo + 1] - base[lo]) / a.Hv;
+    p -= base[lo];
+    it.vh = (int)(p / per_group);
+    p -= it.vh * per_group;
+    int kl = 0, kh = (it.r.n + T - 1) / T;
+#pragma unroll 1
+    for (int step = 0; step < 32 && kh - kl > 1; ++step) {
+      const int mid = (kl + kh) >> 1;
+      if (pg_row_tiles(it.r, mid, T, TS, causal) <= p) kl = mid;
+      else kh = mid;
+    }
+    it.k = kl;
+    it.tiles = pg_item_tiles(it.r, kl, T, TS, causal);
+    it.start = base[lo] + it.vh * per_group + pg_row_tiles(it.r, kl, T, TS, causal);
+    return it;
+  }
+
+  // The item behind `it` (there is one).
+  __device__ __forceinline__ void next(const kvc_pg_args& a, kvc_pg_item& it) const {
+    it.start += it.tiles;
+    if ((it.k + 1) * T < it.r.n) {
+      ++it.k;
+    } else {
+      it.k = 0;
+      if (++it.vh == a.Hv) {
+        it.vh = 0;
+        ++it.b;
+        for (; it.b + 1 < n_rows && base[it.b + 1] == it.start; ++it.b) {
+        }
+        it.r = rows[it.b];
+      }
+    }
+    it.tiles = pg_item_tiles(it.r, it.k, T, TS, causal);
+  }
+};
+
+// Page number of table column `col` of row b (phase 1: of the shared list), or -1 with the error bit.
+__device__ __forceinline__ int pg_page(const kvc_pg_args& a, int b, int col) {
+  const int p = a.phase == 1 ? __ldg(a.prefix_pages + col) : __ldg(a.table + (int64_t)b * a.max_pages + col);
+  if (p < 0 || p >= a.n_pages) {
+    atomicOr(a.err, KVC_DEV_BAD_PAGE);
+    return -1;
+  }
+  return p;
+}
+
+// ---- partials of a shared prefix --------------------------------------------------------
+// Phase 1's items all have the same number of tiles, so which blocks held a token's prefix, and
+// where they left their partials, follows from the prefix length: item i's part of block c stands
+// in slot i + c (item boundaries and block boundaries both only move forward, so no two collide).
+struct kvc_pg_prefix_parts {
+  int first, count;      // slots
+  int row;               // row within a slot
+};
+__device__ __forceinline__ kvc_pg_prefix_parts pg_prefix_parts(const kvc_pg_args& a, int prefix, int t, int vh, int g) {
+  const int T = a.pre_rows / a.Gv;
+  const int m = (a.n_tokens + T - 1) / T;
+  const long long tiles = prefix > a.pre_tile ? (prefix + a.pre_tile - 1) / a.pre_tile : 1;
+  const long long total = tiles * m * a.Hv;
+  long long per = (total + a.pre_grid - 1) / a.pre_grid;
+  const int item = vh * m + t / T;
+  const long long s = item * tiles;
+  const int c0 = (int)(s / per), c1 = (int)((s + tiles - 1) / per);
+  return {item + c0, c1 - c0 + 1, (t % T) * a.Gv + g};
+}
+#endif  // __CUDACC__

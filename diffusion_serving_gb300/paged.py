@@ -1,0 +1,296 @@
+"""Python binding of the paged cache (include/kvc_paged.h): argument marshalling only.
+
+The functions carry the C names and take torch tensors and torch CUDA streams, as those of
+``kvc`` do, and raise ``kvc.KvcError`` on a non-zero return code.  ``PagedKVCache`` bundles a
+handle with its buffers:
+
+    cache = paged.PagedKVCache(batch, 32, 8, 128, torch.bfloat16, page_size=16, n_pages=4096, max_pages=256)
+    cache.block_table[b, :n] = pages          # the caller's allotment
+    cache.kv_len += new                       # tokens of each row, the new ones included
+    cache.append(k, v, rope=table, q=q, q_out=q)
+    out = cache.attend(q)
+    assert cache.get_error() == 0
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+
+import torch
+
+from . import kvc
+from .kvc import (BF16, CAUSAL, CODE_DTYPE, DEV_BAD_CUSEQ, DEV_BAD_KVLEN, DEV_BAD_POS, DEV_TIMEOUT,  # noqa: F401
+                  DTYPE_CODE, ERR_ARG, ERR_CUDA, ERR_DEVICE, ERR_RANGE, ERR_UNSUPPORTED, F16, F32, KERNEL_SIMT, OK,
+                  KvcError)
+
+HEADER_PATH = os.path.join(os.path.dirname(kvc.HEADER_PATH), "kvc_paged.h")
+DEV_BAD_PAGE = 128
+ROPE_HALF = 1
+
+
+class kvc_paged_config(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float)]
+
+
+def _bind():
+    P, I32, I64, U32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
+    cfgp = ctypes.POINTER(kvc_paged_config)
+    sig = {
+        "kvc_paged_workspace_bytes": (SZ, [cfgp]),
+        "kvc_paged_create": (ctypes.c_int, [cfgp, P, P, P, P, P, P, P, ctypes.POINTER(P)]),
+        "kvc_paged_append": (ctypes.c_int, [P, P, P, I64, P, I64, P, I32, P, P, I32, U32, P]),
+        "kvc_paged_attend": (ctypes.c_int, [P, P, P, P, I32, P, I32, U32, P]),
+        "kvc_paged_attend_shared": (ctypes.c_int, [P, P, P, P, I32, P, I32, P, I32, P, U32, P]),
+        "kvc_paged_attend_sparse": (ctypes.c_int, [P, P, P, P, I32, I32, I32, P, U32, P]),
+        "kvc_paged_get_error": (ctypes.c_int, [P, P, ctypes.POINTER(I32)]),
+        "kvc_paged_debug_stall_waits": (ctypes.c_int, [P, ctypes.c_uint64]),
+        "kvc_paged_destroy": (ctypes.c_int, [P]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(kvc._lib, name)
+        fn.restype, fn.argtypes = res, args
+
+
+_bind()
+_lib = kvc._lib
+
+
+def header_functions() -> list[str]:
+    """Names of the functions include/kvc_paged.h declares."""
+    with open(HEADER_PATH) as f:
+        return re.findall(r"^\s*(?:const\s+)?\w+\**\s+\**(kvc_\w+)\s*\(", f.read(), flags=re.M)
+
+
+def make_config(batch, heads, kv_heads, head_dim, dtype, *, page_size, n_pages, max_pages, max_tokens=0,
+                softmax_scale=0.0) -> kvc_paged_config:
+    d = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return kvc_paged_config(batch, heads, kv_heads, head_dim, page_size, n_pages, max_pages, max_tokens or batch, d,
+                            softmax_scale)
+
+
+def kvc_paged_workspace_bytes(cfg: kvc_paged_config) -> int:
+    return _lib.kvc_paged_workspace_bytes(ctypes.byref(cfg))
+
+
+def kvc_paged_create(cfg, k_pages, v_pages, bounds, table, kv_len, workspace, stream=None) -> int:
+    h = ctypes.c_void_p()
+    kvc._check(_lib.kvc_paged_create(ctypes.byref(cfg), kvc._ptr(k_pages), kvc._ptr(v_pages), kvc._ptr(bounds),
+                                     kvc._ptr(table), kvc._ptr(kv_len), kvc._ptr(workspace), kvc._stream(stream),
+                                     ctypes.byref(h)), "kvc_paged_create")
+    return h.value
+
+
+def kvc_paged_get_error(h: int, stream=None) -> int:
+    """The device error bits (0 if none), cleared."""
+    bits = ctypes.c_int32(0)
+    rc = _lib.kvc_paged_get_error(h, kvc._stream(stream), ctypes.byref(bits))
+    if rc not in (OK, ERR_DEVICE):
+        raise KvcError(rc, "kvc_paged_get_error")
+    return bits.value
+
+
+def kvc_paged_debug_stall_waits(h: int, ns: int) -> None:
+    kvc._check(_lib.kvc_paged_debug_stall_waits(h, ns), "kvc_paged_debug_stall_waits")
+
+
+def kvc_paged_destroy(h: int) -> None:
+    kvc._check(_lib.kvc_paged_destroy(h), "kvc_paged_destroy")
+
+
+def _dense(what, t, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"kvc: {what} must be a dense {list(shape)} {dtype} on {device}, got {list(t.shape)} {t.dtype} "
+                         f"on {t.device}" + ("" if t.is_contiguous() else ", strided"))
+    return t
+
+
+class PagedKVCache:
+    """A paged cache: pools of pages, each row's page numbers and length, and a handle over them.
+
+    ``k_pages`` / ``v_pages`` [n_pages, page_size, kv_heads, head_dim], ``block_table`` int32 [batch,
+    max_pages], ``kv_len`` int32 [batch] and ``bounds`` [n_pages, kv_heads, 2, head_dim] (True: allot
+    one; needed by ``attend_sparse``) may be given, so that layers, or handles on different streams,
+    share them.  Token rows of a call are packed ([total, heads, head_dim] with ``cu`` int32 [batch + 1]) or
+    even ([batch, n, heads, head_dim], or [batch * n, ...])."""
+
+    def __init__(self, batch, heads, kv_heads, head_dim, dtype, *, page_size, n_pages, max_pages, max_tokens=0,
+                 bounds=None, softmax_scale=0.0, k_pages=None, v_pages=None, block_table=None, kv_len=None,
+                 device="cuda", stream=None):
+        self.cfg = make_config(batch, heads, kv_heads, head_dim, dtype, page_size=page_size, n_pages=n_pages,
+                               max_pages=max_pages, max_tokens=max_tokens, softmax_scale=softmax_scale)
+        self.handle = None
+        wb = kvc_paged_workspace_bytes(self.cfg)
+        if wb == 0:
+            raise KvcError(ERR_ARG, "kvc_paged_workspace_bytes")
+        self.dtype = CODE_DTYPE[self.cfg.dtype]
+        self.batch, self.heads, self.kv_heads, self.head_dim = batch, heads, kv_heads, head_dim
+        device = torch.device(device)
+        if device.index is None:
+            device = torch.device(device.type, torch.cuda.current_device())
+        self.device = device
+        pool = (n_pages, page_size, kv_heads, head_dim)
+
+        def own(what, t, shape, dt, fill=None):
+            if t is not None:
+                return _dense(what, t, shape, dt, device)
+            return torch.empty(shape, dtype=dt, device=device) if fill is None else torch.full(shape, fill, dtype=dt, device=device)
+
+        self.k_pages = own("k_pages", k_pages, pool, self.dtype)
+        self.v_pages = own("v_pages", v_pages, pool, self.dtype)
+        self.block_table = own("block_table", block_table, (batch, max_pages), torch.int32, -1)
+        self.kv_len = own("kv_len", kv_len, (batch,), torch.int32, 0)
+        self.bounds = None
+        if bounds is not None and bounds is not False:
+            self.bounds = own("bounds", None if bounds is True else bounds, (n_pages, kv_heads, 2, head_dim), self.dtype, 0)
+        self.workspace = torch.empty(wb, dtype=torch.uint8, device=device)
+        with torch.cuda.device(device):
+            self.handle = kvc_paged_create(self.cfg, self.k_pages, self.v_pages, self.bounds, self.block_table,
+                                           self.kv_len, self.workspace, stream)
+
+    # -- arguments ----------------------------------------------------------------------
+    def _stream(self, stream):
+        """The stream's handle; without one, the current stream of the cache's device."""
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _call(self, what, fn, *args):
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                rc = fn(self.handle, *args)
+        else:
+            rc = fn(self.handle, *args)
+        if rc != OK:
+            raise KvcError(rc, what)
+
+    def _tokens(self, what, t, heads):
+        """The number of token rows of ``t``: [total, heads, D] or [batch, n, heads, D]."""
+        shape = t.shape
+        if t.dtype != self.dtype or t.device != self.device or len(shape) not in (3, 4) or shape[-2] != heads or \
+                shape[-1] != self.head_dim or (len(shape) == 4 and shape[0] != self.batch):
+            raise ValueError(f"kvc: {what} must be [tokens, {heads}, {self.head_dim}] or [{self.batch}, n, {heads}, "
+                             f"{self.head_dim}] {self.dtype} on {self.device}, got {list(shape)} {t.dtype} on {t.device}")
+        return shape[0] if len(shape) == 3 else shape[0] * shape[1]
+
+    def _rows(self, what, t, heads):
+        """(token rows, elements from one to the next) of ``t``, whose rows are dense and evenly apart."""
+        n = self._tokens(what, t, heads)
+        s = t.stride()
+        row = s[-3]
+        if s[-1] != 1 or s[-2] != self.head_dim or (len(s) == 4 and t.shape[0] > 1 and s[0] != t.shape[1] * row):
+            raise ValueError(f"kvc: {what}: a token's heads must be dense and its tokens evenly apart, got strides {list(s)}")
+        return n, max(row, heads * self.head_dim) if n == 1 else row
+
+    def _cu(self, cu):
+        if cu is None:
+            return None
+        if cu.dtype != torch.int32 or cu.numel() != self.batch + 1 or cu.device != self.device or not cu.is_contiguous():
+            raise ValueError(f"kvc: row offsets must be a dense int32 [{self.batch + 1}] on {self.device}")
+        return cu.data_ptr()
+
+    def _q(self, q, out, lse):
+        n = self._tokens("q", q, self.heads)
+        if not q.is_contiguous():
+            raise ValueError("kvc: q must be dense")
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+            raise ValueError(f"kvc: out must match q ({list(q.shape)} {q.dtype} on {q.device}, dense)")
+        if lse is True:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        elif lse is not None and (lse.shape != q.shape[:-1] or lse.dtype != torch.float32 or lse.device != q.device or
+                                  not lse.is_contiguous()):
+            raise ValueError(f"kvc: lse must be a dense float32 {list(q.shape[:-1])}")
+        return n, out, lse
+
+    # -- calls --------------------------------------------------------------------------
+    def append(self, k, v, *, cu_new=None, rope=None, half=False, q=None, q_out=None, stream=None):
+        """Store the new tokens' keys, turned by ``rope`` [positions, D/2, 2] fp32 at their positions
+        (``half``: pairs D/2 apart), and values; ``kv_len`` counts them already.  With ``q`` the queries
+        of the same tokens are turned into ``q_out`` (returned; allotted when None)."""
+        n, stride = self._rows("k", k, self.kv_heads)
+        nv, vstride = self._rows("v", v, self.kv_heads)
+        if n != nv or stride != vstride:
+            raise ValueError(f"kvc: k and v must have the same rows and strides ({n}, {stride} and {nv}, {vstride})")
+        n_pos = 0
+        if rope is not None:
+            n_pos = rope.shape[0]
+            _dense("rope", rope, (n_pos, self.head_dim // 2, 2), torch.float32, self.device)
+        qp = op = None
+        q_stride = 0
+        if q is not None:
+            nq, q_stride = self._rows("q", q, self.heads)
+            if nq != n:
+                raise ValueError(f"kvc: q has {nq} tokens, k {n}")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != q.device or not q_out.is_contiguous():
+                raise ValueError("kvc: q_out must be dense and match q")
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("kvc: q_out without q")
+        self._call("kvc_paged_append", _lib.kvc_paged_append, k.data_ptr(), v.data_ptr(), stride, qp, q_stride, op, n,
+                   self._cu(cu_new), None if rope is None else rope.data_ptr(), n_pos, ROPE_HALF if half else 0,
+                   self._stream(stream))
+        return q_out
+
+    def attend(self, q, *, cu_q=None, max_q=None, out=None, lse=None, flags=0, stream=None):
+        """Attention of every token over its row's slots.  ``max_q``: most tokens of a row (with ``cu_q``;
+        None: all of them).  ``lse``: a buffer, or True for a new one; then (out, lse) is returned."""
+        n, out, lse = self._q(q, out, lse)
+        self._call("kvc_paged_attend", _lib.kvc_paged_attend, q.data_ptr(), out.data_ptr(),
+                   None if lse is None else lse.data_ptr(), n, self._cu(cu_q), n if max_q is None else max_q, flags,
+                   self._stream(stream))
+        return out if lse is None else (out, lse)
+
+    def attend_shared(self, q, prefix_pages, prefix_len, *, cu_q=None, max_q=None, out=None, lse=None, flags=0,
+                      stream=None):
+        """``attend`` for rows whose first ``prefix_len`` (int32 [1], on the device) slots are those of
+        ``prefix_pages`` (int32): they are read once for all rows."""
+        n, out, lse = self._q(q, out, lse)
+        for what, t in (("prefix_pages", prefix_pages), ("prefix_len", prefix_len)):
+            if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"kvc: {what} must be a dense int32 tensor on {self.device}")
+        if prefix_len.numel() != 1:
+            raise ValueError("kvc: prefix_len holds one length")
+        self._call("kvc_paged_attend_shared", _lib.kvc_paged_attend_shared, q.data_ptr(), out.data_ptr(),
+                   None if lse is None else lse.data_ptr(), n, self._cu(cu_q), n if max_q is None else max_q,
+                   prefix_pages.data_ptr(), prefix_pages.numel(), prefix_len.data_ptr(), flags, self._stream(stream))
+        return out if lse is None else (out, lse)
+
+    def attend_sparse(self, q, n_select, *, first=1, recent=1, out=None, lse=None, selected=None, flags=0, stream=None):
+        """Attention of one token per row over ``n_select`` pages per kv head: the ``first`` and the newest
+        ``recent`` ones, and those whose bounds promise the largest scores.  Returns (out, lse, selected), or
+        (out, selected) without ``lse``; selected int32 [batch, kv_heads, n_select], -1 behind the last."""
+        n, out, lse = self._q(q, out, lse)
+        if n != self.batch:
+            raise ValueError(f"kvc: attend_sparse takes one token per row ({self.batch}), got {n}")
+        shape = (self.batch, self.kv_heads, n_select)
+        if selected is None:
+            selected = torch.empty(shape, dtype=torch.int32, device=self.device)
+        elif selected.shape != shape or selected.dtype != torch.int32 or selected.device != self.device or \
+                not selected.is_contiguous():
+            raise ValueError(f"kvc: selected must be a dense int32 {list(shape)}")
+        self._call("kvc_paged_attend_sparse", _lib.kvc_paged_attend_sparse, q.data_ptr(), out.data_ptr(),
+                   None if lse is None else lse.data_ptr(), n_select, first, recent, selected.data_ptr(), flags,
+                   self._stream(stream))
+        return (out, selected) if lse is None else (out, lse, selected)
+
+    def get_error(self, stream=None) -> int:
+        with torch.cuda.device(self.device):
+            return kvc_paged_get_error(self.handle, self._stream(stream))
+
+    def close(self):
+        if self.handle:
+            kvc_paged_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
