@@ -297,19 +297,30 @@ k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
 }
 
 template <typename T, int D>
-cudaError_t launch(kvc_paged* c, const void* q, const SelArgs& a, cudaStream_t s) {
+cudaError_t launch(const kvc_paged* c, const void* q, const SelArgs& a, cudaStream_t s, bool prepare) {
+  if (prepare)
+    return cudaFuncSetAttribute(k_paged_rank<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KVC_PG_MAX_SCORED * 4);
   const int blocks = (a.max_pages + 8 * 4 - 1) / (8 * 4);
-  cudaError_t e = kvc_launch_pdl(k_paged_score<T, D>, dim3(blocks, a.Hkv, a.B), dim3(kScoreThreads), 0, s, (const T*)q,
+  const cudaError_t e = kvc_launch_pdl(k_paged_score<T, D>, dim3(blocks, a.Hkv, a.B), dim3(kScoreThreads), 0, s, (const T*)q,
                                  (const T*)c->bounds, a);
   if (e != cudaSuccess) return e;
   const size_t smem = (size_t)a.max_pages * 4;
-  e = cudaFuncSetAttribute(k_paged_rank<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KVC_PG_MAX_SCORED * 4);
-  if (e != cudaSuccess) return e;
   return kvc_launch_pdl(k_paged_rank<T, D>, dim3(a.Hkv, a.B), dim3(kRankThreads), smem, s, (const T*)q,
                         (const T*)c->bounds, a);
 }
 
+cudaError_t dispatch(const kvc_paged* c, const void* q, const SelArgs& a, cudaStream_t s, bool prep) {
+  const bool d64 = c->cfg.head_dim == 64;
+  switch (c->cfg.dtype) {
+    case KVC_F32: return d64 ? launch<float, 64>(c, q, a, s, prep) : launch<float, 128>(c, q, a, s, prep);
+    case KVC_F16: return d64 ? launch<__half, 64>(c, q, a, s, prep) : launch<__half, 128>(c, q, a, s, prep);
+    default: return d64 ? launch<__nv_bfloat16, 64>(c, q, a, s, prep) : launch<__nv_bfloat16, 128>(c, q, a, s, prep);
+  }
+}
+
 }  // namespace
+
+cudaError_t kvc_pg_prepare_select(const kvc_paged* c) { return dispatch(c, nullptr, SelArgs{}, 0, true); }
 
 cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int first, int recent, int32_t* sel,
                                  cudaStream_t s) {
@@ -332,10 +343,5 @@ cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int fir
   a.first = first;
   a.recent = recent;
   a.sel = sel;
-  const bool d64 = g.head_dim == 64;
-  switch (g.dtype) {
-    case KVC_F32: return d64 ? launch<float, 64>(c, q, a, s) : launch<float, 128>(c, q, a, s);
-    case KVC_F16: return d64 ? launch<__half, 64>(c, q, a, s) : launch<__half, 128>(c, q, a, s);
-    default: return d64 ? launch<__nv_bfloat16, 64>(c, q, a, s) : launch<__nv_bfloat16, 128>(c, q, a, s);
-  }
+  return dispatch(c, q, a, s, false);
 }

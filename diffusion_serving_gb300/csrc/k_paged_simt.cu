@@ -195,22 +195,29 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
 }
 
 template <typename T, int D>
-cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s) {
+cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prepare) {
+  if (prepare)
+    return cudaFuncSetAttribute(k_paged_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(sizeof(SimtSmem<D>) + 16 + pg_sched_bytes(KVC_PG_MAX_BATCH)));
   const size_t smem = ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15) + pg_sched_bytes(a.phase == 1 ? 1 : a.B);
-  const cudaError_t e = cudaFuncSetAttribute(k_paged_simt<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)(sizeof(SimtSmem<D>) + 16 + pg_sched_bytes(KVC_PG_MAX_BATCH)));
-  if (e != cudaSuccess) return e;
   return kvc_launch_pdl(k_paged_simt<T, D>, dim3(KVC_PG_GRID_SIMT), dim3(kThreads), smem, s, (const T*)q,
                         (const T*)c->k, (const T*)c->v, (T*)out, a);
 }
 
-}  // namespace
-
-cudaError_t kvc_pg_launch_simt(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s) {
+cudaError_t dispatch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prep) {
   const bool d64 = c->cfg.head_dim == 64;
   switch (c->cfg.dtype) {
-    case KVC_F32: return d64 ? launch<float, 64>(c, a, q, out, s) : launch<float, 128>(c, a, q, out, s);
-    case KVC_F16: return d64 ? launch<__half, 64>(c, a, q, out, s) : launch<__half, 128>(c, a, q, out, s);
-    default: return d64 ? launch<__nv_bfloat16, 64>(c, a, q, out, s) : launch<__nv_bfloat16, 128>(c, a, q, out, s);
+    case KVC_F32: return d64 ? launch<float, 64>(c, a, q, out, s, prep) : launch<float, 128>(c, a, q, out, s, prep);
+    case KVC_F16: return d64 ? launch<__half, 64>(c, a, q, out, s, prep) : launch<__half, 128>(c, a, q, out, s, prep);
+    default:
+      return d64 ? launch<__nv_bfloat16, 64>(c, a, q, out, s, prep) : launch<__nv_bfloat16, 128>(c, a, q, out, s, prep);
   }
+}
+
+}  // namespace
+
+cudaError_t kvc_pg_prepare_simt(const kvc_paged* c) { return dispatch(c, kvc_pg_args{}, nullptr, nullptr, 0, true); }
+
+cudaError_t kvc_pg_launch_simt(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s) {
+  return dispatch(c, a, q, out, s, false);
 }

@@ -56,6 +56,14 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
   return on_device(c) ? KVC_OK : KVC_ERR_ARG;
 }
 
+// Kernel by type and shape: fp32 stores (and KVC_KERNEL_SIMT) run the FMA kernel; 16-bit ones with at
+// most 16 query rows per group the streaming kernel.
+cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, uint32_t flags, cudaStream_t s) {
+  const bool simt = c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT);
+  if (!simt && a.phase != 1 && (int64_t)a.max_q * a.Gv <= 16) return kvc_pg_launch_decode(c, a, q, out, s);
+  return kvc_pg_launch_simt(c, a, q, out, s);
+}
+
 kvc_pg_args attend_args(const kvc_paged* c, float* lse, int32_t n_tokens, const int32_t* d_cu, int32_t max_q,
                         uint32_t flags) {
   kvc_pg_args a = kvc_pg_base_args(c);
@@ -149,6 +157,8 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
     ok = kvc_make_tile_map(&c->tm_k, cfg->dtype, k_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows) &&
          kvc_make_tile_map(&c->tm_v, cfg->dtype, v_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows);
   }
+  ok = ok && kvc_pg_prepare_simt(c) == cudaSuccess && (bounds == nullptr || kvc_pg_prepare_select(c) == cudaSuccess) &&
+       (cfg->dtype == KVC_F32 || kvc_pg_prepare_decode(c) == cudaSuccess);
   ok = ok && cudaMemsetAsync(workspace, 0, kvc_pg_workspace(*cfg).zeroed, as_stream(stream)) == cudaSuccess;
   if (!ok) {
     delete c;
@@ -185,7 +195,7 @@ int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32
   const int rc = check_attend(c, q, out, d_lse, n_tokens, d_cu, max_q, flags);
   if (rc != KVC_OK) return rc;
   const kvc_pg_args a = attend_args(c, d_lse, n_tokens, d_cu, max_q, flags);
-  return launched(kvc_pg_launch_simt(c, a, q, out, as_stream(stream)));
+  return launched(run_attend(c, a, q, out, flags, as_stream(stream)));
 }
 
 int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_tokens,
@@ -205,10 +215,10 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   a.pre_grid = KVC_PG_GRID_SIMT;
   cudaStream_t s = as_stream(stream);
   a.phase = 1;
-  const cudaError_t e = kvc_pg_launch_simt(c, a, q, out, s);
+  const cudaError_t e = run_attend(c, a, q, out, flags, s);
   if (e != cudaSuccess) return KVC_ERR_CUDA;
   a.phase = 2;
-  return launched(kvc_pg_launch_simt(c, a, q, out, s));
+  return launched(run_attend(c, a, q, out, flags, s));
 }
 
 int kvc_paged_attend_sparse(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_select, int32_t first,
@@ -228,7 +238,7 @@ int kvc_paged_attend_sparse(kvc_paged* c, const void* q, void* out, float* d_lse
   kvc_pg_args a = attend_args(c, d_lse, c->cfg.batch, nullptr, 1, flags);
   a.sel = d_selected;
   a.n_sel = n_select;
-  return launched(kvc_pg_launch_simt(c, a, q, out, s));
+  return launched(run_attend(c, a, q, out, flags, s));
 }
 
 int kvc_paged_get_error(kvc_paged* c, void* stream, int32_t* bits) {

@@ -76,6 +76,11 @@ cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int
 cudaError_t kvc_pg_launch_simt(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
 cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int first, int recent, int32_t* sel,
                                  cudaStream_t s);
+cudaError_t kvc_pg_launch_decode(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
+// Shared-memory opt-ins of the kernels a handle may launch, once per handle.
+cudaError_t kvc_pg_prepare_simt(const kvc_paged* c);
+cudaError_t kvc_pg_prepare_select(const kvc_paged* c);
+cudaError_t kvc_pg_prepare_decode(const kvc_paged* c);
 // partial rows per item and slots per tile of the FMA kernel
 #define KVC_PG_SIMT_ROWS 16
 #define KVC_PG_SIMT_TILE 64
