@@ -1,0 +1,728 @@
+// Attention of many query rows per group over a paged store (16-bit): chunks of prompts, and the
+// shared prefix of a batch (sm_103a: tcgen05 + TMEM + TMA).
+//
+// An item is up to 128 query rows, tokens x heads of one group: the Gv heads of a group sit next to
+// one another in q, so one TMA box (64 dims x Gv heads x T tokens) stacks them, and the group's K
+// and V tiles are read once for all of them.  Over a shared prefix the tokens of the whole batch
+// are stacked, which turns B memory-bound passes over the prefix into one product per tile.
+// Items and their 128-slot tiles are shared out evenly among the blocks (paged_internal.h); an item
+// that spans blocks leaves partial states, joined by k_paged_join (or, for a shared prefix, by the
+// launch that attends what follows it).
+//
+// A block is one CTA per SM (256 threads).  Warps: 0 TMA producer of Q and K, 3 of V, 1 issues
+// S = Q K^T (and owns TMEM), 2 issues O += P V, 4-7 softmax, one query row per thread.  TMEM holds
+// three S buffers and O (128 columns each); P overwrites S as packed 16-bit pairs and is the A
+// operand of the second product.  S(j + 3) waits for PV(j) alone, so QK, softmax and PV of
+// neighbouring tiles overlap; the QK issuer also waits until PV(j - 2) is being issued, which keeps
+// the tensor queue alternating.  The running max is moved (and O rescaled) only when a tile's sum of
+// weights shows that it grew by more than 2^8.
+// K and V arrive page by page: one box per page, 64-dim half and tensor (64 dims x min(page, 64)
+// slots); boxes of a tile lie where one 128-slot box would put them (the 128-byte swizzle goes by
+// the address).
+//
+// Every mbarrier wait is bounded (0.5 s); on expiry the block records KVC_DEV_TIMEOUT, lets its TMA
+// loads and MMAs land, frees TMEM and returns.
+#include "paged_finish.h"
+#include "paged_ptx.h"
+
+#include <type_traits>
+
+namespace {
+
+using namespace pg;
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 256;
+constexpr int kSBufs = 3, kKStages = 3, kVStages = 2;
+constexpr uint32_t kBoxBytes = 64 * 2 * 128;             // 64 dims x 128 slots (or query rows)
+constexpr float kRescaleThreshold = 8.0f;                // log2 units
+constexpr float kRescaleSum = 256.0f;                    // 2^kRescaleThreshold
+constexpr int kBadRing = 8;
+
+template <int D>
+struct Smem {
+  uint8_t q[D / 64][kBoxBytes];
+  uint8_t k[kKStages][D / 64][kBoxBytes];
+  uint8_t v[kVStages][D / 64][kBoxBytes];
+  uint64_t q_full, q_free;
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[kSBufs], p_ready[kSBufs], s_free[kSBufs];
+  uint64_t o_done, o_free;
+  uint64_t pv_issued[2];
+  uint64_t drain[2];
+  // boxes of a tile that no page stands behind: read by the softmax warps up to six tiles after the K
+  // producer wrote it (QK(T) is issued once softmax(T - 3) is done, and K(T) loaded once QK(T - 3) is)
+  uint32_t k_bad[kBadRing];
+  uint32_t v_bad[kVStages];
+  uint32_t tmem_base;
+  WaitCtl wc;
+};
+
+// ---- tcgen05 ------------------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Instruction descriptor, kind::f16: fp32 accumulate, A and B of one 16-bit type (0 fp16, 1 bf16), A K-major, B K-major
+// or MN-major, M = 128, N = n.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t fmt, uint32_t b_mn_major, uint32_t n) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (b_mn_major << 16) | ((n >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+}
+// Shared-memory matrix descriptor (128-byte swizzle) as two words; the K steps of a product add their offset >> 4 to the
+// low one (shared addresses stay below 227 KB, so the 14-bit field never carries).
+struct SDesc {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ SDesc sdesc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return {((saddr >> 4) & 0x3FFFu) | (((lbo_bytes >> 4) & 0x3FFFu) << 16),
+          ((sbo_bytes >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29)};
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, SDesc a, SDesc b, uint32_t off, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo + (off >> 4)), "r"(a.hi), "r"(b.lo + (off >> 4)), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, SDesc b, uint32_t b_off, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+#define PG_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                 "=r"(r[i + 6]), "=r"(r[i + 7])
+#define PG_W8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), \
+                 "r"(r[i + 7])
+#define PG_T8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                 "+r"(r[i + 6]), "+r"(r[i + 7])
+// 32 TMEM lanes (one per thread of the warp) x 32 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : PG_R8(0), PG_R8(8), PG_R8(16), PG_R8(24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      PG_W8(0), PG_W8(8), PG_W8(16), PG_W8(24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      PG_W8(0), PG_W8(8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// ties 32 loaded registers to the preceding wait
+__device__ __forceinline__ void reg_fence32(uint32_t* r) {
+  asm volatile("" : PG_T8(0), PG_T8(8), PG_T8(16), PG_T8(24));
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 32 bytes at once (32-byte aligned): the rows that a warp's threads write lie apart, so each store fills a sector
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), PG_W8(0) : "memory");
+}
+
+template <bool kMask>
+__device__ __forceinline__ float row_max(const uint32_t* sr, int valid) {
+  float mx[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kBN; i += 2) {
+    float x0 = __uint_as_float(sr[i]), x1 = __uint_as_float(sr[i + 1]);
+    if (kMask) {
+      x0 = i < valid ? x0 : -INFINITY;
+      x1 = i + 1 < valid ? x1 : -INFINITY;
+    }
+    mx[(i >> 1) & 7] = fmax3(mx[(i >> 1) & 7], x0, x1);
+  }
+  return fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+}
+
+// p = 2^(s c - m), 0 past `valid` when kMask, packed over the first 64 columns of S; returns the row's sum of p.
+template <bool kBf16, bool kMask>
+__device__ __forceinline__ float exp_pack_store(const uint32_t* sr, int valid, float c, float m_use, uint32_t s_addr) {
+  const float2 c2 = make_float2(c, c), nm2 = make_float2(-m_use, -m_use);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int q4 = 0; q4 < 4; ++q4) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c0 = q4 * 32 + 2 * i;
+      const float2 t = __ffma2_rn(make_float2(__uint_as_float(sr[c0]), __uint_as_float(sr[c0 + 1])), c2, nm2);
+      float x0 = pg_ex2(t.x), x1 = pg_ex2(t.y);
+      if (kMask) {
+        x0 = c0 < valid ? x0 : 0.f;
+        x1 = c0 + 1 < valid ? x1 : 0.f;
+      }
+      sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(x0, x1));
+      pk[i] = pack2<kBf16>(x0, x1);
+    }
+    tmem_st16(s_addr + q4 * 16, pk);
+  }
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+           const __grid_constant__ CUtensorMap tm_v, T* __restrict__ out, int min_tiles, kvc_pg_args a) {
+  constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  constexpr int HB = D / 64;
+  extern __shared__ uint8_t raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile WaitCtl* wc = &sm.wc;
+
+  // set-up that touches no global memory runs before the wait for the previous kernel
+  if (threadIdx.x == 0) {
+    wait_init(&sm.wc, a.stall_ns);
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.drain[i], 1);
+      mbar_init(&sm.pv_issued[i], 1);
+    }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(&sm.s_full[i], 2);               // the MMAs' commit, and the issuer (for k_bad)
+      mbar_init(&sm.p_ready[i], kBM / 32);       // one arrival per softmax warp
+      mbar_init(&sm.s_free[i], 1);
+    }
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.o_free, kBM / 32);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&sm.k_full[i], 32);
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&sm.v_full[i], 32);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 32 * 3) {
+    prefetch_map(&tm_q);
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
+  }
+  // query rows that no box writes (Gv does not divide 128)
+  const int stacked = kBM / a.Gv * a.Gv;
+  for (int e = stacked * HB * 8 + threadIdx.x; e < kBM * HB * 8; e += kThreads) {
+    const int r = e / (HB * 8), h = (e / 8) % HB, c = e % 8;
+    *reinterpret_cast<uint4*>(sm.q[h] + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  kvc_pg_sched<kBM, kBN> sch;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), min_tiles);
+  const long long p0 = (long long)blockIdx.x * sch.per;
+  const long long p_end = min(sch.total, p0 + sch.per);
+  long long p = p0;
+  const int ps = 1 << a.ps_log2;
+  kvc_pg_item it;
+  if (p < p_end) it = sch.at(a, p);
+
+  if (warp == 0 || warp == 3) {
+    // ---------------- TMA producers: warp 0 Q and K, warp 3 V ----------------
+    const bool kq = warp == 0;
+    const int stages = kq ? kKStages : kVStages;
+    const CUtensorMap* tm = kq ? &tm_k : &tm_v;
+    const int box_log2 = min(a.ps_log2, 6);
+    const int per_tile = kBN >> box_log2;               // boxes of one half: 2, 4 or 8
+    const uint32_t box_bytes = 128u << box_log2;
+    // lane i < per_tile: the page of the tile's ith box; -1 behind the row's end, -2 a bad one
+    auto look = [&](const kvc_pg_item& w, int j) {
+      const int key = w.r.lo + j * kBN + (lane << box_log2);
+      if (lane >= per_tile || key >= w.r.len) return -1;
+      const int g = pg_page(a, w.b, key >> a.ps_log2);
+      return g < 0 ? -2 : g;
+    };
+    int t = 0, n = 0, q_issued = 0;
+    bool ok = true;
+    int page = p < p_end ? look(it, (int)(p - it.start)) : -1;
+    for (; ok && p < p_end;) {
+      const int tile0 = (int)(p - it.start);
+      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int kvh = it.vh / a.sub;
+      kvc_pg_item nx = it;
+      const bool more = it.start + tile1 < p_end;
+      if (more) sch.next(a, nx);
+      if (kq) {
+        if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_free, (n - 1) & 1, wc));   // the last item's last QK
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(&sm.q_full, HB * stacked * 128);
+          for (int h = 0; h < HB; ++h)
+            tma_load_4d(&tm_q, &sm.q_full, sm.q[h], 64 * h, it.vh * a.Gv, it.r.t0 + it.k * sch.T, 0);
+        }
+        q_issued = n + 1;
+      }
+      for (int j = tile0; j < tile1; ++j, ++t) {
+        int npage = -1;
+        if (j + 1 < tile1) npage = look(it, j + 1);
+        else if (more) npage = look(nx, 0);
+        const int st = t % stages;
+        uint64_t* full = kq ? &sm.k_full[st] : &sm.v_full[st];
+        if (t >= stages)
+          ok = __all_sync(0xffffffffu, mbar_wait(kq ? &sm.k_empty[st] : &sm.v_empty[st], (t / stages - 1) & 1, wc));
+        if (!ok) break;
+        const unsigned good = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
+        if (lane == 0) {
+          if (kq) sm.k_bad[t % kBadRing] = bad;
+          else sm.v_bad[st] = bad;
+          mbar_expect_tx(full, __popc(good) * HB * box_bytes);
+        }
+        __syncwarp();
+        uint8_t* dst = kq ? sm.k[st][0] : sm.v[st][0];
+        const int i = lane & (per_tile - 1), h = lane / per_tile;   // box of the tile, half
+        const int g = __shfl_sync(0xffffffffu, page, i);
+        if (h < HB && g >= 0)
+          tma_load_4d(tm, full, dst + h * kBoxBytes + i * box_bytes, 64 * h, kvh,
+                      (it.r.lo + j * kBN + (i << box_log2)) & (ps - 1), g);
+        __syncwarp();
+        if (lane != 0) mbar_arrive(full);
+        page = npage;
+      }
+      p = it.start + tile1;
+      ++n;
+      if (ok && more) it = nx;
+    }
+    if (wc->abort && lane == 0) {
+      // every load this warp issued lands before the CTA's shared memory is released
+      if (q_issued > 0) mbar_wait(&sm.q_full, (q_issued - 1) & 1, wc, false);
+      for (int i = max(0, t - stages); i < t; ++i)
+        mbar_wait(kq ? &sm.k_full[i % stages] : &sm.v_full[i % stages], (i / stages) & 1, wc, false);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- QK issuer: S(t) = Q K(t)^T into S buffer t % 3 ----------------
+    constexpr uint32_t kIdQK = idesc_f16(kBf16 ? 1u : 0u, 0, kBN);
+    int t = 0, n = 0;
+    bool ok = true;
+    for (; ok && p < p_end;) {
+      const int tile0 = (int)(p - it.start);
+      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, n & 1, wc));
+      for (int j = tile0; ok && j < tile1; ++j, ++t) {
+        const int st = t % kKStages, sb = t % kSBufs;
+        // K(t) landed, PV(t - 3) has read its P from this buffer, and PV(t - 2) is being issued (two barriers in
+        // turn, since a parity could not tell t - 2 from t)
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_full[st], (t / kKStages) & 1, wc) &&
+                                         (t < kSBufs || mbar_wait(&sm.s_free[sb], (t / kSBufs - 1) & 1, wc)) &&
+                                         (t < 2 || mbar_wait(&sm.pv_issued[t & 1], ((t - 2) >> 1) & 1, wc)));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const SDesc qd = sdesc(smem_u32(sm.q[0]), 16, 1024), kd = sdesc(smem_u32(sm.k[st][0]), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + sb * 128u, qd, kd, (kk >> 2) * kBoxBytes + (kk & 3) * 32, kIdQK, kk > 0);
+          mma_commit(&sm.s_full[sb]);
+          mma_commit(&sm.k_empty[st]);
+          if (j + 1 == tile1) mma_commit(&sm.q_free);
+          mbar_arrive(&sm.s_full[sb]);              // (hands k_bad on)
+        }
+        __syncwarp();
+      }
+      p = it.start + tile1;
+      ++n;
+      if (ok && p < p_end) sch.next(a, it);
+    }
+    if (wc->abort && lane == 0) {
+      mma_commit(&sm.drain[0]);
+      mbar_wait(&sm.drain[0], 0, wc, false);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- PV issuer: O += P(t) V(t) ----------------
+    constexpr uint32_t kIdPV = idesc_f16(kBf16 ? 1u : 0u, 1, D);
+    const int box_log2 = min(a.ps_log2, 6);
+    int t = 0, n = 0;
+    bool ok = true;
+    for (; ok && p < p_end;) {
+      const int tile0 = (int)(p - it.start);
+      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (n - 1) & 1, wc));   // the epilogue has read O
+      for (int j = tile0; ok && j < tile1; ++j, ++t) {
+        const int st = t % kVStages, sb = t % kSBufs;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[st], (t / kVStages) & 1, wc));
+        if (!ok) break;
+        const int rem = it.r.len - (it.r.lo + j * kBN);
+        const uint32_t bad = sm.v_bad[st];
+        if (rem < kBN || bad) {
+          // slots that hold nothing of the row may hold anything (NaN included): their V rows become 0, so that P = 0
+          // there adds exactly nothing
+          for (int e = lane; e < kBN * HB * 8; e += 32) {
+            const int r = e / (HB * 8), h = (e / 8) % HB, c = e % 8;
+            if (r >= rem || ((bad >> (r >> box_log2)) & 1))
+              *reinterpret_cast<uint4*>(sm.v[st][h] + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_ready[sb], (t / kSBufs) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const SDesc vd = sdesc(smem_u32(sm.v[st][0]), kBoxBytes, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk) {
+            mma_ts(tmem + 384u, tmem + sb * 128u + kk * 8, vd, kk * 16 * 128, kIdPV, (j > tile0 || kk > 0) ? 1u : 0u);
+            if (kk == 3) mbar_arrive(&sm.pv_issued[t & 1]);
+          }
+          mma_commit(&sm.s_free[sb]);
+          mma_commit(&sm.v_empty[st]);
+          if (j + 1 == tile1) mma_commit(&sm.o_done);
+        }
+        __syncwarp();
+      }
+      p = it.start + tile1;
+      ++n;
+      if (ok && p < p_end) sch.next(a, it);
+    }
+    if (wc->abort && lane == 0) {
+      mma_commit(&sm.drain[1]);
+      mbar_wait(&sm.drain[1], 0, wc, false);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax and epilogue (one query row per thread) ----------------
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t o_addr = lane_addr + 384u;
+    const float c = a.scale_log2;
+    const int box_log2 = min(a.ps_log2, 6);
+    const int prefix = a.phase == 2 ? max(0, *a.prefix_len) : 0;
+    int t = 0, n = 0;
+    bool ok = true;
+    for (; ok && p < p_end;) {
+      const int tile0 = (int)(p - it.start);
+      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
+      const int i_tok = it.k * sch.T + r / a.Gv;
+      // where this row's keys end; rows that are not there see everything (no mask on their account)
+      int limit = 0x3fffffff;
+      if (r < rows) limit = a.phase == 1 ? pg_prefix_limit(a, i_tok, it.r.len) : pg_limit(a, it.r, i_tok);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = tile0; j < tile1; ++j, ++t) {
+        const int sb = t % kSBufs;
+        const uint32_t s_addr = lane_addr + sb * 128u;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (t / kSBufs) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        const int valid = limit - (it.r.lo + j * kBN);
+        const uint32_t bad = sm.k_bad[t % kBadRing];
+        auto tile = [&](auto mask) {
+          constexpr bool kM = decltype(mask)::value;
+          uint32_t sr[128];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(s_addr + q4 * 32, sr + q4 * 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) reg_fence32(sr + q4 * 32);
+          if (kM && bad) {                              // slots without a page (bits past a tile's boxes are 0)
+#pragma unroll
+            for (int i = 0; i < kBN; ++i)
+              if ((bad >> (i >> box_log2)) & 1) sr[i] = 0xff800000u;
+          }
+          // After the first tile P is taken against the running reference at once: every p is at most the row's
+          // sum, so a sum of at most 2^threshold shows that the maximum did not grow by more, and P stands.
+          if (j > tile0) {
+            const float lsum = exp_pack_store<kBf16, kM>(sr, valid, c, m_ref, s_addr);
+            if (!__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) {   // (a NaN sum takes the slow path)
+              l += lsum;
+              return;
+            }
+          }
+          const float m_tile = row_max<kM>(sr, valid) * c;
+          const bool rescale = m_tile > m_ref + kRescaleThreshold || m_ref == -INFINITY;
+          const float m_new = rescale ? m_tile : m_ref;
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;
+          if (j > tile0) {
+            tmem_st_wait();                             // the optimistic P is overwritten below
+            // O may be rescaled only once PV(t - 1) has finished accumulating into it
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_free[(t - 1) % kSBufs], ((t - 1) / kSBufs) & 1, wc))) return;
+            tc_fence_after();
+            const float alpha = rescale ? pg_ex2(m_ref - m_use) : 1.f;
+#pragma unroll 1
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              uint32_t orow[32];
+              tmem_ld32(o_addr + q4 * 32, orow);
+              tmem_ld_wait();
+              reg_fence32(orow);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = __fmul2_rn(make_float2(__uint_as_float(orow[i]), __uint_as_float(orow[i + 1])),
+                                            make_float2(alpha, alpha));
+                orow[i] = __float_as_uint(y.x);
+                orow[i + 1] = __float_as_uint(y.y);
+              }
+              tmem_st32(o_addr + q4 * 32, orow);
+            }
+            tmem_st_wait();
+            l *= alpha;
+          }
+          m_ref = m_new;
+          l += exp_pack_store<kBf16, kM>(sr, valid, c, m_use, s_addr);
+        };
+        if (__all_sync(0xffffffffu, valid >= kBN) && bad == 0) tile(std::false_type{});
+        else tile(std::true_type{});
+        ok = !__any_sync(0xffffffffu, wc->abort);
+        if (!ok) break;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[sb]);
+      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.o_done, n & 1, wc));
+      if (!ok) break;
+      tc_fence_after();
+      // ---- the item's (or this part's) state: straight out, or left as a partial ----
+      const int c0 = (int)(it.start / sch.per), c1 = (int)((it.start + it.tiles - 1) / sch.per);
+      const int cta = blockIdx.x;
+      const bool real = r < rows;
+      const int tok = it.r.t0 + i_tok;
+      if (a.phase == 1 || c0 != c1) {
+        const int m = (it.r.n + sch.T - 1) / sch.T;
+        float* dst = a.phase == 1 ? a.pre + (int64_t)(it.vh * m + it.k + cta) * (kBM * (D + 2))
+                                  : a.part + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (kBM * (D + 2));
+#pragma unroll 1
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t orow[32];
+          tmem_ld32(o_addr + q4 * 32, orow);
+          tmem_ld_wait();
+          reg_fence32(orow);
+          if (real) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_v8(dst + r * D + q4 * 32 + i * 8, orow + 8 * i);
+          }
+        }
+        if (real) *reinterpret_cast<float2*>(dst + kBM * D + 2 * r) = make_float2(m_ref, l);
+      } else {
+        const int h = it.vh * a.Gv + r % a.Gv;
+        float M = m_ref, L = l;
+        kvc_pg_prefix_parts pp{0, 0, 0};
+        if (prefix > 0 && real) {
+          pp = pg_prefix_parts(a, prefix, tok, it.vh, r % a.Gv);
+          for (int i = 0; i < pp.count; ++i)
+            M = fmaxf(M, a.pre[(int64_t)(pp.first + i) * (a.pre_rows * (D + 2)) + a.pre_rows * D + 2 * pp.row]);
+          L = l * pg_weight(m_ref, M);
+          for (int i = 0; i < pp.count; ++i) {
+            const float2 ml = *reinterpret_cast<const float2*>(a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2)) +
+                                                               a.pre_rows * D + 2 * pp.row);
+            L = fmaf(pg_weight(ml.x, M), ml.y, L);
+          }
+        }
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        const float own = l != 0.f ? pg_weight(m_ref, M) * inv : 0.f;
+        if (a.lse != nullptr && real)
+          a.lse[(int64_t)tok * a.H + h] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        T* dst = out + ((int64_t)tok * a.H + h) * D;
+#pragma unroll 1
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t orow[32];
+          tmem_ld32(o_addr + q4 * 32, orow);
+          tmem_ld_wait();
+          reg_fence32(orow);
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(orow[i]) * own;
+          for (int e = 0; e < pp.count; ++e) {
+            const float* src = a.pre + (int64_t)(pp.first + e) * (a.pre_rows * (D + 2));
+            const float w = pg_weight(src[a.pre_rows * D + 2 * pp.row], M) * inv;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(src + pp.row * D + q4 * 32 + i);
+              x[i] = fmaf(w, y.x, x[i]);
+              x[i + 1] = fmaf(w, y.y, x[i + 1]);
+              x[i + 2] = fmaf(w, y.z, x[i + 2]);
+              x[i + 3] = fmaf(w, y.w, x[i + 3]);
+            }
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = pack2<kBf16>(x[2 * i], x[2 * i + 1]);
+          if (real) {                                    // (out is 16-byte aligned, no more)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(dst + q4 * 32 + 8 * i) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          }
+        }
+      }
+      // every TMEM read of O is complete: the next item's first PV may overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_free);
+      p = it.start + tile1;
+      ++n;
+      if (p < p_end) sch.next(a, it);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && sm.wc.abort) atomicOr(a.err, KVC_DEV_TIMEOUT);
+}
+
+// ---- joining split items -------------------------------------------------------------
+// Block (c, y) joins rows y, y + gridDim.y, ... (a warp each) of the item that begins in k_paged_tc's block c
+// and goes on behind it, if there is one.  Parts are added in the order of the blocks.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinY = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+k_paged_join(T* __restrict__ out, int min_tiles, kvc_pg_args a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  // the lengths are as k_paged_tc saw them: that kernel has begun, so what precedes it is done
+  kvc_pg_sched<kBM, kBN> sch;
+  sch.init(a, smem, min_tiles);
+  sch.per = max((long long)min_tiles, (sch.total + KVC_PG_GRID - 1) / KVC_PG_GRID);
+  const int prefix = a.phase == 2 ? max(0, *a.prefix_len) : 0;
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  const long long end = (long long)(blockIdx.x + 1) * sch.per;
+  if (end >= sch.total) return;
+  const kvc_pg_item it = sch.at(a, end - 1);
+  const int c0 = (int)(it.start / sch.per), c1 = (int)((it.start + it.tiles - 1) / sch.per);
+  if (c0 != (int)blockIdx.x || c1 == c0) return;
+  const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int L4 = D / 4;                 // lanes with four dims each
+  for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
+    const int t = it.r.t0 + it.k * sch.T + r / a.Gv, g = r % a.Gv;
+    kvc_pg_prefix_parts pp{0, 0, 0};
+    if (prefix > 0) pp = pg_prefix_parts(a, prefix, t, it.vh, g);
+    const int n_parts = pp.count + c1 - c0 + 1;
+    auto part = [&](int i, int* row, int* R) {
+      if (i < pp.count) {
+        *row = pp.row;
+        *R = a.pre_rows;
+        return a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2));
+      }
+      const int cc = c0 + i - pp.count;
+      *row = r;
+      *R = kBM;
+      return a.part + (int64_t)(2 * cc + (cc == c0 ? 1 : 0)) * (kBM * (D + 2));
+    };
+    auto ml_of = [&](int i) {
+      int row, R;
+      const float* src = part(i, &row, &R);
+      return *reinterpret_cast<const float2*>(src + R * D + 2 * row);
+    };
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n_parts; i += 32) M = fmaxf(M, ml_of(i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n_parts; ++i) {
+      int row, R;
+      const float* src = part(i, &row, &R);
+      const float2 ml = *reinterpret_cast<const float2*>(src + R * D + 2 * row);
+      const float w = pg_weight(ml.x, M);
+      L = fmaf(w, ml.y, L);
+      if (lane < L4 && w > 0.f) pg_acc4(x, w, *reinterpret_cast<const float4*>(src + row * D + 4 * lane));
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const int64_t at = (int64_t)t * a.H + it.vh * a.Gv + g;
+    if (lane < L4) pg_store4(out + at * D + 4 * lane, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    if (lane == 0 && a.lse != nullptr) a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// More than half of an SM's shared memory even where D = 64 needs less: one block per SM, since each takes all of TMEM.
+template <int D>
+size_t smem_bytes(int rows) {
+  const size_t n = 1024 + ((sizeof(Smem<D>) + 15) & ~(size_t)15) + pg_sched_bytes(rows);
+  return n < 120 * 1024 ? 120 * 1024 : n;
+}
+
+template <typename T, int D>
+cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prepare) {
+  static_assert(sizeof(Smem<D>) + 1024 + 16 + (KVC_PG_MAX_BATCH + 1) * 8 + 16 + KVC_PG_MAX_BATCH * 16 <= 232448,
+                "shared memory above the 227 KB a block may opt into");
+  if (prepare)
+    return cudaFuncSetAttribute(k_paged_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem_bytes<D>(KVC_PG_MAX_BATCH));
+  CUtensorMap tm_q;
+  const uint32_t box[4] = {64, (uint32_t)a.Gv, (uint32_t)(kBM / a.Gv), 1};
+  if (!kvc_make_box_map(&tm_q, c->cfg.dtype, q, D, a.H, a.n_tokens, 1, box)) return cudaErrorInvalidValue;
+  // a part below two tiles costs more in joining than it saves; a shared prefix is always cut evenly
+  const int min_tiles = a.phase == 1 ? 1 : 2;
+  const int rows = a.phase == 1 ? 1 : a.B;
+  cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
+                                 c->tm_k, c->tm_v, (T*)out, min_tiles, a);
+  if (e != cudaSuccess || a.phase == 1) return e;
+  return kvc_launch_pdl(k_paged_join<T, D>, dim3(KVC_PG_GRID, kJoinY), dim3(kJoinThreads), pg_sched_bytes(a.B), s, (T*)out,
+                        min_tiles, a);
+}
+
+cudaError_t dispatch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prep) {
+  const bool d64 = c->cfg.head_dim == 64;
+  if (c->cfg.dtype == KVC_F16) return d64 ? launch<__half, 64>(c, a, q, out, s, prep) : launch<__half, 128>(c, a, q, out, s, prep);
+  return d64 ? launch<__nv_bfloat16, 64>(c, a, q, out, s, prep) : launch<__nv_bfloat16, 128>(c, a, q, out, s, prep);
+}
+
+}  // namespace
+
+cudaError_t kvc_pg_prepare_tc(const kvc_paged* c) { return dispatch(c, kvc_pg_args{}, nullptr, nullptr, 0, true); }
+
+cudaError_t kvc_pg_launch_tc(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s) {
+  return dispatch(c, a, q, out, s, false);
+}

@@ -155,5 +155,8 @@ enum kvc_box { KVC_BOX_SW128 = 0, KVC_BOX_SW64 = 2 };
 // False if the driver entry point is missing or the encoding is rejected.
 bool kvc_make_tile_map(CUtensorMap* m, int dtype, const void* base, int D, uint64_t d1, uint64_t d2, uint64_t d3,
                        uint32_t box_rows, kvc_box box = KVC_BOX_SW128);
+// The same over any box of the tensor (box[0] = 64 elements, 128-byte swizzle).
+bool kvc_make_box_map(CUtensorMap* m, int dtype, const void* base, int D, uint64_t d1, uint64_t d2, uint64_t d3,
+                      const uint32_t* box);
 // Decode maps of a store (tm_dk, tm_dv) for the config in c.
 bool kvc_make_decode_maps(kvc_cache* c);

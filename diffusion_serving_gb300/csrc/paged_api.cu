@@ -57,11 +57,14 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
 }
 
 // Kernel by type and shape: fp32 stores (and KVC_KERNEL_SIMT) run the FMA kernel; 16-bit ones with at
-// most 16 query rows per group the streaming kernel.
+// most 16 query rows per group the streaming kernel, with more (and for a shared prefix, where the
+// batch's rows are stacked) the tensor-core kernel.
+bool simt_only(const kvc_paged* c, uint32_t flags) { return c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT); }
+
 cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, uint32_t flags, cudaStream_t s) {
-  const bool simt = c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT);
-  if (!simt && a.phase != 1 && (int64_t)a.max_q * a.Gv <= 16) return kvc_pg_launch_decode(c, a, q, out, s);
-  return kvc_pg_launch_simt(c, a, q, out, s);
+  if (simt_only(c, flags)) return kvc_pg_launch_simt(c, a, q, out, s);
+  if (a.phase != 1 && (int64_t)a.max_q * a.Gv <= 16) return kvc_pg_launch_decode(c, a, q, out, s);
+  return kvc_pg_launch_tc(c, a, q, out, s);
 }
 
 kvc_pg_args attend_args(const kvc_paged* c, float* lse, int32_t n_tokens, const int32_t* d_cu, int32_t max_q,
@@ -86,11 +89,17 @@ kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& g) {
   w.score_max = w.tickets + 4 * (size_t)KVC_PG_GRID_SIMT;
   w.zeroed = up256(w.score_max + 4 * (size_t)g.batch * g.kv_heads);
   w.parts = w.zeroed;
-  const size_t simt = 2 * (size_t)KVC_PG_GRID_SIMT * KVC_PG_SIMT_ROWS * D2 * 4;
-  w.prefix = w.parts + up256(simt);
-  const size_t T = KVC_PG_SIMT_ROWS / Gv;
-  const size_t items = Hv * (((size_t)g.max_tokens + T - 1) / T);
-  w.scores = w.prefix + up256((items + KVC_PG_GRID_SIMT) * KVC_PG_SIMT_ROWS * D2 * 4);
+  // two partials a block; a shared prefix's are at most its items and blocks together
+  auto parts = [&](size_t grid, size_t R) { return 2 * grid * R * D2 * 4; };
+  auto prefix = [&](size_t grid, size_t R) {
+    const size_t T = R / Gv;
+    return (Hv * (((size_t)g.max_tokens + T - 1) / T) + grid) * R * D2 * 4;
+  };
+  const bool tc = g.dtype != KVC_F32;
+  const size_t p0 = parts(KVC_PG_GRID_SIMT, KVC_PG_SIMT_ROWS), p1 = tc ? parts(KVC_PG_GRID, KVC_PG_TC_ROWS) : 0;
+  const size_t x0 = prefix(KVC_PG_GRID_SIMT, KVC_PG_SIMT_ROWS), x1 = tc ? prefix(KVC_PG_GRID, KVC_PG_TC_ROWS) : 0;
+  w.prefix = w.parts + up256(p0 > p1 ? p0 : p1);
+  w.scores = w.prefix + up256(x0 > x1 ? x0 : x1);
   const size_t scored = g.max_pages <= KVC_PG_MAX_SCORED ? (size_t)g.batch * g.kv_heads * g.max_pages * 8 : 0;
   w.total = up256(w.scores + scored);
   return w;
@@ -158,7 +167,8 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
          kvc_make_tile_map(&c->tm_v, cfg->dtype, v_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows);
   }
   ok = ok && kvc_pg_prepare_simt(c) == cudaSuccess && (bounds == nullptr || kvc_pg_prepare_select(c) == cudaSuccess) &&
-       (cfg->dtype == KVC_F32 || kvc_pg_prepare_decode(c) == cudaSuccess);
+       (cfg->dtype == KVC_F32 ||
+        (kvc_pg_prepare_decode(c) == cudaSuccess && kvc_pg_prepare_tc(c) == cudaSuccess));
   ok = ok && cudaMemsetAsync(workspace, 0, kvc_pg_workspace(*cfg).zeroed, as_stream(stream)) == cudaSuccess;
   if (!ok) {
     delete c;
@@ -210,9 +220,10 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   a.prefix_pages = d_prefix_pages;
   a.prefix_cap = prefix_pages;
   a.prefix_len = d_prefix_len;
-  a.pre_rows = KVC_PG_SIMT_ROWS;
-  a.pre_tile = KVC_PG_SIMT_TILE;
-  a.pre_grid = KVC_PG_GRID_SIMT;
+  const bool simt = simt_only(c, flags);
+  a.pre_rows = simt ? KVC_PG_SIMT_ROWS : KVC_PG_TC_ROWS;
+  a.pre_tile = simt ? KVC_PG_SIMT_TILE : KVC_PG_TC_TILE;
+  a.pre_grid = simt ? KVC_PG_GRID_SIMT : KVC_PG_GRID;
   cudaStream_t s = as_stream(stream);
   a.phase = 1;
   const cudaError_t e = run_attend(c, a, q, out, flags, s);

@@ -107,9 +107,9 @@ __device__ __forceinline__ void pg_finish(const kvc_pg_args& a, const kvc_pg_sch
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) {
       s_row[2 * r] = M;
-      s_row[2 * r + 1] = L > 0.f ? 1.f / L : 0.f;    // no visible slot: out 0
+      s_row[2 * r + 1] = L != 0.f ? 1.f / L : 0.f;   // no visible slot: out 0 (a NaN goes on)
       if (a.lse != nullptr)
-        a.lse[(int64_t)t * a.H + it.vh * a.Gv + g] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        a.lse[(int64_t)t * a.H + it.vh * a.Gv + g] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
     }
   }
   bar();
@@ -118,7 +118,7 @@ __device__ __forceinline__ void pg_finish(const kvc_pg_args& a, const kvc_pg_sch
     const int t = it.r.t0 + it.k * sch.T + r / a.Gv, g = r % a.Gv;
     const float M = s_row[2 * r], inv = s_row[2 * r + 1];
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (inv > 0.f) {
+    if (inv != 0.f) {
       if (prefix > 0) {
         const kvc_pg_prefix_parts pp = pg_prefix_parts(a, prefix, t, it.vh, g);
 #pragma unroll 4

@@ -77,10 +77,15 @@ cudaError_t kvc_pg_launch_simt(const kvc_paged* c, const kvc_pg_args& a, const v
 cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int first, int recent, int32_t* sel,
                                  cudaStream_t s);
 cudaError_t kvc_pg_launch_decode(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
+cudaError_t kvc_pg_launch_tc(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
 // Shared-memory opt-ins of the kernels a handle may launch, once per handle.
 cudaError_t kvc_pg_prepare_simt(const kvc_paged* c);
 cudaError_t kvc_pg_prepare_select(const kvc_paged* c);
 cudaError_t kvc_pg_prepare_decode(const kvc_paged* c);
+cudaError_t kvc_pg_prepare_tc(const kvc_paged* c);
+// query rows per item and slots per tile of the tensor-core kernel
+#define KVC_PG_TC_ROWS 128
+#define KVC_PG_TC_TILE 128
 // partial rows per item and slots per tile of the FMA kernel
 #define KVC_PG_SIMT_ROWS 16
 #define KVC_PG_SIMT_TILE 64
