@@ -5,11 +5,19 @@
 // and V, so the kernel is HBM-bound: 2 x 2 bytes x D per slot against 4 D R flops.  Work goes to one
 // block per SM by tiles of 64 slots (paged_internal.h): a block streams one stretch of the line of
 // all rows' tiles, whatever the rows' lengths, through a ring of shared-memory stages that runs on
-// across the borders between rows.  A producer warp looks up the page numbers a tile ahead and
-// issues one TMA box per page, half head and tensor (64 dims x page_size slots, 128-byte swizzle).
-// Four consumer warps take 16 slots of each tile: S = Q K^T and O += P V as warp-level m16n8k16
-// MMAs (query rows in M, slots or dims in N), online softmax per row in between; P goes from
-// accumulators to operands in registers.
+// across the borders between rows.  Warps:
+//   0-7  consumers, two sets of four that take tiles in turn; a warp takes 16 slots of its tile:
+//        S = Q K^T and O += P V as warp-level m16n8k16 MMAs (query rows in M, slots or dims in N),
+//        online softmax per row in between, P going from accumulators to operands in registers.
+//        One set's tile takes about as long as HBM needs for one, so two keep ahead of it.
+//   8    producer: looks up page numbers a tile ahead and issues one TMA box per page, half head
+//        and tensor (64 dims x page_size slots, 128-byte swizzle).
+//   9    helper: brings the queries of the next items to shared memory, and joins the partials of a
+//        shared prefix for them, so that neither latency falls between two items.
+// At an item's end the warps' states meet in shared memory and go straight out, or, where the item
+// spans blocks, to the workspace as a partial; the block that leaves last joins the partials, in
+// their order on the line whichever block it is, so the result does not depend on timing:
+//   O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,  M = max_c m_c.
 //
 // R = 8 leaves half of M free, and P uses it: rows 8..15 carry what rounding P to 16 bits lost, so
 // O is as exact as from fp32 weights at no further MMA.  R = 16 uses all of M, with P rounded once.
@@ -20,24 +28,27 @@ namespace {
 
 using namespace pg;
 
-constexpr int kWarps = 4;                         // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;       // + one producer warp
-constexpr int kTile = kWarps * 16;                // slots per tile
+constexpr int kWarps = 8;                         // consumer warps
+constexpr int kThreads = (kWarps + 2) * 32;       // + producer, helper
+constexpr int kTile = 64;                         // slots per tile: 16 for each of 4 warps
 constexpr uint32_t kHalf = kTile * 128u;          // bytes of 64 dims of a tile
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 8;
 
-template <int D> constexpr int kStages = D == 128 ? 5 : 9;
+template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 5 : 3) : (R == 8 ? 10 : 8);
 template <int D> constexpr uint32_t kStageBytes = 2u * (D / 64) * kHalf;   // K and V
 
-template <int D, int R>
+template <typename T, int D, int R>
 struct Smem {
-  uint8_t stage[kStages<D>][kStageBytes<D>];      // 1024-byte aligned
+  uint8_t stage[kStages<D, R>][kStageBytes<D>];   // 1024-byte aligned
   float acc[kWarps][R][D];
-  float ml[kWarps][R][2];
-  float own_ml[R][2];
-  float row[R][2];
-  int pos[kStages<D>][kTile];                     // slot positions of a stage, INT_MAX: left out
-  uint64_t full[kStages<D>], empty[kStages<D>];
+  float pre_o[2][R][D];                           // an item's shared prefix, joined
+  T q[2][R][D + 8];                               // its queries (+ 8: rows on different banks)
+  float2 ml[kWarps][R];
+  float2 pre_ml[2][R];
+  int limit[2][R];                                // where each query row's keys end
+  int pos[kStages<D, R>][kTile];                  // slot positions of a stage, INT_MAX: left out
+  uint64_t full[kStages<D, R>], empty[kStages<D, R>];
+  uint64_t q_full[2], pre_full[2], item_empty[2];
   WaitCtl wc;
   int flag, abort;
 };
@@ -85,6 +96,34 @@ __device__ __forceinline__ uint32_t split2(float x, float y, uint32_t* rest, con
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Joins `n` states into (M, L, x), eight loads in flight: get(i, &ml, &o) gives state i.
+template <typename Get>
+__device__ __forceinline__ void join_states(int n, float& M, float& L, float4& x, Get get) {
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float2 ml[8];
+    float4 y[8];
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (i0 + i < n) get(i0 + i, &ml[i], &y[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+    const float w0 = pg_weight(M, top);
+    x.x *= w0, x.y *= w0, x.z *= w0, x.w *= w0;
+    L *= w0;
+    M = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i >= n) continue;
+      const float w = pg_weight(ml[i].x, M);
+      L = fmaf(w, ml[i].y, L);
+      if (w != 0.f) pg_acc4(x, w, y[i]);         // (a state without keys may hold anything)
+    }
+  }
+}
+
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -92,18 +131,24 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   constexpr int HB = D / 64;           // 64-dim boxes per tensor
   constexpr int NT = D / 8;            // n-tiles of 8 dims in O
   constexpr int NR = R / 8;            // query rows per lane
-  constexpr int S = kStages<D>;
+  constexpr int S = kStages<D, R>;
   extern __shared__ uint8_t raw[];
-  Smem<D, R>& sm = *reinterpret_cast<Smem<D, R>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  using Sm = Smem<T, D, R>;
+  Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile WaitCtl* wc = &sm.wc;
 
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
     mbar_init(&sm.full[threadIdx.x], 32);
-    mbar_init(&sm.empty[threadIdx.x], kWarps);
+    mbar_init(&sm.empty[threadIdx.x], 4);
   }
-  if (threadIdx.x == 0) wait_init(&sm.wc, a.stall_ns);
+  if (threadIdx.x >= 32 && threadIdx.x < 34) {
+    mbar_init(&sm.q_full[threadIdx.x - 32], 32);
+    mbar_init(&sm.pre_full[threadIdx.x - 32], 32);
+    mbar_init(&sm.item_empty[threadIdx.x - 32], kWarps);
+  }
+  if (threadIdx.x == 64) wait_init(&sm.wc, a.stall_ns);
   if (threadIdx.x == kWarps * 32) {
     prefetch_map(&tm_k);
     prefetch_map(&tm_v);
@@ -113,12 +158,13 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<R, kTile> sch;
-  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D, R>) + 15) & ~(size_t)15), kMinTiles);
-  long long p = (long long)blockIdx.x * sch.per;
-  const long long p_end = min(sch.total, p + sch.per);
-  if (p >= p_end) return;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, gridDim.x);
+  int p, p_end;
+  if (!sch.range(blockIdx.x, &p, &p_end)) return;
   kvc_pg_item it = sch.at(a, p);
+  p_end = sch.clip(it, p_end);
   const int ps = 1 << a.ps_log2;
+  const bool prefix = a.phase == 2 && sch.lo > 0;
 
   if (warp == kWarps) {
     // ---------------- producer: TMA boxes of K and V into the stage ring ----------------
@@ -140,10 +186,10 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     int t = 0;
     bool ok = true;
     int col, page;
-    look(it, (int)(p - it.start), &col, &page);
+    look(it, p - it.start, &col, &page);
     for (; ok && p < p_end;) {
-      const int tile0 = (int)(p - it.start);
-      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int tile0 = p - it.start;
+      const int tile1 = min(it.tiles, p_end - it.start);
       const int kvh = it.vh / a.sub;
       kvc_pg_item nx = it;
       const bool more = it.start + tile1 < p_end;
@@ -157,14 +203,8 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (!ok) break;
         const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) mbar_expect_tx(&sm.full[st], __popc(good) * 2 * HB * box_bytes);
-        // positions of the tile's slots
+        __syncwarp();
         const int first = it.r.lo + j * kTile;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int s = lane + 32 * i;
-          const int c = __shfl_sync(0xffffffffu, col, s >> box_log2), g = __shfl_sync(0xffffffffu, page, s >> box_log2);
-          sm.pos[st][s] = g >= 0 && first + s < it.r.len ? (c << a.ps_log2) + ((first + s) & (ps - 1)) : 0x7fffffff;
-        }
         uint8_t* dst = sm.stage[st];
         const int i = lane & (per_tile - 1), w = lane / per_tile;   // box of the tile; half and tensor (at most 16 boxes)
         const int g = __shfl_sync(0xffffffffu, page, i);
@@ -172,6 +212,13 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const int h = w % HB;
           tma_load_4d(w < HB ? &tm_k : &tm_v, &sm.full[st], dst + w * kHalf + i * box_bytes, 64 * h, kvh,
                       (first + (i << box_log2)) & (ps - 1), g);
+        }
+        // positions of the tile's slots
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int s = lane + 32 * x;
+          const int c = __shfl_sync(0xffffffffu, col, s >> box_log2), gg = __shfl_sync(0xffffffffu, page, s >> box_log2);
+          sm.pos[st][s] = gg >= 0 && first + s < it.r.len ? (c << a.ps_log2) + ((first + s) & (ps - 1)) : 0x7fffffff;
         }
         __syncwarp();
         if (lane != 0) mbar_arrive(&sm.full[st]);
@@ -184,54 +231,91 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (wc->abort && lane == 0) {   // let every load issued here land before the block releases its shared memory
       for (int i = max(0, t - S); i < t; ++i) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
     }
+  } else if (warp == kWarps + 1) {
+    // ---------------- helper: queries and shared prefix of the items to come ----------------
+    constexpr int VQ = D / 8;                               // 16-byte vectors of a query row
+    for (int n = 0; p < p_end; ++n) {
+      const int b = n & 1;
+      if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.item_empty[b], (n / 2 - 1) & 1, wc))) break;
+      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
+      const int t0 = it.r.t0 + it.k * sch.T;
+#pragma unroll
+      for (int e = lane; e < R * VQ; e += 32) {
+        const int r = e / VQ, c = e % VQ;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+          x = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)(t0 + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv) * D) + c);
+        *reinterpret_cast<uint4*>(&sm.q[b][r][8 * c]) = x;
+      }
+      if (lane < R)
+        sm.limit[b][lane] = lane >= rows ? 0 : a.sel != nullptr ? a.kv_len[it.b] : pg_limit(a, it.r, it.k * sch.T + lane / a.Gv);
+      mbar_arrive(&sm.q_full[b]);
+      if (prefix) {
+        // every row's parts in one pass: lane l has dims 4 l .. 4 l + 3
+        for (int r = 0; r < rows; ++r) {
+          const kvc_pg_prefix_parts pp = pg_prefix_parts(a, sch.lo, t0 + r / a.Gv, it.vh, r % a.Gv);
+          float M = -INFINITY, L = 0.f;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int d = min(lane, D / 4 - 1) * 4;
+          join_states(pp.count, M, L, x, [&](int i, float2* ml, float4* y) {
+            const float* src = a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2));
+            *ml = __ldcg(reinterpret_cast<const float2*>(src + a.pre_rows * D + 2 * pp.row));
+            *y = __ldcg(reinterpret_cast<const float4*>(src + pp.row * D + d));
+          });
+          if (lane < D / 4) *reinterpret_cast<float4*>(&sm.pre_o[b][r][d]) = x;
+          if (lane == 0) sm.pre_ml[b][r] = make_float2(M, L);
+        }
+        mbar_arrive(&sm.pre_full[b]);
+      }
+      p = it.start + min(it.tiles, p_end - it.start);
+      if (p < p_end) sch.next(a, it);
+    }
   } else {
     // ---------------- consumers ----------------
     const int hq = lane >> 2, quad = lane & 3;
-    const int r0 = warp * 16;                               // this warp's slots of every tile
+    const int set = warp >> 2;                              // takes every other tile
+    const int r0 = (warp & 3) * 16;                         // this warp's slots of its tiles
     auto bar = [] { named_bar<1>(kWarps * 32); };
-    int t = 0;
-    for (; p < p_end;) {
-      const int tile0 = (int)(p - it.start);
-      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
-      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
+    int t = 0;                                              // tiles of this block before the item's
+    for (int n = 0; p < p_end; ++n) {
+      const int b = n & 1;
+      const int tile0 = p - it.start;
+      const int tile1 = min(it.tiles, p_end - it.start);
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / 2) & 1, wc));
       uint32_t qa[D / 16][4];
       int limit[NR];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = hq + 8 * x;
-        const bool real = x < NR && r < rows;
-        const int i = it.k * sch.T + (real ? r / a.Gv : 0);
-        const T* qp = q + ((int64_t)(it.r.t0 + i) * a.H + it.vh * a.Gv + (real ? r % a.Gv : 0)) * D + 2 * quad;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          qa[kk][x] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * kk)) : 0u;
-          qa[kk][x + 2] = real ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * kk + 8)) : 0u;
+          qa[kk][x] = x < NR ? *reinterpret_cast<const uint32_t*>(&sm.q[b][r % R][16 * kk + 2 * quad]) : 0u;
+          qa[kk][x + 2] = x < NR ? *reinterpret_cast<const uint32_t*>(&sm.q[b][r % R][16 * kk + 8 + 2 * quad]) : 0u;
         }
-        if (x < NR) limit[x] = !real ? 0 : a.sel != nullptr ? a.kv_len[it.b] : pg_limit(a, it.r, i);
+        if (x < NR) limit[x] = sm.limit[b][r % R];
       }
       // slots at or behind `end` hold nothing of the row
-      const int end = a.sel != nullptr ? a.kv_len[it.b] : it.r.len;
+      const int end = a.sel != nullptr ? sm.limit[b][0] : it.r.len;
       float o[NT][4];
       float m[NR], l[NR];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
       for (int x = 0; x < NR; ++x) {
         m[x] = -INFINITY;
         l[x] = 0.f;
       }
-      bool ok = true;
-      for (int j = tile0; j < tile1; ++j, ++t) {
-        const int st = t % S;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (t / S) & 1, wc));
+      const int t_end = t + tile1 - tile0;
+      for (int u = t + ((t ^ set) & 1); ok && u < t_end; u += 2) {
+        const int st = u % S;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (u / S) & 1, wc));
         if (!ok) break;
         const uint32_t kbase = smem_u32(sm.stage[st]), vbase = kbase + HB * kHalf;
         const int2 pa = *reinterpret_cast<const int2*>(&sm.pos[st][r0 + 2 * quad]);
         const int2 pb = *reinterpret_cast<const int2*>(&sm.pos[st][r0 + 8 + 2 * quad]);
         const int pos[4] = {pa.x, pa.y, pb.x, pb.y};
-        const bool dead = pa.x >= end || pa.y >= end || pb.x >= end || pb.y >= end;
-        const bool any_dead = __any_sync(0xffffffffu, dead);
-        const bool any_live = __any_sync(0xffffffffu, pa.x < end || pa.y < end || pb.x < end || pb.y < end);
+        const bool any_dead = __any_sync(0xffffffffu, pa.x >= end || pa.y >= end || pb.x >= end || pb.y >= end);
+        const bool any_live = !any_dead || __any_sync(0xffffffffu, pa.x < end || pa.y < end || pb.x < end || pb.y < end);
         if (any_live) {
           if (any_dead) {
             // such slots may hold anything (NaN included): their V rows become 0, so that P = 0 there adds nothing
@@ -272,12 +356,12 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               m[x] = mx;
               l[x] *= alpha;
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                o[n][2 * x] *= alpha;
-                o[n][2 * x + 1] *= alpha;
+              for (int i = 0; i < NT; ++i) {
+                o[i][2 * x] *= alpha;
+                o[i][2 * x + 1] *= alpha;
                 if (NR == 1) {
-                  o[n][2] *= alpha;
-                  o[n][3] *= alpha;
+                  o[i][2] *= alpha;
+                  o[i][3] *= alpha;
                 }
               }
             }
@@ -300,20 +384,23 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int jj = lane >> 3, i = lane & 7;
             const int slot = r0 + (jj & 1) * 8 + i;
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-              const int chunk = (n & 7) + (jj >> 1);
+            for (int x = 0; x < NT; x += 2) {
+              const int chunk = (x & 7) + (jj >> 1);
               uint32_t bv[4];
-              ldsm_x4_t(vbase + (n >> 3) * kHalf + slot * 128 + ((chunk ^ (slot & 7)) << 4), bv);
-              mma<T>(o[n], pw, bv[0], bv[1]);
-              mma<T>(o[n + 1], pw, bv[2], bv[3]);
+              ldsm_x4_t(vbase + (x >> 3) * kHalf + slot * 128 + ((chunk ^ (slot & 7)) << 4), bv);
+              mma<T>(o[x], pw, bv[0], bv[1]);
+              mma<T>(o[x + 1], pw, bv[2], bv[3]);
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[st]);          // this warp is done with the stage
       }
-      // the block's state: the warps' states, merged
-      bar();
+      t = t_end;
+
+      // ---- the item's end ----
+      if (ok && prefix) ok = __all_sync(0xffffffffu, mbar_wait(&sm.pre_full[b], (n / 2) & 1, wc));
+      bar();                                                // (the last item's states have been read)
       if (threadIdx.x == 0) sm.abort = wc->abort;
 #pragma unroll
       for (int x = 0; x < NR; ++x) {
@@ -321,42 +408,89 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
         const int r = hq + 8 * x;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 y = NR == 1 ? make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3])
-                                   : make_float2(o[n][2 * x], o[n][2 * x + 1]);
-          *reinterpret_cast<float2*>(&sm.acc[warp][r][8 * n + 2 * quad]) = y;
+        for (int i = 0; i < NT; ++i) {
+          const float2 y = NR == 1 ? make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3])
+                                   : make_float2(o[i][2 * x], o[i][2 * x + 1]);
+          *reinterpret_cast<float2*>(&sm.acc[warp][r][8 * i + 2 * quad]) = y;
         }
-        if (quad == 0) {
-          sm.ml[warp][r][0] = m[x];
-          sm.ml[warp][r][1] = l[x];
-        }
+        if (quad == 0) sm.ml[warp][r] = make_float2(m[x], l[x]);
       }
       bar();
       if (sm.abort) break;                                  // (the same for every consumer)
+      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
+      const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
+      const bool split = c0 != c1;
+      auto finish = [&](int r, int d, float M, float L, const float4& x) {
+        const int64_t at = (int64_t)(it.r.t0 + it.k * sch.T + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv;
+        const float inv = L != 0.f ? 1.f / L : 0.f;         // no visible slot: out 0 (a NaN goes on)
+        pg_store4(out + at * D + d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+        if (d == 0 && a.lse != nullptr) a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+      };
+      float* mine = a.part + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * (R * (D + 2));
       for (int v = threadIdx.x; v < rows * (D / 4); v += kWarps * 32) {
         const int r = v / (D / 4), d = 4 * (v % (D / 4));
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][r][0]);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          pg_acc4(x, pg_weight(sm.ml[w][r][0], M), *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
-        *reinterpret_cast<float4*>(&sm.acc[0][r][d]) = x;
-      }
-      if (threadIdx.x < R) {
-        const int r = threadIdx.x;
+        float2 ml[kWarps];
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][r][0]);
+        for (int w = 0; w < kWarps; ++w) {
+          ml[w] = sm.ml[w][r];
+          M = fmaxf(M, ml[w].x);
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (prefix && !split) {
+          const float2 pm = sm.pre_ml[b][r];
+          M = fmaxf(M, pm.x);
+          const float w = pg_weight(pm.x, M);
+          L = w * pm.y;
+          pg_acc4(x, w, *reinterpret_cast<const float4*>(&sm.pre_o[b][r][d]));
+        }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) L = fmaf(pg_weight(sm.ml[w][r][0], M), sm.ml[w][r][1], L);
-        sm.own_ml[r][0] = M;
-        sm.own_ml[r][1] = L;
+        for (int w = 0; w < kWarps; ++w) {
+          const float wt = pg_weight(ml[w].x, M);
+          L = fmaf(wt, ml[w].y, L);
+          pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
+        }
+        if (!split) {
+          finish(r, d, M, L, x);
+        } else {
+          *reinterpret_cast<float4*>(mine + r * D + d) = x;
+          if (d == 0) *reinterpret_cast<float2*>(mine + R * D + 2 * r) = make_float2(M, L);
+        }
       }
-      bar();
-      pg_finish<T, D, R, kTile>(a, sch, it, &sm.acc[0][0][0], &sm.own_ml[0][0], out, &sm.flag, &sm.row[0][0], threadIdx.x,
-                                kWarps * 32, bar);
+      if (split) {
+        // the partial's stores precede thread 0's release (barrier, then a cumulative release); the last
+        // block's loads follow its acquire
+        bar();
+        if (threadIdx.x == 0) {
+          int prev;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + c0) : "memory");
+          const int last = prev == c1 - c0;
+          if (last) a.tickets[c0] = 0;                      // every block of the item is past it
+          sm.flag = last;
+        }
+        bar();
+        if (sm.flag) {
+          for (int v = threadIdx.x; v < rows * (D / 4); v += kWarps * 32) {
+            const int r = v / (D / 4), d = 4 * (v % (D / 4));
+            float M = -INFINITY, L = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (prefix) {
+              const float2 pm = sm.pre_ml[b][r];
+              M = pm.x;
+              L = pm.y;
+              x = *reinterpret_cast<const float4*>(&sm.pre_o[b][r][d]);
+            }
+            join_states(c1 - c0 + 1, M, L, x, [&](int i, float2* ml, float4* y) {
+              const float* src = a.part + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * (R * (D + 2));
+              *ml = __ldcg(reinterpret_cast<const float2*>(src + R * D + 2 * r));
+              *y = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
+            });
+            finish(r, d, M, L, x);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[b]);
       p = it.start + tile1;
       if (p < p_end) sch.next(a, it);
     }
@@ -364,19 +498,17 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   }
 }
 
-template <int D, int R>
-size_t smem_bytes(int rows) {
-  return 1024 + ((sizeof(Smem<D, R>) + 15) & ~(size_t)15) + pg_sched_bytes(rows);
-}
+template <typename T, int D, int R>
+constexpr size_t kSmemBytes = 1024 + ((sizeof(Smem<T, D, R>) + 15) & ~(size_t)15);
 
 template <typename T, int D, int R>
 cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prepare) {
-  static_assert(sizeof(Smem<D, R>) + 1024 + 16 + (KVC_PG_MAX_BATCH + 1) * 8 + 16 + KVC_PG_MAX_BATCH * 16 <= 232448,
+  static_assert(kSmemBytes<T, D, R> + (4 * KVC_PG_MAX_BATCH + 1) * 4 + 16 <= 232448,
                 "shared memory above the 227 KB a block may opt into");
   if (prepare)
     return cudaFuncSetAttribute(k_paged_decode<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem_bytes<D, R>(KVC_PG_MAX_BATCH));
-  return kvc_launch_pdl(k_paged_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D, R>(a.B), s, c->tm_k,
+                                (int)(kSmemBytes<T, D, R> + pg_sched_bytes(KVC_PG_MAX_BATCH)));
+  return kvc_launch_pdl(k_paged_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s, c->tm_k,
                         c->tm_v, (const T*)q, (T*)out, a);
 }
 

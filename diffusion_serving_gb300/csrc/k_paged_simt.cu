@@ -55,18 +55,18 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<kR, kTS> sch;
-  sch.init(a, smem + ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15), 1);
+  sch.init(a, smem + ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15), 1, gridDim.x);
   const int tid = threadIdx.x;
   const int r = tid / kLanes, ln = tid % kLanes;
-  long long p = (long long)blockIdx.x * sch.per;
-  const long long p_end = min(sch.total, p + sch.per);
-  if (p >= p_end) return;
+  int p, p_end;
+  if (!sch.range(blockIdx.x, &p, &p_end)) return;
   kvc_pg_item it = sch.at(a, p);
+  p_end = sch.clip(it, p_end);
   const int ps = 1 << a.ps_log2;
   auto bar = [] { __syncthreads(); };
   for (; p < p_end;) {
-    const int tile0 = (int)(p - it.start);
-    const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+    const int tile0 = p - it.start;
+    const int tile1 = min(it.tiles, p_end - it.start);
     const int n_tok = min(sch.T, it.r.n - it.k * sch.T);
     const int rows = n_tok * a.Gv;
     __syncthreads();

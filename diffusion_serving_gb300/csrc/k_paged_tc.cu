@@ -264,13 +264,14 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<kBM, kBN> sch;
-  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), min_tiles);
-  const long long p0 = (long long)blockIdx.x * sch.per;
-  const long long p_end = min(sch.total, p0 + sch.per);
-  long long p = p0;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), min_tiles, gridDim.x);
+  int p = 0, p_end = 0;
   const int ps = 1 << a.ps_log2;
   kvc_pg_item it;
-  if (p < p_end) it = sch.at(a, p);
+  if (sch.range(blockIdx.x, &p, &p_end)) {
+    it = sch.at(a, p);
+    p_end = sch.clip(it, p_end);
+  }
 
   if (warp == 0 || warp == 3) {
     // ---------------- TMA producers: warp 0 Q and K, warp 3 V ----------------
@@ -289,10 +290,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     };
     int t = 0, n = 0, q_issued = 0;
     bool ok = true;
-    int page = p < p_end ? look(it, (int)(p - it.start)) : -1;
+    int page = p < p_end ? look(it, p - it.start) : -1;
     for (; ok && p < p_end;) {
-      const int tile0 = (int)(p - it.start);
-      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int tile0 = p - it.start;
+      const int tile1 = min(it.tiles, p_end - it.start);
       const int kvh = it.vh / a.sub;
       kvc_pg_item nx = it;
       const bool more = it.start + tile1 < p_end;
@@ -350,8 +351,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     int t = 0, n = 0;
     bool ok = true;
     for (; ok && p < p_end;) {
-      const int tile0 = (int)(p - it.start);
-      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int tile0 = p - it.start;
+      const int tile1 = min(it.tiles, p_end - it.start);
       ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, n & 1, wc));
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int st = t % kKStages, sb = t % kSBufs;
@@ -390,8 +391,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     int t = 0, n = 0;
     bool ok = true;
     for (; ok && p < p_end;) {
-      const int tile0 = (int)(p - it.start);
-      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int tile0 = p - it.start;
+      const int tile1 = min(it.tiles, p_end - it.start);
       if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (n - 1) & 1, wc));   // the epilogue has read O
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int st = t % kVStages, sb = t % kSBufs;
@@ -447,8 +448,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     int t = 0, n = 0;
     bool ok = true;
     for (; ok && p < p_end;) {
-      const int tile0 = (int)(p - it.start);
-      const int tile1 = (int)min((long long)it.tiles, p_end - it.start);
+      const int tile0 = p - it.start;
+      const int tile1 = min(it.tiles, p_end - it.start);
       const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
       const int i_tok = it.k * sch.T + r / a.Gv;
       // where this row's keys end; rows that are not there see everything (no mask on their account)
@@ -529,7 +530,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       if (!ok) break;
       tc_fence_after();
       // ---- the item's (or this part's) state: straight out, or left as a partial ----
-      const int c0 = (int)(it.start / sch.per), c1 = (int)((it.start + it.tiles - 1) / sch.per);
+      const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
       const int cta = blockIdx.x;
       const bool real = r < rows;
       const int tok = it.r.t0 + i_tok;
@@ -631,15 +632,14 @@ k_paged_join(T* __restrict__ out, int min_tiles, kvc_pg_args a) {
   extern __shared__ __align__(16) uint8_t smem[];
   // the lengths are as k_paged_tc saw them: that kernel has begun, so what precedes it is done
   kvc_pg_sched<kBM, kBN> sch;
-  sch.init(a, smem, min_tiles);
-  sch.per = max((long long)min_tiles, (sch.total + KVC_PG_GRID - 1) / KVC_PG_GRID);
+  sch.init(a, smem, min_tiles, KVC_PG_GRID);
   const int prefix = a.phase == 2 ? max(0, *a.prefix_len) : 0;
   kvc_pdl_wait();
   kvc_pdl_release();
-  const long long end = (long long)(blockIdx.x + 1) * sch.per;
-  if (end >= sch.total) return;
+  int p, end;
+  if (!sch.range(blockIdx.x, &p, &end) || end >= sch.total) return;
   const kvc_pg_item it = sch.at(a, end - 1);
-  const int c0 = (int)(it.start / sch.per), c1 = (int)((it.start + it.tiles - 1) / sch.per);
+  const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
   if (c0 != (int)blockIdx.x || c1 == c0) return;
   const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -695,7 +695,7 @@ size_t smem_bytes(int rows) {
 
 template <typename T, int D>
 cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prepare) {
-  static_assert(sizeof(Smem<D>) + 1024 + 16 + (KVC_PG_MAX_BATCH + 1) * 8 + 16 + KVC_PG_MAX_BATCH * 16 <= 232448,
+  static_assert(sizeof(Smem<D>) + 1024 + 16 + (4 * KVC_PG_MAX_BATCH + 1) * 4 + 16 <= 232448,
                 "shared memory above the 227 KB a block may opt into");
   if (prepare)
     return cudaFuncSetAttribute(k_paged_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -216,6 +216,9 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   if (!d_prefix_pages || !d_prefix_len || !aligned(d_prefix_pages, 4) || !aligned(d_prefix_len, 4)) return KVC_ERR_ARG;
   if (prefix_pages < 1 || prefix_pages > c->cfg.max_pages) return KVC_ERR_ARG;
   if (n_tokens > c->cfg.max_tokens) return KVC_ERR_RANGE;
+  // the prefix's tiles, over all items, are counted in 32 bits
+  const int64_t items = (int64_t)c->Hv * (n_tokens / (KVC_PG_SIMT_ROWS / c->Gv) + 1);
+  if (items * ((int64_t)prefix_pages * c->cfg.page_size / KVC_PG_SIMT_TILE + 1) > INT32_MAX - 65536) return KVC_ERR_RANGE;
   kvc_pg_args a = attend_args(c, d_lse, n_tokens, d_cu, max_q, flags);
   a.prefix_pages = d_prefix_pages;
   a.prefix_cap = prefix_pages;

@@ -55,7 +55,7 @@ __device__ __forceinline__ void pg_finish(const kvc_pg_args& a, const kvc_pg_sch
                                           int tid, int threads, Bar bar) {
   const int n_tok = min(sch.T, it.r.n - it.k * sch.T);
   const int rows = n_tok * a.Gv;
-  const int c0 = (int)(it.start / sch.per), c1 = (int)((it.start + it.tiles - 1) / sch.per);
+  const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
   const int cta = blockIdx.x;
   if (a.phase == 1 || c0 != c1) {
     // leave the state: phase 1 in slot item + block, a split item in its block's first or second slot

@@ -195,134 +195,187 @@ __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int 
 // whatever the rows' lengths, and an item that spans several blocks is joined from their
 // partials.  Rows' totals are summed up in shared memory by every block.
 //
-// Tiles of token tile k of a row: ceil(min(a + (k + 1) T, len) - lo / TS), a = len - n, where
-// queries are causal; the same for every k otherwise.
+// Where all items are alike (one row, no causal cut) and there are no more of them than blocks, each
+// item gets a whole number of blocks instead: it is padded to `stride` tiles, a multiple of `per`, so
+// that no block works on two.
+__host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int* per, int* stride) {
+  const int chunks = grid / items;
+  const int even = (tiles + chunks - 1) / chunks;
+  *per = even > min_tiles ? even : min_tiles;
+  *stride = (tiles + *per - 1) / *per * *per;
+}
+
+// Tiles of token tile k of a row: the keys that its last token sees, causal, or all.
 __device__ __forceinline__ int pg_item_tiles(const kvc_pg_row& r, int k, int T, int TS, bool causal) {
   const int end = causal ? min(r.len, r.len - r.n + min((k + 1) * T, r.n)) : r.len;
   const int keys = end - r.lo;
   return keys > TS ? (keys + TS - 1) / TS : 1;
 }
 
-// sum over i in [0, n) of floor((A i + B) / M), A, B >= 0: the lattice points under a line, by the
-// Euclidean recursion (swap axes, reduce).
-__device__ __forceinline__ long long pg_floor_sum(long long n, long long M, long long A, long long B) {
-  long long s = 0;
-#pragma unroll 1
-  for (int step = 0; step < 64 && n > 0; ++step) {
-    s += (A / M) * (n * (n - 1) / 2) + (B / M) * n;
-    A %= M;
-    B %= M;
-    const long long y = A * n + B;
-    if (y < M) break;
-    n = y / M;
-    B = y % M;
-    const long long t = M;
-    M = A;
-    A = t;
-  }
-  return s;
-}
-
-// Tiles of the row's token tiles [0, m).
-__device__ __forceinline__ long long pg_row_tiles(const kvc_pg_row& r, int m, int T, int TS, bool causal) {
-  if (m <= 0) return 0;
-  if (!causal) return (long long)m * pg_item_tiles(r, 0, T, TS, false);
-  const int all = (r.n + T - 1) / T;
-  long long s = 0;
-  int last = m;
-  if (m == all) {                        // the last token tile may be cut short
-    s = pg_item_tiles(r, all - 1, T, TS, true);
-    last = all - 1;
-  }
-  // tile k ends at x_k = a + (k + 1) T; up to TS it takes one tile
-  const long long a = (long long)r.len - r.n - r.lo;
-  long long one = TS - a >= T ? (TS - a) / T : 0;
-  if (one > last) one = last;
-  return s + one + pg_floor_sum(last - one, TS, T, a + (one + 1) * T + TS - 1);
-}
-
 struct kvc_pg_item {
   int b, vh, k;          // row, group, token tile
-  int tiles;
-  long long start;       // its first tile on the line
+  int tiles, start;      // its tiles, the first one's place on the line
   kvc_pg_row r;
 };
 
-// Shared memory of the sums: (rows + 1) x 8 bytes, then rows x 16.
-__host__ __device__ inline size_t pg_sched_bytes(int B) { return (((size_t)(B + 1) * 8 + 15) & ~(size_t)15) + (size_t)B * 16; }
+// Shared memory of the sums: rows + 1 first tiles, then each row's (t0, n, len).
+__host__ __device__ inline size_t pg_sched_bytes(int B) { return ((size_t)(4 * B + 1) * 4 + 15) & ~(size_t)15; }
 
 template <int R, int TS>
 struct kvc_pg_sched {
-  long long* base;       // [rows + 1] first tile of each row
-  kvc_pg_row* rows;
-  int n_rows, T;
+  int* base;             // [rows + 1] first tile of each row
+  int* rows;             // [rows][3]
+  int n_rows, T, lo;     // lo: where the rows' own keys begin (behind a shared prefix, or 0)
   bool causal;
-  long long total, per;
+  int total, per, stride;    // stride: tiles between items' beginnings where they are padded, else 0
 
-  // Every thread of the block calls it (it holds barriers).
-  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles) {
+  __device__ __forceinline__ kvc_pg_row row(int b) const {
+    return kvc_pg_row{rows[3 * b], rows[3 * b + 1], rows[3 * b + 2], min(lo, rows[3 * b + 2])};
+  }
+
+  // Every thread of the block calls it (it holds barriers).  A line too long for 32 bits is refused
+  // with KVC_DEV_OVERFLOW (nothing is attended).
+  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles, int grid) {
     n_rows = a.phase == 1 ? 1 : a.B;
     T = R / a.Gv;
     causal = a.causal && a.phase != 1 && a.sel == nullptr;
-    base = reinterpret_cast<long long*>(smem);
-    rows = reinterpret_cast<kvc_pg_row*>(reinterpret_cast<uint8_t*>(smem) + (((size_t)(n_rows + 1) * 8 + 15) & ~(size_t)15));
+    stride = 0;
+    base = reinterpret_cast<int*>(smem);
+    rows = base + n_rows + 1;
+    lo = a.phase == 2 ? max(0, *a.prefix_len) : 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a row's tiles over its token tiles, per group; -1: more than 32 bits hold
+    auto capped = [&](long long x) { return x <= 0x7fffffffll ? (int)x : -1; };
     for (int b = threadIdx.x; b < n_rows; b += blockDim.x) {
       const kvc_pg_row r = pg_row(a, b);
-      rows[b] = r;
-      base[b + 1] = a.Hv * pg_row_tiles(r, (r.n + T - 1) / T, T, TS, causal);
+      rows[3 * b] = r.t0;
+      rows[3 * b + 1] = r.n;
+      rows[3 * b + 2] = r.len;
+      const int m = (r.n + T - 1) / T;
+      if (!causal || m <= 1) base[b + 1] = m == 0 ? 0 : capped((long long)m * pg_item_tiles(r, 0, T, TS, causal));
     }
-    if (threadIdx.x == 0) base[0] = 0;
     __syncthreads();
-    if (threadIdx.x < 32) {
+    if (causal) {
+      for (int b = warp; b < n_rows; b += blockDim.x >> 5) {
+        const kvc_pg_row r = row(b);
+        const int m = (r.n + T - 1) / T;
+        if (m <= 1) continue;
+        long long x = 0;
+        for (int k = lane; k < m; k += 32) x += pg_item_tiles(r, k, T, TS, true);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) base[b + 1] = capped(x);
+      }
+      __syncthreads();
+    }
+    if (n_rows == 1) {
+      const kvc_pg_row r = row(0);
+      const int m = (r.n + T - 1) / T;
+      if (!causal || m <= 1) {
+        const long long items = (long long)m * a.Hv;
+        if (items > 0 && items <= grid) {
+          pg_even(pg_item_tiles(r, 0, T, TS, causal), (int)items, grid, min_tiles, &per, &stride);
+          total = (int)items * stride;
+          if (threadIdx.x == 0) {
+            base[0] = 0;
+            base[1] = total;
+          }
+          __syncthreads();
+          return;
+        }
+      }
+    }
+    if (warp == 0) {
       long long carry = 0;
+      bool over = false;
       for (int b0 = 0; b0 < n_rows; b0 += 32) {
-        const int b = b0 + threadIdx.x;
+        const int b = b0 + lane;
         long long x = b < n_rows ? base[b + 1] : 0;
+        over = over || x < 0;
+        x *= a.Hv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, x, o);
-          if ((int)threadIdx.x >= o) x += y;
+          if (lane >= o) x += y;
         }
-        if (b < n_rows) base[b + 1] = carry + x;
+        if (b < n_rows) base[b + 1] = (int)(carry + x);
         carry += __shfl_sync(0xffffffffu, x, 31);
+      }
+      over = __any_sync(0xffffffffu, over) || carry > 0x7fffffffll - 65536;
+      if (lane == 0) {
+        base[0] = over ? -1 : 0;
+        if (over) atomicOr(a.err, KVC_DEV_OVERFLOW);
       }
     }
     __syncthreads();
-    total = base[n_rows];
-    per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < min_tiles) per = min_tiles;
+    total = base[0] < 0 ? 0 : base[n_rows];
+    per = max(min_tiles, (total + grid - 1) / grid);
   }
 
-  // The item that holds tile p of the line (p < total).
-  __device__ __forceinline__ kvc_pg_item at(const kvc_pg_args& a, long long p) const {
+  // The tiles [*p, *end) of block c; false if there are none.
+  __device__ __forceinline__ bool range(int c, int* p, int* end) const {
+    if ((long long)c * per >= total) return false;
+    *p = c * per;
+    *end = total - *p > per ? *p + per : total;
+    return true;
+  }
+
+  // The item that holds tile p of the line (p < total); a whole warp calls it.
+  __device__ __forceinline__ kvc_pg_item at(const kvc_pg_args& a, int p) const {
     kvc_pg_item it;
-    int lo = 0, hi = n_rows;
+    int b = 0, hi = n_rows;
 #pragma unroll 1
-    for (int step = 0; step < 11 && hi - lo > 1; ++step) {
-      const int mid = (lo + hi) >> 1;
-      if (base[mid] <= p) lo = mid;
+    for (int step = 0; step < 11 && hi - b > 1; ++step) {
+      const int mid = (b + hi) >> 1;
+      if (base[mid] <= p) b = mid;
       else hi = mid;
     }
-    it.b = lo;
-    it.r = rows[lo];
-    const long long per_group = (base[lo + 1] - base[lo]) / a.Hv;
-    p -= base[lo];
-    it.vh = (int)(p / per_group);
-    p -= it.vh * per_group;
-    int kl = 0, kh = (it.r.n + T - 1) / T;
-#pragma unroll 1
-    for (int step = 0; step < 32 && kh - kl > 1; ++step) {
-      const int mid = (kl + kh) >> 1;
-      if (pg_row_tiles(it.r, mid, T, TS, causal) <= p) kl = mid;
-      else kh = mid;
+    it.b = b;
+    it.r = row(b);
+    const int m = (it.r.n + T - 1) / T;
+    const int group = stride ? m * stride : (base[b + 1] - base[b]) / a.Hv;
+    p -= base[b];
+    it.vh = p / group;
+    it.start = base[b] + it.vh * group;
+    p -= it.vh * group;
+    if (!causal || m == 1) {
+      it.tiles = pg_item_tiles(it.r, 0, T, TS, causal);
+      const int step = stride ? stride : it.tiles;
+      it.k = p / step;
+      it.start += it.k * step;
+      return it;
     }
-    it.k = kl;
-    it.tiles = pg_item_tiles(it.r, kl, T, TS, causal);
-    it.start = base[lo] + it.vh * per_group + pg_row_tiles(it.r, kl, T, TS, causal);
+    const int lane = threadIdx.x & 31;
+    int before = 0;                        // tiles of the token tiles up to k0
+    it.k = 0;
+    it.tiles = 1;
+    for (int k0 = 0; k0 < m; k0 += 32) {
+      int x = k0 + lane < m ? pg_item_tiles(it.r, k0 + lane, T, TS, true) : 0;
+      const int mine = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned behind = __ballot_sync(0xffffffffu, k0 + lane < m && before + x > p);
+      if (behind) {
+        const int l = __ffs(behind) - 1;
+        it.k = k0 + l;
+        it.tiles = __shfl_sync(0xffffffffu, mine, l);
+        it.start += before + __shfl_sync(0xffffffffu, x, l) - it.tiles;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
     return it;
   }
 
-  // The item behind `it` (there is one).
+  // Block c's end within the padded line: a block of a padded item stops where the item's tiles do.
+  __device__ __forceinline__ int clip(const kvc_pg_item& it, int end) const {
+    return stride ? min(end, it.start + it.tiles) : end;
+  }
+
+  // The item behind `it` (there is one, and the line is not padded).
   __device__ __forceinline__ void next(const kvc_pg_args& a, kvc_pg_item& it) const {
     it.start += it.tiles;
     if ((it.k + 1) * T < it.r.n) {
@@ -334,7 +387,7 @@ struct kvc_pg_sched {
         ++it.b;
         for (; it.b + 1 < n_rows && base[it.b + 1] == it.start; ++it.b) {
         }
-        it.r = rows[it.b];
+        it.r = row(it.b);
       }
     }
     it.tiles = pg_item_tiles(it.r, it.k, T, TS, causal);
@@ -361,13 +414,13 @@ struct kvc_pg_prefix_parts {
 };
 __device__ __forceinline__ kvc_pg_prefix_parts pg_prefix_parts(const kvc_pg_args& a, int prefix, int t, int vh, int g) {
   const int T = a.pre_rows / a.Gv;
-  const int m = (a.n_tokens + T - 1) / T;
-  const long long tiles = prefix > a.pre_tile ? (prefix + a.pre_tile - 1) / a.pre_tile : 1;
-  const long long total = tiles * m * a.Hv;
-  long long per = (total + a.pre_grid - 1) / a.pre_grid;
+  const int m = (a.n_tokens + T - 1) / T, items = m * a.Hv;
+  const int tiles = prefix > a.pre_tile ? (prefix + a.pre_tile - 1) / a.pre_tile : 1;
   const int item = vh * m + t / T;
-  const long long s = item * tiles;
-  const int c0 = (int)(s / per), c1 = (int)((s + tiles - 1) / per);
+  int per, stride = tiles;
+  if (items <= a.pre_grid) pg_even(tiles, items, a.pre_grid, 1, &per, &stride);
+  else per = (items * tiles + a.pre_grid - 1) / a.pre_grid;
+  const int c0 = item * stride / per, c1 = (item * stride + tiles - 1) / per;
   return {item + c0, c1 - c0 + 1, (t % T) * a.Gv + g};
 }
 #endif  // __CUDACC__

@@ -107,6 +107,7 @@ int kvc_paged_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stri
  *  A token that sees no slot (kv_len 0, or causal with more tokens than slots) gets out 0 and
  *  lse -inf.  A row with a bad offset (KVC_DEV_BAD_CUSEQ) or length (KVC_DEV_BAD_KVLEN) is left
  *  unwritten; the slots of a bad page (KVC_DEV_BAD_PAGE) are left out of the softmax.
+ *  More work than 2^31 tiles of 64 slots is KVC_DEV_OVERFLOW, and nothing is written.
  *  The result of a call depends on its inputs alone: the same call gives the same bits.
  *  Errors: KVC_ERR_ARG, KVC_ERR_CUDA. */
 int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_tokens, const int32_t* d_cu,
@@ -118,7 +119,8 @@ int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32
  *  d_prefix_pages: int32 [prefix_pages] page numbers; d_prefix_len: int32 [1] on the device, P, a
  *    multiple of page_size, 0 <= P <= prefix_pages * page_size (else KVC_DEV_BAD_KVLEN, nothing written).
  *  A row with kv_len < P sees the first kv_len slots of the prefix.
- *  n_tokens <= cfg.max_tokens (KVC_ERR_RANGE).  The rest as kvc_paged_attend. */
+ *  n_tokens <= cfg.max_tokens, and tokens x heads x prefix within what 32 bits count in tiles (KVC_ERR_RANGE).  The
+ *  rest as kvc_paged_attend. */
 int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_tokens,
                             const int32_t* d_cu, int32_t max_q, const int32_t* d_prefix_pages,
                             int32_t prefix_pages, const int32_t* d_prefix_len, uint32_t flags, void* stream);
