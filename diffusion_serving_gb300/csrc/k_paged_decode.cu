@@ -10,14 +10,15 @@
 //        S = Q K^T and O += P V as warp-level m16n8k16 MMAs (query rows in M, slots or dims in N),
 //        online softmax per row in between, P going from accumulators to operands in registers.
 //        One set's tile takes about as long as HBM needs for one, so two keep ahead of it.
-//   8    producer: looks up page numbers a tile ahead and issues one TMA box per page, half head
-//        and tensor (64 dims x page_size slots, 128-byte swizzle).
-//   9    helper: brings the queries of the next items to shared memory, and joins the partials of a
-//        shared prefix for them, so that neither latency falls between two items.
+//   8    producer: looks up page numbers a tile ahead and issues one TMA box per page and tensor:
+//        [page_size slots][D / 64][64 dims], 128-byte swizzle, from a 5-d view of the pool.  (A box
+//        per 64-dim half would lie free of bank conflicts, where this one's 256-byte rows meet in
+//        pairs; but a copy costs the issuing warp some 80 cycles, and 16 of them a tile, for pages
+//        of 16 slots, are more than HBM leaves time for.)
+//   9    helper: brings the queries of the next items to shared memory, and their shared prefixes'
+//        states, so that neither latency falls between two items.
 // At an item's end the warps' states meet in shared memory and go straight out, or, where the item
-// spans blocks, to the workspace as a partial; the block that leaves last joins the partials, in
-// their order on the line whichever block it is, so the result does not depend on timing:
-//   O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,  M = max_c m_c.
+// spans blocks, to the workspace (pg_finish).
 //
 // R = 8 leaves half of M free, and P uses it: rows 8..15 carry what rounding P to 16 bits lost, so
 // O is as exact as from fp32 weights at no further MMA.  R = 16 uses all of M, with P rounded once.
@@ -32,6 +33,7 @@ constexpr int kWarps = 8;                         // consumer warps
 constexpr int kThreads = (kWarps + 2) * 32;       // + producer, helper
 constexpr int kTile = 64;                         // slots per tile: 16 for each of 4 warps
 constexpr uint32_t kHalf = kTile * 128u;          // bytes of 64 dims of a tile
+constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
 constexpr int kMinTiles = 8;
 
 template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 5 : 3) : (R == 8 ? 10 : 8);
@@ -40,8 +42,8 @@ template <int D> constexpr uint32_t kStageBytes = 2u * (D / 64) * kHalf;   // K 
 template <typename T, int D, int R>
 struct Smem {
   uint8_t stage[kStages<D, R>][kStageBytes<D>];   // 1024-byte aligned
-  float acc[kWarps][R][D];
-  float pre_o[2][R][D];                           // an item's shared prefix, joined
+  float acc[kWarps][R][D + kPad];
+  float pre_o[2][R][D];                           // an item's shared prefix
   T q[2][R][D + 8];                               // its queries (+ 8: rows on different banks)
   float2 ml[kWarps][R];
   float2 pre_ml[2][R];
@@ -96,34 +98,6 @@ __device__ __forceinline__ uint32_t split2(float x, float y, uint32_t* rest, con
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Joins `n` states into (M, L, x), eight loads in flight: get(i, &ml, &o) gives state i.
-template <typename Get>
-__device__ __forceinline__ void join_states(int n, float& M, float& L, float4& x, Get get) {
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    float2 ml[8];
-    float4 y[8];
-    float top = M;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
-      if (i0 + i < n) get(i0 + i, &ml[i], &y[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
-    const float w0 = pg_weight(M, top);
-    x.x *= w0, x.y *= w0, x.z *= w0, x.w *= w0;
-    L *= w0;
-    M = top;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i0 + i >= n) continue;
-      const float w = pg_weight(ml[i].x, M);
-      L = fmaf(w, ml[i].y, L);
-      if (w != 0.f) pg_acc4(x, w, y[i]);         // (a state without keys may hold anything)
-    }
-  }
-}
-
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -141,7 +115,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
     mbar_init(&sm.full[threadIdx.x], 32);
-    mbar_init(&sm.empty[threadIdx.x], 4);
+    mbar_init(&sm.empty[threadIdx.x], kWarps);
   }
   if (threadIdx.x >= 32 && threadIdx.x < 34) {
     mbar_init(&sm.q_full[threadIdx.x - 32], 32);
@@ -205,14 +179,12 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (lane == 0) mbar_expect_tx(&sm.full[st], __popc(good) * 2 * HB * box_bytes);
         __syncwarp();
         const int first = it.r.lo + j * kTile;
-        uint8_t* dst = sm.stage[st];
-        const int i = lane & (per_tile - 1), w = lane / per_tile;   // box of the tile; half and tensor (at most 16 boxes)
+        const int i = lane & (per_tile - 1);                 // box of the tile
         const int g = __shfl_sync(0xffffffffu, page, i);
-        if (w < 2 * HB && g >= 0) {
-          const int h = w % HB;
-          tma_load_4d(w < HB ? &tm_k : &tm_v, &sm.full[st], dst + w * kHalf + i * box_bytes, 64 * h, kvh,
+        if (lane < 2 * per_tile && g >= 0)                   // K's boxes, then V's (at most 8 in all)
+          tma_load_5d(lane < per_tile ? &tm_k : &tm_v, &sm.full[st],
+                      sm.stage[st] + (lane < per_tile ? 0 : HB * kHalf) + i * HB * box_bytes, 0, 0, kvh,
                       (first + (i << box_log2)) & (ps - 1), g);
-        }
         // positions of the tile's slots
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -251,19 +223,14 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         sm.limit[b][lane] = lane >= rows ? 0 : a.sel != nullptr ? a.kv_len[it.b] : pg_limit(a, it.r, it.k * sch.T + lane / a.Gv);
       mbar_arrive(&sm.q_full[b]);
       if (prefix) {
-        // every row's parts in one pass: lane l has dims 4 l .. 4 l + 3
-        for (int r = 0; r < rows; ++r) {
-          const kvc_pg_prefix_parts pp = pg_prefix_parts(a, sch.lo, t0 + r / a.Gv, it.vh, r % a.Gv);
-          float M = -INFINITY, L = 0.f;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int d = min(lane, D / 4 - 1) * 4;
-          join_states(pp.count, M, L, x, [&](int i, float2* ml, float4* y) {
-            const float* src = a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2));
-            *ml = __ldcg(reinterpret_cast<const float2*>(src + a.pre_rows * D + 2 * pp.row));
-            *y = __ldcg(reinterpret_cast<const float4*>(src + pp.row * D + d));
-          });
-          if (lane < D / 4) *reinterpret_cast<float4*>(&sm.pre_o[b][r][d]) = x;
-          if (lane == 0) sm.pre_ml[b][r] = make_float2(M, L);
+        for (int e = lane; e < rows * (D / 4); e += 32) {
+          const int r = e / (D / 4), d = 4 * (e % (D / 4));
+          const int64_t at = (int64_t)(t0 + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv;
+          float2 ml;
+          float4 x;
+          pg_load_prefix<D>(a, at, d, &ml, &x);
+          *reinterpret_cast<float4*>(&sm.pre_o[b][r][d]) = x;
+          if (d == 0) sm.pre_ml[b][r] = ml;
         }
         mbar_arrive(&sm.pre_full[b]);
       }
@@ -275,6 +242,8 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int hq = lane >> 2, quad = lane & 3;
     const int set = warp >> 2;                              // takes every other tile
     const int r0 = (warp & 3) * 16;                         // this warp's slots of its tiles
+    // a tile holds line HB s + h of 128 bytes for slot s and 64-dim half h; its 16-byte chunk c lies at c ^ (line & 7)
+    const uint32_t row0 = r0 * HB * 128;
     auto bar = [] { named_bar<1>(kWarps * 32); };
     int t = 0;                                              // tiles of this block before the item's
     for (int n = 0; p < p_end; ++n) {
@@ -306,11 +275,17 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         l[x] = 0.f;
       }
       const int t_end = t + tile1 - tile0;
-      for (int u = t + ((t ^ set) & 1); ok && u < t_end; u += 2) {
+      for (int u = t; ok && u < t_end; ++u) {
         const int st = u % S;
+        // Every warp waits for every tile and frees every stage, the other set's too: a wait by parity has to see each
+        // phase of its barrier, since two phases on it could not tell one from the other.
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (u / S) & 1, wc));
         if (!ok) break;
-        const uint32_t kbase = smem_u32(sm.stage[st]), vbase = kbase + HB * kHalf;
+        if ((u & 1) != set) {
+          if (lane == 0) mbar_arrive(&sm.empty[st]);
+          continue;
+        }
+        const uint32_t kbase = smem_u32(sm.stage[st]) + row0, vbase = kbase + HB * kHalf;
         const int2 pa = *reinterpret_cast<const int2*>(&sm.pos[st][r0 + 2 * quad]);
         const int2 pb = *reinterpret_cast<const int2*>(&sm.pos[st][r0 + 8 + 2 * quad]);
         const int pos[4] = {pa.x, pa.y, pb.x, pb.y};
@@ -320,9 +295,10 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (any_dead) {
             // such slots may hold anything (NaN included): their V rows become 0, so that P = 0 there adds nothing
             for (int e = lane; e < 16 * HB * 8; e += 32) {
-              const int s = r0 + e / (HB * 8), h = (e / 8) % HB, c = e % 8;
-              if (sm.pos[st][s] >= end)
-                *reinterpret_cast<uint4*>(sm.stage[st] + (HB + h) * kHalf + s * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+              const int s = e / (HB * 8), h = (e / 8) % HB, c = e % 8;
+              if (sm.pos[st][r0 + s] >= end)
+                *reinterpret_cast<uint4*>(sm.stage[st] + HB * kHalf + row0 + (HB * s + h) * 128 + c * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async();                            // before TMA reuses the stage
             __syncwarp();
@@ -331,12 +307,13 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
           {
             const int jj = lane >> 3, i = lane & 7;
-            const int slot = r0 + (jj >> 1) * 8 + i;
+            const int slot = (jj >> 1) * 8 + i;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const int chunk = (kk & 3) * 2 + (jj & 1);
               uint32_t bk[4];
-              ldsm_x4(kbase + (kk >> 2) * kHalf + slot * 128 + ((chunk ^ (slot & 7)) << 4), bk);
+              const int line = HB * slot + (kk >> 2);
+              ldsm_x4(kbase + line * 128 + ((chunk ^ (line & 7)) << 4), bk);
               mma<T>(sc[0], qa[kk], bk[0], bk[1]);
               mma<T>(sc[1], qa[kk], bk[2], bk[3]);
             }
@@ -382,12 +359,13 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           // O += P V: (slots r0..7 | r0 + 8..15) x (dims 8 n..+7 | 8 n + 8..+15) per transposed ldmatrix
           {
             const int jj = lane >> 3, i = lane & 7;
-            const int slot = r0 + (jj & 1) * 8 + i;
+            const int slot = (jj & 1) * 8 + i;
 #pragma unroll
             for (int x = 0; x < NT; x += 2) {
               const int chunk = (x & 7) + (jj >> 1);
               uint32_t bv[4];
-              ldsm_x4_t(vbase + (x >> 3) * kHalf + slot * 128 + ((chunk ^ (slot & 7)) << 4), bv);
+              const int line = HB * slot + (x >> 3);
+              ldsm_x4_t(vbase + line * 128 + ((chunk ^ (line & 7)) << 4), bv);
               mma<T>(o[x], pw, bv[0], bv[1]);
               mma<T>(o[x + 1], pw, bv[2], bv[3]);
             }
@@ -417,78 +395,32 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       bar();
       if (sm.abort) break;                                  // (the same for every consumer)
-      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
-      const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
-      const bool split = c0 != c1;
-      auto finish = [&](int r, int d, float M, float L, const float4& x) {
-        const int64_t at = (int64_t)(it.r.t0 + it.k * sch.T + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv;
-        const float inv = L != 0.f ? 1.f / L : 0.f;         // no visible slot: out 0 (a NaN goes on)
-        pg_store4(out + at * D + d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-        if (d == 0 && a.lse != nullptr) a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-      };
-      float* mine = a.part + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * (R * (D + 2));
-      for (int v = threadIdx.x; v < rows * (D / 4); v += kWarps * 32) {
-        const int r = v / (D / 4), d = 4 * (v % (D / 4));
-        float2 ml[kWarps];
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = sm.ml[w][r];
-          M = fmaxf(M, ml[w].x);
-        }
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (prefix && !split) {
-          const float2 pm = sm.pre_ml[b][r];
-          M = fmaxf(M, pm.x);
-          const float w = pg_weight(pm.x, M);
-          L = w * pm.y;
-          pg_acc4(x, w, *reinterpret_cast<const float4*>(&sm.pre_o[b][r][d]));
-        }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float wt = pg_weight(ml[w].x, M);
-          L = fmaf(wt, ml[w].y, L);
-          pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
-        }
-        if (!split) {
-          finish(r, d, M, L, x);
-        } else {
-          *reinterpret_cast<float4*>(mine + r * D + d) = x;
-          if (d == 0) *reinterpret_cast<float2*>(mine + R * D + 2 * r) = make_float2(M, L);
-        }
-      }
-      if (split) {
-        // the partial's stores precede thread 0's release (barrier, then a cumulative release); the last
-        // block's loads follow its acquire
-        bar();
-        if (threadIdx.x == 0) {
-          int prev;
-          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + c0) : "memory");
-          const int last = prev == c1 - c0;
-          if (last) a.tickets[c0] = 0;                      // every block of the item is past it
-          sm.flag = last;
-        }
-        bar();
-        if (sm.flag) {
-          for (int v = threadIdx.x; v < rows * (D / 4); v += kWarps * 32) {
-            const int r = v / (D / 4), d = 4 * (v % (D / 4));
+      pg_finish<T, D, R, kTile>(
+          a, sch, it, out, &sm.flag, threadIdx.x, kWarps * 32, prefix,
+          [&](int r, int d, float* Mp, float* Lp) {
+            float2 ml[kWarps];
             float M = -INFINITY, L = 0.f;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (prefix) {
-              const float2 pm = sm.pre_ml[b][r];
-              M = pm.x;
-              L = pm.y;
-              x = *reinterpret_cast<const float4*>(&sm.pre_o[b][r][d]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              ml[w] = sm.ml[w][r];
+              M = fmaxf(M, ml[w].x);
             }
-            join_states(c1 - c0 + 1, M, L, x, [&](int i, float2* ml, float4* y) {
-              const float* src = a.part + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * (R * (D + 2));
-              *ml = __ldcg(reinterpret_cast<const float2*>(src + R * D + 2 * r));
-              *y = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
-            });
-            finish(r, d, M, L, x);
-          }
-        }
-      }
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float wt = pg_weight(ml[w].x, M);
+              L = fmaf(wt, ml[w].y, L);
+              pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
+            }
+            *Mp = M;
+            *Lp = L;
+            return x;
+          },
+          [&](int r, int d, float2* ml, float4* y) {
+            *ml = sm.pre_ml[b][r];
+            *y = *reinterpret_cast<const float4*>(&sm.pre_o[b][r][d]);
+          },
+          bar);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[b]);
       p = it.start + tile1;
@@ -508,8 +440,8 @@ cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void
   if (prepare)
     return cudaFuncSetAttribute(k_paged_decode<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(kSmemBytes<T, D, R> + pg_sched_bytes(KVC_PG_MAX_BATCH)));
-  return kvc_launch_pdl(k_paged_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s, c->tm_k,
-                        c->tm_v, (const T*)q, (T*)out, a);
+  return kvc_launch_pdl(k_paged_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s, c->tm_dk,
+                        c->tm_dv, (const T*)q, (T*)out, a);
 }
 
 template <typename T>

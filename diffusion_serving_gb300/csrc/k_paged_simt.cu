@@ -22,7 +22,6 @@ struct SimtSmem {
   float p[kR][kTS];
   float o[kR][D];
   float ml[kR][2];
-  float row[kR][2];
   long long slot[kTS];      // slot's row in the pools, -1: left out
   int pos[kTS];             // its position (INT_MAX: left out)
   int limit[kR];
@@ -188,7 +187,18 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
       sm.ml[r][1] = l;
     }
     __syncthreads();
-    pg_finish<T, D, kR, kTS>(a, sch, it, &sm.o[0][0], &sm.ml[0][0], out, &sm.flag, &sm.row[0][0], tid, kThreads, bar);
+    pg_finish<T, D, kR, kTS>(
+        a, sch, it, out, &sm.flag, tid, kThreads, a.phase == 2 && sch.lo > 0,
+        [&](int rr, int d, float* M, float* L) {
+          *M = sm.ml[rr][0];
+          *L = sm.ml[rr][1];
+          return *reinterpret_cast<const float4*>(&sm.o[rr][d]);
+        },
+        [&](int rr, int d, float2* ml, float4* y) {
+          const int64_t at = (int64_t)(it.r.t0 + it.k * sch.T + rr / a.Gv) * a.H + it.vh * a.Gv + rr % a.Gv;
+          pg_load_prefix<D>(a, at, d, ml, y);
+        },
+        bar);
     p = it.start + tile1;
     if (p < p_end) sch.next(a, it);
   }

@@ -444,7 +444,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const uint32_t o_addr = lane_addr + 384u;
     const float c = a.scale_log2;
     const int box_log2 = min(a.ps_log2, 6);
-    const int prefix = a.phase == 2 ? max(0, *a.prefix_len) : 0;
+    const int prefix = a.phase == 2 ? sch.lo : 0;
     int t = 0, n = 0;
     bool ok = true;
     for (; ok && p < p_end;) {
@@ -541,6 +541,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t orow[32];
+          __syncwarp();
           tmem_ld32(o_addr + q4 * 32, orow);
           tmem_ld_wait();
           reg_fence32(orow);
@@ -553,42 +554,37 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       } else {
         const int h = it.vh * a.Gv + r % a.Gv;
         float M = m_ref, L = l;
-        kvc_pg_prefix_parts pp{0, 0, 0};
+        const int64_t at = (int64_t)tok * a.H + h;
+        float2 pm = make_float2(-INFINITY, 0.f);         // the shared prefix's state
         if (prefix > 0 && real) {
-          pp = pg_prefix_parts(a, prefix, tok, it.vh, r % a.Gv);
-          for (int i = 0; i < pp.count; ++i)
-            M = fmaxf(M, a.pre[(int64_t)(pp.first + i) * (a.pre_rows * (D + 2)) + a.pre_rows * D + 2 * pp.row]);
-          L = l * pg_weight(m_ref, M);
-          for (int i = 0; i < pp.count; ++i) {
-            const float2 ml = *reinterpret_cast<const float2*>(a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2)) +
-                                                               a.pre_rows * D + 2 * pp.row);
-            L = fmaf(pg_weight(ml.x, M), ml.y, L);
-          }
+          pm = __ldcg(a.pre_ml + at);
+          M = fmaxf(M, pm.x);
+          L = fmaf(pg_weight(pm.x, M), pm.y, l * pg_weight(m_ref, M));
         }
         const float inv = L != 0.f ? 1.f / L : 0.f;
         const float own = l != 0.f ? pg_weight(m_ref, M) * inv : 0.f;
+        const float pw = pm.y != 0.f ? pg_weight(pm.x, M) * inv : 0.f;
         if (a.lse != nullptr && real)
-          a.lse[(int64_t)tok * a.H + h] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-        T* dst = out + ((int64_t)tok * a.H + h) * D;
+          a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        T* dst = out + at * D;
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t orow[32];
+          __syncwarp();
           tmem_ld32(o_addr + q4 * 32, orow);
           tmem_ld_wait();
           reg_fence32(orow);
           float x[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(orow[i]) * own;
-          for (int e = 0; e < pp.count; ++e) {
-            const float* src = a.pre + (int64_t)(pp.first + e) * (a.pre_rows * (D + 2));
-            const float w = pg_weight(src[a.pre_rows * D + 2 * pp.row], M) * inv;
+          if (pw != 0.f) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(src + pp.row * D + q4 * 32 + i);
-              x[i] = fmaf(w, y.x, x[i]);
-              x[i + 1] = fmaf(w, y.y, x[i + 1]);
-              x[i + 2] = fmaf(w, y.z, x[i + 2]);
-              x[i + 3] = fmaf(w, y.w, x[i + 3]);
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.pre_o + at * D + q4 * 32 + i));
+              x[i] = fmaf(pw, y.x, x[i]);
+              x[i + 1] = fmaf(pw, y.y, x[i + 1]);
+              x[i + 2] = fmaf(pw, y.z, x[i + 2]);
+              x[i + 3] = fmaf(pw, y.w, x[i + 3]);
             }
           }
           uint32_t pk[16];
@@ -620,72 +616,6 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   if (threadIdx.x == 0 && sm.wc.abort) atomicOr(a.err, KVC_DEV_TIMEOUT);
 }
 
-// ---- joining split items -------------------------------------------------------------
-// Block (c, y) joins rows y, y + gridDim.y, ... (a warp each) of the item that begins in k_paged_tc's block c
-// and goes on behind it, if there is one.  Parts are added in the order of the blocks.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinY = 8;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads)
-k_paged_join(T* __restrict__ out, int min_tiles, kvc_pg_args a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  // the lengths are as k_paged_tc saw them: that kernel has begun, so what precedes it is done
-  kvc_pg_sched<kBM, kBN> sch;
-  sch.init(a, smem, min_tiles, KVC_PG_GRID);
-  const int prefix = a.phase == 2 ? max(0, *a.prefix_len) : 0;
-  kvc_pdl_wait();
-  kvc_pdl_release();
-  int p, end;
-  if (!sch.range(blockIdx.x, &p, &end) || end >= sch.total) return;
-  const kvc_pg_item it = sch.at(a, end - 1);
-  const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
-  if (c0 != (int)blockIdx.x || c1 == c0) return;
-  const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int L4 = D / 4;                 // lanes with four dims each
-  for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
-    const int t = it.r.t0 + it.k * sch.T + r / a.Gv, g = r % a.Gv;
-    kvc_pg_prefix_parts pp{0, 0, 0};
-    if (prefix > 0) pp = pg_prefix_parts(a, prefix, t, it.vh, g);
-    const int n_parts = pp.count + c1 - c0 + 1;
-    auto part = [&](int i, int* row, int* R) {
-      if (i < pp.count) {
-        *row = pp.row;
-        *R = a.pre_rows;
-        return a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2));
-      }
-      const int cc = c0 + i - pp.count;
-      *row = r;
-      *R = kBM;
-      return a.part + (int64_t)(2 * cc + (cc == c0 ? 1 : 0)) * (kBM * (D + 2));
-    };
-    auto ml_of = [&](int i) {
-      int row, R;
-      const float* src = part(i, &row, &R);
-      return *reinterpret_cast<const float2*>(src + R * D + 2 * row);
-    };
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < n_parts; i += 32) M = fmaxf(M, ml_of(i).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n_parts; ++i) {
-      int row, R;
-      const float* src = part(i, &row, &R);
-      const float2 ml = *reinterpret_cast<const float2*>(src + R * D + 2 * row);
-      const float w = pg_weight(ml.x, M);
-      L = fmaf(w, ml.y, L);
-      if (lane < L4 && w > 0.f) pg_acc4(x, w, *reinterpret_cast<const float4*>(src + row * D + 4 * lane));
-    }
-    const float inv = L != 0.f ? 1.f / L : 0.f;
-    const int64_t at = (int64_t)t * a.H + it.vh * a.Gv + g;
-    if (lane < L4) pg_store4(out + at * D + 4 * lane, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-    if (lane == 0 && a.lse != nullptr) a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-  }
-}
-
 // More than half of an SM's shared memory even where D = 64 needs less: one block per SM, since each takes all of TMEM.
 template <int D>
 size_t smem_bytes(int rows) {
@@ -706,11 +636,10 @@ cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void
   // a part below two tiles costs more in joining than it saves; a shared prefix is always cut evenly
   const int min_tiles = a.phase == 1 ? 1 : 2;
   const int rows = a.phase == 1 ? 1 : a.B;
-  cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
+  const cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
                                  c->tm_k, c->tm_v, (T*)out, min_tiles, a);
   if (e != cudaSuccess || a.phase == 1) return e;
-  return kvc_launch_pdl(k_paged_join<T, D>, dim3(KVC_PG_GRID, kJoinY), dim3(kJoinThreads), pg_sched_bytes(a.B), s, (T*)out,
-                        min_tiles, a);
+  return kvc_pg_launch_join(c, a, min_tiles, out, s);
 }
 
 cudaError_t dispatch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prep) {

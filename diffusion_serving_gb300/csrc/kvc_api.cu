@@ -130,6 +130,21 @@ bool kvc_make_box_map(CUtensorMap* m, int dtype, const void* base, int D, uint64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool kvc_make_page_map(CUtensorMap* m, int dtype, const void* base, int D, uint64_t heads, uint64_t page_size,
+                       uint64_t n_pages, uint32_t box_slots) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr || (dtype != KVC_BF16 && dtype != KVC_F16)) return false;
+  const cuuint64_t halves = (cuuint64_t)D / 64, row = heads * D * 2ull;
+  const cuuint64_t dims[5] = {64, halves, heads, page_size, n_pages};
+  const cuuint64_t strides[4] = {128, (cuuint64_t)D * 2ull, row, row * page_size};
+  const cuuint32_t boxdim[5] = {64, (cuuint32_t)halves, 1, box_slots, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUtensorMapDataType t = dtype == KVC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(m, t, 5, const_cast<void*>(base), dims, strides, boxdim, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int kvc_internal_check_config(const kvc_config* cfg, int* cap) { return check_cfg(cfg, cap); }
 int kvc_internal_decode_splits(const kvc_config& cfg, int cap) { return decode_splits(cfg, cap); }
 

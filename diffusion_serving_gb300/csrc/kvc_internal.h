@@ -158,5 +158,9 @@ bool kvc_make_tile_map(CUtensorMap* m, int dtype, const void* base, int D, uint6
 // The same over any box of the tensor (box[0] = 64 elements, 128-byte swizzle).
 bool kvc_make_box_map(CUtensorMap* m, int dtype, const void* base, int D, uint64_t d1, uint64_t d2, uint64_t d3,
                       const uint32_t* box);
+// Pages [n_pages][page_size][heads][D] of a 16-bit pool as 5-d boxes [box_slots][D / 64][64 dims] of one head
+// (128-byte swizzle): whole rows of a page's slots in one copy.
+bool kvc_make_page_map(CUtensorMap* m, int dtype, const void* base, int D, uint64_t heads, uint64_t page_size,
+                       uint64_t n_pages, uint32_t box_slots);
 // Decode maps of a store (tm_dk, tm_dv) for the config in c.
 bool kvc_make_decode_maps(kvc_cache* c);

@@ -99,7 +99,10 @@ kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& g) {
   const size_t p0 = parts(KVC_PG_GRID_SIMT, KVC_PG_SIMT_ROWS), p1 = tc ? parts(KVC_PG_GRID, KVC_PG_TC_ROWS) : 0;
   const size_t x0 = prefix(KVC_PG_GRID_SIMT, KVC_PG_SIMT_ROWS), x1 = tc ? prefix(KVC_PG_GRID, KVC_PG_TC_ROWS) : 0;
   w.prefix = w.parts + up256(p0 > p1 ? p0 : p1);
-  w.scores = w.prefix + up256(x0 > x1 ? x0 : x1);
+  w.pre_o = w.prefix + up256(x0 > x1 ? x0 : x1);
+  const size_t rows = (size_t)g.max_tokens * g.heads;
+  w.pre_ml = w.pre_o + up256(rows * g.head_dim * 4);
+  w.scores = w.pre_ml + up256(rows * 8);
   const size_t scored = g.max_pages <= KVC_PG_MAX_SCORED ? (size_t)g.batch * g.kv_heads * g.max_pages * 8 : 0;
   w.total = up256(w.scores + scored);
   return w;
@@ -125,6 +128,8 @@ kvc_pg_args kvc_pg_base_args(const kvc_paged* c) {
   a.tickets = reinterpret_cast<int*>(c->ws + w.tickets);
   a.part = reinterpret_cast<float*>(c->ws + w.parts);
   a.pre = reinterpret_cast<float*>(c->ws + w.prefix);
+  a.pre_o = reinterpret_cast<float*>(c->ws + w.pre_o);
+  a.pre_ml = reinterpret_cast<float2*>(c->ws + w.pre_ml);
   a.stall_ns = c->debug_stall_ns;
   return a;
 }
@@ -164,7 +169,9 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
   if (ok && cfg->dtype != KVC_F32) {
     const uint32_t rows = cfg->page_size < 64 ? cfg->page_size : 64;
     ok = kvc_make_tile_map(&c->tm_k, cfg->dtype, k_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows) &&
-         kvc_make_tile_map(&c->tm_v, cfg->dtype, v_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows);
+         kvc_make_tile_map(&c->tm_v, cfg->dtype, v_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows) &&
+         kvc_make_page_map(&c->tm_dk, cfg->dtype, k_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows) &&
+         kvc_make_page_map(&c->tm_dv, cfg->dtype, v_pages, cfg->head_dim, cfg->kv_heads, cfg->page_size, cfg->n_pages, rows);
   }
   ok = ok && kvc_pg_prepare_simt(c) == cudaSuccess && (bounds == nullptr || kvc_pg_prepare_select(c) == cudaSuccess) &&
        (cfg->dtype == KVC_F32 ||
@@ -224,12 +231,12 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   a.prefix_cap = prefix_pages;
   a.prefix_len = d_prefix_len;
   const bool simt = simt_only(c, flags);
-  a.pre_rows = simt ? KVC_PG_SIMT_ROWS : KVC_PG_TC_ROWS;
-  a.pre_tile = simt ? KVC_PG_SIMT_TILE : KVC_PG_TC_TILE;
-  a.pre_grid = simt ? KVC_PG_GRID_SIMT : KVC_PG_GRID;
   cudaStream_t s = as_stream(stream);
   a.phase = 1;
-  const cudaError_t e = run_attend(c, a, q, out, flags, s);
+  cudaError_t e = run_attend(c, a, q, out, flags, s);
+  if (e == cudaSuccess)
+    e = kvc_pg_launch_join_prefix(c, a, simt ? KVC_PG_SIMT_ROWS : KVC_PG_TC_ROWS, simt ? KVC_PG_SIMT_TILE : KVC_PG_TC_TILE,
+                                  simt ? KVC_PG_GRID_SIMT : KVC_PG_GRID, s);
   if (e != cudaSuccess) return KVC_ERR_CUDA;
   a.phase = 2;
   return launched(run_attend(c, a, q, out, flags, s));

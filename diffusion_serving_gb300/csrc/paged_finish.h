@@ -1,9 +1,6 @@
-// How an item of the paged attentions ends: its block's state (O unnormalised, running max m in
-// the exp2 domain, sum l) is written out at once, or left as a partial and joined by the block
-// that leaves last, or left for the launch that attends what follows a shared prefix.
-//   O = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,  M = max_c m_c,
-// over the item's own parts and, behind a shared prefix, the prefix's.  The parts are added in
-// their order on the line, whichever block does it, so the result does not depend on timing.
+// States of the paged attentions: O (unnormalised), the running maximum m in the exp2 domain and the
+// sum l of a query row's weights over some of its keys.  States over disjoint keys join as
+//   O = sum_c 2^(m_c - M) O_c,  L = sum_c 2^(m_c - M) l_c,  M = max_c m_c.
 #pragma once
 
 #include "paged_internal.h"
@@ -34,106 +31,106 @@ __device__ __forceinline__ void pg_acc4(float4& a, float w, const float4& x) {
 // weight of a part with maximum m against M (M finite wherever a part has keys)
 __device__ __forceinline__ float pg_weight(float m, float M) { return m == -INFINITY ? 0.f : pg_ex2(m - M); }
 
-// One state: O rows of D floats, and (m, l) per row.
-struct kvc_pg_state {
-  const float* o;
-  const float* ml;
-};
-// Slot `i` of a buffer of partials with R rows.
-template <int R, int D>
-__device__ __forceinline__ kvc_pg_state pg_part(const float* buf, int64_t i) {
-  const float* p = buf + i * (int64_t)(R * (D + 2));
-  return {p, p + R * D};
+// Joins `n` states into (M, L, x), eight loads in flight: get(i, &ml, &o) gives state i's (m, l) and four dims of O.
+template <typename Get>
+__device__ __forceinline__ void pg_join(int n, float& M, float& L, float4& x, Get get) {
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float2 ml[8];
+    float4 y[8];
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i < n) get(i0 + i, &ml[i], &y[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+    const float w0 = pg_weight(M, top);
+    x.x *= w0, x.y *= w0, x.z *= w0, x.w *= w0;
+    L *= w0;
+    M = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = pg_weight(ml[i].x, M);
+      L = fmaf(w, ml[i].y, L);
+      if (w != 0.f) pg_acc4(x, w, y[i]);         // (a state without keys may hold anything)
+    }
+  }
 }
 
-// `threads` threads (tid 0 .. threads - 1, all of a named set that bar() separates) end an item.
-// own_o [R][D] and own_ml [R][2]: this block's state, in shared memory.  s_flag, s_row: shared scratch
-// (one int; 2 R floats).  bar(): a barrier of the set.  rows: the item's real rows.
-template <typename T, int D, int R, int TS, typename Bar>
+// Partials of R rows: slot i of a buffer, row r.
+template <int R, int D>
+__device__ __forceinline__ void pg_load_part(const float* buf, int64_t i, int r, int d, float2* ml, float4* y) {
+  const float* p = buf + i * (int64_t)(R * (D + 2));
+  *ml = __ldcg(reinterpret_cast<const float2*>(p + R * D + 2 * r));
+  *y = __ldcg(reinterpret_cast<const float4*>(p + r * D + d));
+}
+
+// Four dims d .. d + 3 of one token and head, from its joined state.
+template <typename T, int D>
+__device__ __forceinline__ void pg_emit(const kvc_pg_args& a, T* out, int64_t at, int d, float M, float L, const float4& x) {
+  const float inv = L != 0.f ? 1.f / L : 0.f;          // no visible slot: out 0 (a NaN goes on)
+  pg_store4(out + at * D + d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+  if (d == 0 && a.lse != nullptr) a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The end of an item: this block's state own(r, d, &M, &L) -> O's four dims, for the item's real rows, goes straight
+// out, or is left as a partial where the item spans blocks (and where phase 1 leaves it for kvc_pg_launch_join_prefix).
+// The block that leaves last joins the partials, in their order on the line whichever block it is, so the result does
+// not depend on timing.  Behind a shared prefix, pre(r, d, &ml, &o) is the prefix's state.
+// `threads` threads call it (tid 0 .. threads - 1); bar() separates them; s_flag is an int they share.
+template <typename T, int D, int R, int TS, typename Own, typename Pre, typename Bar>
 __device__ __forceinline__ void pg_finish(const kvc_pg_args& a, const kvc_pg_sched<R, TS>& sch, const kvc_pg_item& it,
-                                          const float* own_o, const float* own_ml, T* out, int* s_flag, float* s_row,
-                                          int tid, int threads, Bar bar) {
-  const int n_tok = min(sch.T, it.r.n - it.k * sch.T);
-  const int rows = n_tok * a.Gv;
+                                          T* out, int* s_flag, int tid, int threads, bool prefix, Own own, Pre pre,
+                                          Bar bar) {
+  const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
   const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
   const int cta = blockIdx.x;
-  if (a.phase == 1 || c0 != c1) {
-    // leave the state: phase 1 in slot item + block, a split item in its block's first or second slot
-    const int m = (it.r.n + sch.T - 1) / sch.T;
-    float* dst = a.phase == 1 ? a.pre + (int64_t)(it.vh * m + it.k + cta) * (R * (D + 2))
-                              : a.part + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (R * (D + 2));
-    for (int v = tid; v < rows * (D / 4); v += threads)
-      reinterpret_cast<float4*>(dst)[v] = reinterpret_cast<const float4*>(own_o)[v];
-    for (int v = tid; v < rows * 2; v += threads) dst[R * D + v] = own_ml[v];
-    if (a.phase == 1) return;
-    // the partial's stores precede thread 0's release (barrier, then a cumulative release); the last
-    // block's loads follow its acquire
-    bar();
-    if (tid == 0) {
-      int prev;
-      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + c0) : "memory");
-      const int last = prev == c1 - c0;
-      if (last) a.tickets[c0] = 0;       // every block of the item is past it
-      *s_flag = last;
-    }
-    bar();
-    if (!*s_flag) return;
-  }
-  const int prefix = a.phase == 2 ? max(0, *a.prefix_len) : 0;
-  const bool split = c0 != c1;
-  auto own = [&](int c) { return split ? pg_part<R, D>(a.part, 2 * c + (c == c0 ? 1 : 0)) : kvc_pg_state{own_o, own_ml}; };
-  // maximum and sum of each row: one warp per row, its lanes over the parts
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int r = warp; r < rows; r += threads >> 5) {
-    const int t = it.r.t0 + it.k * sch.T + r / a.Gv, g = r % a.Gv;
-    kvc_pg_prefix_parts pp{0, 0, 0};
-    if (prefix > 0) pp = pg_prefix_parts(a, prefix, t, it.vh, g);
-    auto ml_of = [&](int i) {            // part i: the prefix's first, then the item's own
-      const float* p;
-      if (i < pp.count) p = a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2)) + a.pre_rows * D + 2 * pp.row;
-      else p = own(c0 + i - pp.count).ml + 2 * r;
-      return *reinterpret_cast<const float2*>(p);
-    };
-    const int n_parts = pp.count + c1 - c0 + 1;
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < n_parts; i += 32) M = fmaxf(M, ml_of(i).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int i = lane; i < n_parts; i += 32) {
-      const float2 x = ml_of(i);
-      L = fmaf(pg_weight(x.x, M), x.y, L);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) {
-      s_row[2 * r] = M;
-      s_row[2 * r + 1] = L != 0.f ? 1.f / L : 0.f;   // no visible slot: out 0 (a NaN goes on)
-      if (a.lse != nullptr)
-        a.lse[(int64_t)t * a.H + it.vh * a.Gv + g] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-    }
-  }
-  bar();
+  const bool left = a.phase == 1 || c0 != c1;
+  auto at = [&](int r) { return (int64_t)(it.r.t0 + it.k * sch.T + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv; };
+  // phase 1: slot item + block (item and block borders only move forward, so no two collide); else the block's second
+  // slot for the item that begins in it, its first for one that goes on
+  float* mine = a.phase == 1 ? a.pre + (int64_t)(it.vh * ((it.r.n + sch.T - 1) / sch.T) + it.k + cta) * (R * (D + 2))
+                             : a.part + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (R * (D + 2));
   for (int v = tid; v < rows * (D / 4); v += threads) {
     const int r = v / (D / 4), d = 4 * (v % (D / 4));
-    const int t = it.r.t0 + it.k * sch.T + r / a.Gv, g = r % a.Gv;
-    const float M = s_row[2 * r], inv = s_row[2 * r + 1];
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (inv != 0.f) {
-      if (prefix > 0) {
-        const kvc_pg_prefix_parts pp = pg_prefix_parts(a, prefix, t, it.vh, g);
-#pragma unroll 4
-        for (int i = 0; i < pp.count; ++i) {
-          const float* p = a.pre + (int64_t)(pp.first + i) * (a.pre_rows * (D + 2));
-          const float m = p[a.pre_rows * D + 2 * pp.row];
-          pg_acc4(x, pg_weight(m, M), *reinterpret_cast<const float4*>(p + pp.row * D + d));
-        }
-      }
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const kvc_pg_state st = own(c);
-        pg_acc4(x, pg_weight(st.ml[2 * r], M), *reinterpret_cast<const float4*>(st.o + r * D + d));
-      }
+    float M, L;
+    float4 x = own(r, d, &M, &L);
+    if (left) {
+      *reinterpret_cast<float4*>(mine + r * D + d) = x;
+      if (d == 0) *reinterpret_cast<float2*>(mine + R * D + 2 * r) = make_float2(M, L);
+      continue;
     }
-    pg_store4(out + ((int64_t)t * a.H + it.vh * a.Gv + g) * D + d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    if (prefix) pg_join(1, M, L, x, [&](int, float2* ml, float4* y) { pre(r, d, ml, y); });
+    pg_emit<T, D>(a, out, at(r), d, M, L, x);
   }
+  if (!left || a.phase == 1) return;
+  // the partial's stores precede thread 0's release (barrier, then a cumulative release); the last block's loads
+  // follow its acquire
+  bar();
+  if (tid == 0) {
+    int prev;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + c0) : "memory");
+    const int last = prev == c1 - c0;
+    if (last) a.tickets[c0] = 0;       // every block of the item is past it
+    *s_flag = last;
+  }
+  bar();
+  if (!*s_flag) return;
+  for (int v = tid; v < rows * (D / 4); v += threads) {
+    const int r = v / (D / 4), d = 4 * (v % (D / 4));
+    float M = -INFINITY, L = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (prefix) pg_join(1, M, L, x, [&](int, float2* ml, float4* y) { pre(r, d, ml, y); });
+    pg_join(c1 - c0 + 1, M, L, x,
+            [&](int i, float2* ml, float4* y) { pg_load_part<R, D>(a.part, 2 * (c0 + i) + (i == 0 ? 1 : 0), r, d, ml, y); });
+    pg_emit<T, D>(a, out, at(r), d, M, L, x);
+  }
+}
+// The state that a shared prefix left for one token and head (in global memory).
+template <int D>
+__device__ __forceinline__ void pg_load_prefix(const kvc_pg_args& a, int64_t at, int d, float2* ml, float4* y) {
+  *ml = __ldcg(a.pre_ml + at);
+  *y = __ldcg(reinterpret_cast<const float4*>(a.pre_o + at * D + d));
 }

@@ -27,7 +27,9 @@ struct kvc_paged {
   uint8_t* ws;
   int device;
   uint64_t debug_stall_ns;
-  CUtensorMap tm_k, tm_v;   // pages as boxes of 64 dims x 1 head x min(page_size, 64) slots (16-bit stores)
+  // pages of a 16-bit store: boxes of 64 dims x min(page_size, 64) slots of one head, for the tensor-core kernel;
+  // boxes of [min(page_size, 64) slots][D / 64][64 dims], for the streaming kernel
+  CUtensorMap tm_k, tm_v, tm_dk, tm_dv;
 };
 
 // Workspace, in bytes from its start.
@@ -37,6 +39,7 @@ struct kvc_pg_layout {
   size_t zeroed;        // end of what has to start at zero (and is left at zero)
   size_t parts;         // split partials
   size_t prefix;        // partials of a shared prefix
+  size_t pre_o, pre_ml; // what they join to: fp32 [max_tokens * H][D], and (max, sum)
   size_t scores;        // fp32 [batch, Hkv, max_pages]
   size_t total;
 };
@@ -62,8 +65,9 @@ struct kvc_pg_args {
   int n_sel;
   float* part;                // [2 * grid][R][D + 2]: O (unnormalised), then (max, sum) per row
   int* tickets;
-  float* pre;                 // phase 1's partials [items + blocks][pre_rows][D + 2]
-  int pre_rows, pre_tile, pre_grid;
+  float* pre;                 // phase 1's partials [items + blocks][R][D + 2]
+  float* pre_o;               // joined: [n_tokens * H][D], unnormalised
+  float2* pre_ml;             // (max, sum)
   uint64_t stall_ns;
 };
 
@@ -78,6 +82,10 @@ cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int fir
                                  cudaStream_t s);
 cudaError_t kvc_pg_launch_decode(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
 cudaError_t kvc_pg_launch_tc(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
+// Phase 1's partials (R rows an item, TS slots a tile, `grid` blocks) joined to one state per token and head.
+cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, int R, int TS, int grid, cudaStream_t s);
+// Split items of the tensor-core kernel.
+cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, int min_tiles, void* out, cudaStream_t s);
 // Shared-memory opt-ins of the kernels a handle may launch, once per handle.
 cudaError_t kvc_pg_prepare_simt(const kvc_paged* c);
 cudaError_t kvc_pg_prepare_select(const kvc_paged* c);
@@ -98,62 +106,47 @@ struct kvc_pg_row {
   int t0, n, len, lo;
 };
 
-// The shared prefix's length; -1 (with the error bit) where it is not one.
-__device__ __forceinline__ int pg_prefix_len(const kvc_pg_args& a) {
-  const int p = *a.prefix_len;
-  if (p < 0 || (p & ((1 << a.ps_log2) - 1)) || (p >> a.ps_log2) > a.prefix_cap) {
-    atomicOr(a.err, KVC_DEV_BAD_KVLEN);
-    return -1;
-  }
-  return p;
+// What the device arrays say of row b, loaded together (each load waits for none of the others).
+struct kvc_pg_raw {
+  int lo, hi, len, prefix;
+};
+__device__ __forceinline__ kvc_pg_raw pg_load(const kvc_pg_args& a, int b) {
+  kvc_pg_raw x;
+  const int n = a.cu == nullptr ? a.n_tokens / a.B : 0;
+  x.lo = a.cu == nullptr ? b * n : a.cu[b];
+  x.hi = a.cu == nullptr ? x.lo + n : a.cu[b + 1];
+  x.len = a.kv_len[b];
+  x.prefix = a.phase != 0 ? *a.prefix_len : 0;
+  return x;
 }
-
-// Tokens of row b, checked: false for a bad offset.
-__device__ __forceinline__ bool pg_tokens(const kvc_pg_args& a, int b, int* t0, int* n) {
-  if (a.cu == nullptr) {
-    *n = a.n_tokens / a.B;
-    *t0 = b * *n;
-    return true;
-  }
-  const int lo = a.cu[b], hi = a.cu[b + 1];
-  *t0 = lo;
-  *n = hi - lo;
-  if (lo < 0 || hi < lo || hi > a.n_tokens || hi - lo > a.max_q) {
-    atomicOr(a.err, KVC_DEV_BAD_CUSEQ);
-    return false;
-  }
-  return true;
+// The checks, each with its error bit.
+__device__ __forceinline__ bool pg_tokens_ok(const kvc_pg_args& a, const kvc_pg_raw& x) {
+  const bool ok = x.lo >= 0 && x.hi >= x.lo && x.hi <= a.n_tokens && x.hi - x.lo <= a.max_q;
+  if (!ok) atomicOr(a.err, KVC_DEV_BAD_CUSEQ);
+  return ok;
 }
-
-__device__ __forceinline__ int pg_len(const kvc_pg_args& a, int b) {
-  const int len = a.kv_len[b];
-  if (len < 0 || len > (a.max_pages << a.ps_log2)) {
-    atomicOr(a.err, KVC_DEV_BAD_KVLEN);
-    return -1;
-  }
-  return len;
+__device__ __forceinline__ bool pg_len_ok(const kvc_pg_args& a, int len) {
+  const bool ok = len >= 0 && len <= (a.max_pages << a.ps_log2);
+  if (!ok) atomicOr(a.err, KVC_DEV_BAD_KVLEN);
+  return ok;
+}
+__device__ __forceinline__ bool pg_prefix_ok(const kvc_pg_args& a, int p) {
+  const bool ok = p >= 0 && (p & ((1 << a.ps_log2) - 1)) == 0 && (p >> a.ps_log2) <= a.prefix_cap;
+  if (!ok) atomicOr(a.err, KVC_DEV_BAD_KVLEN);
+  return ok;
 }
 
 __device__ __forceinline__ kvc_pg_row pg_row(const kvc_pg_args& a, int b) {
-  kvc_pg_row r{0, 0, 0, 0};
+  const kvc_pg_row none{0, 0, 0, 0};
   if (a.phase == 1) {
-    const int p = pg_prefix_len(a);
-    if (p > 0) r = kvc_pg_row{0, a.n_tokens, p, 0};
-    return r;
+    const int p = *a.prefix_len;
+    return pg_prefix_ok(a, p) && p > 0 ? kvc_pg_row{0, a.n_tokens, p, 0} : none;
   }
-  int t0, n;
-  const bool ok = pg_tokens(a, b, &t0, &n);
-  const int len = pg_len(a, b);
-  if (!ok || len < 0) return r;
-  r = kvc_pg_row{t0, n, len, 0};
-  if (a.phase == 2) {
-    const int p = pg_prefix_len(a);
-    if (p < 0) return kvc_pg_row{0, 0, 0, 0};
-    r.lo = min(p, len);
-  } else if (a.sel != nullptr) {
-    const int pages = (len + (1 << a.ps_log2) - 1) >> a.ps_log2;
-    r.len = min(pages, a.n_sel) << a.ps_log2;
-  }
+  const kvc_pg_raw x = pg_load(a, b);
+  const bool tok = pg_tokens_ok(a, x), len = pg_len_ok(a, x.len);
+  if (!tok || !len || (a.phase == 2 && !pg_prefix_ok(a, x.prefix))) return none;
+  kvc_pg_row r{x.lo, x.hi - x.lo, x.len, a.phase == 2 ? min(x.prefix, x.len) : 0};
+  if (a.sel != nullptr) r.len = min((x.len + (1 << a.ps_log2) - 1) >> a.ps_log2, a.n_sel) << a.ps_log2;
   return r;
 }
 
@@ -180,11 +173,9 @@ __device__ __forceinline__ int pg_row_of(const kvc_pg_args& a, int t) {
 __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int prefix) {
   const int b = pg_row_of(a, t);
   if (b < 0) return 0;
-  int t0, n;
-  const bool ok = pg_tokens(a, b, &t0, &n);
-  const int len = pg_len(a, b);
-  if (!ok || len < 0) return 0;
-  return max(0, min(prefix, a.causal ? len - n + (t - t0) + 1 : len));
+  const kvc_pg_raw x = pg_load(a, b);
+  if (!pg_tokens_ok(a, x) || !pg_len_ok(a, x.len)) return 0;
+  return max(0, min(prefix, a.causal ? x.len - (x.hi - x.lo) + (t - x.lo) + 1 : x.len));
 }
 
 // ---- work ------------------------------------------------------------------------------
@@ -402,25 +393,5 @@ __device__ __forceinline__ int pg_page(const kvc_pg_args& a, int b, int col) {
     return -1;
   }
   return p;
-}
-
-// ---- partials of a shared prefix --------------------------------------------------------
-// Phase 1's items all have the same number of tiles, so which blocks held a token's prefix, and
-// where they left their partials, follows from the prefix length: item i's part of block c stands
-// in slot i + c (item boundaries and block boundaries both only move forward, so no two collide).
-struct kvc_pg_prefix_parts {
-  int first, count;      // slots
-  int row;               // row within a slot
-};
-__device__ __forceinline__ kvc_pg_prefix_parts pg_prefix_parts(const kvc_pg_args& a, int prefix, int t, int vh, int g) {
-  const int T = a.pre_rows / a.Gv;
-  const int m = (a.n_tokens + T - 1) / T, items = m * a.Hv;
-  const int tiles = prefix > a.pre_tile ? (prefix + a.pre_tile - 1) / a.pre_tile : 1;
-  const int item = vh * m + t / T;
-  int per, stride = tiles;
-  if (items <= a.pre_grid) pg_even(tiles, items, a.pre_grid, 1, &per, &stride);
-  else per = (items * tiles + a.pre_grid - 1) / a.pre_grid;
-  const int c0 = item * stride / per, c1 = (item * stride + tiles - 1) / per;
-  return {item + c0, c1 - c0 + 1, (t % T) * a.Gv + g};
 }
 #endif  // __CUDACC__
