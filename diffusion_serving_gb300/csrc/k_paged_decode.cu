@@ -15,8 +15,9 @@
 //        per 64-dim half would lie free of bank conflicts, where this one's 256-byte rows meet in
 //        pairs; but a copy costs the issuing warp some 80 cycles, and 16 of them a tile, for pages
 //        of 16 slots, are more than HBM leaves time for.)
-//   9    helper: brings the queries of the next items to shared memory, and their shared prefixes'
-//        states, so that neither latency falls between two items.
+//   9    helper: works out the next items for the consumers (their rows' places, limits, extents) and
+//        brings their queries and their shared prefixes' states to shared memory, so that none of it
+//        falls between two items.
 // At an item's end the warps' states meet in shared memory and go straight out, or, where the item
 // spans blocks, to the workspace (pg_finish).
 //
@@ -47,12 +48,17 @@ struct Smem {
   T q[2][R][D + 8];                               // its queries (+ 8: rows on different banks)
   float2 ml[kWarps][R];
   float2 pre_ml[2][R];
+  int64_t at[2][R];                               // rows of the outputs
   int limit[2][R];                                // where each query row's keys end
+  kvc_pg_end end[2];
+  int tiles[2];                                   // this block's tiles of the item; -1: there is none
+  int keys[2];                                    // slots at or behind this hold nothing of the row
   int pos[kStages<D, R>][kTile];                  // slot positions of a stage, INT_MAX: left out
   uint64_t full[kStages<D, R>], empty[kStages<D, R>];
   uint64_t q_full[2], pre_full[2], item_empty[2];
   WaitCtl wc;
-  int flag, abort;
+  int flag;
+  int fail[2];                                    // a consumer's wait gave up: before an item, within it
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
@@ -122,7 +128,10 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     mbar_init(&sm.pre_full[threadIdx.x - 32], 32);
     mbar_init(&sm.item_empty[threadIdx.x - 32], kWarps);
   }
-  if (threadIdx.x == 64) wait_init(&sm.wc, a.stall_ns);
+  if (threadIdx.x == 64) {
+    wait_init(&sm.wc, a.stall_ns);
+    sm.fail[0] = sm.fail[1] = 0;
+  }
   if (threadIdx.x == kWarps * 32) {
     prefetch_map(&tm_k);
     prefetch_map(&tm_v);
@@ -135,8 +144,11 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, gridDim.x);
   int p, p_end;
   if (!sch.range(blockIdx.x, &p, &p_end)) return;
-  kvc_pg_item it = sch.at(a, p);
-  p_end = sch.clip(it, p_end);
+  kvc_pg_item it;
+  if (warp >= kWarps) {
+    it = sch.at(a, p);
+    p_end = sch.clip(it, p_end);
+  }
   const int ps = 1 << a.ps_log2;
   const bool prefix = a.phase == 2 && sch.lo > 0;
 
@@ -145,16 +157,17 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int box_log2 = min(a.ps_log2, 6);                 // slots per box
     const int per_tile = kTile >> box_log2;                 // boxes (of one half and tensor) per tile
     const uint32_t box_bytes = 128u << box_log2;
-    // lane i < per_tile: the table column and page of the tile's ith box
+    // lane i < per_tile: the table column of the tile's ith box and the page number there, not looked at before it is
+    // used (a tile later); column -1: no box
     auto look = [&](const kvc_pg_item& w, int j, int* col, int* page) {
       *col = -1;
-      *page = -1;
+      *page = 0;
       const int key = w.r.lo + j * kTile + (lane << box_log2);
       if (lane < per_tile && key < w.r.len) {
         int c = key >> a.ps_log2;
         if (a.sel != nullptr) c = __ldg(a.sel + ((int64_t)w.b * a.Hkv + w.vh / a.sub) * a.n_sel + c);
         *col = c;
-        if (c >= 0) *page = pg_page(a, w.b, c);
+        if (c >= 0) *page = __ldg(a.table + (int64_t)w.b * a.max_pages + c);
       }
     };
     int t = 0;
@@ -164,17 +177,23 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (; ok && p < p_end;) {
       const int tile0 = p - it.start;
       const int tile1 = min(it.tiles, p_end - it.start);
-      const int kvh = it.vh / a.sub;
+      const int kvh = a.sub == 1 ? it.vh : it.vh / a.sub;
       kvc_pg_item nx = it;
       const bool more = it.start + tile1 < p_end;
       if (more) sch.next(a, nx);
       for (int j = tile0; j < tile1; ++j, ++t) {
-        int ncol = -1, npage = -1;                          // the next tile's, in flight meanwhile
+        int ncol = -1, npage = 0;                           // the next tile's, in flight meanwhile
         if (j + 1 < tile1) look(it, j + 1, &ncol, &npage);
         else if (more) look(nx, 0, &ncol, &npage);
         const int st = t % S;
         if (t >= S) ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[st], (t / S - 1) & 1, wc));
         if (!ok) break;
+        if (col < 0) {
+          page = -1;
+        } else if (page < 0 || page >= a.n_pages) {
+          atomicOr(a.err, KVC_DEV_BAD_PAGE);
+          page = -1;
+        }
         const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) mbar_expect_tx(&sm.full[st], __popc(good) * 2 * HB * box_bytes);
         __syncwarp();
@@ -206,35 +225,54 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   } else if (warp == kWarps + 1) {
     // ---------------- helper: queries and shared prefix of the items to come ----------------
     constexpr int VQ = D / 8;                               // 16-byte vectors of a query row
-    for (int n = 0; p < p_end; ++n) {
+    for (int n = 0;; ++n) {
       const int b = n & 1;
       if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.item_empty[b], (n / 2 - 1) & 1, wc))) break;
-      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
-      const int t0 = it.r.t0 + it.k * sch.T;
-#pragma unroll
-      for (int e = lane; e < R * VQ; e += 32) {
-        const int r = e / VQ, c = e % VQ;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          x = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)(t0 + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv) * D) + c);
-        *reinterpret_cast<uint4*>(&sm.q[b][r][8 * c]) = x;
+      if (p >= p_end) {
+        if (lane == 0) sm.tiles[b] = -1;
+        __syncwarp();
+        mbar_arrive(&sm.q_full[b]);
+        break;
       }
-      if (lane < R)
-        sm.limit[b][lane] = lane >= rows ? 0 : a.sel != nullptr ? a.kv_len[it.b] : pg_limit(a, it.r, it.k * sch.T + lane / a.Gv);
+      const int tile1 = min(it.tiles, p_end - it.start);
+      const kvc_pg_end e = pg_end(a, sch, it);
+      int64_t at = 0;
+      if (lane < R) {
+        at = pg_at(a, sch, it, lane < e.rows ? lane : 0);
+        sm.at[b][lane] = at;
+        sm.limit[b][lane] = lane >= e.rows ? 0 : a.sel != nullptr ? a.kv_len[it.b]
+                                                                  : pg_limit(a, it.r, it.k * sch.T + lane / a.Gv);
+      }
+      if (lane == 0) {
+        sm.end[b] = e;
+        sm.tiles[b] = tile1 - (p - it.start);
+        sm.keys[b] = a.sel != nullptr ? a.kv_len[it.b] : it.r.len;
+      }
+#pragma unroll
+      for (int x = 0; x < R * VQ / 32; ++x) {
+        const int v = lane + 32 * x, r = v / VQ, c = v % VQ;
+        const int64_t row = __shfl_sync(0xffffffffu, at, r);
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (r < e.rows) y = __ldg(reinterpret_cast<const uint4*>(q + row * D) + c);
+        *reinterpret_cast<uint4*>(&sm.q[b][r][8 * c]) = y;
+      }
       mbar_arrive(&sm.q_full[b]);
       if (prefix) {
-        for (int e = lane; e < rows * (D / 4); e += 32) {
-          const int r = e / (D / 4), d = 4 * (e % (D / 4));
-          const int64_t at = (int64_t)(t0 + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv;
-          float2 ml;
-          float4 x;
-          pg_load_prefix<D>(a, at, d, &ml, &x);
-          *reinterpret_cast<float4*>(&sm.pre_o[b][r][d]) = x;
-          if (d == 0) sm.pre_ml[b][r] = ml;
+#pragma unroll
+        for (int x = 0; x < R * D / 128; ++x) {
+          const int v = lane + 32 * x, r = v / (D / 4), d = 4 * (v % (D / 4));
+          const int64_t row = __shfl_sync(0xffffffffu, at, r);
+          if (r < e.rows) {
+            float2 ml;
+            float4 y;
+            pg_load_prefix<D>(a, row, d, &ml, &y);
+            *reinterpret_cast<float4*>(&sm.pre_o[b][r][d]) = y;
+            if (d == 0) sm.pre_ml[b][r] = ml;
+          }
         }
         mbar_arrive(&sm.pre_full[b]);
       }
-      p = it.start + min(it.tiles, p_end - it.start);
+      p = it.start + tile1;
       if (p < p_end) sch.next(a, it);
     }
   } else {
@@ -246,11 +284,14 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const uint32_t row0 = r0 * HB * 128;
     auto bar = [] { named_bar<1>(kWarps * 32); };
     int t = 0;                                              // tiles of this block before the item's
-    for (int n = 0; p < p_end; ++n) {
+    for (int n = 0;; ++n) {
       const int b = n & 1;
-      const int tile0 = p - it.start;
-      const int tile1 = min(it.tiles, p_end - it.start);
       bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / 2) & 1, wc));
+      if (!ok) sm.fail[0] = 1;
+      bar();                                                // (the last item's states have been read, too)
+      if (sm.fail[0]) break;                                // what ends the loop is the same for every consumer
+      const int tiles = sm.tiles[b];
+      if (tiles < 0) break;
       uint32_t qa[D / 16][4];
       int limit[NR];
 #pragma unroll
@@ -264,7 +305,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (x < NR) limit[x] = sm.limit[b][r % R];
       }
       // slots at or behind `end` hold nothing of the row
-      const int end = a.sel != nullptr ? sm.limit[b][0] : it.r.len;
+      const int end = sm.keys[b];
       float o[NT][4];
       float m[NR], l[NR];
 #pragma unroll
@@ -274,7 +315,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         m[x] = -INFINITY;
         l[x] = 0.f;
       }
-      const int t_end = t + tile1 - tile0;
+      const int t_end = t + tiles;
       for (int u = t; ok && u < t_end; ++u) {
         const int st = u % S;
         // Every warp waits for every tile and frees every stage, the other set's too: a wait by parity has to see each
@@ -378,13 +419,13 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
       // ---- the item's end ----
       if (ok && prefix) ok = __all_sync(0xffffffffu, mbar_wait(&sm.pre_full[b], (n / 2) & 1, wc));
-      bar();                                                // (the last item's states have been read)
-      if (threadIdx.x == 0) sm.abort = wc->abort;
+      if (!ok) sm.fail[1] = 1;
 #pragma unroll
       for (int x = 0; x < NR; ++x) {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
         const int r = hq + 8 * x;
+        if (r >= sm.end[b].rows) continue;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const float2 y = NR == 1 ? make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3])
@@ -394,9 +435,10 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (quad == 0) sm.ml[warp][r] = make_float2(m[x], l[x]);
       }
       bar();
-      if (sm.abort) break;                                  // (the same for every consumer)
-      pg_finish<T, D, R, kTile>(
-          a, sch, it, out, &sm.flag, threadIdx.x, kWarps * 32, prefix,
+      if (sm.fail[1]) break;
+      const kvc_pg_end e = sm.end[b];
+      pg_finish<T, D, R>(
+          a, e, out, &sm.flag, threadIdx.x, kWarps * 32, prefix,
           [&](int r, int d, float* Mp, float* Lp) {
             float2 ml[kWarps];
             float M = -INFINITY, L = 0.f;
@@ -420,11 +462,9 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             *ml = sm.pre_ml[b][r];
             *y = *reinterpret_cast<const float4*>(&sm.pre_o[b][r][d]);
           },
-          bar);
+          [&](int r) { return sm.at[b][r]; }, bar);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[b]);
-      p = it.start + tile1;
-      if (p < p_end) sch.next(a, it);
     }
     if (threadIdx.x == 0 && wc->abort) atomicOr(a.err, KVC_DEV_TIMEOUT);
   }

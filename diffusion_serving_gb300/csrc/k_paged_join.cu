@@ -39,10 +39,15 @@ k_paged_join(T* __restrict__ out, int min_tiles, kvc_pg_args a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = 4 * (lane % (D / 4));
   for (int r = blockIdx.y * kWarps + warp; r < rows; r += gridDim.y * kWarps) {
-    const int64_t at = (int64_t)(it.r.t0 + it.k * sch.T + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv;
+    const int64_t at = pg_at(a, sch, it, r);
     float M = -INFINITY, L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (prefix) pg_join(1, M, L, x, [&](int, float2* ml, float4* y) { pg_load_prefix<D>(a, at, d, ml, y); });
+    if (prefix) {
+      float2 ml;
+      float4 y;
+      pg_load_prefix<D>(a, at, d, &ml, &y);
+      pg_join1(M, L, x, ml, y);
+    }
     pg_join(c1 - c0 + 1, M, L, x,
             [&](int i, float2* ml, float4* y) { pg_load_part<R, D>(a.part, 2 * (c0 + i) + (i == 0 ? 1 : 0), r, d, ml, y); });
     if (lane < D / 4) pg_emit<T, D>(a, out, at, d, M, L, x);

@@ -187,18 +187,15 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
       sm.ml[r][1] = l;
     }
     __syncthreads();
-    pg_finish<T, D, kR, kTS>(
-        a, sch, it, out, &sm.flag, tid, kThreads, a.phase == 2 && sch.lo > 0,
+    pg_finish<T, D, kR>(
+        a, pg_end(a, sch, it), out, &sm.flag, tid, kThreads, a.phase == 2 && sch.lo > 0,
         [&](int rr, int d, float* M, float* L) {
           *M = sm.ml[rr][0];
           *L = sm.ml[rr][1];
           return *reinterpret_cast<const float4*>(&sm.o[rr][d]);
         },
-        [&](int rr, int d, float2* ml, float4* y) {
-          const int64_t at = (int64_t)(it.r.t0 + it.k * sch.T + rr / a.Gv) * a.H + it.vh * a.Gv + rr % a.Gv;
-          pg_load_prefix<D>(a, at, d, ml, y);
-        },
-        bar);
+        [&](int rr, int d, float2* ml, float4* y) { pg_load_prefix<D>(a, pg_at(a, sch, it, rr), d, ml, y); },
+        [&](int rr) { return pg_at(a, sch, it, rr); }, bar);
     p = it.start + tile1;
     if (p < p_end) sch.next(a, it);
   }

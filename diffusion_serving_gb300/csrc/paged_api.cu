@@ -73,6 +73,7 @@ kvc_pg_args attend_args(const kvc_paged* c, float* lse, int32_t n_tokens, const 
   a.lse = lse;
   a.n_tokens = n_tokens;
   a.cu = d_cu;
+  a.even = n_tokens / c->cfg.batch;
   a.max_q = d_cu != nullptr ? max_q : n_tokens / c->cfg.batch;
   a.causal = (flags & KVC_CAUSAL) != 0;
   return a;

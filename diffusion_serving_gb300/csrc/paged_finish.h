@@ -59,6 +59,16 @@ __device__ __forceinline__ void pg_join(int n, float& M, float& L, float4& x, Ge
   }
 }
 
+// One more state.
+__device__ __forceinline__ void pg_join1(float& M, float& L, float4& x, float2 ml, const float4& y) {
+  const float top = fmaxf(M, ml.x);
+  const float w0 = pg_weight(M, top), w = pg_weight(ml.x, top);
+  x.x *= w0, x.y *= w0, x.z *= w0, x.w *= w0;
+  L = fmaf(w, ml.y, L * w0);
+  M = top;
+  if (w != 0.f) pg_acc4(x, w, y);
+}
+
 // Partials of R rows: slot i of a buffer, row r.
 template <int R, int D>
 __device__ __forceinline__ void pg_load_part(const float* buf, int64_t i, int r, int d, float2* ml, float4* y) {
@@ -75,56 +85,84 @@ __device__ __forceinline__ void pg_emit(const kvc_pg_args& a, T* out, int64_t at
   if (d == 0 && a.lse != nullptr) a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// The end of an item: this block's state own(r, d, &M, &L) -> O's four dims, for the item's real rows, goes straight
-// out, or is left as a partial where the item spans blocks (and where phase 1 leaves it for kvc_pg_launch_join_prefix).
-// The block that leaves last joins the partials, in their order on the line whichever block it is, so the result does
-// not depend on timing.  Behind a shared prefix, pre(r, d, &ml, &o) is the prefix's state.
-// `threads` threads call it (tid 0 .. threads - 1); bar() separates them; s_flag is an int they share.
-template <typename T, int D, int R, int TS, typename Own, typename Pre, typename Bar>
-__device__ __forceinline__ void pg_finish(const kvc_pg_args& a, const kvc_pg_sched<R, TS>& sch, const kvc_pg_item& it,
-                                          T* out, int* s_flag, int tid, int threads, bool prefix, Own own, Pre pre,
-                                          Bar bar) {
-  const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
-  const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
-  const int cta = blockIdx.x;
-  const bool left = a.phase == 1 || c0 != c1;
-  auto at = [&](int r) { return (int64_t)(it.r.t0 + it.k * sch.T + r / a.Gv) * a.H + it.vh * a.Gv + r % a.Gv; };
-  // phase 1: slot item + block (item and block borders only move forward, so no two collide); else the block's second
+// What the end of an item needs to know of it.
+struct kvc_pg_end {
+  int rows;              // real query rows
+  int c0, c1;            // the blocks it spans
+  int slot;              // where this block leaves its state, if it does
+  bool left;             // it does: the item spans blocks, or phase 1 leaves it for kvc_pg_launch_join_prefix
+};
+template <int R, int TS>
+__device__ __forceinline__ kvc_pg_end pg_end(const kvc_pg_args& a, const kvc_pg_sched<R, TS>& sch, const kvc_pg_item& it) {
+  kvc_pg_end e;
+  e.rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
+  e.c0 = it.start / sch.per;
+  e.c1 = (it.start + it.tiles - 1) / sch.per;
+  e.left = a.phase == 1 || e.c0 != e.c1;
+  // phase 1: item + block (item and block borders only move forward, so no two collide); else the block's second
   // slot for the item that begins in it, its first for one that goes on
-  float* mine = a.phase == 1 ? a.pre + (int64_t)(it.vh * ((it.r.n + sch.T - 1) / sch.T) + it.k + cta) * (R * (D + 2))
-                             : a.part + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (R * (D + 2));
-  for (int v = tid; v < rows * (D / 4); v += threads) {
+  e.slot = a.phase == 1 ? it.vh * ((it.r.n + sch.T - 1) / sch.T) + it.k + (int)blockIdx.x
+                        : 2 * (int)blockIdx.x + ((int)blockIdx.x == e.c0 ? 1 : 0);
+  return e;
+}
+// Row of the outputs [n_tokens * H] for query row r of an item.
+template <int R, int TS>
+__device__ __forceinline__ int64_t pg_at(const kvc_pg_args& a, const kvc_pg_sched<R, TS>& sch, const kvc_pg_item& it, int r) {
+  const int i = r / a.Gv;
+  return (int64_t)(it.r.t0 + it.k * sch.T + i) * a.H + it.vh * a.Gv + r - i * a.Gv;
+}
+
+// The end of an item: this block's state own(r, d, &M, &L) -> O's four dims, for the item's real rows, goes straight
+// out to row at(r), or is left as a partial.  The block that leaves last joins the partials, in their order on the
+// line whichever block it is, so the result does not depend on timing.  Behind a shared prefix, pre(r, d, &ml, &o) is
+// the prefix's state.
+// `threads` threads call it (tid 0 .. threads - 1); bar() separates them; s_flag is an int they share.
+template <typename T, int D, int R, typename Own, typename Pre, typename At, typename Bar>
+__device__ __forceinline__ void pg_finish(const kvc_pg_args& a, const kvc_pg_end& e, T* out, int* s_flag, int tid,
+                                          int threads, bool prefix, Own own, Pre pre, At at, Bar bar) {
+  float* mine = (a.phase == 1 ? a.pre : a.part) + (int64_t)e.slot * (R * (D + 2));
+  for (int v = tid; v < e.rows * (D / 4); v += threads) {
     const int r = v / (D / 4), d = 4 * (v % (D / 4));
     float M, L;
     float4 x = own(r, d, &M, &L);
-    if (left) {
+    if (e.left) {
       *reinterpret_cast<float4*>(mine + r * D + d) = x;
       if (d == 0) *reinterpret_cast<float2*>(mine + R * D + 2 * r) = make_float2(M, L);
       continue;
     }
-    if (prefix) pg_join(1, M, L, x, [&](int, float2* ml, float4* y) { pre(r, d, ml, y); });
+    if (prefix) {
+      float2 ml;
+      float4 y;
+      pre(r, d, &ml, &y);
+      pg_join1(M, L, x, ml, y);
+    }
     pg_emit<T, D>(a, out, at(r), d, M, L, x);
   }
-  if (!left || a.phase == 1) return;
+  if (!e.left || a.phase == 1) return;
   // the partial's stores precede thread 0's release (barrier, then a cumulative release); the last block's loads
   // follow its acquire
   bar();
   if (tid == 0) {
     int prev;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + c0) : "memory");
-    const int last = prev == c1 - c0;
-    if (last) a.tickets[c0] = 0;       // every block of the item is past it
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(a.tickets + e.c0) : "memory");
+    const int last = prev == e.c1 - e.c0;
+    if (last) a.tickets[e.c0] = 0;     // every block of the item is past it
     *s_flag = last;
   }
   bar();
   if (!*s_flag) return;
-  for (int v = tid; v < rows * (D / 4); v += threads) {
+  for (int v = tid; v < e.rows * (D / 4); v += threads) {
     const int r = v / (D / 4), d = 4 * (v % (D / 4));
     float M = -INFINITY, L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (prefix) pg_join(1, M, L, x, [&](int, float2* ml, float4* y) { pre(r, d, ml, y); });
-    pg_join(c1 - c0 + 1, M, L, x,
-            [&](int i, float2* ml, float4* y) { pg_load_part<R, D>(a.part, 2 * (c0 + i) + (i == 0 ? 1 : 0), r, d, ml, y); });
+    if (prefix) {
+      float2 ml;
+      float4 y;
+      pre(r, d, &ml, &y);
+      pg_join1(M, L, x, ml, y);
+    }
+    pg_join(e.c1 - e.c0 + 1, M, L, x,
+            [&](int i, float2* ml, float4* y) { pg_load_part<R, D>(a.part, 2 * (e.c0 + i) + (i == 0 ? 1 : 0), r, d, ml, y); });
     pg_emit<T, D>(a, out, at(r), d, M, L, x);
   }
 }

@@ -54,6 +54,7 @@ struct kvc_pg_args {
   const int32_t* kv_len;
   const int32_t* cu;
   int n_tokens, max_q;
+  int even;                   // tokens per row where cu is null
   int causal, phase;
   float scale_log2;
   float* lse;
@@ -112,9 +113,8 @@ struct kvc_pg_raw {
 };
 __device__ __forceinline__ kvc_pg_raw pg_load(const kvc_pg_args& a, int b) {
   kvc_pg_raw x;
-  const int n = a.cu == nullptr ? a.n_tokens / a.B : 0;
-  x.lo = a.cu == nullptr ? b * n : a.cu[b];
-  x.hi = a.cu == nullptr ? x.lo + n : a.cu[b + 1];
+  x.lo = a.cu == nullptr ? b * a.even : a.cu[b];
+  x.hi = a.cu == nullptr ? x.lo + a.even : a.cu[b + 1];
   x.len = a.kv_len[b];
   x.prefix = a.phase != 0 ? *a.prefix_len : 0;
   return x;
@@ -158,7 +158,7 @@ __device__ __forceinline__ int pg_limit(const kvc_pg_args& a, const kvc_pg_row& 
 // The row that token t of the call belongs to, or -1: binary search in cu, which need not be in
 // order for it to end.
 __device__ __forceinline__ int pg_row_of(const kvc_pg_args& a, int t) {
-  if (a.cu == nullptr) return t / (a.n_tokens / a.B);
+  if (a.cu == nullptr) return t / a.even;
   int lo = 0, hi = a.B;   // the last b with cu[b] <= t
 #pragma unroll 1
   for (int step = 0; step < 11 && hi - lo > 1; ++step) {
@@ -190,6 +190,8 @@ __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int 
 // item gets a whole number of blocks instead: it is padded to `stride` tiles, a multiple of `per`, so
 // that no block works on two.
 __host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int* per, int* stride) {
+  *per = *stride = min_tiles;
+  if (tiles <= min_tiles) return;
   const int chunks = grid / items;
   const int even = (tiles + chunks - 1) / chunks;
   *per = even > min_tiles ? even : min_tiles;
@@ -228,7 +230,7 @@ struct kvc_pg_sched {
   // with KVC_DEV_OVERFLOW (nothing is attended).
   __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles, int grid) {
     n_rows = a.phase == 1 ? 1 : a.B;
-    T = R / a.Gv;
+    T = a.Gv == 1 ? R : R / a.Gv;
     causal = a.causal && a.phase != 1 && a.sel == nullptr;
     stride = 0;
     base = reinterpret_cast<int*>(smem);
@@ -242,7 +244,7 @@ struct kvc_pg_sched {
       rows[3 * b] = r.t0;
       rows[3 * b + 1] = r.n;
       rows[3 * b + 2] = r.len;
-      const int m = (r.n + T - 1) / T;
+      const int m = r.n <= T ? r.n > 0 : (r.n + T - 1) / T;
       if (!causal || m <= 1) base[b + 1] = m == 0 ? 0 : capped((long long)m * pg_item_tiles(r, 0, T, TS, causal));
     }
     __syncthreads();
@@ -261,7 +263,7 @@ struct kvc_pg_sched {
     }
     if (n_rows == 1) {
       const kvc_pg_row r = row(0);
-      const int m = (r.n + T - 1) / T;
+      const int m = r.n <= T ? r.n > 0 : (r.n + T - 1) / T;
       if (!causal || m <= 1) {
         const long long items = (long long)m * a.Hv;
         if (items > 0 && items <= grid) {
@@ -323,7 +325,7 @@ struct kvc_pg_sched {
     }
     it.b = b;
     it.r = row(b);
-    const int m = (it.r.n + T - 1) / T;
+    const int m = it.r.n <= T ? 1 : (it.r.n + T - 1) / T;
     const int group = stride ? m * stride : (base[b + 1] - base[b]) / a.Hv;
     p -= base[b];
     it.vh = p / group;
@@ -332,7 +334,7 @@ struct kvc_pg_sched {
     if (!causal || m == 1) {
       it.tiles = pg_item_tiles(it.r, 0, T, TS, causal);
       const int step = stride ? stride : it.tiles;
-      it.k = p / step;
+      it.k = m == 1 ? 0 : p / step;
       it.start += it.k * step;
       return it;
     }
