@@ -35,7 +35,8 @@ constexpr int kThreads = (kWarps + 2) * 32;       // + producer, helper
 constexpr int kTile = 64;                         // slots per tile: 16 for each of 4 warps
 constexpr uint32_t kHalf = kTile * 128u;          // bytes of 64 dims of a tile
 constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
-constexpr int kMinTiles = 8;
+constexpr int kMinTiles = 8;                      // fewest tiles for a block
+constexpr int kItemCost = 4;                      // an item's beginning and end, in tiles
 
 template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 5 : 3) : (R == 8 ? 10 : 8);
 template <int D> constexpr uint32_t kStageBytes = 2u * (D / 64) * kHalf;   // K and V
@@ -141,14 +142,11 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<R, kTile> sch;
-  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, gridDim.x);
-  int p, p_end;
-  if (!sch.range(blockIdx.x, &p, &p_end)) return;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, kItemCost,
+           gridDim.x);
   kvc_pg_item it;
-  if (warp >= kWarps) {
-    it = sch.at(a, p);
-    p_end = sch.clip(it, p_end);
-  }
+  bool more = false;
+  if (warp >= kWarps) more = sch.first(a, blockIdx.x, it);
   const int ps = 1 << a.ps_log2;
   const bool prefix = a.phase == 2 && sch.lo > 0;
 
@@ -173,14 +171,12 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     int t = 0;
     bool ok = true;
     int col, page;
-    look(it, p - it.start, &col, &page);
-    for (; ok && p < p_end;) {
-      const int tile0 = p - it.start;
-      const int tile1 = min(it.tiles, p_end - it.start);
+    if (more) look(it, it.tile0, &col, &page);
+    for (; ok && more;) {
+      const int tile0 = it.tile0, tile1 = it.tile1;
       const int kvh = a.sub == 1 ? it.vh : it.vh / a.sub;
       kvc_pg_item nx = it;
-      const bool more = it.start + tile1 < p_end;
-      if (more) sch.next(a, nx);
+      more = sch.next(a, nx);
       for (int j = tile0; j < tile1; ++j, ++t) {
         int ncol = -1, npage = 0;                           // the next tile's, in flight meanwhile
         if (j + 1 < tile1) look(it, j + 1, &ncol, &npage);
@@ -216,8 +212,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         col = ncol;
         page = npage;
       }
-      p = it.start + tile1;
-      if (ok && more) it = nx;
+      it = nx;
     }
     if (wc->abort && lane == 0) {   // let every load issued here land before the block releases its shared memory
       for (int i = max(0, t - S); i < t; ++i) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
@@ -228,13 +223,12 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int n = 0;; ++n) {
       const int b = n & 1;
       if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.item_empty[b], (n / 2 - 1) & 1, wc))) break;
-      if (p >= p_end) {
+      if (!more) {
         if (lane == 0) sm.tiles[b] = -1;
         __syncwarp();
         mbar_arrive(&sm.q_full[b]);
         break;
       }
-      const int tile1 = min(it.tiles, p_end - it.start);
       const kvc_pg_end e = pg_end(a, sch, it);
       int64_t at = 0;
       if (lane < R) {
@@ -245,35 +239,47 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       if (lane == 0) {
         sm.end[b] = e;
-        sm.tiles[b] = tile1 - (p - it.start);
+        sm.tiles[b] = it.tile1 - it.tile0;
         sm.keys[b] = a.sel != nullptr ? a.kv_len[it.b] : it.r.len;
       }
+      // every load is issued before any is stored
+      constexpr int NQ = R * VQ / 32, NP = R * D / 128;
+      uint4 qv[NQ];
+      float4 pv[NP];
+      float2 pm = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int x = 0; x < R * VQ / 32; ++x) {
+      for (int x = 0; x < NQ; ++x) {
         const int v = lane + 32 * x, r = v / VQ, c = v % VQ;
         const int64_t row = __shfl_sync(0xffffffffu, at, r);
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (r < e.rows) y = __ldg(reinterpret_cast<const uint4*>(q + row * D) + c);
-        *reinterpret_cast<uint4*>(&sm.q[b][r][8 * c]) = y;
+        qv[x] = make_uint4(0, 0, 0, 0);
+        if (r < e.rows) qv[x] = __ldg(reinterpret_cast<const uint4*>(q + row * D) + c);
+      }
+      if (prefix) {
+        if (lane < e.rows) pm = __ldcg(a.pre_ml + at);
+#pragma unroll
+        for (int x = 0; x < NP; ++x) {
+          const int v = lane + 32 * x, r = v / (D / 4), d = 4 * (v % (D / 4));
+          const int64_t row = __shfl_sync(0xffffffffu, at, r);
+          pv[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < e.rows) pv[x] = __ldcg(reinterpret_cast<const float4*>(a.pre_o + row * D + d));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+        const int v = lane + 32 * x;
+        *reinterpret_cast<uint4*>(&sm.q[b][v / VQ][8 * (v % VQ)]) = qv[x];
       }
       mbar_arrive(&sm.q_full[b]);
       if (prefix) {
+        if (lane < R) sm.pre_ml[b][lane] = pm;
 #pragma unroll
-        for (int x = 0; x < R * D / 128; ++x) {
-          const int v = lane + 32 * x, r = v / (D / 4), d = 4 * (v % (D / 4));
-          const int64_t row = __shfl_sync(0xffffffffu, at, r);
-          if (r < e.rows) {
-            float2 ml;
-            float4 y;
-            pg_load_prefix<D>(a, row, d, &ml, &y);
-            *reinterpret_cast<float4*>(&sm.pre_o[b][r][d]) = y;
-            if (d == 0) sm.pre_ml[b][r] = ml;
-          }
+        for (int x = 0; x < NP; ++x) {
+          const int v = lane + 32 * x;
+          *reinterpret_cast<float4*>(&sm.pre_o[b][v / (D / 4)][4 * (v % (D / 4))]) = pv[x];
         }
         mbar_arrive(&sm.pre_full[b]);
       }
-      p = it.start + tile1;
-      if (p < p_end) sch.next(a, it);
+      more = sch.next(a, it);
     }
   } else {
     // ---------------- consumers ----------------

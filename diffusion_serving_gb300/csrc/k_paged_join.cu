@@ -17,17 +17,18 @@ constexpr int kRowBlocks = 8;             // blocks per split item
 // there is one.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-k_paged_join(T* __restrict__ out, int min_tiles, kvc_pg_args a) {
+k_paged_join(T* __restrict__ out, kvc_pg_args a) {
   constexpr int R = KVC_PG_TC_ROWS;
   extern __shared__ __align__(16) uint8_t smem[];
   kvc_pg_sched<R, KVC_PG_TC_TILE> sch;
-  sch.init(a, smem, min_tiles, KVC_PG_GRID);
-  int p, end;
-  const bool any = sch.range(blockIdx.x, &p, &end) && end < sch.total;
+  sch.init(a, smem, KVC_PG_TC_MIN, KVC_PG_TC_COST, KVC_PG_GRID);
+  // the item at the end of the block's stretch
+  const long long end = (long long)(blockIdx.x + 1) * sch.per;
+  const bool any = end < sch.total;
   kvc_pg_item it;
   int c0 = 0, c1 = 0;
   if (any) {
-    it = sch.at(a, end - 1);
+    it = sch.at(a, (int)end - 1);
     c0 = it.start / sch.per;
     c1 = (it.start + it.tiles - 1) / sch.per;
   }
@@ -58,7 +59,7 @@ k_paged_join(T* __restrict__ out, int min_tiles, kvc_pg_args a) {
 // it, follows from the prefix length.
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads)
-k_paged_join_prefix(int TS, int grid, kvc_pg_args a) {
+k_paged_join_prefix(int TS, int cost, int grid, kvc_pg_args a) {
   const int T = R / a.Gv, m = (a.n_tokens + T - 1) / T, items = m * a.Hv;
   const int prefix = *a.prefix_len;
   const int tiles = prefix > TS ? (prefix + TS - 1) / TS : 1;
@@ -68,13 +69,18 @@ k_paged_join_prefix(int TS, int grid, kvc_pg_args a) {
   kvc_pdl_wait();
   kvc_pdl_release();
   if (prefix <= 0 || !pg_prefix_ok(a, prefix) || r >= T * a.Gv) return;
-  int per, stride = tiles;
-  if (items <= grid) pg_even(tiles, items, grid, 1, &per, &stride);
-  else per = max(1, (items * tiles + grid - 1) / grid);
+  // (as kvc_pg_sched has it)
+  int per, stride = tiles + cost, lead = cost;
+  if (items <= grid) {
+    pg_even(tiles, items, grid, 1, &per, &stride);
+    lead = 0;
+  } else {
+    per = (items * stride + grid - 1) / grid;
+  }
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int vh = item / m, t = (item % m) * T + r / a.Gv;
     if (t >= a.n_tokens) continue;
-    const int c0 = item * stride / per, c1 = (item * stride + tiles - 1) / per;
+    const int c0 = (item * stride + lead) / per, c1 = (item * stride + lead + tiles - 1) / per;
     float M = -INFINITY, L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     pg_join(c1 - c0 + 1, M, L, x,
@@ -86,29 +92,33 @@ k_paged_join_prefix(int TS, int grid, kvc_pg_args a) {
 }
 
 template <int D>
-cudaError_t launch_prefix(const kvc_pg_args& a, int R, int TS, int grid, cudaStream_t s) {
+cudaError_t launch_prefix(const kvc_pg_args& a, int R, int TS, int cost, int grid, cudaStream_t s) {
   const int T = R / a.Gv;
   const int64_t items = (int64_t)a.Hv * ((a.n_tokens + T - 1) / T);
   const unsigned gx = (unsigned)(items < 4 * KVC_PG_GRID ? items : 4 * KVC_PG_GRID);
   if (R == KVC_PG_TC_ROWS)
-    return kvc_launch_pdl(k_paged_join_prefix<D, KVC_PG_TC_ROWS>, dim3(gx, R / kWarps), dim3(kThreads), 0, s, TS, grid, a);
-  return kvc_launch_pdl(k_paged_join_prefix<D, KVC_PG_SIMT_ROWS>, dim3(gx, R / kWarps), dim3(kThreads), 0, s, TS, grid, a);
+    return kvc_launch_pdl(k_paged_join_prefix<D, KVC_PG_TC_ROWS>, dim3(gx, R / kWarps), dim3(kThreads), 0, s, TS, cost,
+                          grid, a);
+  return kvc_launch_pdl(k_paged_join_prefix<D, KVC_PG_SIMT_ROWS>, dim3(gx, R / kWarps), dim3(kThreads), 0, s, TS, cost,
+                          grid, a);
 }
 
 template <typename T, int D>
-cudaError_t launch(const kvc_pg_args& a, int min_tiles, void* out, cudaStream_t s) {
+cudaError_t launch(const kvc_pg_args& a, void* out, cudaStream_t s) {
   return kvc_launch_pdl(k_paged_join<T, D>, dim3(KVC_PG_GRID, kRowBlocks), dim3(kThreads), pg_sched_bytes(a.B), s,
-                        (T*)out, min_tiles, a);
+                        (T*)out, a);
 }
 
 }  // namespace
 
-cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, int R, int TS, int grid, cudaStream_t s) {
-  return c->cfg.head_dim == 64 ? launch_prefix<64>(a, R, TS, grid, s) : launch_prefix<128>(a, R, TS, grid, s);
+cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, bool simt, cudaStream_t s) {
+  const int R = simt ? KVC_PG_SIMT_ROWS : KVC_PG_TC_ROWS, TS = simt ? KVC_PG_SIMT_TILE : KVC_PG_TC_TILE;
+  const int cost = simt ? 1 : KVC_PG_TC_COST, grid = simt ? KVC_PG_GRID_SIMT : KVC_PG_GRID;
+  return c->cfg.head_dim == 64 ? launch_prefix<64>(a, R, TS, cost, grid, s) : launch_prefix<128>(a, R, TS, cost, grid, s);
 }
 
-cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, int min_tiles, void* out, cudaStream_t s) {
+cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, void* out, cudaStream_t s) {
   const bool d64 = c->cfg.head_dim == 64;
-  if (c->cfg.dtype == KVC_F16) return d64 ? launch<__half, 64>(a, min_tiles, out, s) : launch<__half, 128>(a, min_tiles, out, s);
-  return d64 ? launch<__nv_bfloat16, 64>(a, min_tiles, out, s) : launch<__nv_bfloat16, 128>(a, min_tiles, out, s);
+  if (c->cfg.dtype == KVC_F16) return d64 ? launch<__half, 64>(a, out, s) : launch<__half, 128>(a, out, s);
+  return d64 ? launch<__nv_bfloat16, 64>(a, out, s) : launch<__nv_bfloat16, 128>(a, out, s);
 }

@@ -54,18 +54,15 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<kR, kTS> sch;
-  sch.init(a, smem + ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15), 1, gridDim.x);
+  sch.init(a, smem + ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15), 1, 1, gridDim.x);
   const int tid = threadIdx.x;
   const int r = tid / kLanes, ln = tid % kLanes;
-  int p, p_end;
-  if (!sch.range(blockIdx.x, &p, &p_end)) return;
-  kvc_pg_item it = sch.at(a, p);
-  p_end = sch.clip(it, p_end);
+  kvc_pg_item it;
+  if (!sch.first(a, blockIdx.x, it)) return;
   const int ps = 1 << a.ps_log2;
   auto bar = [] { __syncthreads(); };
-  for (; p < p_end;) {
-    const int tile0 = p - it.start;
-    const int tile1 = min(it.tiles, p_end - it.start);
+  for (bool more = true; more; more = sch.next(a, it)) {
+    const int tile0 = it.tile0, tile1 = it.tile1;
     const int n_tok = min(sch.T, it.r.n - it.k * sch.T);
     const int rows = n_tok * a.Gv;
     __syncthreads();
@@ -196,8 +193,6 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
         },
         [&](int rr, int d, float2* ml, float4* y) { pg_load_prefix<D>(a, pg_at(a, sch, it, rr), d, ml, y); },
         [&](int rr) { return pg_at(a, sch, it, rr); }, bar);
-    p = it.start + tile1;
-    if (p < p_end) sch.next(a, it);
   }
 }
 

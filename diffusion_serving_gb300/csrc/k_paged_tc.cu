@@ -207,7 +207,7 @@ __device__ __forceinline__ float exp_pack_store(const uint32_t* sr, int valid, f
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-           const __grid_constant__ CUtensorMap tm_v, T* __restrict__ out, int min_tiles, kvc_pg_args a) {
+           const __grid_constant__ CUtensorMap tm_v, T* __restrict__ out, kvc_pg_args a) {
   constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
   constexpr int HB = D / 64;
   extern __shared__ uint8_t raw[];
@@ -264,14 +264,11 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<kBM, kBN> sch;
-  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), min_tiles, gridDim.x);
-  int p = 0, p_end = 0;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), a.phase == 1 ? 1 : KVC_PG_TC_MIN,
+           KVC_PG_TC_COST, gridDim.x);
   const int ps = 1 << a.ps_log2;
   kvc_pg_item it;
-  if (sch.range(blockIdx.x, &p, &p_end)) {
-    it = sch.at(a, p);
-    p_end = sch.clip(it, p_end);
-  }
+  bool more = sch.first(a, blockIdx.x, it);
 
   if (warp == 0 || warp == 3) {
     // ---------------- TMA producers: warp 0 Q and K, warp 3 V ----------------
@@ -290,14 +287,12 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     };
     int t = 0, n = 0, q_issued = 0;
     bool ok = true;
-    int page = p < p_end ? look(it, p - it.start) : -1;
-    for (; ok && p < p_end;) {
-      const int tile0 = p - it.start;
-      const int tile1 = min(it.tiles, p_end - it.start);
+    int page = more ? look(it, it.tile0) : -1;
+    for (; ok && more;) {
+      const int tile0 = it.tile0, tile1 = it.tile1;
       const int kvh = it.vh / a.sub;
       kvc_pg_item nx = it;
-      const bool more = it.start + tile1 < p_end;
-      if (more) sch.next(a, nx);
+      more = sch.next(a, nx);
       if (kq) {
         if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_free, (n - 1) & 1, wc));   // the last item's last QK
         if (!ok) break;
@@ -334,9 +329,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         if (lane != 0) mbar_arrive(full);
         page = npage;
       }
-      p = it.start + tile1;
       ++n;
-      if (ok && more) it = nx;
+      it = nx;
     }
     if (wc->abort && lane == 0) {
       // every load this warp issued lands before the CTA's shared memory is released
@@ -350,9 +344,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     constexpr uint32_t kIdQK = idesc_f16(kBf16 ? 1u : 0u, 0, kBN);
     int t = 0, n = 0;
     bool ok = true;
-    for (; ok && p < p_end;) {
-      const int tile0 = p - it.start;
-      const int tile1 = min(it.tiles, p_end - it.start);
+    for (; ok && more; more = sch.next(a, it)) {
+      const int tile0 = it.tile0, tile1 = it.tile1;
       ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, n & 1, wc));
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int st = t % kKStages, sb = t % kSBufs;
@@ -375,9 +368,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         __syncwarp();
       }
-      p = it.start + tile1;
       ++n;
-      if (ok && p < p_end) sch.next(a, it);
     }
     if (wc->abort && lane == 0) {
       mma_commit(&sm.drain[0]);
@@ -390,9 +381,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const int box_log2 = min(a.ps_log2, 6);
     int t = 0, n = 0;
     bool ok = true;
-    for (; ok && p < p_end;) {
-      const int tile0 = p - it.start;
-      const int tile1 = min(it.tiles, p_end - it.start);
+    for (; ok && more; more = sch.next(a, it)) {
+      const int tile0 = it.tile0, tile1 = it.tile1;
       if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (n - 1) & 1, wc));   // the epilogue has read O
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int st = t % kVStages, sb = t % kSBufs;
@@ -427,9 +417,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         __syncwarp();
       }
-      p = it.start + tile1;
       ++n;
-      if (ok && p < p_end) sch.next(a, it);
     }
     if (wc->abort && lane == 0) {
       mma_commit(&sm.drain[1]);
@@ -447,9 +435,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const int prefix = a.phase == 2 ? sch.lo : 0;
     int t = 0, n = 0;
     bool ok = true;
-    for (; ok && p < p_end;) {
-      const int tile0 = p - it.start;
-      const int tile1 = min(it.tiles, p_end - it.start);
+    for (; ok && more; more = sch.next(a, it)) {
+      const int tile0 = it.tile0, tile1 = it.tile1;
       const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
       const int i_tok = it.k * sch.T + r / a.Gv;
       // where this row's keys end; rows that are not there see everything (no mask on their account)
@@ -601,9 +588,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free);
-      p = it.start + tile1;
       ++n;
-      if (p < p_end) sch.next(a, it);
     }
   }
 
@@ -633,13 +618,11 @@ cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void
   CUtensorMap tm_q;
   const uint32_t box[4] = {64, (uint32_t)a.Gv, (uint32_t)(kBM / a.Gv), 1};
   if (!kvc_make_box_map(&tm_q, c->cfg.dtype, q, D, a.H, a.n_tokens, 1, box)) return cudaErrorInvalidValue;
-  // a part below two tiles costs more in joining than it saves; a shared prefix is always cut evenly
-  const int min_tiles = a.phase == 1 ? 1 : 2;
   const int rows = a.phase == 1 ? 1 : a.B;
   const cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
-                                 c->tm_k, c->tm_v, (T*)out, min_tiles, a);
+                                 c->tm_k, c->tm_v, (T*)out, a);
   if (e != cudaSuccess || a.phase == 1) return e;
-  return kvc_pg_launch_join(c, a, min_tiles, out, s);
+  return kvc_pg_launch_join(c, a, out, s);
 }
 
 cudaError_t dispatch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prep) {

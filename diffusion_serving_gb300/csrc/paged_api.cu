@@ -226,18 +226,16 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   if (n_tokens > c->cfg.max_tokens) return KVC_ERR_RANGE;
   // the prefix's tiles, over all items, are counted in 32 bits
   const int64_t items = (int64_t)c->Hv * (n_tokens / (KVC_PG_SIMT_ROWS / c->Gv) + 1);
-  if (items * ((int64_t)prefix_pages * c->cfg.page_size / KVC_PG_SIMT_TILE + 1) > INT32_MAX - 65536) return KVC_ERR_RANGE;
+  if (items * ((int64_t)prefix_pages * c->cfg.page_size / KVC_PG_SIMT_TILE + 1 + KVC_PG_TC_COST) > INT32_MAX - 65536) return KVC_ERR_RANGE;
   kvc_pg_args a = attend_args(c, d_lse, n_tokens, d_cu, max_q, flags);
   a.prefix_pages = d_prefix_pages;
   a.prefix_cap = prefix_pages;
   a.prefix_len = d_prefix_len;
-  const bool simt = simt_only(c, flags);
   cudaStream_t s = as_stream(stream);
   a.phase = 1;
   cudaError_t e = run_attend(c, a, q, out, flags, s);
   if (e == cudaSuccess)
-    e = kvc_pg_launch_join_prefix(c, a, simt ? KVC_PG_SIMT_ROWS : KVC_PG_TC_ROWS, simt ? KVC_PG_SIMT_TILE : KVC_PG_TC_TILE,
-                                  simt ? KVC_PG_GRID_SIMT : KVC_PG_GRID, s);
+    e = kvc_pg_launch_join_prefix(c, a, simt_only(c, flags), s);
   if (e != cudaSuccess) return KVC_ERR_CUDA;
   a.phase = 2;
   return launched(run_attend(c, a, q, out, flags, s));

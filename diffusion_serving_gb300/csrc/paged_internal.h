@@ -83,10 +83,10 @@ cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int fir
                                  cudaStream_t s);
 cudaError_t kvc_pg_launch_decode(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
 cudaError_t kvc_pg_launch_tc(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
-// Phase 1's partials (R rows an item, TS slots a tile, `grid` blocks) joined to one state per token and head.
-cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, int R, int TS, int grid, cudaStream_t s);
+// Phase 1's partials joined to one state per token and head; `simt`: phase 1 ran in the FMA kernel.
+cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, bool simt, cudaStream_t s);
 // Split items of the tensor-core kernel.
-cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, int min_tiles, void* out, cudaStream_t s);
+cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, void* out, cudaStream_t s);
 // Shared-memory opt-ins of the kernels a handle may launch, once per handle.
 cudaError_t kvc_pg_prepare_simt(const kvc_paged* c);
 cudaError_t kvc_pg_prepare_select(const kvc_paged* c);
@@ -95,6 +95,9 @@ cudaError_t kvc_pg_prepare_tc(const kvc_paged* c);
 // query rows per item and slots per tile of the tensor-core kernel
 #define KVC_PG_TC_ROWS 128
 #define KVC_PG_TC_TILE 128
+// fewest tiles for a block (a shared prefix is always cut evenly), and what an item's beginning and end cost, in tiles
+#define KVC_PG_TC_MIN 2
+#define KVC_PG_TC_COST 3
 // partial rows per item and slots per tile of the FMA kernel
 #define KVC_PG_SIMT_ROWS 16
 #define KVC_PG_SIMT_TILE 64
@@ -181,14 +184,15 @@ __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int 
 // ---- work ------------------------------------------------------------------------------
 // An item is the R query rows (T = R / Gv tokens x Gv heads) of one (row, group) and token tile;
 // it takes tiles of TS slots, at least one (an item without keys still writes its output).
-// All items' tiles stand in one line, rows outermost, then groups, then token tiles; block c
-// takes the tiles [c * per, (c + 1) * per) of that line, so every block streams the same amount
-// whatever the rows' lengths, and an item that spans several blocks is joined from their
-// partials.  Rows' totals are summed up in shared memory by every block.
+// All items stand in one line, rows outermost, then groups, then token tiles, each as `cost` empty
+// places (what beginning and ending an item costs, in tiles) and then its tiles; block c takes the
+// stretch [c * per, (c + 1) * per) of that line, so every block has the same to do whatever the rows'
+// lengths, and an item that spans several blocks is joined from their partials.  Rows' totals are
+// summed up in shared memory by every block.
 //
-// Where all items are alike (one row, no causal cut) and there are no more of them than blocks, each
-// item gets a whole number of blocks instead: it is padded to `stride` tiles, a multiple of `per`, so
-// that no block works on two.
+// Where there are no more items than blocks, and they are alike or short, each item gets a whole
+// number of blocks instead: it is padded to `stride` places, a multiple of `per` (no empty ones), so
+// that no block works on two and no item is cut without need.
 __host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int* per, int* stride) {
   *per = *stride = min_tiles;
   if (tiles <= min_tiles) return;
@@ -208,50 +212,52 @@ __device__ __forceinline__ int pg_item_tiles(const kvc_pg_row& r, int k, int T, 
 struct kvc_pg_item {
   int b, vh, k;          // row, group, token tile
   int tiles, start;      // its tiles, the first one's place on the line
+  int tile0, tile1;      // those of this block
   kvc_pg_row r;
 };
 
-// Shared memory of the sums: rows + 1 first tiles, then each row's (t0, n, len).
+// Shared memory of the sums: rows + 1 first places, then each row's (t0, n, len).
 __host__ __device__ inline size_t pg_sched_bytes(int B) { return ((size_t)(4 * B + 1) * 4 + 15) & ~(size_t)15; }
 
 template <int R, int TS>
 struct kvc_pg_sched {
-  int* base;             // [rows + 1] first tile of each row
+  int* base;             // [rows + 1] first place of each row
   int* rows;             // [rows][3]
   int n_rows, T, lo;     // lo: where the rows' own keys begin (behind a shared prefix, or 0)
   bool causal;
-  int total, per, stride;    // stride: tiles between items' beginnings where they are padded, else 0
+  int total, per, stride, cost;   // stride: places between items' beginnings where they are padded, else 0
+  int end;               // of this block's stretch
 
   __device__ __forceinline__ kvc_pg_row row(int b) const {
     return kvc_pg_row{rows[3 * b], rows[3 * b + 1], rows[3 * b + 2], min(lo, rows[3 * b + 2])};
   }
+  __device__ __forceinline__ int token_tiles(int n) const { return n <= T ? n > 0 : (n + T - 1) / T; }
 
   // Every thread of the block calls it (it holds barriers).  A line too long for 32 bits is refused
   // with KVC_DEV_OVERFLOW (nothing is attended).
-  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles, int grid) {
+  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles, int item_cost, int grid) {
     n_rows = a.phase == 1 ? 1 : a.B;
     T = a.Gv == 1 ? R : R / a.Gv;
     causal = a.causal && a.phase != 1 && a.sel == nullptr;
-    stride = 0;
     base = reinterpret_cast<int*>(smem);
     rows = base + n_rows + 1;
     lo = a.phase == 2 ? max(0, *a.prefix_len) : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // a row's tiles over its token tiles, per group; -1: more than 32 bits hold
+    // base[b + 1]: the row's tiles over its token tiles, per group; -1: more than 32 bits hold
     auto capped = [&](long long x) { return x <= 0x7fffffffll ? (int)x : -1; };
     for (int b = threadIdx.x; b < n_rows; b += blockDim.x) {
       const kvc_pg_row r = pg_row(a, b);
       rows[3 * b] = r.t0;
       rows[3 * b + 1] = r.n;
       rows[3 * b + 2] = r.len;
-      const int m = r.n <= T ? r.n > 0 : (r.n + T - 1) / T;
+      const int m = token_tiles(r.n);
       if (!causal || m <= 1) base[b + 1] = m == 0 ? 0 : capped((long long)m * pg_item_tiles(r, 0, T, TS, causal));
     }
     __syncthreads();
     if (causal) {
       for (int b = warp; b < n_rows; b += blockDim.x >> 5) {
         const kvc_pg_row r = row(b);
-        const int m = (r.n + T - 1) / T;
+        const int m = token_tiles(r.n);
         if (m <= 1) continue;
         long long x = 0;
         for (int k = lane; k < m; k += 32) x += pg_item_tiles(r, k, T, TS, true);
@@ -261,59 +267,74 @@ struct kvc_pg_sched {
       }
       __syncthreads();
     }
-    if (n_rows == 1) {
-      const kvc_pg_row r = row(0);
-      const int m = r.n <= T ? r.n > 0 : (r.n + T - 1) / T;
-      if (!causal || m <= 1) {
-        const long long items = (long long)m * a.Hv;
-        if (items > 0 && items <= grid) {
-          pg_even(pg_item_tiles(r, 0, T, TS, causal), (int)items, grid, min_tiles, &per, &stride);
-          total = (int)items * stride;
-          if (threadIdx.x == 0) {
-            base[0] = 0;
-            base[1] = total;
-          }
-          __syncthreads();
-          return;
-        }
-      }
+    // every warp works out the same sums (no warp has to hand them on)
+    long long tiles = 0, items = 0;
+    int most = 0;
+    bool over = false;
+    for (int b = lane; b < n_rows; b += 32) {
+      const int x = base[b + 1];
+      over = over || x < 0;
+      const kvc_pg_row r = row(b);
+      const int m = token_tiles(r.n);
+      tiles += x;
+      items += m;
+      if (m > 0) most = max(most, pg_item_tiles(r, m - 1, T, TS, causal));
     }
+    if (n_rows > 1) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      }
+    } else {
+      tiles = __shfl_sync(0xffffffffu, tiles, 0);
+      items = __shfl_sync(0xffffffffu, items, 0);
+      most = __shfl_sync(0xffffffffu, most, 0);
+    }
+    tiles *= a.Hv;
+    items *= a.Hv;
+    over = __any_sync(0xffffffffu, over) || tiles + items * item_cost > 0x7fffffffll - 65536;
+    stride = 0;
+    cost = item_cost;
+    if (over) {
+      if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_OVERFLOW);
+      total = 0;
+      per = 1;
+      return;
+    }
+    if (items > 0 && items <= grid && (most <= 2 * min_tiles || most * items * 4 <= 5 * tiles)) {
+      pg_even(most, (int)items, grid, min_tiles, &per, &stride);
+      cost = 0;
+      total = (int)items * stride;
+    } else {
+      total = (int)(tiles + items * cost);
+      per = max(min_tiles, (total + grid - 1) / grid);
+    }
+    __syncthreads();                       // (every warp has read the rows' own tiles)
     if (warp == 0) {
-      long long carry = 0;
-      bool over = false;
+      int carry = 0;
       for (int b0 = 0; b0 < n_rows; b0 += 32) {
         const int b = b0 + lane;
-        long long x = b < n_rows ? base[b + 1] : 0;
-        over = over || x < 0;
-        x *= a.Hv;
+        int x = 0;
+        if (b < n_rows) {
+          const int m = token_tiles(rows[3 * b + 1]);
+          x = a.Hv * (stride ? m * stride : base[b + 1] + m * cost);
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
           if (lane >= o) x += y;
         }
-        if (b < n_rows) base[b + 1] = (int)(carry + x);
+        if (b < n_rows) base[b + 1] = carry + x;
         carry += __shfl_sync(0xffffffffu, x, 31);
       }
-      over = __any_sync(0xffffffffu, over) || carry > 0x7fffffffll - 65536;
-      if (lane == 0) {
-        base[0] = over ? -1 : 0;
-        if (over) atomicOr(a.err, KVC_DEV_OVERFLOW);
-      }
+      if (lane == 0) base[0] = 0;
     }
     __syncthreads();
-    total = base[0] < 0 ? 0 : base[n_rows];
-    per = max(min_tiles, (total + grid - 1) / grid);
   }
 
-  // The tiles [*p, *end) of block c; false if there are none.
-  __device__ __forceinline__ bool range(int c, int* p, int* end) const {
-    if ((long long)c * per >= total) return false;
-    *p = c * per;
-    *end = total - *p > per ? *p + per : total;
-    return true;
-  }
-
-  // The item that holds tile p of the line (p < total); a whole warp calls it.
+  // The item that holds place p of the line (p < total); a whole warp calls it.
   __device__ __forceinline__ kvc_pg_item at(const kvc_pg_args& a, int p) const {
     kvc_pg_item it;
     int b = 0, hi = n_rows;
@@ -325,26 +346,26 @@ struct kvc_pg_sched {
     }
     it.b = b;
     it.r = row(b);
-    const int m = it.r.n <= T ? 1 : (it.r.n + T - 1) / T;
+    const int m = token_tiles(it.r.n);
     const int group = stride ? m * stride : (base[b + 1] - base[b]) / a.Hv;
     p -= base[b];
     it.vh = p / group;
     it.start = base[b] + it.vh * group;
     p -= it.vh * group;
-    if (!causal || m == 1) {
-      it.tiles = pg_item_tiles(it.r, 0, T, TS, causal);
-      const int step = stride ? stride : it.tiles;
+    if (stride || !causal || m == 1) {
+      const int step = stride ? stride : pg_item_tiles(it.r, 0, T, TS, causal) + cost;
       it.k = m == 1 ? 0 : p / step;
-      it.start += it.k * step;
+      it.start += it.k * step + cost;
+      it.tiles = pg_item_tiles(it.r, it.k, T, TS, causal);
       return it;
     }
     const int lane = threadIdx.x & 31;
-    int before = 0;                        // tiles of the token tiles up to k0
+    int before = 0;                        // places of the token tiles up to k0
     it.k = 0;
     it.tiles = 1;
     for (int k0 = 0; k0 < m; k0 += 32) {
-      int x = k0 + lane < m ? pg_item_tiles(it.r, k0 + lane, T, TS, true) : 0;
-      const int mine = x;
+      const int mine = k0 + lane < m ? pg_item_tiles(it.r, k0 + lane, T, TS, true) : 0;
+      int x = mine > 0 ? mine + cost : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -363,14 +384,21 @@ struct kvc_pg_sched {
     return it;
   }
 
-  // Block c's end within the padded line: a block of a padded item stops where the item's tiles do.
-  __device__ __forceinline__ int clip(const kvc_pg_item& it, int end) const {
-    return stride ? min(end, it.start + it.tiles) : end;
+  // Block c's first item; false if it has none.  A whole warp calls it.
+  __device__ __forceinline__ bool first(const kvc_pg_args& a, int c, kvc_pg_item& it) {
+    if ((long long)c * per >= total) return false;
+    const int p = c * per;
+    end = total - p > per ? p + per : total;
+    it = at(a, p);
+    it.tile0 = max(0, p - it.start);
+    it.tile1 = min(it.tiles, end - it.start);
+    return it.tile1 > it.tile0;            // (not if the stretch ends before the item's tiles begin)
   }
 
-  // The item behind `it` (there is one, and the line is not padded).
-  __device__ __forceinline__ void next(const kvc_pg_args& a, kvc_pg_item& it) const {
-    it.start += it.tiles;
+  // The block's next item; false if there is none.
+  __device__ __forceinline__ bool next(const kvc_pg_args& a, kvc_pg_item& it) const {
+    if (stride || it.start + it.tiles + cost >= end) return false;
+    it.start += it.tiles + cost;
     if ((it.k + 1) * T < it.r.n) {
       ++it.k;
     } else {
@@ -378,12 +406,15 @@ struct kvc_pg_sched {
       if (++it.vh == a.Hv) {
         it.vh = 0;
         ++it.b;
-        for (; it.b + 1 < n_rows && base[it.b + 1] == it.start; ++it.b) {
+        for (; it.b + 1 < n_rows && base[it.b + 1] == it.start - cost; ++it.b) {
         }
         it.r = row(it.b);
       }
     }
     it.tiles = pg_item_tiles(it.r, it.k, T, TS, causal);
+    it.tile0 = 0;
+    it.tile1 = min(it.tiles, end - it.start);
+    return true;
   }
 };
 
