@@ -1,16 +1,22 @@
 // Which pages a token attends: scores from the pages' key bounds, then the n_select best.
 //
 //   U(page) = max over the group's heads g of sum_d max(q_gd hi_d, q_gd lo_d)
+//           = max over g of (q_g+ . hi + q_g- . lo),  q+ = max(q, 0), q- = min(q, 0),
 // bounds every score q_g . k of the page's keys from above.
 //
-// k_paged_score writes U in fp32 for every (row, kv head, page): a warp per page.  HBM-bound: it
-// reads each page's bounds once, 1 / page_size of the bytes of the keys and values themselves.
+// k_paged_score_mma (16-bit stores) takes the second form: a product of [q+ q-] with a page's 2 D
+// bounds, by warp-level MMAs, heads in M and pages in N.  It is HBM-bound: each page's bounds are
+// read once, 1 / page_size of the bytes of its keys and values.  The order of the contraction is free,
+// so a lane takes 8 dims of a page in one 16-byte load, and the queries are laid out to match.
+// k_paged_score does fp32 stores with FMAs, a warp per page.
 //
-// k_paged_rank, a block per (row, kv head), finds the n_select largest by radix selection on the
-// fp32 scores, a byte a pass.  Rounding could swap pages whose scores nearly agree, so it decides
-// nothing: with |error| <= delta, a page more than 2 delta above the last one taken is in, one more
-// than 2 delta below is out, and those between (mostly the last one alone, and then nothing is left
-// to decide) are scored again in fp64 and ranked by that, equal ones by column.
+// k_paged_rank, a block per (row, kv head), takes the n_select largest.  Rounding could swap pages
+// whose scores nearly agree, so it decides nothing: with |error| <= delta, a page more than 2 delta
+// above the last one taken is in, one more than 2 delta below is out, and those between are scored
+// again in fp64 and ranked by that, equal ones by column.  "The last one taken" need only be known to
+// within a narrow interval: a histogram of 2048 equal steps between the least and the largest score
+// gives one that mostly holds a few pages.  Where it does not serve (scores all but equal, or not
+// finite), radix selection takes its place.
 #include "paged_internal.h"
 
 #include <cuda_bf16.h>
@@ -88,7 +94,127 @@ k_paged_score(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) 
   if (lane == 0 && terms > 0.f) atomicMax(a.score_max + b * a.Hkv + kvh, __float_as_uint(terms));
 }
 
-constexpr int kRankThreads = 512;
+// ---- 16-bit stores --------------------------------------------------------------------
+constexpr int kMmaWarps = 4;
+
+template <typename T>
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1);   // A's rows 8..15 are zero
+template <>
+__device__ __forceinline__ void mma<__half>(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(0u), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(0u), "r"(a[1]), "r"(0u), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float2 pair_f(uint32_t u, const __half*) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+__device__ __forceinline__ float2 pair_f(uint32_t u, const __nv_bfloat16*) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+}
+// the pair's positive (or negative) parts: a 16-bit half whose sign bit does not fit becomes 0
+__device__ __forceinline__ uint32_t part_of(uint32_t u, bool negative) {
+  const uint32_t sign = u & 0x80008000u;
+  const uint32_t neg = (sign >> 15) * 0xffffu;             // ffff where the half is negative
+  return negative ? u & neg : u & ~neg;
+}
+
+// A warp takes 8 pages at a time: lane (n, c) = (lane / 4, lane % 4) holds dims 32 v + 8 c .. + 7 of page n's bounds.
+// The two k16 steps of a vector pair its dims as (0, 1 | 2, 3) and (4, 5 | 6, 7) where the MMA counts k = 2 c, 2 c + 1 |
+// 2 c + 8, 2 c + 9; the queries' fragments hold the same dims, so the sum is the same.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMmaWarps * 32)
+k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
+  constexpr int V = D / 32;                 // 16-byte vectors per lane of one bound
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = lane >> 2, c = lane & 3;
+  const int kvh = blockIdx.y, b = blockIdx.z;
+  const int np = row_pages(a, b);
+  if (np <= a.n_sel) return;                // every page is taken: nothing to rank
+  const int first = (blockIdx.x * kMmaWarps + warp) * 8, step = gridDim.x * kMmaWarps * 8;
+  if (first >= np) return;
+  const T* type = nullptr;
+  float* out = reinterpret_cast<float*>(a.scores + ((int64_t)b * a.Hkv + kvh) * a.max_pages);
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  float terms = 0.f;
+  for (int g0 = 0; g0 < a.G; g0 += 8) {     // 8 heads a pass
+    uint32_t qa[2][V][2][2];                // [hi, lo][vector][k16 step][k half]
+    float l1 = 0.f;
+    const bool real = g0 + n < a.G;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (real) x = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)b * a.H + kvh * a.G + g0 + n) * D + 32 * v + 8 * c));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        qa[0][v][i >> 1][i & 1] = part_of(w[i], false);
+        qa[1][v][i >> 1][i & 1] = part_of(w[i], true);
+        const float2 f = pair_f(w[i], type);
+        l1 += fabsf(f.x) + fabsf(f.y);
+      }
+    }
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, o));
+    float top = 0.f;
+    int page = first + n < np ? __ldg(table + first + n) : -1;
+    for (int j = first; j < np; j += step) {
+      const bool ok = page >= 0 && page < a.n_pages;       // (a bad page is reported by the attention that meets it)
+      const uint4* bd = reinterpret_cast<const uint4*>(bounds + ((int64_t)(ok ? page : 0) * a.Hkv + kvh) * 2 * D);
+      uint4 x[2][V];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[h][v] = ok ? __ldg(bd + h * (D / 8) + 4 * v + c) : make_uint4(0, 0, 0, 0);
+      page = j + step + n < np ? __ldg(table + j + step + n) : -1;
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const uint32_t w[4] = {x[h][v].x, x[h][v].y, x[h][v].z, x[h][v].w};
+          mma<T>(s[h], qa[h][v][0], w[0], w[1]);
+          mma<T>(s[h], qa[h][v][1], w[2], w[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = pair_f(w[i], type);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+      // head g0 + n of this lane: pages j + 2 c, + 1
+      const bool good = __shfl_sync(0xffffffffu, ok, 8 * c), good1 = __shfl_sync(0xffffffffu, ok, 8 * c + 4);
+      float u0 = real && good ? s[0][0] + s[1][0] : -INFINITY, u1 = real && good1 ? s[0][1] + s[1][1] : -INFINITY;
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
+        u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
+      }
+      if (lane < 4) {
+        const int i = j + 2 * lane;
+        if (i < np) out[i] = g0 == 0 ? u0 : fmaxf(out[i], u0);
+        if (i + 1 < np) out[i + 1] = g0 == 0 ? u1 : fmaxf(out[i + 1], u1);
+      }
+    }
+    terms = fmaxf(terms, l1 * top);         // no score's terms sum to more
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) terms = fmaxf(terms, __shfl_xor_sync(0xffffffffu, terms, o));
+  if (lane == 0 && terms > 0.f) atomicMax(a.score_max + b * a.Hkv + kvh, __float_as_uint(terms));
+}
+
+// ---- ranking ----------------------------------------------------------------------------
+constexpr int kRankThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kList = 1024;                 // candidates ranked by comparing each with each
 
 // order-preserving whole numbers
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -178,9 +304,12 @@ __device__ __forceinline__ K radix_select(int n, int need, int* s_hist, int* s_p
 template <typename T, int D>
 __global__ void __launch_bounds__(kRankThreads)
 k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
-  extern __shared__ uint32_t s_key[];                // [np]
-  __shared__ int s_hist[256], s_pick[2], s_warp[kRankThreads / 32], s_n;
-  __shared__ int s_cand[1024];
+  extern __shared__ float s_score[];                 // [np]
+  __shared__ int s_hist[kBins], s_pick[2], s_warp[kRankThreads / 32], s_n[2];
+  __shared__ int s_cand[kList];
+  __shared__ double s_exact[kList];
+  __shared__ uint32_t s_won[KVC_PG_MAX_SCORED / 32]; // candidates that are taken
+  __shared__ float s_lo[kRankThreads / 32], s_hi[kRankThreads / 32];
   kvc_pdl_wait();
   kvc_pdl_release();
   const int kvh = blockIdx.x, b = blockIdx.y;
@@ -199,100 +328,155 @@ k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
   double* exact = a.scores + pair * a.max_pages;
   const float* approx = reinterpret_cast<const float*>(exact);
   const float delta = __uint_as_float(a.score_max[pair]) * 0x1p-16f;
-  for (int i = tid; i < np; i += kRankThreads) s_key[i] = key_of(approx[i]);
+  auto forced = [&](int i) { return i < a.first || i >= np - a.recent; };
+  const int need = a.n_sel - a.first - a.recent;     // of the others (there are more than that)
+  // the others' scores, their least and largest
+  float lo = INFINITY, hi = -INFINITY;
+  for (int i = tid; i < np; i += kRankThreads) {
+    const float x = approx[i];
+    s_score[i] = x;
+    if (!forced(i)) {
+      lo = fminf(lo, x);
+      hi = fmaxf(hi, x);
+    }
+  }
+  for (int i = tid; i < kBins; i += kRankThreads) s_hist[i] = 0;
+  for (int i = tid; i < (np + 31) / 32; i += kRankThreads) s_won[i] = 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  if (lane == 0) {
+    s_lo[warp] = lo;
+    s_hi[warp] = hi;
+  }
+  if (tid == 0) s_n[0] = s_n[1] = 0;
   __syncthreads();
   if (tid == 0) a.score_max[pair] = 0u;              // for the next call
-  auto forced = [&](int i) { return i < a.first || i >= np - a.recent; };
-  const int need = a.n_sel - a.first - a.recent;     // of the others
-  uint32_t lo_key = 0xffffffffu, hi_key = 0xffffffffu;   // candidates: lo_key <= key <= hi_key
-  uint64_t last = 0;                                 // in fp64: the last candidate taken
-  int ties = 0;                                      // of candidates equal to it: how many
-  int take = 0;                                      // 0: no candidate is taken, 1: all, 2: by fp64 score
-  if (need > 0) {
-    const float t = of_key(radix_select<uint32_t>(np, need, s_hist, s_pick, [&](int i) { return s_key[i]; },
+  lo = s_lo[lane];
+  hi = s_hi[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  // the interval [t0, t1] that holds the last score taken (t1 < t0: none is)
+  float t0 = INFINITY, t1 = -INFINITY;
+  const float width = (hi - lo) / kBins;
+  if (need > 0 && width > 1e-30f && width < INFINITY) {
+    const float inv = 1.f / width;
+    auto bin = [&](float x) { return min(kBins - 1, max(0, (int)((x - lo) * inv))); };
+    for (int i = tid; i < np; i += kRankThreads)
+      if (!forced(i)) atomicAdd(s_hist + bin(s_score[i]), 1);
+    __syncthreads();
+    // thread t has bins 2047 - 2 t, 2046 - 2 t: how many lie above them
+    const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
+    int all;
+    const int above = block_scan(c0 + c1, s_warp, &all);
+    if (above < need && need <= above + c0 + c1) s_pick[0] = need <= above + c0 ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
+    __syncthreads();
+    // a step more on each side than the bin: its edges are rounded
+    t0 = lo + (s_pick[0] - 1) * width;
+    t1 = lo + (s_pick[0] + 2) * width;
+  } else if (need > 0) {
+    const float t = of_key(radix_select<uint32_t>(np, need, s_hist, s_pick, [&](int i) { return key_of(s_score[i]); },
                                                   [&](int i) { return !forced(i); }));
-    const float dd = delta == delta ? 2.f * delta : INFINITY;
-    const float lo_f = t - dd, hi_f = t + dd;
-    lo_key = lo_f == lo_f ? key_of(lo_f) : 0u;
-    hi_key = hi_f == hi_f ? key_of(hi_f) : 0xffffffffu;
-    int sure = 0, cand = 0;
-    for (int i = tid; i < np; i += kRankThreads) {
-      if (forced(i)) continue;
-      sure += s_key[i] > hi_key;
-      cand += s_key[i] <= hi_key && s_key[i] >= lo_key;
-    }
-    int n_sure, n_cand;
-    block_scan(sure, s_warp, &n_sure);
-    block_scan(cand, s_warp, &n_cand);
-    const int rest = need - n_sure;
-    take = rest <= 0 ? 0 : rest >= n_cand ? 1 : 2;
-    if (take == 2) {
-      // fp64 scores of the candidates, a warp each; they replace the fp32 ones in the workspace
-      auto score = [&](int i) {
-        const int page = a.table[(int64_t)b * a.max_pages + i];
-        double best = -INFINITY;
-        if (page >= 0 && page < a.n_pages) {
-          const T* bd = bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D;
-          for (int g = 0; g < a.G; ++g) {
-            const T* qp = q + ((int64_t)b * a.H + kvh * a.G + g) * D;
-            double u = 0.0;
-#pragma unroll
-            for (int d = lane; d < D; d += 32) {
-              const float x = to_f(qp[d]);
-              u = fma((double)x, (double)to_f(x > 0.f ? bd[d] : bd[D + d]), u);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-            best = u > best ? u : best;
-          }
-        }
-        if (lane == 0) exact[i] = best;
-      };
-      if (tid == 0) s_n = 0;
-      __syncthreads();
-      if (n_cand <= 1024) {                          // a list of them, so that every warp has work
-        for (int i = tid; i < np; i += kRankThreads)
-          if (!forced(i) && s_key[i] <= hi_key && s_key[i] >= lo_key) s_cand[atomicAdd(&s_n, 1)] = i;
-        __syncthreads();
-        for (int e = warp; e < n_cand; e += kRankThreads / 32) score(s_cand[e]);
-      } else {
-        for (int i = warp; i < np; i += kRankThreads / 32)
-          if (!forced(i) && s_key[i] <= hi_key && s_key[i] >= lo_key) score(i);
-      }
-      __syncthreads();
-      auto is_cand = [&](int i) { return !forced(i) && s_key[i] <= hi_key && s_key[i] >= lo_key; };
-      last = radix_select<uint64_t>(np, rest, s_hist, s_pick, [&](int i) { return key_of(exact[i]); }, is_cand);
-      ties = s_pick[1];
+    t0 = t1 = t;
+  }
+  // candidates: scores in [c_lo, c_hi]; above they are in, below out
+  const float dd = delta == delta ? 2.f * delta : INFINITY;
+  float c_lo = t0 - dd, c_hi = t1 + dd;
+  if (!(c_lo == c_lo)) c_lo = -INFINITY;             // (infinities in the scores)
+  if (!(c_hi == c_hi)) c_hi = INFINITY;
+  const bool none = need <= 0;
+  auto is_cand = [&](int i) { return !none && !forced(i) && s_score[i] >= c_lo && s_score[i] <= c_hi; };
+  auto is_sure = [&](int i) { return forced(i) || (!none && s_score[i] > c_hi); };
+  int sure = 0;
+  for (int i = tid; i < np; i += kRankThreads) {
+    sure += is_sure(i) && !forced(i);
+    if (is_cand(i)) {
+      const int at = atomicAdd(&s_n[0], 1);
+      if (at < kList) s_cand[at] = i;
     }
   }
-  // columns in order: each thread a stretch of them; ties are given out in order too
+  int n_sure;
+  block_scan(sure, s_warp, &n_sure);
+  __syncthreads();
+  const int n_cand = s_n[0], rest = need - n_sure;
+  // fp64 score of page i by a warp (every lane returns it)
+  auto score = [&](int i) {
+    const int page = a.table[(int64_t)b * a.max_pages + i];
+    double best = -INFINITY;
+    if (page >= 0 && page < a.n_pages) {
+      const T* bd = bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D;
+      for (int g = 0; g < a.G; ++g) {
+        const T* qp = q + ((int64_t)b * a.H + kvh * a.G + g) * D;
+        double u = 0.0;
+#pragma unroll
+        for (int d = lane; d < D; d += 32) {
+          const float x = to_f(qp[d]);
+          u = fma((double)x, (double)to_f(x > 0.f ? bd[d] : bd[D + d]), u);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+        best = u > best ? u : best;
+      }
+    }
+    return best;
+  };
+  int take = rest <= 0 ? 0 : rest >= n_cand ? 1 : n_cand <= kList ? 2 : 3;   // candidates: none, all, by the list, by radix
+  uint64_t last = 0;
+  int ties = 0;
+  if (take == 2) {
+    for (int e = warp; e < n_cand; e += kRankThreads / 32) {
+      const double x = score(s_cand[e]);
+      if (lane == 0) s_exact[e] = x;
+    }
+    __syncthreads();
+    for (int e = tid; e < n_cand; e += kRankThreads) {
+      const double x = s_exact[e];
+      const int i = s_cand[e];
+      int better = 0;
+      for (int f = 0; f < n_cand; ++f) better += s_exact[f] > x || (s_exact[f] == x && s_cand[f] < i);
+      if (better < rest) atomicOr(s_won + (i >> 5), 1u << (i & 31));
+    }
+    __syncthreads();
+  } else if (take == 3) {
+    // the fp64 scores replace the fp32 ones in the workspace
+    __syncthreads();
+    for (int i = warp; i < np; i += kRankThreads / 32) {
+      if (!is_cand(i)) continue;
+      const double x = score(i);
+      if (lane == 0) exact[i] = x;
+    }
+    __syncthreads();
+    last = radix_select<uint64_t>(np, rest, s_hist, s_pick, [&](int i) { return key_of(exact[i]); }, is_cand);
+    ties = s_pick[1];
+  }
+  // columns in order: each thread a stretch of them (and ties, where radix left them, in order too)
   const int stretch = (np + kRankThreads - 1) / kRankThreads;
   const int i0 = min(np, tid * stretch), i1 = min(np, i0 + stretch);
-  auto state = [&](int i) {                          // 1 taken, 0 not, 2 one of the ties
-    if (forced(i) || s_key[i] > hi_key) return 1;
-    if (take == 0 || s_key[i] < lo_key) return 0;
-    if (take == 1) return 1;
+  int tie = 0, total;
+  if (take == 3) {
+    int n_tie = 0;
+    for (int i = i0; i < i1; ++i) n_tie += is_cand(i) && key_of(exact[i]) == last;
+    tie = block_scan(n_tie, s_warp, &total);
+  }
+  auto taken = [&](int i, int& t) {
+    if (is_sure(i)) return true;
+    if (take == 0 || !is_cand(i)) return false;
+    if (take == 1) return true;
+    if (take == 2) return ((s_won[i >> 5] >> (i & 31)) & 1) != 0;
     const uint64_t x = key_of(exact[i]);
-    return x > last ? 1 : x == last ? 2 : 0;
+    return x > last || (x == last && t++ < ties);
   };
-  int n_tie = 0, n_in = 0, total;
-  for (int i = i0; i < i1; ++i) n_tie += state(i) == 2;
-  int tie = block_scan(n_tie, s_warp, &total);
-  const int tie0 = tie;
-  for (int i = i0; i < i1; ++i) {
-    const int st = state(i);
-    n_in += st == 1 || (st == 2 && tie < ties);
-    tie += st == 2;
-  }
+  int n_in = 0, t = tie;
+  for (int i = i0; i < i1; ++i) n_in += taken(i, t);
   int at = block_scan(n_in, s_warp, &total);
-  tie = tie0;
-  for (int i = i0; i < i1; ++i) {
-    const int st = state(i);
-    const bool in = st == 1 || (st == 2 && tie < ties);
-    tie += st == 2;
-    if (in && at < a.n_sel) sel[at++] = i;
-  }
-  // (scores that are not numbers may leave fewer)
+  t = tie;
+  for (int i = i0; i < i1; ++i)
+    if (taken(i, t) && at < a.n_sel) sel[at++] = i;
   for (int i = total + tid; i < a.n_sel; i += kRankThreads) sel[i] = -1;
 }
 
@@ -300,9 +484,19 @@ template <typename T, int D>
 cudaError_t launch(const kvc_paged* c, const void* q, const SelArgs& a, cudaStream_t s, bool prepare) {
   if (prepare)
     return cudaFuncSetAttribute(k_paged_rank<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KVC_PG_MAX_SCORED * 4);
-  const int blocks = (a.max_pages + 8 * 4 - 1) / (8 * 4);
-  const cudaError_t e = kvc_launch_pdl(k_paged_score<T, D>, dim3(blocks, a.Hkv, a.B), dim3(kScoreThreads), 0, s, (const T*)q,
-                                 (const T*)c->bounds, a);
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2) {
+    // 8 pages a warp; a warp takes up to four such sets where that still leaves 16 warps an SM
+    const int64_t sets = ((int64_t)a.max_pages + 7) / 8 * a.Hkv * a.B;
+    const int per_warp = sets >= (int64_t)KVC_PG_GRID * 16 * 4 ? 4 : 1;
+    const int blocks = (a.max_pages + 8 * kMmaWarps * per_warp - 1) / (8 * kMmaWarps * per_warp);
+    e = kvc_launch_pdl(k_paged_score_mma<T, D>, dim3(blocks, a.Hkv, a.B), dim3(kMmaWarps * 32), 0, s, (const T*)q,
+                       (const T*)c->bounds, a);
+  } else {
+    const int blocks = (a.max_pages + 8 * 4 - 1) / (8 * 4);
+    e = kvc_launch_pdl(k_paged_score<T, D>, dim3(blocks, a.Hkv, a.B), dim3(kScoreThreads), 0, s, (const T*)q,
+                       (const T*)c->bounds, a);
+  }
   if (e != cudaSuccess) return e;
   const size_t smem = (size_t)a.max_pages * 4;
   return kvc_launch_pdl(k_paged_rank<T, D>, dim3(a.Hkv, a.B), dim3(kRankThreads), smem, s, (const T*)q,
