@@ -13,10 +13,12 @@
 // k_paged_rank, a block per (row, kv head), takes the n_select largest.  Rounding could swap pages
 // whose scores nearly agree, so it decides nothing: with |error| <= delta, a page more than 2 delta
 // above the last one taken is in, one more than 2 delta below is out, and those between are scored
-// again in fp64 and ranked by that, equal ones by column.  "The last one taken" need only be known to
-// within a narrow interval: a histogram of 2048 equal steps between the least and the largest score
-// gives one that mostly holds a few pages.  Where it does not serve (scores all but equal, or not
-// finite), radix selection takes its place.
+// again in twice fp32's precision (products and sums with their rounding errors; fp64 is some fifty
+// times slower than fp32 here) and ranked by that, equal ones by column.  "The last one taken" need
+// only be known to within a narrow interval: a histogram of 2048 equal steps between the least and
+// the largest score gives one that mostly holds a few pages.  Where it does not serve (scores all but
+// equal, or not finite), radix selection takes its place.  Bound by the latency of its eight or so
+// phases between barriers.
 #include "paged_internal.h"
 
 #include <cuda_bf16.h>
@@ -212,9 +214,9 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
 }
 
 // ---- ranking ----------------------------------------------------------------------------
-constexpr int kRankThreads = 1024;
+constexpr int kRankThreads = 512, kRankWarps = kRankThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kList = 1024;                 // candidates ranked by comparing each with each
+constexpr int kList = 512;                  // candidates ranked by comparing each with each
 
 // order-preserving whole numbers
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -241,15 +243,15 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
   __syncthreads();
   if (lane == 31) s_warp[warp] = y;
   __syncthreads();
-  int before = 0, all = 0;
+  const int mine = lane < kRankThreads / 32 ? s_warp[lane] : 0;
+  int sums = mine;
 #pragma unroll
-  for (int w = 0; w < kRankThreads / 32; ++w) {
-    const int v = s_warp[w];
-    before += w < warp ? v : 0;
-    all += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += z;
   }
-  *total = all;
-  return before + y - x;
+  *total = __shfl_sync(0xffffffffu, sums, 31);
+  return __shfl_sync(0xffffffffu, sums - mine, warp) + y - x;
 }
 
 // The need-th largest (need >= 1) of key(i) over i in [0, n) with in(i), a byte a pass from the top.
@@ -301,21 +303,56 @@ __device__ __forceinline__ K radix_select(int n, int need, int* s_hist, int* s_p
   return prefix;
 }
 
+// x + y and its rounding error
+__device__ __forceinline__ float two_sum(float x, float y, float& err) {
+  const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
+  err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
+  return s;
+}
+
+// Score of a page for one head, in twice fp32's precision; every lane of the warp returns it.
+template <typename T, int D>
+__device__ __forceinline__ double fine_score(const T* q, const T* bd, int lane) {
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int d = lane + 32 * i;
+    const float x = to_f(q[d]), y = to_f(x > 0.f ? bd[d] : bd[D + d]);
+    const float p = __fmul_rn(x, y), e = __fmaf_rn(x, y, -p);
+    float r;
+    hi = two_sum(hi, p, r);
+    lo += r + e;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    float r;
+    const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+    // (the same on both sides of the exchange: the sum is symmetric)
+    hi = two_sum(fmaxf(hi, h), fminf(hi, h), r);
+    lo = (lo + l) + r;
+  }
+  return (double)hi + (double)lo;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kRankThreads)
 k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
-  extern __shared__ float s_score[];                 // [np]
-  __shared__ int s_hist[kBins], s_pick[2], s_warp[kRankThreads / 32], s_n[2];
+  extern __shared__ float s_score[];                 // [np, rounded up to whole words of 32 pages]
+  constexpr int kWords = KVC_PG_MAX_SCORED / 32;
+  __shared__ int s_hist[kBins], s_pick[2], s_warp[kRankWarps], s_n[2];
   __shared__ int s_cand[kList];
-  __shared__ double s_exact[kList];
-  __shared__ uint32_t s_won[KVC_PG_MAX_SCORED / 32]; // candidates that are taken
-  __shared__ float s_lo[kRankThreads / 32], s_hi[kRankThreads / 32];
+  __shared__ unsigned long long s_key[kList];
+  __shared__ uint32_t s_in[kWords], s_maybe[kWords]; // a bit per page: taken, candidate
+  __shared__ float s_lo[kRankWarps], s_hi[kRankWarps];
   kvc_pdl_wait();
   kvc_pdl_release();
   const int kvh = blockIdx.x, b = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t pair = (int64_t)b * a.Hkv + kvh;
   int32_t* sel = a.sel + pair * a.n_sel;
+  double* exact = a.scores + pair * a.max_pages;
+  const float* approx = reinterpret_cast<const float*>(exact);
+  const uint32_t max_bits = a.score_max[pair];
   const int np = row_pages(a, b);
   if (np < 0) {
     if (tid == 0) atomicOr(a.err, KVC_DEV_BAD_KVLEN);
@@ -325,23 +362,30 @@ k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
     for (int i = tid; i < a.n_sel; i += kRankThreads) sel[i] = i < np ? i : -1;
     return;
   }
-  double* exact = a.scores + pair * a.max_pages;
-  const float* approx = reinterpret_cast<const float*>(exact);
-  const float delta = __uint_as_float(a.score_max[pair]) * 0x1p-16f;
-  auto forced = [&](int i) { return i < a.first || i >= np - a.recent; };
-  const int need = a.n_sel - a.first - a.recent;     // of the others (there are more than that)
-  // the others' scores, their least and largest
+  const float delta = __uint_as_float(max_bits) * 0x1p-16f;
+  const int last_others = np - a.recent;             // pages [first, last_others) are ranked, the others always taken
+  auto forced = [&](int i) { return i < a.first || i >= last_others; };
+  const int need = a.n_sel - a.first - a.recent;     // of those ranked (there are more than that)
+  // the scores, their least and largest
   float lo = INFINITY, hi = -INFINITY;
-  for (int i = tid; i < np; i += kRankThreads) {
-    const float x = approx[i];
-    s_score[i] = x;
-    if (!forced(i)) {
-      lo = fminf(lo, x);
-      hi = fmaxf(hi, x);
+  for (int i0 = tid; i0 < np; i0 += 4 * kRankThreads) {
+    float x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * kRankThreads < np) x[u] = approx[i0 + u * kRankThreads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kRankThreads;
+      if (i >= np) continue;
+      s_score[i] = x[u];
+      if (!forced(i)) {
+        lo = fminf(lo, x[u]);
+        hi = fmaxf(hi, x[u]);
+      }
     }
   }
   for (int i = tid; i < kBins; i += kRankThreads) s_hist[i] = 0;
-  for (int i = tid; i < (np + 31) / 32; i += kRankThreads) s_won[i] = 0;
+  if (tid < kList) s_key[tid] = 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -353,130 +397,144 @@ k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
   }
   if (tid == 0) s_n[0] = s_n[1] = 0;
   __syncthreads();
-  if (tid == 0) a.score_max[pair] = 0u;              // for the next call
-  lo = s_lo[lane];
-  hi = s_hi[lane];
+  if (tid == 0) a.score_max[pair] = 0u;              // for the next call (every thread has read it)
+  lo = s_lo[lane % kRankWarps];
+  hi = s_hi[lane % kRankWarps];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = kRankWarps / 2; o > 0; o >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  // the interval [t0, t1] that holds the last score taken (t1 < t0: none is)
-  float t0 = INFINITY, t1 = -INFINITY;
+  // the interval [t0, t1] that holds the last score taken
+  float t0 = INFINITY, t1 = INFINITY;
   const float width = (hi - lo) / kBins;
   if (need > 0 && width > 1e-30f && width < INFINITY) {
     const float inv = 1.f / width;
-    auto bin = [&](float x) { return min(kBins - 1, max(0, (int)((x - lo) * inv))); };
     for (int i = tid; i < np; i += kRankThreads)
-      if (!forced(i)) atomicAdd(s_hist + bin(s_score[i]), 1);
+      if (!forced(i)) atomicAdd(s_hist + min(kBins - 1, max(0, (int)((s_score[i] - lo) * inv))), 1);
     __syncthreads();
-    // thread t has bins 2047 - 2 t, 2046 - 2 t: how many lie above them
-    const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
-    int all;
-    const int above = block_scan(c0 + c1, s_warp, &all);
-    if (above < need && need <= above + c0 + c1) s_pick[0] = need <= above + c0 ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
+    // thread t has four bins, from the top down; how many scores lie above them
+    constexpr int kPer = kBins / kRankThreads;
+    int c[kPer], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      c[i] = s_hist[kBins - 1 - kPer * tid - i];
+      sum += c[i];
+    }
+    int above = block_scan(sum, s_warp, &all);
+    if (above < need && need <= above + sum) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (above < need && need <= above + c[i]) s_pick[0] = kBins - 1 - kPer * tid - i;
+        above += c[i];
+      }
+    }
     __syncthreads();
     // a step more on each side than the bin: its edges are rounded
     t0 = lo + (s_pick[0] - 1) * width;
     t1 = lo + (s_pick[0] + 2) * width;
   } else if (need > 0) {
-    const float t = of_key(radix_select<uint32_t>(np, need, s_hist, s_pick, [&](int i) { return key_of(s_score[i]); },
-                                                  [&](int i) { return !forced(i); }));
-    t0 = t1 = t;
+    t0 = t1 = of_key(radix_select<uint32_t>(np, need, s_hist, s_pick, [&](int i) { return key_of(s_score[i]); },
+                                            [&](int i) { return !forced(i); }));
   }
-  // candidates: scores in [c_lo, c_hi]; above they are in, below out
+  // candidates: scores in [c_lo, c_hi]; above they are in, below out (need = 0: none is in)
   const float dd = delta == delta ? 2.f * delta : INFINITY;
   float c_lo = t0 - dd, c_hi = t1 + dd;
-  if (!(c_lo == c_lo)) c_lo = -INFINITY;             // (infinities in the scores)
-  if (!(c_hi == c_hi)) c_hi = INFINITY;
-  const bool none = need <= 0;
-  auto is_cand = [&](int i) { return !none && !forced(i) && s_score[i] >= c_lo && s_score[i] <= c_hi; };
-  auto is_sure = [&](int i) { return forced(i) || (!none && s_score[i] > c_hi); };
-  int sure = 0;
-  for (int i = tid; i < np; i += kRankThreads) {
-    sure += is_sure(i) && !forced(i);
-    if (is_cand(i)) {
-      const int at = atomicAdd(&s_n[0], 1);
-      if (at < kList) s_cand[at] = i;
+  if (!(c_lo == c_lo) || need <= 0) c_lo = need > 0 ? -INFINITY : INFINITY;     // (infinities in the scores)
+  if (!(c_hi == c_hi) || need <= 0) c_hi = INFINITY;
+  auto is_cand = [&](int i) { return need > 0 && !forced(i) && s_score[i] >= c_lo && s_score[i] <= c_hi; };
+  // a bit per page, a word per warp and step
+  const int words = (np + 31) / 32;
+  for (int w = warp; w < words; w += kRankWarps) {
+    const int i = 32 * w + lane;
+    const bool there = i < np;
+    const bool cand = there && is_cand(i), in = there && (forced(i) || s_score[i] > c_hi);
+    const uint32_t bits_in = __ballot_sync(0xffffffffu, in), bits_maybe = __ballot_sync(0xffffffffu, cand);
+    const int n_in = __popc(__ballot_sync(0xffffffffu, in && !forced(i)));
+    int at = 0;
+    if (lane == 0) {
+      s_in[w] = bits_in;
+      s_maybe[w] = bits_maybe;
+      if (n_in) atomicAdd(&s_n[1], n_in);
+      if (bits_maybe) at = atomicAdd(&s_n[0], __popc(bits_maybe));
     }
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(bits_maybe & ((1u << lane) - 1));
+    if (cand && at < kList) s_cand[at] = i;
   }
-  int n_sure;
-  block_scan(sure, s_warp, &n_sure);
   __syncthreads();
-  const int n_cand = s_n[0], rest = need - n_sure;
-  // fp64 score of page i by a warp (every lane returns it)
-  auto score = [&](int i) {
+  const int n_cand = s_n[0], rest = need - s_n[1];
+  // candidates: none are taken, all, those that rank high in the list, or by radix selection
+  const int take = rest <= 0 ? 0 : rest >= n_cand ? 1 : n_cand <= kList ? 2 : 3;
+  auto score = [&](int i, int g) {
     const int page = a.table[(int64_t)b * a.max_pages + i];
-    double best = -INFINITY;
-    if (page >= 0 && page < a.n_pages) {
-      const T* bd = bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D;
-      for (int g = 0; g < a.G; ++g) {
-        const T* qp = q + ((int64_t)b * a.H + kvh * a.G + g) * D;
-        double u = 0.0;
-#pragma unroll
-        for (int d = lane; d < D; d += 32) {
-          const float x = to_f(qp[d]);
-          u = fma((double)x, (double)to_f(x > 0.f ? bd[d] : bd[D + d]), u);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        best = u > best ? u : best;
-      }
-    }
-    return best;
+    if (page < 0 || page >= a.n_pages) return -(double)INFINITY;
+    const double u = fine_score<T, D>(q + ((int64_t)b * a.H + kvh * a.G + g) * D,
+                                      bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D, lane);
+    return u == u ? u : -(double)INFINITY;
   };
-  int take = rest <= 0 ? 0 : rest >= n_cand ? 1 : n_cand <= kList ? 2 : 3;   // candidates: none, all, by the list, by radix
-  uint64_t last = 0;
-  int ties = 0;
+  int total;
   if (take == 2) {
-    for (int e = warp; e < n_cand; e += kRankThreads / 32) {
-      const double x = score(s_cand[e]);
-      if (lane == 0) s_exact[e] = x;
+    for (int e = warp; e < n_cand * a.G; e += kRankWarps) {
+      const int f = e / a.G;
+      const uint64_t key = key_of(score(s_cand[f], e - f * a.G));
+      if (lane == 0) atomicMax(&s_key[f], (unsigned long long)key);
     }
     __syncthreads();
     for (int e = tid; e < n_cand; e += kRankThreads) {
-      const double x = s_exact[e];
+      const unsigned long long x = s_key[e];
       const int i = s_cand[e];
       int better = 0;
-      for (int f = 0; f < n_cand; ++f) better += s_exact[f] > x || (s_exact[f] == x && s_cand[f] < i);
-      if (better < rest) atomicOr(s_won + (i >> 5), 1u << (i & 31));
+      for (int f = 0; f < n_cand; ++f) better += s_key[f] > x || (s_key[f] == x && s_cand[f] < i);
+      if (better < rest) atomicOr(s_in + (i >> 5), 1u << (i & 31));
     }
     __syncthreads();
   } else if (take == 3) {
-    // the fp64 scores replace the fp32 ones in the workspace
+    // the fine scores replace the others in the workspace
+    for (int w = warp; w < words; w += kRankWarps)
+      for (uint32_t left = s_maybe[w]; left; left &= left - 1) {
+        const int i = 32 * w + __ffs(left) - 1;
+        double best = -INFINITY;
+        for (int g = 0; g < a.G; ++g) best = fmax(best, score(i, g));
+        if (lane == 0) exact[i] = best;
+      }
     __syncthreads();
-    for (int i = warp; i < np; i += kRankThreads / 32) {
-      if (!is_cand(i)) continue;
-      const double x = score(i);
-      if (lane == 0) exact[i] = x;
+    const uint64_t last = radix_select<uint64_t>(np, rest, s_hist, s_pick, [&](int i) { return key_of(exact[i]); }, is_cand);
+    const int ties = s_pick[1];                      // of those equal to the last: how many, the lowest columns first
+    const int stretch = (words + kRankThreads - 1) / kRankThreads;
+    const int w0 = min(words, tid * stretch), w1 = min(words, w0 + stretch);
+    int n_tie = 0;
+    for (int w = w0; w < w1; ++w)
+      for (uint32_t left = s_maybe[w]; left; left &= left - 1) n_tie += key_of(exact[32 * w + __ffs(left) - 1]) == last;
+    int t = block_scan(n_tie, s_warp, &total);
+    for (int w = w0; w < w1; ++w) {
+      uint32_t won = 0;
+      for (uint32_t left = s_maybe[w]; left; left &= left - 1) {
+        const uint64_t x = key_of(exact[32 * w + __ffs(left) - 1]);
+        if (x > last || (x == last && t++ < ties)) won |= left & -left;
+      }
+      s_in[w] |= won;
     }
     __syncthreads();
-    last = radix_select<uint64_t>(np, rest, s_hist, s_pick, [&](int i) { return key_of(exact[i]); }, is_cand);
-    ties = s_pick[1];
   }
-  // columns in order: each thread a stretch of them (and ties, where radix left them, in order too)
-  const int stretch = (np + kRankThreads - 1) / kRankThreads;
-  const int i0 = min(np, tid * stretch), i1 = min(np, i0 + stretch);
-  int tie = 0, total;
-  if (take == 3) {
-    int n_tie = 0;
-    for (int i = i0; i < i1; ++i) n_tie += is_cand(i) && key_of(exact[i]) == last;
-    tie = block_scan(n_tie, s_warp, &total);
+  // columns in order: each thread's words, counted, then written a word per warp and step
+  const int stretch = (words + kRankThreads - 1) / kRankThreads;
+  const int w0 = min(words, tid * stretch), w1 = min(words, w0 + stretch);
+  int n = 0;
+  for (int w = w0; w < w1; ++w) {
+    if (take == 1) s_in[w] |= s_maybe[w];
+    n += __popc(s_in[w]);
   }
-  auto taken = [&](int i, int& t) {
-    if (is_sure(i)) return true;
-    if (take == 0 || !is_cand(i)) return false;
-    if (take == 1) return true;
-    if (take == 2) return ((s_won[i >> 5] >> (i & 31)) & 1) != 0;
-    const uint64_t x = key_of(exact[i]);
-    return x > last || (x == last && t++ < ties);
-  };
-  int n_in = 0, t = tie;
-  for (int i = i0; i < i1; ++i) n_in += taken(i, t);
-  int at = block_scan(n_in, s_warp, &total);
-  t = tie;
-  for (int i = i0; i < i1; ++i)
-    if (taken(i, t) && at < a.n_sel) sel[at++] = i;
+  int at = block_scan(n, s_warp, &total);
+  for (int w = w0; w < w1; ++w) {
+    s_maybe[w] = at;                                 // (where the word's first page goes)
+    at += __popc(s_in[w]);
+  }
+  __syncthreads();
+  for (int w = warp; w < words; w += kRankWarps) {
+    const uint32_t in = s_in[w];
+    const int to = (int)s_maybe[w] + __popc(in & ((1u << lane) - 1));
+    if (((in >> lane) & 1) && to < a.n_sel) sel[to] = 32 * w + lane;
+  }
   for (int i = total + tid; i < a.n_sel; i += kRankThreads) sel[i] = -1;
 }
 
