@@ -39,6 +39,17 @@ constexpr float kRescaleThreshold = 8.0f;                // log2 units
 constexpr float kRescaleSum = 256.0f;                    // 2^kRescaleThreshold
 constexpr int kBadRing = 8;
 
+// An item as the softmax warps see it (worked out by the PV issuer, which would otherwise idle, so that none of it
+// takes registers next to a row of S).
+struct Desc {
+  int tiles;             // this block's; -1: no more items
+  int key0;              // position of the first tile's first slot
+  int len, limit0;       // where the keys end, and for the item's first token (causal)
+  int i0;                // its first token within the row
+  int64_t at0;           // output row of its first token and head
+  kvc_pg_end end;
+};
+
 template <int D>
 struct Smem {
   uint8_t q[D / 64][kBoxBytes];
@@ -51,6 +62,8 @@ struct Smem {
   uint64_t o_done, o_free;
   uint64_t pv_issued[2];
   uint64_t drain[2];
+  uint64_t desc_full[2];
+  Desc desc[2];
   // boxes of a tile that no page stands behind: read by the softmax warps up to six tiles after the K
   // producer wrote it (QK(T) is issued once softmax(T - 3) is done, and K(T) loaded once QK(T - 3) is)
   uint32_t k_bad[kBadRing];
@@ -223,6 +236,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.drain[i], 1);
       mbar_init(&sm.pv_issued[i], 1);
+      mbar_init(&sm.desc_full[i], 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&sm.s_full[i], 2);               // the MMAs' commit, and the issuer (for k_bad)
@@ -278,12 +292,13 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const int box_log2 = min(a.ps_log2, 6);
     const int per_tile = kBN >> box_log2;               // boxes of one half: 2, 4 or 8
     const uint32_t box_bytes = 128u << box_log2;
-    // lane i < per_tile: the page of the tile's ith box; -1 behind the row's end, -2 a bad one
+    // lane i < per_tile: the page number of the tile's ith box, not looked at before it is used (a tile later); -1 behind
+    // the row's end (where -1 is found in a table, it is a bad page: the box lies before the end)
     auto look = [&](const kvc_pg_item& w, int j) {
       const int key = w.r.lo + j * kBN + (lane << box_log2);
       if (lane >= per_tile || key >= w.r.len) return -1;
-      const int g = pg_page(a, w.b, key >> a.ps_log2);
-      return g < 0 ? -2 : g;
+      const int col = key >> a.ps_log2;
+      return a.phase == 1 ? __ldg(a.prefix_pages + col) : __ldg(a.table + (int64_t)w.b * a.max_pages + col);
     };
     int t = 0, n = 0, q_issued = 0;
     bool ok = true;
@@ -312,7 +327,11 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         if (t >= stages)
           ok = __all_sync(0xffffffffu, mbar_wait(kq ? &sm.k_empty[st] : &sm.v_empty[st], (t / stages - 1) & 1, wc));
         if (!ok) break;
-        const unsigned good = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
+        const bool there = lane < per_tile && it.r.lo + j * kBN + (lane << box_log2) < it.r.len;
+        const bool fine = there && page >= 0 && page < a.n_pages;
+        if (there && !fine) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+        if (!fine) page = -1;
+        const unsigned good = __ballot_sync(0xffffffffu, fine), bad = __ballot_sync(0xffffffffu, there && !fine);
         if (lane == 0) {
           if (kq) sm.k_bad[t % kBadRing] = bad;
           else sm.v_bad[st] = bad;
@@ -381,7 +400,23 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const int box_log2 = min(a.ps_log2, 6);
     int t = 0, n = 0;
     bool ok = true;
-    for (; ok && more; more = sch.next(a, it)) {
+    for (;; more = sch.next(a, it)) {
+      // (the softmax warps are done with item n - 2's descriptor: o_free of that item has been waited for)
+      if (lane == 0) {
+        Desc& d = sm.desc[n & 1];
+        d.tiles = more ? it.tile1 - it.tile0 : -1;
+        if (more) {
+          d.key0 = it.r.lo + it.tile0 * kBN;
+          d.len = it.r.len;
+          d.i0 = it.k * sch.T;
+          d.limit0 = pg_limit(a, it.r, d.i0);
+          d.at0 = (int64_t)(it.r.t0 + d.i0) * a.H + it.vh * a.Gv;
+          d.end = pg_end(a, sch, it);
+        }
+        mbar_arrive(&sm.desc_full[n & 1]);
+      }
+      __syncwarp();
+      if (!more) break;
       const int tile0 = it.tile0, tile1 = it.tile1;
       if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (n - 1) & 1, wc));   // the epilogue has read O
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
@@ -418,6 +453,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         __syncwarp();
       }
       ++n;
+      if (!ok) break;
     }
     if (wc->abort && lane == 0) {
       mma_commit(&sm.drain[1]);
@@ -432,24 +468,29 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     const uint32_t o_addr = lane_addr + 384u;
     const float c = a.scale_log2;
     const int box_log2 = min(a.ps_log2, 6);
-    const int prefix = a.phase == 2 ? sch.lo : 0;
-    int t = 0, n = 0;
+    const bool prefix = a.phase == 2 && sch.lo > 0;
+    const int i_tok = r / a.Gv, g = r - i_tok * a.Gv;        // this row's token and head within an item
+    int t = 0;
     bool ok = true;
-    for (; ok && more; more = sch.next(a, it)) {
-      const int tile0 = it.tile0, tile1 = it.tile1;
-      const int rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
-      const int i_tok = it.k * sch.T + r / a.Gv;
+    for (int n = 0;; ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.desc_full[n & 1], (n >> 1) & 1, wc));
+      if (!ok) break;
+      const volatile Desc& it = sm.desc[n & 1];
+      const int tiles = it.tiles;
+      if (tiles < 0) break;
       // where this row's keys end; rows that are not there see everything (no mask on their account)
       int limit = 0x3fffffff;
-      if (r < rows) limit = a.phase == 1 ? pg_prefix_limit(a, i_tok, it.r.len) : pg_limit(a, it.r, i_tok);
+      if (r < it.end.rows)
+        limit = a.phase == 1 ? pg_prefix_limit(a, it.i0 + i_tok, it.len) : a.causal ? it.limit0 + i_tok : it.len;
+      limit -= it.key0;                                      // (as of the first tile)
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = tile0; j < tile1; ++j, ++t) {
+      for (int j = 0; j < tiles; ++j, ++t) {
         const int sb = t % kSBufs;
         const uint32_t s_addr = lane_addr + sb * 128u;
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (t / kSBufs) & 1, wc));
         if (!ok) break;
         tc_fence_after();
-        const int valid = limit - (it.r.lo + j * kBN);
+        const int valid = limit - j * kBN;
         const uint32_t bad = sm.k_bad[t % kBadRing];
         auto tile = [&](auto mask) {
           constexpr bool kM = decltype(mask)::value;
@@ -459,14 +500,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           tmem_ld_wait();
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) reg_fence32(sr + q4 * 32);
-          if (kM && bad) {                              // slots without a page (bits past a tile's boxes are 0)
-#pragma unroll
-            for (int i = 0; i < kBN; ++i)
-              if ((bad >> (i >> box_log2)) & 1) sr[i] = 0xff800000u;
-          }
           // After the first tile P is taken against the running reference at once: every p is at most the row's
           // sum, so a sum of at most 2^threshold shows that the maximum did not grow by more, and P stands.
-          if (j > tile0) {
+          if (j > 0) {
             const float lsum = exp_pack_store<kBf16, kM>(sr, valid, c, m_ref, s_addr);
             if (!__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) {   // (a NaN sum takes the slow path)
               l += lsum;
@@ -477,7 +513,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           const bool rescale = m_tile > m_ref + kRescaleThreshold || m_ref == -INFINITY;
           const float m_new = rescale ? m_tile : m_ref;
           const float m_use = m_new == -INFINITY ? 0.f : m_new;
-          if (j > tile0) {
+          if (j > 0) {
             tmem_st_wait();                             // the optimistic P is overwritten below
             // O may be rescaled only once PV(t - 1) has finished accumulating into it
             if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_free[(t - 1) % kSBufs], ((t - 1) / kSBufs) & 1, wc))) return;
@@ -504,7 +540,21 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           m_ref = m_new;
           l += exp_pack_store<kBf16, kM>(sr, valid, c, m_use, s_addr);
         };
-        if (__all_sync(0xffffffffu, valid >= kBN) && bad == 0) tile(std::false_type{});
+        if (bad) {                                      // slots without a page: their scores become -inf where they are
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t x[32];
+            tmem_ld32(s_addr + q4 * 32, x);
+            tmem_ld_wait();
+            reg_fence32(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bad >> ((q4 * 32 + i) >> box_log2)) & 1) x[i] = 0xff800000u;
+            tmem_st32(s_addr + q4 * 32, x);
+          }
+          tmem_st_wait();
+        }
+        if (__all_sync(0xffffffffu, valid >= kBN)) tile(std::false_type{});
         else tile(std::true_type{});
         ok = !__any_sync(0xffffffffu, wc->abort);
         if (!ok) break;
@@ -517,14 +567,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       if (!ok) break;
       tc_fence_after();
       // ---- the item's (or this part's) state: straight out, or left as a partial ----
-      const int c0 = it.start / sch.per, c1 = (it.start + it.tiles - 1) / sch.per;
-      const int cta = blockIdx.x;
-      const bool real = r < rows;
-      const int tok = it.r.t0 + i_tok;
-      if (a.phase == 1 || c0 != c1) {
-        const int m = (it.r.n + sch.T - 1) / sch.T;
-        float* dst = a.phase == 1 ? a.pre + (int64_t)(it.vh * m + it.k + cta) * (kBM * (D + 2))
-                                  : a.part + (int64_t)(2 * cta + (cta == c0 ? 1 : 0)) * (kBM * (D + 2));
+      const bool real = r < it.end.rows;
+      const int64_t at = it.at0 + (int64_t)i_tok * a.H + g;
+      if (it.end.left) {
+        float* dst = (a.phase == 1 ? a.pre : a.part) + (int64_t)it.end.slot * (kBM * (D + 2));
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t orow[32];
@@ -539,11 +585,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         if (real) *reinterpret_cast<float2*>(dst + kBM * D + 2 * r) = make_float2(m_ref, l);
       } else {
-        const int h = it.vh * a.Gv + r % a.Gv;
         float M = m_ref, L = l;
-        const int64_t at = (int64_t)tok * a.H + h;
         float2 pm = make_float2(-INFINITY, 0.f);         // the shared prefix's state
-        if (prefix > 0 && real) {
+        if (prefix && real) {
           pm = __ldcg(a.pre_ml + at);
           M = fmaxf(M, pm.x);
           L = fmaf(pg_weight(pm.x, M), pm.y, l * pg_weight(m_ref, M));
@@ -584,11 +628,10 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
         }
       }
-      // every TMEM read of O is complete: the next item's first PV may overwrite it
+      // every TMEM read of O is complete (the next item's first PV may overwrite it), and the descriptor read
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_free);
-      ++n;
     }
   }
 
