@@ -506,7 +506,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             const float lsum = exp_pack_store<kBf16, kM>(sr, valid, c, m_ref, s_addr);
             if (!__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) {   // (a NaN sum takes the slow path)
               l += lsum;
-              return;
+              return true;
             }
           }
           const float m_tile = row_max<kM>(sr, valid) * c;
@@ -516,7 +516,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           if (j > 0) {
             tmem_st_wait();                             // the optimistic P is overwritten below
             // O may be rescaled only once PV(t - 1) has finished accumulating into it
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_free[(t - 1) % kSBufs], ((t - 1) / kSBufs) & 1, wc))) return;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_free[(t - 1) % kSBufs], ((t - 1) / kSBufs) & 1, wc)))
+              return false;
             tc_fence_after();
             const float alpha = rescale ? pg_ex2(m_ref - m_use) : 1.f;
 #pragma unroll 1
@@ -539,6 +540,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
           m_ref = m_new;
           l += exp_pack_store<kBf16, kM>(sr, valid, c, m_use, s_addr);
+          return true;
         };
         if (bad) {                                      // slots without a page: their scores become -inf where they are
 #pragma unroll 1
@@ -554,10 +556,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
           tmem_st_wait();
         }
-        if (__all_sync(0xffffffffu, valid >= kBN)) tile(std::false_type{});
-        else tile(std::true_type{});
-        ok = !__any_sync(0xffffffffu, wc->abort);
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, valid >= kBN) ? tile(std::false_type{}) : tile(std::true_type{});
+        if (!ok) break;                                 // (the same for the whole warp)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -569,6 +569,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       // ---- the item's (or this part's) state: straight out, or left as a partial ----
       const bool real = r < it.end.rows;
       const int64_t at = it.at0 + (int64_t)i_tok * a.H + g;
+      bool last = !it.end.left;                          // this block writes the item's output
       if (it.end.left) {
         float* dst = (a.phase == 1 ? a.pre : a.part) + (int64_t)it.end.slot * (kBM * (D + 2));
 #pragma unroll 1
@@ -584,16 +585,41 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
         }
         if (real) *reinterpret_cast<float2*>(dst + kBM * D + 2 * r) = make_float2(m_ref, l);
-      } else {
-        float M = m_ref, L = l;
-        float2 pm = make_float2(-INFINITY, 0.f);         // the shared prefix's state
-        if (prefix && real) {
-          pm = __ldcg(a.pre_ml + at);
-          M = fmaxf(M, pm.x);
-          L = fmaf(pg_weight(pm.x, M), pm.y, l * pg_weight(m_ref, M));
+        if (a.join_here) {
+          // Each warp has a ticket of its own for its 32 rows: its stores precede its release, and the last block's
+          // loads follow the acquire.
+          __syncwarp();
+          int* ticket = a.warp_tickets + 4 * it.end.c0 + quad;
+          int prev = 0;
+          if (lane == 0)
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(ticket) : "memory");
+          prev = __shfl_sync(0xffffffffu, prev, 0);
+          __syncwarp();                                  // (orders lane 0's acquire before the other lanes' loads)
+          last = prev == it.end.c1 - it.end.c0;
+          if (last && lane == 0) *ticket = 0;            // every block of the item is past it
+        }
+      }
+      if (last) {
+        // The prefix's state, then the parts in their order on the line (this block's from TMEM), whichever block is last.
+        const int c0 = it.end.left ? it.end.c0 : (int)blockIdx.x, c1 = it.end.left ? it.end.c1 : (int)blockIdx.x;
+        auto part = [&](int cc) { return a.part + (int64_t)(2 * cc + (cc == c0 ? 1 : 0)) * (kBM * (D + 2)); };
+        auto ml_of = [&](int cc) {
+          if (cc == (int)blockIdx.x) return make_float2(m_ref, l);
+          return __ldcg(reinterpret_cast<const float2*>(part(cc) + kBM * D + 2 * r));
+        };
+        float2 pm = make_float2(-INFINITY, 0.f);
+        float M = -INFINITY, L = 0.f;
+        if (real) {
+          if (prefix) pm = __ldcg(a.pre_ml + at);
+          M = pm.x;
+          for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, ml_of(cc).x);
+          L = pg_weight(pm.x, M) * pm.y;
+          for (int cc = c0; cc <= c1; ++cc) {
+            const float2 ml = ml_of(cc);
+            L = fmaf(pg_weight(ml.x, M), ml.y, L);
+          }
         }
         const float inv = L != 0.f ? 1.f / L : 0.f;
-        const float own = l != 0.f ? pg_weight(m_ref, M) * inv : 0.f;
         const float pw = pm.y != 0.f ? pg_weight(pm.x, M) * inv : 0.f;
         if (a.lse != nullptr && real)
           a.lse[at] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
@@ -607,15 +633,26 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           reg_fence32(orow);
           float x[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(orow[i]) * own;
-          if (pw != 0.f) {
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+          auto add = [&](float w, const float* src) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.pre_o + at * D + q4 * 32 + i));
-              x[i] = fmaf(pw, y.x, x[i]);
-              x[i + 1] = fmaf(pw, y.y, x[i + 1]);
-              x[i + 2] = fmaf(pw, y.z, x[i + 2]);
-              x[i + 3] = fmaf(pw, y.w, x[i + 3]);
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(src + q4 * 32 + i));
+              x[i] = fmaf(w, y.x, x[i]);
+              x[i + 1] = fmaf(w, y.y, x[i + 1]);
+              x[i + 2] = fmaf(w, y.z, x[i + 2]);
+              x[i + 3] = fmaf(w, y.w, x[i + 3]);
+            }
+          };
+          if (pw != 0.f) add(pw, a.pre_o + at * D);
+          for (int cc = c0; cc <= c1; ++cc) {
+            const float2 ml = real ? ml_of(cc) : make_float2(0.f, 0.f);
+            const float w = ml.y != 0.f ? pg_weight(ml.x, M) * inv : 0.f;
+            if (cc == (int)blockIdx.x) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = fmaf(w, __uint_as_float(orow[i]), x[i]);
+            } else if (w != 0.f) {
+              add(w, part(cc) + r * D);
             }
           }
           uint32_t pk[16];
@@ -652,7 +689,7 @@ size_t smem_bytes(int rows) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prepare) {
+cudaError_t launch(const kvc_paged* c, kvc_pg_args a, const void* q, void* out, cudaStream_t s, bool prepare) {
   static_assert(sizeof(Smem<D>) + 1024 + 16 + (4 * KVC_PG_MAX_BATCH + 1) * 4 + 16 <= 232448,
                 "shared memory above the 227 KB a block may opt into");
   if (prepare)
@@ -662,9 +699,11 @@ cudaError_t launch(const kvc_paged* c, const kvc_pg_args& a, const void* q, void
   const uint32_t box[4] = {64, (uint32_t)a.Gv, (uint32_t)(kBM / a.Gv), 1};
   if (!kvc_make_box_map(&tm_q, c->cfg.dtype, q, D, a.H, a.n_tokens, 1, box)) return cudaErrorInvalidValue;
   const int rows = a.phase == 1 ? 1 : a.B;
+  const int T_tok = kBM / a.Gv;
+  a.join_here = a.phase != 1 && 3 * (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok) >= KVC_PG_GRID;
   const cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
                                  c->tm_k, c->tm_v, (T*)out, a);
-  if (e != cudaSuccess || a.phase == 1) return e;
+  if (e != cudaSuccess || a.phase == 1 || a.join_here) return e;
   return kvc_pg_launch_join(c, a, out, s);
 }
 

@@ -87,7 +87,8 @@ kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& g) {
   const int sub = sub_groups(g.heads / g.kv_heads);
   const size_t Gv = (size_t)g.heads / g.kv_heads / sub, Hv = (size_t)g.kv_heads * sub;
   w.tickets = 256;
-  w.score_max = w.tickets + 4 * (size_t)KVC_PG_GRID_SIMT;
+  w.warp_tickets = w.tickets + 4 * (size_t)KVC_PG_GRID_SIMT;
+  w.score_max = w.warp_tickets + 4 * 4 * (size_t)KVC_PG_GRID;
   w.zeroed = up256(w.score_max + 4 * (size_t)g.batch * g.kv_heads);
   w.parts = w.zeroed;
   // two partials a block; a shared prefix's are at most its items and blocks together
@@ -127,6 +128,7 @@ kvc_pg_args kvc_pg_base_args(const kvc_paged* c) {
   a.scale_log2 = c->scale * 1.4426950408889634f;
   a.err = reinterpret_cast<int32_t*>(c->ws);
   a.tickets = reinterpret_cast<int*>(c->ws + w.tickets);
+  a.warp_tickets = reinterpret_cast<int*>(c->ws + w.warp_tickets);
   a.part = reinterpret_cast<float*>(c->ws + w.parts);
   a.pre = reinterpret_cast<float*>(c->ws + w.prefix);
   a.pre_o = reinterpret_cast<float*>(c->ws + w.pre_o);

@@ -35,6 +35,7 @@ struct kvc_paged {
 // Workspace, in bytes from its start.
 struct kvc_pg_layout {
   size_t tickets;       // int32 per block: blocks that have left their part of a split item
+  size_t warp_tickets;  // the same per softmax warp of the tensor-core kernel
   size_t score_max;     // fp32 per (row, kv head): bound of a score's terms
   size_t zeroed;        // end of what has to start at zero (and is left at zero)
   size_t parts;         // split partials
@@ -66,6 +67,8 @@ struct kvc_pg_args {
   int n_sel;
   float* part;                // [2 * grid][R][D + 2]: O (unnormalised), then (max, sum) per row
   int* tickets;
+  int* warp_tickets;          // the tensor-core kernel's, 4 per block, where it joins split items itself (join_here)
+  int join_here;
   float* pre;                 // phase 1's partials [items + blocks][R][D + 2]
   float* pre_o;               // joined: [n_tokens * H][D], unnormalised
   float2* pre_ml;             // (max, sum)
