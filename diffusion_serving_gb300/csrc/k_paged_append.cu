@@ -5,9 +5,12 @@
 // decode step's few tokens.  A block takes one run: the new tokens of one row that fall into one
 // page, so the row, the page number and the bounds are dealt with once per page.  A lane owns two
 // 16-byte vectors of a token's row, D/2 apart in one head: both halves of the pairs (x[j],
-// x[j + D/2]), or two vectors of pairs (x[2j], x[2j+1]).  Warps of a block share its columns out
-// and take every kth token of the run, kUnroll tokens loaded before any is stored.  A run's keys,
-// after rounding, give the page's maximum and minimum in registers: no second pass, no atomics.
+// x[j + D/2]), or two vectors of pairs (x[2j], x[2j+1]).  A block's warps are divided between columns
+// (32 such lanes' worth of the keys' and values' heads, or of the queries') and tokens: few tokens to
+// a run, and all of them are on columns; many, and each takes every eighth token, some four in all,
+// so that a long page does not become a long chain.  kUnroll tokens are loaded before any is stored.
+// A run's keys, after rounding, give the page's maximum and minimum in registers: no second pass, no
+// atomics.
 #include "paged_internal.h"
 #include "paged_rope.h"
 
@@ -45,9 +48,10 @@ struct AppendArgs {
   const float2* rope;
   int rope_positions;
   int B, n_tokens, ps_log2, n_pages, max_pages;
-  int runs, groups_y;         // run blocks (behind them: query blocks), column groups per block
+  int groups_y;               // column groups per block
   int64_t kv_stride, q_stride;
   int kv_cols, q_cols;        // vector pairs of a key / query row
+  int kv_groups;              // column groups of the keys; those of the queries follow
   int H, Hkv;
   int half;
 };
@@ -57,25 +61,21 @@ template <typename T, int D>
 __device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const float2* cs, int c, bool half) {
   constexpr int VL = Vec<T>::N;
   const T* type = nullptr;
-  if (half) {
 #pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const float2 t = __ldg(cs + c * VL + i);
-      const float a = to_f(x.e[i]), b = to_f(y.e[i]);
-      from_f(x.e[i], pg_rot(a, t.x, b, t.y, type));
-      from_f(y.e[i], pg_rot(a, t.y, b, -t.x, type));
-    }
-  } else {
+  for (int w = 0; w < 2; ++w) {
+    // VL / 2 pairs: of the two halves' elements w VL/2 .., or of vector w
+    const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+    float4 t[VL / 4];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      Vec<T>& z = w ? y : x;
+    for (int i = 0; i < VL / 4; ++i) t[i] = __ldg(reinterpret_cast<const float4*>(cs + first) + i);
 #pragma unroll
-      for (int i = 0; i < VL; i += 2) {
-        const float2 t = __ldg(cs + (w * (D / 2) + c * VL + i) / 2);
-        const float a = to_f(z.e[i]), b = to_f(z.e[i + 1]);
-        from_f(z.e[i], pg_rot(a, t.x, b, t.y, type));
-        from_f(z.e[i + 1], pg_rot(a, t.y, b, -t.x, type));
-      }
+    for (int i = 0; i < VL / 2; ++i) {
+      const float co = i & 1 ? t[i / 2].z : t[i / 2].x, si = i & 1 ? t[i / 2].w : t[i / 2].y;
+      T& e0 = half ? x.e[w * (VL / 2) + i] : (w ? y : x).e[2 * i];
+      T& e1 = half ? y.e[w * (VL / 2) + i] : (w ? y : x).e[2 * i + 1];
+      const float a = to_f(e0), b = to_f(e1);
+      from_f(e0, pg_rot(a, co, b, si, type));
+      from_f(e1, pg_rot(a, si, b, -co, type));
     }
   }
 }
@@ -138,36 +138,7 @@ k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* 
   if (blockIdx.x == 0 && blockIdx.y == 0)      // every row is checked once, whether or not a block comes to it
     for (int b = threadIdx.x; b < a.B; b += kThreads) row_of(a, b);
 
-  if ((int)blockIdx.x >= a.runs) {
-    // ---- queries: one warp per token and 32 vector pairs ----
-    const int groups = (a.q_cols + 31) / 32;
-    const long long n_warps = (long long)(gridDim.x - a.runs) * gridDim.y * kWarps;
-    const long long first = ((long long)(blockIdx.x - a.runs) * gridDim.y + blockIdx.y) * kWarps + warp;
-    for (long long e = first; e < (long long)a.n_tokens * groups; e += n_warps) {
-      const int t = (int)(e / groups), col = (int)(e % groups) * 32 + lane;
-      const int b = a.cu == nullptr ? t / (a.n_tokens / a.B) : search(a.B, t, [&](int i) { return (long long)a.cu[i]; });
-      const Row r = row_of(a, b);
-      if (!r.ok || t < r.t0 || t >= r.t0 + r.n) continue;
-      const int pos = r.len - r.n + (t - r.t0);
-      if (pos >= a.rope_positions) {
-        if (lane == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
-        continue;
-      }
-      if (col >= a.q_cols) continue;
-      const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
-      const T* src = q + (int64_t)t * a.q_stride + off;
-      Vec<T> x, y;
-      x.u = *reinterpret_cast<const uint4*>(src);
-      y.u = *reinterpret_cast<const uint4*>(src + D / 2);
-      turn<T, D>(x, y, a.rope + (int64_t)pos * (D / 2), col % PH, a.half);
-      T* dst = q_out + (int64_t)t * a.H * D + off;
-      *reinterpret_cast<uint4*>(dst) = x.u;
-      *reinterpret_cast<uint4*>(dst + D / 2) = y.u;
-    }
-    return;
-  }
-
-  // ---- keys and values: the run of this block ----
+  // ---- the run of this block ----
   // Runs are numbered with room to spare: row b's start at cu[b] / page_size + 2 b, which leaves each
   // row at least as many numbers as its tokens can touch pages.
   int b, j;
@@ -188,17 +159,46 @@ k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* 
   const int column = (p0 >> a.ps_log2) + j;
   const int lo = max(p0, column << a.ps_log2), hi = min(r.len, (column + 1) << a.ps_log2);
   if (lo >= hi) return;
-  const int page = a.table[(int64_t)b * a.max_pages + column];
-  if (page < 0 || page >= a.n_pages) {
-    if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_PAGE);
-    return;
-  }
   const int end = a.rope != nullptr ? min(hi, a.rope_positions) : hi;
   if (end < hi && threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
   const int gw = a.groups_y;                        // column groups this block's warps divide into
-  const int col = ((int)blockIdx.y * gw + warp % gw) * 32 + lane;
+  const int group = (int)blockIdx.y * gw + warp % gw;
   const int stride = kWarps / gw;
-  const bool have = col < a.kv_cols;
+  if (group >= a.kv_groups) {
+    // ---- queries ----
+    const int col = (group - a.kv_groups) * 32 + lane;
+    if (col < a.q_cols) {
+      const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
+      for (int p = lo + warp / gw; p < end; p += stride * kUnroll) {
+        Vec<T> x[kUnroll], y[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int pp = p + u * stride;
+          if (pp >= end) continue;
+          const T* src = q + (int64_t)(r.t0 + pp - p0) * a.q_stride + off;
+          x[u].u = *reinterpret_cast<const uint4*>(src);
+          y[u].u = *reinterpret_cast<const uint4*>(src + D / 2);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int pp = p + u * stride;
+          if (pp >= end) continue;
+          turn<T, D>(x[u], y[u], a.rope + (int64_t)pp * (D / 2), col % PH, a.half);
+          T* dst = q_out + (int64_t)(r.t0 + pp - p0) * a.H * D + off;
+          *reinterpret_cast<uint4*>(dst) = x[u].u;
+          *reinterpret_cast<uint4*>(dst + D / 2) = y[u].u;
+        }
+      }
+    }
+  }
+  // ---- keys and values ----
+  const int page = a.table[(int64_t)b * a.max_pages + column];
+  if (page < 0 || page >= a.n_pages) {              // (the same for the whole block)
+    if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+    return;
+  }
+  const int col = group * 32 + lane;
+  const bool have = group < a.kv_groups && col < a.kv_cols;
   const int head = have ? col / PH : 0, c = have ? col % PH : 0;
   const int64_t src0 = (int64_t)head * D + c * VL;
   const int64_t dst_row = (int64_t)a.Hkv * D;
@@ -285,18 +285,17 @@ cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, vo
   constexpr int VL = Vec<T>::N;
   a.kv_cols = a.Hkv * (D / 2 / VL);
   a.q_cols = q != nullptr ? a.H * (D / 2 / VL) : 0;
-  // warps of a block over column groups of 32 vector pairs: 1, 2, 4 or 8 of them, the rest over tokens
-  const int groups = (a.kv_cols + 31) / 32;
-  a.groups_y = groups >= 8 ? 8 : groups >= 4 ? 4 : groups >= 2 ? 2 : 1;
-  const int gy = (groups + a.groups_y - 1) / a.groups_y;
+  a.kv_groups = (a.kv_cols + 31) / 32;
+  const int groups = a.kv_groups + (a.q_cols + 31) / 32;
+  // a warp takes about four tokens of a run: one warp of a column for runs of up to 4 tokens, ... 8 for more than 16
   const int ps = 1 << a.ps_log2;
+  const int mean = (a.n_tokens + a.B - 1) / a.B, run = mean < ps ? mean : ps;
+  const int on_tokens = run <= 4 ? 1 : run <= 8 ? 2 : run <= 16 ? 4 : 8;
+  a.groups_y = kWarps / on_tokens;
+  const int gy = (groups + a.groups_y - 1) / a.groups_y;
   const int64_t runs = a.cu == nullptr ? (int64_t)a.B * ((a.n_tokens / a.B + ps - 2) / ps + 1)
                                        : (int64_t)a.n_tokens / ps + 2 * (int64_t)a.B;
-  const int64_t q_warps = (int64_t)a.n_tokens * ((a.q_cols + 31) / 32);
-  int64_t q_blocks = (q_warps + (int64_t)kWarps * gy - 1) / ((int64_t)kWarps * gy);
-  if (q_blocks > 16 * KVC_PG_GRID) q_blocks = 16 * KVC_PG_GRID;
-  a.runs = (int)runs;
-  const dim3 grid((unsigned)(runs + q_blocks), gy);
+  const dim3 grid((unsigned)runs, gy);
   if (c->bounds != nullptr)
     return kvc_launch_pdl(k_paged_append<T, D, true>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
                           (T*)c->k, (T*)c->v, (T*)q_out, (T*)c->bounds, a);

@@ -199,7 +199,7 @@ int kvc_paged_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stri
   const int64_t vec = g.dtype == KVC_F32 ? 4 : 8;      // elements of 16 bytes
   const int64_t kv_row = (int64_t)g.kv_heads * g.head_dim, q_row = (int64_t)g.heads * g.head_dim;
   if (kv_stride < kv_row || kv_stride % vec) return KVC_ERR_ARG;
-  if (d_rope != nullptr && (!aligned(d_rope, 8) || rope_positions < 1)) return KVC_ERR_ARG;
+  if (d_rope != nullptr && (!aligned(d_rope, 16) || rope_positions < 1)) return KVC_ERR_ARG;
   if ((q == nullptr) != (q_out == nullptr)) return KVC_ERR_ARG;
   if (q != nullptr) {
     if (d_rope == nullptr || !aligned(q, 16) || !aligned(q_out, 16) || q_stride < q_row || q_stride % vec) return KVC_ERR_ARG;

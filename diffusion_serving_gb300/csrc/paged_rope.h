@@ -8,7 +8,11 @@
 // midpoint of the store type, which its low bits show.  The rest (less than one in 400 of N(0, 1)
 // data) goes through fp64: both products are exact there, their difference is a rounded sum plus
 // its exact rest (Knuth's TwoSum), and rounding that to odd in fp32 leaves one rounding to come.
-// fp32 stores: the fp64 sum rounds right except on an fp32 midpoint, where the rest decides.
+// fp32 stores: both products and their errors, and the errors of the sums, in fp32; the result stands
+// if moving the last of them by a bound on what is neglected does not change its rounding (all but
+// some 2^-22 of the cases).  The rest goes through fp64, whose sum rounds right except on an fp32
+// midpoint, where its own rest decides.  (fp64 for every element would take some twenty times as long
+// as the copy.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -54,7 +58,7 @@ __device__ __forceinline__ float pg_rot(float a, float b, float c, float d, cons
                   pg_clear(r2, type);
   return ok ? r2 : pg_rot_odd(a, b, c, d);
 }
-__device__ __forceinline__ float pg_rot(float a, float b, float c, float d, const float*) {
+__device__ __noinline__ float pg_rot_f32(float a, float b, float c, float d) {
   double rest;
   const double s = pg_two_prod_diff(a, b, c, d, &rest);
   const float f = __double2float_rn(s);
@@ -65,4 +69,22 @@ __device__ __forceinline__ float pg_rot(float a, float b, float c, float d, cons
   const double down = isinf(lo) ? copysign(0x1p128, (double)lo) : (double)lo;
   if (s != 0.5 * (up + down)) return f;
   return rest > 0.0 ? hi : lo;
+}
+__device__ __forceinline__ float pg_two_sum(float x, float y, float* err) {
+  const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
+  *err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
+  return s;
+}
+__device__ __forceinline__ float pg_rot(float a, float b, float c, float d, const float*) {
+  const float p = __fmul_rn(a, b), ep = __fmaf_rn(a, b, -p);
+  const float q = __fmul_rn(c, d), eq = __fmaf_rn(c, d, -q);
+  float es, e;
+  const float s = pg_two_sum(p, -q, &es);
+  const float u = __fsub_rn(ep, eq);                  // a b - c d = s + es + u, but for u's rounding
+  const float r = pg_two_sum(s, __fadd_rn(es, u), &e);
+  const float slack = (fabsf(es) + fabsf(ep) + fabsf(eq)) * 0x1p-22f;   // bounds that and the sum's own rounding
+  const float m = fminf(fabsf(p), fabsf(q));
+  const bool ok = m >= 0x1p-100f && fabsf(r) >= 0x1p-100f && fabsf(r) <= 0x1p126f &&
+                  __fadd_rn(r, __fadd_rn(e, slack)) == r && __fadd_rn(r, __fsub_rn(e, slack)) == r;
+  return ok ? r : pg_rot_f32(a, b, c, d);
 }
