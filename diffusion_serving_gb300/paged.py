@@ -108,6 +108,14 @@ def _dense(what, t, shape, dtype, device):
     return t
 
 
+# The current stream's handle without a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(index):
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class PagedKVCache:
     """A paged cache: pools of pages, each row's page numbers and length, and a handle over them.
 
@@ -131,7 +139,7 @@ class PagedKVCache:
         device = torch.device(device)
         if device.index is None:
             device = torch.device(device.type, torch.cuda.current_device())
-        self.device = device
+        self.device, self._index = device, device.index
         pool = (n_pages, page_size, kv_heads, head_dim)
 
         def own(what, t, shape, dt, fill=None):
@@ -152,43 +160,55 @@ class PagedKVCache:
                                            self.kv_len, self.workspace, stream)
 
     # -- arguments ----------------------------------------------------------------------
+    # (A decode step's kernels take some ten microseconds, and what these checks take comes on top of each
+    # call: they look at each property once, and build messages only when one is wrong.)
     def _stream(self, stream):
         """The stream's handle; without one, the current stream of the cache's device."""
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _call(self, what, fn, *args):
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
+        rc = fn(self.handle, *args)
+        if rc == ERR_ARG and torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self.device):       # (refused before anything was enqueued)
                 rc = fn(self.handle, *args)
-        else:
-            rc = fn(self.handle, *args)
         if rc != OK:
             raise KvcError(rc, what)
 
     def _tokens(self, what, t, heads):
         """The number of token rows of ``t``: [total, heads, D] or [batch, n, heads, D]."""
         shape = t.shape
-        if t.dtype != self.dtype or t.device != self.device or len(shape) not in (3, 4) or shape[-2] != heads or \
-                shape[-1] != self.head_dim or (len(shape) == 4 and shape[0] != self.batch):
-            raise ValueError(f"kvc: {what} must be [tokens, {heads}, {self.head_dim}] or [{self.batch}, n, {heads}, "
-                             f"{self.head_dim}] {self.dtype} on {self.device}, got {list(shape)} {t.dtype} on {t.device}")
-        return shape[0] if len(shape) == 3 else shape[0] * shape[1]
+        if t.dtype is self.dtype and t.get_device() == self._index:
+            if len(shape) == 3:
+                n, h, d = shape
+                if h == heads and d == self.head_dim:
+                    return n
+            elif len(shape) == 4:
+                b, n, h, d = shape
+                if h == heads and d == self.head_dim and b == self.batch:
+                    return b * n
+        raise ValueError(f"kvc: {what} must be [tokens, {heads}, {self.head_dim}] or [{self.batch}, n, {heads}, "
+                         f"{self.head_dim}] {self.dtype} on {self.device}, got {list(shape)} {t.dtype} on {t.device}")
 
     def _rows(self, what, t, heads):
         """(token rows, elements from one to the next) of ``t``, whose rows are dense and evenly apart."""
         n = self._tokens(what, t, heads)
         s = t.stride()
-        row = s[-3]
-        if s[-1] != 1 or s[-2] != self.head_dim or (len(s) == 4 and t.shape[0] > 1 and s[0] != t.shape[1] * row):
+        if len(s) == 3:
+            row, head, one = s
+            even = True
+        else:
+            batch, row, head, one = s
+            even = batch == t.shape[1] * row or t.shape[0] == 1
+        if one != 1 or not even or (head != self.head_dim and heads > 1):
             raise ValueError(f"kvc: {what}: a token's heads must be dense and its tokens evenly apart, got strides {list(s)}")
-        return n, max(row, heads * self.head_dim) if n == 1 else row
+        return n, row if n > 1 else max(row, heads * self.head_dim)
 
     def _cu(self, cu):
         if cu is None:
             return None
-        if cu.dtype != torch.int32 or cu.numel() != self.batch + 1 or cu.device != self.device or not cu.is_contiguous():
+        if cu.dtype is not torch.int32 or cu.numel() != self.batch + 1 or cu.get_device() != self._index or not cu.is_contiguous():
             raise ValueError(f"kvc: row offsets must be a dense int32 [{self.batch + 1}] on {self.device}")
         return cu.data_ptr()
 
@@ -196,16 +216,22 @@ class PagedKVCache:
         n = self._tokens("q", q, self.heads)
         if not q.is_contiguous():
             raise ValueError("kvc: q must be dense")
+        shape = q.shape
         if out is None:
             out = torch.empty_like(q)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
-            raise ValueError(f"kvc: out must match q ({list(q.shape)} {q.dtype} on {q.device}, dense)")
+        elif out.dtype is not self.dtype or out.shape != shape or out.get_device() != self._index or not out.is_contiguous():
+            raise ValueError(f"kvc: out must match q ({list(shape)} {q.dtype} on {q.device}, dense)")
+        if lse is None:
+            return n, out, None, None
         if lse is True:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-        elif lse is not None and (lse.shape != q.shape[:-1] or lse.dtype != torch.float32 or lse.device != q.device or
-                                  not lse.is_contiguous()):
-            raise ValueError(f"kvc: lse must be a dense float32 {list(q.shape[:-1])}")
-        return n, out, lse
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        else:
+            rows = lse.shape
+            if lse.dtype is not torch.float32 or len(rows) != len(shape) - 1 or rows[0] != shape[0] or \
+                    rows[-1] != self.heads or lse.numel() != n * self.heads or lse.get_device() != self._index or \
+                    not lse.is_contiguous():
+                raise ValueError(f"kvc: lse must be a dense float32 {list(shape[:-1])}")
+        return n, out, lse, lse.data_ptr()
 
     # -- calls --------------------------------------------------------------------------
     def append(self, k, v, *, cu_new=None, rope=None, half=False, q=None, q_out=None, stream=None):
@@ -216,10 +242,12 @@ class PagedKVCache:
         nv, vstride = self._rows("v", v, self.kv_heads)
         if n != nv or stride != vstride:
             raise ValueError(f"kvc: k and v must have the same rows and strides ({n}, {stride} and {nv}, {vstride})")
-        n_pos = 0
+        n_pos, rp = 0, None
         if rope is not None:
-            n_pos = rope.shape[0]
-            _dense("rope", rope, (n_pos, self.head_dim // 2, 2), torch.float32, self.device)
+            if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.numel() != len(rope) * self.head_dim or \
+                    rope.shape[2] != 2 or rope.get_device() != self._index or not rope.is_contiguous():
+                raise ValueError(f"kvc: rope must be a dense float32 [positions, {self.head_dim // 2}, 2] on {self.device}")
+            n_pos, rp = len(rope), rope.data_ptr()
         qp = op = None
         q_stride = 0
         if q is not None:
@@ -228,22 +256,23 @@ class PagedKVCache:
                 raise ValueError(f"kvc: q has {nq} tokens, k {n}")
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != q.device or not q_out.is_contiguous():
+            elif q_out.dtype is not self.dtype or q_out.shape != q.shape or q_out.get_device() != self._index or \
+                    not q_out.is_contiguous():
                 raise ValueError("kvc: q_out must be dense and match q")
             qp, op = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("kvc: q_out without q")
         self._call("kvc_paged_append", _lib.kvc_paged_append, k.data_ptr(), v.data_ptr(), stride, qp, q_stride, op, n,
-                   self._cu(cu_new), None if rope is None else rope.data_ptr(), n_pos, ROPE_HALF if half else 0,
+                   self._cu(cu_new), rp, n_pos, ROPE_HALF if half else 0,
                    self._stream(stream))
         return q_out
 
     def attend(self, q, *, cu_q=None, max_q=None, out=None, lse=None, flags=0, stream=None):
         """Attention of every token over its row's slots.  ``max_q``: most tokens of a row (with ``cu_q``;
         None: all of them).  ``lse``: a buffer, or True for a new one; then (out, lse) is returned."""
-        n, out, lse = self._q(q, out, lse)
+        n, out, lse, lse_ptr = self._q(q, out, lse)
         self._call("kvc_paged_attend", _lib.kvc_paged_attend, q.data_ptr(), out.data_ptr(),
-                   None if lse is None else lse.data_ptr(), n, self._cu(cu_q), n if max_q is None else max_q, flags,
+                   lse_ptr, n, self._cu(cu_q), n if max_q is None else max_q, flags,
                    self._stream(stream))
         return out if lse is None else (out, lse)
 
@@ -251,14 +280,14 @@ class PagedKVCache:
                       stream=None):
         """``attend`` for rows whose first ``prefix_len`` (int32 [1], on the device) slots are those of
         ``prefix_pages`` (int32): they are read once for all rows."""
-        n, out, lse = self._q(q, out, lse)
+        n, out, lse, lse_ptr = self._q(q, out, lse)
         for what, t in (("prefix_pages", prefix_pages), ("prefix_len", prefix_len)):
-            if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous():
+            if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous():
                 raise ValueError(f"kvc: {what} must be a dense int32 tensor on {self.device}")
         if prefix_len.numel() != 1:
             raise ValueError("kvc: prefix_len holds one length")
         self._call("kvc_paged_attend_shared", _lib.kvc_paged_attend_shared, q.data_ptr(), out.data_ptr(),
-                   None if lse is None else lse.data_ptr(), n, self._cu(cu_q), n if max_q is None else max_q,
+                   lse_ptr, n, self._cu(cu_q), n if max_q is None else max_q,
                    prefix_pages.data_ptr(), prefix_pages.numel(), prefix_len.data_ptr(), flags, self._stream(stream))
         return out if lse is None else (out, lse)
 
@@ -266,17 +295,17 @@ class PagedKVCache:
         """Attention of one token per row over ``n_select`` pages per kv head: the ``first`` and the newest
         ``recent`` ones, and those whose bounds promise the largest scores.  Returns (out, lse, selected), or
         (out, selected) without ``lse``; selected int32 [batch, kv_heads, n_select], -1 behind the last."""
-        n, out, lse = self._q(q, out, lse)
+        n, out, lse, lse_ptr = self._q(q, out, lse)
         if n != self.batch:
             raise ValueError(f"kvc: attend_sparse takes one token per row ({self.batch}), got {n}")
         shape = (self.batch, self.kv_heads, n_select)
         if selected is None:
             selected = torch.empty(shape, dtype=torch.int32, device=self.device)
-        elif selected.shape != shape or selected.dtype != torch.int32 or selected.device != self.device or \
+        elif selected.dtype is not torch.int32 or selected.shape != shape or selected.get_device() != self._index or \
                 not selected.is_contiguous():
             raise ValueError(f"kvc: selected must be a dense int32 {list(shape)}")
         self._call("kvc_paged_attend_sparse", _lib.kvc_paged_attend_sparse, q.data_ptr(), out.data_ptr(),
-                   None if lse is None else lse.data_ptr(), n_select, first, recent, selected.data_ptr(), flags,
+                   lse_ptr, n_select, first, recent, selected.data_ptr(), flags,
                    self._stream(stream))
         return (out, selected) if lse is None else (out, lse, selected)
 

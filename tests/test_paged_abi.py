@@ -62,7 +62,7 @@ class Fake(paged.PagedKVCache):
 
     def __init__(self, dtype=torch.bfloat16):
         self.batch, self.heads, self.kv_heads, self.head_dim, self.dtype = 2, 8, 2, 64, dtype
-        self.device, self.handle, self.calls = torch.device("cpu"), None, []
+        self.device, self._index, self.handle, self.calls = torch.device("cpu"), -1, None, []
 
     def _stream(self, stream):
         return None
