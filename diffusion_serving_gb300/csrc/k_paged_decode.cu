@@ -509,7 +509,7 @@ cudaError_t kvc_pg_prepare_decode(const kvc_paged* c) {
   return cudaSuccess;
 }
 
-// Rows of at most max_q tokens of Gv heads each: max_q * Gv <= 16.
+// (More than 16 rows to a group make several items of up to 16, each with a pass of its own over the keys.)
 cudaError_t kvc_pg_launch_decode(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s) {
   const bool wide = a.max_q * a.Gv > 8;
   return c->cfg.dtype == KVC_F16 ? launch_t<__half>(c, a, q, out, wide, s, false)

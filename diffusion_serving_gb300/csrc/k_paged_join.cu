@@ -29,8 +29,7 @@ k_paged_join(T* __restrict__ out, kvc_pg_args a) {
   int c0 = 0, c1 = 0;
   if (any) {
     it = sch.at(a, (int)end - 1);
-    c0 = it.start / sch.per;
-    c1 = (it.start + it.tiles - 1) / sch.per;
+    sch.span(it, &c0, &c1);
   }
   kvc_pdl_wait();
   kvc_pdl_release();

@@ -277,7 +277,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   const uint32_t tmem = sm.tmem_base;
   kvc_pdl_wait();
   kvc_pdl_release();
-  kvc_pg_sched<kBM, kBN> sch;
+  kvc_pg_sched<kBM, kBN, true> sch;
   sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), a.phase == 1 ? 1 : KVC_PG_TC_MIN,
            KVC_PG_TC_COST, gridDim.x);
   const int ps = 1 << a.ps_log2;
@@ -684,13 +684,13 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
 // More than half of an SM's shared memory even where D = 64 needs less: one block per SM, since each takes all of TMEM.
 template <int D>
 size_t smem_bytes(int rows) {
-  const size_t n = 1024 + ((sizeof(Smem<D>) + 15) & ~(size_t)15) + pg_sched_bytes(rows);
+  const size_t n = 1024 + ((sizeof(Smem<D>) + 15) & ~(size_t)15) + pg_sched_bytes(rows, true);
   return n < 120 * 1024 ? 120 * 1024 : n;
 }
 
 template <typename T, int D>
 cudaError_t launch(const kvc_paged* c, kvc_pg_args a, const void* q, void* out, cudaStream_t s, bool prepare) {
-  static_assert(sizeof(Smem<D>) + 1024 + 16 + (4 * KVC_PG_MAX_BATCH + 1) * 4 + 16 <= 232448,
+  static_assert(sizeof(Smem<D>) + 1024 + 16 + (5 * KVC_PG_MAX_BATCH + KVC_PG_GRID + 3) * 4 + 16 <= 232448,
                 "shared memory above the 227 KB a block may opt into");
   if (prepare)
     return cudaFuncSetAttribute(k_paged_tc<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -56,14 +56,18 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
   return on_device(c) ? KVC_OK : KVC_ERR_ARG;
 }
 
-// Kernel by type and shape: fp32 stores (and KVC_KERNEL_SIMT) run the FMA kernel; 16-bit ones with at
-// most 16 query rows per group the streaming kernel, with more (and for a shared prefix, where the
-// batch's rows are stacked) the tensor-core kernel.
+// Kernel by type and shape: fp32 stores (and KVC_KERNEL_SIMT) run the FMA kernel; 16-bit ones with few
+// query rows per group the streaming kernel, with more (and for a shared prefix, where the batch's rows
+// are stacked) the tensor-core kernel.  "Few" is 16 rows, one pass over a row's keys, or 32, two passes,
+// where rows can hold no more than 2048 slots (behind the prefix): 20 rows over 500 slots take 11.8 us
+// in two passes and 15.1 in the tensor-core kernel, over 8000 slots of 8 rows 90 and 59; 48 rows over
+// 500 slots of 8 rows 19.5 and 20.5, over 300 slots of 32 rows 42 and 31.
 bool simt_only(const kvc_paged* c, uint32_t flags) { return c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT); }
 
 cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, uint32_t flags, cudaStream_t s) {
   if (simt_only(c, flags)) return kvc_pg_launch_simt(c, a, q, out, s);
-  if (a.phase != 1 && (int64_t)a.max_q * a.Gv <= 16) return kvc_pg_launch_decode(c, a, q, out, s);
+  const int slots = (a.max_pages - (a.phase == 2 ? a.prefix_cap : 0)) << a.ps_log2;
+  if (a.phase != 1 && (int64_t)a.max_q * a.Gv <= (slots <= 2048 ? 32 : 16)) return kvc_pg_launch_decode(c, a, q, out, s);
   return kvc_pg_launch_tc(c, a, q, out, s);
 }
 

@@ -92,12 +92,11 @@ struct kvc_pg_end {
   int slot;              // where this block leaves its state, if it does
   bool left;             // it does: the item spans blocks, or phase 1 leaves it for kvc_pg_launch_join_prefix
 };
-template <int R, int TS>
-__device__ __forceinline__ kvc_pg_end pg_end(const kvc_pg_args& a, const kvc_pg_sched<R, TS>& sch, const kvc_pg_item& it) {
+template <int R, int TS, bool kW>
+__device__ __forceinline__ kvc_pg_end pg_end(const kvc_pg_args& a, const kvc_pg_sched<R, TS, kW>& sch, const kvc_pg_item& it) {
   kvc_pg_end e;
   e.rows = min(sch.T, it.r.n - it.k * sch.T) * a.Gv;
-  e.c0 = it.start / sch.per;
-  e.c1 = (it.start + it.tiles - 1) / sch.per;
+  sch.span(it, &e.c0, &e.c1);
   e.left = a.phase == 1 || e.c0 != e.c1;
   // phase 1: item + block (item and block borders only move forward, so no two collide); else the block's second
   // slot for the item that begins in it, its first for one that goes on
@@ -106,8 +105,8 @@ __device__ __forceinline__ kvc_pg_end pg_end(const kvc_pg_args& a, const kvc_pg_
   return e;
 }
 // Row of the outputs [n_tokens * H] for query row r of an item.
-template <int R, int TS>
-__device__ __forceinline__ int64_t pg_at(const kvc_pg_args& a, const kvc_pg_sched<R, TS>& sch, const kvc_pg_item& it, int r) {
+template <int R, int TS, bool kW>
+__device__ __forceinline__ int64_t pg_at(const kvc_pg_args& a, const kvc_pg_sched<R, TS, kW>& sch, const kvc_pg_item& it, int r) {
   const int i = r / a.Gv;
   return (int64_t)(it.r.t0 + it.k * sch.T + i) * a.H + it.vh * a.Gv + r - i * a.Gv;
 }

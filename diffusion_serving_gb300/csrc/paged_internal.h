@@ -196,6 +196,12 @@ __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int 
 // Where there are no more items than blocks, and they are alike or short, each item gets a whole
 // number of blocks instead: it is padded to `stride` places, a multiple of `per` (no empty ones), so
 // that no block works on two and no item is cut without need.
+//
+// Where there are many more items than blocks (kWaves, the tensor-core kernel), stretches would spread
+// the blocks over all rows and groups at once, whose K and V together may not fit in L2; then block c
+// first takes the whole items c, c + grid, ... of as many waves as surely end before the mean
+// load (blocks that run together are on neighbouring items and share their K and V), and the rest of
+// the line is cut into stretches that bring every block to that load.
 __host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int* per, int* stride) {
   *per = *stride = min_tiles;
   if (tiles <= min_tiles) return;
@@ -216,13 +222,17 @@ struct kvc_pg_item {
   int b, vh, k;          // row, group, token tile
   int tiles, start;      // its tiles, the first one's place on the line
   int tile0, tile1;      // those of this block
+  bool whole;            // taken whole, in a wave
   kvc_pg_row r;
 };
 
-// Shared memory of the sums: rows + 1 first places, then each row's (t0, n, len).
-__host__ __device__ inline size_t pg_sched_bytes(int B) { return ((size_t)(4 * B + 1) * 4 + 15) & ~(size_t)15; }
+// Shared memory of the sums: rows + 1 first places, then each row's (t0, n, len); with waves, rows + 1 first items and
+// the blocks' borders behind.
+__host__ __device__ inline size_t pg_sched_bytes(int B, bool waves = false) {
+  return ((size_t)(4 * B + 1 + (waves ? B + 1 + KVC_PG_GRID + 1 : 0)) * 4 + 15) & ~(size_t)15;
+}
 
-template <int R, int TS>
+template <int R, int TS, bool kWaves = false>
 struct kvc_pg_sched {
   int* base;             // [rows + 1] first place of each row
   int* rows;             // [rows][3]
@@ -230,6 +240,9 @@ struct kvc_pg_sched {
   bool causal;
   int total, per, stride, cost;   // stride: places between items' beginnings where they are padded, else 0
   int end;               // of this block's stretch
+  int waves, wave, from; // waves of whole items (0: none), the one at hand, where the stretches begin on the line
+  int* ibase;            // [rows + 1] first item of each row
+  int* cut;              // [KVC_PG_GRID + 1] the stretches' borders, as of `from`
 
   __device__ __forceinline__ kvc_pg_row row(int b) const {
     return kvc_pg_row{rows[3 * b], rows[3 * b + 1], rows[3 * b + 2], min(lo, rows[3 * b + 2])};
@@ -300,6 +313,7 @@ struct kvc_pg_sched {
     over = __any_sync(0xffffffffu, over) || tiles + items * item_cost > 0x7fffffffll - 65536;
     stride = 0;
     cost = item_cost;
+    waves = 0;
     if (over) {
       if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_OVERFLOW);
       total = 0;
@@ -313,8 +327,25 @@ struct kvc_pg_sched {
     } else {
       total = (int)(tiles + items * cost);
       per = max(min_tiles, (total + grid - 1) / grid);
+      if (kWaves && a.join_here) waves = (total / grid) / (most + cost);
     }
     __syncthreads();                       // (every warp has read the rows' own tiles)
+    if (kWaves && waves > 0 && warp == 1) {
+      ibase = rows + 3 * n_rows;
+      int carry = 0;
+      for (int b0 = 0; b0 < n_rows; b0 += 32) {
+        const int b = b0 + lane;
+        int x = b < n_rows ? a.Hv * token_tiles(rows[3 * b + 1]) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (b < n_rows) ibase[b + 1] = carry + x;
+        carry += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) ibase[0] = 0;
+    }
     if (warp == 0) {
       int carry = 0;
       for (int b0 = 0; b0 < n_rows; b0 += 32) {
@@ -335,11 +366,100 @@ struct kvc_pg_sched {
       if (lane == 0) base[0] = 0;
     }
     __syncthreads();
+    if (kWaves && waves > 0) {
+      ibase = rows + 3 * n_rows;
+      cut = ibase + n_rows + 1;
+      // what each block's whole items leave of the mean load (a place more, so that it is never nothing)
+      const int mean = total / grid + 2;
+      for (int c = threadIdx.x; c < grid; c += blockDim.x) {
+        int load = 0;
+        for (int w = 0; w < waves; ++w) load += item(a, c + w * grid).tiles + cost;
+        cut[c + 1] = mean - load;
+      }
+      const kvc_pg_item next_item = item(a, waves * grid, true);
+      from = next_item.tiles > 0 ? next_item.start - cost : total;
+      __syncthreads();
+      if (warp == 0) {
+        long long carry = 0;
+        for (int c0 = 0; c0 < grid; c0 += 32) {
+          const int c = c0 + lane;
+          long long x = c < grid ? cut[c + 1] : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          if (c < grid) cut[c + 1] = (int)min((long long)(total - from), carry + x);
+          carry += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) cut[0] = 0;
+      }
+      __syncthreads();
+    }
+  }
+
+  // Item i of the line, whole; with tiles = 0 where there are not so many.  Its start is left out unless asked for (token
+  // tiles before it are added up one by one where they differ).
+  __device__ __forceinline__ kvc_pg_item item(const kvc_pg_args& a, int i, bool with_start = false) const {
+    kvc_pg_item it;
+    it.tiles = 0;
+    if (i >= ibase[n_rows]) return it;
+    int b = 0, hi = n_rows;
+#pragma unroll 1
+    for (int step = 0; step < 11 && hi - b > 1; ++step) {
+      const int mid = (b + hi) >> 1;
+      if (ibase[mid] <= i) b = mid;
+      else hi = mid;
+    }
+    it.b = b;
+    it.r = row(b);
+    const int m = token_tiles(it.r.n);
+    i -= ibase[b];
+    it.vh = i / m;
+    it.k = i - it.vh * m;
+    it.tiles = pg_item_tiles(it.r, it.k, T, TS, causal);
+    it.start = 0;
+    if (with_start) {
+      it.start = base[b] + it.vh * ((base[b + 1] - base[b]) / a.Hv) + cost;
+      if (!causal) it.start += it.k * (it.tiles + cost);
+      else
+        for (int k = 0; k < it.k; ++k) it.start += pg_item_tiles(it.r, k, T, TS, true) + cost;
+    }
+    it.tile0 = 0;
+    it.tile1 = it.tiles;
+    it.whole = true;
+    return it;
+  }
+
+  // The blocks that an item spans.
+  __device__ __forceinline__ void span(const kvc_pg_item& it, int* c0, int* c1) const {
+    if (kWaves && it.whole) {
+      *c0 = *c1 = blockIdx.x;
+      return;
+    }
+    if (!kWaves || waves == 0) {
+      *c0 = it.start / per;
+      *c1 = (it.start + it.tiles - 1) / per;
+      return;
+    }
+    auto block_of = [&](int p) {           // the last c with cut[c] <= p (a block without a stretch holds no place)
+      int c = 0, hi = KVC_PG_GRID;
+#pragma unroll 1
+      for (int step = 0; step < 9 && hi - c > 1; ++step) {
+        const int mid = (c + hi) >> 1;
+        if (cut[mid] <= p) c = mid;
+        else hi = mid;
+      }
+      return c;
+    };
+    *c0 = block_of(it.start - from);
+    *c1 = block_of(it.start + it.tiles - 1 - from);
   }
 
   // The item that holds place p of the line (p < total); a whole warp calls it.
   __device__ __forceinline__ kvc_pg_item at(const kvc_pg_args& a, int p) const {
     kvc_pg_item it;
+    it.whole = false;
     int b = 0, hi = n_rows;
 #pragma unroll 1
     for (int step = 0; step < 11 && hi - b > 1; ++step) {
@@ -389,17 +509,33 @@ struct kvc_pg_sched {
 
   // Block c's first item; false if it has none.  A whole warp calls it.
   __device__ __forceinline__ bool first(const kvc_pg_args& a, int c, kvc_pg_item& it) {
+    if (kWaves && waves > 0) {
+      wave = 0;
+      it = item(a, c);
+      return true;
+    }
     if ((long long)c * per >= total) return false;
     const int p = c * per;
-    end = total - p > per ? p + per : total;
+    return stretch(a, p, total - p > per ? p + per : total, it);
+  }
+  __device__ __forceinline__ bool stretch(const kvc_pg_args& a, int p, int end_, kvc_pg_item& it) {
+    end = end_;
     it = at(a, p);
     it.tile0 = max(0, p - it.start);
     it.tile1 = min(it.tiles, end - it.start);
     return it.tile1 > it.tile0;            // (not if the stretch ends before the item's tiles begin)
   }
 
-  // The block's next item; false if there is none.
-  __device__ __forceinline__ bool next(const kvc_pg_args& a, kvc_pg_item& it) const {
+  // The block's next item; false if there is none.  A whole warp calls it.
+  __device__ __forceinline__ bool next(const kvc_pg_args& a, kvc_pg_item& it) {
+    if (kWaves && waves > 0 && wave < waves) {
+      if (++wave < waves) {
+        it = item(a, blockIdx.x + wave * gridDim.x);
+        return true;
+      }
+      const int p = from + cut[blockIdx.x], e = from + cut[blockIdx.x + 1];
+      return p < e && stretch(a, p, e, it);
+    }
     if (stride || it.start + it.tiles + cost >= end) return false;
     it.start += it.tiles + cost;
     if ((it.k + 1) * T < it.r.n) {

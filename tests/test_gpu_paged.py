@@ -256,6 +256,8 @@ ATTEND = [
     (36, 2, 64, 16, [90, 17], [2, 9], True),                # groups of 18 heads
     (34, 2, 128, 16, [70], [40], True),                     # a group of 17
     (16, 1, 128, 16, [2000], [33], True),
+    (16, 8, 64, 64, [150, 290, 160, 30, 133], [140, 150, 150, 0, 133], True),   # more items than blocks
+    (12, 12, 128, 16, [400, 131], [260, 129], False),
 ]
 
 
