@@ -119,10 +119,25 @@ __device__ __forceinline__ float2 pair_f(uint32_t u, const __half*) { return __h
 __device__ __forceinline__ float2 pair_f(uint32_t u, const __nv_bfloat16*) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
-// the pair's positive (or negative) parts: a 16-bit half whose sign bit does not fit becomes 0
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, const __half*) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, const __nv_bfloat16*) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __half*) {
+  const __half2 r = __hmin2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __nv_bfloat16*) {
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// the pair's positive (or negative) parts
 __device__ __forceinline__ uint32_t part_of(uint32_t u, bool negative) {
-  const uint32_t sign = u & 0x80008000u;
-  const uint32_t neg = (sign >> 15) * 0xffffu;             // ffff where the half is negative
+  const uint32_t neg = __byte_perm(u, 0u, 0xbb99u);        // ffff where the half is negative
   return negative ? u & neg : u & ~neg;
 }
 
@@ -167,7 +182,7 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, o));
-    float top = 0.f;
+    uint32_t top2 = 0u, low2 = 0u;          // largest upper and least lower bound (or 0), 16-bit pairs
     int page = first + n < np ? __ldg(table + first + n) : -1;
     for (int j = first; j < np; j += step) {
       const bool ok = page >= 0 && page < a.n_pages;       // (a bad page is reported by the attention that meets it)
@@ -188,8 +203,8 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
           mma<T>(s[h], qa[h][v][1], w[2], w[3]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 f = pair_f(w[i], type);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            if (h == 0) top2 = max2(top2, w[i], type);
+            else low2 = min2(low2, w[i], type);
           }
         }
       // head g0 + n of this lane: pages j + 2 c, + 1
@@ -206,7 +221,9 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
         if (i + 1 < np) out[i + 1] = g0 == 0 ? u1 : fmaxf(out[i + 1], u1);
       }
     }
-    terms = fmaxf(terms, l1 * top);         // no score's terms sum to more
+    // no score's terms sum to more (an upper bound below 0 has a lower one further from it)
+    const float2 top = pair_f(top2, type), low = pair_f(low2, type);
+    terms = fmaxf(terms, l1 * fmaxf(fmaxf(top.x, top.y), -fminf(low.x, low.y)));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) terms = fmaxf(terms, __shfl_xor_sync(0xffffffffu, terms, o));
