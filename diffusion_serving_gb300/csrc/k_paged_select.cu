@@ -137,7 +137,8 @@ __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __nv_bflo
 }
 // the pair's positive (or negative) parts
 __device__ __forceinline__ uint32_t part_of(uint32_t u, bool negative) {
-  const uint32_t neg = __byte_perm(u, 0u, 0xbb99u);        // ffff where the half is negative
+  uint32_t neg;                                            // ffff where the half is negative
+  asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(neg) : "r"(u));
   return negative ? u & neg : u & ~neg;
 }
 
