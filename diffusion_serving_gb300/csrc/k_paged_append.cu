@@ -17,7 +17,6 @@
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnroll = 2;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -57,17 +56,28 @@ struct AppendArgs {
 };
 
 // Turns the two vectors x (elements c VL ..) and y (D/2 further) of a head by the row `cs` of the table.
+template <typename T>
+struct Turn {
+  float4 t[2][Vec<T>::N / 4];
+};
+// The entries of VL / 2 pairs each: of the two halves' elements w VL/2 .., or of vector w.
 template <typename T, int D>
-__device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const float2* cs, int c, bool half) {
+__device__ __forceinline__ void load_turn(Turn<T>& t, const float2* cs, int c, bool half) {
+  constexpr int VL = Vec<T>::N;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+#pragma unroll
+    for (int i = 0; i < VL / 4; ++i) t.t[w][i] = __ldg(reinterpret_cast<const float4*>(cs + first) + i);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const Turn<T>& cs, bool half) {
   constexpr int VL = Vec<T>::N;
   const T* type = nullptr;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    // VL / 2 pairs: of the two halves' elements w VL/2 .., or of vector w
-    const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
-    float4 t[VL / 4];
-#pragma unroll
-    for (int i = 0; i < VL / 4; ++i) t[i] = __ldg(reinterpret_cast<const float4*>(cs + first) + i);
+    const float4* t = cs.t[w];
 #pragma unroll
     for (int i = 0; i < VL / 2; ++i) {
       const float co = i & 1 ? t[i / 2].z : t[i / 2].x, si = i & 1 ? t[i / 2].w : t[i / 2].y;
@@ -125,7 +135,7 @@ __device__ __forceinline__ int search(int B, long long x, F f) {
 }
 
 template <typename T, int D, bool kBounds>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
                T* q_out, T* __restrict__ bounds, AppendArgs a) {
   constexpr int VL = Vec<T>::N;
@@ -169,25 +179,17 @@ k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* 
     const int col = (group - a.kv_groups) * 32 + lane;
     if (col < a.q_cols) {
       const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
-      for (int p = lo + warp / gw; p < end; p += stride * kUnroll) {
-        Vec<T> x[kUnroll], y[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int pp = p + u * stride;
-          if (pp >= end) continue;
-          const T* src = q + (int64_t)(r.t0 + pp - p0) * a.q_stride + off;
-          x[u].u = *reinterpret_cast<const uint4*>(src);
-          y[u].u = *reinterpret_cast<const uint4*>(src + D / 2);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int pp = p + u * stride;
-          if (pp >= end) continue;
-          turn<T, D>(x[u], y[u], a.rope + (int64_t)pp * (D / 2), col % PH, a.half);
-          T* dst = q_out + (int64_t)(r.t0 + pp - p0) * a.H * D + off;
-          *reinterpret_cast<uint4*>(dst) = x[u].u;
-          *reinterpret_cast<uint4*>(dst + D / 2) = y[u].u;
-        }
+      for (int p = lo + warp / gw; p < end; p += stride) {
+        Vec<T> x, y;
+        Turn<T> cs;
+        const T* src = q + (int64_t)(r.t0 + p - p0) * a.q_stride + off;
+        x.u = *reinterpret_cast<const uint4*>(src);
+        y.u = *reinterpret_cast<const uint4*>(src + D / 2);
+        load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), col % PH, a.half);
+        turn<T>(x, y, cs, a.half);
+        T* dst = q_out + (int64_t)(r.t0 + p - p0) * a.H * D + off;
+        *reinterpret_cast<uint4*>(dst) = x.u;
+        *reinterpret_cast<uint4*>(dst + D / 2) = y.u;
       }
     }
   }
@@ -205,41 +207,33 @@ k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* 
   Vec<T> mx0, mx1, mn0, mn1;
   bool any = false;
   if (have) {
-    for (int p = lo + warp / gw; p < end; p += stride * kUnroll) {
-      Vec<T> x[kUnroll], y[kUnroll], vx[kUnroll], vy[kUnroll];
+    for (int p = lo + warp / gw; p < end; p += stride) {
+      Vec<T> x, y, vx, vy;
+      Turn<T> cs;
+      const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
+      x.u = __ldg(reinterpret_cast<const uint4*>(k + off));
+      y.u = __ldg(reinterpret_cast<const uint4*>(k + off + D / 2));
+      if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+      vx.u = __ldg(reinterpret_cast<const uint4*>(v + off));
+      vy.u = __ldg(reinterpret_cast<const uint4*>(v + off + D / 2));
+      const int64_t dst = (((int64_t)page << a.ps_log2) + (p & (ps - 1))) * dst_row + src0;
+      *reinterpret_cast<uint4*>(vp + dst) = vx.u;
+      *reinterpret_cast<uint4*>(vp + dst + D / 2) = vy.u;
+      if (a.rope != nullptr) turn<T>(x, y, cs, a.half);
+      *reinterpret_cast<uint4*>(kp + dst) = x.u;
+      *reinterpret_cast<uint4*>(kp + dst + D / 2) = y.u;
+      if (kBounds) {
+        if (!any) {
+          mx0.u = mn0.u = x.u;
+          mx1.u = mn1.u = y.u;
+          any = true;
+        } else {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int pp = p + u * stride;
-        if (pp >= end) continue;
-        const int64_t off = (int64_t)(r.t0 + pp - p0) * a.kv_stride + src0;
-        x[u].u = __ldg(reinterpret_cast<const uint4*>(k + off));
-        y[u].u = __ldg(reinterpret_cast<const uint4*>(k + off + D / 2));
-        vx[u].u = __ldg(reinterpret_cast<const uint4*>(v + off));
-        vy[u].u = __ldg(reinterpret_cast<const uint4*>(v + off + D / 2));
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int pp = p + u * stride;
-        if (pp >= end) continue;
-        const int64_t dst = (((int64_t)page << a.ps_log2) + (pp & (ps - 1))) * dst_row + src0;
-        *reinterpret_cast<uint4*>(vp + dst) = vx[u].u;
-        *reinterpret_cast<uint4*>(vp + dst + D / 2) = vy[u].u;
-        if (a.rope != nullptr) turn<T, D>(x[u], y[u], a.rope + (int64_t)pp * (D / 2), c, a.half);
-        *reinterpret_cast<uint4*>(kp + dst) = x[u].u;
-        *reinterpret_cast<uint4*>(kp + dst + D / 2) = y[u].u;
-        if (kBounds) {
-          if (!any) {
-            mx0.u = mn0.u = x[u].u;
-            mx1.u = mn1.u = y[u].u;
-            any = true;
-          } else {
-#pragma unroll
-            for (int i = 0; i < VL; ++i) {
-              mx0.e[i] = pick_max(mx0.e[i], x[u].e[i]);
-              mn0.e[i] = pick_min(mn0.e[i], x[u].e[i]);
-              mx1.e[i] = pick_max(mx1.e[i], y[u].e[i]);
-              mn1.e[i] = pick_min(mn1.e[i], y[u].e[i]);
-            }
+          for (int i = 0; i < VL; ++i) {
+            mx0.e[i] = pick_max(mx0.e[i], x.e[i]);
+            mn0.e[i] = pick_min(mn0.e[i], x.e[i]);
+            mx1.e[i] = pick_max(mx1.e[i], y.e[i]);
+            mn1.e[i] = pick_min(mn1.e[i], y.e[i]);
           }
         }
       }
