@@ -321,7 +321,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       for (int j = tile0; j < tile1; ++j, ++t) {
         int npage = -1;
         if (j + 1 < tile1) npage = look(it, j + 1);
-        else if (more) npage = look(nx, 0);
+        else if (more) npage = look(nx, nx.tile0);
         const int st = t % stages;
         uint64_t* full = kq ? &sm.k_full[st] : &sm.v_full[st];
         if (t >= stages)

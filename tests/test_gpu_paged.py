@@ -258,6 +258,8 @@ ATTEND = [
     (16, 1, 128, 16, [2000], [33], True),
     (16, 8, 64, 64, [150, 290, 160, 30, 133], [140, 150, 150, 0, 133], True),   # more items than blocks
     (12, 12, 128, 16, [400, 131], [260, 129], False),
+    (16, 8, 64, 64, [1500, 1400], [700, 700], False),       # and the rest of them cut in the middle of long rows
+    (24, 24, 128, 32, [900, 1000], [400, 500], True),
 ]
 
 
