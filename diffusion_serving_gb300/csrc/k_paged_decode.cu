@@ -214,7 +214,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       it = nx;
     }
-    if (wc->abort && lane == 0) {   // let every load issued here land before the block releases its shared memory
+    if (lane == 0) {   // every load issued here lands before the block releases its shared memory, consumers that gave up or not
       for (int i = max(0, t - S); i < t; ++i) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
     }
   } else if (warp == kWarps + 1) {

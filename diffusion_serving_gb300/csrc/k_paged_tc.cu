@@ -351,8 +351,9 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       ++n;
       it = nx;
     }
-    if (wc->abort && lane == 0) {
-      // every load this warp issued lands before the CTA's shared memory is released
+    if (lane == 0) {
+      // every load this warp issued lands before the CTA's shared memory is released, whether or not a warp gave up (one
+      // may yet do so after this warp is through)
       if (q_issued > 0) mbar_wait(&sm.q_full, (q_issued - 1) & 1, wc, false);
       for (int i = max(0, t - stages); i < t; ++i)
         mbar_wait(kq ? &sm.k_full[i % stages] : &sm.v_full[i % stages], (i / stages) & 1, wc, false);
@@ -389,7 +390,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       }
       ++n;
     }
-    if (wc->abort && lane == 0) {
+    if (lane == 0) {                                     // (lands before TMEM is freed, whichever warp gave up)
       mma_commit(&sm.drain[0]);
       mbar_wait(&sm.drain[0], 0, wc, false);
     }
@@ -455,7 +456,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       ++n;
       if (!ok) break;
     }
-    if (wc->abort && lane == 0) {
+    if (lane == 0) {                                     // (lands before TMEM is freed, whichever warp gave up)
       mma_commit(&sm.drain[1]);
       mbar_wait(&sm.drain[1], 0, wc, false);
     }
