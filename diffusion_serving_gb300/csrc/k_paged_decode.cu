@@ -155,6 +155,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int box_log2 = min(a.ps_log2, 6);                 // slots per box
     const int per_tile = kTile >> box_log2;                 // boxes (of one half and tensor) per tile
     const uint32_t box_bytes = 128u << box_log2;
+    const int shared_cols = a.phase == 0 && a.prefix_len != nullptr ? *a.prefix_len >> a.ps_log2 : 0;
     // lane i < per_tile: the table column of the tile's ith box and the page number there, not looked at before it is
     // used (a tile later); column -1: no box
     auto look = [&](const kvc_pg_item& w, int j, int* col, int* page) {
@@ -165,7 +166,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         int c = key >> a.ps_log2;
         if (a.sel != nullptr) c = __ldg(a.sel + ((int64_t)w.b * a.Hkv + w.vh / a.sub) * a.n_sel + c);
         *col = c;
-        if (c >= 0) *page = __ldg(a.table + (int64_t)w.b * a.max_pages + c);
+        if (c >= 0) *page = __ldg((c < shared_cols ? a.prefix_pages : a.table + (int64_t)w.b * a.max_pages) + c);
       }
     };
     int t = 0;

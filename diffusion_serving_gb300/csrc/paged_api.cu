@@ -64,11 +64,23 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
 // 500 slots of 8 rows 19.5 and 20.5, over 300 slots of 32 rows 42 and 31.
 bool simt_only(const kvc_paged* c, uint32_t flags) { return c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT); }
 
+bool few_rows(const kvc_pg_args& a, int slots) { return (int64_t)a.max_q * a.Gv <= (slots <= 2048 ? 32 : 16); }
+
 cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, uint32_t flags, cudaStream_t s) {
   if (simt_only(c, flags)) return kvc_pg_launch_simt(c, a, q, out, s);
   const int slots = (a.max_pages - (a.phase == 2 ? a.prefix_cap : 0)) << a.ps_log2;
-  if (a.phase != 1 && (int64_t)a.max_q * a.Gv <= (slots <= 2048 ? 32 : 16)) return kvc_pg_launch_decode(c, a, q, out, s);
+  if (a.phase != 1 && few_rows(a, slots)) return kvc_pg_launch_decode(c, a, q, out, s);
   return kvc_pg_launch_tc(c, a, q, out, s);
+}
+
+// A shared prefix of few rows is cheaper read once per row, from L2, in the streaming kernel alone (it takes the page
+// numbers below the prefix's end from the shared list) than once for all in three launches.  What counts is the bytes
+// that all rows' passes over it read: at 34 MB (8 rows, 1024 slots, 8 heads of 128) 13.5 us against 22.2, at 67 MB 18.4
+// against 23.2 (heads of 64: 23.5 against 23.5), at 134 MB 29.2 against 25.4, at 268 MB 50 and 26.
+bool one_pass(const kvc_pg_args& a, int head_dim) {
+  const int T = 16 / a.Gv;                             // tokens to an item
+  const int64_t passes = (int64_t)a.B * a.Hv * ((a.max_q + T - 1) / T);
+  return passes * ((int64_t)a.prefix_cap << a.ps_log2) * head_dim * 4 <= (int64_t)64 << 20;
 }
 
 kvc_pg_args attend_args(const kvc_paged* c, float* lse, int32_t n_tokens, const int32_t* d_cu, int32_t max_q,
@@ -238,6 +250,8 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   a.prefix_cap = prefix_pages;
   a.prefix_len = d_prefix_len;
   cudaStream_t s = as_stream(stream);
+  if (!simt_only(c, flags) && few_rows(a, a.max_pages << a.ps_log2) && one_pass(a, c->cfg.head_dim))
+    return launched(kvc_pg_launch_decode(c, a, q, out, s));
   a.phase = 1;
   cudaError_t e = run_attend(c, a, q, out, flags, s);
   if (e == cudaSuccess)

@@ -46,8 +46,9 @@ struct kvc_pg_layout {
 };
 kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& cfg);
 
-// What a launch is told.  `phase`: 0 attends a row's slots; 1 the shared prefix (one row of all
-// tokens, partials only); 2 the slots behind the prefix, joined with phase 1's partials.
+// What a launch is told.  `phase`: 0 attends a row's slots (with prefix_len, the first of them in the shared list's
+// pages: the streaming kernel alone); 1 the shared prefix (one row of all tokens, partials only); 2 the slots behind the
+// prefix, joined with phase 1's partials.
 struct kvc_pg_args {
   int B, H, Hkv, Hv, Gv, sub;
   int ps_log2, n_pages, max_pages;
@@ -122,7 +123,7 @@ __device__ __forceinline__ kvc_pg_raw pg_load(const kvc_pg_args& a, int b) {
   x.lo = a.cu == nullptr ? b * a.even : a.cu[b];
   x.hi = a.cu == nullptr ? x.lo + a.even : a.cu[b + 1];
   x.len = a.kv_len[b];
-  x.prefix = a.phase != 0 ? *a.prefix_len : 0;
+  x.prefix = a.prefix_len != nullptr ? *a.prefix_len : 0;
   return x;
 }
 // The checks, each with its error bit.
@@ -150,7 +151,7 @@ __device__ __forceinline__ kvc_pg_row pg_row(const kvc_pg_args& a, int b) {
   }
   const kvc_pg_raw x = pg_load(a, b);
   const bool tok = pg_tokens_ok(a, x), len = pg_len_ok(a, x.len);
-  if (!tok || !len || (a.phase == 2 && !pg_prefix_ok(a, x.prefix))) return none;
+  if (!tok || !len || (a.prefix_len != nullptr && !pg_prefix_ok(a, x.prefix))) return none;
   kvc_pg_row r{x.lo, x.hi - x.lo, x.len, a.phase == 2 ? min(x.prefix, x.len) : 0};
   if (a.sel != nullptr) r.len = min((x.len + (1 << a.ps_log2) - 1) >> a.ps_log2, a.n_sel) << a.ps_log2;
   return r;

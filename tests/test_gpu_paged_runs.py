@@ -239,16 +239,36 @@ def test_what_the_entry_points_refuse():
     assert c.get_error() == 0 and c2.get_error() == 0
 
 
-@pytest.mark.parametrize("what", ["decode", "decode over many blocks", "chunk", "chunk in waves", "shared"])
+def test_shared_prefix_in_a_pass_of_its_own_refuses_bad_lengths():
+    lens, P = [4100 + i for i in range(20)], 4096
+    c, g = big(lens, 8, 2, 128, BF16, 16, seed=14, max_tokens=20)
+    q = torch.randn(20, 8, 128, device="cuda", generator=g).to(BF16)
+    pages = c.block_table[0, :P // 16].clone()
+    c.block_table[:, :P // 16] = pages
+    want, lse = c.attend(q, lse=True)
+    for bad in (-16, 8, P + 16, -2 ** 31):
+        out = torch.full_like(q, 7.0)
+        c.attend_shared(q, pages, ints([bad]), out=out)
+        assert c.get_error() & paged.DEV_BAD_KVLEN
+        assert torch.all(out == 7.0)
+    got, lse2 = c.attend_shared(q, pages, ints([P]), lse=True)
+    assert c.get_error() == 0
+    same_sums(lse, lse2)
+    got, lse2 = c.attend_shared(q, pages, ints([0]), lse=True)   # the prefix may shrink to nothing on the device
+    assert c.get_error() == 0
+    same_sums(lse, lse2)
+
+
+@pytest.mark.parametrize("what", ["decode", "decode over many blocks", "chunk", "chunk in waves", "shared", "shared of many rows"])
 def test_wait_that_runs_out_returns_and_reports(what):
-    lens = [5000, 3000] if "many" in what else [700, 400]
-    heads, kv_heads = (24, 24) if "waves" in what else (8, 2)
+    lens = [5000, 3000] if "many blocks" in what else [700, 400] + [500] * (100 if "many rows" in what else 0)
+    heads, kv_heads = (24, 24) if "waves" in what else (32, 8) if "rows" in what else (8, 2)
     new = 300 if "chunk" in what else 1
-    c, g = big(lens, heads, kv_heads, 128, BF16, 16, seed=13, max_tokens=2)
-    q = torch.randn(2, new, heads, 128, device="cuda", generator=g).to(BF16)
+    c, g = big(lens, heads, kv_heads, 128, BF16, 16, seed=13, max_tokens=len(lens))
+    q = torch.randn(len(lens), new, heads, 128, device="cuda", generator=g).to(BF16)
     pages, plen = c.block_table[0, :20].clone(), ints([320])
-    c.block_table[1, :20] = pages
-    run = (lambda: c.attend_shared(q, pages, plen, lse=True)) if what == "shared" else \
+    c.block_table[:, :20] = pages
+    run = (lambda: c.attend_shared(q, pages, plen, lse=True)) if "shared" in what else \
         (lambda: c.attend(q, lse=True, flags=paged.CAUSAL))
     want = run()
     assert c.get_error() == 0
