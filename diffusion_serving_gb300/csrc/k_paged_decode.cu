@@ -21,6 +21,11 @@
 // At an item's end the warps' states meet in shared memory and go straight out, or, where the item
 // spans blocks, to the workspace (pg_finish).
 //
+// Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 170.5 us, 6.4 TB/s, 0.94 of
+// a plain copy; DRAM reads equal the algorithmic bytes, issue slots 22 % busy.  One row of 490 slots: 9.9 us, of which
+// 4 go by before the first tile lands (launch, lengths, page numbers, descriptors: a chain of loads).  Heads of 64 halve
+// a tile's bytes and not its fixed costs: 3.3 TB/s, from L2 as from HBM, bound by the consumers.
+//
 // R = 8 leaves half of M free, and P uses it: rows 8..15 carry what rounding P to 16 bits lost, so
 // O is as exact as from fp32 weights at no further MMA.  R = 16 uses all of M, with P rounded once.
 #include "paged_finish.h"

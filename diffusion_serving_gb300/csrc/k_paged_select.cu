@@ -7,7 +7,10 @@
 // k_paged_score_mma (16-bit stores) takes the second form: a product of [q+ q-] with a page's 2 D
 // bounds, by warp-level MMAs, heads in M and pages in N.  It is HBM-bound: each page's bounds are
 // read once, 1 / page_size of the bytes of its keys and values.  The order of the contraction is free,
-// so a lane takes 8 dims of a page in one 16-byte load, and the queries are laid out to match.
+// so a lane takes 8 dims of a page in one 16-byte load, and the queries are laid out to match.  16 rows of up to 2048
+// pages, 8 kv heads of 128 (83 MB): 33 us, 2.5 TB/s; 4.7 us for one row.  What holds it back is the loads in flight: a
+// warp waits for a set of 8 pages before it asks for the next.  A ring of bulk copies through shared memory took 9 us
+// off the one and added 3 to the other, and was left out.
 // k_paged_score does fp32 stores with FMAs, a warp per page.
 //
 // k_paged_rank, a block per (row, kv head), takes the n_select largest.  Rounding could swap pages
@@ -18,7 +21,7 @@
 // only be known to within a narrow interval: a histogram of 2048 equal steps between the least and
 // the largest score gives one that mostly holds a few pages.  Where it does not serve (scores all but
 // equal, or not finite), radix selection takes its place.  Bound by the latency of its eight or so
-// phases between barriers.
+// phases between barriers: 8 us for one row of 2048 pages, 10 for 16.
 #include "paged_internal.h"
 
 #include <cuda_bf16.h>

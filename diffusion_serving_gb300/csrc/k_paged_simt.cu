@@ -5,7 +5,9 @@
 //   s = scale q k^T, running max m and sum l per row, O = sum 2^(s - m) v,
 // K and V of a tile staged as fp32 in shared memory, 16 threads to a query row.  Work is shared out
 // among the blocks by tiles (paged_internal.h), so one long row keeps every SM busy.  Bound by
-// shared-memory reads: each FMA of the two products takes a quarter of a 16-byte read per operand.
+// shared-memory reads: each FMA of the two products takes a quarter of a 16-byte read per operand.  On a 16-bit store,
+// as a cross-check: 1.4 ms where the streaming kernel takes 0.17 (32 rows of up to 16384 slots), 28 ms where the
+// tensor-core kernel takes 0.285 (chunks over 16384 slots).
 #include "paged_finish.h"
 
 namespace {

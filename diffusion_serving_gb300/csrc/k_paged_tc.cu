@@ -6,8 +6,9 @@
 // and V tiles are read once for all of them.  Over a shared prefix the tokens of the whole batch
 // are stacked, which turns B memory-bound passes over the prefix into one product per tile.
 // Items and their 128-slot tiles are shared out evenly among the blocks (paged_internal.h); an item
-// that spans blocks leaves partial states, joined by k_paged_join (or, for a shared prefix, by the
-// launch that attends what follows it).
+// that spans blocks leaves partial states.  Where items are many, few blocks share one, and the last of them joins it
+// here; where they are few, an item has ten or twenty parts of 64 KB each, and k_paged_join spreads the joining over the
+// GPU (the crossing lies near a third of the blocks: 152 / 3 items); a shared prefix's parts go to k_paged_join_prefix.
 //
 // A block is one CTA per SM (256 threads).  Warps: 0 TMA producer of Q and K, 3 of V, 1 issues
 // S = Q K^T (and owns TMEM), 2 issues O += P V, 4-7 softmax, one query row per thread.  TMEM holds
@@ -19,6 +20,13 @@
 // K and V arrive page by page: one box per page, 64-dim half and tensor (64 dims x min(page, 64)
 // slots); boxes of a tile lie where one 128-slot box would put them (the 128-byte swizzle goes by
 // the address).
+//
+// Bound by the tensor pipe and the softmax warps that feed it.  Chunks of 700 and 1024 tokens over 9000 and 16384 slots,
+// causal, 32 heads over 8 kv heads of 128, bf16, pages of 64: 285 us, 1.27 PFLOP/s of visible pairs (0.65 of a library
+// matrix product's burst, 0.74 of its sustained rate); the rest is masked halves of diagonal tiles and the last wave's cut
+// items.  2 x 1024 tokens over 2 x 16384 slots, not causal: 391 us, 1.36 PFLOP/s, against 377 us of the linear store's
+// kernel.  Pages of 16 make it 520 us: 16 copies a tile from one warp, some 80 cycles each, are more than a tile's products
+// take.  (Lanes issue in turn; one lane issuing all takes twice that a copy.)
 //
 // Every mbarrier wait is bounded (0.5 s); on expiry the block records KVC_DEV_TIMEOUT, lets its TMA
 // loads and MMAs land, frees TMEM and returns.

@@ -77,7 +77,7 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
 /* Append new tokens: row b's n_b tokens go to slots kv_len_b - n_b .. kv_len_b - 1.
  *  k, v: n_tokens rows of [Hkv, D], rows kv_stride elements apart (>= Hkv * D; a multiple of
  *    16 bytes), so that they may be slices of a joint projection.
- *  d_rope: NULL (keys are stored as they come), or fp32 (cos, sin) [rope_positions][D/2][2]:
+ *  d_rope: NULL (keys are stored as they come), or fp32 (cos, sin) [rope_positions][D/2][2], 16-byte aligned:
  *    the key at position p is turned by the angles of row p first, and the store holds the
  *    exact rotation rounded once to nearest-even (finite inputs), as kvc_write_rope's does.
  *    Without KVC_ROPE_HALF pair j is (x[2j], x[2j+1]), with it (x[j], x[j + D/2]).
@@ -104,6 +104,8 @@ int kvc_paged_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stri
  *    KVC_DEV_BAD_CUSEQ.
  *  flags: KVC_CAUSAL (token i of a row's n sees the slots up to its own, kv_len - n + i),
  *    KVC_KERNEL_SIMT (the fp32-FMA kernel for any type, a cross-check).
+ *  Slots behind a row's length may hold anything.  The values of the slots that it has must be finite where a token must
+ *  not see them either (causal): a weight of 0 times infinity is NaN.
  *  A token that sees no slot (kv_len 0, or causal with more tokens than slots) gets out 0 and
  *  lse -inf.  A row with a bad offset (KVC_DEV_BAD_CUSEQ) or length (KVC_DEV_BAD_KVLEN) is left
  *  unwritten; the slots of a bad page (KVC_DEV_BAD_PAGE) are left out of the softmax.
@@ -114,8 +116,8 @@ int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32
                      int32_t max_q, uint32_t flags, void* stream);
 
 /* kvc_paged_attend for rows whose first slots are the same pages (a common prompt): slots
- * [0, P) are read from d_prefix_pages, once for all rows' tokens together, and slots [P, kv_len) from
- * each row's own table at their usual columns (the columns below P / page_size are not read).
+ * [0, P) are read from d_prefix_pages, once for all rows' tokens together (short prefixes of few rows, up to 64 MB of
+ * reads in all, once per row), and slots [P, kv_len) from each row's own table at their usual columns (the columns below P / page_size are not read).
  *  d_prefix_pages: int32 [prefix_pages] page numbers; d_prefix_len: int32 [1] on the device, P, a
  *    multiple of page_size, 0 <= P <= prefix_pages * page_size (else KVC_DEV_BAD_KVLEN, nothing written).
  *  A row with kv_len < P sees the first kv_len slots of the prefix.
@@ -129,8 +131,9 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
  *  A page's score is the largest that any key within its bounds could have with any query
  *  of the head's group: max over g of sum_d max(q_gd hi_d, q_gd lo_d).  The first `first` pages and
  *  the newest `recent` ones are always taken (first + recent <= n_select), then those with the
- *  largest scores, of equal scores the lower column.  Which pages are taken follows from scores in
- *  (at least) 48 bits, so no rounding decides it.  A row with at most n_select pages attends all of them.
+ *  largest scores, of equal scores the lower column.  Scores that fp32 cannot tell apart are taken in twice its precision
+ *  (off by some 2^-44 of the sum of their terms' magnitudes), so no fp32 rounding decides.
+ *  A row with at most n_select pages attends all of them.
  *  q, out: [batch, H, D]; d_lse: NULL or fp32 [batch, H].
  *  d_selected: int32 [batch, Hkv, n_select], written: the columns taken, ascending, then -1.
  *  A row with kv_len 0 gets out 0, lse -inf and -1 throughout; one with a bad length is left unwritten.
