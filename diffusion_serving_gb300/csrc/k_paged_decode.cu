@@ -6,26 +6,27 @@
 // block per SM by tiles of 64 slots (paged_internal.h): a block streams one stretch of the line of
 // all rows' tiles, whatever the rows' lengths, through a ring of shared-memory stages that runs on
 // across the borders between rows.  Warps:
-//   0-7  consumers, two sets of four that take tiles in turn; a warp takes 16 slots of its tile:
-//        S = Q K^T and O += P V as warp-level m16n8k16 MMAs (query rows in M, slots or dims in N),
-//        online softmax per row in between, P going from accumulators to operands in registers.
-//        One set's tile takes about as long as HBM needs for one, so two keep ahead of it.
-//   8    producer: looks up page numbers a tile ahead and issues one TMA box per page and tensor:
+//   0-7  consumers: a warp takes 16 slots of a tile: S = Q K^T and O += P V as warp-level m16n8k16
+//        MMAs (query rows in M, slots or dims in N), online softmax per row in between, P going from
+//        accumulators to operands in registers.  Tiles are 32 KB: of 64 slots of 128 dims, which two sets
+//        of four warps take in turn (one set's tile takes about as long as HBM needs for one, so two keep
+//        ahead of it), or of 128 slots of 64 dims, which all eight share.
+//   8,10 producers of K and of V: look up page numbers a tile ahead and issue one TMA box per page:
 //        [page_size slots][D / 64][64 dims], 128-byte swizzle, from a 5-d view of the pool.  (A box
 //        per 64-dim half would lie free of bank conflicts, where this one's 256-byte rows meet in
-//        pairs; but a copy costs the issuing warp some 80 cycles, and 16 of them a tile, for pages
-//        of 16 slots, are more than HBM leaves time for.)
+//        pairs; but a copy costs the issuing warp some 80 cycles, and for pages of 16 slots even one box a
+//        page and tensor from a single warp is too many: heads of 64 4.4 TB/s against 5.5 with two.)
 //   9    helper: works out the next items for the consumers (their rows' places, limits, extents) and
 //        brings their queries and their shared prefixes' states to shared memory, so that none of it
 //        falls between two items.
 // At an item's end the warps' states meet in shared memory and go straight out, or, where the item
 // spans blocks, to the workspace (pg_finish).
 //
-// Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 170.5 us, 6.4 TB/s, 0.94 of
-// a plain copy; DRAM reads equal the algorithmic bytes, issue slots 22 % busy.  One row of 490 slots: 9.9 us, of which
-// 4 go by before the first tile lands (launch, lengths, page numbers, descriptors: a chain of loads).  Heads of 64 halve
-// a tile's bytes and not its fixed costs: 3.3 TB/s, from L2 as from HBM, bound by the consumers.
-//
+// Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 171 us, 6.4 TB/s, 0.94 of
+// a plain copy; DRAM reads equal the algorithmic bytes, issue slots 22 % busy.  One row of 490 slots: 9.5 us, of which
+// 4 go by before the first tile lands (launch, lengths, page numbers, descriptors: a chain of loads).  Heads of 64, the
+// same rows: 98 us, 5.6 TB/s (from L2 8.7): a slot's 128 bytes are short pieces to DRAM.
+
 // R = 8 leaves half of M free, and P uses it: rows 8..15 carry what rounding P to 16 bits lost, so
 // O is as exact as from fp32 weights at no further MMA.  R = 16 uses all of M, with P rounded once.
 #include "paged_finish.h"
@@ -36,15 +37,16 @@ namespace {
 using namespace pg;
 
 constexpr int kWarps = 8;                         // consumer warps
-constexpr int kThreads = (kWarps + 2) * 32;       // + producer, helper
-constexpr int kTile = 64;                         // slots per tile: 16 for each of 4 warps
-constexpr uint32_t kHalf = kTile * 128u;          // bytes of 64 dims of a tile
+constexpr int kThreads = (kWarps + 3) * 32;       // + producer of K, helper, producer of V
+template <int D> constexpr int kSets = D == 128 ? 2 : 1;                  // of consumers, which take tiles in turn
+template <int D> constexpr int kTile = kWarps / kSets<D> * 16;            // slots per tile: 16 for each warp of a set
+template <int D> constexpr uint32_t kHalf = kTile<D> * 128u;              // bytes of 64 dims of a tile
 constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
-constexpr int kMinTiles = 8;                      // fewest tiles for a block
-constexpr int kItemCost = 4;                      // an item's beginning and end, in tiles
+template <int D> constexpr int kMinTiles = 512 / kTile<D>;                // fewest tiles for a block
+template <int D> constexpr int kItemCost = 256 / kTile<D>;                // an item's beginning and end, in tiles
 
-template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 5 : 3) : (R == 8 ? 10 : 8);
-template <int D> constexpr uint32_t kStageBytes = 2u * (D / 64) * kHalf;   // K and V
+template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 5 : 3) : (R == 8 ? 5 : 4);
+template <int D> constexpr uint32_t kStageBytes = 2u * (D / 64) * kHalf<D>;   // K and V (32 KB)
 
 template <typename T, int D, int R>
 struct Smem {
@@ -59,7 +61,7 @@ struct Smem {
   kvc_pg_end end[2];
   int tiles[2];                                   // this block's tiles of the item; -1: there is none
   int keys[2];                                    // slots at or behind this hold nothing of the row
-  int pos[kStages<D, R>][kTile];                  // slot positions of a stage, INT_MAX: left out
+  int pos[kStages<D, R>][kTile<D>];                 // slot positions of a stage, INT_MAX: left out
   uint64_t full[kStages<D, R>], empty[kStages<D, R>];
   uint64_t q_full[2], pre_full[2], item_empty[2];
   WaitCtl wc;
@@ -126,7 +128,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
-    mbar_init(&sm.full[threadIdx.x], 32);
+    mbar_init(&sm.full[threadIdx.x], 64);            // both producers' lanes
     mbar_init(&sm.empty[threadIdx.x], kWarps);
   }
   if (threadIdx.x >= 32 && threadIdx.x < 34) {
@@ -146,8 +148,8 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   __syncthreads();
   kvc_pdl_wait();
   kvc_pdl_release();
-  kvc_pg_sched<R, kTile> sch;
-  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, kItemCost,
+  kvc_pg_sched<R, kTile<D>> sch;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles<D>, kItemCost<D>,
            gridDim.x);
   kvc_pg_item it;
   bool more = false;
@@ -155,10 +157,11 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   const int ps = 1 << a.ps_log2;
   const bool prefix = a.phase == 2 && sch.lo > 0;
 
-  if (warp == kWarps) {
-    // ---------------- producer: TMA boxes of K and V into the stage ring ----------------
+  if (warp == kWarps || warp == kWarps + 2) {
+    // ---------------- producers: TMA boxes of K (warp 8) and V (warp 10) into the stage ring ----------------
+    const bool is_k = warp == kWarps;
     const int box_log2 = min(a.ps_log2, 6);                 // slots per box
-    const int per_tile = kTile >> box_log2;                 // boxes (of one half and tensor) per tile
+    const int per_tile = kTile<D> >> box_log2;               // boxes (of one half and tensor) per tile
     const uint32_t box_bytes = 128u << box_log2;
     const int shared_cols = a.phase == 0 && a.prefix_len != nullptr ? *a.prefix_len >> a.ps_log2 : 0;
     // lane i < per_tile: the table column of the tile's ith box and the page number there, not looked at before it is
@@ -166,7 +169,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     auto look = [&](const kvc_pg_item& w, int j, int* col, int* page) {
       *col = -1;
       *page = 0;
-      const int key = w.r.lo + j * kTile + (lane << box_log2);
+      const int key = w.r.lo + j * kTile<D> + (lane << box_log2);
       if (lane < per_tile && key < w.r.len) {
         int c = key >> a.ps_log2;
         if (a.sel != nullptr) c = __ldg(a.sel + ((int64_t)w.b * a.Hkv + w.vh / a.sub) * a.n_sel + c);
@@ -193,25 +196,24 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         if (col < 0) {
           page = -1;
         } else if (page < 0 || page >= a.n_pages) {
-          atomicOr(a.err, KVC_DEV_BAD_PAGE);
+          if (is_k) atomicOr(a.err, KVC_DEV_BAD_PAGE);
           page = -1;
         }
         const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane == 0) mbar_expect_tx(&sm.full[st], __popc(good) * 2 * HB * box_bytes);
+        if (lane == 0) mbar_expect_tx(&sm.full[st], __popc(good) * HB * box_bytes);
         __syncwarp();
-        const int first = it.r.lo + j * kTile;
-        const int i = lane & (per_tile - 1);                 // box of the tile
-        const int g = __shfl_sync(0xffffffffu, page, i);
-        if (lane < 2 * per_tile && g >= 0)                   // K's boxes, then V's (at most 8 in all)
-          tma_load_5d(lane < per_tile ? &tm_k : &tm_v, &sm.full[st],
-                      sm.stage[st] + (lane < per_tile ? 0 : HB * kHalf) + i * HB * box_bytes, 0, 0, kvh,
-                      (first + (i << box_log2)) & (ps - 1), g);
-        // positions of the tile's slots
+        const int first = it.r.lo + j * kTile<D>;
+        if (page >= 0)                                       // (lanes of the tile's boxes alone; at most 8)
+          tma_load_5d(is_k ? &tm_k : &tm_v, &sm.full[st],
+                      sm.stage[st] + (is_k ? 0 : HB * kHalf<D>) + lane * HB * box_bytes, 0, 0, kvh,
+                      (first + (lane << box_log2)) & (ps - 1), page);
+        if (is_k) {                                          // positions of the tile's slots
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int s = lane + 32 * x;
-          const int c = __shfl_sync(0xffffffffu, col, s >> box_log2), gg = __shfl_sync(0xffffffffu, page, s >> box_log2);
-          sm.pos[st][s] = gg >= 0 && first + s < it.r.len ? (c << a.ps_log2) + ((first + s) & (ps - 1)) : 0x7fffffff;
+          for (int x = 0; x < kTile<D> / 32; ++x) {
+            const int s = lane + 32 * x;
+            const int c = __shfl_sync(0xffffffffu, col, s >> box_log2), gg = __shfl_sync(0xffffffffu, page, s >> box_log2);
+            sm.pos[st][s] = gg >= 0 && first + s < it.r.len ? (c << a.ps_log2) + ((first + s) & (ps - 1)) : 0x7fffffff;
+          }
         }
         __syncwarp();
         if (lane != 0) mbar_arrive(&sm.full[st]);
@@ -290,8 +292,8 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   } else {
     // ---------------- consumers ----------------
     const int hq = lane >> 2, quad = lane & 3;
-    const int set = warp >> 2;                              // takes every other tile
-    const int r0 = (warp & 3) * 16;                         // this warp's slots of its tiles
+    const int set = kSets<D> == 1 ? 0 : warp >> 2;          // takes every other tile
+    const int r0 = (kSets<D> == 1 ? warp : warp & 3) * 16;                       // this warp's slots of its tiles
     // a tile holds line HB s + h of 128 bytes for slot s and 64-dim half h; its 16-byte chunk c lies at c ^ (line & 7)
     const uint32_t row0 = r0 * HB * 128;
     auto bar = [] { named_bar<1>(kWarps * 32); };
@@ -334,11 +336,11 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // phase of its barrier, since two phases on it could not tell one from the other.
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (u / S) & 1, wc));
         if (!ok) break;
-        if ((u & 1) != set) {
+        if (kSets<D> > 1 && (u & 1) != set) {
           if (lane == 0) mbar_arrive(&sm.empty[st]);
           continue;
         }
-        const uint32_t kbase = smem_u32(sm.stage[st]) + row0, vbase = kbase + HB * kHalf;
+        const uint32_t kbase = smem_u32(sm.stage[st]) + row0, vbase = kbase + HB * kHalf<D>;
         const int2 pa = *reinterpret_cast<const int2*>(&sm.pos[st][r0 + 2 * quad]);
         const int2 pb = *reinterpret_cast<const int2*>(&sm.pos[st][r0 + 8 + 2 * quad]);
         const int pos[4] = {pa.x, pa.y, pb.x, pb.y};
@@ -350,7 +352,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int e = lane; e < 16 * HB * 8; e += 32) {
               const int s = e / (HB * 8), h = (e / 8) % HB, c = e % 8;
               if (sm.pos[st][r0 + s] >= end)
-                *reinterpret_cast<uint4*>(sm.stage[st] + HB * kHalf + row0 + (HB * s + h) * 128 + c * 16) =
+                *reinterpret_cast<uint4*>(sm.stage[st] + HB * kHalf<D> + row0 + (HB * s + h) * 128 + c * 16) =
                     make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async();                            // before TMA reuses the stage

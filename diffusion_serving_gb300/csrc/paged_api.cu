@@ -75,12 +75,13 @@ cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, 
 
 // A shared prefix of few rows is cheaper read once per row, from L2, in the streaming kernel alone (it takes the page
 // numbers below the prefix's end from the shared list) than once for all in three launches.  What counts is the bytes
-// that all rows' passes over it read: at 34 MB (8 rows, 1024 slots, 8 heads of 128) 13.5 us against 22.2, at 67 MB 18.4
-// against 23.2 (heads of 64: 23.5 against 23.5), at 134 MB 29.2 against 25.4, at 268 MB 50 and 26.
+// that all rows' passes over it read: at 34 MB (8 rows, 1024 slots, 8 heads of 128) 12.6 us against 22.2, at 67 MB 17.1
+// against 24.0, at 134 MB 26.1 against 25.3 (pages of 64: 23.0 against 25.5; heads of 64: 26.2 against 25.1), at 268 MB
+// 43 and 26.
 bool one_pass(const kvc_pg_args& a, int head_dim) {
   const int T = 16 / a.Gv;                             // tokens to an item
   const int64_t passes = (int64_t)a.B * a.Hv * ((a.max_q + T - 1) / T);
-  return passes * ((int64_t)a.prefix_cap << a.ps_log2) * head_dim * 4 <= (int64_t)64 << 20;
+  return passes * ((int64_t)a.prefix_cap << a.ps_log2) * head_dim * 4 <= (int64_t)96 << 20;
 }
 
 kvc_pg_args attend_args(const kvc_paged* c, float* lse, int32_t n_tokens, const int32_t* d_cu, int32_t max_q,

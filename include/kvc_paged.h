@@ -116,7 +116,7 @@ int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32
                      int32_t max_q, uint32_t flags, void* stream);
 
 /* kvc_paged_attend for rows whose first slots are the same pages (a common prompt): slots
- * [0, P) are read from d_prefix_pages, once for all rows' tokens together (short prefixes of few rows, up to 64 MB of
+ * [0, P) are read from d_prefix_pages, once for all rows' tokens together (short prefixes of few rows, up to 96 MB of
  * reads in all, once per row), and slots [P, kv_len) from each row's own table at their usual columns (the columns below P / page_size are not read).
  *  d_prefix_pages: int32 [prefix_pages] page numbers; d_prefix_len: int32 [1] on the device, P, a
  *    multiple of page_size, 0 <= P <= prefix_pages * page_size (else KVC_DEV_BAD_KVLEN, nothing written).

@@ -385,10 +385,10 @@ SHARED = [
     (12, 12, 128, 32, 2048, [2049 + i for i in range(40)], [1] * 40, False),
     (34, 2, 64, 16, 160, [161, 170], [1, 3], True),             # groups of 17 heads
     # more than rows read one by one: the prefix in a pass of its own
-    (8, 2, 128, 16, 4096, [4097 + 9 * i for i in range(16)] + [4096], [1, 2] * 8 + [1], True),
-    (34, 2, 64, 16, 4096, [4100, 4111], [1, 3], True),
+    (8, 2, 128, 16, 4096, [4097 + 9 * i for i in range(25)] + [4096], [1, 2] * 13, True),
+    (34, 2, 64, 16, 6400, [6404, 6415], [1, 3], True),
     (40, 8, 64, 32, 3200, [3205, 100, 0, 3201, 3300, 3217, 3199, 3230, 3264, 3250, 3260], [5, 1, 1, 4, 2, 5, 1, 1, 0, 1, 3], True),
-    (12, 12, 128, 128, 1408, [1409 + 31 * i for i in range(9)], [1] * 9, False),
+    (12, 12, 128, 128, 1408, [1409 + 31 * i for i in range(12)], [1] * 12, False),
 ]
 
 

@@ -240,9 +240,9 @@ def test_what_the_entry_points_refuse():
 
 
 def test_shared_prefix_in_a_pass_of_its_own_refuses_bad_lengths():
-    lens, P = [4100 + i for i in range(20)], 4096
-    c, g = big(lens, 8, 2, 128, BF16, 16, seed=14, max_tokens=20)
-    q = torch.randn(20, 8, 128, device="cuda", generator=g).to(BF16)
+    lens, P = [4100 + i for i in range(26)], 4096
+    c, g = big(lens, 8, 2, 128, BF16, 16, seed=14, max_tokens=26)
+    q = torch.randn(26, 8, 128, device="cuda", generator=g).to(BF16)
     pages = c.block_table[0, :P // 16].clone()
     c.block_table[:, :P // 16] = pages
     want, lse = c.attend(q, lse=True)
