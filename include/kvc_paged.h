@@ -98,8 +98,8 @@ int kvc_paged_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stri
                      int32_t rope_positions, uint32_t flags, void* stream);
 
 /* out = softmax(scale q k^T) v of every token over its row's slots [0, kv_len).
- *  q, out: [n_tokens, H, D], dense; d_lse: NULL or fp32 [n_tokens, H], the natural
- *    log-sum-exp of the scaled scores.
+ *  q, out: [n_tokens, H, D], dense, 16-byte aligned, apart from one another; d_lse: NULL or fp32 [n_tokens, H],
+ *    the natural log-sum-exp of the scaled scores.
  *  max_q: most tokens a row has (with d_cu; ignored without it); a row with more is
  *    KVC_DEV_BAD_CUSEQ.
  *  flags: KVC_CAUSAL (token i of a row's n sees the slots up to its own, kv_len - n + i),

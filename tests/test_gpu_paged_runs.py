@@ -211,6 +211,90 @@ def test_buffers_aligned_to_16_bytes_only(dtype, new):
     assert c.get_error() == 0
 
 
+def against_plain(c, q, out, lse, cu, causal, rows, sel=None):
+    """Rows `rows` of a call against the plain form."""
+    k, v, table, lens = to64(c.k_pages), to64(c.v_pages), c.block_table.cpu().numpy(), c.kv_len.tolist()
+    for b in rows:
+        n, t0, t1 = lens[b], cu[b], cu[b + 1]
+        kk, vv = ref.gather(k, table[b], 0, n), ref.gather(v, table[b], 0, n)
+        see = ref.visible_mask(n, 0, t1 - t0, n, causal)
+        want = ref.attend_rows(to64(q[t0:t1]), kk, vv, see, c.head_dim ** -0.5, c.dtype)
+        ref.check(out[t0:t1], lse[t0:t1], want, f"row {b}")
+
+
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(BF16, 4, 2, 128), (F16, 6, 1, 64), (F32, 2, 2, 64)])
+def test_the_largest_batch(dtype, heads, kv_heads, dim):
+    """1024 rows: single tokens, ragged chunks, a shared prefix both ways, chosen pages, appends."""
+    B, page = 1024, 16
+    lens = [1 + (37 * b) % 90 for b in range(B)]
+    c, g = big(lens, heads, kv_heads, dim, dtype, page, seed=21, bounds=True, max_tokens=4 * B)
+    some = list(range(0, B, 61)) + [B - 1]
+    q = torch.randn(B, heads, dim, device="cuda", generator=g).to(dtype)
+    one = list(range(B + 1))
+    out, lse = c.attend(q, lse=True)
+    against_plain(c, q, out, lse, one, False, some)
+    new = [b % 5 if b % 7 else 70 for b in range(B)]
+    new = [min(n, m) for n, m in zip(new, lens)]
+    cu = wl.seqlens_to_cu(new)
+    qc = torch.randn(cu[-1], heads, dim, device="cuda", generator=g).to(dtype)
+    for most in (max(new), 1 << 30):
+        out, lse = c.attend(qc, cu_q=ints(cu), max_q=most, lse=True, flags=paged.CAUSAL)
+        against_plain(c, qc, out, lse, cu, True, [b for b in some if new[b]])
+    pages = torch.arange(2, dtype=torch.int32, device="cuda")
+    c.block_table[:, :2] = pages                                 # (rows of one page see the first slots of a full one)
+    for P in (32, 0):
+        out, lse = c.attend_shared(q, pages, ints([P]), lse=True)
+        against_plain(c, q, out, lse, one, False, some)
+        q4 = torch.randn(4 * B, heads, dim, device="cuda", generator=g).to(dtype)
+        out, lse = c.attend_shared(q4, pages, ints([P]), lse=True, flags=paged.CAUSAL)
+        against_plain(c, q4, out, lse, list(range(0, 4 * B + 1, 4)), True, some)
+    out, lse, sel = c.attend_sparse(q, 3, lse=True)
+    full = c.kv_len.cpu().numpy() <= 3 * page
+    assert all(sel[b, :, :-(-lens[b] // page)].tolist() == [list(range(-(-lens[b] // page)))] * kv_heads for b in some if full[b])
+    against_plain(c, q, out, lse, one, False, [b for b in some if full[b]])
+    assert c.get_error() == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(71, 1), (96, 1), (128, 2)])
+def test_wide_groups(heads, kv_heads):
+    """Groups of 71 (a prime), 96 and 64 heads."""
+    lens, new = [900, 130, 47], [3, 40, 1]
+    c, g = big(lens, heads, kv_heads, 64, BF16, 32, seed=22, bounds=True)
+    q = torch.randn(3, heads, 64, device="cuda", generator=g).to(BF16)
+    out, lse = c.attend(q, lse=True)
+    against_plain(c, q, out, lse, [0, 1, 2, 3], False, range(3))
+    cu = wl.seqlens_to_cu(new)
+    qc = torch.randn(cu[-1], heads, 64, device="cuda", generator=g).to(BF16)
+    out, lse = c.attend(qc, cu_q=ints(cu), max_q=40, lse=True, flags=paged.CAUSAL)
+    against_plain(c, qc, out, lse, cu, True, range(3))
+    # more places than any row has pages: everything is attended
+    out, lse, sel = c.attend_sparse(q, c.cfg.max_pages + 9, lse=True)
+    against_plain(c, q, out, lse, [0, 1, 2, 3], False, range(3))
+    assert sel[0, 0].tolist() == list(range(29)) + [-1] * (sel.shape[2] - 29)
+    # one place
+    _, sel = c.attend_sparse(q, 1, first=0, recent=0)
+    bd, table = to64(c.bounds), c.block_table.cpu().numpy()
+    for b, n in enumerate(lens):
+        assert sel[b].tolist() == ref.select(to64(q[b]), bd, table[b], -(-n // 32), 1, 0, 0)
+    assert c.get_error() == 0
+
+
+def test_as_many_pages_as_selection_takes():
+    """32768 columns, and one more refused."""
+    page, n = 16, 32768
+    c, g = big([n * page - 5, 1], 8, 1, 64, BF16, page, seed=23, bounds=True)
+    q = torch.randn(2, 8, 64, device="cuda", generator=g).to(BF16)
+    out, sel = c.attend_sparse(q, 600)
+    bd, table = to64(c.bounds), c.block_table.cpu().numpy()
+    assert sel[0].tolist() == ref.select(to64(q[0]), bd, table[0], n, 600, 1, 1)
+    assert sel[1, 0, 0] == 0 and torch.all(sel[1, 0, 1:] == -1)
+    assert c.get_error() == 0
+    d = paged.PagedKVCache(1, 8, 1, 64, BF16, page_size=page, n_pages=4, max_pages=n + 1, bounds=True)
+    with pytest.raises(kvc.KvcError) as e:
+        d.attend_sparse(q[:1], 4)
+    assert e.value.code == kvc.ERR_RANGE
+
+
 def test_what_the_entry_points_refuse():
     c, g = big([100, 60], 8, 2, 64, BF16, 16, seed=12, max_tokens=4)
     q = torch.randn(2, 8, 64, device="cuda", generator=g).to(BF16)
