@@ -7,10 +7,10 @@
 // k_paged_score_mma (16-bit stores) takes the second form: a product of [q+ q-] with a page's 2 D
 // bounds, by warp-level MMAs, heads in M and pages in N.  It is HBM-bound: each page's bounds are
 // read once, 1 / page_size of the bytes of its keys and values.  The order of the contraction is free,
-// so a lane takes 8 dims of a page in one 16-byte load, and the queries are laid out to match.  16 rows of up to 2048
-// pages, 8 kv heads of 128 (83 MB): 33 us, 2.5 TB/s; 4.7 us for one row.  What holds it back is the loads in flight: a
-// warp waits for a set of 8 pages before it asks for the next.  A ring of bulk copies through shared memory took 9 us
-// off the one and added 3 to the other, and was left out.
+// so a lane takes 8 dims of a page in one 16-byte load, and the queries are laid out to match.  A
+// block's life is short (8 sets of 8 pages a warp), so its chain of loads counts: the row's length, page numbers and
+// queries are asked for together, the first bounds before the queries are worked on.  16 rows of up to 2048 pages,
+// 8 kv heads of 128 (83 MB): 22 us, 3.8 TB/s (33 with the loads one after another); 4.5 us for one row.
 // k_paged_score does fp32 stores with FMAs, a warp per page.
 //
 // k_paged_rank, a block per (row, kv head), takes the n_select largest.  Rounding could swap pages
@@ -157,23 +157,49 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = lane >> 2, c = lane & 3;
   const int kvh = blockIdx.y, b = blockIdx.z;
-  const int np = row_pages(a, b);
-  if (np <= a.n_sel) return;                // every page is taken: nothing to rank
   const int first = (blockIdx.x * kMmaWarps + warp) * 8, step = gridDim.x * kMmaWarps * 8;
-  if (first >= np) return;
   const T* type = nullptr;
   float* out = reinterpret_cast<float*>(a.scores + ((int64_t)b * a.Hkv + kvh) * a.max_pages);
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
+  // the row's length, its first pages' numbers (used where the length says so) and the first queries, loaded together
+  int page = first + n < a.max_pages ? __ldg(table + first + n) : -1;
+  uint4 qx[V];
+  auto load_q = [&](int g0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      qx[v] = make_uint4(0, 0, 0, 0);
+      if (g0 + n < a.G) qx[v] = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)b * a.H + kvh * a.G + g0 + n) * D + 32 * v + 8 * c));
+    }
+  };
+  load_q(0);
+  const int np = row_pages(a, b);
+  if (np <= a.n_sel) return;                // every page is taken: nothing to rank
+  if (first >= np) return;
   float terms = 0.f;
   for (int g0 = 0; g0 < a.G; g0 += 8) {     // 8 heads a pass
+    if (g0 > 0) {
+      load_q(g0);
+      page = first + n < np ? __ldg(table + first + n) : -1;
+    } else if (first + n >= np) {
+      page = -1;
+    }
+    bool ok;
+    uint4 x[2][V];
+    auto load_x = [&] {                     // (a bad page is reported by the attention that meets it)
+      ok = page >= 0 && page < a.n_pages;
+      const uint4* bd = reinterpret_cast<const uint4*>(bounds + ((int64_t)(ok ? page : 0) * a.Hkv + kvh) * 2 * D);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[h][v] = ok ? __ldg(bd + h * (D / 8) + 4 * v + c) : make_uint4(0, 0, 0, 0);
+    };
+    load_x();
     uint32_t qa[2][V][2][2];                // [hi, lo][vector][k16 step][k half]
     float l1 = 0.f;
     const bool real = g0 + n < a.G;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (real) x = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)b * a.H + kvh * a.G + g0 + n) * D + 32 * v + 8 * c));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t w[4] = {qx[v].x, qx[v].y, qx[v].z, qx[v].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         qa[0][v][i >> 1][i & 1] = part_of(w[i], false);
@@ -187,15 +213,8 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, o));
     uint32_t top2 = 0u, low2 = 0u;          // largest upper and least lower bound (or 0), 16-bit pairs
-    int page = first + n < np ? __ldg(table + first + n) : -1;
     for (int j = first; j < np; j += step) {
-      const bool ok = page >= 0 && page < a.n_pages;       // (a bad page is reported by the attention that meets it)
-      const uint4* bd = reinterpret_cast<const uint4*>(bounds + ((int64_t)(ok ? page : 0) * a.Hkv + kvh) * 2 * D);
-      uint4 x[2][V];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[h][v] = ok ? __ldg(bd + h * (D / 8) + 4 * v + c) : make_uint4(0, 0, 0, 0);
+      if (j > first) load_x();
       page = j + step + n < np ? __ldg(table + j + step + n) : -1;
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -565,9 +584,11 @@ cudaError_t launch(const kvc_paged* c, const void* q, const SelArgs& a, cudaStre
     return cudaFuncSetAttribute(k_paged_rank<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KVC_PG_MAX_SCORED * 4);
   cudaError_t e;
   if constexpr (sizeof(T) == 2) {
-    // 8 pages a warp; a warp takes up to four such sets where that still leaves 16 warps an SM
+    // 8 pages a warp; a warp takes four or eight such sets where that still leaves 16 warps an SM (16 rows of up to 2048
+    // pages, 8 heads: 65.3 us with eight, 66.0 with four, 64.6 with sixteen, all three launches)
     const int64_t sets = ((int64_t)a.max_pages + 7) / 8 * a.Hkv * a.B;
-    const int per_warp = sets >= (int64_t)KVC_PG_GRID * 16 * 4 ? 4 : 1;
+    const int64_t warps = (int64_t)KVC_PG_GRID * 16;
+    const int per_warp = sets >= warps * 8 ? 8 : sets >= warps * 4 ? 4 : 1;
     const int blocks = (a.max_pages + 8 * kMmaWarps * per_warp - 1) / (8 * kMmaWarps * per_warp);
     e = kvc_launch_pdl(k_paged_score_mma<T, D>, dim3(blocks, a.Hkv, a.B), dim3(kMmaWarps * 32), 0, s, (const T*)q,
                        (const T*)c->bounds, a);

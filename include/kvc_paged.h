@@ -88,7 +88,8 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
  *    written; one that is continued widens.  (After kv_len was taken back, a continued page's
  *    bounds still cover the tokens given up: wider than need be, never too narrow.)
  *  Two rows must not append to one page in one call.
- *  Device errors: KVC_DEV_BAD_CUSEQ (that row is skipped), KVC_DEV_BAD_KVLEN (kv_len outside
+ *  Device errors: KVC_DEV_BAD_CUSEQ (that row is skipped; where offsets go back, tokens of the rows before may be left
+ *  out too), KVC_DEV_BAD_KVLEN (kv_len outside
  *  [0, max_pages * page_size], or less than the row's new tokens: skipped), KVC_DEV_BAD_PAGE
  *  (those slots are not written), KVC_DEV_BAD_POS (a position outside the rope table: that token is
  *  not written, its query neither).
