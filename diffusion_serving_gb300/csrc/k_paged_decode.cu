@@ -149,7 +149,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<R, kTile<D>> sch;
-  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles<D>, kItemCost<D>,
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles<D>, kMinTiles<D>, kItemCost<D>,
            gridDim.x);
   kvc_pg_item it;
   bool more = false;

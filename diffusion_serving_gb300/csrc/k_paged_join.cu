@@ -21,7 +21,7 @@ k_paged_join(T* __restrict__ out, kvc_pg_args a) {
   constexpr int R = KVC_PG_TC_ROWS;
   extern __shared__ __align__(16) uint8_t smem[];
   kvc_pg_sched<R, KVC_PG_TC_TILE> sch;
-  sch.init(a, smem, KVC_PG_TC_MIN, KVC_PG_TC_COST, KVC_PG_GRID);
+  sch.init(a, smem, KVC_PG_TC_MIN, KVC_PG_TC_WHOLE, KVC_PG_TC_COST, KVC_PG_GRID);
   // the item at the end of the block's stretch
   const long long end = (long long)(blockIdx.x + 1) * sch.per;
   const bool any = end < sch.total;
@@ -71,7 +71,7 @@ k_paged_join_prefix(int TS, int cost, int grid, kvc_pg_args a) {
   // (as kvc_pg_sched has it)
   int per, stride = tiles + cost, lead = cost;
   if (items <= grid) {
-    pg_even(tiles, items, grid, 1, &per, &stride);
+    pg_even(tiles, items, grid, 1, 1, &per, &stride);
     lead = 0;
   } else {
     per = (items * stride + grid - 1) / grid;

@@ -582,8 +582,10 @@ template <typename T, int D>
 cudaError_t launch(const kvc_paged* c, const void* q, const SelArgs& a, cudaStream_t s, bool prepare) {
   if (prepare)
     return cudaFuncSetAttribute(k_paged_rank<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KVC_PG_MAX_SCORED * 4);
-  cudaError_t e;
-  if constexpr (sizeof(T) == 2) {
+  cudaError_t e = cudaSuccess;
+  if (a.max_pages <= a.n_sel) {
+    // no row has more pages than are taken: nothing to rank
+  } else if constexpr (sizeof(T) == 2) {
     // 8 pages a warp; a warp takes four or eight such sets where that still leaves 16 warps an SM (16 rows of up to 2048
     // pages, 8 heads: 65.3 us with eight, 66.0 with four, 64.6 with sixteen, all three launches)
     const int64_t sets = ((int64_t)a.max_pages + 7) / 8 * a.Hkv * a.B;

@@ -56,7 +56,7 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
   kvc_pdl_wait();
   kvc_pdl_release();
   kvc_pg_sched<kR, kTS> sch;
-  sch.init(a, smem + ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15), 1, 1, gridDim.x);
+  sch.init(a, smem + ((sizeof(SimtSmem<D>) + 15) & ~(size_t)15), 1, 1, 1, gridDim.x);
   const int tid = threadIdx.x;
   const int r = tid / kLanes, ln = tid % kLanes;
   kvc_pg_item it;

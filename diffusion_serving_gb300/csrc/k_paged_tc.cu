@@ -287,7 +287,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   kvc_pdl_release();
   kvc_pg_sched<kBM, kBN, true> sch;
   sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), a.phase == 1 ? 1 : KVC_PG_TC_MIN,
-           KVC_PG_TC_COST, gridDim.x);
+           a.phase == 1 ? 1 : KVC_PG_TC_WHOLE, KVC_PG_TC_COST, gridDim.x);
   const int ps = 1 << a.ps_log2;
   kvc_pg_item it;
   bool more = sch.first(a, blockIdx.x, it);

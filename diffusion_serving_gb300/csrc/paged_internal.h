@@ -99,9 +99,12 @@ cudaError_t kvc_pg_prepare_tc(const kvc_paged* c);
 // query rows per item and slots per tile of the tensor-core kernel
 #define KVC_PG_TC_ROWS 128
 #define KVC_PG_TC_TILE 128
-// fewest tiles for a block (a shared prefix is always cut evenly), and what an item's beginning and end cost, in tiles
+// fewest tiles for a block (a shared prefix is always cut evenly), what an item's beginning and end cost, in tiles, and
+// the items that are not worth cutting: joining takes longer than eight tiles (434 tokens over 600 slots, 32 heads:
+// 15.7 us whole, 33.8 cut by two tiles; 40 over 2000 slots, sixteen tiles: 19 cut, 22 to 24 in two halves or whole)
 #define KVC_PG_TC_MIN 2
 #define KVC_PG_TC_COST 3
+#define KVC_PG_TC_WHOLE 8
 // partial rows per item and slots per tile of the FMA kernel
 #define KVC_PG_SIMT_ROWS 16
 #define KVC_PG_SIMT_TILE 64
@@ -196,16 +199,16 @@ __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int 
 //
 // Where there are no more items than blocks, and they are alike or short, each item gets a whole
 // number of blocks instead: it is padded to `stride` places, a multiple of `per` (no empty ones), so
-// that no block works on two and no item is cut without need.
+// that no block works on two and no item is cut without need (at most `whole` tiles: not at all).
 //
 // Where there are many more items than blocks (kWaves, the tensor-core kernel), stretches would spread
 // the blocks over all rows and groups at once, whose K and V together may not fit in L2; then block c
 // first takes the whole items c, c + grid, ... of as many waves as surely end before the mean
 // load (blocks that run together are on neighbouring items and share their K and V), and the rest of
 // the line is cut into stretches that bring every block to that load.
-__host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int* per, int* stride) {
-  *per = *stride = min_tiles;
-  if (tiles <= min_tiles) return;
+__host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int whole, int* per, int* stride) {
+  *per = *stride = whole;
+  if (tiles <= whole) return;
   const int chunks = grid / items;
   const int even = (tiles + chunks - 1) / chunks;
   *per = even > min_tiles ? even : min_tiles;
@@ -252,7 +255,7 @@ struct kvc_pg_sched {
 
   // Every thread of the block calls it (it holds barriers).  A line too long for 32 bits is refused
   // with KVC_DEV_OVERFLOW (nothing is attended).
-  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles, int item_cost, int grid) {
+  __device__ __forceinline__ void init(const kvc_pg_args& a, void* smem, int min_tiles, int whole, int item_cost, int grid) {
     n_rows = a.phase == 1 ? 1 : a.B;
     T = a.Gv == 1 ? R : R / a.Gv;
     causal = a.causal && a.phase != 1 && a.sel == nullptr;
@@ -321,8 +324,8 @@ struct kvc_pg_sched {
       per = 1;
       return;
     }
-    if (items > 0 && items <= grid && (most <= 2 * min_tiles || most * items * 4 <= 5 * tiles)) {
-      pg_even(most, (int)items, grid, min_tiles, &per, &stride);
+    if (items > 0 && items <= grid && (most <= (whole > 2 * min_tiles ? whole : 2 * min_tiles) || most * items * 4 <= 5 * tiles)) {
+      pg_even(most, (int)items, grid, min_tiles, whole, &per, &stride);
       cost = 0;
       total = (int)items * stride;
     } else {
