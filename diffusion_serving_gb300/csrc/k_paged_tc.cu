@@ -713,6 +713,9 @@ cudaError_t launch(const kvc_paged* c, kvc_pg_args a, const void* q, void* out, 
   const cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
                                  c->tm_k, c->tm_v, (T*)out, a);
   if (e != cudaSuccess || a.phase == 1 || a.join_here) return e;
+  // rows that hold no more than an uncut item's slots, and at most an item a block: nothing to join (the launch would take 5 us)
+  const int64_t items = (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok + a.B);
+  if (((int64_t)a.max_pages << a.ps_log2) <= KVC_PG_TC_WHOLE * kBN && items <= KVC_PG_GRID) return e;
   return kvc_pg_launch_join(c, a, out, s);
 }
 
