@@ -49,7 +49,7 @@ k_paged_join(T* __restrict__ out, kvc_pg_args a) {
       pg_join1(M, L, x, ml, y);
     }
     pg_join(c1 - c0 + 1, M, L, x,
-            [&](int i, float2* ml, float4* y) { pg_load_part<R, D>(a.part, 2 * (c0 + i) + (i == 0 ? 1 : 0), r, d, ml, y); });
+            [&](int i, float2* ml, float4* y) { pg_load_part<R, D, true>(a.part, 2 * (c0 + i) + (i == 0 ? 1 : 0), r, d, ml, y); });
     if (lane < D / 4) pg_emit<T, D>(a, out, at, d, M, L, x);
   }
 }

@@ -581,6 +581,8 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       bool last = !it.end.left;                          // this block writes the item's output
       if (it.end.left) {
         float* dst = (a.phase == 1 ? a.pre : a.part) + (int64_t)it.end.slot * (kBM * (D + 2));
+        float* mine = dst + r * (a.phase == 1 ? D : 8);
+        const int step = a.phase == 1 ? 8 : kBM * 8;         // between the row's vectors of 8 dims
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t orow[32];
@@ -590,7 +592,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           reg_fence32(orow);
           if (real) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st_v8(dst + r * D + q4 * 32 + i * 8, orow + 8 * i);
+            for (int i = 0; i < 4; ++i) st_v8(mine + (q4 * 4 + i) * step, orow + 8 * i);
           }
         }
         if (real) *reinterpret_cast<float2*>(dst + kBM * D + 2 * r) = make_float2(m_ref, l);
@@ -643,17 +645,17 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           float x[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0.f;
-          auto add = [&](float w, const float* src) {
+          auto add = [&](float w, const float* src, int step) {    // step: between a row's vectors of 8 dims
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(src + q4 * 32 + i));
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (q4 * 4 + (i >> 3)) * step + (i & 7)));
               x[i] = fmaf(w, y.x, x[i]);
               x[i + 1] = fmaf(w, y.y, x[i + 1]);
               x[i + 2] = fmaf(w, y.z, x[i + 2]);
               x[i + 3] = fmaf(w, y.w, x[i + 3]);
             }
           };
-          if (pw != 0.f) add(pw, a.pre_o + at * D);
+          if (pw != 0.f) add(pw, a.pre_o + at * D, 8);
           for (int cc = c0; cc <= c1; ++cc) {
             const float2 ml = real ? ml_of(cc) : make_float2(0.f, 0.f);
             const float w = ml.y != 0.f ? pg_weight(ml.x, M) * inv : 0.f;
@@ -661,7 +663,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = fmaf(w, __uint_as_float(orow[i]), x[i]);
             } else if (w != 0.f) {
-              add(w, part(cc) + r * D);
+              add(w, part(cc) + r * 8, kBM * 8);
             }
           }
           uint32_t pk[16];

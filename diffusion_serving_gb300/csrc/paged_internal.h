@@ -105,6 +105,9 @@ cudaError_t kvc_pg_prepare_tc(const kvc_paged* c);
 #define KVC_PG_TC_MIN 2
 #define KVC_PG_TC_COST 3
 #define KVC_PG_TC_WHOLE 8
+// the idle tiles per block that taking every item whole may leave before some are cut and joined instead (3 x 434 tokens
+// over 600 slots, 336 items of up to five tiles: 50 us cut, 35 whole; over 2000 slots 78 and 58)
+#define KVC_PG_TC_JOIN 24
 // partial rows per item and slots per tile of the FMA kernel
 #define KVC_PG_SIMT_ROWS 16
 #define KVC_PG_SIMT_TILE 64
@@ -205,7 +208,8 @@ __device__ __forceinline__ int pg_prefix_limit(const kvc_pg_args& a, int t, int 
 // the blocks over all rows and groups at once, whose K and V together may not fit in L2; then block c
 // first takes the whole items c, c + grid, ... of as many waves as surely end before the mean
 // load (blocks that run together are on neighbouring items and share their K and V), and the rest of
-// the line is cut into stretches that bring every block to that load.
+// the line is cut into stretches that bring every block to that load; where all of them taken whole
+// leave less idle than cutting costs, nothing is cut.
 __host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_tiles, int whole, int* per, int* stride) {
   *per = *stride = whole;
   if (tiles <= whole) return;
@@ -331,7 +335,10 @@ struct kvc_pg_sched {
     } else {
       total = (int)(tiles + items * cost);
       per = max(min_tiles, (total + grid - 1) / grid);
-      if (kWaves && a.join_here) waves = (total / grid) / (most + cost);
+      if (kWaves && a.join_here) {
+        const long long rounds = (items + grid - 1) / grid;
+        waves = rounds * (most + cost) <= total / grid + KVC_PG_TC_JOIN ? (int)rounds : (total / grid) / (most + cost);
+      }
     }
     __syncthreads();                       // (every warp has read the rows' own tiles)
     if (kWaves && waves > 0 && warp == 1) {
@@ -393,7 +400,7 @@ struct kvc_pg_sched {
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
           }
-          if (c < grid) cut[c + 1] = (int)min((long long)(total - from), carry + x);
+          if (c < grid) cut[c + 1] = (int)max(0ll, min((long long)(total - from), carry + x));
           carry += __shfl_sync(0xffffffffu, x, 31);
         }
         if (lane == 0) cut[0] = 0;
@@ -516,7 +523,7 @@ struct kvc_pg_sched {
     if (kWaves && waves > 0) {
       wave = 0;
       it = item(a, c);
-      return true;
+      return it.tiles > 0;
     }
     if ((long long)c * per >= total) return false;
     const int p = c * per;
@@ -535,7 +542,7 @@ struct kvc_pg_sched {
     if (kWaves && waves > 0 && wave < waves) {
       if (++wave < waves) {
         it = item(a, blockIdx.x + wave * gridDim.x);
-        return true;
+        return it.tiles > 0;
       }
       const int p = from + cut[blockIdx.x], e = from + cut[blockIdx.x + 1];
       return p < e && stretch(a, p, e, it);
