@@ -55,12 +55,16 @@ def same_sums(lse, other):
     torch.testing.assert_close(lse, other, rtol=0, atol=2.0 ** -12)
 
 
-def test_long_chunks_of_whole_and_cut_items():
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim,page,lens,new", [
+    (BF16, 32, 8, 128, 64, [4500, 7000], [700, 1024]),
+    (F16, 40, 40, 64, 16, [5200, 3000], [333, 300]),
+    (BF16, 64, 64, 128, 128, [300, 9000, 40], [290, 129, 40]),       # one long row among short ones
+])
+def test_long_chunks_of_whole_and_cut_items(dtype, heads, kv_heads, dim, page, lens, new):
     """More items than blocks over long rows: whole ones first, the rest cut anywhere."""
-    lens, new = [4500, 7000], [700, 1024]
-    c, g = big(lens, 32, 8, 128, BF16, 64, seed=5)
+    c, g = big(lens, heads, kv_heads, dim, dtype, page, seed=5)
     cu = wl.seqlens_to_cu(new)
-    q = torch.randn(cu[-1], 32, 128, device="cuda", generator=g).to(BF16)
+    q = torch.randn(cu[-1], heads, dim, device="cuda", generator=g).to(dtype)
     args = dict(cu_q=ints(cu), max_q=max(new), lse=True)
     out, lse = c.attend(q, flags=paged.CAUSAL, **args)
     simt, lse_simt = c.attend(q, flags=paged.CAUSAL | SIMT, **args)
@@ -72,7 +76,30 @@ def test_long_chunks_of_whole_and_cut_items():
         for i in range(b, new[b], 97):
             t = cu[b] + i
             see = ref.visible_mask(n, 0, new[b], n, True)[i:i + 1]
-            ref.check(out[t:t + 1], lse[t:t + 1], ref.attend_rows(to64(q[t:t + 1]), kk, vv, see, 128 ** -0.5, BF16), f"token {t}")
+            ref.check(out[t:t + 1], lse[t:t + 1], ref.attend_rows(to64(q[t:t + 1]), kk, vv, see, dim ** -0.5, dtype), f"token {t}")
+
+
+@pytest.mark.parametrize("dtype,heads,kv_heads,dim", [(F16, 24, 24, 64), (BF16, 40, 8, 128)])
+def test_long_chunks_behind_a_shared_prefix(dtype, heads, kv_heads, dim):
+    """Items cut and joined next to the prefix's state."""
+    lens, new, P = [8000, 700, 256], [300, 200, 33], 256
+    c, g = big(lens, heads, kv_heads, dim, dtype, 32, seed=15, max_tokens=540)
+    pages = c.block_table[0, :P // 32].clone()
+    c.block_table[:, :P // 32] = pages
+    cu = wl.seqlens_to_cu(new)
+    q = torch.randn(cu[-1], heads, dim, device="cuda", generator=g).to(dtype)
+    args = dict(cu_q=ints(cu), max_q=max(new), lse=True)
+    out, lse = c.attend_shared(q, pages, ints([P]), flags=paged.CAUSAL, **args)
+    _, lse_simt = c.attend(q, flags=paged.CAUSAL | SIMT, **args)
+    assert c.get_error() == 0
+    same_sums(lse, lse_simt)
+    k, v, table = to64(c.k_pages), to64(c.v_pages), c.block_table.cpu().numpy()
+    for b, n in enumerate(lens):
+        kk, vv = ref.gather(k, table[b], 0, n), ref.gather(v, table[b], 0, n)
+        for i in range(b, new[b], 41):
+            t = cu[b] + i
+            see = ref.visible_mask(n, 0, new[b], n, True)[i:i + 1]
+            ref.check(out[t:t + 1], lse[t:t + 1], ref.attend_rows(to64(q[t:t + 1]), kk, vv, see, dim ** -0.5, dtype), f"token {t}")
 
 
 @pytest.mark.parametrize("new", [1, 4])
