@@ -22,7 +22,7 @@
 // the address).
 //
 // Bound by the tensor pipe and the softmax warps that feed it.  Chunks of 700 and 1024 tokens over 9000 and 16384 slots,
-// causal, 32 heads over 8 kv heads of 128, bf16, pages of 64: 285 us, 1.27 PFLOP/s of visible pairs (0.65 of a library
+// causal, 32 heads over 8 kv heads of 128, bf16, pages of 64: 288 us, 1.26 PFLOP/s of visible pairs (0.65 of a library
 // matrix product's burst, 0.74 of its sustained rate); the rest is masked halves of diagonal tiles and the last wave's cut
 // items.  2 x 1024 tokens over 2 x 16384 slots, not causal: 391 us, 1.36 PFLOP/s, against 377 us of the linear store's
 // kernel.  Pages of 16 make it 520 us: 16 copies a tile from one warp, some 80 cycles each, are more than a tile's products

@@ -59,16 +59,18 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
 // Kernel by type and shape: fp32 stores (and KVC_KERNEL_SIMT) run the FMA kernel; 16-bit ones with few
 // query rows per group the streaming kernel, with more (and for a shared prefix, where the batch's rows
 // are stacked) the tensor-core kernel.  "Few" is 16 rows, one pass over a row's keys, or 32, two passes,
-// where rows can hold no more than 2048 slots (behind the prefix): 20 rows over 500 slots take 11.8 us
-// in two passes and 15.1 in the tensor-core kernel, over 8000 slots of 8 rows 90 and 59; 48 rows over
-// 500 slots of 8 rows 19.5 and 20.5, over 300 slots of 32 rows 42 and 31.
+// where all rows' and groups' slots (behind the prefix) are at most 128 K: 20 rows a group, 8 groups of 128 dims, take
+// 18.5 us in two passes and 23.1 in the tensor-core kernel for a batch of 1 over 8000 slots, 25.6 and 27.6 for 8 over 2000,
+// 26.4 and 34.1 for 32 over 300; but 85 and 64 for 8 over 8000, 96 and 67 for 32 over 2000.
 bool simt_only(const kvc_paged* c, uint32_t flags) { return c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT); }
 
-bool few_rows(const kvc_pg_args& a, int slots) { return (int64_t)a.max_q * a.Gv <= (slots <= 2048 ? 32 : 16); }
+bool few_rows(const kvc_pg_args& a, int64_t slots) {
+  return (int64_t)a.max_q * a.Gv <= (a.B * a.Hv * slots <= 128 * 1024 ? 32 : 16);
+}
 
 cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, uint32_t flags, cudaStream_t s) {
   if (simt_only(c, flags)) return kvc_pg_launch_simt(c, a, q, out, s);
-  const int slots = (a.max_pages - (a.phase == 2 ? a.prefix_cap : 0)) << a.ps_log2;
+  const int64_t slots = (int64_t)(a.max_pages - (a.phase == 2 ? a.prefix_cap : 0)) << a.ps_log2;
   if (a.phase != 1 && few_rows(a, slots)) return kvc_pg_launch_decode(c, a, q, out, s);
   return kvc_pg_launch_tc(c, a, q, out, s);
 }
@@ -251,7 +253,7 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
   a.prefix_cap = prefix_pages;
   a.prefix_len = d_prefix_len;
   cudaStream_t s = as_stream(stream);
-  if (!simt_only(c, flags) && few_rows(a, a.max_pages << a.ps_log2) && one_pass(a, c->cfg.head_dim))
+  if (!simt_only(c, flags) && few_rows(a, (int64_t)a.max_pages << a.ps_log2) && one_pass(a, c->cfg.head_dim))
     return launched(kvc_pg_launch_decode(c, a, q, out, s));
   a.phase = 1;
   cudaError_t e = run_attend(c, a, q, out, flags, s);
