@@ -382,13 +382,14 @@ struct kvc_pg_sched {
       cut = ibase + n_rows + 1;
       // what each block's whole items leave of the mean load (a place more, so that it is never nothing)
       const int mean = total / grid + 2;
+      const bool all = (long long)waves * grid >= items;         // nothing is left to cut
       for (int c = threadIdx.x; c < grid; c += blockDim.x) {
-        int load = 0;
-        for (int w = 0; w < waves; ++w) load += item(a, c + w * grid).tiles + cost;
+        int load = all ? mean : 0;
+        if (!all)
+          for (int w = 0; w < waves; ++w) load += item(a, c + w * grid).tiles + cost;
         cut[c + 1] = mean - load;
       }
-      const kvc_pg_item next_item = item(a, waves * grid, true);
-      from = next_item.tiles > 0 ? next_item.start - cost : total;
+      from = all ? total : item(a, waves * grid, true).start - cost;
       __syncthreads();
       if (warp == 0) {
         long long carry = 0;
@@ -400,7 +401,7 @@ struct kvc_pg_sched {
             const long long y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
           }
-          if (c < grid) cut[c + 1] = (int)max(0ll, min((long long)(total - from), carry + x));
+          if (c < grid) cut[c + 1] = (int)min((long long)(total - from), carry + x);
           carry += __shfl_sync(0xffffffffu, x, 31);
         }
         if (lane == 0) cut[0] = 0;
