@@ -192,18 +192,22 @@ class PagedKVCache:
                          f"{self.head_dim}] {self.dtype} on {self.device}, got {list(shape)} {t.dtype} on {t.device}")
 
     def _rows(self, what, t, heads):
-        """(token rows, elements from one to the next) of ``t``, whose rows are dense and evenly apart."""
+        """(token rows, elements from one to the next) of ``t``, whose rows are dense and evenly apart.  (The stride of a
+        dimension of size 1 means nothing.)"""
         n = self._tokens(what, t, heads)
         s = t.stride()
-        if len(s) == 3:
-            row, head, one = s
-            even = True
+        even = True
+        if n == 1:
+            row = heads * self.head_dim
+        elif len(s) == 3:
+            row = s[0]
         else:
-            batch, row, head, one = s
-            even = batch == t.shape[1] * row or t.shape[0] == 1
-        if one != 1 or not even or (head != self.head_dim and heads > 1):
+            b, per_row = t.shape[:2]
+            row = s[1] if per_row > 1 else s[0]
+            even = b == 1 or per_row == 1 or s[0] == per_row * row
+        if s[-1] != 1 or not even or (heads > 1 and s[-2] != self.head_dim):
             raise ValueError(f"kvc: {what}: a token's heads must be dense and its tokens evenly apart, got strides {list(s)}")
-        return n, row if n > 1 else max(row, heads * self.head_dim)
+        return n, row
 
     def _cu(self, cu):
         if cu is None:
