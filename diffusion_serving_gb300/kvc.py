@@ -115,6 +115,21 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream`` to write and the current stream to use afterwards.  torch's allocator hands
+    memory out by stream: what the current stream has freed may have work pending there, so the memory is ``stream``'s, and
+    it is not handed out again before what the current stream has been given by then is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    h, current = _stream(stream), torch.cuda.current_stream(device)
+    if h == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(h, device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _check(rc: int, what: str):
     if rc != OK:
         raise KvcError(rc, what)

@@ -123,7 +123,12 @@ class PagedKVCache:
     max_pages], ``kv_len`` int32 [batch] and ``bounds`` [n_pages, kv_heads, 2, head_dim] (True: allot
     one; needed by ``attend_sparse``) may be given, so that layers, or handles on different streams,
     share them.  Token rows of a call are packed ([total, heads, head_dim] with ``cu`` int32 [batch + 1]) or
-    even ([batch, n, heads, head_dim], or [batch * n, ...])."""
+    even ([batch, n, heads, head_dim], or [batch * n, ...]).
+
+    ``stream`` is where a call runs (None: the current stream).  The caller orders streams: what a call reads is ready
+    there, and results are waited for before they are read on another.  Results that a call allots itself are safe to
+    use on that stream and on the one that was current; the cache's own buffers are kept from reuse until the
+    calls made so far are done, whichever streams they ran on.  Buffers passed in are the caller's to keep."""
 
     def __init__(self, batch, heads, kv_heads, head_dim, dtype, *, page_size, n_pages, max_pages, max_tokens=0,
                  bounds=None, softmax_scale=0.0, k_pages=None, v_pages=None, block_table=None, kv_len=None,
@@ -142,10 +147,14 @@ class PagedKVCache:
         self.device, self._index = device, device.index
         pool = (n_pages, page_size, kv_heads, head_dim)
 
+        self._own, self._streams = [], {_current_stream(self._index)}    # buffers allotted here, streams they may be used on
+
         def own(what, t, shape, dt, fill=None):
             if t is not None:
                 return _dense(what, t, shape, dt, device)
-            return torch.empty(shape, dtype=dt, device=device) if fill is None else torch.full(shape, fill, dtype=dt, device=device)
+            t = torch.empty(shape, dtype=dt, device=device) if fill is None else torch.full(shape, fill, dtype=dt, device=device)
+            self._own.append(t)
+            return t
 
         self.k_pages = own("k_pages", k_pages, pool, self.dtype)
         self.v_pages = own("v_pages", v_pages, pool, self.dtype)
@@ -154,19 +163,29 @@ class PagedKVCache:
         self.bounds = None
         if bounds is not None and bounds is not False:
             self.bounds = own("bounds", None if bounds is True else bounds, (n_pages, kv_heads, 2, head_dim), self.dtype, 0)
-        self.workspace = torch.empty(wb, dtype=torch.uint8, device=device)
+        self.workspace = own("workspace", None, (wb,), torch.uint8)
+        h, current = self._stream(stream), torch.cuda.current_stream(device)
+        other = None if h == current.cuda_stream else torch.cuda.ExternalStream(h, device=device)
+        if other is not None:                              # (what was allotted and filled above)
+            other.wait_stream(current)
         with torch.cuda.device(device):
             self.handle = kvc_paged_create(self.cfg, self.k_pages, self.v_pages, self.bounds, self.block_table,
-                                           self.kv_len, self.workspace, stream)
+                                           self.kv_len, self.workspace, h)
+        if other is not None:                              # (the workspace's zeros)
+            current.wait_stream(other)
 
     # -- arguments ----------------------------------------------------------------------
     # (A decode step's kernels take some ten microseconds, and what these checks take comes on top of each
     # call: they look at each property once, and build messages only when one is wrong.)
     def _stream(self, stream):
         """The stream's handle; without one, the current stream of the cache's device."""
-        if stream is None:
-            return _current_stream(self._index)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        h = _current_stream(self._index) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+        if h not in self._streams:
+            s = torch.cuda.ExternalStream(h, device=self.device)
+            for t in self._own:
+                t.record_stream(s)
+            self._streams.add(h)
+        return h
 
     def _call(self, what, fn, *args):
         rc = fn(self.handle, *args)
@@ -216,19 +235,19 @@ class PagedKVCache:
             raise ValueError(f"kvc: row offsets must be a dense int32 [{self.batch + 1}] on {self.device}")
         return cu.data_ptr()
 
-    def _q(self, q, out, lse):
+    def _q(self, q, out, lse, stream):
         n = self._tokens("q", q, self.heads)
         if not q.is_contiguous():
             raise ValueError("kvc: q must be dense")
         shape = q.shape
         if out is None:
-            out = torch.empty_like(q)
+            out = kvc._empty(shape, q.dtype, q.device, stream)
         elif out.dtype is not self.dtype or out.shape != shape or out.get_device() != self._index or not out.is_contiguous():
             raise ValueError(f"kvc: out must match q ({list(shape)} {q.dtype} on {q.device}, dense)")
         if lse is None:
             return n, out, None, None
         if lse is True:
-            lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+            lse = kvc._empty(shape[:-1], torch.float32, q.device, stream)
         else:
             rows = lse.shape
             if lse.dtype is not torch.float32 or len(rows) != len(shape) - 1 or rows[0] != shape[0] or \
@@ -259,7 +278,7 @@ class PagedKVCache:
             if nq != n:
                 raise ValueError(f"kvc: q has {nq} tokens, k {n}")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = kvc._empty(q.shape, q.dtype, q.device, stream)
             elif q_out.dtype is not self.dtype or q_out.shape != q.shape or q_out.get_device() != self._index or \
                     not q_out.is_contiguous():
                 raise ValueError("kvc: q_out must be dense and match q")
@@ -274,7 +293,7 @@ class PagedKVCache:
     def attend(self, q, *, cu_q=None, max_q=None, out=None, lse=None, flags=0, stream=None):
         """Attention of every token over its row's slots.  ``max_q``: most tokens of a row (with ``cu_q``;
         None: all of them).  ``lse``: a buffer, or True for a new one; then (out, lse) is returned."""
-        n, out, lse, lse_ptr = self._q(q, out, lse)
+        n, out, lse, lse_ptr = self._q(q, out, lse, stream)
         self._call("kvc_paged_attend", _lib.kvc_paged_attend, q.data_ptr(), out.data_ptr(),
                    lse_ptr, n, self._cu(cu_q), n if max_q is None else max_q, flags,
                    self._stream(stream))
@@ -284,7 +303,7 @@ class PagedKVCache:
                       stream=None):
         """``attend`` for rows whose first ``prefix_len`` (int32 [1], on the device) slots are those of
         ``prefix_pages`` (int32): they are read once for all rows."""
-        n, out, lse, lse_ptr = self._q(q, out, lse)
+        n, out, lse, lse_ptr = self._q(q, out, lse, stream)
         for what, t in (("prefix_pages", prefix_pages), ("prefix_len", prefix_len)):
             if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous():
                 raise ValueError(f"kvc: {what} must be a dense int32 tensor on {self.device}")
@@ -299,12 +318,12 @@ class PagedKVCache:
         """Attention of one token per row over ``n_select`` pages per kv head: the ``first`` and the newest
         ``recent`` ones, and those whose bounds promise the largest scores.  Returns (out, lse, selected), or
         (out, selected) without ``lse``; selected int32 [batch, kv_heads, n_select], -1 behind the last."""
-        n, out, lse, lse_ptr = self._q(q, out, lse)
+        n, out, lse, lse_ptr = self._q(q, out, lse, stream)
         if n != self.batch:
             raise ValueError(f"kvc: attend_sparse takes one token per row ({self.batch}), got {n}")
         shape = (self.batch, self.kv_heads, n_select)
         if selected is None:
-            selected = torch.empty(shape, dtype=torch.int32, device=self.device)
+            selected = kvc._empty(shape, torch.int32, self.device, stream)
         elif selected.dtype is not torch.int32 or selected.shape != shape or selected.get_device() != self._index or \
                 not selected.is_contiguous():
             raise ValueError(f"kvc: selected must be a dense int32 {list(shape)}")
