@@ -369,7 +369,7 @@ class KVCache:
         if k.shape[1] != 1 or q.shape[1] != 1:
             raise ValueError("kvc: append_attend takes one new token and one query per row")
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty(q.shape, q.dtype, q.device, stream)
         self._check_q(q, out)
         kvc_append_attend_decode(self.handle, k, v, q, out, stream)
         return out
@@ -390,7 +390,7 @@ class KVCache:
 
     def attend(self, q, out=None, flags=0, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty(q.shape, q.dtype, q.device, stream)
         self._check_q(q, out)
         kvc_attend(self.handle, q, out, q.shape[1], flags, stream)
         return out
@@ -398,9 +398,9 @@ class KVCache:
     def attend_lse(self, q, out=None, flags=0, stream=None):
         """(out, lse) with lse [B, n_q, H] fp32."""
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty(q.shape, q.dtype, q.device, stream)
         self._check_q(q, out)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = _empty(q.shape[:3], torch.float32, q.device, stream)
         kvc_attend_lse(self.handle, q, out, lse, q.shape[1], flags, stream)
         return out, lse
 

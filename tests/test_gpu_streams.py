@@ -12,7 +12,7 @@ from tests.test_gpu_paged import BF16, F32, bits, ints, make, randn
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
-    from diffusion_serving_gb300 import paged
+    from diffusion_serving_gb300 import kvc, paged
 
 SLEEP = 100_000_000                                      # clocks
 
@@ -109,3 +109,32 @@ def test_a_cache_made_on_a_stream_that_is_not_the_current_one():
     torch.cuda.synchronize()
     assert torch.equal(bits(first), bits(want)) and torch.equal(bits(second), bits(want))
     assert d.get_error() == 0
+
+
+@pytest.mark.parametrize("dtype,n_q", [(BF16, 1), (BF16, 200), (F32, 1)])
+def test_linear_cache_outputs_are_not_memory_that_the_current_stream_still_writes(dtype, n_q):
+    c = kvc.KVCache(2, 8, 2, 128, dtype, "linear", capacity=600)
+    g = torch.Generator().manual_seed(39)
+    k = randn(g, 2, 500, 2, 128, dtype=dtype).cuda()
+    c.append(k, k)
+    q = randn(g, 2, n_q, 8, 128, dtype=dtype).cuda()
+    s = torch.cuda.Stream()
+    calls = [lambda st: [c.attend(q, stream=st)], lambda st: c.attend_lse(q, stream=st)]
+    if n_q == 1 and dtype != F32:
+        new = randn(g, 2, 1, 2, 128, dtype=dtype).cuda()
+
+        def step(st):
+            c.reset(stream=st)
+            c.append(k, k, stream=st)
+            return [c.append_attend(new, new, q, stream=st)]
+        calls.append(step)
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        pending(*want)
+        got = call(s)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            # (the order of sums may differ between calls: outputs below 2 in size, three roundings of half a step each)
+            torch.testing.assert_close(x, y, rtol=0, atol=2.0 ** -5)
+    assert c.get_error() == 0
