@@ -68,7 +68,7 @@ __device__ __forceinline__ void load_turn(Turn<T>& t, const float2* cs, int c, b
   for (int w = 0; w < 2; ++w) {
     const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
 #pragma unroll
-    for (int i = 0; i < VL / 4; ++i) t.t[w][i] = __ldg(reinterpret_cast<const float4*>(cs + first) + i);
+    for (int i = 0; i < VL / 4; ++i) t.t[w][i] = pg_ld(reinterpret_cast<const float4*>(cs + first) + i);
   }
 }
 template <typename T>
@@ -136,7 +136,7 @@ __device__ __forceinline__ int search(int B, long long x, F f) {
 
 template <typename T, int D, bool kBounds>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
-k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
+k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
                T* q_out, T* __restrict__ bounds, AppendArgs a) {
   constexpr int VL = Vec<T>::N;
   constexpr int PH = D / 2 / VL;          // vector pairs of a head
@@ -211,11 +211,11 @@ k_paged_append(const T* __restrict__ k, const T* __restrict__ v, const T* q, T* 
       Vec<T> x, y, vx, vy;
       Turn<T> cs;
       const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
-      x.u = __ldg(reinterpret_cast<const uint4*>(k + off));
-      y.u = __ldg(reinterpret_cast<const uint4*>(k + off + D / 2));
+      x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
+      y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
       if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
-      vx.u = __ldg(reinterpret_cast<const uint4*>(v + off));
-      vy.u = __ldg(reinterpret_cast<const uint4*>(v + off + D / 2));
+      vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
+      vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
       const int64_t dst = (((int64_t)page << a.ps_log2) + (p & (ps - 1))) * dst_row + src0;
       *reinterpret_cast<uint4*>(vp + dst) = vx.u;
       *reinterpret_cast<uint4*>(vp + dst + D / 2) = vy.u;

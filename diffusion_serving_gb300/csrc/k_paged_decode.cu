@@ -115,7 +115,7 @@ __device__ __forceinline__ uint32_t split2(float x, float y, uint32_t* rest, con
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-               const T* __restrict__ q, T* __restrict__ out, kvc_pg_args a) {
+               const T* q, T* __restrict__ out, kvc_pg_args a) {
   constexpr int HB = D / 64;           // 64-dim boxes per tensor
   constexpr int NT = D / 8;            // n-tiles of 8 dims in O
   constexpr int NR = R / 8;            // query rows per lane
@@ -172,9 +172,9 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int key = w.r.lo + j * kTile<D> + (lane << box_log2);
       if (lane < per_tile && key < w.r.len) {
         int c = key >> a.ps_log2;
-        if (a.sel != nullptr) c = __ldg(a.sel + ((int64_t)w.b * a.Hkv + w.vh / a.sub) * a.n_sel + c);
+        if (a.sel != nullptr) c = pg_ld(a.sel + ((int64_t)w.b * a.Hkv + w.vh / a.sub) * a.n_sel + c);
         *col = c;
-        if (c >= 0) *page = __ldg((c < shared_cols ? a.prefix_pages : a.table + (int64_t)w.b * a.max_pages) + c);
+        if (c >= 0) *page = pg_ld((c < shared_cols ? a.prefix_pages : a.table + (int64_t)w.b * a.max_pages) + c);
       }
     };
     int t = 0;
@@ -260,7 +260,7 @@ k_paged_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int v = lane + 32 * x, r = v / VQ, c = v % VQ;
         const int64_t row = __shfl_sync(0xffffffffu, at, r);
         qv[x] = make_uint4(0, 0, 0, 0);
-        if (r < e.rows) qv[x] = __ldg(reinterpret_cast<const uint4*>(q + row * D) + c);
+        if (r < e.rows) qv[x] = pg_ld(reinterpret_cast<const uint4*>(q + row * D) + c);
       }
       if (prefix) {
         if (lane < e.rows) pm = __ldcg(a.pre_ml + at);

@@ -55,7 +55,7 @@ constexpr int kScoreThreads = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads)
-k_paged_score(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
+k_paged_score(const T* q, const T* bounds, SelArgs a) {
   constexpr int N = D / 32;
   kvc_pdl_wait();
   kvc_pdl_release();
@@ -150,7 +150,7 @@ __device__ __forceinline__ uint32_t part_of(uint32_t u, bool negative) {
 // 2 c + 8, 2 c + 9; the queries' fragments hold the same dims, so the sum is the same.
 template <typename T, int D>
 __global__ void __launch_bounds__(kMmaWarps * 32)
-k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
+k_paged_score_mma(const T* q, const T* bounds, SelArgs a) {
   constexpr int V = D / 32;                 // 16-byte vectors per lane of one bound
   kvc_pdl_wait();
   kvc_pdl_release();
@@ -162,13 +162,13 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
   float* out = reinterpret_cast<float*>(a.scores + ((int64_t)b * a.Hkv + kvh) * a.max_pages);
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
   // the row's length, its first pages' numbers (used where the length says so) and the first queries, loaded together
-  int page = first + n < a.max_pages ? __ldg(table + first + n) : -1;
+  int page = first + n < a.max_pages ? pg_ld(table + first + n) : -1;
   uint4 qx[V];
   auto load_q = [&](int g0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       qx[v] = make_uint4(0, 0, 0, 0);
-      if (g0 + n < a.G) qx[v] = __ldg(reinterpret_cast<const uint4*>(q + ((int64_t)b * a.H + kvh * a.G + g0 + n) * D + 32 * v + 8 * c));
+      if (g0 + n < a.G) qx[v] = pg_ld(reinterpret_cast<const uint4*>(q + ((int64_t)b * a.H + kvh * a.G + g0 + n) * D + 32 * v + 8 * c));
     }
   };
   load_q(0);
@@ -179,7 +179,7 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
   for (int g0 = 0; g0 < a.G; g0 += 8) {     // 8 heads a pass
     if (g0 > 0) {
       load_q(g0);
-      page = first + n < np ? __ldg(table + first + n) : -1;
+      page = first + n < np ? pg_ld(table + first + n) : -1;
     } else if (first + n >= np) {
       page = -1;
     }
@@ -191,7 +191,7 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int v = 0; v < V; ++v) x[h][v] = ok ? __ldg(bd + h * (D / 8) + 4 * v + c) : make_uint4(0, 0, 0, 0);
+        for (int v = 0; v < V; ++v) x[h][v] = ok ? pg_ld(bd + h * (D / 8) + 4 * v + c) : make_uint4(0, 0, 0, 0);
     };
     load_x();
     uint32_t qa[2][V][2][2];                // [hi, lo][vector][k16 step][k half]
@@ -215,7 +215,7 @@ k_paged_score_mma(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs
     uint32_t top2 = 0u, low2 = 0u;          // largest upper and least lower bound (or 0), 16-bit pairs
     for (int j = first; j < np; j += step) {
       if (j > first) load_x();
-      page = j + step + n < np ? __ldg(table + j + step + n) : -1;
+      page = j + step + n < np ? pg_ld(table + j + step + n) : -1;
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -376,7 +376,7 @@ __device__ __forceinline__ double fine_score(const T* q, const T* bd, int lane) 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kRankThreads)
-k_paged_rank(const T* __restrict__ q, const T* __restrict__ bounds, SelArgs a) {
+k_paged_rank(const T* q, const T* bounds, SelArgs a) {
   extern __shared__ float s_score[];                 // [np, rounded up to whole words of 32 pages]
   constexpr int kWords = KVC_PG_MAX_SCORED / 32;
   __shared__ int s_hist[kBins], s_pick[2], s_warp[kRankWarps], s_n[2];

@@ -31,12 +31,12 @@ struct SimtSmem {
 };
 
 __device__ __forceinline__ void load4(const float* p, float* x) {
-  const float4 u = *reinterpret_cast<const float4*>(p);
+  const float4 u = pg_ld(reinterpret_cast<const float4*>(p));
   x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
 }
 template <typename T2, typename T>
 __device__ __forceinline__ void load4_16(const T* p, float* x) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const uint2 u = pg_ld(reinterpret_cast<const uint2*>(p));
   const T2* h = reinterpret_cast<const T2*>(&u);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -49,7 +49,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) { load4_
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restrict__ vp, T* __restrict__ out,
+k_paged_simt(const T* q, const T* kp, const T* vp, T* __restrict__ out,
              kvc_pg_args a) {
   extern __shared__ __align__(16) uint8_t smem[];
   SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(smem);
@@ -100,7 +100,7 @@ k_paged_simt(const T* __restrict__ q, const T* __restrict__ kp, const T* __restr
         int pos = 0x7fffffff;
         if (key < it.r.len) {
           int col = key >> a.ps_log2;
-          if (a.sel != nullptr) col = __ldg(a.sel + ((int64_t)it.b * a.Hkv + it.vh / a.sub) * a.n_sel + col);
+          if (a.sel != nullptr) col = pg_ld(a.sel + ((int64_t)it.b * a.Hkv + it.vh / a.sub) * a.n_sel + col);
           if (col >= 0) {
             const int page = pg_page(a, it.b, col);
             if (page >= 0) {

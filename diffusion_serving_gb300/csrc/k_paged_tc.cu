@@ -306,7 +306,7 @@ k_paged_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
       const int key = w.r.lo + j * kBN + (lane << box_log2);
       if (lane >= per_tile || key >= w.r.len) return -1;
       const int col = key >> a.ps_log2;
-      return a.phase == 1 ? __ldg(a.prefix_pages + col) : __ldg(a.table + (int64_t)w.b * a.max_pages + col);
+      return a.phase == 1 ? pg_ld(a.prefix_pages + col) : pg_ld(a.table + (int64_t)w.b * a.max_pages + col);
     };
     int t = 0, n = 0, q_issued = 0;
     bool ok = true;

@@ -113,6 +113,30 @@ cudaError_t kvc_pg_prepare_tc(const kvc_paged* c);
 #define KVC_PG_SIMT_TILE 64
 
 #ifdef __CUDACC__
+// Loads of what the kernel before may have written: plain ones, not the read-only path of __ldg (or of const __restrict__
+// pointers), which is defined for data that nobody writes while the kernel lives; a programmatic dependent lives while its
+// predecessor still writes.  Volatile, so that they stay behind kvc_pdl_wait().
+__device__ __forceinline__ int32_t pg_ld(const int32_t* p) {
+  int32_t x;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint2 pg_ld(const uint2* p) {
+  uint2 x;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint4 pg_ld(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float4 pg_ld(const float4* p) {
+  float4 x;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p));
+  return x;
+}
+
 // ---- rows of a call -------------------------------------------------------------------
 // Row b: tokens [t0, t0 + n) of the call, keys at positions [lo, len) (`len` counts virtual slots
 // of the selected pages when pages are selected).  n = 0 for a row that is skipped.
@@ -571,7 +595,7 @@ struct kvc_pg_sched {
 
 // Page number of table column `col` of row b (phase 1: of the shared list), or -1 with the error bit.
 __device__ __forceinline__ int pg_page(const kvc_pg_args& a, int b, int col) {
-  const int p = a.phase == 1 ? __ldg(a.prefix_pages + col) : __ldg(a.table + (int64_t)b * a.max_pages + col);
+  const int p = a.phase == 1 ? pg_ld(a.prefix_pages + col) : pg_ld(a.table + (int64_t)b * a.max_pages + col);
   if (p < 0 || p >= a.n_pages) {
     atomicOr(a.err, KVC_DEV_BAD_PAGE);
     return -1;
