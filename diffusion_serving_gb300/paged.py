@@ -213,20 +213,23 @@ class PagedKVCache:
     def _rows(self, what, t, heads):
         """(token rows, elements from one to the next) of ``t``, whose rows are dense and evenly apart.  (The stride of a
         dimension of size 1 means nothing.)"""
-        n = self._tokens(what, t, heads)
-        s = t.stride()
-        even = True
-        if n == 1:
-            row = heads * self.head_dim
-        elif len(s) == 3:
-            row = s[0]
-        else:
-            b, per_row = t.shape[:2]
-            row = s[1] if per_row > 1 else s[0]
-            even = b == 1 or per_row == 1 or s[0] == per_row * row
-        if s[-1] != 1 or not even or (heads > 1 and s[-2] != self.head_dim):
-            raise ValueError(f"kvc: {what}: a token's heads must be dense and its tokens evenly apart, got strides {list(s)}")
-        return n, row
+        shape, s = t.shape, t.stride()
+        if t.dtype is self.dtype and t.get_device() == self._index:
+            if len(shape) == 3:
+                n, h, d = shape
+                row, head, one = s
+                if h == heads and d == self.head_dim and one == 1 and (head == d or h == 1):
+                    return n, row if n > 1 else h * d
+            elif len(shape) == 4:
+                b, m, h, d = shape
+                batch, row, head, one = s
+                if h == heads and d == self.head_dim and b == self.batch and one == 1 and (head == d or h == 1):
+                    if m == 1:
+                        return b, batch if b > 1 else h * d
+                    if b == 1 or batch == m * row:
+                        return b * m, row
+        self._tokens(what, t, heads)                       # (says what else is wrong)
+        raise ValueError(f"kvc: {what}: a token's heads must be dense and its tokens evenly apart, got strides {list(s)}")
 
     def _cu(self, cu):
         if cu is None:
