@@ -24,12 +24,21 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& y, float x) { y = x; }
 __device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn(x); }
 __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ float pick_max(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ __half pick_max(__half a, __half b) { return __hmax(a, b); }
-__device__ __forceinline__ __nv_bfloat16 pick_max(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmax(a, b); }
-__device__ __forceinline__ float pick_min(float a, float b) { return fminf(a, b); }
-__device__ __forceinline__ __half pick_min(__half a, __half b) { return __hmin(a, b); }
-__device__ __forceinline__ __nv_bfloat16 pick_min(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmin(a, b); }
+// (a NaN goes on: the page's bounds show it wherever in the page it stands)
+__device__ __forceinline__ float pick_max(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ __half pick_max(__half a, __half b) { return __hmax_nan(a, b); }
+__device__ __forceinline__ __nv_bfloat16 pick_max(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmax_nan(a, b); }
+__device__ __forceinline__ float pick_min(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ __half pick_min(__half a, __half b) { return __hmin_nan(a, b); }
+__device__ __forceinline__ __nv_bfloat16 pick_min(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmin_nan(a, b); }
 
 template <typename T>
 union Vec {

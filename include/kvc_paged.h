@@ -66,7 +66,7 @@ size_t kvc_paged_workspace_bytes(const kvc_paged_config* cfg);
  *  k_pages, v_pages: [n_pages, page_size, Hkv, D]; d_table, d_kv_len: as above (4-byte aligned).
  *  bounds: NULL, or the key bounds that kvc_paged_attend_sparse scores pages by, [n_pages,
  *    Hkv, 2, D] of the store's type: channelwise maximum, then minimum, over a page's filled
- *    slots.  kvc_paged_append keeps them.
+ *    slots (NaN where one of the keys is).  kvc_paged_append keeps them.
  *  workspace: kvc_paged_workspace_bytes(cfg) bytes; its counters and error word are zeroed on `stream`.
  *  The handle belongs to the current device; calls with another one current are KVC_ERR_ARG.
  *  Errors: KVC_ERR_ARG, KVC_ERR_UNSUPPORTED (head_dim, page_size or batch not listed above), KVC_ERR_CUDA. */
