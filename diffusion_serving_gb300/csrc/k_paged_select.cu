@@ -13,6 +13,10 @@
 // 8 kv heads of 128 (83 MB): 22 us, 3.8 TB/s (33 with the loads one after another); 4.5 us for one row.
 // k_paged_score does fp32 stores with FMAs, a warp per page.
 //
+// Bounds that are infinite or NaN.  The first pass's scores then say nothing (an infinity meets the zeroed half of q as
+// 0 times infinity; max drops a NaN), so any of them makes the error bound of its (row, kv head) infinite: every page is
+// scored again by the definition, a query element of 0 adding 0, and a page whose score is NaN ranks first.
+//
 // k_paged_rank, a block per (row, kv head), takes the n_select largest.  Rounding could swap pages
 // whose scores nearly agree, so it decides nothing: with |error| <= delta, a page more than 2 delta
 // above the last one taken is in, one more than 2 delta below is out, and those between are scored
@@ -91,7 +95,7 @@ k_paged_score(const T* q, const T* bounds, SelArgs a) {
           t += __shfl_xor_sync(0xffffffffu, t, o);
         }
         best = fmaxf(best, u);
-        terms = fmaxf(terms, t);
+        terms = t < INFINITY && u == u ? fmaxf(terms, t) : INFINITY;
       }
     }
     if (lane == 0) out[j] = best;
@@ -123,19 +127,19 @@ __device__ __forceinline__ float2 pair_f(uint32_t u, const __nv_bfloat16*) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, const __half*) {
-  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, const __nv_bfloat16*) {
-  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __half*) {
-  const __half2 r = __hmin2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, const __nv_bfloat16*) {
-  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 // the pair's positive (or negative) parts
@@ -210,6 +214,7 @@ k_paged_score_mma(const T* q, const T* bounds, SelArgs a) {
     }
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (!(l1 < INFINITY)) l1 = INFINITY;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l1 = fmaxf(l1, __shfl_xor_sync(0xffffffffu, l1, o));
     uint32_t top2 = 0u, low2 = 0u;          // largest upper and least lower bound (or 0), 16-bit pairs
@@ -244,9 +249,11 @@ k_paged_score_mma(const T* q, const T* bounds, SelArgs a) {
         if (i + 1 < np) out[i + 1] = g0 == 0 ? u1 : fmaxf(out[i + 1], u1);
       }
     }
-    // no score's terms sum to more (an upper bound below 0 has a lower one further from it)
+    // no score's terms sum to more (an upper bound below 0 has a lower one further from it); NaN where one of these is
     const float2 top = pair_f(top2, type), low = pair_f(low2, type);
-    terms = fmaxf(terms, l1 * fmaxf(fmaxf(top.x, top.y), -fminf(low.x, low.y)));
+    const float t = l1 * fmaxf(fmaxf(top.x, top.y), -fminf(low.x, low.y));
+    const bool finite = t < INFINITY && top.x == top.x && top.y == top.y && low.x == low.x && low.y == low.y;
+    terms = finite ? fmaxf(terms, t) : INFINITY;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) terms = fmaxf(terms, __shfl_xor_sync(0xffffffffu, terms, o));
@@ -267,6 +274,7 @@ __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 __device__ __forceinline__ uint64_t key_of(double x) {
+  if (x != x) return ~0ull;                          // NaN before all
   const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);      // -0 counts as 0
   return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
@@ -350,14 +358,15 @@ __device__ __forceinline__ float two_sum(float x, float y, float& err) {
   return s;
 }
 
-// Score of a page for one head, in twice fp32's precision; every lane of the warp returns it.
+// Score of a page for one head, in twice fp32's precision (in fp64 where it leaves fp32's range); every lane of the warp
+// returns it.  A query element of 0 adds 0, whatever the bounds.
 template <typename T, int D>
 __device__ __forceinline__ double fine_score(const T* q, const T* bd, int lane) {
   float hi = 0.f, lo = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const int d = lane + 32 * i;
-    const float x = to_f(q[d]), y = to_f(x > 0.f ? bd[d] : bd[D + d]);
+    const float x = to_f(q[d]), y = x == 0.f ? 0.f : to_f(x > 0.f ? bd[d] : bd[D + d]);
     const float p = __fmul_rn(x, y), e = __fmaf_rn(x, y, -p);
     float r;
     hi = two_sum(hi, p, r);
@@ -367,11 +376,21 @@ __device__ __forceinline__ double fine_score(const T* q, const T* bd, int lane) 
   for (int o = 16; o > 0; o >>= 1) {
     float r;
     const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
-    // (the same on both sides of the exchange: the sum is symmetric)
-    hi = two_sum(fmaxf(hi, h), fminf(hi, h), r);
+    // (the same on both sides of the exchange: the sum and its error, which is exact, are symmetric)
+    hi = two_sum(hi, h, r);
     lo = (lo + l) + r;
   }
-  return (double)hi + (double)lo;
+  if (fabsf(hi) < INFINITY) return (double)hi + (double)lo;
+  double u = 0.0;                                    // (the same branch in every lane)
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int d = lane + 32 * i;
+    const float x = to_f(q[d]);
+    if (x != 0.f) u += (double)x * (double)to_f(x > 0.f ? bd[d] : bd[D + d]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  return u;
 }
 
 template <typename T, int D>
@@ -482,7 +501,7 @@ k_paged_rank(const T* q, const T* bounds, SelArgs a) {
   float c_lo = t0 - dd, c_hi = t1 + dd;
   if (!(c_lo == c_lo) || need <= 0) c_lo = need > 0 ? -INFINITY : INFINITY;     // (infinities in the scores)
   if (!(c_hi == c_hi) || need <= 0) c_hi = INFINITY;
-  auto is_cand = [&](int i) { return need > 0 && !forced(i) && s_score[i] >= c_lo && s_score[i] <= c_hi; };
+  auto is_cand = [&](int i) { return need > 0 && !forced(i) && !(s_score[i] < c_lo) && !(s_score[i] > c_hi); };
   // a bit per page, a word per warp and step
   const int words = (np + 31) / 32;
   for (int w = warp; w < words; w += kRankWarps) {
@@ -508,9 +527,7 @@ k_paged_rank(const T* q, const T* bounds, SelArgs a) {
   auto score = [&](int i, int g) {
     const int page = a.table[(int64_t)b * a.max_pages + i];
     if (page < 0 || page >= a.n_pages) return -(double)INFINITY;
-    const double u = fine_score<T, D>(q + ((int64_t)b * a.H + kvh * a.G + g) * D,
-                                      bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D, lane);
-    return u == u ? u : -(double)INFINITY;
+    return fine_score<T, D>(q + ((int64_t)b * a.H + kvh * a.G + g) * D, bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D, lane);
   };
   int total;
   if (take == 2) {
@@ -534,7 +551,11 @@ k_paged_rank(const T* q, const T* bounds, SelArgs a) {
       for (uint32_t left = s_maybe[w]; left; left &= left - 1) {
         const int i = 32 * w + __ffs(left) - 1;
         double best = -INFINITY;
-        for (int g = 0; g < a.G; ++g) best = fmax(best, score(i, g));
+        for (int g = 0; g < a.G; ++g) {
+          const double u = score(i, g);
+          if (!(u <= best)) best = u;                // (a NaN comes in, and stays, below)
+          if (u != u) break;
+        }
         if (lane == 0) exact[i] = best;
       }
     __syncthreads();

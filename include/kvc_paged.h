@@ -134,6 +134,7 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
  *  the newest `recent` ones are always taken (first + recent <= n_select), then those with the
  *  largest scores, of equal scores the lower column.  Scores that fp32 cannot tell apart are taken in twice its precision
  *  (off by some 2^-44 of the sum of their terms' magnitudes), so no fp32 rounding decides.
+ *  A query element of 0 adds 0, whatever the bounds; a page whose score is NaN comes before all others.
  *  A row with at most n_select pages attends all of them.
  *  q, out: [batch, H, D]; d_lse: NULL or fp32 [batch, H].
  *  d_selected: int32 [batch, Hkv, n_select], written: the columns taken, ascending, then -1.
