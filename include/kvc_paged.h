@@ -144,7 +144,10 @@ int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse
 int kvc_paged_attend_sparse(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_select, int32_t first,
                             int32_t recent, int32_t* d_selected, uint32_t flags, void* stream);
 
-/* As kvc_get_error: synchronise `stream`, report and clear the handle's error word. */
+/* As kvc_get_error: synchronise `stream`, report and clear the handle's error word.  KVC_DEV_TIMEOUT in it (a wait in an
+ * attention ran out, 0.5 s) means that the outputs of every call on the handle since the last kvc_paged_get_error are
+ * undefined: a kernel that gave up may leave counters behind by which later calls join the parts of a row too soon or not at
+ * all (nothing hangs or faults by it).  This call puts the counters right, so what follows it is sound. */
 int kvc_paged_get_error(kvc_paged* c, void* stream, int32_t* bits);
 
 /* Testing hook, as kvc_debug_stall_waits. */
