@@ -243,6 +243,17 @@ __host__ __device__ inline void pg_even(int tiles, int items, int grid, int min_
   *stride = (tiles + *per - 1) / *per * *per;
 }
 
+// Whether `items` items of `tiles` tiles in all, the longest of `most`, are padded: no more than blocks, short or alike, and
+// the padded line within 32 bits (places, with room for the blocks' rounding).
+#define KVC_PG_LINE (0x7fffffffll - 65536)
+__host__ __device__ inline bool pg_padded(int most, long long items, long long tiles, int grid, int min_tiles, int whole, int* per,
+                                          int* stride) {
+  if (items <= 0 || items > grid) return false;
+  if (most > (whole > 2 * min_tiles ? whole : 2 * min_tiles) && most * items * 4 > 5 * tiles) return false;
+  pg_even(most, (int)items, grid, min_tiles, whole, per, stride);
+  return items * *stride <= KVC_PG_LINE;
+}
+
 // Tiles of token tile k of a row: the keys that its last token sees, causal, or all.
 __device__ __forceinline__ int pg_item_tiles(const kvc_pg_row& r, int k, int T, int TS, bool causal) {
   const int end = causal ? min(r.len, r.len - r.n + min((k + 1) * T, r.n)) : r.len;
@@ -342,21 +353,21 @@ struct kvc_pg_sched {
     }
     tiles *= a.Hv;
     items *= a.Hv;
-    over = __any_sync(0xffffffffu, over) || tiles + items * item_cost > 0x7fffffffll - 65536;
-    stride = 0;
+    over = __any_sync(0xffffffffu, over) || tiles + items * item_cost > KVC_PG_LINE;
     cost = item_cost;
     waves = 0;
     if (over) {
       if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_OVERFLOW);
       total = 0;
       per = 1;
+      stride = 0;
       return;
     }
-    if (items > 0 && items <= grid && (most <= (whole > 2 * min_tiles ? whole : 2 * min_tiles) || most * items * 4 <= 5 * tiles)) {
-      pg_even(most, (int)items, grid, min_tiles, whole, &per, &stride);
+    if (pg_padded(most, items, tiles, grid, min_tiles, whole, &per, &stride)) {
       cost = 0;
       total = (int)items * stride;
     } else {
+      stride = 0;
       total = (int)(tiles + items * cost);
       per = max(min_tiles, (total + grid - 1) / grid);
       if (kWaves && a.join_here) {
