@@ -15,7 +15,7 @@
 //
 // Bounds that are infinite or NaN.  The first pass's scores then say nothing (an infinity meets the zeroed half of q as
 // 0 times infinity; max drops a NaN), so any of them makes the error bound of its (row, kv head) infinite: every page is
-// scored again by the definition, a query element of 0 adding 0, and a page whose score is NaN ranks first.
+// scored again in fp64 by the definition, a query element of 0 adding 0, and a page whose score is NaN ranks first.
 //
 // k_paged_rank, a block per (row, kv head), takes the n_select largest.  Rounding could swap pages
 // whose scores nearly agree, so it decides nothing: with |error| <= delta, a page more than 2 delta
@@ -56,6 +56,7 @@ __device__ __forceinline__ int row_pages(const SelArgs& a, int b) {
 }
 
 constexpr int kScoreThreads = 256;
+constexpr float kWide = 0x1p120f;          // sums of terms above it count as infinite (their fp32 sums could leave the range)
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads)
@@ -95,7 +96,7 @@ k_paged_score(const T* q, const T* bounds, SelArgs a) {
           t += __shfl_xor_sync(0xffffffffu, t, o);
         }
         best = fmaxf(best, u);
-        terms = t < INFINITY && u == u ? fmaxf(terms, t) : INFINITY;
+        terms = t < kWide && u == u ? fmaxf(terms, t) : INFINITY;
       }
     }
     if (lane == 0) out[j] = best;
@@ -252,7 +253,7 @@ k_paged_score_mma(const T* q, const T* bounds, SelArgs a) {
     // no score's terms sum to more (an upper bound below 0 has a lower one further from it); NaN where one of these is
     const float2 top = pair_f(top2, type), low = pair_f(low2, type);
     const float t = l1 * fmaxf(fmaxf(top.x, top.y), -fminf(low.x, low.y));
-    const bool finite = t < INFINITY && top.x == top.x && top.y == top.y && low.x == low.x && low.y == low.y;
+    const bool finite = t < kWide && top.x == top.x && top.y == top.y && low.x == low.x && low.y == low.y;
     terms = finite ? fmaxf(terms, t) : INFINITY;
   }
 #pragma unroll
@@ -273,9 +274,10 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-__device__ __forceinline__ uint64_t key_of(double x) {
-  if (x != x) return ~0ull;                          // NaN before all
-  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);      // -0 counts as 0
+__device__ __forceinline__ uint64_t key_of(double x) {             // (in whole numbers: fp64 instructions are slow here)
+  const uint64_t u = (uint64_t)__double_as_longlong(x), m = u << 1;
+  if (m > 0xffe0000000000000ull) return ~0ull;       // NaN before all
+  if (m == 0) return 0x8000000000000000ull;          // -0 counts as 0
   return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
@@ -358,15 +360,21 @@ __device__ __forceinline__ float two_sum(float x, float y, float& err) {
   return s;
 }
 
-// Score of a page for one head, in twice fp32's precision (in fp64 where it leaves fp32's range); every lane of the warp
-// returns it.  A query element of 0 adds 0, whatever the bounds.
+// Score of a page for one head, in twice fp32's precision, where no sum of terms leaves fp32's range; every lane of the warp
+// returns it.
 template <typename T, int D>
 __device__ __forceinline__ double fine_score(const T* q, const T* bd, int lane) {
   float hi = 0.f, lo = 0.f;
+  T qx[D / 32], up[D / 32], dn[D / 32];              // (both bounds: which one counts is known only with q)
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const int d = lane + 32 * i;
-    const float x = to_f(q[d]), y = x == 0.f ? 0.f : to_f(x > 0.f ? bd[d] : bd[D + d]);
+    qx[i] = q[lane + 32 * i];
+    up[i] = bd[lane + 32 * i];
+    dn[i] = bd[D + lane + 32 * i];
+  }
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const float x = to_f(qx[i]), y = to_f(x > 0.f ? up[i] : dn[i]);
     const float p = __fmul_rn(x, y), e = __fmaf_rn(x, y, -p);
     float r;
     hi = two_sum(hi, p, r);
@@ -380,11 +388,14 @@ __device__ __forceinline__ double fine_score(const T* q, const T* bd, int lane) 
     hi = two_sum(hi, h, r);
     lo = (lo + l) + r;
   }
-  if (fabsf(hi) < INFINITY) return (double)hi + (double)lo;
-  double u = 0.0;                                    // (the same branch in every lane)
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int d = lane + 32 * i;
+  return (double)hi + (double)lo;
+}
+
+// The same in fp64, for terms that leave that range, infinite bounds and NaN among them; a query element of 0 adds 0.
+template <typename T, int D>
+__device__ __forceinline__ double wide_score(const T* q, const T* bd, int lane) {
+  double u = 0.0;
+  for (int d = lane; d < D; d += 32) {
     const float x = to_f(q[d]);
     if (x != 0.f) u += (double)x * (double)to_f(x > 0.f ? bd[d] : bd[D + d]);
   }
@@ -522,18 +533,19 @@ k_paged_rank(const T* q, const T* bounds, SelArgs a) {
   }
   __syncthreads();
   const int n_cand = s_n[0], rest = need - s_n[1];
-  // candidates: none are taken, all, those that rank high in the list, or by radix selection
-  const int take = rest <= 0 ? 0 : rest >= n_cand ? 1 : n_cand <= kList ? 2 : 3;
-  auto score = [&](int i, int g) {
+  // candidates: none are taken, all, those that rank high in the list, or by radix selection (also where scores are in fp64)
+  const bool wide = !(dd < INFINITY);
+  const int take = rest <= 0 ? 0 : rest >= n_cand ? 1 : n_cand <= kList && !wide ? 2 : 3;
+  auto score = [&](int i, int g, auto f) {
     const int page = a.table[(int64_t)b * a.max_pages + i];
     if (page < 0 || page >= a.n_pages) return -(double)INFINITY;
-    return fine_score<T, D>(q + ((int64_t)b * a.H + kvh * a.G + g) * D, bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D, lane);
+    return f(q + ((int64_t)b * a.H + kvh * a.G + g) * D, bounds + ((int64_t)page * a.Hkv + kvh) * 2 * D, lane);
   };
   int total;
   if (take == 2) {
     for (int e = warp; e < n_cand * a.G; e += kRankWarps) {
       const int f = e / a.G;
-      const uint64_t key = key_of(score(s_cand[f], e - f * a.G));
+      const uint64_t key = key_of(score(s_cand[f], e - f * a.G, fine_score<T, D>));
       if (lane == 0) atomicMax(&s_key[f], (unsigned long long)key);
     }
     __syncthreads();
@@ -552,7 +564,7 @@ k_paged_rank(const T* q, const T* bounds, SelArgs a) {
         const int i = 32 * w + __ffs(left) - 1;
         double best = -INFINITY;
         for (int g = 0; g < a.G; ++g) {
-          const double u = score(i, g);
+          const double u = wide ? score(i, g, wide_score<T, D>) : score(i, g, fine_score<T, D>);
           if (!(u <= best)) best = u;                // (a NaN comes in, and stays, below)
           if (u != u) break;
         }
