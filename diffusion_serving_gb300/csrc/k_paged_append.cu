@@ -8,7 +8,9 @@
 // x[j + D/2]), or two vectors of pairs (x[2j], x[2j+1]).  A block's warps are divided between columns
 // (32 such lanes' worth of the keys' and values' heads, or of the queries') and tokens: few tokens to
 // a run, and all of them are on columns; many, and each takes every eighth token, some four in all,
-// so that a long page does not become a long chain.  kUnroll tokens are loaded before any is stored.
+// so that a long page does not become a long chain.  One token of a warp is in flight, all its loads together
+// (eight 16-byte ones a lane, and 32 warps an SM: 5.2 TB/s for prompts, 0.77 of a copy; a decode step of 32 rows takes
+// 5 us replayed, of which the loads that wait for the page number, though only the stores need it, are a part).
 // A run's keys, after rounding, give the page's maximum and minimum in registers: no second pass, no
 // atomics.
 #include "paged_internal.h"

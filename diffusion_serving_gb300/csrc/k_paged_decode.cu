@@ -28,7 +28,8 @@
 // same rows: 98 us, 5.6 TB/s (from L2 8.7): a slot's 128 bytes are short pieces to DRAM.
 
 // R = 8 leaves half of M free, and P uses it: rows 8..15 carry what rounding P to 16 bits lost, so
-// O is as exact as from fp32 weights at no further MMA.  R = 16 uses all of M, with P rounded once.
+// O is as exact as from fp32 weights at no further MMA.  R = 16 uses all of M, with P rounded once (as much error again
+// as the output's own rounding; the rest would take a second set of MMAs).
 #include "paged_finish.h"
 #include "paged_ptx.h"
 

@@ -17,6 +17,9 @@
 // neighbouring tiles overlap; the QK issuer also waits until PV(j - 2) is being issued, which keeps
 // the tensor queue alternating.  The running max is moved (and O rescaled) only when a tile's sum of
 // weights shows that it grew by more than 2^8.
+// P is rounded to the store's type, once, for its product (l sums it unrounded): a second product for what the rounding left
+// would be half as much tensor work again in a kernel that this bounds.  It adds as much error again as rounding the output does (against
+// 64 bits 0.0023 of the output in bf16 where the output's own rounding makes 0.0017, 0.00028 and 0.00021 in fp16).
 // K and V arrive page by page: one box per page, 64-dim half and tensor (64 dims x min(page, 64)
 // slots); boxes of a tile lie where one 128-slot box would put them (the 128-byte swizzle goes by
 // the address).
@@ -26,7 +29,8 @@
 // matrix product's burst, 0.74 of its sustained rate); the rest is masked halves of diagonal tiles and the last wave's cut
 // items.  2 x 1024 tokens over 2 x 16384 slots, not causal: 391 us, 1.36 PFLOP/s, against 377 us of the linear store's
 // kernel.  Pages of 16 make it 520 us: 16 copies a tile from one warp, some 80 cycles each, are more than a tile's products
-// take.  (Lanes issue in turn; one lane issuing all takes twice that a copy.)
+// take.  (Lanes issue in turn; one lane issuing all takes twice that a copy.)  The causal chunks above, replayed by themselves: 268 us
+// with pages of 64, 297 of 32, 362 of 16, and 362 of 128.
 //
 // Every mbarrier wait is bounded (0.5 s); on expiry the block records KVC_DEV_TIMEOUT, lets its TMA
 // loads and MMAs land, frees TMEM and returns.

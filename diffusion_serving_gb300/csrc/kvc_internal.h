@@ -95,7 +95,9 @@ __device__ __forceinline__ int64_t kvc_kv_offset(const kvc_geom& g, int b, int r
 // instructions) while the previous kernel on the stream is still finishing; each of
 // them calls kvc_pdl_wait() before it touches any global memory, which blocks until
 // every prerequisite grid has completed and its writes are visible, so the stream
-// order of the data is unchanged.  kvc_pdl_release() lets the next such kernel start.
+// order of the data is unchanged.  kvc_pdl_release() lets the next such kernel start; every
+// kernel calls it behind its own wait, so a dependent's predecessors but the last one are complete when
+// it begins (by that alone k_paged_join.cu reads lengths, which nothing writes next to it, before its wait).
 __device__ __forceinline__ void kvc_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void kvc_pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

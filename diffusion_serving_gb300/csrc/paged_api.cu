@@ -61,7 +61,8 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
 // are stacked) the tensor-core kernel.  "Few" is 16 rows, one pass over a row's keys, or 32, two passes,
 // where all rows' and groups' slots (behind the prefix) are at most 128 K: 20 rows a group, 8 groups of 128 dims, take
 // 18.5 us in two passes and 23.1 in the tensor-core kernel for a batch of 1 over 8000 slots, 25.6 and 27.6 for 8 over 2000,
-// 26.4 and 34.1 for 32 over 300; but 85 and 64 for 8 over 8000, 96 and 67 for 32 over 2000.
+// 26.4 and 34.1 for 32 over 300; but 85 and 64 for 8 over 8000, 96 and 67 for 32 over 2000.  Lengths are on the device, so the slots
+// are those that the table has columns for: with one sized for far longer rows these batches take the second figure of each pair.
 bool simt_only(const kvc_paged* c, uint32_t flags) { return c->cfg.dtype == KVC_F32 || (flags & KVC_KERNEL_SIMT); }
 
 bool few_rows(const kvc_pg_args& a, int64_t slots) {
@@ -79,7 +80,7 @@ cudaError_t run_attend(const kvc_paged* c, const kvc_pg_args& a, const void* q, 
 // numbers below the prefix's end from the shared list) than once for all in three launches.  What counts is the bytes
 // that all rows' passes over it read: at 34 MB (8 rows, 1024 slots, 8 heads of 128) 12.6 us against 22.2, at 67 MB 17.1
 // against 24.0, at 134 MB 26.1 against 25.3 (pages of 64: 23.0 against 25.5; heads of 64: 26.2 against 25.1), at 268 MB
-// 43 and 26.
+// 43 and 26.  (The prefix counts with the length of its list, not the length on the device: 1024 slots in a list of 8192, 21.3 us.)
 bool one_pass(const kvc_pg_args& a, int head_dim) {
   const int T = 16 / a.Gv;                             // tokens to an item
   const int64_t passes = (int64_t)a.B * a.Hv * ((a.max_q + T - 1) / T);

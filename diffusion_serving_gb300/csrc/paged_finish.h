@@ -69,10 +69,11 @@ __device__ __forceinline__ void pg_join1(float& M, float& L, float4& x, float2 m
   if (w != 0.f) pg_acc4(x, w, y);
 }
 
-// Partials of R rows: slot i of a buffer, row r.  Where the tensor-core kernel, which has a row to a thread, may join them
-// itself (`by8`: not a shared prefix's), 8 dims of all rows lie together, so that a warp's stores and loads are whole
-// lines; else rows do, for the joining kernels, which have a warp to a row (a prefix of 4096 slots, 8 rows: 28.0 us, and
-// 33.6 with 8 dims together; 1302 tokens over 8000 slots, 40 heads: 155 us with 8 dims together, 180 with rows).
+// Partials of R rows: slot i of a buffer, row r.  What the tensor-core kernel leaves of rows' own slots (`by8`) has 8 dims of
+// all rows together, whoever joins it: that kernel, with a row to a thread, or k_paged_join; its stores, and its own loads, are then
+// whole lines (1302 tokens over 8000 slots, 40 heads: 155 us, and 180 with a row's dims together).  All others have a row's dims
+// together: a shared prefix's, which k_paged_join_prefix reads with a warp to a row (4096 slots, 8 rows: 28.0 us, and 33.6 with
+// 8 dims together), and the streaming and FMA kernels'.
 template <int R, int D, bool by8 = false>
 __device__ __forceinline__ void pg_load_part(const float* buf, int64_t i, int r, int d, float2* ml, float4* y) {
   const float* p = buf + i * (int64_t)(R * (D + 2));

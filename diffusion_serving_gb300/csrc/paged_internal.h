@@ -41,7 +41,7 @@ struct kvc_pg_layout {
   size_t parts;         // split partials
   size_t prefix;        // partials of a shared prefix
   size_t pre_o, pre_ml; // what they join to: fp32 [max_tokens * H][D], and (max, sum)
-  size_t scores;        // fp32 [batch, Hkv, max_pages]
+  size_t scores;        // 8 bytes [batch, Hkv, max_pages]: fp32 scores, or the border's in fp64
   size_t total;
 };
 kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& cfg);

@@ -294,8 +294,9 @@ class PagedKVCache:
         return q_out
 
     def attend(self, q, *, cu_q=None, max_q=None, out=None, lse=None, flags=0, stream=None):
-        """Attention of every token over its row's slots.  ``max_q``: most tokens of a row (with ``cu_q``;
-        None: all of them).  ``lse``: a buffer, or True for a new one; then (out, lse) is returned."""
+        """Attention of every token over its row's slots.  ``max_q``: most tokens of a row (with ``cu_q``; None: as many as
+        the call has in all, which is right but runs packed single tokens in the chunks' kernel: give it).
+        ``lse``: a buffer, or True for a new one; then (out, lse) is returned."""
         n, out, lse, lse_ptr = self._q(q, out, lse, stream)
         self._call("kvc_paged_attend", _lib.kvc_paged_attend, q.data_ptr(), out.data_ptr(),
                    lse_ptr, n, self._cu(cu_q), n if max_q is None else max_q, flags,

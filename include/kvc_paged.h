@@ -17,8 +17,8 @@
  *
  * Rows of a call.  n_tokens token rows stand one behind another, row b's at
  * [d_cu[b], d_cu[b + 1]) (int32 [batch + 1], not decreasing, at most n_tokens); d_cu = NULL
- * means n_tokens / batch for every row.  A row may have none.  Tokens behind the last row's
- * are neither read nor written.
+ * means n_tokens / batch for every row.  A row may have none.  Nothing is written for tokens behind
+ * the last row's, and what their rows of q, k and v hold does not matter (attentions may read it).
  *
  * Order.  Calls on one handle share its workspace: the caller orders them (one stream, or
  * events).  Attentions that may run at the same time need a handle and a workspace each; the
@@ -58,8 +58,8 @@ enum {
   KVC_ROPE_HALF = 1         /* pairs (x[j], x[j + D/2]) instead of (x[2j], x[2j+1])        */
 };
 
-/* Bytes of the workspace (error word, split partials, counters, scores); 0 for a config
- * that kvc_paged_create would refuse. */
+/* Bytes of the workspace (error word, split partials, counters, 8 bytes per row, kv head and column for
+ * scores where max_pages is at most 32768); 0 for a config that kvc_paged_create would refuse. */
 size_t kvc_paged_workspace_bytes(const kvc_paged_config* cfg);
 
 /* Create a handle.
@@ -102,7 +102,9 @@ int kvc_paged_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stri
  *  q, out: [n_tokens, H, D], dense, 16-byte aligned, apart from one another; d_lse: NULL or fp32 [n_tokens, H],
  *    the natural log-sum-exp of the scaled scores.
  *  max_q: most tokens a row has (with d_cu; ignored without it); a row with more is
- *    KVC_DEV_BAD_CUSEQ.
+ *    KVC_DEV_BAD_CUSEQ.  It chooses the kernel, as lengths are on the device: single tokens under a large max_q run
+ *    in the chunks' kernel.  So do the columns of the table for 17 to 32 query rows a group (tokens x heads / kv_heads), which
+ *    the streaming kernel takes only where batch x kv_heads x max_pages x page_size is at most 128 K.
  *  flags: KVC_CAUSAL (token i of a row's n sees the slots up to its own, kv_len - n + i),
  *    KVC_KERNEL_SIMT (the fp32-FMA kernel for any type, a cross-check).
  *  Slots behind a row's length may hold anything.  The values of the slots that it has must be finite where a token must
@@ -117,8 +119,8 @@ int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32
                      int32_t max_q, uint32_t flags, void* stream);
 
 /* kvc_paged_attend for rows whose first slots are the same pages (a common prompt): slots
- * [0, P) are read from d_prefix_pages, once for all rows' tokens together (short prefixes of few rows, up to 96 MB of
- * reads in all, once per row), and slots [P, kv_len) from each row's own table at their usual columns (the columns below P / page_size are not read).
+ * [0, P) are read from d_prefix_pages, once for all rows' tokens together (short lists of few rows, up to 96 MB of
+ * reads in all by prefix_pages, once per row), and slots [P, kv_len) from each row's own table at their usual columns (the columns below P / page_size are not read).
  *  d_prefix_pages: int32 [prefix_pages] page numbers; d_prefix_len: int32 [1] on the device, P, a
  *    multiple of page_size, 0 <= P <= prefix_pages * page_size (else KVC_DEV_BAD_KVLEN, nothing written).
  *  A row with kv_len < P sees the first kv_len slots of the prefix.
