@@ -115,6 +115,11 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _stream_of(h: int, device):
+    """The torch stream of a handle (0 is the default stream; ExternalStream would take it for none)."""
+    return torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor for a call on ``stream`` to write and the current stream to use afterwards.  torch's allocator hands
     memory out by stream: what the current stream has freed may have work pending there, so the memory is ``stream``'s, and
@@ -124,7 +129,7 @@ def _empty(shape, dtype, device, stream):
     h, current = _stream(stream), torch.cuda.current_stream(device)
     if h == current.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(h, device=device)):
+    with torch.cuda.stream(_stream_of(h, device)):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(current)
     return t

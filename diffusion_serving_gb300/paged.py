@@ -165,7 +165,7 @@ class PagedKVCache:
             self.bounds = own("bounds", None if bounds is True else bounds, (n_pages, kv_heads, 2, head_dim), self.dtype, 0)
         self.workspace = own("workspace", None, (wb,), torch.uint8)
         h, current = self._stream(stream), torch.cuda.current_stream(device)
-        other = None if h == current.cuda_stream else torch.cuda.ExternalStream(h, device=device)
+        other = None if h == current.cuda_stream else kvc._stream_of(h, device)
         if other is not None:                              # (what was allotted and filled above)
             other.wait_stream(current)
         with torch.cuda.device(device):
@@ -181,7 +181,7 @@ class PagedKVCache:
         """The stream's handle; without one, the current stream of the cache's device."""
         h = _current_stream(self._index) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
         if h not in self._streams:
-            s = torch.cuda.ExternalStream(h, device=self.device)
+            s = kvc._stream_of(h, self.device)
             for t in self._own:
                 t.record_stream(s)
             self._streams.add(h)

@@ -53,6 +53,27 @@ def test_outputs_are_not_memory_that_the_current_stream_still_writes(dtype, new,
     assert c.get_error() == 0
 
 
+@pytest.mark.parametrize("default", [0, "default_stream"])
+def test_the_default_stream_from_another(default):
+    """Its handle is 0."""
+    c, table, g = make(2, 8, 2, 128, BF16, 32, [300, 40], seed=41)
+    q = randn(g, 2, 8, 128, dtype=BF16).cuda()
+    want = c.attend(q, lse=True)
+    on = default if default == 0 else torch.cuda.default_stream()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        pending(*want)
+        got = c.attend(q, lse=True, stream=on)
+        d = paged.PagedKVCache(2, 8, 2, 128, BF16, page_size=32, n_pages=c.cfg.n_pages, max_pages=c.cfg.max_pages, k_pages=c.k_pages,
+                               v_pages=c.v_pages, block_table=c.block_table, kv_len=c.kv_len, stream=on)
+        more = d.attend(q, lse=True, stream=on)
+    torch.cuda.synchronize()
+    for x, y, z in zip(got, more, want):
+        assert torch.equal(bits(x), bits(z)) and torch.equal(bits(y), bits(z))
+    assert c.get_error() == 0 and d.get_error() == 0
+
+
 def test_outputs_are_not_handed_out_again_while_the_current_stream_reads_them():
     c, table, g = make(2, 8, 2, 128, BF16, 32, [300, 40], seed=36)
     q = randn(g, 2, 8, 128, dtype=BF16).cuda()
@@ -138,3 +159,25 @@ def test_linear_cache_outputs_are_not_memory_that_the_current_stream_still_write
             # (the order of sums may differ between calls: outputs below 2 in size, three roundings of half a step each)
             torch.testing.assert_close(x, y, rtol=0, atol=2.0 ** -5)
     assert c.get_error() == 0
+
+
+def test_a_cache_of_another_stream_given_back_while_the_default_one_has_calls_pending():
+    c, table, g = make(2, 8, 2, 128, BF16, 32, [3000, 400], seed=40)
+    q = randn(g, 2, 8, 128, dtype=BF16).cuda()
+    want, out = c.attend(q), torch.empty_like(q)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        d = paged.PagedKVCache(2, 8, 2, 128, BF16, page_size=32, n_pages=c.cfg.n_pages, max_pages=c.cfg.max_pages)
+        for x, y in ((d.k_pages, c.k_pages), (d.v_pages, c.v_pages), (d.block_table, c.block_table), (d.kv_len, c.kv_len)):
+            x.copy_(y)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SLEEP)
+    d.attend(q, out=out)
+    shapes = [(t.shape, t.dtype) for t in (d.k_pages, d.v_pages, d.block_table, d.kv_len, d.workspace)]
+    del d, x, y
+    with torch.cuda.stream(s):
+        for shape, dtype in shapes:
+            torch.empty(shape, dtype=dtype, device="cuda").fill_(1)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), bits(want))
