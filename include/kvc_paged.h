@@ -123,7 +123,8 @@ int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32
  * reads in all by prefix_pages, once per row), and slots [P, kv_len) from each row's own table at their usual columns (the columns below P / page_size are not read).
  *  d_prefix_pages: int32 [prefix_pages] page numbers; d_prefix_len: int32 [1] on the device, P, a
  *    multiple of page_size, 0 <= P <= prefix_pages * page_size (else KVC_DEV_BAD_KVLEN, nothing written).
- *  A row with kv_len < P sees the first kv_len slots of the prefix.
+ *  A row with kv_len < P sees the first kv_len slots of the prefix.  All P slots must hold finite values, also where every
+ *  row is shorter: the prefix is read as one row of its own.
  *  n_tokens <= cfg.max_tokens, and tokens x heads x prefix within what 32 bits count in tiles (KVC_ERR_RANGE).  The
  *  rest as kvc_paged_attend. */
 int kvc_paged_attend_shared(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_tokens,
