@@ -13,6 +13,9 @@
 // 5 us replayed, of which the loads that wait for the page number, though only the stores need it, are a part).
 // A run's keys, after rounding, give the page's maximum and minimum in registers: no second pass, no
 // atomics.
+//
+// With positions of several axes (kAxes) each pair takes its angles from the row of its axis: two neighbouring pairs of
+// one axis by one 16-byte load, as before, others by two of 8 bytes.
 #include "paged_internal.h"
 #include "paged_rope.h"
 
@@ -64,6 +67,9 @@ struct AppendArgs {
   int kv_groups;              // column groups of the keys; those of the queries follow
   int H, Hkv;
   int half;
+  const int32_t* pos;         // [n_tokens][n_axes], with axes
+  int n_axes;
+  uint32_t pair_axis[4];      // two bits a pair
 };
 
 // Turns the two vectors x (elements c VL ..) and y (D/2 further) of a head by the row `cs` of the table.
@@ -82,6 +88,62 @@ __device__ __forceinline__ void load_turn(Turn<T>& t, const float2* cs, int c, b
     for (int i = 0; i < VL / 4; ++i) t.t[w][i] = pg_ld(reinterpret_cast<const float4*>(cs + first) + i);
   }
 }
+// A token's positions, one per axis (those that there are not repeat the last).
+struct Place {
+  int p[4];
+  __device__ __forceinline__ int of(int axis) const {
+    return axis & 2 ? (axis & 1 ? p[3] : p[2]) : (axis & 1 ? p[1] : p[0]);
+  }
+};
+__device__ __forceinline__ bool load_place(const AppendArgs& a, int64_t token, Place& at) {
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    at.p[i] = i < a.n_axes ? pg_ld(a.pos + token * a.n_axes + i) : at.p[i > 0 ? i - 1 : 0];
+    ok = ok && at.p[i] >= 0 && at.p[i] < a.rope_positions;
+  }
+  if (!ok && (threadIdx.x & 31) == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
+  return ok;
+}
+// The axes of a lane's pairs, two bits each: VL / 2 pairs from `first`, for both w.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t lane_axes(const AppendArgs& a, int c, bool half) {
+  constexpr int VL = Vec<T>::N;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+#pragma unroll
+    for (int i = 0; i < VL / 2; ++i) {
+      const int j = first + i, word = j >> 4;
+      const uint32_t x = word & 2 ? (word & 1 ? a.pair_axis[3] : a.pair_axis[2]) : (word & 1 ? a.pair_axis[1] : a.pair_axis[0]);
+      bits |= (x >> (2 * (j & 15)) & 3) << (2 * (w * (VL / 2) + i));
+    }
+  }
+  return bits;
+}
+template <typename T, int D>
+__device__ __forceinline__ void load_turn_axes(Turn<T>& t, const float2* rope, const Place& at, uint32_t axes, int c, bool half) {
+  constexpr int VL = Vec<T>::N;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+#pragma unroll
+    for (int i = 0; i < VL / 4; ++i) {
+      const int sh = 2 * (w * (VL / 2) + 2 * i), j = first + 2 * i;
+      const int p0 = at.of(axes >> sh & 3), p1 = at.of(axes >> (sh + 2) & 3);
+      const float2* r0 = rope + (int64_t)p0 * (D / 2) + j;
+      if (p0 == p1) {
+        t.t[w][i] = pg_ld(reinterpret_cast<const float4*>(r0));
+      } else {
+        const uint2 x = pg_ld(reinterpret_cast<const uint2*>(r0));
+        const uint2 y = pg_ld(reinterpret_cast<const uint2*>(rope + (int64_t)p1 * (D / 2) + j + 1));
+        t.t[w][i] = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(y.x), __uint_as_float(y.y));
+      }
+    }
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const Turn<T>& cs, bool half) {
   constexpr int VL = Vec<T>::N;
@@ -145,7 +207,7 @@ __device__ __forceinline__ int search(int B, long long x, F f) {
   return lo;
 }
 
-template <typename T, int D, bool kBounds>
+template <typename T, int D, bool kBounds, bool kAxes>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
                T* q_out, T* __restrict__ bounds, AppendArgs a) {
@@ -180,7 +242,7 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   const int column = (p0 >> a.ps_log2) + j;
   const int lo = max(p0, column << a.ps_log2), hi = min(r.len, (column + 1) << a.ps_log2);
   if (lo >= hi) return;
-  const int end = a.rope != nullptr ? min(hi, a.rope_positions) : hi;
+  const int end = !kAxes && a.rope != nullptr ? min(hi, a.rope_positions) : hi;
   if (end < hi && threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
   const int gw = a.groups_y;                        // column groups this block's warps divide into
   const int group = (int)blockIdx.y * gw + warp % gw;
@@ -190,13 +252,17 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
     const int col = (group - a.kv_groups) * 32 + lane;
     if (col < a.q_cols) {
       const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
+      const uint32_t axes = kAxes ? lane_axes<T, D>(a, col % PH, a.half) : 0;
       for (int p = lo + warp / gw; p < end; p += stride) {
         Vec<T> x, y;
         Turn<T> cs;
+        Place at;
+        if (kAxes && !load_place(a, r.t0 + p - p0, at)) continue;
         const T* src = q + (int64_t)(r.t0 + p - p0) * a.q_stride + off;
         x.u = *reinterpret_cast<const uint4*>(src);
         y.u = *reinterpret_cast<const uint4*>(src + D / 2);
-        load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), col % PH, a.half);
+        if (kAxes) load_turn_axes<T, D>(cs, a.rope, at, axes, col % PH, a.half);
+        else load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), col % PH, a.half);
         turn<T>(x, y, cs, a.half);
         T* dst = q_out + (int64_t)(r.t0 + p - p0) * a.H * D + off;
         *reinterpret_cast<uint4*>(dst) = x.u;
@@ -218,19 +284,23 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   Vec<T> mx0, mx1, mn0, mn1;
   bool any = false;
   if (have) {
+    const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
     for (int p = lo + warp / gw; p < end; p += stride) {
       Vec<T> x, y, vx, vy;
       Turn<T> cs;
+      Place at;
+      if (kAxes && !load_place(a, r.t0 + p - p0, at)) continue;
       const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
       x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
       y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
-      if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+      if (kAxes) load_turn_axes<T, D>(cs, a.rope, at, axes, c, a.half);
+      else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
       vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
       vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
       const int64_t dst = (((int64_t)page << a.ps_log2) + (p & (ps - 1))) * dst_row + src0;
       *reinterpret_cast<uint4*>(vp + dst) = vx.u;
       *reinterpret_cast<uint4*>(vp + dst + D / 2) = vy.u;
-      if (a.rope != nullptr) turn<T>(x, y, cs, a.half);
+      if (kAxes || a.rope != nullptr) turn<T>(x, y, cs, a.half);
       *reinterpret_cast<uint4*>(kp + dst) = x.u;
       *reinterpret_cast<uint4*>(kp + dst + D / 2) = y.u;
       if (kBounds) {
@@ -252,11 +322,24 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   }
   if (!kBounds || end <= lo) return;                // (uniform per block)
   // warps of the same columns, then what the page held before
+  if (kAxes && !any) {                              // (tokens may have been left out)
+#pragma unroll
+    for (int i = 0; i < VL; ++i) {
+      from_f(mx0.e[i], -INFINITY);
+      from_f(mn0.e[i], INFINITY);
+    }
+    mx1.u = mx0.u;
+    mn1.u = mn0.u;
+  }
   s_red[warp][0][lane] = mx0.u;
   s_red[warp][1][lane] = mx1.u;
   s_red[warp][2][lane] = mn0.u;
   s_red[warp][3][lane] = mn1.u;
-  __syncthreads();
+  if (kAxes) {
+    if (!__syncthreads_or(any)) return;             // nothing written to this page
+  } else {
+    __syncthreads();
+  }
   if (warp >= gw || !have) return;                  // the warp of the run's first token has one for sure
   auto widen = [&](const uint4& a0, const uint4& a1, const uint4& i0, const uint4& i1) {
     Vec<T> u0, u1, w0, w1;
@@ -301,18 +384,20 @@ cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, vo
   const int64_t runs = a.cu == nullptr ? (int64_t)a.B * ((a.n_tokens / a.B + ps - 2) / ps + 1)
                                        : (int64_t)a.n_tokens / ps + 2 * (int64_t)a.B;
   const dim3 grid((unsigned)runs, gy);
-  if (c->bounds != nullptr)
-    return kvc_launch_pdl(k_paged_append<T, D, true>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
-                          (T*)c->k, (T*)c->v, (T*)q_out, (T*)c->bounds, a);
-  return kvc_launch_pdl(k_paged_append<T, D, false>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
-                        (T*)c->k, (T*)c->v, (T*)q_out, (T*)nullptr, a);
+  auto go = [&](auto kernel) {
+    return kvc_launch_pdl(kernel, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q, (T*)c->k, (T*)c->v,
+                          (T*)q_out, (T*)c->bounds, a);
+  };
+  if (a.pos != nullptr) return c->bounds != nullptr ? go(k_paged_append<T, D, true, true>) : go(k_paged_append<T, D, false, true>);
+  return c->bounds != nullptr ? go(k_paged_append<T, D, true, false>) : go(k_paged_append<T, D, false, false>);
 }
 
 }  // namespace
 
 cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stride, const void* q,
                                  int64_t q_stride, void* q_out, int n_tokens, const int32_t* cu, const float* rope,
-                                 int rope_positions, bool half, cudaStream_t s) {
+                                 int rope_positions, const kvc_rope_axes* axes, const int32_t* positions, bool half,
+                                 cudaStream_t s) {
   const kvc_paged_config& g = c->cfg;
   AppendArgs a{};
   a.table = c->table;
@@ -331,6 +416,11 @@ cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int
   a.H = g.heads;
   a.Hkv = g.kv_heads;
   a.half = half;
+  if (axes != nullptr) {
+    a.pos = positions;
+    a.n_axes = axes->n_axes;
+    for (int j = 0; j < g.head_dim / 2; ++j) a.pair_axis[j >> 4] |= (uint32_t)axes->pair_axis[j] << (2 * (j & 15));
+  }
   const bool d64 = g.head_dim == 64;
   switch (g.dtype) {
     case KVC_F32: return d64 ? launch<float, 64>(c, k, v, q, q_out, a, s) : launch<float, 128>(c, k, v, q, q_out, a, s);

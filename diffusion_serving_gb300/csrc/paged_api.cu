@@ -40,9 +40,9 @@ bool on_device(const kvc_paged* c) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
 }
 
-int check_rows(const kvc_paged* c, int32_t n_tokens, const int32_t* d_cu) {
+int check_rows(const kvc_paged_config& g, int32_t n_tokens, const int32_t* d_cu) {
   if (n_tokens < 1 || !aligned(d_cu, 4)) return KVC_ERR_ARG;
-  if (d_cu == nullptr && n_tokens % c->cfg.batch) return KVC_ERR_ARG;
+  if (d_cu == nullptr && n_tokens % g.batch) return KVC_ERR_ARG;
   return KVC_OK;
 }
 
@@ -51,7 +51,7 @@ int check_attend(const kvc_paged* c, const void* q, const void* out, const float
   if (c == nullptr || !q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return KVC_ERR_ARG;
   if (flags & ~(uint32_t)(KVC_CAUSAL | KVC_KERNEL_SIMT)) return KVC_ERR_ARG;
   if (d_cu != nullptr && max_q < 1) return KVC_ERR_ARG;
-  const int rc = check_rows(c, n_tokens, d_cu);
+  const int rc = check_rows(c->cfg, n_tokens, d_cu);
   if (rc != KVC_OK) return rc;
   return on_device(c) ? KVC_OK : KVC_ERR_ARG;
 }
@@ -157,6 +157,33 @@ kvc_pg_args kvc_pg_base_args(const kvc_paged* c) {
   return a;
 }
 
+int kvc_pg_check_append(const kvc_paged_config& g, const void* k, const void* v, int64_t kv_stride, const void* q,
+                        int64_t q_stride, const void* q_out, int32_t n_tokens, const int32_t* d_cu, const float* d_rope,
+                        int32_t rope_positions, uint32_t flags) {
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return KVC_ERR_ARG;
+  if (flags & ~(uint32_t)KVC_ROPE_HALF) return KVC_ERR_ARG;
+  const int rc = check_rows(g, n_tokens, d_cu);
+  if (rc != KVC_OK) return rc;
+  const int64_t vec = g.dtype == KVC_F32 ? 4 : 8;      // elements of 16 bytes
+  const int64_t kv_row = (int64_t)g.kv_heads * g.head_dim, q_row = (int64_t)g.heads * g.head_dim;
+  if (kv_stride < kv_row || kv_stride % vec) return KVC_ERR_ARG;
+  if (d_rope != nullptr && (!aligned(d_rope, 16) || rope_positions < 1)) return KVC_ERR_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return KVC_ERR_ARG;
+  if (q != nullptr) {
+    if (d_rope == nullptr || !aligned(q, 16) || !aligned(q_out, 16) || q_stride < q_row || q_stride % vec) return KVC_ERR_ARG;
+    if (q == q_out && q_stride != q_row) return KVC_ERR_ARG;
+  }
+  return KVC_OK;
+}
+
+int kvc_pg_check_axes(const kvc_paged_config& g, const float* d_rope, const kvc_rope_axes* axes, const int32_t* d_positions) {
+  if (!d_rope || !axes || !d_positions || !aligned(d_positions, 4)) return KVC_ERR_ARG;
+  if (axes->n_axes < 1 || axes->n_axes > 4) return KVC_ERR_ARG;
+  for (int j = 0; j < g.head_dim / 2; ++j)
+    if (axes->pair_axis[j] >= axes->n_axes) return KVC_ERR_ARG;
+  return KVC_OK;
+}
+
 extern "C" {
 
 size_t kvc_paged_workspace_bytes(const kvc_paged_config* cfg) {
@@ -211,23 +238,24 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
 int kvc_paged_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stride, const void* q, int64_t q_stride,
                      void* q_out, int32_t n_tokens, const int32_t* d_cu, const float* d_rope, int32_t rope_positions,
                      uint32_t flags, void* stream) {
-  if (c == nullptr || !k || !v || !aligned(k, 16) || !aligned(v, 16)) return KVC_ERR_ARG;
-  if (flags & ~(uint32_t)KVC_ROPE_HALF) return KVC_ERR_ARG;
-  const int rc = check_rows(c, n_tokens, d_cu);
+  if (c == nullptr) return KVC_ERR_ARG;
+  const int rc = kvc_pg_check_append(c->cfg, k, v, kv_stride, q, q_stride, q_out, n_tokens, d_cu, d_rope, rope_positions, flags);
   if (rc != KVC_OK) return rc;
-  const kvc_paged_config& g = c->cfg;
-  const int64_t vec = g.dtype == KVC_F32 ? 4 : 8;      // elements of 16 bytes
-  const int64_t kv_row = (int64_t)g.kv_heads * g.head_dim, q_row = (int64_t)g.heads * g.head_dim;
-  if (kv_stride < kv_row || kv_stride % vec) return KVC_ERR_ARG;
-  if (d_rope != nullptr && (!aligned(d_rope, 16) || rope_positions < 1)) return KVC_ERR_ARG;
-  if ((q == nullptr) != (q_out == nullptr)) return KVC_ERR_ARG;
-  if (q != nullptr) {
-    if (d_rope == nullptr || !aligned(q, 16) || !aligned(q_out, 16) || q_stride < q_row || q_stride % vec) return KVC_ERR_ARG;
-    if (q == q_out && q_stride != q_row) return KVC_ERR_ARG;
-  }
   if (!on_device(c)) return KVC_ERR_ARG;
   return launched(kvc_pg_launch_append(c, k, v, kv_stride, q, q_stride, q_out, n_tokens, d_cu, d_rope, rope_positions,
-                                       (flags & KVC_ROPE_HALF) != 0, as_stream(stream)));
+                                       nullptr, nullptr, (flags & KVC_ROPE_HALF) != 0, as_stream(stream)));
+}
+
+int kvc_paged_append_axes(kvc_paged* c, const void* k, const void* v, int64_t kv_stride, const void* q, int64_t q_stride,
+                          void* q_out, int32_t n_tokens, const int32_t* d_cu, const float* d_rope, int32_t rope_positions,
+                          const kvc_rope_axes* axes, const int32_t* d_positions, uint32_t flags, void* stream) {
+  if (c == nullptr) return KVC_ERR_ARG;
+  int rc = kvc_pg_check_append(c->cfg, k, v, kv_stride, q, q_stride, q_out, n_tokens, d_cu, d_rope, rope_positions, flags);
+  if (rc == KVC_OK) rc = kvc_pg_check_axes(c->cfg, d_rope, axes, d_positions);
+  if (rc != KVC_OK) return rc;
+  if (!on_device(c)) return KVC_ERR_ARG;
+  return launched(kvc_pg_launch_append(c, k, v, kv_stride, q, q_stride, q_out, n_tokens, d_cu, d_rope, rope_positions,
+                                       axes, d_positions, (flags & KVC_ROPE_HALF) != 0, as_stream(stream)));
 }
 
 int kvc_paged_attend(kvc_paged* c, const void* q, void* out, float* d_lse, int32_t n_tokens, const int32_t* d_cu,

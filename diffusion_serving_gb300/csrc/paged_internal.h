@@ -3,6 +3,7 @@
 #pragma once
 
 #include "../../include/kvc_paged.h"
+#include "../../include/kvc_rope_axes.h"
 #include "kvc_internal.h"
 
 // Blocks of the attention kernels' grids (one per SM of a 152-SM GB300; two for the FMA
@@ -78,10 +79,17 @@ struct kvc_pg_args {
 
 kvc_pg_args kvc_pg_base_args(const kvc_paged* c);
 
+// Argument checks of an append (KVC_OK, or what the call returns).
+int kvc_pg_check_append(const kvc_paged_config& g, const void* k, const void* v, int64_t kv_stride, const void* q,
+                        int64_t q_stride, const void* q_out, int32_t n_tokens, const int32_t* d_cu, const float* d_rope,
+                        int32_t rope_positions, uint32_t flags);
+int kvc_pg_check_axes(const kvc_paged_config& g, const float* d_rope, const kvc_rope_axes* axes, const int32_t* d_positions);
+
 // ---- launchers ----------------------------------------------------------------------
 cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int64_t kv_stride, const void* q,
                                  int64_t q_stride, void* q_out, int n_tokens, const int32_t* cu, const float* rope,
-                                 int rope_positions, bool half, cudaStream_t s);
+                                 int rope_positions, const kvc_rope_axes* axes, const int32_t* positions, bool half,
+                                 cudaStream_t s);
 cudaError_t kvc_pg_launch_simt(const kvc_paged* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
 cudaError_t kvc_pg_launch_select(kvc_paged* c, const void* q, int n_sel, int first, int recent, int32_t* sel,
                                  cudaStream_t s);

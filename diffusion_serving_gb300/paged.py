@@ -25,6 +25,7 @@ from .kvc import (BF16, CAUSAL, CODE_DTYPE, DEV_BAD_CUSEQ, DEV_BAD_KVLEN, DEV_BA
                   KvcError)
 
 HEADER_PATH = os.path.join(os.path.dirname(kvc.HEADER_PATH), "kvc_paged.h")
+AXES_HEADER_PATH = os.path.join(os.path.dirname(kvc.HEADER_PATH), "kvc_rope_axes.h")
 DEV_BAD_PAGE = 128
 ROPE_HALF = 1
 
@@ -36,6 +37,23 @@ class kvc_paged_config(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float)]
 
 
+class kvc_rope_axes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * 64)]
+
+
+def rope_axes(pair_axis, n_axes=None) -> kvc_rope_axes:
+    """Which axis (0 .. n_axes - 1, at most 4 of them) each of a head's D/2 rotated pairs goes by: [0] * 16 + [1] * 24 +
+    [2] * 24 for sections of time, height and width side by side in heads of 128.  Made once, given to each ``append``."""
+    pair_axis = [int(x) for x in pair_axis]
+    n = max(pair_axis, default=0) + 1 if n_axes is None else int(n_axes)
+    if not 1 <= len(pair_axis) <= 64 or not 1 <= n <= 4 or min(pair_axis) < 0 or max(pair_axis) >= n:
+        raise ValueError(f"kvc: rope_axes takes an axis from 0 to {n - 1} (at most 4 axes) for each of up to 64 pairs")
+    a = kvc_rope_axes(n_axes=n)
+    a.pair_axis[:len(pair_axis)] = pair_axis
+    a.pairs = len(pair_axis)
+    return a
+
+
 def _bind():
     P, I32, I64, U32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
     cfgp = ctypes.POINTER(kvc_paged_config)
@@ -43,6 +61,8 @@ def _bind():
         "kvc_paged_workspace_bytes": (SZ, [cfgp]),
         "kvc_paged_create": (ctypes.c_int, [cfgp, P, P, P, P, P, P, P, ctypes.POINTER(P)]),
         "kvc_paged_append": (ctypes.c_int, [P, P, P, I64, P, I64, P, I32, P, P, I32, U32, P]),
+        "kvc_paged_append_axes": (ctypes.c_int, [P, P, P, I64, P, I64, P, I32, P, P, I32, ctypes.POINTER(kvc_rope_axes), P,
+                                                 U32, P]),
         "kvc_paged_attend": (ctypes.c_int, [P, P, P, P, I32, P, I32, U32, P]),
         "kvc_paged_attend_shared": (ctypes.c_int, [P, P, P, P, I32, P, I32, P, I32, P, U32, P]),
         "kvc_paged_attend_sparse": (ctypes.c_int, [P, P, P, P, I32, I32, I32, P, U32, P]),
@@ -260,10 +280,22 @@ class PagedKVCache:
         return n, out, lse, lse.data_ptr()
 
     # -- calls --------------------------------------------------------------------------
-    def append(self, k, v, *, cu_new=None, rope=None, half=False, q=None, q_out=None, stream=None):
+    def append(self, k, v, *, cu_new=None, rope=None, half=False, q=None, q_out=None, positions=None, axes=None,
+               stream=None):
         """Store the new tokens' keys, turned by ``rope`` [positions, D/2, 2] fp32 at their positions
         (``half``: pairs D/2 apart), and values; ``kv_len`` counts them already.  With ``q`` the queries
-        of the same tokens are turned into ``q_out`` (returned; allotted when None)."""
+        of the same tokens are turned into ``q_out`` (returned; allotted when None).
+
+        Tokens' positions are their slots, or ``positions``, int32 [tokens, axes] or [batch, n, axes]: several axes with
+        ``axes`` (``rope_axes``: which of them each pair goes by), one without."""
+        args, q_out = self._append_args(k, v, cu_new, rope, half, q, q_out, positions, axes, stream)
+        if positions is None:
+            self._call("kvc_paged_append", _lib.kvc_paged_append, *args)
+        else:
+            self._call("kvc_paged_append_axes", _lib.kvc_paged_append_axes, *args)
+        return q_out
+
+    def _append_args(self, k, v, cu_new, rope, half, q, q_out, positions, axes, stream):
         n, stride = self._rows("k", k, self.kv_heads)
         nv, vstride = self._rows("v", v, self.kv_heads)
         if n != nv or stride != vstride:
@@ -288,10 +320,32 @@ class PagedKVCache:
             qp, op = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("kvc: q_out without q")
-        self._call("kvc_paged_append", _lib.kvc_paged_append, k.data_ptr(), v.data_ptr(), stride, qp, q_stride, op, n,
-                   self._cu(cu_new), rp, n_pos, ROPE_HALF if half else 0,
-                   self._stream(stream))
-        return q_out
+        where = ()
+        if positions is not None:
+            where = self._positions(positions, axes, n, rope)
+        elif axes is not None:
+            raise ValueError("kvc: axes without positions")
+        return (k.data_ptr(), v.data_ptr(), stride, qp, q_stride, op, n, self._cu(cu_new), rp, n_pos, *where,
+                ROPE_HALF if half else 0, self._stream(stream)), q_out
+
+    def _positions(self, positions, axes, n, rope):
+        if axes is None:
+            axes = self._one_axis
+        if axes.pairs != self.head_dim // 2:
+            raise ValueError(f"kvc: axes must name an axis for each of the {self.head_dim // 2} pairs of a head, got {axes.pairs}")
+        s = positions.shape
+        if positions.dtype is not torch.int32 or positions.get_device() != self._index or not positions.is_contiguous() or \
+                s[-1:] != (axes.n_axes,) or positions.numel() != n * axes.n_axes or \
+                not (len(s) == 2 or len(s) == 3 and s[0] == self.batch):
+            raise ValueError(f"kvc: positions must be a dense int32 [{n}, {axes.n_axes}] (or [{self.batch}, n, {axes.n_axes}]) "
+                             f"on {self.device}, got {list(s)} {positions.dtype} on {positions.device}")
+        if rope is None:
+            raise ValueError("kvc: positions without rope")
+        return ctypes.byref(axes), positions.data_ptr()
+
+    @property
+    def _one_axis(self):
+        return rope_axes([0] * (self.head_dim // 2))
 
     def attend(self, q, *, cu_q=None, max_q=None, out=None, lse=None, flags=0, stream=None):
         """Attention of every token over its row's slots.  ``max_q``: most tokens of a row (with ``cu_q``; None: as many as
