@@ -1,0 +1,254 @@
+// Append to, and read from, the 4-bit paged store.
+//
+// Append: the runs, lanes and loads of the 16-bit append (k_paged_append.cu).  A lane has two vectors of 8 dims, D/2
+// apart in one head, so four neighbouring lanes hold two groups of 32 dims that share a scale: two shuffles
+// find a group's largest magnitude, and each lane's 8 codes make one 32-bit word.  The quotient x / s decides the code and
+// ties are common (both have few bits), so it has to be exact where it is exact: q = x (1 / s), and one residual step
+// q + (x - q s) (1 / s), gives the correctly rounded quotient (1 / s is).  |x| <= 7 s by then, so nothing overflows.
+// Bound by HBM for prompts and by latency for a step's few tokens.
+//
+// Read: a lane takes a word of 8 dims of the key and of the value, 4 + 1 bytes in and 16 bytes out each.
+#include "paged4_internal.h"
+#include "paged_append.h"
+
+namespace {
+
+// Code words of a lane's 8 dims x and of its 8 dims y, and their groups' scales, among four lanes.
+template <typename T>
+struct Held {
+  uint32_t w0, w1;
+  uint32_t s0, s1;        // e4m3 bits
+};
+__device__ __forceinline__ float pick_abs(float m, float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(x)));
+  return y;
+}
+// e4m3 of top / 7, to nearest even, 448 at most (a NaN stays one)
+__device__ __forceinline__ uint32_t scale_bits(float top) {
+  uint16_t b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(__fdiv_rn(top, 7.f)));
+  return b & 0xFFu;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t code_word(const Vec<T>& x, uint32_t bits) {
+  const uint32_t h = pg4_e4m3x2(bits, (const __half*)nullptr);
+  const float s = __half2float(*reinterpret_cast<const __half*>(&h));
+  if (s == 0.f) return 0x88888888u;
+  const float inv = __frcp_rn(s), most = 7.f * s;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = fminf(fmaxf(to_f(x.e[i]), -most), most);
+    const float q0 = v * inv;
+    const float q = __fmaf_rn(__fmaf_rn(-q0, s, v), inv, q0);
+    // 1.5 2^23 + 8 + q: rounded to a whole number, whose low bits are the code
+    w |= (__float_as_uint(q + 12582920.f) & 0xFu) << (4 * (i >> 1) + 16 * (i & 1));
+  }
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ Held<T> hold(const Vec<T>& x, const Vec<T>& y) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m0 = pick_abs(m0, to_f(x.e[i]));
+    m1 = pick_abs(m1, to_f(y.e[i]));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m0 = pick_abs(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = pick_abs(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+  Held<T> r;
+  r.s0 = scale_bits(m0);
+  r.s1 = scale_bits(m1);
+  r.w0 = code_word(x, r.s0);
+  r.w1 = code_word(y, r.s1);
+  return r;
+}
+
+template <typename T, int D, bool kAxes>
+__global__ void __launch_bounds__(kThreads, 4)
+k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, T* q_out, AppendArgs a) {
+  constexpr int VL = 8;
+  constexpr int PH = D / 2 / VL;          // vector pairs of a head
+  constexpr int NX = D / 32;              // groups of a head
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ps = 1 << a.ps_log2;
+  int b, j;
+  if (!find_run(a, b, j)) return;
+  const Row r = row_of(a, b);
+  if (!r.ok || r.n == 0) return;
+  const int p0 = r.len - r.n;                       // position of the row's first new token
+  const int column = (p0 >> a.ps_log2) + j;
+  const int lo = max(p0, column << a.ps_log2), hi = min(r.len, (column + 1) << a.ps_log2);
+  if (lo >= hi) return;
+  const int end = !kAxes && a.rope != nullptr ? min(hi, a.rope_positions) : hi;
+  if (end < hi && threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
+  const int gw = a.groups_y;
+  const int group = (int)blockIdx.y * gw + warp % gw;
+  const int stride = kWarps / gw;
+  if (group >= a.kv_groups) {
+    append_queries<T, D, kAxes>(a, r, q, q_out, group - a.kv_groups, lo + warp / gw, end, stride, p0);
+    return;
+  }
+  const int page = a.table[(int64_t)b * a.max_pages + column];
+  if (page < 0 || page >= a.n_pages) {              // (the same for the whole block)
+    if (lane == 0) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+    return;
+  }
+  const int col = group * 32 + lane;
+  const bool have = col < a.kv_cols;
+  const int head = have ? col / PH : 0, c = col % PH;     // (lanes past the last head take part in the shuffles)
+  const int64_t src0 = (int64_t)head * D + c * VL;
+  uint8_t* rec = pool + ((int64_t)page * a.Hkv + head) * kvc_pg4_record(D, a.ps_log2);
+  const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
+  for (int p = lo + warp / gw; p < end; p += stride) {
+    Vec<T> x, y, vx, vy;
+    Turn<T> cs;
+    Place at;
+    if (kAxes && !load_place(a, r.t0 + p - p0, at)) continue;        // (the same for the whole warp)
+    const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
+    x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
+    y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
+    if (kAxes) load_turn_axes<T, D>(cs, a.rope, at, axes, c, a.half);
+    else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+    vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
+    vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
+    if (kAxes || a.rope != nullptr) turn<T>(x, y, cs, a.half);
+    const Held<T> hk = hold(x, y), hv = hold(vx, vy);
+    if (!have) continue;
+    const int s = p & (ps - 1);
+    const int g0 = c >> 2, g1 = NX / 2 + (c >> 2);        // groups (and 16-byte pieces) of the two words
+    const int turn4 = (s >> 2) & (NX - 1);
+    uint8_t* kc = rec + s * (D / 2);
+    uint8_t* vc = kc + (ps * (D / 2));
+    *reinterpret_cast<uint32_t*>(kc + 4 * c) = hk.w0;
+    *reinterpret_cast<uint32_t*>(kc + D / 4 + 4 * c) = hk.w1;
+    *reinterpret_cast<uint32_t*>(vc + 16 * (g0 ^ turn4) + 4 * (c & 3)) = hv.w0;
+    *reinterpret_cast<uint32_t*>(vc + 16 * (g1 ^ turn4) + 4 * (c & 3)) = hv.w1;
+    if ((c & 3) == 0) {
+      uint8_t* ks = rec + ps * D + s * NX;
+      uint8_t* vs = rec + ps * D + ps * NX + s;
+      ks[g0] = (uint8_t)hk.s0;
+      ks[g1] = (uint8_t)hk.s1;
+      vs[g0 * ps] = (uint8_t)hv.s0;
+      vs[g1 * ps] = (uint8_t)hv.s1;
+    }
+  }
+}
+
+// Eight held values.
+template <typename T>
+__device__ __forceinline__ uint4 unheld(uint32_t word, uint32_t bits) {
+  const kvc_pg4_scale sc = pg4_scale<T>(pg4_e4m3x2(bits | bits << 8, (const T*)nullptr));
+  return make_uint4(pg4_pair<T, 0>(word, sc), pg4_pair<T, 1>(word, sc), pg4_pair<T, 2>(word, sc), pg4_pair<T, 3>(word, sc));
+}
+__device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 4)
+k_paged4_read(const uint8_t* pool, T* __restrict__ k_out, T* __restrict__ v_out, AppendArgs a) {
+  constexpr int W = D / 8, NX = D / 32;
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ps = 1 << a.ps_log2;
+  int b, j;
+  if (!find_run(a, b, j)) return;
+  const Row r = row_of(a, b);
+  if (!r.ok || r.n == 0) return;
+  const int p0 = r.len - r.n;
+  const int column = (p0 >> a.ps_log2) + j;
+  const int lo = max(p0, column << a.ps_log2), hi = min(r.len, (column + 1) << a.ps_log2);
+  if (lo >= hi) return;
+  const int page = pg_ld(a.table + (int64_t)b * a.max_pages + column);
+  if (page < 0 || page >= a.n_pages) {
+    if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+    return;
+  }
+  const int gw = a.groups_y;
+  const int col = ((int)blockIdx.y * gw + warp % gw) * 32 + lane;
+  if (col >= a.kv_cols) return;
+  const int head = col / W, w = col % W;
+  const uint8_t* rec = pool + ((int64_t)page * a.Hkv + head) * kvc_pg4_record(D, a.ps_log2);
+  for (int p = lo + warp / gw; p < hi; p += kWarps / gw) {
+    const int s = p & (ps - 1);
+    const int piece = (w >> 2) ^ ((s >> 2) & (NX - 1));
+    const uint32_t kw = (uint32_t)pg_ld(reinterpret_cast<const int32_t*>(rec + s * (D / 2) + 4 * w));
+    const uint32_t vw = (uint32_t)pg_ld(reinterpret_cast<const int32_t*>(rec + (ps + s) * (D / 2) + 16 * piece + 4 * (w & 3)));
+    const uint32_t ks = ld_byte(rec + ps * D + s * NX + (w >> 2));
+    const uint32_t vs = ld_byte(rec + ps * D + ps * NX + (w >> 2) * ps + s);
+    const int64_t dst = ((int64_t)(r.t0 + p - p0) * a.Hkv + head) * D + 8 * w;
+    if (k_out != nullptr) *reinterpret_cast<uint4*>(k_out + dst) = unheld<T>(kw, ks);
+    if (v_out != nullptr) *reinterpret_cast<uint4*>(v_out + dst) = unheld<T>(vw, vs);
+  }
+}
+
+AppendArgs base_args(const kvc_paged4* c, int n_tokens, const int32_t* cu) {
+  const kvc_paged_config& g = c->cfg;
+  AppendArgs a{};
+  a.table = c->table;
+  a.kv_len = c->kv_len;
+  a.cu = cu;
+  a.err = reinterpret_cast<int32_t*>(c->ws);
+  a.B = g.batch;
+  a.n_tokens = n_tokens;
+  a.ps_log2 = c->ps_log2;
+  a.n_pages = g.n_pages;
+  a.max_pages = g.max_pages;
+  a.H = g.heads;
+  a.Hkv = g.kv_heads;
+  return a;
+}
+
+template <typename T, int D>
+cudaError_t launch(kvc_paged4* c, const void* k, const void* v, const void* q, void* q_out, AppendArgs a, cudaStream_t s) {
+  a.kv_cols = a.Hkv * (D / 16);
+  a.q_cols = q != nullptr ? a.H * (D / 16) : 0;
+  a.kv_groups = (a.kv_cols + 31) / 32;
+  const dim3 grid = run_grid(a, a.kv_groups + (a.q_cols + 31) / 32);
+  if (a.pos != nullptr)
+    return kvc_launch_pdl(k_paged4_append<T, D, true>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
+                          c->pages, (T*)q_out, a);
+  return kvc_launch_pdl(k_paged4_append<T, D, false>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
+                        c->pages, (T*)q_out, a);
+}
+template <typename T, int D>
+cudaError_t launch_read(kvc_paged4* c, void* k_out, void* v_out, AppendArgs a, cudaStream_t s) {
+  a.kv_cols = a.Hkv * (D / 8);
+  const dim3 grid = run_grid(a, (a.kv_cols + 31) / 32);
+  return kvc_launch_pdl(k_paged4_read<T, D>, grid, dim3(kThreads), 0, s, (const uint8_t*)c->pages, (T*)k_out, (T*)v_out, a);
+}
+
+}  // namespace
+
+cudaError_t kvc_pg4_launch_append(kvc_paged4* c, const void* k, const void* v, int64_t kv_stride, const void* q,
+                                  int64_t q_stride, void* q_out, int n_tokens, const int32_t* cu, const float* rope,
+                                  int rope_positions, const kvc_rope_axes* axes, const int32_t* positions, bool half,
+                                  cudaStream_t s) {
+  AppendArgs a = base_args(c, n_tokens, cu);
+  a.rope = reinterpret_cast<const float2*>(rope);
+  a.rope_positions = rope_positions;
+  a.kv_stride = kv_stride;
+  a.q_stride = q_stride;
+  a.half = half;
+  if (axes != nullptr) set_axes(a, *axes, positions, c->cfg.head_dim);
+  const bool d64 = c->cfg.head_dim == 64;
+  if (c->cfg.dtype == KVC_F16) return d64 ? launch<__half, 64>(c, k, v, q, q_out, a, s) : launch<__half, 128>(c, k, v, q, q_out, a, s);
+  return d64 ? launch<__nv_bfloat16, 64>(c, k, v, q, q_out, a, s) : launch<__nv_bfloat16, 128>(c, k, v, q, q_out, a, s);
+}
+
+cudaError_t kvc_pg4_launch_read(kvc_paged4* c, void* k_out, void* v_out, int n_tokens, const int32_t* cu, cudaStream_t s) {
+  const AppendArgs a = base_args(c, n_tokens, cu);
+  const bool d64 = c->cfg.head_dim == 64;
+  if (c->cfg.dtype == KVC_F16) return d64 ? launch_read<__half, 64>(c, k_out, v_out, a, s) : launch_read<__half, 128>(c, k_out, v_out, a, s);
+  return d64 ? launch_read<__nv_bfloat16, 64>(c, k_out, v_out, a, s) : launch_read<__nv_bfloat16, 128>(c, k_out, v_out, a, s);
+}

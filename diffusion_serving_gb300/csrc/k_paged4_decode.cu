@@ -1,0 +1,496 @@
+// Attention of few query rows per group over the 4-bit paged store: decode steps, drafted tokens (and chunks of any length,
+// by items of up to 16 rows).
+//
+// Work goes to blocks as in the 16-bit streaming kernel (k_paged_decode.cu, paged_internal.h): a block takes one stretch
+// of the line of all rows' tiles, here of 128 slots, through a ring of shared-memory stages.  A page's slots of a head are
+// one record, so a tile arrives as one bulk copy per page.  Warps:
+//   0-7  consumers: 16 slots of each tile
+//   8,10 producers: page numbers, copies (every other record each)
+//   9    helper: the next items' queries and extents
+//
+// At a quarter of the 16-bit store's bytes a slot, instructions bound this kernel as much as HBM does, so the slots stand in M
+// of the m16n8k16 MMAs and the up to 8 (16: two MMAs) query rows in N: an MMA takes 16 slots x 16 dims of codes, twice what it
+// would with the queries in M.  Codes become operands in registers, without a pass through shared memory:
+//   S^T = K Q^T   A is K.  Any order of dims along k will do if Q has the same, so a lane's four A registers of all
+//                 steps are its slot's D/4 neighbouring dims: one 16-byte load per slot, one scale.
+//   O^T = V^T P^T A is V^T: pairs of neighbouring slots of one dim.  ldmatrix.trans moves 16-bit units, four codes of
+//                 a slot, and leaves a lane one unit of two slots in the halves of a register, so masking the
+//                 ith code of both gives such a pair; which dims share an MMA's rows does not matter.
+//                 B is P^T: S^T's accumulators, packed, through movmatrix.
+// Two codes become two values by a shift, a mask-and-or and one multiply-add (paged4_internal.h).
+// The running maximum of a query is looked for only when a weight outgrows its reference by 2^7 (one vote per tile);
+// weights are taken 2^8 too large, so that fp16 holds them with full precision down to 2^-22 of the reference, and
+// rounded to fp16 once for the product with V (their sum takes them unrounded).
+#include "paged4_internal.h"
+#include "paged_finish.h"
+#include "paged_ptx.h"
+
+namespace {
+
+using namespace pg;
+
+constexpr int kWarps = 8;                         // consumer warps
+constexpr int kThreads = (kWarps + 3) * 32;       // + producer, helper, producer
+constexpr int kTile = 16 * kWarps;                // slots per tile: 16 for each warp
+constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
+constexpr int kMinTiles = 4, kItemCost = 2;       // fewest tiles for a block; an item's beginning and end, in tiles
+constexpr float kBias = 8.f, kTop = 15.f;         // log2 of a weight at its reference, and of the largest taken
+
+template <int D> constexpr uint32_t kStageBytes = kTile * (D + D / 16);
+template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 8 : 6) : 12;
+
+template <typename T, int D, int R>
+struct Smem {
+  uint8_t stage[kStages<D, R>][kStageBytes<D>];   // 128-byte aligned
+  float acc[kWarps][R][D + kPad];
+  T q[2][R][D + 8];                               // an item's queries (+ 8: rows on different banks)
+  float2 ml[kWarps][R];
+  int64_t at[2][R];                               // rows of the outputs
+  int limit[2][R];                                // where each query row's keys end
+  kvc_pg_end end[2];
+  int tiles[2];                                   // this block's tiles of the item; -1: there is none
+  int key0[2];                                    // position of the first one's first slot
+  int len[2], open[2];                            // where the row's slots end; below this every query row sees all
+  uint32_t bad[2][kStages<D, R>];                 // records of a stage that no page stands behind, by producer
+  uint64_t full[kStages<D, R>], empty[kStages<D, R>];
+  uint64_t q_full[2], item_empty[2];
+  WaitCtl wc;
+  int flag;
+  int fail[2];                                    // a consumer's wait gave up: before an item, within it
+};
+
+__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// d += A B, A 16 x 16 (rows lane / 4 in a0, a2; rows lane / 4 + 8 in a1, a3), B 16 x 8
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const __half*) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const __nv_bfloat16*) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// D / 32 words of codes at a shared address (16 or 8 bytes).
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* r) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_byte(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_args a) {
+  constexpr int W = D / 32;            // words of a slot's codes to a lane; pieces of 32 dims
+  constexpr int MT = D / 16;           // 16-dim tiles of O^T
+  constexpr int NQ = R / 8;            // 8-query tiles
+  constexpr int S = kStages<D, R>;
+  const T* type = nullptr;
+  const __half* half_type = nullptr;
+  extern __shared__ uint8_t raw[];
+  using Sm = Smem<T, D, R>;
+  Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile WaitCtl* wc = &sm.wc;
+
+  // set-up that touches no global memory runs before the wait for the previous kernel
+  if (threadIdx.x < S) {
+    mbar_init(&sm.full[threadIdx.x], 64);            // both producers' lanes
+    mbar_init(&sm.empty[threadIdx.x], kWarps);
+  }
+  if (threadIdx.x >= 32 && threadIdx.x < 34) {
+    mbar_init(&sm.q_full[threadIdx.x - 32], 32);
+    mbar_init(&sm.item_empty[threadIdx.x - 32], kWarps);
+  }
+  if (threadIdx.x == 64) {
+    wait_init(&sm.wc, a.stall_ns);
+    sm.fail[0] = sm.fail[1] = 0;
+  }
+  fence_mbar_init();
+  __syncthreads();
+  kvc_pdl_wait();
+  kvc_pdl_release();
+  kvc_pg_sched<R, kTile> sch;
+  sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, kMinTiles, kItemCost, gridDim.x);
+  kvc_pg_item it;
+  bool more = false;
+  if (warp >= kWarps) more = sch.first(a, blockIdx.x, it);
+  const int ps = 1 << a.ps_log2;
+  const uint32_t record = (uint32_t)kvc_pg4_record(D, a.ps_log2);
+
+  if (warp == kWarps || warp == kWarps + 2) {
+    // ---------------- producers: records of a tile, every other one each ----------------
+    const int me = warp == kWarps ? 0 : 1;
+    const int per_tile = kTile >> a.ps_log2;                // 1, 2, 4 or 8
+    // lane i < per_tile: the page number of the tile's ith record, not looked at before it is used (a tile later); -1: not
+    // this producer's, or behind the row's end (where -1 is found in a table, it is a bad page)
+    auto look = [&](const kvc_pg_item& w, int j) {
+      const int key = j * kTile + (lane << a.ps_log2);
+      if (lane >= per_tile || (lane & 1) != me || key >= w.r.len) return -1;
+      return pg_ld(a.table + (int64_t)w.b * a.max_pages + (key >> a.ps_log2));
+    };
+    int t = 0;
+    bool ok = true;
+    int page = more ? look(it, it.tile0) : -1;
+    for (; ok && more;) {
+      const int tile0 = it.tile0, tile1 = it.tile1;
+      const int kvh = a.sub == 1 ? it.vh : it.vh / a.sub;
+      kvc_pg_item nx = it;
+      more = sch.next(a, nx);
+      for (int j = tile0; j < tile1; ++j, ++t) {
+        int npage = -1;                                     // the next tile's, in flight meanwhile
+        if (j + 1 < tile1) npage = look(it, j + 1);
+        else if (more) npage = look(nx, nx.tile0);
+        const int st = t % S;
+        if (t >= S) ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[st], (t / S - 1) & 1, wc));
+        if (!ok) break;
+        const bool there = lane < per_tile && (lane & 1) == me && j * kTile + (lane << a.ps_log2) < it.r.len;
+        const bool fine = there && page >= 0 && page < a.n_pages;
+        if (there && !fine) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+        const unsigned good = __ballot_sync(0xffffffffu, fine), bad = __ballot_sync(0xffffffffu, there && !fine);
+        if (lane == 0) {
+          sm.bad[me][st] = bad;
+          mbar_expect_tx(&sm.full[st], __popc(good) * record);
+        }
+        __syncwarp();
+        if (fine)
+          bulk_load(&sm.full[st], sm.stage[st] + lane * record, pool + ((int64_t)page * a.Hkv + kvh) * record, record);
+        __syncwarp();
+        if (lane != 0) mbar_arrive(&sm.full[st]);
+        page = npage;
+      }
+      it = nx;
+    }
+    if (lane == 0) {   // every load issued here lands before the block releases its shared memory, consumers that gave up or not
+      for (int i = max(0, t - S); i < t; ++i) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
+    }
+  } else if (warp == kWarps + 1) {
+    // ---------------- helper: queries of the items to come ----------------
+    constexpr int VQ = D / 8;                               // 16-byte vectors of a query row
+    for (int n = 0;; ++n) {
+      const int b = n & 1;
+      if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.item_empty[b], (n / 2 - 1) & 1, wc))) break;
+      if (!more) {
+        if (lane == 0) sm.tiles[b] = -1;
+        __syncwarp();
+        mbar_arrive(&sm.q_full[b]);
+        break;
+      }
+      const kvc_pg_end e = pg_end(a, sch, it);
+      int64_t at = 0;
+      int limit = 0x3fffffff;                               // rows that are not there see everything (no mask on their account)
+      if (lane < R) {
+        at = pg_at(a, sch, it, lane < e.rows ? lane : 0);
+        sm.at[b][lane] = at;
+        if (lane < e.rows) limit = pg_limit(a, it.r, it.k * sch.T + lane / a.Gv);
+        sm.limit[b][lane] = limit;
+      }
+      const int open = min(it.r.len, __reduce_min_sync(0xffffffffu, limit));
+      if (lane == 0) {
+        sm.end[b] = e;
+        sm.tiles[b] = it.tile1 - it.tile0;
+        sm.key0[b] = it.tile0 * kTile;
+        sm.len[b] = it.r.len;
+        sm.open[b] = open;
+      }
+      // every load is issued before any is stored
+      constexpr int NL = R * VQ / 32;
+      uint4 qv[NL];
+#pragma unroll
+      for (int x = 0; x < NL; ++x) {
+        const int v = lane + 32 * x, r = v / VQ, c = v % VQ;
+        const int64_t row = __shfl_sync(0xffffffffu, at, r);
+        qv[x] = make_uint4(0, 0, 0, 0);
+        if (r < e.rows) qv[x] = pg_ld(reinterpret_cast<const uint4*>(q + row * D) + c);
+      }
+#pragma unroll
+      for (int x = 0; x < NL; ++x) {
+        const int v = lane + 32 * x;
+        *reinterpret_cast<uint4*>(&sm.q[b][v / VQ][8 * (v % VQ)]) = qv[x];
+      }
+      mbar_arrive(&sm.q_full[b]);
+      more = sch.next(a, it);
+    }
+  } else {
+    // ---------------- consumers ----------------
+    const int g = lane >> 2, quad = lane & 3;
+    // Row r of S^T's first eight rows is slot 4 (r / 2) + r % 2 of the warp's sixteen, row r + 8 the slot two behind it, so that
+    // a lane's four slots of P^T and V^T are neighbours (one 4-byte load of their scales).
+    const int slot = 4 * (g >> 1) + (g & 1);
+    const int r0 = warp * 16;                               // the warp's slots within a tile
+    const int rec_i = r0 >> a.ps_log2, s0 = r0 & (ps - 1);   // their record, and where they begin in it
+    const uint32_t k_off = rec_i * record + (s0 + slot) * (D / 2) + quad * (D / 8);
+    const uint32_t ks_off = rec_i * record + ps * D + (s0 + slot) * W + (W == 4 ? quad : quad >> 1);
+    const uint32_t vs_off = rec_i * record + ps * (D + W) + s0 + 4 * quad;
+    // ldmatrix: lanes 8 m .. address the rows of matrix m: slots of the first eight rows or the others, one of two pieces
+    const int lr = lane & 7, l_slot = 4 * (lr >> 1) + (lr & 1) + 2 * (lane >> 3 & 1), l_piece = lane >> 4;
+    const uint32_t v_off = rec_i * record + (ps + s0 + l_slot) * (D / 2);
+    const int l_turn = (l_slot >> 2) & (W - 1);
+    auto bar = [] { named_bar<1>(kWarps * 32); };
+    int t = 0;                                              // tiles of this block before the item's
+    for (int n = 0;; ++n) {
+      const int b = n & 1;
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / 2) & 1, wc));
+      if (!ok) sm.fail[0] = 1;
+      bar();                                                // (the last item's states have been read, too)
+      if (sm.fail[0]) break;                                // what ends the loop is the same for every consumer
+      const int tiles = sm.tiles[b];
+      if (tiles < 0) break;
+      uint32_t qb[NQ][2 * W][2];                            // B operands: query 8 x + g, this lane's dims
+      int limit[NQ][2];
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+        for (int kk = 0; kk < 2 * W; ++kk) {
+          const uint2 v = *reinterpret_cast<const uint2*>(&sm.q[b][8 * x + g][quad * (D / 4) + 4 * kk]);
+          qb[x][kk][0] = v.x;
+          qb[x][kk][1] = v.y;
+        }
+        limit[x][0] = sm.limit[b][8 * x + 2 * quad];
+        limit[x][1] = sm.limit[b][8 * x + 2 * quad + 1];
+      }
+      const int len = sm.len[b], open = sm.open[b];
+      int key = sm.key0[b] + r0;                            // position of the warp's first slot
+      float o[NQ][MT][4];
+      float m[NQ][2], l[NQ][2];                             // references, sums of this lane's slots
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
+        m[x][0] = m[x][1] = -INFINITY;
+        l[x][0] = l[x][1] = 0.f;
+      }
+      const int t_end = t + tiles;
+      for (int u = t; u < t_end; ++u, key += kTile) {
+        const int st = u % S;
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (u / S) & 1, wc));
+        if (!ok) break;
+        const uint32_t base = smem_u32(sm.stage[st]);
+        const uint32_t gone = (sm.bad[0][st] | sm.bad[1][st]) >> rec_i & 1;
+        if (key < len && !gone) {
+          const bool masked = key + 16 > open;
+          // ---- S^T ----
+          float sc[NQ][4];
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+          {
+            uint32_t k0[W], k1[W];
+            lds_words<W>(base + k_off, k0);
+            lds_words<W>(base + k_off + 2 * (D / 2), k1);
+            const uint32_t b0 = lds_byte(base + ks_off), b1 = lds_byte(base + ks_off + 2 * W);
+            const kvc_pg4_scale s_0 = pg4_scale<T>(pg4_e4m3x2(b0 | b0 << 8, type)), s_1 = pg4_scale<T>(pg4_e4m3x2(b1 | b1 << 8, type));
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              const uint32_t a0[4] = {pg4_pair<T, 0>(k0[w], s_0), pg4_pair<T, 0>(k1[w], s_1), pg4_pair<T, 1>(k0[w], s_0),
+                                      pg4_pair<T, 1>(k1[w], s_1)};
+              const uint32_t a1[4] = {pg4_pair<T, 2>(k0[w], s_0), pg4_pair<T, 2>(k1[w], s_1), pg4_pair<T, 3>(k0[w], s_0),
+                                      pg4_pair<T, 3>(k1[w], s_1)};
+#pragma unroll
+              for (int x = 0; x < NQ; ++x) {
+                mma(sc[x], a0, qb[x][2 * w][0], qb[x][2 * w][1], type);
+                mma(sc[x], a1, qb[x][2 * w + 1][0], qb[x][2 * w + 1][1], type);
+              }
+            }
+          }
+          // ---- weights: element e of sc is slot (e < 2 ? slot : slot + 2), query 2 quad + e % 2 ----
+          uint32_t pb[NQ][2];
+          float p[NQ][4];
+          bool high = false;
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (masked && key + slot + (e & 2) >= limit[x][e & 1]) sc[x][e] = -INFINITY;
+              p[x][e] = fmaf(sc[x][e], a.scale_log2, kBias - m[x][e & 1]);
+              high = high || !(p[x][e] <= kTop);
+            }
+          }
+          if (__any_sync(0xffffffffu, high)) {              // a reference is too low (or not there yet, or a score is NaN)
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float mx = fmaxf(sc[x][y], sc[x][y + 2]) * a.scale_log2;
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float m_new = fmaxf(m[x][y], mx), ref = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = m[x][y] == -INFINITY ? 0.f : pg_ex2(m[x][y] - ref);
+                m[x][y] = m_new;
+                l[x][y] *= alpha;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  o[x][i][y] *= alpha;
+                  o[x][i][y + 2] *= alpha;
+                }
+                p[x][y] = fmaf(sc[x][y], a.scale_log2, kBias - ref);
+                p[x][y + 2] = fmaf(sc[x][y + 2], a.scale_log2, kBias - ref);
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[x][e] = pg_ex2(p[x][e]);
+            l[x][0] += p[x][0] + p[x][2];
+            l[x][1] += p[x][1] + p[x][3];
+            pb[x][0] = transposed(pack_half(p[x][0], p[x][1]));
+            pb[x][1] = transposed(pack_half(p[x][2], p[x][3]));
+          }
+          // ---- O^T ----
+          // slots at or behind the row's end may hold anything (a scale of NaN included): their values become 0
+          uint32_t keep = 0xffffffffu;
+          if (key + 16 > len) {
+            const int left = len - key - 4 * quad;
+            keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+          }
+#pragma unroll
+          for (int x2 = 0; x2 < W; x2 += 2) {
+            uint32_t v[4];
+            ldsm_x4_t(base + v_off + 16 * ((x2 + l_piece) ^ l_turn), v);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t sb = lds_word(base + vs_off + (x2 + y) * ps) & keep;
+              const kvc_pg4_scale lo = pg4_scale<__half>(pg4_e4m3x2(sb, half_type)), hi = pg4_scale<__half>(pg4_e4m3x2(sb >> 16, half_type));
+              const uint32_t v0 = v[2 * y], v1 = v[2 * y + 1];
+              const uint32_t a0[4] = {pg4_pair<__half, 0>(v0, lo), pg4_pair<__half, 1>(v0, lo), pg4_pair<__half, 0>(v1, hi),
+                                      pg4_pair<__half, 1>(v1, hi)};
+              const uint32_t a1[4] = {pg4_pair<__half, 2>(v0, lo), pg4_pair<__half, 3>(v0, lo), pg4_pair<__half, 2>(v1, hi),
+                                      pg4_pair<__half, 3>(v1, hi)};
+#pragma unroll
+              for (int x = 0; x < NQ; ++x) {
+                mma(o[x][2 * (x2 + y)], a0, pb[x][0], pb[x][1], half_type);
+                mma(o[x][2 * (x2 + y) + 1], a1, pb[x][0], pb[x][1], half_type);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[st]);          // this warp is done with the stage
+      }
+      t = t_end;
+
+      // ---- the item's end ----
+      if (!ok) sm.fail[1] = 1;
+      const kvc_pg_end e = sm.end[b];
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], w);
+          const int r = 8 * x + 2 * quad + y;
+          if (r >= e.rows) continue;
+          // unit g of a piece holds dims 8 (g / 2) + g % 2 + 2 i, its codes i = 0 .. 3
+          float* dst = &sm.acc[warp][r][8 * (g >> 1) + (g & 1)];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            dst[32 * (i >> 1) + 4 * (i & 1)] = o[x][i][y];
+            dst[32 * (i >> 1) + 4 * (i & 1) + 2] = o[x][i][y + 2];
+          }
+          if (g == 0) sm.ml[warp][r] = make_float2(m[x][y] - kBias, l[x][y]);
+        }
+      }
+      bar();
+      if (sm.fail[1]) break;
+      pg_finish<T, D, R>(
+          a, e, out, &sm.flag, threadIdx.x, kWarps * 32, false,
+          [&](int r, int d, float* Mp, float* Lp) {
+            float2 ml[kWarps];
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              ml[w] = sm.ml[w][r];
+              M = fmaxf(M, ml[w].x);
+            }
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+              const float wt = pg_weight(ml[w].x, M);
+              L = fmaf(wt, ml[w].y, L);
+              pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
+            }
+            *Mp = M;
+            *Lp = L;
+            return x;
+          },
+          [](int, int, float2*, float4*) {}, [&](int r) { return sm.at[b][r]; }, bar);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[b]);
+    }
+    if (threadIdx.x == 0 && wc->abort) atomicOr(a.err, KVC_DEV_TIMEOUT);
+  }
+}
+
+template <typename T, int D, int R>
+constexpr size_t kSmemBytes = 128 + ((sizeof(Smem<T, D, R>) + 15) & ~(size_t)15);
+
+template <typename T, int D, int R>
+cudaError_t launch(const kvc_paged4* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s, bool prepare) {
+  static_assert(kSmemBytes<T, D, R> + (4 * KVC_PG_MAX_BATCH + 1) * 4 + 16 <= 232448,
+                "shared memory above the 227 KB a block may opt into");
+  if (prepare)
+    return cudaFuncSetAttribute(k_paged4_decode<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(kSmemBytes<T, D, R> + pg_sched_bytes(KVC_PG_MAX_BATCH)));
+  return kvc_launch_pdl(k_paged4_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s,
+                        (const uint8_t*)c->pages, (const T*)q, (T*)out, a);
+}
+
+template <typename T>
+cudaError_t launch_t(const kvc_paged4* c, const kvc_pg_args& a, const void* q, void* out, bool wide, cudaStream_t s, bool prepare) {
+  if (c->cfg.head_dim == 64)
+    return wide ? launch<T, 64, 16>(c, a, q, out, s, prepare) : launch<T, 64, 8>(c, a, q, out, s, prepare);
+  return wide ? launch<T, 128, 16>(c, a, q, out, s, prepare) : launch<T, 128, 8>(c, a, q, out, s, prepare);
+}
+
+}  // namespace
+
+cudaError_t kvc_pg4_prepare_decode(const kvc_paged4* c) {
+  const kvc_pg_args a{};
+  for (int wide = 0; wide < 2; ++wide) {
+    const cudaError_t e = c->cfg.dtype == KVC_F16 ? launch_t<__half>(c, a, nullptr, nullptr, wide, 0, true)
+                                                  : launch_t<__nv_bfloat16>(c, a, nullptr, nullptr, wide, 0, true);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// (More than 16 rows to a group make several items of up to 16, each with a pass of its own over the keys.)
+cudaError_t kvc_pg4_launch_decode(const kvc_paged4* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s) {
+  const bool wide = (int64_t)a.max_q * a.Gv > 8;
+  return c->cfg.dtype == KVC_F16 ? launch_t<__half>(c, a, q, out, wide, s, false)
+                                 : launch_t<__nv_bfloat16>(c, a, q, out, wide, s, false);
+}

@@ -14,44 +14,15 @@ cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 int launched(cudaError_t e) { return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int check_cfg(const kvc_paged_config* g) {
-  if (g == nullptr) return KVC_ERR_ARG;
-  if (g->batch < 1 || g->heads < 1 || g->kv_heads < 1 || g->heads % g->kv_heads) return KVC_ERR_ARG;
-  if (g->dtype < KVC_F32 || g->dtype > KVC_BF16) return KVC_ERR_ARG;
-  if (g->n_pages < 1 || g->max_pages < 1 || g->max_tokens < 1) return KVC_ERR_ARG;
-  if (!(g->softmax_scale >= 0.f) || isinf(g->softmax_scale)) return KVC_ERR_ARG;
-  if (g->head_dim != 64 && g->head_dim != 128) return KVC_ERR_UNSUPPORTED;
-  if (g->page_size != 16 && g->page_size != 32 && g->page_size != 64 && g->page_size != 128) return KVC_ERR_UNSUPPORTED;
-  if (g->batch > KVC_PG_MAX_BATCH || g->heads > 4096) return KVC_ERR_UNSUPPORTED;
-  if ((int64_t)g->max_pages * g->page_size > (1 << 30)) return KVC_ERR_ARG;
-  return KVC_OK;
-}
-
-// A group of G query heads is taken as `sub` groups of at most 16.
-int sub_groups(int G) {
-  for (int sub = 1; sub < G; ++sub)
-    if (G % sub == 0 && G / sub <= 16) return sub;
-  return G;
-}
-
 // The handle's device has to be the current one: its streams and buffers belong to it.
-bool on_device(const kvc_paged* c) {
-  int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
-}
-
-int check_rows(const kvc_paged_config& g, int32_t n_tokens, const int32_t* d_cu) {
-  if (n_tokens < 1 || !aligned(d_cu, 4)) return KVC_ERR_ARG;
-  if (d_cu == nullptr && n_tokens % g.batch) return KVC_ERR_ARG;
-  return KVC_OK;
-}
+bool on_device(const kvc_paged* c) { return kvc_pg_on_device(c->device); }
 
 int check_attend(const kvc_paged* c, const void* q, const void* out, const float* lse, int32_t n_tokens,
                  const int32_t* d_cu, int32_t max_q, uint32_t flags) {
   if (c == nullptr || !q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return KVC_ERR_ARG;
   if (flags & ~(uint32_t)(KVC_CAUSAL | KVC_KERNEL_SIMT)) return KVC_ERR_ARG;
   if (d_cu != nullptr && max_q < 1) return KVC_ERR_ARG;
-  const int rc = check_rows(c->cfg, n_tokens, d_cu);
+  const int rc = kvc_pg_check_rows(c->cfg, n_tokens, d_cu);
   if (rc != KVC_OK) return rc;
   return on_device(c) ? KVC_OK : KVC_ERR_ARG;
 }
@@ -104,7 +75,7 @@ kvc_pg_args attend_args(const kvc_paged* c, float* lse, int32_t n_tokens, const 
 kvc_pg_layout kvc_pg_workspace(const kvc_paged_config& g) {
   kvc_pg_layout w{};
   const size_t D2 = (size_t)g.head_dim + 2;
-  const int sub = sub_groups(g.heads / g.kv_heads);
+  const int sub = kvc_pg_sub_groups(g.heads / g.kv_heads);
   const size_t Gv = (size_t)g.heads / g.kv_heads / sub, Hv = (size_t)g.kv_heads * sub;
   w.tickets = 256;
   w.warp_tickets = w.tickets + 4 * (size_t)KVC_PG_GRID_SIMT;
@@ -157,12 +128,54 @@ kvc_pg_args kvc_pg_base_args(const kvc_paged* c) {
   return a;
 }
 
+int kvc_pg_check_config(const kvc_paged_config* g) {
+  if (g == nullptr) return KVC_ERR_ARG;
+  if (g->batch < 1 || g->heads < 1 || g->kv_heads < 1 || g->heads % g->kv_heads) return KVC_ERR_ARG;
+  if (g->dtype < KVC_F32 || g->dtype > KVC_BF16) return KVC_ERR_ARG;
+  if (g->n_pages < 1 || g->max_pages < 1 || g->max_tokens < 1) return KVC_ERR_ARG;
+  if (!(g->softmax_scale >= 0.f) || isinf(g->softmax_scale)) return KVC_ERR_ARG;
+  if (g->head_dim != 64 && g->head_dim != 128) return KVC_ERR_UNSUPPORTED;
+  if (g->page_size != 16 && g->page_size != 32 && g->page_size != 64 && g->page_size != 128) return KVC_ERR_UNSUPPORTED;
+  if (g->batch > KVC_PG_MAX_BATCH || g->heads > 4096) return KVC_ERR_UNSUPPORTED;
+  if ((int64_t)g->max_pages * g->page_size > (1 << 30)) return KVC_ERR_ARG;
+  return KVC_OK;
+}
+
+int kvc_pg_sub_groups(int G) {
+  for (int sub = 1; sub < G; ++sub)
+    if (G % sub == 0 && G / sub <= 16) return sub;
+  return G;
+}
+
+bool kvc_pg_on_device(int device) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == device;
+}
+
+int kvc_pg_check_rows(const kvc_paged_config& g, int32_t n_tokens, const int32_t* d_cu) {
+  if (n_tokens < 1 || !aligned(d_cu, 4)) return KVC_ERR_ARG;
+  if (d_cu == nullptr && n_tokens % g.batch) return KVC_ERR_ARG;
+  return KVC_OK;
+}
+
+int kvc_pg_get_error(int32_t* word, size_t counters, cudaStream_t s, int32_t* bits) {
+  int32_t x = 0;
+  if (cudaMemcpyAsync(&x, word, sizeof(x), cudaMemcpyDeviceToHost, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    return KVC_ERR_CUDA;
+  if (bits != nullptr) *bits = x;
+  if (x == 0) return KVC_OK;
+  // a kernel that gave up may have left counters off zero
+  const size_t n = (x & KVC_DEV_TIMEOUT) ? counters : sizeof(int32_t);
+  if (cudaMemsetAsync(word, 0, n, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) return KVC_ERR_CUDA;
+  return KVC_ERR_DEVICE;
+}
+
 int kvc_pg_check_append(const kvc_paged_config& g, const void* k, const void* v, int64_t kv_stride, const void* q,
                         int64_t q_stride, const void* q_out, int32_t n_tokens, const int32_t* d_cu, const float* d_rope,
                         int32_t rope_positions, uint32_t flags) {
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return KVC_ERR_ARG;
   if (flags & ~(uint32_t)KVC_ROPE_HALF) return KVC_ERR_ARG;
-  const int rc = check_rows(g, n_tokens, d_cu);
+  const int rc = kvc_pg_check_rows(g, n_tokens, d_cu);
   if (rc != KVC_OK) return rc;
   const int64_t vec = g.dtype == KVC_F32 ? 4 : 8;      // elements of 16 bytes
   const int64_t kv_row = (int64_t)g.kv_heads * g.head_dim, q_row = (int64_t)g.heads * g.head_dim;
@@ -187,14 +200,14 @@ int kvc_pg_check_axes(const kvc_paged_config& g, const float* d_rope, const kvc_
 extern "C" {
 
 size_t kvc_paged_workspace_bytes(const kvc_paged_config* cfg) {
-  return check_cfg(cfg) == KVC_OK ? kvc_pg_workspace(*cfg).total : 0;
+  return kvc_pg_check_config(cfg) == KVC_OK ? kvc_pg_workspace(*cfg).total : 0;
 }
 
 int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, void* bounds, const int32_t* d_table,
                      const int32_t* d_kv_len, void* workspace, void* stream, kvc_paged** out) {
   if (out == nullptr) return KVC_ERR_ARG;
   *out = nullptr;
-  const int rc = check_cfg(cfg);
+  const int rc = kvc_pg_check_config(cfg);
   if (rc != KVC_OK) return rc;
   if (!k_pages || !v_pages || !d_table || !d_kv_len || !workspace) return KVC_ERR_ARG;
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(bounds, 16) || !aligned(workspace, 256)) return KVC_ERR_ARG;
@@ -204,7 +217,7 @@ int kvc_paged_create(const kvc_paged_config* cfg, void* k_pages, void* v_pages, 
   c->cfg = *cfg;
   c->ps_log2 = cfg->page_size == 16 ? 4 : cfg->page_size == 32 ? 5 : cfg->page_size == 64 ? 6 : 7;
   const int G = cfg->heads / cfg->kv_heads;
-  c->sub = sub_groups(G);
+  c->sub = kvc_pg_sub_groups(G);
   c->Gv = G / c->sub;
   c->Hv = cfg->kv_heads * c->sub;
   c->scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / sqrtf((float)cfg->head_dim);
@@ -315,17 +328,7 @@ int kvc_paged_attend_sparse(kvc_paged* c, const void* q, void* out, float* d_lse
 
 int kvc_paged_get_error(kvc_paged* c, void* stream, int32_t* bits) {
   if (c == nullptr || !on_device(c)) return KVC_ERR_ARG;
-  cudaStream_t s = as_stream(stream);
-  int32_t word = 0;
-  if (cudaMemcpyAsync(&word, c->ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return KVC_ERR_CUDA;
-  if (bits != nullptr) *bits = word;
-  if (word == 0) return KVC_OK;
-  // a kernel that gave up may have left counters off zero
-  const size_t n = (word & KVC_DEV_TIMEOUT) ? kvc_pg_workspace(c->cfg).zeroed : sizeof(int32_t);
-  if (cudaMemsetAsync(c->ws, 0, n, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) return KVC_ERR_CUDA;
-  return KVC_ERR_DEVICE;
+  return kvc_pg_get_error(reinterpret_cast<int32_t*>(c->ws), kvc_pg_workspace(c->cfg).zeroed, as_stream(stream), bits);
 }
 
 int kvc_paged_debug_stall_waits(kvc_paged* c, uint64_t ns) {

@@ -79,7 +79,15 @@ struct kvc_pg_args {
 
 kvc_pg_args kvc_pg_base_args(const kvc_paged* c);
 
-// Argument checks of an append (KVC_OK, or what the call returns).
+// ---- the host's part that paged stores of 16, 32 and 4 bits share ----
+// Checks return KVC_OK, or what the call returns.
+int kvc_pg_check_config(const kvc_paged_config* g);
+int kvc_pg_check_rows(const kvc_paged_config& g, int32_t n_tokens, const int32_t* d_cu);
+int kvc_pg_sub_groups(int G);     // a group of G query heads is taken as so many groups of at most 16
+bool kvc_pg_on_device(int device);
+// Reports and clears the error word at `word`; after KVC_DEV_TIMEOUT the `counters` bytes from there on.
+int kvc_pg_get_error(int32_t* word, size_t counters, cudaStream_t s, int32_t* bits);
+// Arguments of an append.
 int kvc_pg_check_append(const kvc_paged_config& g, const void* k, const void* v, int64_t kv_stride, const void* q,
                         int64_t q_stride, const void* q_out, int32_t n_tokens, const int32_t* d_cu, const float* d_rope,
                         int32_t rope_positions, uint32_t flags);

@@ -26,7 +26,7 @@ __device__ __forceinline__ double pg_two_prod_diff(float a, float b, float c, fl
   return s;
 }
 
-__device__ __noinline__ float pg_rot_odd(float a, float b, float c, float d) {
+static __device__ __noinline__ float pg_rot_odd(float a, float b, float c, float d) {
   double rest;
   const double s = pg_two_prod_diff(a, b, c, d, &rest);
   const float t = __double2float_rz(s);
@@ -58,7 +58,7 @@ __device__ __forceinline__ float pg_rot(float a, float b, float c, float d, cons
                   pg_clear(r2, type);
   return ok ? r2 : pg_rot_odd(a, b, c, d);
 }
-__device__ __noinline__ float pg_rot_f32(float a, float b, float c, float d) {
+static __device__ __noinline__ float pg_rot_f32(float a, float b, float c, float d) {
   double rest;
   const double s = pg_two_prod_diff(a, b, c, d, &rest);
   const float f = __double2float_rn(s);
