@@ -4,9 +4,8 @@
 // Work goes to blocks as in the 16-bit streaming kernel (k_paged_decode.cu, paged_internal.h): a block takes one stretch
 // of the line of all rows' tiles, here of 128 slots, through a ring of shared-memory stages.  A page's slots of a head are
 // one record, so a tile arrives as one bulk copy per page.  Warps:
-//   0-7  consumers: 16 slots of each tile
-//   8,10 producers: page numbers, copies (every other record each)
-//   9    helper: the next items' queries and extents
+//   0-7, for up to 8 query rows 8-15 too: consumers, 16 slots of a tile each, two sets of eight in turn
+//   the last three: producers (page numbers, copies, every other record each) and between them a helper: the next items' queries and extents
 //
 // At a quarter of the 16-bit store's bytes a slot, instructions bound this kernel as much as HBM does, so the slots stand in M
 // of the m16n8k16 MMAs and the up to 8 (16: two MMAs) query rows in N: an MMA takes 16 slots x 16 dims of codes, twice what it
@@ -17,7 +16,11 @@
 //                 a slot, and leaves a lane one unit of two slots in the halves of a register, so masking the
 //                 ith code of both gives such a pair; which dims share an MMA's rows does not matter.
 //                 B is P^T: S^T's accumulators, packed, through movmatrix.
-// Two codes become two values by a shift, a mask-and-or and one multiply-add (paged4_internal.h).
+// Two codes become two values by half a shift, a mask-and-or and one multiply-add (paged4_internal.h), as fp16 whichever the
+// 16-bit type; the values are halves, and the scores' scale and the weights' reference make up for it.  Queries of bf16 are
+// taken as fp16 too, each times a power of 2 that brings its largest element to 2^14 .. 2^15: its elements are exact down to
+// 2^-28 of that, and below it off by 2^-40 of it at most; held magnitudes span less than 2^21, so a score is off by less
+// than 2^-19 of the sum of its terms' magnitudes, as an fp32 sum of so many terms may be.
 // The running maximum of a query is looked for only when a weight outgrows its reference by 2^7 (one vote per tile);
 // weights are taken 2^8 too large, so that fp16 holds them with full precision down to 2^-22 of the reference, and
 // rounded to fp16 once for the product with V (their sum takes them unrounded).
@@ -25,26 +28,30 @@
 #include "paged_finish.h"
 #include "paged_ptx.h"
 
+#include <type_traits>
+
 namespace {
 
 using namespace pg;
 
-constexpr int kWarps = 8;                         // consumer warps
-constexpr int kThreads = (kWarps + 3) * 32;       // + producer, helper, producer
-constexpr int kTile = 16 * kWarps;                // slots per tile: 16 for each warp
+constexpr int kTile = 128;                        // slots per tile: 16 for each warp of a set
+template <int R> constexpr int kSets = R == 8 ? 2 : 1;                 // of consumers, which take tiles in turn
+template <int R> constexpr int kWarps = 8 * kSets<R>;                  // consumer warps
+template <int R> constexpr int kThreads = (kWarps<R> + 3) * 32;        // + producer, helper, producer
 constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
 constexpr int kMinTiles = 4, kItemCost = 2;       // fewest tiles for a block; an item's beginning and end, in tiles
 constexpr float kBias = 8.f, kTop = 15.f;         // log2 of a weight at its reference, and of the largest taken
 
 template <int D> constexpr uint32_t kStageBytes = kTile * (D + D / 16);
-template <int D, int R> constexpr int kStages = D == 128 ? (R == 8 ? 8 : 6) : 12;
+template <int D, int R> constexpr int kStages = D == 128 ? 6 : 14;     // even: a stage belongs to one set
 
 template <typename T, int D, int R>
 struct Smem {
   uint8_t stage[kStages<D, R>][kStageBytes<D>];   // 128-byte aligned
-  float acc[kWarps][R][D + kPad];
-  T q[2][R][D + 8];                               // an item's queries (+ 8: rows on different banks)
-  float2 ml[kWarps][R];
+  float acc[kWarps<R>][R][D + kPad];
+  __half q[2][R][D + 8];                          // an item's queries (+ 8: rows on different banks)
+  float q_scale[2][R];                            // of their scores, to log2 units
+  float2 ml[kWarps<R>][R];
   int64_t at[2][R];                               // rows of the outputs
   int limit[2][R];                                // where each query row's keys end
   kvc_pg_end end[2];
@@ -75,14 +82,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 // d += A B, A 16 x 16 (rows lane / 4 in a0, a2; rows lane / 4 + 8 in a1, a3), B 16 x 8
-__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const __half*) {
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1, const __nv_bfloat16*) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -91,6 +92,27 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// A query row's 8 elements, VQ lanes to a row, as fp16 times a power of 2; returns what undoes it.
+template <typename T, int VQ>
+__device__ __forceinline__ float as_half(uint4& v) {
+  if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+#pragma unroll
+    for (int o = 1; o < VQ; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // exponents of the factors: 14 - e and e - 14 for a top of 2^e .. 2^(e + 1), within fp32's range
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    const int up = e == 128 ? 0 : min(max(14 - e, -120), 120);            // (a row with an infinity or a NaN stays one)
+    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = pack_half(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+    return __uint_as_float((uint32_t)(127 - up) << 23);
+  }
+  return 1.f;
 }
 // D / 32 words of codes at a shared address (16 or 8 bytes).
 template <int W>
@@ -112,14 +134,13 @@ __device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
 }
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<R>, 1)
 k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_args a) {
+  constexpr int kW = kWarps<R>;        // consumer warps
   constexpr int W = D / 32;            // words of a slot's codes to a lane; pieces of 32 dims
   constexpr int MT = D / 16;           // 16-dim tiles of O^T
   constexpr int NQ = R / 8;            // 8-query tiles
   constexpr int S = kStages<D, R>;
-  const T* type = nullptr;
-  const __half* half_type = nullptr;
   extern __shared__ uint8_t raw[];
   using Sm = Smem<T, D, R>;
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
@@ -129,11 +150,11 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
     mbar_init(&sm.full[threadIdx.x], 64);            // both producers' lanes
-    mbar_init(&sm.empty[threadIdx.x], kWarps);
+    mbar_init(&sm.empty[threadIdx.x], 8);             // a set's warps
   }
   if (threadIdx.x >= 32 && threadIdx.x < 34) {
     mbar_init(&sm.q_full[threadIdx.x - 32], 32);
-    mbar_init(&sm.item_empty[threadIdx.x - 32], kWarps);
+    mbar_init(&sm.item_empty[threadIdx.x - 32], kW);
   }
   if (threadIdx.x == 64) {
     wait_init(&sm.wc, a.stall_ns);
@@ -147,13 +168,13 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, kMinTiles, kItemCost, gridDim.x);
   kvc_pg_item it;
   bool more = false;
-  if (warp >= kWarps) more = sch.first(a, blockIdx.x, it);
+  if (warp >= kW) more = sch.first(a, blockIdx.x, it);
   const int ps = 1 << a.ps_log2;
   const uint32_t record = (uint32_t)kvc_pg4_record(D, a.ps_log2);
 
-  if (warp == kWarps || warp == kWarps + 2) {
+  if (warp == kW || warp == kW + 2) {
     // ---------------- producers: records of a tile, every other one each ----------------
-    const int me = warp == kWarps ? 0 : 1;
+    const int me = warp == kW ? 0 : 1;
     const int per_tile = kTile >> a.ps_log2;                // 1, 2, 4 or 8
     // lane i < per_tile: the page number of the tile's ith record, not looked at before it is used (a tile later); -1: not
     // this producer's, or behind the row's end (where -1 is found in a table, it is a bad page)
@@ -197,7 +218,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     if (lane == 0) {   // every load issued here lands before the block releases its shared memory, consumers that gave up or not
       for (int i = max(0, t - S); i < t; ++i) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
     }
-  } else if (warp == kWarps + 1) {
+  } else if (warp == kW + 1) {
     // ---------------- helper: queries of the items to come ----------------
     constexpr int VQ = D / 8;                               // 16-byte vectors of a query row
     for (int n = 0;; ++n) {
@@ -239,7 +260,9 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
 #pragma unroll
       for (int x = 0; x < NL; ++x) {
         const int v = lane + 32 * x;
+        const float f = as_half<T, VQ>(qv[x]);
         *reinterpret_cast<uint4*>(&sm.q[b][v / VQ][8 * (v % VQ)]) = qv[x];
+        if (v % VQ == 0) sm.q_scale[b][v / VQ] = 2.f * f * a.scale_log2;
       }
       mbar_arrive(&sm.q_full[b]);
       more = sch.next(a, it);
@@ -250,7 +273,8 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     // Row r of S^T's first eight rows is slot 4 (r / 2) + r % 2 of the warp's sixteen, row r + 8 the slot two behind it, so that
     // a lane's four slots of P^T and V^T are neighbours (one 4-byte load of their scales).
     const int slot = 4 * (g >> 1) + (g & 1);
-    const int r0 = warp * 16;                               // the warp's slots within a tile
+    const int set = warp >> 3;                              // takes every other tile, where there are two
+    const int r0 = (warp & 7) * 16;                         // the warp's slots within a tile
     const int rec_i = r0 >> a.ps_log2, s0 = r0 & (ps - 1);   // their record, and where they begin in it
     const uint32_t k_off = rec_i * record + (s0 + slot) * (D / 2) + quad * (D / 8);
     const uint32_t ks_off = rec_i * record + ps * D + (s0 + slot) * W + (W == 4 ? quad : quad >> 1);
@@ -259,8 +283,10 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     const int lr = lane & 7, l_slot = 4 * (lr >> 1) + (lr & 1) + 2 * (lane >> 3 & 1), l_piece = lane >> 4;
     const uint32_t v_off = rec_i * record + (ps + s0 + l_slot) * (D / 2);
     const int l_turn = (l_slot >> 2) & (W - 1);
-    auto bar = [] { named_bar<1>(kWarps * 32); };
+    auto bar = [] { named_bar<1>(kW * 32); };
     int t = 0;                                              // tiles of this block before the item's
+    int u = set, st = set;                                  // this warp's next tile and its stage,
+    uint32_t phase = 0;                                     // whose barrier's phase it is
     for (int n = 0;; ++n) {
       const int b = n & 1;
       bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / 2) & 1, wc));
@@ -270,7 +296,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
       const int tiles = sm.tiles[b];
       if (tiles < 0) break;
       uint32_t qb[NQ][2 * W][2];                            // B operands: query 8 x + g, this lane's dims
-      int limit[NQ][2];
+      float qs[NQ][2];                                      // scales of queries 8 x + 2 quad + {0, 1}
 #pragma unroll
       for (int x = 0; x < NQ; ++x) {
 #pragma unroll
@@ -279,53 +305,78 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
           qb[x][kk][0] = v.x;
           qb[x][kk][1] = v.y;
         }
-        limit[x][0] = sm.limit[b][8 * x + 2 * quad];
-        limit[x][1] = sm.limit[b][8 * x + 2 * quad + 1];
+        qs[x][0] = sm.q_scale[b][8 * x + 2 * quad];
+        qs[x][1] = sm.q_scale[b][8 * x + 2 * quad + 1];
       }
       const int len = sm.len[b], open = sm.open[b];
-      int key = sm.key0[b] + r0;                            // position of the warp's first slot
+      const int t_end = t + tiles;
+      int key = sm.key0[b] + r0 + (u - t) * kTile;          // position of the warp's first slot
       float o[NQ][MT][4];
-      float m[NQ][2], l[NQ][2];                             // references, sums of this lane's slots
+      float nm[NQ][2], l[NQ][2];                            // kBias less the references, sums of this lane's slots
 #pragma unroll
       for (int x = 0; x < NQ; ++x) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
-        m[x][0] = m[x][1] = -INFINITY;
+        nm[x][0] = nm[x][1] = INFINITY;
         l[x][0] = l[x][1] = 0.f;
       }
-      const int t_end = t + tiles;
-      for (int u = t; u < t_end; ++u, key += kTile) {
-        const int st = u % S;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (u / S) & 1, wc));
+      for (; u < t_end; u += kSets<R>, key += kSets<R> * kTile) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], phase, wc));
         if (!ok) break;
         const uint32_t base = smem_u32(sm.stage[st]);
         const uint32_t gone = (sm.bad[0][st] | sm.bad[1][st]) >> rec_i & 1;
         if (key < len && !gone) {
-          const bool masked = key + 16 > open;
-          // ---- S^T ----
-          float sc[NQ][4];
+          // all loads first: nothing of V waits for the weights but its products
+          uint32_t k0[W], k1[W], v[2 * W], vs[W];
+          lds_words<W>(base + k_off, k0);
+          lds_words<W>(base + k_off + 2 * (D / 2), k1);
+          const uint32_t b0 = lds_byte(base + ks_off), b1 = lds_byte(base + ks_off + 2 * W);
 #pragma unroll
-          for (int x = 0; x < NQ; ++x) sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+          for (int x = 0; x < W; x += 2) ldsm_x4_t(base + v_off + 16 * ((x + l_piece) ^ l_turn), v + 2 * x);
+#pragma unroll
+          for (int x = 0; x < W; ++x) vs[x] = lds_word(base + vs_off + x * ps);
+          // ---- S^T (two sums, so that half as many products wait for one another) ----
+          float sc[NQ][4];
           {
-            uint32_t k0[W], k1[W];
-            lds_words<W>(base + k_off, k0);
-            lds_words<W>(base + k_off + 2 * (D / 2), k1);
-            const uint32_t b0 = lds_byte(base + ks_off), b1 = lds_byte(base + ks_off + 2 * W);
-            const kvc_pg4_scale s_0 = pg4_scale<T>(pg4_e4m3x2(b0 | b0 << 8, type)), s_1 = pg4_scale<T>(pg4_e4m3x2(b1 | b1 << 8, type));
+            float s2[NQ][4];
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+              sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
+              s2[x][0] = s2[x][1] = s2[x][2] = s2[x][3] = 0.f;
+            }
+            const kvc_pg4_half_scale s_0 = pg4_half_scale(b0 * 0x101u), s_1 = pg4_half_scale(b1 * 0x101u);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-              const uint32_t a0[4] = {pg4_pair<T, 0>(k0[w], s_0), pg4_pair<T, 0>(k1[w], s_1), pg4_pair<T, 1>(k0[w], s_0),
-                                      pg4_pair<T, 1>(k1[w], s_1)};
-              const uint32_t a1[4] = {pg4_pair<T, 2>(k0[w], s_0), pg4_pair<T, 2>(k1[w], s_1), pg4_pair<T, 3>(k0[w], s_0),
-                                      pg4_pair<T, 3>(k1[w], s_1)};
+              uint32_t x0[4], x1[4];
+              pg4_half_pairs(k0[w], s_0, x0);
+              pg4_half_pairs(k1[w], s_1, x1);
+              const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
 #pragma unroll
               for (int x = 0; x < NQ; ++x) {
-                mma(sc[x], a0, qb[x][2 * w][0], qb[x][2 * w][1], type);
-                mma(sc[x], a1, qb[x][2 * w + 1][0], qb[x][2 * w + 1][1], type);
+                mma(sc[x], a0, qb[x][2 * w][0], qb[x][2 * w][1]);
+                mma(s2[x], a1, qb[x][2 * w + 1][0], qb[x][2 * w + 1][1]);
               }
+            }
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[x][e] += s2[x][e];
             }
           }
           // ---- weights: element e of sc is slot (e < 2 ? slot : slot + 2), query 2 quad + e % 2 ----
+          if (key + 16 > open) {                            // some query row does not see all of these slots
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key + slot + (e & 2) >= sm.limit[b][8 * x + 2 * quad + (e & 1)]) sc[x][e] = -INFINITY;
+            }
+            // slots at or behind the row's end may hold anything (a scale of NaN included): their values become 0
+            const int left = len - key - 4 * quad;
+            const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+#pragma unroll
+            for (int x = 0; x < W; ++x) vs[x] &= keep;
+          }
           uint32_t pb[NQ][2];
           float p[NQ][4];
           bool high = false;
@@ -333,8 +384,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
           for (int x = 0; x < NQ; ++x) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (masked && key + slot + (e & 2) >= limit[x][e & 1]) sc[x][e] = -INFINITY;
-              p[x][e] = fmaf(sc[x][e], a.scale_log2, kBias - m[x][e & 1]);
+              p[x][e] = fmaf(sc[x][e], qs[x][e & 1], nm[x][e & 1]);
               high = high || !(p[x][e] <= kTop);
             }
           }
@@ -343,21 +393,22 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
             for (int x = 0; x < NQ; ++x) {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                float mx = fmaxf(sc[x][y], sc[x][y + 2]) * a.scale_log2;
+                float mx = fmaxf(sc[x][y], sc[x][y + 2]) * qs[x][y];
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float m_new = fmaxf(m[x][y], mx), ref = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = m[x][y] == -INFINITY ? 0.f : pg_ex2(m[x][y] - ref);
-                m[x][y] = m_new;
+                const float nm_new = fminf(nm[x][y], kBias - mx);
+                const float alpha = nm[x][y] == INFINITY ? 0.f : pg_ex2(nm_new - nm[x][y]);
+                nm[x][y] = nm_new;
                 l[x][y] *= alpha;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                   o[x][i][y] *= alpha;
                   o[x][i][y + 2] *= alpha;
                 }
-                p[x][y] = fmaf(sc[x][y], a.scale_log2, kBias - ref);
-                p[x][y + 2] = fmaf(sc[x][y + 2], a.scale_log2, kBias - ref);
+                const float off = nm_new == INFINITY ? 0.f : nm_new;     // (no slot seen so far: every score is -inf)
+                p[x][y] = fmaf(sc[x][y], qs[x][y], off);
+                p[x][y + 2] = fmaf(sc[x][y + 2], qs[x][y], off);
               }
             }
           }
@@ -371,35 +422,26 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
             pb[x][1] = transposed(pack_half(p[x][2], p[x][3]));
           }
           // ---- O^T ----
-          // slots at or behind the row's end may hold anything (a scale of NaN included): their values become 0
-          uint32_t keep = 0xffffffffu;
-          if (key + 16 > len) {
-            const int left = len - key - 4 * quad;
-            keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-          }
 #pragma unroll
-          for (int x2 = 0; x2 < W; x2 += 2) {
-            uint32_t v[4];
-            ldsm_x4_t(base + v_off + 16 * ((x2 + l_piece) ^ l_turn), v);
+          for (int y = 0; y < W; ++y) {
+            uint32_t x0[4], x1[4];
+            pg4_half_pairs(v[2 * y], pg4_half_scale(vs[y]), x0);
+            pg4_half_pairs(v[2 * y + 1], pg4_half_scale(vs[y] >> 16), x1);
+            const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t sb = lds_word(base + vs_off + (x2 + y) * ps) & keep;
-              const kvc_pg4_scale lo = pg4_scale<__half>(pg4_e4m3x2(sb, half_type)), hi = pg4_scale<__half>(pg4_e4m3x2(sb >> 16, half_type));
-              const uint32_t v0 = v[2 * y], v1 = v[2 * y + 1];
-              const uint32_t a0[4] = {pg4_pair<__half, 0>(v0, lo), pg4_pair<__half, 1>(v0, lo), pg4_pair<__half, 0>(v1, hi),
-                                      pg4_pair<__half, 1>(v1, hi)};
-              const uint32_t a1[4] = {pg4_pair<__half, 2>(v0, lo), pg4_pair<__half, 3>(v0, lo), pg4_pair<__half, 2>(v1, hi),
-                                      pg4_pair<__half, 3>(v1, hi)};
-#pragma unroll
-              for (int x = 0; x < NQ; ++x) {
-                mma(o[x][2 * (x2 + y)], a0, pb[x][0], pb[x][1], half_type);
-                mma(o[x][2 * (x2 + y) + 1], a1, pb[x][0], pb[x][1], half_type);
-              }
+            for (int x = 0; x < NQ; ++x) {
+              mma(o[x][2 * y], a0, pb[x][0], pb[x][1]);
+              mma(o[x][2 * y + 1], a1, pb[x][0], pb[x][1]);
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[st]);          // this warp is done with the stage
+        st += kSets<R>;
+        if (st >= S) {
+          st -= S;
+          phase ^= 1;
+        }
       }
       t = t_end;
 
@@ -421,24 +463,25 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
             dst[32 * (i >> 1) + 4 * (i & 1)] = o[x][i][y];
             dst[32 * (i >> 1) + 4 * (i & 1) + 2] = o[x][i][y + 2];
           }
-          if (g == 0) sm.ml[warp][r] = make_float2(m[x][y] - kBias, l[x][y]);
+          // (O is over halves of values: the state is that of weights half as large)
+          if (g == 0) sm.ml[warp][r] = make_float2(1.f - nm[x][y], 0.5f * l[x][y]);
         }
       }
       bar();
       if (sm.fail[1]) break;
       pg_finish<T, D, R>(
-          a, e, out, &sm.flag, threadIdx.x, kWarps * 32, false,
+          a, e, out, &sm.flag, threadIdx.x, kW * 32, false,
           [&](int r, int d, float* Mp, float* Lp) {
-            float2 ml[kWarps];
+            float2 ml[kW];
             float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < kW; ++w) {
               ml[w] = sm.ml[w][r];
               M = fmaxf(M, ml[w].x);
             }
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < kW; ++w) {
               const float wt = pg_weight(ml[w].x, M);
               L = fmaf(wt, ml[w].y, L);
               pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
@@ -465,7 +508,7 @@ cudaError_t launch(const kvc_paged4* c, const kvc_pg_args& a, const void* q, voi
   if (prepare)
     return cudaFuncSetAttribute(k_paged4_decode<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(kSmemBytes<T, D, R> + pg_sched_bytes(KVC_PG_MAX_BATCH)));
-  return kvc_launch_pdl(k_paged4_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s,
+  return kvc_launch_pdl(k_paged4_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads<R>), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s,
                         (const uint8_t*)c->pages, (const T*)q, (T*)out, a);
 }
 
