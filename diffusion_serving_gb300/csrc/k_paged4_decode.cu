@@ -4,7 +4,7 @@
 // Work goes to blocks as in the 16-bit streaming kernel (k_paged_decode.cu, paged_internal.h): a block takes one stretch
 // of the line of all rows' tiles, here of 128 slots, through a ring of shared-memory stages.  A page's slots of a head are
 // one record, so a tile arrives as one bulk copy per page.  Warps:
-//   0-7, for up to 8 query rows 8-15 too: consumers, 16 slots of a tile each, two sets of eight in turn
+//   consumers: sets of four, which take tiles in turn, 32 slots of a tile to a warp; three sets for up to 8 query rows, else two
 //   the last three: producers (page numbers, copies, every other record each) and between them a helper: the next items' queries and extents
 //
 // At a quarter of the 16-bit store's bytes a slot, instructions bound this kernel as much as HBM does, so the slots stand in M
@@ -34,16 +34,16 @@ namespace {
 
 using namespace pg;
 
-constexpr int kTile = 128;                        // slots per tile: 16 for each warp of a set
-template <int R> constexpr int kSets = R == 8 ? 2 : 1;                 // of consumers, which take tiles in turn
-template <int R> constexpr int kWarps = 8 * kSets<R>;                  // consumer warps
+constexpr int kTile = 128;                        // slots per tile: 32 for each warp of a set
+template <int R> constexpr int kSets = R == 8 ? 3 : 2;                 // of four consumers, which take tiles in turn
+template <int R> constexpr int kWarps = 4 * kSets<R>;                  // consumer warps
 template <int R> constexpr int kThreads = (kWarps<R> + 3) * 32;        // + producer, helper, producer
 constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
 constexpr int kMinTiles = 4, kItemCost = 2;       // fewest tiles for a block; an item's beginning and end, in tiles
 constexpr float kBias = 8.f, kTop = 15.f;         // log2 of a weight at its reference, and of the largest taken
 
 template <int D> constexpr uint32_t kStageBytes = kTile * (D + D / 16);
-template <int D, int R> constexpr int kStages = D == 128 ? 6 : 14;     // even: a stage belongs to one set
+template <int D, int R> constexpr int kStages = D == 128 ? 6 : 12;     // a multiple of the sets: a stage belongs to one
 
 template <typename T, int D, int R>
 struct Smem {
@@ -150,7 +150,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
     mbar_init(&sm.full[threadIdx.x], 64);            // both producers' lanes
-    mbar_init(&sm.empty[threadIdx.x], 8);             // a set's warps
+    mbar_init(&sm.empty[threadIdx.x], 4);             // a set's warps
   }
   if (threadIdx.x >= 32 && threadIdx.x < 34) {
     mbar_init(&sm.q_full[threadIdx.x - 32], 32);
@@ -273,12 +273,15 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     // Row r of S^T's first eight rows is slot 4 (r / 2) + r % 2 of the warp's sixteen, row r + 8 the slot two behind it, so that
     // a lane's four slots of P^T and V^T are neighbours (one 4-byte load of their scales).
     const int slot = 4 * (g >> 1) + (g & 1);
-    const int set = warp >> 3;                              // takes every other tile, where there are two
-    const int r0 = (warp & 7) * 16;                         // the warp's slots within a tile
-    const int rec_i = r0 >> a.ps_log2, s0 = r0 & (ps - 1);   // their record, and where they begin in it
+    const int set = warp >> 2;
+    const int r0 = (warp & 3) * 32;                         // the warp's slots within a tile: two blocks of 16,
+    const int rec_i = r0 >> a.ps_log2, s0 = r0 & (ps - 1);  // the first one's record, and where it begins in it;
+    const bool split = ps == 16;                            // the second is the next record's, or lies behind it
+    const int rec_bit[2] = {rec_i, rec_i + split};
     const uint32_t k_off = rec_i * record + (s0 + slot) * (D / 2) + quad * (D / 8);
     const uint32_t ks_off = rec_i * record + ps * D + (s0 + slot) * W + (W == 4 ? quad : quad >> 1);
     const uint32_t vs_off = rec_i * record + ps * (D + W) + s0 + 4 * quad;
+    const uint32_t code_step = split ? record : 16 * (D / 2), ks_step = split ? record : 16 * W, vs_step = split ? record : 16;
     // ldmatrix: lanes 8 m .. address the rows of matrix m: slots of the first eight rows or the others, one of two pieces
     const int lr = lane & 7, l_slot = 4 * (lr >> 1) + (lr & 1) + 2 * (lane >> 3 & 1), l_piece = lane >> 4;
     const uint32_t v_off = rec_i * record + (ps + s0 + l_slot) * (D / 2);
@@ -324,68 +327,85 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], phase, wc));
         if (!ok) break;
         const uint32_t base = smem_u32(sm.stage[st]);
-        const uint32_t gone = (sm.bad[0][st] | sm.bad[1][st]) >> rec_i & 1;
-        if (key < len && !gone) {
-          // all loads first: nothing of V waits for the weights but its products
-          uint32_t k0[W], k1[W], v[2 * W], vs[W];
-          lds_words<W>(base + k_off, k0);
-          lds_words<W>(base + k_off + 2 * (D / 2), k1);
-          const uint32_t b0 = lds_byte(base + ks_off), b1 = lds_byte(base + ks_off + 2 * W);
-#pragma unroll
-          for (int x = 0; x < W; x += 2) ldsm_x4_t(base + v_off + 16 * ((x + l_piece) ^ l_turn), v + 2 * x);
-#pragma unroll
-          for (int x = 0; x < W; ++x) vs[x] = lds_word(base + vs_off + x * ps);
-          // ---- S^T (two sums, so that half as many products wait for one another) ----
-          float sc[NQ][4];
+        const uint32_t gone = sm.bad[0][st] | sm.bad[1][st];
+        if (key < len) {
+          // ---- S^T ----
+          float sc[2][NQ][4];
           {
-            float s2[NQ][4];
+            uint32_t k0[2][W], k1[2][W], b0[2], b1[2];
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-              sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.f;
-              s2[x][0] = s2[x][1] = s2[x][2] = s2[x][3] = 0.f;
+            for (int s = 0; s < 2; ++s) {
+              lds_words<W>(base + k_off + s * code_step, k0[s]);
+              lds_words<W>(base + k_off + 2 * (D / 2) + s * code_step, k1[s]);
+              b0[s] = lds_byte(base + ks_off + s * ks_step);
+              b1[s] = lds_byte(base + ks_off + 2 * W + s * ks_step);
             }
-            const kvc_pg4_half_scale s_0 = pg4_half_scale(b0 * 0x101u), s_1 = pg4_half_scale(b1 * 0x101u);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+              for (int x = 0; x < NQ; ++x) sc[s][x][0] = sc[s][x][1] = sc[s][x][2] = sc[s][x][3] = 0.f;
+            }
+            kvc_pg4_half_scale s_0[2], s_1[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              s_0[s] = pg4_half_scale(b0[s] * 0x101u);
+              s_1[s] = pg4_half_scale(b1[s] * 0x101u);
+            }
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-              uint32_t x0[4], x1[4];
-              pg4_half_pairs(k0[w], s_0, x0);
-              pg4_half_pairs(k1[w], s_1, x1);
-              const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
 #pragma unroll
-              for (int x = 0; x < NQ; ++x) {
-                mma(sc[x], a0, qb[x][2 * w][0], qb[x][2 * w][1]);
-                mma(s2[x], a1, qb[x][2 * w + 1][0], qb[x][2 * w + 1][1]);
+              for (int s = 0; s < 2; ++s) {
+                uint32_t x0[4], x1[4];
+                pg4_half_pairs(k0[s][w], s_0[s], x0);
+                pg4_half_pairs(k1[s][w], s_1[s], x1);
+                const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                  mma(sc[s][x], a0, qb[x][2 * w][0], qb[x][2 * w][1]);
+                  mma(sc[s][x], a1, qb[x][2 * w + 1][0], qb[x][2 * w + 1][1]);
+                }
               }
             }
+          }
+          uint32_t v[2][2 * W], vs[2][W];
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
+          for (int s = 0; s < 2; ++s) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sc[x][e] += s2[x][e];
+            for (int x = 0; x < W; x += 2) ldsm_x4_t(base + v_off + 16 * ((x + l_piece) ^ l_turn) + s * code_step, v[s] + 2 * x);
+#pragma unroll
+            for (int x = 0; x < W; ++x) vs[s][x] = lds_word(base + vs_off + x * ps + s * vs_step);
+          }
+          // ---- weights: element e of sc is slot (e < 2 ? slot : slot + 2) of a block, query 2 quad + e % 2 ----
+          if (key + 32 > open || gone) {                    // some query row does not see all of these slots
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const bool dead = gone >> rec_bit[s] & 1;
+              const int first = key + 16 * s;
+#pragma unroll
+              for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (dead || first + slot + (e & 2) >= sm.limit[b][8 * x + 2 * quad + (e & 1)]) sc[s][x][e] = -INFINITY;
+              }
+              // slots at or behind the row's end may hold anything (a scale of NaN included): their values become 0
+              const int left = dead ? 0 : len - first - 4 * quad;
+              const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+#pragma unroll
+              for (int x = 0; x < W; ++x) vs[s][x] &= keep;
             }
           }
-          // ---- weights: element e of sc is slot (e < 2 ? slot : slot + 2), query 2 quad + e % 2 ----
-          if (key + 16 > open) {                            // some query row does not see all of these slots
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (key + slot + (e & 2) >= sm.limit[b][8 * x + 2 * quad + (e & 1)]) sc[x][e] = -INFINITY;
-            }
-            // slots at or behind the row's end may hold anything (a scale of NaN included): their values become 0
-            const int left = len - key - 4 * quad;
-            const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-#pragma unroll
-            for (int x = 0; x < W; ++x) vs[x] &= keep;
-          }
-          uint32_t pb[NQ][2];
-          float p[NQ][4];
+          uint32_t pb[2][NQ][2];
+          float p[2][NQ][4];
           bool high = false;
 #pragma unroll
-          for (int x = 0; x < NQ; ++x) {
+          for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[x][e] = fmaf(sc[x][e], qs[x][e & 1], nm[x][e & 1]);
-              high = high || !(p[x][e] <= kTop);
+            for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                p[s][x][e] = fmaf(sc[s][x][e], qs[x][e & 1], nm[x][e & 1]);
+                high = high || !(p[s][x][e] <= kTop);
+              }
             }
           }
           if (__any_sync(0xffffffffu, high)) {              // a reference is too low (or not there yet, or a score is NaN)
@@ -393,7 +413,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
             for (int x = 0; x < NQ; ++x) {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                float mx = fmaxf(sc[x][y], sc[x][y + 2]) * qs[x][y];
+                float mx = fmaxf(fmaxf(sc[0][x][y], sc[0][x][y + 2]), fmaxf(sc[1][x][y], sc[1][x][y + 2])) * qs[x][y];
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -407,31 +427,40 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
                   o[x][i][y + 2] *= alpha;
                 }
                 const float off = nm_new == INFINITY ? 0.f : nm_new;     // (no slot seen so far: every score is -inf)
-                p[x][y] = fmaf(sc[x][y], qs[x][y], off);
-                p[x][y + 2] = fmaf(sc[x][y + 2], qs[x][y], off);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                  p[s][x][y] = fmaf(sc[s][x][y], qs[x][y], off);
+                  p[s][x][y + 2] = fmaf(sc[s][x][y + 2], qs[x][y], off);
+                }
               }
             }
           }
 #pragma unroll
-          for (int x = 0; x < NQ; ++x) {
+          for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[x][e] = pg_ex2(p[x][e]);
-            l[x][0] += p[x][0] + p[x][2];
-            l[x][1] += p[x][1] + p[x][3];
-            pb[x][0] = transposed(pack_half(p[x][0], p[x][1]));
-            pb[x][1] = transposed(pack_half(p[x][2], p[x][3]));
+            for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) p[s][x][e] = pg_ex2(p[s][x][e]);
+              l[x][0] += p[s][x][0] + p[s][x][2];
+              l[x][1] += p[s][x][1] + p[s][x][3];
+              pb[s][x][0] = transposed(pack_half(p[s][x][0], p[s][x][1]));
+              pb[s][x][1] = transposed(pack_half(p[s][x][2], p[s][x][3]));
+            }
           }
           // ---- O^T ----
 #pragma unroll
           for (int y = 0; y < W; ++y) {
-            uint32_t x0[4], x1[4];
-            pg4_half_pairs(v[2 * y], pg4_half_scale(vs[y]), x0);
-            pg4_half_pairs(v[2 * y + 1], pg4_half_scale(vs[y] >> 16), x1);
-            const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-              mma(o[x][2 * y], a0, pb[x][0], pb[x][1]);
-              mma(o[x][2 * y + 1], a1, pb[x][0], pb[x][1]);
+            for (int s = 0; s < 2; ++s) {
+              uint32_t x0[4], x1[4];
+              pg4_half_pairs(v[s][2 * y], pg4_half_scale(vs[s][y]), x0);
+              pg4_half_pairs(v[s][2 * y + 1], pg4_half_scale(vs[s][y] >> 16), x1);
+              const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
+#pragma unroll
+              for (int x = 0; x < NQ; ++x) {
+                mma(o[x][2 * y], a0, pb[s][x][0], pb[s][x][1]);
+                mma(o[x][2 * y + 1], a1, pb[s][x][0], pb[s][x][1]);
+              }
             }
           }
         }
