@@ -176,28 +176,34 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     // ---------------- producers: records of a tile, every other one each ----------------
     const int me = warp == kW ? 0 : 1;
     const int per_tile = kTile >> a.ps_log2;                // 1, 2, 4 or 8
-    // lane i < per_tile: the page number of the tile's ith record, not looked at before it is used (a tile later); -1: not
-    // this producer's, or behind the row's end (where -1 is found in a table, it is a bad page)
-    auto look = [&](const kvc_pg_item& w, int j) {
+    // A window: the page numbers of 32 records, one to a lane, from a tile's first on; not looked at before they are used,
+    // a window later (a tile's are gone in a third of the time that a load takes).  -1 behind the row's end (where -1 is found in a
+    // table, it is a bad page).
+    auto window = [&](const kvc_pg_item& w, int j) {
       const int key = j * kTile + (lane << a.ps_log2);
-      if (lane >= per_tile || (lane & 1) != me || key >= w.r.len) return -1;
-      return pg_ld(a.table + (int64_t)w.b * a.max_pages + (key >> a.ps_log2));
+      return key < w.r.len ? pg_ld(a.table + (int64_t)w.b * a.max_pages + (key >> a.ps_log2)) : -1;
     };
+    const int wide = 32 / per_tile;                         // tiles to a window
     int t = 0;
     bool ok = true;
-    int page = more ? look(it, it.tile0) : -1;
+    int ahead = more ? window(it, it.tile0) : -1;
     for (; ok && more;) {
       const int tile0 = it.tile0, tile1 = it.tile1;
       const int kvh = a.sub == 1 ? it.vh : it.vh / a.sub;
       kvc_pg_item nx = it;
       more = sch.next(a, nx);
-      for (int j = tile0; j < tile1; ++j, ++t) {
-        int npage = -1;                                     // the next tile's, in flight meanwhile
-        if (j + 1 < tile1) npage = look(it, j + 1);
-        else if (more) npage = look(nx, nx.tile0);
+      int pages = -1, at = wide;                            // this window, and the next tile's place in it
+      for (int j = tile0; j < tile1; ++j, ++t, ++at) {
+        if (at == wide) {
+          at = 0;
+          pages = ahead;
+          if (j + wide < tile1) ahead = window(it, j + wide);
+          else if (more) ahead = window(nx, nx.tile0);
+        }
         const int st = t % S;
         if (t >= S) ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[st], (t / S - 1) & 1, wc));
         if (!ok) break;
+        const int page = __shfl_sync(0xffffffffu, pages, at * per_tile + (lane & (per_tile - 1)));
         const bool there = lane < per_tile && (lane & 1) == me && j * kTile + (lane << a.ps_log2) < it.r.len;
         const bool fine = there && page >= 0 && page < a.n_pages;
         if (there && !fine) atomicOr(a.err, KVC_DEV_BAD_PAGE);
@@ -211,7 +217,6 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
           bulk_load(&sm.full[st], sm.stage[st] + lane * record, pool + ((int64_t)page * a.Hkv + kvh) * record, record);
         __syncwarp();
         if (lane != 0) mbar_arrive(&sm.full[st]);
-        page = npage;
       }
       it = nx;
     }
