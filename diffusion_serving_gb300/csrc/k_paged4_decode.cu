@@ -37,13 +37,14 @@ using namespace pg;
 constexpr int kTile = 128;                        // slots per tile: 32 for each warp of a set
 template <int R> constexpr int kSets = R == 8 ? 3 : 2;                 // of four consumers, which take tiles in turn
 template <int R> constexpr int kWarps = 4 * kSets<R>;                  // consumer warps
-template <int R> constexpr int kThreads = (kWarps<R> + 3) * 32;        // + producer, helper, producer
+constexpr int kProducers = 3;                     // producer warps, which take tiles in turn
+template <int R> constexpr int kThreads = (kWarps<R> + kProducers + 1) * 32;   // + helper
 constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
 constexpr int kMinTiles = 4, kItemCost = 2;       // fewest tiles for a block; an item's beginning and end, in tiles
 constexpr float kBias = 8.f, kTop = 15.f;         // log2 of a weight at its reference, and of the largest taken
 
 template <int D> constexpr uint32_t kStageBytes = kTile * (D + D / 16);
-template <int D, int R> constexpr int kStages = D == 128 ? 6 : 12;     // a multiple of the sets: a stage belongs to one
+template <int D, int R> constexpr int kStages = D == 128 ? 6 : 12;     // a multiple of sets and producers: a stage belongs to one of each
 
 template <typename T, int D, int R>
 struct Smem {
@@ -58,7 +59,7 @@ struct Smem {
   int tiles[2];                                   // this block's tiles of the item; -1: there is none
   int key0[2];                                    // position of the first one's first slot
   int len[2], open[2];                            // where the row's slots end; below this every query row sees all
-  uint32_t bad[2][kStages<D, R>];                 // records of a stage that no page stands behind, by producer
+  uint32_t bad[kStages<D, R>];                    // records of a stage that no page stands behind
   uint64_t full[kStages<D, R>], empty[kStages<D, R>];
   uint64_t q_full[2], item_empty[2];
   WaitCtl wc;
@@ -149,7 +150,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
 
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
-    mbar_init(&sm.full[threadIdx.x], 64);            // both producers' lanes
+    mbar_init(&sm.full[threadIdx.x], 1);             // its producer's first lane
     mbar_init(&sm.empty[threadIdx.x], 4);             // a set's warps
   }
   if (threadIdx.x >= 32 && threadIdx.x < 34) {
@@ -172,58 +173,63 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   const int ps = 1 << a.ps_log2;
   const uint32_t record = (uint32_t)kvc_pg4_record(D, a.ps_log2);
 
-  if (warp == kW || warp == kW + 2) {
-    // ---------------- producers: records of a tile, every other one each ----------------
-    const int me = warp == kW ? 0 : 1;
+  if (warp >= kW && warp < kW + kProducers) {
+    // ---------------- producers: a tile's records, one lane each ----------------
     const int per_tile = kTile >> a.ps_log2;                // 1, 2, 4 or 8
+    const int wide = 32 / per_tile;                         // tiles to a window
     // A window: the page numbers of 32 records, one to a lane, from a tile's first on; not looked at before they are used,
-    // a window later (a tile's are gone in a third of the time that a load takes).  -1 behind the row's end (where -1 is found in a
+    // a window later (tiles are gone sooner than a load is back).  -1 behind the row's end (where -1 is found in a
     // table, it is a bad page).
     auto window = [&](const kvc_pg_item& w, int j) {
       const int key = j * kTile + (lane << a.ps_log2);
       return key < w.r.len ? pg_ld(a.table + (int64_t)w.b * a.max_pages + (key >> a.ps_log2)) : -1;
     };
-    const int wide = 32 / per_tile;                         // tiles to a window
-    int t = 0;
+    int t = 0;                                              // tiles of this block before the item's
+    int u = warp - kW, st = u, round = 0;                   // this warp's next tile, its stage, rounds of the ring before it
     bool ok = true;
     int ahead = more ? window(it, it.tile0) : -1;
     for (; ok && more;) {
       const int tile0 = it.tile0, tile1 = it.tile1;
-      const int kvh = a.sub == 1 ? it.vh : it.vh / a.sub;
+      const uint8_t* heads = pool + (int64_t)(a.sub == 1 ? it.vh : it.vh / a.sub) * record;
       kvc_pg_item nx = it;
       more = sch.next(a, nx);
-      int pages = -1, at = wide;                            // this window, and the next tile's place in it
-      for (int j = tile0; j < tile1; ++j, ++t, ++at) {
-        if (at == wide) {
-          at = 0;
+      int pages = ahead, w0 = tile0;                        // the window at hand, and where it begins
+      auto look = [&] { return w0 + wide < tile1 ? window(it, w0 + wide) : more ? window(nx, nx.tile0) : -1; };
+      ahead = look();
+      int j = tile0 + u - t;
+      for (; j < tile1; j += kProducers, u += kProducers) {
+        if (j >= w0 + wide) {                               // (a window holds a tile of each producer at least)
+          w0 += wide;
           pages = ahead;
-          if (j + wide < tile1) ahead = window(it, j + wide);
-          else if (more) ahead = window(nx, nx.tile0);
+          ahead = look();
         }
-        const int st = t % S;
-        if (t >= S) ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[st], (t / S - 1) & 1, wc));
+        if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[st], (round - 1) & 1, wc));
         if (!ok) break;
-        const int page = __shfl_sync(0xffffffffu, pages, at * per_tile + (lane & (per_tile - 1)));
-        const bool there = lane < per_tile && (lane & 1) == me && j * kTile + (lane << a.ps_log2) < it.r.len;
+        const int page = __shfl_sync(0xffffffffu, pages, (j - w0) * per_tile + (lane & (per_tile - 1)));
+        const bool there = lane < per_tile && j * kTile + (lane << a.ps_log2) < it.r.len;
         const bool fine = there && page >= 0 && page < a.n_pages;
-        if (there && !fine) atomicOr(a.err, KVC_DEV_BAD_PAGE);
-        const unsigned good = __ballot_sync(0xffffffffu, fine), bad = __ballot_sync(0xffffffffu, there && !fine);
+        const unsigned want = __ballot_sync(0xffffffffu, there), good = __ballot_sync(0xffffffffu, fine);
         if (lane == 0) {
-          sm.bad[me][st] = bad;
+          if (want != good) atomicOr(a.err, KVC_DEV_BAD_PAGE);
+          sm.bad[st] = want ^ good;
           mbar_expect_tx(&sm.full[st], __popc(good) * record);
         }
         __syncwarp();
-        if (fine)
-          bulk_load(&sm.full[st], sm.stage[st] + lane * record, pool + ((int64_t)page * a.Hkv + kvh) * record, record);
-        __syncwarp();
-        if (lane != 0) mbar_arrive(&sm.full[st]);
+        if (fine) bulk_load(&sm.full[st], sm.stage[st] + lane * record, heads + (int64_t)page * a.Hkv * record, record);
+        st += kProducers;
+        if (st >= S) {
+          st -= S;
+          ++round;
+        }
       }
+      if (w0 + wide < tile1 && more) ahead = window(nx, nx.tile0);   // (the last window held no tile of this warp's)
+      t += tile1 - tile0;
       it = nx;
     }
     if (lane == 0) {   // every load issued here lands before the block releases its shared memory, consumers that gave up or not
-      for (int i = max(0, t - S); i < t; ++i) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
+      for (int i = u - kProducers; i >= 0 && i >= u - S; i -= kProducers) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
     }
-  } else if (warp == kW + 1) {
+  } else if (warp == kW + kProducers) {
     // ---------------- helper: queries of the items to come ----------------
     constexpr int VQ = D / 8;                               // 16-byte vectors of a query row
     for (int n = 0;; ++n) {
@@ -332,7 +338,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], phase, wc));
         if (!ok) break;
         const uint32_t base = smem_u32(sm.stage[st]);
-        const uint32_t gone = sm.bad[0][st] | sm.bad[1][st];
+        const uint32_t gone = sm.bad[st];
         if (key < len) {
           // ---- S^T ----
           float sc[2][NQ][4];
