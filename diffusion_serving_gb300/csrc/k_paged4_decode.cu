@@ -16,11 +16,12 @@
 //                 a slot, and leaves a lane one unit of two slots in the halves of a register, so masking the
 //                 ith code of both gives such a pair; which dims share an MMA's rows does not matter.
 //                 B is P^T: S^T's accumulators, packed, through movmatrix.
-// Two codes become two values by half a shift, a mask-and-or and one multiply-add (paged4_internal.h), as fp16 whichever the
-// 16-bit type; the values are halves, and the scores' scale and the weights' reference make up for it.  Queries of bf16 are
-// taken as fp16 too, each times a power of 2 that brings its largest element to 2^14 .. 2^15: its elements are exact down to
-// 2^-28 of that, and below it off by 2^-40 of it at most; held magnitudes span less than 2^21, so a score is off by less
-// than 2^-19 of the sum of its terms' magnitudes, as an fp32 sum of so many terms may be.
+// Two codes become two values by a quarter of a shift, a mask-and-or and one multiply-add (paged4_internal.h), as fp16 whichever
+// the 16-bit type; every other pair comes out 16 times too small, which its queries make up for, or the outputs (dims
+// are rows of O^T, and a row's pairs are of one kind).  Queries are taken as fp16, each times a power of 2 that brings its
+// largest element to 2^10 .. 2^11 (and 16 times that, where the keys are too small): elements are exact down to 2^-25 of the
+// largest, and below it off by 2^-36 of it at most; held magnitudes span less than 2^21, so a score is off by less than 2^-15
+// of the sum of its terms' magnitudes, at queries and keys made for it.
 // The running maximum of a query is looked for only when a weight outgrows its reference by 2^7 (one vote per tile);
 // weights are taken 2^8 too large, so that fp16 holds them with full precision down to 2^-22 of the reference, and
 // rounded to fp16 once for the product with V (their sum takes them unrounded).
@@ -94,26 +95,38 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// A query row's 8 elements, VQ lanes to a row, as fp16 times a power of 2; returns what undoes it.
+// A query row's 8 elements, VQ lanes to a row, as fp16 times a power of 2 (words 0 and 2: 16 times that); returns what undoes it.
+__device__ __forceinline__ float2 floats(uint32_t w, const __half*) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ float2 floats(uint32_t w, const __nv_bfloat16*) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 template <typename T, int VQ>
 __device__ __forceinline__ float as_half(uint4& v) {
-  if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-    float top = 0.f;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+  float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-#pragma unroll
-    for (int o = 1; o < VQ; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // exponents of the factors: 14 - e and e - 14 for a top of 2^e .. 2^(e + 1), within fp32's range
-    const int e = (int)(__float_as_uint(top) >> 23) - 127;
-    const int up = e == 128 ? 0 : min(max(14 - e, -120), 120);            // (a row with an infinity or a NaN stays one)
-    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = pack_half(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-    return __uint_as_float((uint32_t)(127 - up) << 23);
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = floats(w[i], (const T*)nullptr);
+    top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
   }
-  return 1.f;
+#pragma unroll
+  for (int o = 1; o < VQ; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;       // top is 2^e .. 2^(e + 1)
+  const int up = e == 128 ? 0 : min(10 - e, 120);              // (an infinity stays one; factors within fp32's range)
+  const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = floats(w[i], (const T*)nullptr);
+    const float y = i & 1 ? f : 16.f * f;
+    w[i] = pack_half(x.x * y, x.y * y);
+  }
+  return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+// (a NaN goes on)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // D / 32 words of codes at a shared address (16 or 8 bytes).
 template <int W>
@@ -136,7 +149,7 @@ __device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
 
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads<R>, 1)
-k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_args a) {
+k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_args a, uint32_t sixty_four) {
   constexpr int kW = kWarps<R>;        // consumer warps
   constexpr int W = D / 32;            // words of a slot's codes to a lane; pieces of 32 dims
   constexpr int MT = D / 16;           // 16-dim tiles of O^T
@@ -273,7 +286,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         const int v = lane + 32 * x;
         const float f = as_half<T, VQ>(qv[x]);
         *reinterpret_cast<uint4*>(&sm.q[b][v / VQ][8 * (v % VQ)]) = qv[x];
-        if (v % VQ == 0) sm.q_scale[b][v / VQ] = 2.f * f * a.scale_log2;
+        if (v % VQ == 0) sm.q_scale[b][v / VQ] = f * a.scale_log2;
       }
       mbar_arrive(&sm.q_full[b]);
       more = sch.next(a, it);
@@ -356,19 +369,19 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
 #pragma unroll
               for (int x = 0; x < NQ; ++x) sc[s][x][0] = sc[s][x][1] = sc[s][x][2] = sc[s][x][3] = 0.f;
             }
-            kvc_pg4_half_scale s_0[2], s_1[2];
+            kvc_pg4_fast_scale s_0[2], s_1[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              s_0[s] = pg4_half_scale(b0[s] * 0x101u);
-              s_1[s] = pg4_half_scale(b1[s] * 0x101u);
+              s_0[s] = pg4_fast_scale(b0[s] * 0x101u);
+              s_1[s] = pg4_fast_scale(b1[s] * 0x101u);
             }
 #pragma unroll
             for (int w = 0; w < W; ++w) {
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
                 uint32_t x0[4], x1[4];
-                pg4_half_pairs(k0[s][w], s_0[s], x0);
-                pg4_half_pairs(k1[s][w], s_1[s], x1);
+                pg4_fast_pairs(k0[s][w], s_0[s], sixty_four, x0);
+                pg4_fast_pairs(k1[s][w], s_1[s], sixty_four, x1);
                 const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]}, a1[4] = {x0[2], x1[2], x0[3], x1[3]};
 #pragma unroll
                 for (int x = 0; x < NQ; ++x) {
@@ -407,19 +420,18 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
           }
           uint32_t pb[2][NQ][2];
           float p[2][NQ][4];
-          bool high = false;
+          float top = -INFINITY;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                p[s][x][e] = fmaf(sc[s][x][e], qs[x][e & 1], nm[x][e & 1]);
-                high = high || !(p[s][x][e] <= kTop);
-              }
+              for (int e = 0; e < 4; ++e) p[s][x][e] = fmaf(sc[s][x][e], qs[x][e & 1], nm[x][e & 1]);
+              top = max3(top, p[s][x][0], p[s][x][1]);
+              top = max3(top, p[s][x][2], p[s][x][3]);
             }
           }
-          if (__any_sync(0xffffffffu, high)) {              // a reference is too low (or not there yet, or a score is NaN)
+          if (__any_sync(0xffffffffu, !(top <= kTop))) {              // a reference is too low (or not there yet, or a score is NaN)
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
 #pragma unroll
@@ -464,8 +476,8 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               uint32_t x0[4], x1[4];
-              pg4_half_pairs(v[s][2 * y], pg4_half_scale(vs[s][y]), x0);
-              pg4_half_pairs(v[s][2 * y + 1], pg4_half_scale(vs[s][y] >> 16), x1);
+              pg4_fast_pairs(v[s][2 * y], pg4_fast_scale(vs[s][y]), sixty_four, x0);
+              pg4_fast_pairs(v[s][2 * y + 1], pg4_fast_scale(vs[s][y] >> 16), sixty_four, x1);
               const uint32_t a0[4] = {x0[0], x0[1], x1[0], x1[1]}, a1[4] = {x0[2], x0[3], x1[2], x1[3]};
 #pragma unroll
               for (int x = 0; x < NQ; ++x) {
@@ -500,11 +512,10 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
           float* dst = &sm.acc[warp][r][8 * (g >> 1) + (g & 1)];
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            dst[32 * (i >> 1) + 4 * (i & 1)] = o[x][i][y];
+            dst[32 * (i >> 1) + 4 * (i & 1)] = 16.f * o[x][i][y];
             dst[32 * (i >> 1) + 4 * (i & 1) + 2] = o[x][i][y + 2];
           }
-          // (O is over halves of values: the state is that of weights half as large)
-          if (g == 0) sm.ml[warp][r] = make_float2(1.f - nm[x][y], 0.5f * l[x][y]);
+          if (g == 0) sm.ml[warp][r] = make_float2(-nm[x][y], l[x][y]);
         }
       }
       bar();
@@ -549,7 +560,7 @@ cudaError_t launch(const kvc_paged4* c, const kvc_pg_args& a, const void* q, voi
     return cudaFuncSetAttribute(k_paged4_decode<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(kSmemBytes<T, D, R> + pg_sched_bytes(KVC_PG_MAX_BATCH)));
   return kvc_launch_pdl(k_paged4_decode<T, D, R>, dim3(KVC_PG_GRID), dim3(kThreads<R>), kSmemBytes<T, D, R> + pg_sched_bytes(a.B), s,
-                        (const uint8_t*)c->pages, (const T*)q, (T*)out, a);
+                        (const uint8_t*)c->pages, (const T*)q, (T*)out, a, 0x54005400u);
 }
 
 template <typename T>

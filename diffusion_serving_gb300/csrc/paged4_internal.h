@@ -107,24 +107,26 @@ __device__ __forceinline__ uint32_t pg4_pair(uint32_t word, const kvc_pg4_scale&
   return pg4_fma(x, sc.s, sc.o, (const T*)nullptr);
 }
 
-// Halves of held values as pairs of fp16, (c - 8) s / 2, at fewer instructions: a word shifted left by 2 has codes 0 and 1
-// of each half in the mantissa's bits 2 .. 5 and 6 .. 9, one shifted right by 6 codes 2 and 3; under exponents of 128 and 8 they
-// read 128 + c / 2 and 8 + c / 2.  132 s and 12 s have 9 and 6 significant bits; 132 s is finite where 264 s would not be.
-struct kvc_pg4_half_scale {
-  uint32_t s, lo, hi;     // s, -132 s, -12 s
+// The same as fp16 at fewer instructions, up to a power of 2: codes 0 and 1 of each half stand in the mantissa's bits 0 .. 3 and
+// 4 .. 7 as they are, codes 2 and 3 once the word is shifted by 8; under an exponent of 64 they read 64 + c / 16 and 64 + c.
+// So pairs 0 and 2 come out as (c - 8) s / 16, pairs 1 and 3 as (c - 8) s, and whoever multiplies makes up for it.  64.5 s and
+// 72 s have 11 significant bits at most (129 times four bits; 9 times four), so all of it is exact.
+struct kvc_pg4_fast_scale {
+  uint32_t s, o0, o1;     // s, -64.5 s, -72 s
 };
-__device__ __forceinline__ kvc_pg4_half_scale pg4_half_scale(uint32_t two_e4m3) {
+__device__ __forceinline__ kvc_pg4_fast_scale pg4_fast_scale(uint32_t two_e4m3) {
   const __half* t = nullptr;
   const uint32_t s = pg4_e4m3x2(two_e4m3, t);
-  return {s, pg4_mul(s, 0xD820D820u, t), pg4_mul(s, 0xCA00CA00u, t)};
+  return {s, pg4_mul(s, 0xD408D408u, t), pg4_mul(s, 0xD480D480u, t)};
 }
-// The four pairs of a word: d[i] is dims 2 i and 2 i + 1 (of K), or the ith codes of the word's halves.
-__device__ __forceinline__ void pg4_half_pairs(uint32_t word, const kvc_pg4_half_scale& sc, uint32_t* d) {
+// `sixty_four`: 0x54005400 in a register (a constant known to the compiler would cost a second logic operation each: an
+// instruction takes one immediate).  d[i]: dims 2 i and 2 i + 1 (of K), or the ith codes of the word's halves.
+__device__ __forceinline__ void pg4_fast_pairs(uint32_t word, const kvc_pg4_fast_scale& sc, uint32_t sixty_four, uint32_t* d) {
   const __half* t = nullptr;
-  const uint32_t a = word << 2, b = word >> 6;
-  d[0] = pg4_fma((a & 0x003C003Cu) | 0x58005800u, sc.s, sc.lo, t);
-  d[1] = pg4_fma((a & 0x03C003C0u) | 0x48004800u, sc.s, sc.hi, t);
-  d[2] = pg4_fma((b & 0x003C003Cu) | 0x58005800u, sc.s, sc.lo, t);
-  d[3] = pg4_fma((b & 0x03C003C0u) | 0x48004800u, sc.s, sc.hi, t);
+  const uint32_t b = word >> 8;
+  d[0] = pg4_fma((word & 0x000F000Fu) | sixty_four, sc.s, sc.o0, t);
+  d[1] = pg4_fma((word & 0x00F000F0u) | sixty_four, sc.s, sc.o1, t);
+  d[2] = pg4_fma((b & 0x000F000Fu) | sixty_four, sc.s, sc.o0, t);
+  d[3] = pg4_fma((b & 0x00F000F0u) | sixty_four, sc.s, sc.o1, t);
 }
 #endif  // __CUDACC__
