@@ -144,8 +144,9 @@ k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, 
 // Eight held values.
 template <typename T>
 __device__ __forceinline__ uint4 unheld(uint32_t word, uint32_t bits) {
+  constexpr uint32_t base = kvc_pg4_type<T>::kBase;
   const kvc_pg4_scale sc = pg4_scale<T>(pg4_e4m3x2(bits | bits << 8, (const T*)nullptr));
-  return make_uint4(pg4_pair<T, 0>(word, sc), pg4_pair<T, 1>(word, sc), pg4_pair<T, 2>(word, sc), pg4_pair<T, 3>(word, sc));
+  return make_uint4(pg4_pair<T, 0>(word, sc, base), pg4_pair<T, 1>(word, sc, base), pg4_pair<T, 2>(word, sc, base), pg4_pair<T, 3>(word, sc, base));
 }
 __device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) {
   uint32_t x;

@@ -116,8 +116,8 @@ cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, 
   return c->cfg.head_dim == 64 ? launch_prefix<64>(a, R, TS, cost, grid, s) : launch_prefix<128>(a, R, TS, cost, grid, s);
 }
 
-cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, void* out, cudaStream_t s) {
-  const bool d64 = c->cfg.head_dim == 64;
-  if (c->cfg.dtype == KVC_F16) return d64 ? launch<__half, 64>(a, out, s) : launch<__half, 128>(a, out, s);
+cudaError_t kvc_pg_launch_join(const kvc_paged_config& g, const kvc_pg_args& a, void* out, cudaStream_t s) {
+  const bool d64 = g.head_dim == 64;
+  if (g.dtype == KVC_F16) return d64 ? launch<__half, 64>(a, out, s) : launch<__half, 128>(a, out, s);
   return d64 ? launch<__nv_bfloat16, 64>(a, out, s) : launch<__nv_bfloat16, 128>(a, out, s);
 }

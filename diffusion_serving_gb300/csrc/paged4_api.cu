@@ -23,12 +23,16 @@ int check_config(const kvc_paged_config* g) {
 kvc_pg4_layout workspace_of(const kvc_paged_config& g) {
   kvc_pg4_layout w{};
   w.tickets = 256;
-  w.zeroed = up256(w.tickets + 4 * (size_t)KVC_PG_GRID);
+  w.warp_tickets = w.tickets + 4 * (size_t)KVC_PG_GRID;
+  w.zeroed = up256(w.warp_tickets + 4 * 4 * (size_t)KVC_PG_GRID);
   w.parts = w.zeroed;
-  // two partials of 16 rows a block
-  w.total = up256(w.parts + 2 * (size_t)KVC_PG_GRID * 16 * (g.head_dim + 2) * 4);
+  // two partials a block
+  w.total = up256(w.parts + 2 * (size_t)KVC_PG_GRID * KVC_PG_TC_ROWS * (g.head_dim + 2) * 4);
   return w;
 }
+
+// Few query rows per group go to the streaming kernel, more to the tensor-core kernel.
+bool few_rows(const kvc_pg_args& a) { return (int64_t)a.max_q * a.Gv <= 16; }
 
 }  // namespace
 
@@ -64,7 +68,7 @@ int kvc_paged4_create(const kvc_paged_config* cfg, void* pages, const int32_t* d
   c->kv_len = d_kv_len;
   c->ws = reinterpret_cast<uint8_t*>(workspace);
   c->debug_stall_ns = 0;
-  if (cudaGetDevice(&c->device) != cudaSuccess || kvc_pg4_prepare_decode(c) != cudaSuccess ||
+  if (cudaGetDevice(&c->device) != cudaSuccess || kvc_pg4_prepare_decode(c) != cudaSuccess || kvc_pg4_prepare_tc(c) != cudaSuccess ||
       cudaMemsetAsync(workspace, 0, workspace_of(*cfg).zeroed, as_stream(stream)) != cudaSuccess) {
     delete c;
     return KVC_ERR_CUDA;
@@ -118,6 +122,7 @@ int kvc_paged4_attend(kvc_paged4* c, const void* q, void* out, float* d_lse, int
   a.scale_log2 = c->scale * 1.4426950408889634f;
   a.err = reinterpret_cast<int32_t*>(c->ws);
   a.tickets = reinterpret_cast<int*>(c->ws + w.tickets);
+  a.warp_tickets = reinterpret_cast<int*>(c->ws + w.warp_tickets);
   a.part = reinterpret_cast<float*>(c->ws + w.parts);
   a.stall_ns = c->debug_stall_ns;
   a.lse = d_lse;
@@ -126,7 +131,8 @@ int kvc_paged4_attend(kvc_paged4* c, const void* q, void* out, float* d_lse, int
   a.even = n_tokens / g.batch;
   a.max_q = d_cu != nullptr ? max_q : n_tokens / g.batch;
   a.causal = (flags & KVC_CAUSAL) != 0;
-  return launched(kvc_pg4_launch_decode(c, a, q, out, as_stream(stream)));
+  const cudaStream_t s = as_stream(stream);
+  return launched(few_rows(a) ? kvc_pg4_launch_decode(c, a, q, out, s) : kvc_pg4_launch_tc(c, a, q, out, s));
 }
 
 int kvc_paged4_get_error(kvc_paged4* c, void* stream, int32_t* bits) {

@@ -20,6 +20,7 @@ struct kvc_paged4 {
 // Workspace, in bytes from its start.
 struct kvc_pg4_layout {
   size_t tickets;       // int32 per block: blocks that have left their part of a split item
+  size_t warp_tickets;  // the same per softmax warp of the tensor-core kernel
   size_t zeroed;        // end of what has to start at zero (and is left at zero)
   size_t parts;         // split partials
   size_t total;
@@ -34,29 +35,32 @@ cudaError_t kvc_pg4_launch_append(kvc_paged4* c, const void* k, const void* v, i
                                   cudaStream_t s);
 cudaError_t kvc_pg4_launch_read(kvc_paged4* c, void* k_out, void* v_out, int n_tokens, const int32_t* cu, cudaStream_t s);
 cudaError_t kvc_pg4_launch_decode(const kvc_paged4* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
+cudaError_t kvc_pg4_launch_tc(const kvc_paged4* c, const kvc_pg_args& a, const void* q, void* out, cudaStream_t s);
 // Shared-memory opt-ins of the kernels a handle may launch, once per handle.
 cudaError_t kvc_pg4_prepare_decode(const kvc_paged4* c);
+cudaError_t kvc_pg4_prepare_tc(const kvc_paged4* c);
 
 #ifdef __CUDACC__
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 
-// Held values are (c - 8) s.  A code moved into the mantissa of 16 reads 16 + c, and one fused multiply-add makes it
-// (16 + c) s - 24 s: 24 s has 6 significant bits and the result 7 at most, so all of it is exact in either 16-bit type.
+// Held values are (c - 8) s.  A code moved into a mantissa reads 64 + c (fp16, under an exponent of 64) or 128 + c (bf16), and
+// one fused multiply-add makes it (64 + c) s - 72 s: 72 s has 8 significant bits at most, 136 s too (17 times four bits), and the
+// result 7, so all of it is exact in either 16-bit type.
 template <typename T>
 struct kvc_pg4_type;
 template <>
 struct kvc_pg4_type<__half> {
-  static constexpr uint32_t kMask = 0x03C003C0u, kSixteen = 0x4C004C00u;
-  static constexpr int kAt = 6;         // the mantissa's top four bits
+  static constexpr uint32_t kMask = 0x00F000F0u, kBase = 0x54005400u, kOff = 0xD480D480u;    // 64, -72
+  static constexpr int kAt = 4;
 };
 template <>
 struct kvc_pg4_type<__nv_bfloat16> {
-  static constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
-  static constexpr int kAt = 3;
+  static constexpr uint32_t kMask = 0x000F000Fu, kBase = 0x43004300u, kOff = 0xC308C308u;    // 128, -136
+  static constexpr int kAt = 0;
 };
 
-// A scale pair for a pair of values: (s, -24 s) in T.
+// What a pair of values is made with: s and -72 s (-136 s).
 struct kvc_pg4_scale {
   uint32_t s, o;
 };
@@ -95,15 +99,14 @@ __device__ __forceinline__ uint32_t pg4_e4m3x2(uint32_t two, const __nv_bfloat16
 }
 template <typename T>
 __device__ __forceinline__ kvc_pg4_scale pg4_scale(uint32_t s) {
-  constexpr uint32_t kM24 = sizeof(T) == 2 && kvc_pg4_type<T>::kAt == 6 ? 0xCE00CE00u : 0xC1C0C1C0u;
-  return {s, pg4_mul(s, kM24, (const T*)nullptr)};
+  return {s, pg4_mul(s, kvc_pg4_type<T>::kOff, (const T*)nullptr)};
 }
-// Pair i of a word of codes (dims 2 i and 2 i + 1 of the word's eight).
+// Pair i of a word of codes (dims 2 i and 2 i + 1 of the word's eight).  `base`: kBase, in a register (a constant known to the
+// compiler would cost a second logic operation: an instruction takes one immediate).
 template <typename T, int i>
-__device__ __forceinline__ uint32_t pg4_pair(uint32_t word, const kvc_pg4_scale& sc) {
-  using P = kvc_pg4_type<T>;
-  constexpr int kUp = P::kAt - 4 * i;
-  const uint32_t x = ((kUp >= 0 ? word << (kUp >= 0 ? kUp : 0) : word >> (kUp < 0 ? -kUp : 0)) & P::kMask) | P::kSixteen;
+__device__ __forceinline__ uint32_t pg4_pair(uint32_t word, const kvc_pg4_scale& sc, uint32_t base) {
+  constexpr int kDown = 4 * i - kvc_pg4_type<T>::kAt;
+  const uint32_t x = ((kDown < 0 ? word << (kDown < 0 ? -kDown : 0) : word >> (kDown > 0 ? kDown : 0)) & kvc_pg4_type<T>::kMask) | base;
   return pg4_fma(x, sc.s, sc.o, (const T*)nullptr);
 }
 
@@ -119,8 +122,7 @@ __device__ __forceinline__ kvc_pg4_fast_scale pg4_fast_scale(uint32_t two_e4m3) 
   const uint32_t s = pg4_e4m3x2(two_e4m3, t);
   return {s, pg4_mul(s, 0xD408D408u, t), pg4_mul(s, 0xD480D480u, t)};
 }
-// `sixty_four`: 0x54005400 in a register (a constant known to the compiler would cost a second logic operation each: an
-// instruction takes one immediate).  d[i]: dims 2 i and 2 i + 1 (of K), or the ith codes of the word's halves.
+// `sixty_four`: kvc_pg4_type<__half>::kBase, in a register (as pg4_pair's).  d[i]: dims 2 i and 2 i + 1 (of K), or the ith codes of the word's halves.
 __device__ __forceinline__ void pg4_fast_pairs(uint32_t word, const kvc_pg4_fast_scale& sc, uint32_t sixty_four, uint32_t* d) {
   const __half* t = nullptr;
   const uint32_t b = word >> 8;

@@ -106,7 +106,7 @@ cudaError_t kvc_pg_launch_tc(const kvc_paged* c, const kvc_pg_args& a, const voi
 // Phase 1's partials joined to one state per token and head; `simt`: phase 1 ran in the FMA kernel.
 cudaError_t kvc_pg_launch_join_prefix(const kvc_paged* c, const kvc_pg_args& a, bool simt, cudaStream_t s);
 // Split items of the tensor-core kernel.
-cudaError_t kvc_pg_launch_join(const kvc_paged* c, const kvc_pg_args& a, void* out, cudaStream_t s);
+cudaError_t kvc_pg_launch_join(const kvc_paged_config& g, const kvc_pg_args& a, void* out, cudaStream_t s);
 // Shared-memory opt-ins of the kernels a handle may launch, once per handle.
 cudaError_t kvc_pg_prepare_simt(const kvc_paged* c);
 cudaError_t kvc_pg_prepare_select(const kvc_paged* c);
