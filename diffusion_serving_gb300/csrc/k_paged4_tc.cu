@@ -66,71 +66,113 @@ struct Smem {
   WaitCtl wc;
 };
 
+// mbar_wait with its polling out of line, so that the roles' loops stay small.
+__device__ __noinline__ bool poll(uint64_t* bar, uint32_t parity, volatile WaitCtl* wc, bool honour_abort) {
+  return mbar_wait(bar, parity, wc, honour_abort);
+}
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, volatile WaitCtl* wc, bool honour_abort = true) {
+  return mbar_test_wait(bar, parity) || poll(bar, parity, wc, honour_abort);
+}
 __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
 
-// One warp's 32 slots of a tile: records at `raw` to rows of operand tiles at `dst` (64 dims each, 128-byte swizzle).  A lane
-// takes 32 dims of a slot at a time; eight neighbouring lanes two such pieces of four slots, whose 16-byte stores meet in no bank.
+// One warp's 32 slots of a tile: records to rows of operand tiles (64 dims each, 128-byte swizzle).  A lane takes 32 dims of a slot
+// at a time; eight neighbouring lanes two such pieces of four slots, whose 16-byte stores meet in no bank.
 template <typename T, int D, bool kV>
-__device__ __forceinline__ void expand(uint32_t raw, uint32_t dst, int warp, int lane, int ps_log2, uint32_t record, int rem, uint32_t bad,
-                                       uint32_t base) {
-  constexpr int W = D / 32, N = W;                 // pieces of a slot, rounds of 32 / W slots
-  const int ps = 1 << ps_log2;
-  const int piece = (lane & 1) | (W == 4 ? lane >> 2 & 2 : 0);
-  const int low = (lane >> 1 & 3) | (W == 4 ? lane >> 2 & 4 : lane >> 1 & 12);
-  uint32_t w[N][4], sb[N];
+struct Expand {
+  static constexpr int W = D / 32;                 // pieces of a slot
+  static constexpr int RN = W / 2;                 // rounds of 32 / W slots in a half, 16 slots
+  uint32_t code[RN], scale;                        // where a round's codes and its scale stand among a tile's records,
+  uint32_t code_step, scale_step;                  // and how much further they do in the second half
+  int slot0;                                       // the first slot,
+  uint32_t row;                                    // whose row it is in the operand tile, and the pieces' turn in it
+  int turn, piece;
+
+  __device__ __forceinline__ void init(int warp, int lane, int ps_log2) {
+    const int ps = 1 << ps_log2;
+    const uint32_t record = (uint32_t)kvc_pg4_record(D, ps_log2);
+    piece = (lane & 1) | (W == 4 ? lane >> 2 & 2 : 0);
+    slot0 = 32 * warp + ((lane >> 1 & 3) | (W == 4 ? lane >> 2 & 4 : lane >> 1 & 12));
+    turn = slot0 & 7;
+    row = (piece >> 1) * kBoxBytes + slot0 * 128;
+    const int rec = slot0 >> ps_log2, s0 = slot0 & (ps - 1);
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int slot = 32 * warp + n * (32 / W) + low;
-    const int rec = slot >> ps_log2, s = slot & (ps - 1);
-    const uint32_t at = raw + rec * record;
-    const uint32_t code = at + (kV ? ps + s : s) * (D / 2) + 16 * (kV ? piece ^ ((s >> 2) & (W - 1)) : piece);
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[n][0]), "=r"(w[n][1]), "=r"(w[n][2]), "=r"(w[n][3]) : "r"(code));
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[n]) : "r"(at + ps * D + (kV ? ps * W + piece * ps + s : s * W + piece)));
-    // slots that hold nothing of the row may hold anything (NaN included): their values become 0, so that P = 0 adds nothing
-    if (kV && (slot >= rem || (bad >> rec & 1))) sb[n] = 0;
+    for (int n = 0; n < RN; ++n) {
+      const int s = s0 + 8 * n;
+      code[n] = rec * record + (kV ? ps + s : s) * (D / 2) + 16 * (kV ? piece ^ ((s >> 2) & (W - 1)) : piece);
+    }
+    scale = rec * record + ps * D + (kV ? ps * W + piece * ps + s0 : s0 * W + piece);
+    code_step = ps == 16 ? record : 16 * (D / 2);
+    scale_step = ps == 16 ? record : kV ? 16 : 16 * W;
   }
+  // dead: some slots hold nothing of the row (those from `rem` on, or of a record in `bad`).  They may hold anything, NaN
+  // included: V's become 0, so that P = 0 adds nothing.
+  __device__ __forceinline__ void run(uint32_t raw, uint32_t dst, bool dead, int rem, uint32_t bad, int ps_log2, uint32_t base) const {
+    uint32_t at[4];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int slot = 32 * warp + n * (32 / W) + low;
-    const uint32_t row = dst + (piece >> 1) * kBoxBytes + slot * 128;
-    const uint32_t two = sb[n] * 0x101u;
+    for (int i = 0; i < 4; ++i) at[i] = dst + row + 16 * (((piece & 1) * 4 + i) ^ turn);
+    // (rolled up: three roles' loops share a scheduler's instruction cache)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[RN][4], sb[RN];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t x[4];
-      if constexpr (kV) {
-        const kvc_pg4_fast_scale sc = pg4_fast_scale(two);
-        pg4_fast_pairs(w[n][i], sc, base, x);
-      } else {
-        const kvc_pg4_scale sc = pg4_scale<T>(pg4_e4m3x2(two, (const T*)nullptr));
-        x[0] = pg4_pair<T, 0>(w[n][i], sc, base);
-        x[1] = pg4_pair<T, 1>(w[n][i], sc, base);
-        x[2] = pg4_pair<T, 2>(w[n][i], sc, base);
-        x[3] = pg4_pair<T, 3>(w[n][i], sc, base);
+      for (int n = 0; n < RN; ++n) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[n][0]), "=r"(w[n][1]), "=r"(w[n][2]), "=r"(w[n][3])
+                     : "r"(raw + code[n] + h * code_step));
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[n]) : "r"(raw + scale + h * scale_step + n * (kV ? 8 : 8 * W)));
       }
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + 16 * (((piece & 1) * 4 + i) ^ (slot & 7))), "r"(x[0]), "r"(x[1]),
-                   "r"(x[2]), "r"(x[3])
-                   : "memory");
+      if (kV && dead) {
+#pragma unroll
+        for (int n = 0; n < RN; ++n) {
+          const int slot = slot0 + 16 * h + 8 * n;
+          if (slot >= rem || (bad >> (slot >> ps_log2) & 1)) sb[n] = 0;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < RN; ++n) {
+        const uint32_t two = sb[n] * 0x101u;
+        kvc_pg4_fast_scale fs;
+        kvc_pg4_scale sc;
+        if constexpr (kV) fs = pg4_fast_scale(two);
+        else sc = pg4_scale<T>(pg4_e4m3x2(two, (const T*)nullptr));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[4];
+          if constexpr (kV) {
+            pg4_fast_pairs(w[n][i], fs, base, x);
+          } else {
+            x[0] = pg4_pair<T, 0>(w[n][i], sc, base);
+            x[1] = pg4_pair<T, 1>(w[n][i], sc, base);
+            x[2] = pg4_pair<T, 2>(w[n][i], sc, base);
+            x[3] = pg4_pair<T, 3>(w[n][i], sc, base);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[i] + n * (8 * 128)), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                       "r"(x[3])
+                       : "memory");
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[i] += 16 * 128;
     }
   }
-}
+};
 
 // p = 2^(s c + off), 0 past `valid` when kMask, of the row's 128 scores at s_addr, packed to p_addr; returns the row's sum of p.
 template <bool kMask>
 __device__ __forceinline__ float exp_row(uint32_t s_addr, uint32_t p_addr, int valid, float c, float off) {
   const float2 c2 = make_float2(c, c), o2 = make_float2(off, off);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  uint32_t sr[2][32];
-  tmem_ld32(s_addr, sr[0]);
-#pragma unroll
+  // (rolled up, without a load ahead: the roles' loops share an instruction cache, and 64 columns a turn take 175 us where these
+  // take 148: 1024 tokens over 8192 slots, 32 heads)
+#pragma unroll 1
   for (int q4 = 0; q4 < 4; ++q4) {
-    uint32_t* x = sr[q4 & 1];
+    uint32_t x[32];
+    tmem_ld32(s_addr + q4 * 32, x);
     tmem_ld_wait();
     reg_fence32(x);
-    if (q4 < 3) tmem_ld32(s_addr + (q4 + 1) * 32, sr[(q4 + 1) & 1]);
     uint32_t pk[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -148,7 +190,6 @@ __device__ __forceinline__ float exp_row(uint32_t s_addr, uint32_t p_addr, int v
   }
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
-template <bool kMask>
 __device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
   float mx = -INFINITY;
 #pragma unroll 1
@@ -160,10 +201,8 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
-      if (kMask) {
-        x0 = q4 * 32 + i < valid ? x0 : -INFINITY;
-        x1 = q4 * 32 + i + 1 < valid ? x1 : -INFINITY;
-      }
+      x0 = q4 * 32 + i < valid ? x0 : -INFINITY;
+      x1 = q4 * 32 + i + 1 < valid ? x1 : -INFINITY;
       mx = fmax3(mx, x0, x1);
     }
   }
@@ -226,13 +265,13 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
   kvc_pg_sched<kBM, kBN, true> sch;
   sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Smem<D>) + 15) & ~(size_t)15), KVC_PG_TC_MIN, KVC_PG_TC_WHOLE, KVC_PG_TC_COST,
            gridDim.x);
-  const uint32_t record = (uint32_t)kvc_pg4_record(D, a.ps_log2);
   kvc_pg_item it;
   bool more = sch.first(a, blockIdx.x, it);
 
   if (warp == 0) {
     // ---------------- producer: Q, and a tile's records, one lane each ----------------
     const int per_tile = kBN >> a.ps_log2;                  // 1, 2, 4 or 8
+    const uint32_t record = (uint32_t)kvc_pg4_record(D, a.ps_log2);
     // lane i < per_tile: the page number of the tile's ith record, not looked at before it is used (a tile later); -1 behind
     // the row's end (where -1 is found in a table, it is a bad page: the record lies before the end)
     auto look = [&](const kvc_pg_item& w, int j) {
@@ -248,7 +287,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
       const uint8_t* heads = pool + (int64_t)(it.vh / a.sub) * record;
       kvc_pg_item nx = it;
       more = sch.next(a, nx);
-      if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_free, (n - 1) & 1, wc));   // the last item's last QK
+      if (n >= 1) ok = __all_sync(0xffffffffu, await(&sm.q_free, (n - 1) & 1, wc));   // the last item's last QK
       if (!ok) break;
       if (lane == 0) {
         mbar_expect_tx(&sm.q_full, HB * stacked * 128);
@@ -261,7 +300,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
         if (j + 1 < tile1) npage = look(it, j + 1);
         else if (more) npage = look(nx, nx.tile0);
         const int st = t % kRaw;
-        if (t >= kRaw) ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_empty[st], (t / kRaw - 1) & 1, wc));
+        if (t >= kRaw) ok = __all_sync(0xffffffffu, await(&sm.raw_empty[st], (t / kRaw - 1) & 1, wc));
         if (!ok) break;
         const bool there = lane < per_tile && j * kBN + (lane << a.ps_log2) < it.r.len;
         const bool fine = there && page >= 0 && page < a.n_pages;
@@ -281,8 +320,8 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     }
     if (lane == 0) {
       // every load this warp issued lands before the CTA's shared memory is released, whether or not a warp gave up
-      if (q_issued > 0) mbar_wait(&sm.q_full, (q_issued - 1) & 1, wc, false);
-      for (int i = max(0, t - kRaw); i < t; ++i) mbar_wait(&sm.raw_full[i % kRaw], (i / kRaw) & 1, wc, false);
+      if (q_issued > 0) await(&sm.q_full, (q_issued - 1) & 1, wc, false);
+      for (int i = max(0, t - kRaw); i < t; ++i) await(&sm.raw_full[i % kRaw], (i / kRaw) & 1, wc, false);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -292,12 +331,12 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     bool ok = true;
     for (; ok && more; more = sch.next(a, it)) {
       const int tile0 = it.tile0, tile1 = it.tile1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, n & 1, wc));
+      ok = __all_sync(0xffffffffu, await(&sm.q_full, n & 1, wc));
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int sb = t & 1;
         // K(t) is expanded, and the softmax of t - 2 has read this buffer
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_full[sb], (t >> 1) & 1, wc) &&
-                                         (t < 2 || mbar_wait(&sm.p_ready[sb], ((t >> 1) - 1) & 1, wc)));
+        ok = __all_sync(0xffffffffu, await(&sm.k_full[sb], (t >> 1) & 1, wc) &&
+                                         (t < 2 || await(&sm.p_ready[sb], ((t >> 1) - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
@@ -316,7 +355,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     }
     if (lane == 0) {                                     // (lands before TMEM is freed, whichever warp gave up)
       mma_commit(&sm.drain[0]);
-      mbar_wait(&sm.drain[0], 0, wc, false);
+      await(&sm.drain[0], 0, wc, false);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -341,10 +380,10 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
       __syncwarp();
       if (!more) break;
       const int tile0 = it.tile0, tile1 = it.tile1;
-      if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (n - 1) & 1, wc));   // the epilogue has read O
+      if (n >= 1) ok = __all_sync(0xffffffffu, await(&sm.o_free, (n - 1) & 1, wc));   // the epilogue has read O
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int sb = t & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[sb], (t >> 1) & 1, wc) && mbar_wait(&sm.p_ready[sb], (t >> 1) & 1, wc));
+        ok = __all_sync(0xffffffffu, await(&sm.v_full[sb], (t >> 1) & 1, wc) && await(&sm.p_ready[sb], (t >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
@@ -363,32 +402,39 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     }
     if (lane == 0) {                                     // (lands before TMEM is freed, whichever warp gave up)
       mma_commit(&sm.drain[1]);
-      mbar_wait(&sm.drain[1], 0, wc, false);
+      await(&sm.drain[1], 0, wc, false);
     }
     __syncwarp();
   } else if (warp >= 8) {
     // ---------------- expanding warps: records to operand tiles ----------------
-    const bool is_v = warp >= 12;
-    int t = 0;
-    bool ok = true;
-    for (; ok && more; more = sch.next(a, it)) {
-      for (int j = it.tile0; j < it.tile1; ++j, ++t) {
-        const int st = t % kRaw, buf = t & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.raw_full[st], (t / kRaw) & 1, wc) &&
-                                         (t < 2 || mbar_wait(is_v ? &sm.v_empty[buf] : &sm.k_empty[buf], ((t >> 1) - 1) & 1, wc)));
-        if (!ok) break;
-        const uint32_t from = smem_u32(sm.raw[st]);
-        const int rem = it.r.len - j * kBN;
-        const uint32_t bad = sm.bad[t % kBadRing];
-        if (is_v) expand<T, D, true>(from, smem_u32(sm.v[buf][0]), warp - 12, lane, a.ps_log2, record, rem, bad, v_base);
-        else expand<T, D, false>(from, smem_u32(sm.k[buf][0]), warp - 8, lane, a.ps_log2, record, rem, bad, k_base);
-        fence_proxy_async();                             // (before the MMAs read the tile, and a copy overwrites the records)
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(is_v ? &sm.v_full[buf] : &sm.k_full[buf]);
-          mbar_arrive(&sm.raw_empty[st]);
+    auto work = [&](auto& e, bool is_v, uint64_t* full, uint64_t* empty, auto& tiles, uint32_t base) {
+      e.init(warp & 3, lane, a.ps_log2);
+      int t = 0;
+      bool ok = true;
+      for (; ok && more; more = sch.next(a, it)) {
+        for (int j = it.tile0; j < it.tile1; ++j, ++t) {
+          const int st = t % kRaw, buf = t & 1;
+          ok = __all_sync(0xffffffffu, await(&sm.raw_full[st], (t / kRaw) & 1, wc) &&
+                                           (t < 2 || await(&empty[buf], ((t >> 1) - 1) & 1, wc)));
+          if (!ok) break;
+          const int rem = it.r.len - j * kBN;
+          const uint32_t bad = is_v ? sm.bad[t % kBadRing] : 0;
+          e.run(smem_u32(sm.raw[st]), smem_u32(tiles[buf]), rem < kBN || bad, rem, bad, a.ps_log2, base);
+          fence_proxy_async();                           // (before the MMAs read the tile, and a copy overwrites the records)
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[buf]);
+            mbar_arrive(&sm.raw_empty[st]);
+          }
         }
       }
+    };
+    if (warp >= 12) {
+      Expand<T, D, true> e;
+      work(e, true, sm.v_full, sm.v_empty, sm.v, v_base);
+    } else {
+      Expand<T, D, false> e;
+      work(e, false, sm.k_full, sm.k_empty, sm.k, k_base);
     }
   } else if (warp >= 4) {
     // ---------------- softmax and epilogue (one query row per thread) ----------------
@@ -401,7 +447,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     int t = 0;
     bool ok = true;
     for (int n = 0;; ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.desc_full[n & 1], (n >> 1) & 1, wc));
+      ok = __all_sync(0xffffffffu, await(&sm.desc_full[n & 1], (n >> 1) & 1, wc));
       if (!ok) break;
       const volatile Desc& it = sm.desc[n & 1];
       const int tiles = it.tiles;
@@ -415,31 +461,45 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
         const int sb = t & 1;
         const uint32_t s_addr = lane_addr + kTmS + sb * 128u, p_addr = lane_addr + kTmP + sb * 64u;
         // S(t) is there, and PV(t - 2) has read this buffer's P
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (t >> 1) & 1, wc) &&
-                                         (t < 2 || mbar_wait(&sm.pv_done[sb], ((t >> 1) - 1) & 1, wc)));
+        ok = __all_sync(0xffffffffu, await(&sm.s_full[sb], (t >> 1) & 1, wc) &&
+                                         (t < 2 || await(&sm.pv_done[sb], ((t >> 1) - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
         const int valid = limit - j * kBN;
         const uint32_t bad = sm.bad[t % kBadRing];
-        auto tile = [&](auto mask) {
-          constexpr bool kM = decltype(mask)::value;
-          // After the first tile P is taken against the running reference at once: every p is at most the row's
-          // sum, so a sum of at most 2^threshold shows that the maximum did not grow by more, and P stands.
-          if (j > 0) {
-            const float lsum = exp_row<kM>(s_addr, p_addr, valid, c, kBias - m_ref);
-            if (!__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) {   // (a NaN sum takes the slow path)
-              l += lsum;
-              return true;
-            }
+        if (bad) {                                      // slots without a page: their scores become -inf where they are
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t x[32];
+            tmem_ld32(s_addr + q4 * 32, x);
+            tmem_ld_wait();
+            reg_fence32(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bad >> ((q4 * 32 + i) >> a.ps_log2)) & 1) x[i] = 0xff800000u;
+            tmem_st32(s_addr + q4 * 32, x);
           }
-          const float m_tile = row_max<kM>(s_addr, valid) * c;
+          tmem_st_wait();
+        }
+        // After the first tile P is taken against the running reference at once: every p is at most the row's
+        // sum, so a sum of at most 2^threshold shows that the maximum did not grow by more, and P stands.
+        bool stands = false;
+        if (j > 0) {
+          const float lsum = __all_sync(0xffffffffu, valid >= kBN) ? exp_row<false>(s_addr, p_addr, valid, c, kBias - m_ref)
+                                                                   : exp_row<true>(s_addr, p_addr, valid, c, kBias - m_ref);
+          stands = !__any_sync(0xffffffffu, !(lsum <= kRescaleSum));      // (not with a NaN sum)
+          if (stands) l += lsum;
+        }
+        if (!stands) {
+          const float m_tile = row_max(s_addr, valid) * c;
           const bool rescale = m_tile > m_ref + kRescaleThreshold || m_ref == -INFINITY;
           const float m_new = rescale ? m_tile : m_ref;
           const float m_use = m_new == -INFINITY ? 0.f : m_new;
           if (j > 0) {
             tmem_st_wait();                             // the optimistic P is overwritten below
             // O may be rescaled only once PV(t - 1) has finished accumulating into it
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc))) return false;
+            ok = __all_sync(0xffffffffu, await(&sm.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc));
+            if (!ok) break;
             tc_fence_after();
             const float alpha = rescale ? pg_ex2(m_ref - m_use) : 1.f;
 #pragma unroll 1
@@ -461,31 +521,14 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
             l *= alpha;
           }
           m_ref = m_new;
-          l += exp_row<kM>(s_addr, p_addr, valid, c, kBias - m_use);
-          return true;
-        };
-        if (bad) {                                      // slots without a page: their scores become -inf where they are
-#pragma unroll 1
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t x[32];
-            tmem_ld32(s_addr + q4 * 32, x);
-            tmem_ld_wait();
-            reg_fence32(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((bad >> ((q4 * 32 + i) >> a.ps_log2)) & 1) x[i] = 0xff800000u;
-            tmem_st32(s_addr + q4 * 32, x);
-          }
-          tmem_st_wait();
+          l += exp_row<true>(s_addr, p_addr, valid, c, kBias - m_use);
         }
-        ok = __all_sync(0xffffffffu, valid >= kBN) ? tile(std::false_type{}) : tile(std::true_type{});
-        if (!ok) break;                                 // (the same for the whole warp)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_ready[sb]);
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.o_done, n & 1, wc));
+      ok = ok && __all_sync(0xffffffffu, await(&sm.o_done, n & 1, wc));
       if (!ok) break;
       tc_fence_after();
       // ---- the item's (or this part's) state: straight out, or left as a partial ----
