@@ -272,16 +272,16 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     // ---------------- producer: Q, and a tile's records, one lane each ----------------
     const int per_tile = kBN >> a.ps_log2;                  // 1, 2, 4 or 8
     const uint32_t record = (uint32_t)kvc_pg4_record(D, a.ps_log2);
-    // lane i < per_tile: the page number of the tile's ith record, not looked at before it is used (a tile later); -1 behind
-    // the row's end (where -1 is found in a table, it is a bad page: the record lies before the end)
-    auto look = [&](const kvc_pg_item& w, int j) {
+    // A window: the page numbers of 32 records, one to a lane, from a tile's first on; not looked at before they are used, a
+    // window later (a load takes as long as a tile).  -1 behind the row's end (where -1 is found in a table, it is a bad page).
+    const int wide = 32 / per_tile;                         // tiles to a window
+    auto window = [&](const kvc_pg_item& w, int j) {
       const int key = j * kBN + (lane << a.ps_log2);
-      if (lane >= per_tile || key >= w.r.len) return -1;
-      return pg_ld(a.table + (int64_t)w.b * a.max_pages + (key >> a.ps_log2));
+      return key < w.r.len ? pg_ld(a.table + (int64_t)w.b * a.max_pages + (key >> a.ps_log2)) : -1;
     };
     int t = 0, n = 0, q_issued = 0;
     bool ok = true;
-    int page = more ? look(it, it.tile0) : -1;
+    int ahead = more ? window(it, it.tile0) : -1;
     for (; ok && more;) {
       const int tile0 = it.tile0, tile1 = it.tile1;
       const uint8_t* heads = pool + (int64_t)(it.vh / a.sub) * record;
@@ -295,13 +295,18 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
           tma_load_4d(&tm_q, &sm.q_full, sm.q[h], 64 * h, it.vh * a.Gv, it.r.t0 + it.k * sch.T, 0);
       }
       q_issued = n + 1;
-      for (int j = tile0; j < tile1; ++j, ++t) {
-        int npage = -1;
-        if (j + 1 < tile1) npage = look(it, j + 1);
-        else if (more) npage = look(nx, nx.tile0);
+      int pages = -1, at = wide;                            // this window, and the next tile's place in it
+      for (int j = tile0; j < tile1; ++j, ++t, ++at) {
+        if (at == wide) {
+          at = 0;
+          pages = ahead;
+          if (j + wide < tile1) ahead = window(it, j + wide);
+          else if (more) ahead = window(nx, nx.tile0);
+        }
         const int st = t % kRaw;
         if (t >= kRaw) ok = __all_sync(0xffffffffu, await(&sm.raw_empty[st], (t / kRaw - 1) & 1, wc));
         if (!ok) break;
+        const int page = __shfl_sync(0xffffffffu, pages, at * per_tile + (lane & (per_tile - 1)));
         const bool there = lane < per_tile && j * kBN + (lane << a.ps_log2) < it.r.len;
         const bool fine = there && page >= 0 && page < a.n_pages;
         const unsigned want = __ballot_sync(0xffffffffu, there), good = __ballot_sync(0xffffffffu, fine);
@@ -313,7 +318,6 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
         __syncwarp();
         if (fine) bulk_load(&sm.raw_full[st], sm.raw[st] + lane * record, heads + (int64_t)page * a.Hkv * record, record);
         __syncwarp();
-        page = npage;
       }
       ++n;
       it = nx;
