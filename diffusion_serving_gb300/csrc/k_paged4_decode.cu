@@ -18,10 +18,7 @@
 //                 B is P^T: S^T's accumulators, packed, through movmatrix.
 // Two codes become two values by a quarter of a shift, a mask-and-or and one multiply-add (paged4_internal.h), as fp16 whichever
 // the 16-bit type; every other pair comes out 16 times too small, which its queries make up for, or the outputs (dims
-// are rows of O^T, and a row's pairs are of one kind).  Queries are taken as fp16, each times a power of 2 that brings its
-// largest element to 2^10 .. 2^11 (and 16 times that, where the keys are too small): elements are exact down to 2^-25 of the
-// largest, and below it off by 2^-36 of it at most; held magnitudes span less than 2^21, so a score is off by less than 2^-15
-// of the sum of its terms' magnitudes, at queries and keys made for it.
+// are rows of O^T, and a row's pairs are of one kind).  Queries are taken as fp16 too, each row times a power of 2.
 // The running maximum of a query is looked for only when a weight outgrows its reference by 2^7 (one vote per tile);
 // weights are taken 2^8 too large, so that fp16 holds them with full precision down to 2^-22 of the reference, and
 // rounded to fp16 once for the product with V (their sum takes them unrounded).
@@ -90,37 +87,16 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// A query row's 8 elements, VQ lanes to a row, as fp16 times a power of 2 (words 0 and 2: 16 times that); returns what undoes it.
-__device__ __forceinline__ float2 floats(uint32_t w, const __half*) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-__device__ __forceinline__ float2 floats(uint32_t w, const __nv_bfloat16*) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
+// A query row's 8 elements, VQ lanes to a row, as pg4_query_vec has them; returns what undoes the row's factor.
 template <typename T, int VQ>
 __device__ __forceinline__ float as_half(uint4& v) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = floats(w[i], (const T*)nullptr);
-    top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-  }
+  float top = pg4_query_top<T>(v, 0.f);
 #pragma unroll
   for (int o = 1; o < VQ; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const int e = (int)(__float_as_uint(top) >> 23) - 127;       // top is 2^e .. 2^(e + 1)
-  const int up = e == 128 ? 0 : min(10 - e, 120);              // (an infinity stays one; factors within fp32's range)
-  const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = floats(w[i], (const T*)nullptr);
-    const float y = i & 1 ? f : 16.f * f;
-    w[i] = pack_half(x.x * y, x.y * y);
-  }
-  return __uint_as_float((uint32_t)(127 - up) << 23);
+  float undo;
+  const float f = pg4_query_factor(top, &undo);
+  pg4_query_vec<T>(v, f);
+  return undo;
 }
 // (a NaN goes on)
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -466,8 +442,8 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
               for (int e = 0; e < 4; ++e) p[s][x][e] = pg_ex2(p[s][x][e]);
               l[x][0] += p[s][x][0] + p[s][x][2];
               l[x][1] += p[s][x][1] + p[s][x][3];
-              pb[s][x][0] = transposed(pack_half(p[s][x][0], p[s][x][1]));
-              pb[s][x][1] = transposed(pack_half(p[s][x][2], p[s][x][3]));
+              pb[s][x][0] = transposed(pg4_pack(p[s][x][0], p[s][x][1]));
+              pb[s][x][1] = transposed(pg4_pack(p[s][x][2], p[s][x][3]));
             }
           }
           // ---- O^T ----

@@ -3,11 +3,13 @@
 // Items, tiles, their division among blocks and the join of split items are the 16-bit kernel's (k_paged_tc.cu): an item is up to
 // 128 query rows, tokens x heads of one group, over tiles of 128 slots.  Records arrive packed, one bulk copy per page; eight
 // warps expand them into the swizzled operand tiles that the MMAs read, once per tile for all 128 rows, while the tensor cores and
-// the softmax are at the tiles before.  K is expanded to the queries' type (exact); V to fp16 (exact but for a factor of 16 on
-// half of the dims, put right when O leaves TMEM), as P is fp16 whichever the type: rounded once, to 11 bits.
+// the softmax are at the tiles before.  Both are expanded to fp16, whichever the 16-bit type, by one piece of code: exact but for a
+// factor of 16 on half of the dims, which K's queries make up for (taken to fp16 too, paged4_internal.h) and O when it leaves
+// TMEM.  P is fp16, rounded once.
 //
 // A block is one CTA per SM (512 threads).  Warps: 0 producer of Q (TMA) and of records, 1 issues S = Q K^T (and owns TMEM),
-// 2 issues O += P V, 4-7 softmax, one query row per thread, 8-11 expand K, 12-15 V.  TMEM: two S buffers (128 columns), two P (64),
+// 2 issues O += P V, 4-7 softmax, one query row per thread, 8-11 expand K, 12-15 V (and turn an
+// item's queries to fp16).  TMEM: two S buffers (128 columns), two P (64),
 // O (128).  P has columns of its own, so S(t + 2) waits for the softmax of t alone, not for its product with V, and the softmax,
 // which finds S where it was if its weights turn out too large, takes a row by pieces of 32 columns (the 128 registers that
 // 512 threads leave it would not hold it whole).
@@ -51,7 +53,7 @@ struct Smem {
   uint8_t k[2][D / 64][kBoxBytes];
   uint8_t v[2][D / 64][kBoxBytes];
   uint8_t raw[kRaw][kBN * (D + D / 16)];
-  uint64_t q_full, q_free;
+  uint64_t q_full, q_ready, q_free;
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_ready[2], pv_done[2];
@@ -59,6 +61,7 @@ struct Smem {
   uint64_t drain[2];
   uint64_t desc_full[2];
   Desc desc[2];
+  float q_scale[2][kBM];   // of an item's scores, to log2 units
   // records of a tile that no page stands behind: the producer is at most four tiles ahead of the softmax (two of records,
   // two of K tiles)
   uint32_t bad[kBadRing];
@@ -81,7 +84,7 @@ __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* 
 
 // One warp's 32 slots of a tile: records to rows of operand tiles (64 dims each, 128-byte swizzle).  A lane takes 32 dims of a slot
 // at a time; eight neighbouring lanes two such pieces of four slots, whose 16-byte stores meet in no bank.
-template <typename T, int D, bool kV>
+template <int D>
 struct Expand {
   static constexpr int W = D / 32;                 // pieces of a slot
   static constexpr int RN = W / 2;                 // rounds of 32 / W slots in a half, 16 slots
@@ -90,8 +93,9 @@ struct Expand {
   int slot0;                                       // the first slot,
   uint32_t row;                                    // whose row it is in the operand tile, and the pieces' turn in it
   int turn, piece;
+  uint32_t scale_round;                            // a scale's way to the next round's
 
-  __device__ __forceinline__ void init(int warp, int lane, int ps_log2) {
+  __device__ __forceinline__ void init(int warp, int lane, int ps_log2, bool is_v) {
     const int ps = 1 << ps_log2;
     const uint32_t record = (uint32_t)kvc_pg4_record(D, ps_log2);
     piece = (lane & 1) | (W == 4 ? lane >> 2 & 2 : 0);
@@ -102,14 +106,15 @@ struct Expand {
 #pragma unroll
     for (int n = 0; n < RN; ++n) {
       const int s = s0 + 8 * n;
-      code[n] = rec * record + (kV ? ps + s : s) * (D / 2) + 16 * (kV ? piece ^ ((s >> 2) & (W - 1)) : piece);
+      code[n] = rec * record + (is_v ? ps + s : s) * (D / 2) + 16 * (is_v ? piece ^ ((s >> 2) & (W - 1)) : piece);
     }
-    scale = rec * record + ps * D + (kV ? ps * W + piece * ps + s0 : s0 * W + piece);
+    scale = rec * record + ps * D + (is_v ? ps * W + piece * ps + s0 : s0 * W + piece);
+    scale_round = is_v ? 8 : 8 * W;
     code_step = ps == 16 ? record : 16 * (D / 2);
-    scale_step = ps == 16 ? record : kV ? 16 : 16 * W;
+    scale_step = ps == 16 ? record : 2 * scale_round;
   }
   // dead: some slots hold nothing of the row (those from `rem` on, or of a record in `bad`).  They may hold anything, NaN
-  // included: V's become 0, so that P = 0 adds nothing.
+  // included: they become 0, so that P = 0 adds nothing (a key's score is masked, whatever it is).
   __device__ __forceinline__ void run(uint32_t raw, uint32_t dst, bool dead, int rem, uint32_t bad, int ps_log2, uint32_t base) const {
     uint32_t at[4];
 #pragma unroll
@@ -122,9 +127,9 @@ struct Expand {
       for (int n = 0; n < RN; ++n) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[n][0]), "=r"(w[n][1]), "=r"(w[n][2]), "=r"(w[n][3])
                      : "r"(raw + code[n] + h * code_step));
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[n]) : "r"(raw + scale + h * scale_step + n * (kV ? 8 : 8 * W)));
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[n]) : "r"(raw + scale + h * scale_step + n * scale_round));
       }
-      if (kV && dead) {
+      if (dead) {
 #pragma unroll
         for (int n = 0; n < RN; ++n) {
           const int slot = slot0 + 16 * h + 8 * n;
@@ -134,21 +139,11 @@ struct Expand {
 #pragma unroll
       for (int n = 0; n < RN; ++n) {
         const uint32_t two = sb[n] * 0x101u;
-        kvc_pg4_fast_scale fs;
-        kvc_pg4_scale sc;
-        if constexpr (kV) fs = pg4_fast_scale(two);
-        else sc = pg4_scale<T>(pg4_e4m3x2(two, (const T*)nullptr));
+        const kvc_pg4_fast_scale sc = pg4_fast_scale(two);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t x[4];
-          if constexpr (kV) {
-            pg4_fast_pairs(w[n][i], fs, base, x);
-          } else {
-            x[0] = pg4_pair<T, 0>(w[n][i], sc, base);
-            x[1] = pg4_pair<T, 1>(w[n][i], sc, base);
-            x[2] = pg4_pair<T, 2>(w[n][i], sc, base);
-            x[3] = pg4_pair<T, 3>(w[n][i], sc, base);
-          }
+          pg4_fast_pairs(w[n][i], sc, base, x);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at[i] + n * (8 * 128)), "r"(x[0]), "r"(x[1]), "r"(x[2]),
                        "r"(x[3])
                        : "memory");
@@ -211,8 +206,7 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __restrict__ out, kvc_pg_args a, uint32_t k_base,
-            uint32_t v_base) {
+k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __restrict__ out, kvc_pg_args a, uint32_t base) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int HB = D / 64;
   extern __shared__ uint8_t raw_smem[];
@@ -224,6 +218,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
   if (threadIdx.x == 0) {
     wait_init(&sm.wc, a.stall_ns);
     mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_ready, 4);
     mbar_init(&sm.q_free, 1);
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&sm.raw_full[i], 1);
@@ -330,12 +325,12 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- QK issuer: S(t) = Q K(t)^T ----------------
-    constexpr uint32_t kIdQK = idesc_f16(kBf16 ? 1u : 0u, 0, kBN);
+    constexpr uint32_t kIdQK = idesc_f16(0u, 0, kBN);
     int t = 0, n = 0;
     bool ok = true;
     for (; ok && more; more = sch.next(a, it)) {
       const int tile0 = it.tile0, tile1 = it.tile1;
-      ok = __all_sync(0xffffffffu, await(&sm.q_full, n & 1, wc));
+      ok = __all_sync(0xffffffffu, await(&sm.q_ready, n & 1, wc));
       for (int j = tile0; ok && j < tile1; ++j, ++t) {
         const int sb = t & 1;
         // K(t) is expanded, and the softmax of t - 2 has read this buffer
@@ -411,34 +406,56 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     __syncwarp();
   } else if (warp >= 8) {
     // ---------------- expanding warps: records to operand tiles ----------------
-    auto work = [&](auto& e, bool is_v, uint64_t* full, uint64_t* empty, auto& tiles, uint32_t base) {
-      e.init(warp & 3, lane, a.ps_log2);
-      int t = 0;
-      bool ok = true;
-      for (; ok && more; more = sch.next(a, it)) {
-        for (int j = it.tile0; j < it.tile1; ++j, ++t) {
-          const int st = t % kRaw, buf = t & 1;
-          ok = __all_sync(0xffffffffu, await(&sm.raw_full[st], (t / kRaw) & 1, wc) &&
-                                           (t < 2 || await(&empty[buf], ((t >> 1) - 1) & 1, wc)));
-          if (!ok) break;
-          const int rem = it.r.len - j * kBN;
-          const uint32_t bad = is_v ? sm.bad[t % kBadRing] : 0;
-          e.run(smem_u32(sm.raw[st]), smem_u32(tiles[buf]), rem < kBN || bad, rem, bad, a.ps_log2, base);
-          fence_proxy_async();                           // (before the MMAs read the tile, and a copy overwrites the records)
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[buf]);
-            mbar_arrive(&sm.raw_empty[st]);
+    const bool is_v = warp >= 12;
+    Expand<D> e;
+    e.init(warp & 3, lane, a.ps_log2, is_v);
+    uint64_t *full = is_v ? sm.v_full : sm.k_full, *empty = is_v ? sm.v_empty : sm.k_empty;
+    const uint32_t tiles = smem_u32(is_v ? sm.v[0][0] : sm.k[0][0]);
+    int t = 0, n = 0;
+    bool ok = true;
+    for (; ok && more; more = sch.next(a, it), ++n) {
+      if (is_v) {
+        // ---- the item's queries to fp16, where they are: a row to a lane ----
+        ok = __all_sync(0xffffffffu, await(&sm.q_full, n & 1, wc));
+        if (!ok) break;
+        const int r = (warp - 12) * 32 + lane;
+        float top = 0.f, undo;
+#pragma unroll 1
+        for (int h = 0; h < HB; ++h) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) top = pg4_query_top<T>(*reinterpret_cast<const uint4*>(sm.q[h] + r * 128 + 16 * (c ^ (r & 7))), top);
+        }
+        const float f = pg4_query_factor(top, &undo);
+        sm.q_scale[n & 1][r] = undo * a.scale_log2;
+#pragma unroll 1
+        for (int h = 0; h < HB; ++h) {
+#pragma unroll 4
+          for (int c = 0; c < 8; ++c) {
+            uint4* p = reinterpret_cast<uint4*>(sm.q[h] + r * 128 + 16 * (c ^ (r & 7)));
+            uint4 v = *p;
+            pg4_query_vec<T>(v, f);
+            *p = v;
           }
         }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_ready);
       }
-    };
-    if (warp >= 12) {
-      Expand<T, D, true> e;
-      work(e, true, sm.v_full, sm.v_empty, sm.v, v_base);
-    } else {
-      Expand<T, D, false> e;
-      work(e, false, sm.k_full, sm.k_empty, sm.k, k_base);
+      for (int j = it.tile0; j < it.tile1; ++j, ++t) {
+        const int st = t % kRaw, buf = t & 1;
+        ok = __all_sync(0xffffffffu, await(&sm.raw_full[st], (t / kRaw) & 1, wc) &&
+                                         (t < 2 || await(&empty[buf], ((t >> 1) - 1) & 1, wc)));
+        if (!ok) break;
+        const int rem = it.r.len - j * kBN;
+        const uint32_t bad = sm.bad[t % kBadRing];
+        e.run(smem_u32(sm.raw[st]), tiles + buf * HB * kBoxBytes, rem < kBN || bad, rem, bad, a.ps_log2, base);
+        fence_proxy_async();                             // (before the MMAs read the tile, and a copy overwrites the records)
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[buf]);
+          mbar_arrive(&sm.raw_empty[st]);
+        }
+      }
     }
   } else if (warp >= 4) {
     // ---------------- softmax and epilogue (one query row per thread) ----------------
@@ -446,7 +463,6 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
     const int r = quad * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t o_addr = lane_addr + kTmO;
-    const float c = a.scale_log2;
     const int i_tok = r / a.Gv, g = r - i_tok * a.Gv;        // this row's token and head within an item
     int t = 0;
     bool ok = true;
@@ -460,7 +476,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
       int limit = 0x3fffffff;
       if (r < it.end.rows) limit = a.causal ? it.limit0 + i_tok : it.len;
       limit -= it.key0;                                      // (as of the first tile)
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = -INFINITY, l = 0.f, c = 0.f;
       for (int j = 0; j < tiles; ++j, ++t) {
         const int sb = t & 1;
         const uint32_t s_addr = lane_addr + kTmS + sb * 128u, p_addr = lane_addr + kTmP + sb * 64u;
@@ -469,6 +485,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
                                          (t < 2 || await(&sm.pv_done[sb], ((t >> 1) - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
+        if (j == 0) c = sm.q_scale[n & 1][r];
         const int valid = limit - j * kBN;
         const uint32_t bad = sm.bad[t % kBadRing];
         if (bad) {                                      // slots without a page: their scores become -inf where they are
@@ -666,7 +683,7 @@ cudaError_t launch(const kvc_paged4* c, kvc_pg_args a, const void* q, void* out,
   if (!kvc_make_box_map(&tm_q, c->cfg.dtype, q, D, a.H, a.n_tokens, 1, box)) return cudaErrorInvalidValue;
   a.join_here = 3 * (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok) >= KVC_PG_GRID;
   const cudaError_t e = kvc_launch_pdl(k_paged4_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(a.B), s, tm_q,
-                                       (const uint8_t*)c->pages, (T*)out, a, kvc_pg4_type<T>::kBase, kvc_pg4_type<__half>::kBase);
+                                       (const uint8_t*)c->pages, (T*)out, a, kvc_pg4_type<__half>::kBase);
   if (e != cudaSuccess || a.join_here) return e;
   // rows that hold no more than an uncut item's slots, and at most an item a block: nothing to join
   const int64_t items = (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok + a.B);

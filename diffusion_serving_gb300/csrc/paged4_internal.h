@@ -131,4 +131,46 @@ __device__ __forceinline__ void pg4_fast_pairs(uint32_t word, const kvc_pg4_fast
   d[2] = pg4_fma((b & 0x000F000Fu) | sixty_four, sc.s, sc.o0, t);
   d[3] = pg4_fma((b & 0x00F000F0u) | sixty_four, sc.s, sc.o1, t);
 }
+
+// ---- queries for such pairs ----
+// A row of queries as fp16, times a power of 2 that brings its largest element to 2^10 .. 2^11, and 16 times that at the dims of
+// pairs 0 and 2, whose keys come out too small.  Elements are exact down to 2^-25 of the largest, and below it off by 2^-36 of
+// it at most; held magnitudes span less than 2^21, so a score is off by less than 2^-15 of the sum of its terms' magnitudes, at
+// queries and keys made for it.
+__device__ __forceinline__ uint32_t pg4_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 pg4_floats(uint32_t w, const __half*) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ float2 pg4_floats(uint32_t w, const __nv_bfloat16*) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ float pg4_query_top(const uint4& v, float top) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = pg4_floats(w[i], (const T*)nullptr);
+    top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+  }
+  return top;
+}
+// The factor of a row whose largest magnitude is `top`, and what undoes it.  (An infinity stays one; both are within fp32's range.)
+__device__ __forceinline__ float pg4_query_factor(float top, float* undo) {
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;       // top is 2^e .. 2^(e + 1)
+  const int up = e == 128 ? 0 : min(10 - e, 120);
+  *undo = __uint_as_float((uint32_t)(127 - up) << 23);
+  return __uint_as_float((uint32_t)(127 + up) << 23);
+}
+template <typename T>
+__device__ __forceinline__ void pg4_query_vec(uint4& v, float f) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = pg4_floats(w[i], (const T*)nullptr);
+    const float y = i & 1 ? f : 16.f * f;
+    w[i] = pg4_pack(x.x * y, x.y * y);
+  }
+}
 #endif  // __CUDACC__
