@@ -37,6 +37,11 @@ constexpr float kBias = 6.0f;                            // log2 of a weight at 
 constexpr float kRescaleThreshold = 8.0f;                // log2 units
 constexpr float kRescaleSum = 16384.0f;                  // 2^(kBias + kRescaleThreshold)
 constexpr int kBadRing = 8;
+// Items left over from whole waves are cut among all blocks.  Where that makes more than so many parts each, of rows as long
+// as so many tiles a block, a launch of its own (some 10 us) joins them, spread over the GPU, instead of the block that is last:
+// 1560 tokens over 32768 slots, 12 heads (156 items, four of them in 38 parts each): 328 us, and 418 joined by the last block;
+// 1024 tokens over 8192 slots, 32 heads over 8 (256 items, parts of 1.5 blocks): 159 and 148.
+constexpr int kManyParts = 6, kLong = 48;
 
 // An item as the softmax warps see it (worked out by the PV issuer, which would otherwise idle).
 struct Desc {
@@ -681,13 +686,17 @@ cudaError_t launch(const kvc_paged4* c, kvc_pg_args a, const void* q, void* out,
   const int T_tok = kBM / a.Gv;
   const uint32_t box[4] = {64, (uint32_t)a.Gv, (uint32_t)T_tok, 1};
   if (!kvc_make_box_map(&tm_q, c->cfg.dtype, q, D, a.H, a.n_tokens, 1, box)) return cudaErrorInvalidValue;
-  a.join_here = 3 * (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok) >= KVC_PG_GRID;
+  const int64_t items = (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok);            // as one row's
+  const int64_t tiles = ((int64_t)a.max_pages << a.ps_log2) / kBN + 1;                 // of one, at most
+  const int64_t left = items % KVC_PG_GRID;
+  a.waves = 3 * items >= KVC_PG_GRID;
+  a.idle = KVC_PG_TC_JOIN;
+  a.join_here = a.waves && !(left > 0 && left * kManyParts < KVC_PG_GRID && items * tiles >= (int64_t)KVC_PG_GRID * kLong);
   const cudaError_t e = kvc_launch_pdl(k_paged4_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(a.B), s, tm_q,
                                        (const uint8_t*)c->pages, (T*)out, a, kvc_pg4_type<__half>::kBase);
   if (e != cudaSuccess || a.join_here) return e;
   // rows that hold no more than an uncut item's slots, and at most an item a block: nothing to join
-  const int64_t items = (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok + a.B);
-  if (((int64_t)a.max_pages << a.ps_log2) <= KVC_PG_TC_WHOLE * kBN && items <= KVC_PG_GRID) return e;
+  if (((int64_t)a.max_pages << a.ps_log2) <= KVC_PG_TC_WHOLE * kBN && items + (int64_t)a.Hv * a.B <= KVC_PG_GRID) return e;
   return kvc_pg_launch_join(c->cfg, a, out, s);
 }
 

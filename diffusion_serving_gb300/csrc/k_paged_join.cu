@@ -13,18 +13,19 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRowBlocks = 8;             // blocks per split item
 
-// Block (c, y) joins rows y * 8 + warp, ... of the item that begins in k_paged_tc's block c and goes on behind it, if
-// there is one.
+// Block (c, y) joins rows y * 8 + warp, ... of the item that begins in block c of k_paged_tc (or k_paged4_tc) and goes on behind
+// it, if there is one.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 k_paged_join(T* __restrict__ out, kvc_pg_args a) {
   constexpr int R = KVC_PG_TC_ROWS;
   extern __shared__ __align__(16) uint8_t smem[];
-  kvc_pg_sched<R, KVC_PG_TC_TILE> sch;
+  kvc_pg_sched<R, KVC_PG_TC_TILE, true> sch;
   sch.init(a, smem, KVC_PG_TC_MIN, KVC_PG_TC_WHOLE, KVC_PG_TC_COST, KVC_PG_GRID);
   // the item at the end of the block's stretch
-  const long long end = (long long)(blockIdx.x + 1) * sch.per;
-  const bool any = end < sch.total;
+  const bool waves = sch.waves > 0;
+  const long long end = waves ? sch.from + sch.cut[blockIdx.x + 1] : (long long)(blockIdx.x + 1) * sch.per;
+  const bool any = end < sch.total && (!waves || sch.cut[blockIdx.x] < sch.cut[blockIdx.x + 1]);
   kvc_pg_item it;
   int c0 = 0, c1 = 0;
   if (any) {
@@ -104,7 +105,7 @@ cudaError_t launch_prefix(const kvc_pg_args& a, int R, int TS, int cost, int gri
 
 template <typename T, int D>
 cudaError_t launch(const kvc_pg_args& a, void* out, cudaStream_t s) {
-  return kvc_launch_pdl(k_paged_join<T, D>, dim3(KVC_PG_GRID, kRowBlocks), dim3(kThreads), pg_sched_bytes(a.B), s,
+  return kvc_launch_pdl(k_paged_join<T, D>, dim3(KVC_PG_GRID, kRowBlocks), dim3(kThreads), pg_sched_bytes(a.B, true), s,
                         (T*)out, a);
 }
 

@@ -613,6 +613,8 @@ cudaError_t launch(const kvc_paged* c, kvc_pg_args a, const void* q, void* out, 
   const int rows = a.phase == 1 ? 1 : a.B;
   const int T_tok = kBM / a.Gv;
   a.join_here = a.phase != 1 && 3 * (int64_t)a.Hv * ((a.n_tokens + T_tok - 1) / T_tok) >= KVC_PG_GRID;
+  a.waves = a.join_here;
+  a.idle = KVC_PG_TC_JOIN;
   const cudaError_t e = kvc_launch_pdl(k_paged_tc<T, D>, dim3(KVC_PG_GRID), dim3(kThreads), smem_bytes<D>(rows), s, tm_q,
                                  c->tm_k, c->tm_v, (T*)out, a);
   if (e != cudaSuccess || a.phase == 1 || a.join_here) return e;

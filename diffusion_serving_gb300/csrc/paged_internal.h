@@ -69,8 +69,10 @@ struct kvc_pg_args {
   int n_sel;
   float* part;                // [2 * grid][R][D + 2]: O (unnormalised), then (max, sum) per row
   int* tickets;
-  int* warp_tickets;          // the tensor-core kernel's, 4 per block, where it joins split items itself (join_here)
+  int* warp_tickets;          // the tensor-core kernels', 4 per block, where they join split items themselves (join_here)
   int join_here;
+  int waves;                  // many items: whole ones in waves, where that pays
+  int idle;                   // the idle tiles per block that taking every item whole may leave before some are cut
   float* pre;                 // phase 1's partials [items + blocks][R][D + 2]
   float* pre_o;               // joined: [n_tokens * H][D], unnormalised
   float2* pre_ml;             // (max, sum)
@@ -386,9 +388,9 @@ struct kvc_pg_sched {
       stride = 0;
       total = (int)(tiles + items * cost);
       per = max(min_tiles, (total + grid - 1) / grid);
-      if (kWaves && a.join_here) {
+      if (kWaves && a.waves) {
         const long long rounds = (items + grid - 1) / grid;
-        waves = rounds * (most + cost) <= total / grid + KVC_PG_TC_JOIN ? (int)rounds : (total / grid) / (most + cost);
+        waves = rounds * (most + cost) <= total / grid + a.idle ? (int)rounds : (total / grid) / (most + cost);
       }
     }
     __syncthreads();                       // (every warp has read the rows' own tiles)
