@@ -68,7 +68,7 @@ __device__ __forceinline__ Held<T> hold(const Vec<T>& x, const Vec<T>& y) {
   return r;
 }
 
-template <typename T, int D, bool kAxes>
+template <typename T, int D, int kAxes>
 __global__ void __launch_bounds__(kThreads, 4)
 k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, T* q_out, AppendArgs a) {
   constexpr int VL = 8;
@@ -106,15 +106,15 @@ k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, 
   const int64_t src0 = (int64_t)head * D + c * VL;
   uint8_t* rec = pool + ((int64_t)page * a.Hkv + head) * kvc_pg4_record(D, a.ps_log2);
   const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
+  Places places;
   for (int p = lo + warp / gw; p < end; p += stride) {
     Vec<T> x, y, vx, vy;
     Turn<T> cs;
-    Place at;
-    if (kAxes && !load_place(a, r.t0 + p - p0, at)) continue;        // (the same for the whole warp)
     const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
     x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
     y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
-    if (kAxes) load_turn_axes<T, D>(cs, a.rope, at, axes, c, a.half);
+    if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;        // (the same for the whole warp)
+    if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
     else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
     vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
     vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
@@ -216,11 +216,14 @@ cudaError_t launch(kvc_paged4* c, const void* k, const void* v, const void* q, v
   a.q_cols = q != nullptr ? a.H * (D / 16) : 0;
   a.kv_groups = (a.kv_cols + 31) / 32;
   const dim3 grid = run_grid(a, a.kv_groups + (a.q_cols + 31) / 32);
-  if (a.pos != nullptr)
-    return kvc_launch_pdl(k_paged4_append<T, D, true>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
-                          c->pages, (T*)q_out, a);
-  return kvc_launch_pdl(k_paged4_append<T, D, false>, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q,
-                        c->pages, (T*)q_out, a);
+  auto go = [&](auto kernel) {
+    return kvc_launch_pdl(kernel, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q, c->pages, (T*)q_out, a);
+  };
+  switch (axes_kind(a, D, 8)) {
+    case kSlots: return go(k_paged4_append<T, D, kSlots>);
+    case kFlat: return go(k_paged4_append<T, D, kFlat>);
+    default: return go(k_paged4_append<T, D, kAny>);
+  }
 }
 template <typename T, int D>
 cudaError_t launch_read(kvc_paged4* c, void* k_out, void* v_out, AppendArgs a, cudaStream_t s) {

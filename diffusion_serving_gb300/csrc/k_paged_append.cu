@@ -14,8 +14,8 @@
 // A run's keys, after rounding, give the page's maximum and minimum in registers: no second pass, no
 // atomics.
 //
-// With positions of several axes (kAxes) each pair takes its angles from the row of its axis: two neighbouring pairs of
-// one axis by one 16-byte load, as before, others by two of 8 bytes.
+// With positions of several axes (kAxes) each pair takes its angles from the row of its axis: by the same 16-byte loads where a
+// lane's pairs of a vector go by one axis (sections side by side), else pair by pair.
 #include "paged_append.h"
 
 namespace {
@@ -36,7 +36,7 @@ __device__ __forceinline__ float pick_min(float a, float b) {
 __device__ __forceinline__ __half pick_min(__half a, __half b) { return __hmin_nan(a, b); }
 __device__ __forceinline__ __nv_bfloat16 pick_min(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmin_nan(a, b); }
 
-template <typename T, int D, bool kBounds, bool kAxes>
+template <typename T, int D, bool kBounds, int kAxes>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
                T* q_out, T* __restrict__ bounds, AppendArgs a) {
@@ -75,18 +75,19 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   const int64_t dst_row = (int64_t)a.Hkv * D;
   Vec<T> mx0, mx1, mn0, mn1;
   bool any = false;
-  if (have) {
+  if (kAxes || have) {                              // (with axes a warp stays whole)
     const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
+    Places places;
     for (int p = lo + warp / gw; p < end; p += stride) {
       Vec<T> x, y, vx, vy;
       Turn<T> cs;
-      Place at;
-      if (kAxes && !load_place(a, r.t0 + p - p0, at)) continue;
       const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
       x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
       y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
-      if (kAxes) load_turn_axes<T, D>(cs, a.rope, at, axes, c, a.half);
+      if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
+      if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
       else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+      if (kAxes && !have) continue;
       vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
       vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
       const int64_t dst = (((int64_t)page << a.ps_log2) + (p & (ps - 1))) * dst_row + src0;
@@ -172,8 +173,12 @@ cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, vo
     return kvc_launch_pdl(kernel, grid, dim3(kThreads), 0, s, (const T*)k, (const T*)v, (const T*)q, (T*)c->k, (T*)c->v,
                           (T*)q_out, (T*)c->bounds, a);
   };
-  if (a.pos != nullptr) return c->bounds != nullptr ? go(k_paged_append<T, D, true, true>) : go(k_paged_append<T, D, false, true>);
-  return c->bounds != nullptr ? go(k_paged_append<T, D, true, false>) : go(k_paged_append<T, D, false, false>);
+  const bool bounds = c->bounds != nullptr;
+  switch (axes_kind(a, D, VL)) {
+    case kSlots: return bounds ? go(k_paged_append<T, D, true, kSlots>) : go(k_paged_append<T, D, false, kSlots>);
+    case kFlat: return bounds ? go(k_paged_append<T, D, true, kFlat>) : go(k_paged_append<T, D, false, kFlat>);
+    default: return bounds ? go(k_paged_append<T, D, true, kAny>) : go(k_paged_append<T, D, false, kAny>);
+  }
 }
 
 }  // namespace

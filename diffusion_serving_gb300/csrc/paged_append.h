@@ -58,23 +58,31 @@ __device__ __forceinline__ void load_turn(Turn<T>& t, const float2* cs, int c, b
     for (int i = 0; i < VL / 4; ++i) t.t[w][i] = pg_ld(reinterpret_cast<const float4*>(cs + first) + i);
   }
 }
-// A token's positions, one per axis (those that there are not repeat the last).
-struct Place {
-  int p[4];
-  __device__ __forceinline__ int of(int axis) const {
-    return axis & 2 ? (axis & 1 ? p[3] : p[2]) : (axis & 1 ? p[1] : p[0]);
+// Positions of a warp's tokens, eight at a time, four axes of a token in neighbouring lanes (those that there are not repeat the
+// last): the angles' loads wait for one load of positions in eight tokens, not for one each.
+struct Places {
+  int v, i;
+  unsigned bad;
+  __device__ __forceinline__ Places() : v(0), i(-1), bad(0) {}
+  // The next token's, `token` of the call; its warp's others follow it `stride` apart and end before `end`.  A whole warp calls it;
+  // false, and the error bit, if one is outside the table.
+  __device__ __forceinline__ bool next(const AppendArgs& a, int token, int stride, int end) {
+    const int lane = threadIdx.x & 31;
+    if ((++i & 7) == 0) {
+      const int t = token + (lane >> 2) * stride;
+      v = t < end ? pg_ld(a.pos + (int64_t)t * a.n_axes + min(lane & 3, a.n_axes - 1)) : 0;
+      bad = __ballot_sync(0xffffffffu, v < 0 || v >= a.rope_positions);
+    }
+    const bool ok = (bad >> (4 * (i & 7)) & 15) == 0;
+    if (!ok && lane == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
+    return ok;
   }
+  // The token's position on an axis of the lane's own.
+  __device__ __forceinline__ int of(int axis) const { return __shfl_sync(0xffffffffu, v, 4 * (i & 7) + axis); }
 };
-__device__ __forceinline__ bool load_place(const AppendArgs& a, int64_t token, Place& at) {
-  bool ok = true;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    at.p[i] = i < a.n_axes ? pg_ld(a.pos + token * a.n_axes + i) : at.p[i > 0 ? i - 1 : 0];
-    ok = ok && at.p[i] >= 0 && at.p[i] < a.rope_positions;
-  }
-  if (!ok && (threadIdx.x & 31) == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
-  return ok;
-}
+// How positions are given: slots; several axes, with each lane's VL / 2 pairs of a vector on one of them (kFlat: sections side by
+// side); several axes in any order.
+enum { kSlots = 0, kFlat = 1, kAny = 2 };
 // The axes of a lane's pairs, two bits each: VL / 2 pairs from `first`, for both w.
 template <typename T, int D>
 __device__ __forceinline__ uint32_t lane_axes(const AppendArgs& a, int c, bool half) {
@@ -92,21 +100,27 @@ __device__ __forceinline__ uint32_t lane_axes(const AppendArgs& a, int c, bool h
   }
   return bits;
 }
-template <typename T, int D>
-__device__ __forceinline__ void load_turn_axes(Turn<T>& t, const float2* rope, const Place& at, uint32_t axes, int c, bool half) {
+// (A whole warp calls it.)
+template <typename T, int D, int kAxes>
+__device__ __forceinline__ void load_turn_axes(Turn<T>& t, const float2* rope, const Places& at, uint32_t axes, int c, bool half) {
   constexpr int VL = Vec<T>::N;
+  if constexpr (kAxes == kFlat) {
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+    for (int w = 0; w < 2; ++w) {
+      const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+      const float2* row = rope + (int64_t)at.of(axes >> (w * VL) & 3) * (D / 2) + first;
 #pragma unroll
-    for (int i = 0; i < VL / 4; ++i) {
-      const int sh = 2 * (w * (VL / 2) + 2 * i), j = first + 2 * i;
-      const int p0 = at.of(axes >> sh & 3), p1 = at.of(axes >> (sh + 2) & 3);
-      const float2* r0 = rope + (int64_t)p0 * (D / 2) + j;
-      if (p0 == p1) {
-        t.t[w][i] = pg_ld(reinterpret_cast<const float4*>(r0));
-      } else {
-        const uint2 x = pg_ld(reinterpret_cast<const uint2*>(r0));
+      for (int i = 0; i < VL / 4; ++i) t.t[w][i] = pg_ld(reinterpret_cast<const float4*>(row) + i);
+    }
+  } else {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int first = half ? c * VL + w * (VL / 2) : (w * (D / 2) + c * VL) / 2;
+#pragma unroll
+      for (int i = 0; i < VL / 4; ++i) {
+        const int sh = 2 * (w * (VL / 2) + 2 * i), j = first + 2 * i;
+        const int p0 = at.of(axes >> sh & 3), p1 = at.of(axes >> (sh + 2) & 3);
+        const uint2 x = pg_ld(reinterpret_cast<const uint2*>(rope + (int64_t)p0 * (D / 2) + j));
         const uint2 y = pg_ld(reinterpret_cast<const uint2*>(rope + (int64_t)p1 * (D / 2) + j + 1));
         t.t[w][i] = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(y.x), __uint_as_float(y.y));
       }
@@ -200,25 +214,29 @@ __device__ __forceinline__ bool find_run(const AppendArgs& a, int& b, int& j) {
 }
 
 // Column group `group` of the queries of tokens at slots [p, end), every `stride`th.
-template <typename T, int D, bool kAxes>
+template <typename T, int D, int kAxes>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, const Row& r, const T* q, T* q_out, int group, int p, int end,
                                                int stride, int p0) {
   constexpr int VL = Vec<T>::N;
   constexpr int PH = D / 2 / VL;          // vector pairs of a head
   const int col = group * 32 + (threadIdx.x & 31);
-  if (col >= a.q_cols) return;
+  const bool have = col < a.q_cols;
+  if (!kAxes && !have) return;            // (with axes a warp stays whole)
   const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
   const uint32_t axes = kAxes ? lane_axes<T, D>(a, col % PH, a.half) : 0;
+  Places places;
   for (; p < end; p += stride) {
     Vec<T> x, y;
     Turn<T> cs;
-    Place at;
-    if (kAxes && !load_place(a, r.t0 + p - p0, at)) continue;
     const T* src = q + (int64_t)(r.t0 + p - p0) * a.q_stride + off;
-    x.u = *reinterpret_cast<const uint4*>(src);
-    y.u = *reinterpret_cast<const uint4*>(src + D / 2);
-    if (kAxes) load_turn_axes<T, D>(cs, a.rope, at, axes, col % PH, a.half);
+    if (have) {
+      x.u = *reinterpret_cast<const uint4*>(src);
+      y.u = *reinterpret_cast<const uint4*>(src + D / 2);
+    }
+    if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
+    if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, col % PH, a.half);
     else load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), col % PH, a.half);
+    if (kAxes && !have) continue;
     turn<T>(x, y, cs, a.half);
     T* dst = q_out + (int64_t)(r.t0 + p - p0) * a.H * D + off;
     *reinterpret_cast<uint4*>(dst) = x.u;
@@ -242,6 +260,14 @@ inline void set_axes(AppendArgs& a, const kvc_rope_axes& axes, const int32_t* po
   a.pos = positions;
   a.n_axes = axes.n_axes;
   for (int j = 0; j < head_dim / 2; ++j) a.pair_axis[j >> 4] |= (uint32_t)axes.pair_axis[j] << (2 * (j & 15));
+}
+// The kind of an append: kSlots, kFlat or kAny, for vectors of `vl` elements.
+inline int axes_kind(const AppendArgs& a, int head_dim, int vl) {
+  if (a.pos == nullptr) return kSlots;
+  auto axis = [&](int j) { return a.pair_axis[j >> 4] >> (2 * (j & 15)) & 3; };
+  for (int j = 0; j < head_dim / 2; ++j)
+    if (axis(j) != axis(j - j % (vl / 2))) return kAny;
+  return kFlat;
 }
 
 }  // namespace
