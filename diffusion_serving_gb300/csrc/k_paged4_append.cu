@@ -4,7 +4,7 @@
 // apart in one head, so four neighbouring lanes hold two groups of 32 dims that share a scale: two shuffles
 // find a group's largest magnitude, and each lane's 8 codes make one 32-bit word.  The quotient x / s decides the code and
 // ties are common (both have few bits), so it has to be exact where it is exact: q = x (1 / s), and one residual step
-// q + (x - q s) (1 / s), gives the correctly rounded quotient (1 / s is).  |x| <= 7 s by then, so nothing overflows.
+// q + (x - q s) (1 / s), gives the correctly rounded quotient (1 / s is).
 // Bound by HBM for prompts and by latency for a step's few tokens.
 //
 // Read: a lane takes a word of 8 dims of the key and of the value, 4 + 1 bytes in and 16 bytes out each.
@@ -31,21 +31,29 @@ __device__ __forceinline__ uint32_t scale_bits(float top) {
   return b & 0xFFu;
 }
 template <typename T>
-__device__ __forceinline__ uint32_t code_word(const Vec<T>& x, uint32_t bits) {
+__device__ __forceinline__ uint32_t code_word(const Vec<T>& x, uint32_t bits, float top) {
   const uint32_t h = pg4_e4m3x2(bits, (const __half*)nullptr);
   const float s = __half2float(*reinterpret_cast<const __half*>(&h));
   if (s == 0.f) return 0x88888888u;
   const float inv = __frcp_rn(s), most = 7.f * s;
-  uint32_t w = 0;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f(x.e[i]);
+  if (!(top < 7.5f * s)) {                         // (the scale is at its end, or has few bits: else nothing rounds past 7)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -most), most);
+  }
+  // 1.5 2^23 + 8 + q rounds to a whole number, whose low bits are the code; what is above them is taken off all eight at once
+  uint32_t w = 0, magic = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = fminf(fmaxf(to_f(x.e[i]), -most), most);
-    const float q0 = v * inv;
-    const float q = __fmaf_rn(__fmaf_rn(-q0, s, v), inv, q0);
-    // 1.5 2^23 + 8 + q: rounded to a whole number, whose low bits are the code
-    w |= (__float_as_uint(q + 12582920.f) & 0xFu) << (4 * (i >> 1) + 16 * (i & 1));
+    const int at = 4 * (i >> 1) + 16 * (i & 1);
+    const float q0 = v[i] * inv;
+    const float q = __fmaf_rn(__fmaf_rn(-q0, s, v[i]), inv, q0);
+    w += __float_as_uint(q + 12582920.f) << at;
+    magic += 0x4B400000u << at;
   }
-  return w;
+  return w - magic;
 }
 template <typename T>
 __device__ __forceinline__ Held<T> hold(const Vec<T>& x, const Vec<T>& y) {
@@ -63,8 +71,8 @@ __device__ __forceinline__ Held<T> hold(const Vec<T>& x, const Vec<T>& y) {
   Held<T> r;
   r.s0 = scale_bits(m0);
   r.s1 = scale_bits(m1);
-  r.w0 = code_word(x, r.s0);
-  r.w1 = code_word(y, r.s1);
+  r.w0 = code_word(x, r.s0, m0);
+  r.w1 = code_word(y, r.s1, m1);
   return r;
 }
 
