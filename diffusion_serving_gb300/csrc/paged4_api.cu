@@ -31,8 +31,19 @@ kvc_pg4_layout workspace_of(const kvc_paged_config& g) {
   return w;
 }
 
-// Few query rows per group go to the streaming kernel, more to the tensor-core kernel.
-bool few_rows(const kvc_pg_args& a) { return (int64_t)a.max_q * a.Gv <= 16; }
+// Up to 16 query rows per group are one pass of the streaming kernel over a row's keys.  More make several passes there, which
+// still beat the tensor-core kernel where they are few and short in all (four, 128 or 512 items of a head's rows, and 768 K or 4 M slots over
+// them, for heads of 128 or 64).  32 heads over 8, streaming and tensor-core kernel: 32 rows a group, heads of 128: 18 and 24 us
+// for a batch of 1 over 8000 slots, 21 and 29 for 8 over 2000, but 38 and 27 for 32 over 600, 183 and 165 for 32 over 8000; heads of
+// 64: 32 and 50 for 8 over 8000, 102 and 141 for 32 over 8000; 64 rows: 12 and 22 for 1 over 8000 of 64 dims, 25 and 16 for 8 over 600 of
+// 128.  Lengths are on the device: the slots are those that the table has columns for.
+bool few_rows(const kvc_pg_args& a, int head_dim) {
+  const int T = 16 / a.Gv;                             // tokens to an item
+  const int64_t passes = ((int64_t)a.max_q + T - 1) / T, items = a.B * (int64_t)a.Hv * passes;
+  if (passes == 1) return true;
+  const bool d64 = head_dim == 64;
+  return passes <= 4 && items <= (d64 ? 512 : 128) && items * ((int64_t)a.max_pages << a.ps_log2) <= (d64 ? 4 << 20 : 768 << 10);
+}
 
 }  // namespace
 
@@ -132,7 +143,7 @@ int kvc_paged4_attend(kvc_paged4* c, const void* q, void* out, float* d_lse, int
   a.max_q = d_cu != nullptr ? max_q : n_tokens / g.batch;
   a.causal = (flags & KVC_CAUSAL) != 0;
   const cudaStream_t s = as_stream(stream);
-  return launched(few_rows(a) ? kvc_pg4_launch_decode(c, a, q, out, s) : kvc_pg4_launch_tc(c, a, q, out, s));
+  return launched(few_rows(a, g.head_dim) ? kvc_pg4_launch_decode(c, a, q, out, s) : kvc_pg4_launch_tc(c, a, q, out, s));
 }
 
 int kvc_paged4_get_error(kvc_paged4* c, void* stream, int32_t* bits) {
