@@ -66,7 +66,9 @@ struct Smem {
   uint64_t drain[2];
   uint64_t desc_full[2];
   Desc desc[2];
-  float q_scale[2][kBM];   // of an item's scores, to log2 units
+  // of an item's scores, to log2 units.  Four: item n's are written once the products of item n - 1 with K are done, and then
+  // the softmax, two tiles behind them at most, may be about to read item n - 2's (items of a tile each).
+  float q_scale[4][kBM];
   // records of a tile that no page stands behind: the producer is at most four tiles ahead of the softmax (two of records,
   // two of K tiles)
   uint32_t bad[kBadRing];
@@ -431,7 +433,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
           for (int c = 0; c < 8; ++c) top = pg4_query_top<T>(*reinterpret_cast<const uint4*>(sm.q[h] + r * 128 + 16 * (c ^ (r & 7))), top);
         }
         const float f = pg4_query_factor(top, &undo);
-        sm.q_scale[n & 1][r] = undo * a.scale_log2;
+        sm.q_scale[n & 3][r] = undo * a.scale_log2;
 #pragma unroll 1
         for (int h = 0; h < HB; ++h) {
 #pragma unroll 4
@@ -490,7 +492,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
                                          (t < 2 || await(&sm.pv_done[sb], ((t >> 1) - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
-        if (j == 0) c = sm.q_scale[n & 1][r];
+        if (j == 0) c = sm.q_scale[n & 3][r];
         const int valid = limit - j * kBN;
         const uint32_t bad = sm.bad[t % kBadRing];
         if (bad) {                                      // slots without a page: their scores become -inf where they are
