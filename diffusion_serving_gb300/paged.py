@@ -50,7 +50,7 @@ def rope_axes(pair_axis, n_axes=None) -> kvc_rope_axes:
         raise ValueError(f"kvc: rope_axes takes an axis from 0 to {n - 1} (at most 4 axes) for each of up to 64 pairs")
     a = kvc_rope_axes(n_axes=n)
     a.pair_axis[:len(pair_axis)] = pair_axis
-    a.pairs = len(pair_axis)
+    a.pairs, a.ref = len(pair_axis), ctypes.byref(a)
     return a
 
 
@@ -297,15 +297,17 @@ class PagedKVCache:
 
     def _append_args(self, k, v, cu_new, rope, half, q, q_out, positions, axes, stream):
         n, stride = self._rows("k", k, self.kv_heads)
-        nv, vstride = self._rows("v", v, self.kv_heads)
-        if n != nv or stride != vstride:
-            raise ValueError(f"kvc: k and v must have the same rows and strides ({n}, {stride} and {nv}, {vstride})")
+        if v.shape != k.shape or v.stride() != k.stride() or v.dtype is not self.dtype or v.get_device() != self._index:
+            nv, vstride = self._rows("v", v, self.kv_heads)
+            if n != nv or stride != vstride:
+                raise ValueError(f"kvc: k and v must have the same rows and strides ({n}, {stride} and {nv}, {vstride})")
         n_pos, rp = 0, None
         if rope is not None:
-            if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.numel() != len(rope) * self.head_dim or \
-                    rope.shape[2] != 2 or rope.get_device() != self._index or not rope.is_contiguous():
+            s = rope.shape
+            if rope.dtype is not torch.float32 or len(s) != 3 or 2 * s[1] != self.head_dim or s[2] != 2 or \
+                    rope.get_device() != self._index or not rope.is_contiguous():
                 raise ValueError(f"kvc: rope must be a dense float32 [positions, {self.head_dim // 2}, 2] on {self.device}")
-            n_pos, rp = len(rope), rope.data_ptr()
+            n_pos, rp = s[0], rope.data_ptr()
         qp = op = None
         q_stride = 0
         if q is not None:
@@ -335,13 +337,13 @@ class PagedKVCache:
             raise ValueError(f"kvc: axes must name an axis for each of the {self.head_dim // 2} pairs of a head, got {axes.pairs}")
         s = positions.shape
         if positions.dtype is not torch.int32 or positions.get_device() != self._index or not positions.is_contiguous() or \
-                s[-1:] != (axes.n_axes,) or positions.numel() != n * axes.n_axes or \
-                not (len(s) == 2 or len(s) == 3 and s[0] == self.batch):
+                not (len(s) == 2 and s[0] == n or len(s) == 3 and s[0] == self.batch and s[0] * s[1] == n) or \
+                s[-1] != axes.n_axes:
             raise ValueError(f"kvc: positions must be a dense int32 [{n}, {axes.n_axes}] (or [{self.batch}, n, {axes.n_axes}]) "
                              f"on {self.device}, got {list(s)} {positions.dtype} on {positions.device}")
         if rope is None:
             raise ValueError("kvc: positions without rope")
-        return ctypes.byref(axes), positions.data_ptr()
+        return axes.ref, positions.data_ptr()
 
     @property
     def _one_axis(self):
