@@ -90,7 +90,7 @@ __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* 
 }
 
 // One warp's 32 slots of a tile: records to rows of operand tiles (64 dims each, 128-byte swizzle).  A lane takes 32 dims of a slot
-// at a time; eight neighbouring lanes two such pieces of four slots, whose 16-byte stores meet in no bank.
+// at a time; which ones eight neighbouring lanes have is such that neither their loads nor their stores of 16 bytes meet in a bank.
 template <int D>
 struct Expand {
   static constexpr int W = D / 32;                 // pieces of a slot
@@ -105,8 +105,9 @@ struct Expand {
   __device__ __forceinline__ void init(int warp, int lane, int ps_log2, bool is_v) {
     const int ps = 1 << ps_log2;
     const uint32_t record = (uint32_t)kvc_pg4_record(D, ps_log2);
-    piece = (lane & 1) | (W == 4 ? lane >> 2 & 2 : 0);
-    slot0 = 32 * warp + ((lane >> 1 & 3) | (W == 4 ? lane >> 2 & 4 : lane >> 1 & 12));
+    // Eight neighbouring lanes: two pieces of four slots, or (D = 128) pieces 0 and 1 of two slots and 2 and 3 of the next two.
+    piece = W == 4 ? lane >> 1 & 3 : lane & 1;
+    slot0 = 32 * warp + (W == 4 ? (lane & 1) | ((lane >> 1 ^ lane >> 2) & 2) | (lane >> 2 & 4) : lane >> 1);
     turn = slot0 & 7;
     row = (piece >> 1) * kBoxBytes + slot0 * 128;
     const int rec = slot0 >> ps_log2, s0 = slot0 & (ps - 1);
