@@ -22,6 +22,12 @@
 // The running maximum of a query is looked for only when a weight outgrows its reference by 2^7 (one vote per tile);
 // weights are taken 2^8 too large, so that fp16 holds them with full precision down to 2^-22 of the reference, and
 // rounded to fp16 once for the product with V (their sum takes them unrounded).
+//
+// Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 76 us, 3.8 TB/s of codes and scales,
+// 0.56 of a plain copy (the 16-bit kernel 171 us); 2 rows of 100001 and 131072 slots, pages of 64: 62 us, 4.1 TB/s.  Bound by the
+// consumers' instructions and their latency: 325 a warp for 16 slots of 128 dims, issue slots 58 % busy; of 67 us (32 rows of 8192) the
+// copies by themselves take 52, the products with K and with V 18 each, waits and work split 16.  More warps of fewer registers
+// (four sets: spills) took 94 us, fewer (two sets) 68; nine stages for six changed nothing.  One row of 490 slots: 8 us.
 #include "paged4_internal.h"
 #include "paged_finish.h"
 #include "paged_ptx.h"
