@@ -136,7 +136,7 @@ __device__ __forceinline__ void pg4_fast_pairs(uint32_t word, const kvc_pg4_fast
 // A row of queries as fp16, times a power of 2 that brings its largest element to 2^10 .. 2^11, and 16 times that at the dims of
 // pairs 0 and 2, whose keys come out too small.  Elements are exact down to 2^-25 of the largest, and below it off by 2^-36 of
 // it at most; held magnitudes span less than 2^21, so a score is off by less than 2^-15 of the sum of its terms' magnitudes, at
-// queries and keys made for it.
+// queries and keys made for it.  (A row whose largest element is below 2^-110 is brought up by 2^120 and no more.)
 __device__ __forceinline__ uint32_t pg4_pack(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -329,6 +329,30 @@ def test_calls_between_a_wait_that_ran_out_and_the_report(what):
             assert torch.equal(x, y) and torch.equal(x, z)
 
 
+def test_reading_keys_or_values_alone_and_queries_turned_in_place():
+    """By the C entry: either output may be missing.  q_out may be q where its rows are dense."""
+    c, table, g, k, v = make(2, 4, 2, 64, BF16, 16, [20, 37], seed=26)
+    cu, n = ints([0, 20, 57]), 57
+    want = c.read(n, cu=cu)
+    for i in range(2):
+        out = torch.full((n, 2, 64), 7.0, dtype=BF16, device="cuda")
+        ptr = [None, None]
+        ptr[i] = out.data_ptr()
+        assert kvc._lib.kvc_paged4_read(c.handle, *ptr, n, cu.data_ptr(), torch.cuda.current_stream().cuda_stream) == kvc.OK
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want[i]))
+    assert kvc._lib.kvc_paged4_read(c.handle, None, None, n, cu.data_ptr(), None) == kvc.ERR_ARG
+    q = randn(g, n, 4, 64, dtype=BF16).cuda()
+    kn, rope = randn(g, n, 2, 64, dtype=BF16).cuda(), wl.rope_table(64, 64).cuda()
+    pos = torch.randint(0, 64, (n, 2), generator=g, dtype=torch.int32).cuda()
+    for kw in (dict(), dict(positions=pos, axes=paged.rope_axes([j % 2 for j in range(32)])), dict(positions=pos, axes=paged.rope_axes([0] * 16 + [1] * 16))):
+        turned_q = c.append(kn, kn, cu_new=cu, rope=rope, q=q, **kw)
+        same = q.clone()
+        assert c.append(kn, kn, cu_new=cu, rope=rope, q=same, q_out=same, **kw) is same
+        assert torch.equal(bits(same), bits(turned_q))
+    assert c.get_error() == 0
+
+
 def test_refusals():
     c, table, g, k, v = make(2, 4, 2, 64, BF16, 16, [20, 20], seed=25)
     q = randn(g, 2, 4, 64, dtype=BF16).cuda()
