@@ -5,8 +5,9 @@
 // find a group's largest magnitude, and each lane's 8 codes make one 32-bit word.  The quotient x / s decides the code and
 // ties are common (both have few bits), so it has to be exact where it is exact: q = x (1 / s), and one residual step
 // q + (x - q s) (1 / s), gives the correctly rounded quotient (1 / s is).
-// 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 54 us, 3.3 TB/s; bound by the rotation's
-// and the codes' arithmetic (issue slots 62 % busy, with the branches of the exact rotation).  A step of 32 rows: 4.2 us replayed.
+// 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 47 us, 3.8 TB/s; bound by the rotation's
+// and the codes' arithmetic (with a branch per component of a rotated pair, not per pair, 54 us, issue slots 62 % busy).  A step of 32
+// rows: 4.0 us replayed.
 //
 // Read: a lane takes a word of 8 dims of the key and of the value, 4 + 1 bytes in and 16 bytes out each.  8288 tokens: 10.5 us, 4.1
 // TB/s; a step's 32: 2.2 us replayed.

@@ -140,9 +140,10 @@ __device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const Turn<T>& cs, bo
       const float co = i & 1 ? t[i / 2].z : t[i / 2].x, si = i & 1 ? t[i / 2].w : t[i / 2].y;
       T& e0 = half ? x.e[w * (VL / 2) + i] : (w ? y : x).e[2 * i];
       T& e1 = half ? y.e[w * (VL / 2) + i] : (w ? y : x).e[2 * i + 1];
-      const float a = to_f(e0), b = to_f(e1);
-      from_f(e0, pg_rot(a, co, b, si, type));
-      from_f(e1, pg_rot(a, si, b, -co, type));
+      float u, v;
+      pg_rot_pair(to_f(e0), to_f(e1), co, si, &u, &v, type);
+      from_f(e0, u);
+      from_f(e1, v);
     }
   }
 }

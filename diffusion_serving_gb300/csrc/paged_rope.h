@@ -88,3 +88,31 @@ __device__ __forceinline__ float pg_rot(float a, float b, float c, float d, cons
                   __fadd_rn(r, __fadd_rn(e, slack)) == r && __fadd_rn(r, __fsub_rn(e, slack)) == r;
   return ok ? r : pg_rot_f32(a, b, c, d);
 }
+
+// Both components of a rotated pair, a co - b si and a si + b co, as pg_rot has them.
+__device__ __forceinline__ void pg_rot_pair(float a, float b, float co, float si, float* x, float* y, const float* type) {
+  *x = pg_rot(a, co, b, si, type);
+  *y = pg_rot(a, si, b, -co, type);
+}
+// 16-bit stores: one test and one branch for the two.  r2 stands where |p| <= 2^20 |r2| and |r2| >= 2^-60 (an inexact e, where
+// |c d| < 2^-100, is off by 2^-149 at most then, nothing next to an ulp of r2) and r2 is clear of midpoints; all else, zeros
+// too, goes by pg_rot.
+template <typename T>
+static __device__ __noinline__ float pg_rot_careful(float a, float b, float c, float d) {
+  return pg_rot(a, b, c, d, (const T*)nullptr);
+}
+__device__ __forceinline__ bool pg_safe(float r, const __nv_bfloat16* t) { return pg_clear(r, t) && fabsf(r) >= 0x1p-60f; }
+__device__ __forceinline__ bool pg_safe(float r, const __half* t) { return pg_clear(r, t); }   // (clear from 2^-14 on alone)
+template <typename T>
+__device__ __forceinline__ void pg_rot_pair(float a, float b, float co, float si, float* x, float* y, const T* type) {
+  const float p = __fmul_rn(b, si), q = __fmul_rn(b, -co);
+  const float r = __fsub_rn(__fmaf_rn(a, co, -p), __fmaf_rn(b, si, -p));
+  const float s = __fsub_rn(__fmaf_rn(a, si, -q), __fmaf_rn(b, -co, -q));
+  *x = r;
+  *y = s;
+  const bool ok = fabsf(p) <= fabsf(r) * 0x1p20f && fabsf(q) <= fabsf(s) * 0x1p20f && pg_safe(r, type) && pg_safe(s, type);
+  if (!ok) {
+    *x = pg_rot_careful<T>(a, co, b, si);
+    *y = pg_rot_careful<T>(a, si, b, -co);
+  }
+}
