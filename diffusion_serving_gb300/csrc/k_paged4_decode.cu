@@ -58,7 +58,7 @@ struct Smem {
   float q_scale[2][R];                            // of their scores, to log2 units
   float2 ml[kWarps<R>][R];
   int64_t at[2][R];                               // rows of the outputs
-  int limit[2][R];                                // where each query row's keys end
+  int limit[2][R];                                // where each query row's keys end (rows that are not there: all)
   kvc_pg_end end[2];
   int tiles[2];                                   // this block's tiles of the item; -1: there is none
   int key0[2];                                    // position of the first one's first slot
@@ -238,14 +238,16 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
       }
       const kvc_pg_end e = pg_end(a, sch, it);
       int64_t at = 0;
-      int limit = 0x3fffffff;                               // rows that are not there see everything (no mask on their account)
+      // Query rows that are not there see the row's slots: what stands behind them must not decide, by a NaN, when the warps look
+      // for new references.
+      int limit = it.r.len;
       if (lane < R) {
         at = pg_at(a, sch, it, lane < e.rows ? lane : 0);
         sm.at[b][lane] = at;
         if (lane < e.rows) limit = pg_limit(a, it.r, it.k * sch.T + lane / a.Gv);
         sm.limit[b][lane] = limit;
       }
-      const int open = min(it.r.len, __reduce_min_sync(0xffffffffu, limit));
+      const int open = __reduce_min_sync(0xffffffffu, limit);
       if (lane == 0) {
         sm.end[b] = e;
         sm.tiles[b] = it.tile1 - it.tile0;

@@ -126,6 +126,30 @@ def test_long_chunks_of_whole_and_cut_items(dtype, heads, kv_heads, dim, page, l
             ref.check(out[t:t + 1], lse[t:t + 1], got, f"token {t}")
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_what_shared_memory_held_before_decides_nothing(dim):
+    """Slots behind a row's end in a tile are not brought in: query rows that an item does not have (3 of 5 heads' tokens in 16 rows)
+    meet there what an earlier block left.  The same call gives the same bits whatever ran before it."""
+    lens, new = [1552, 353, 2475, 546, 349], [4, 2, 2, 1, 4]
+    c, g, _, _ = big(lens, 40, 8, dim, BF16, 16, seed=31)
+    cu = wl.seqlens_to_cu(new)
+    q = (3 * torch.randn(cu[-1], 40, dim, device="cuda", generator=g)).to(BF16)
+    noise = paged4.PagedKVCache4(64, 8, 8, dim, F16, page_size=16, n_pages=64 * 40, max_pages=40)
+    noise.block_table.copy_(torch.arange(64 * 40, dtype=torch.int32).reshape(64, 40))
+    noise.kv_len.fill_(640)
+    qn = torch.randn(64, 8, dim, device="cuda", generator=g).half()
+    args = dict(cu_q=ints(cu), max_q=max(new), lse=True)
+    want = c.attend(q, **args)
+    for fill in (255, 127, 0, 119, 256):
+        noise.pages.copy_(torch.randint(0, 256, noise.pages.shape, device="cuda", generator=g, dtype=torch.uint8) if fill == 256
+                          else torch.full_like(noise.pages, fill))
+        for _ in range(4):
+            noise.attend(qn)
+            for x, y in zip(c.attend(q, **args), want):
+                assert torch.equal(bits(x), bits(y)), fill
+    assert c.get_error() == 0
+
+
 def test_a_batch_of_1024_rows():
     rng = np.random.default_rng(3)
     lens = [int(x) for x in rng.integers(0, 70, 1024)]
