@@ -270,7 +270,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         const int v = lane + 32 * x;
         const float f = as_half<T, VQ>(qv[x]);
         *reinterpret_cast<uint4*>(&sm.q[b][v / VQ][8 * (v % VQ)]) = qv[x];
-        if (v % VQ == 0) sm.q_scale[b][v / VQ] = f * a.scale_log2;
+        if (v % VQ == 0) sm.q_scale[b][v / VQ] = pg4_score_scale(f, a.scale_log2);
       }
       mbar_arrive(&sm.q_full[b]);
       more = sch.next(a, it);

@@ -442,7 +442,7 @@ k_paged4_tc(const __grid_constant__ CUtensorMap tm_q, const uint8_t* pool, T* __
           for (int c = 0; c < 8; ++c) top = pg4_query_top<T>(*reinterpret_cast<const uint4*>(sm.q[h] + r * 128 + 16 * (c ^ (r & 7))), top);
         }
         const float f = pg4_query_factor(top, &undo);
-        sm.q_scale[n & 3][r] = undo * a.scale_log2;
+        sm.q_scale[n & 3][r] = pg4_score_scale(undo, a.scale_log2);
 #pragma unroll 1
         for (int h = 0; h < HB; ++h) {
 #pragma unroll 4

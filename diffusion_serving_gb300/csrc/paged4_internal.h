@@ -163,6 +163,9 @@ __device__ __forceinline__ float pg4_query_factor(float top, float* undo) {
   *undo = __uint_as_float((uint32_t)(127 - up) << 23);
   return __uint_as_float((uint32_t)(127 + up) << 23);
 }
+// What takes a row's scores to log2 units.  (Never 0, which would make NaN of a masked score: a scale that is less than fp32's normal
+// range leaves scores, 2^31 at most, that no weight shows.)
+__device__ __forceinline__ float pg4_score_scale(float undo, float scale_log2) { return fmaxf(undo * scale_log2, 0x1p-126f); }
 template <typename T>
 __device__ __forceinline__ void pg4_query_vec(uint4& v, float f) {
   uint32_t* w = reinterpret_cast<uint32_t*>(&v);

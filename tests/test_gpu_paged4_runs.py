@@ -237,6 +237,17 @@ def test_queries_of_zero_and_infinity(new):
     assert np.allclose(to64(lse[:, 0]), np.log(300), atol=1e-5)
 
 
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_queries_of_zero_under_a_tiny_scale(new):
+    """A zero row is brought up by 2^120, and the scale 2^-93 times what undoes that is below fp32: masked scores stay masked."""
+    lens = [300, 45]
+    c, table, g, k, v = make(2, 4, 2, 128, BF16, 16, lens, seed=22, scale=2.0 ** -93)
+    q = torch.zeros(2 * new, 4, 128, dtype=BF16)
+    out, lse = c.attend(q.cuda(), lse=True, flags=paged.CAUSAL)
+    assert c.get_error() == 0
+    check(out, lse, expect(c, k, v, q, lens, None, True), "zero queries, tiny scale")
+
+
 def test_two_rows_may_share_pages():
     lens = [100, 100]
     c, table, g, k, v = make(2, 4, 2, 64, F16, 16, lens, seed=17)
