@@ -14,6 +14,7 @@ handle with its buffers:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -345,7 +346,7 @@ class PagedKVCache:
             raise ValueError("kvc: positions without rope")
         return axes.ref, positions.data_ptr()
 
-    @property
+    @functools.cached_property
     def _one_axis(self):
         return rope_axes([0] * (self.head_dim // 2))
 
