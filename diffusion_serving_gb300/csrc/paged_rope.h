@@ -26,6 +26,12 @@ __device__ __forceinline__ double pg_two_prod_diff(float a, float b, float c, fl
   return s;
 }
 
+__device__ __forceinline__ float pg_two_sum(float x, float y, float* err) {
+  const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
+  *err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
+  return s;
+}
+
 static __device__ __noinline__ float pg_rot_odd(float a, float b, float c, float d) {
   double rest;
   const double s = pg_two_prod_diff(a, b, c, d, &rest);
@@ -70,11 +76,6 @@ static __device__ __noinline__ float pg_rot_f32(float a, float b, float c, float
   if (s != 0.5 * (up + down)) return f;
   return rest > 0.0 ? hi : lo;
 }
-__device__ __forceinline__ float pg_two_sum(float x, float y, float* err) {
-  const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
-  *err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
-  return s;
-}
 __device__ __forceinline__ float pg_rot(float a, float b, float c, float d, const float*) {
   const float p = __fmul_rn(a, b), ep = __fmaf_rn(a, b, -p);
   const float q = __fmul_rn(c, d), eq = __fmaf_rn(c, d, -q);
@@ -95,10 +96,23 @@ __device__ __forceinline__ void pg_rot_pair(float a, float b, float co, float si
   *y = pg_rot(a, si, b, -co, type);
 }
 // 16-bit stores: one test and one branch for the two.  r2 stands where |p| <= 2^20 |r2| and |r2| >= 2^-60 (an inexact e, where
-// |c d| < 2^-100, is off by 2^-149 at most then, nothing next to an ulp of r2) and r2 is clear of midpoints; all else, zeros
-// too, goes by pg_rot.
+// |c d| < 2^-100, is off by 2^-149 at most then, nothing next to an ulp of r2) and r2 is clear of midpoints.  All else goes on:
+// the sum of both products and their errors as r + e, whose neglected rest is less than `slack`.  Where |e| exceeds that, the
+// exact value lies between r and its neighbour on e's side, and rounds to odd as pg_rot_odd has it; where all errors are 0 it is r.
+// Zeros and the rest go by pg_rot.  (At once by pg_rot, fp64 held up the fp16 store, where 1 in 25 of a warp's pairs is near a
+// midpoint.)
 template <typename T>
 static __device__ __noinline__ float pg_rot_careful(float a, float b, float c, float d) {
+  const float p = __fmul_rn(a, b), ep = __fmaf_rn(a, b, -p);
+  const float q = __fmul_rn(c, d), eq = __fmaf_rn(c, d, -q);
+  float es, e;
+  const float s = pg_two_sum(p, -q, &es);
+  const float r = pg_two_sum(s, __fadd_rn(es, __fsub_rn(ep, eq)), &e);
+  const float sum = fabsf(es) + fabsf(ep) + fabsf(eq), slack = sum * 0x1p-22f;
+  if (fminf(fabsf(p), fabsf(q)) >= 0x1p-100f && fabsf(r) >= 0x1p-60f && fabsf(r) <= 0x1p126f) {
+    if (fabsf(e) > slack) return __uint_as_float((__float_as_uint(r) - ((e > 0.f) != (r > 0.f) ? 1u : 0u)) | 1u);
+    if (sum == 0.f) return r;
+  }
   return pg_rot(a, b, c, d, (const T*)nullptr);
 }
 __device__ __forceinline__ bool pg_safe(float r, const __nv_bfloat16* t) { return pg_clear(r, t) && fabsf(r) >= 0x1p-60f; }
