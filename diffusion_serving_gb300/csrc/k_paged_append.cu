@@ -86,6 +86,13 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
       const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
       x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
       y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
+      if (p + stride < end) {
+        const int64_t next = off + stride * a.kv_stride;
+        ahead(k + next);
+        ahead(k + next + D / 2);
+        ahead(v + next);
+        ahead(v + next + D / 2);
+      }
       if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
       if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
       else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);

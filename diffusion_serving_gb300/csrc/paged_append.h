@@ -148,6 +148,9 @@ __device__ __forceinline__ void turn(Vec<T>& x, Vec<T>& y, const Turn<T>& cs, bo
   }
 }
 
+// The lines that the warp's next token will load.
+__device__ __forceinline__ void ahead(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Row b's tokens and length, checked (the error bits are set by the first block alone).
 struct Row {
   int t0, n, len;
@@ -233,6 +236,10 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const Row& r
     if (have) {
       x.u = *reinterpret_cast<const uint4*>(src);
       y.u = *reinterpret_cast<const uint4*>(src + D / 2);
+      if (p + stride < end) {
+        ahead(src + stride * a.q_stride);
+        ahead(src + stride * a.q_stride + D / 2);
+      }
     }
     if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
     if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, col % PH, a.half);
