@@ -95,8 +95,9 @@ __device__ __forceinline__ void pg_rot_pair(float a, float b, float co, float si
   *x = pg_rot(a, co, b, si, type);
   *y = pg_rot(a, si, b, -co, type);
 }
-// 16-bit stores: one test and one branch for the two.  r2 stands where |p| <= 2^20 |r2| and |r2| >= 2^-60 (an inexact e, where
-// |c d| < 2^-100, is off by 2^-149 at most then, nothing next to an ulp of r2) and r2 is clear of midpoints.  All else goes on:
+// 16-bit stores: one test and one branch for the two.  r2 stands where |p| <= 2^20 |r2| (each p of each r2) and |r2| >= 2^-60 (an
+// inexact e, where |c d| < 2^-100, is off by 2^-149 at most then, nothing next to an ulp of r2; in fp16 where it is normal) and
+// r2 is clear of midpoints.  All else goes on:
 // the sum of both products and their errors as r + e, whose neglected rest is less than `slack`.  Where |e| exceeds that, the
 // exact value lies between r and its neighbour on e's side, and rounds to odd as pg_rot_odd has it; where all errors are 0 it is r.
 // Zeros and the rest go by pg_rot.  (At once by pg_rot, fp64 held up the fp16 store, where 1 in 25 of a warp's pairs is near a
@@ -115,8 +116,11 @@ static __device__ __noinline__ float pg_rot_careful(float a, float b, float c, f
   }
   return pg_rot(a, b, c, d, (const T*)nullptr);
 }
-__device__ __forceinline__ bool pg_safe(float r, const __nv_bfloat16* t) { return pg_clear(r, t) && fabsf(r) >= 0x1p-60f; }
-__device__ __forceinline__ bool pg_safe(float r, const __half* t) { return pg_clear(r, t); }   // (clear from 2^-14 on alone)
+// The least |r2| taken, and whether low bits are clear of the type's midpoint (pg_clear's test, as one shift-and-add).
+__device__ __forceinline__ constexpr float pg_least(const __nv_bfloat16*) { return 0x1p-60f; }
+__device__ __forceinline__ constexpr float pg_least(const __half*) { return 0x1p-14f; }
+__device__ __forceinline__ bool pg_off_midpoint(float r, const __nv_bfloat16*) { return (__float_as_uint(r) << 16) - (0x7FFEu << 16) > 4u << 16; }
+__device__ __forceinline__ bool pg_off_midpoint(float r, const __half*) { return (__float_as_uint(r) << 19) - (0x0FFEu << 19) > 4u << 19; }
 template <typename T>
 __device__ __forceinline__ void pg_rot_pair(float a, float b, float co, float si, float* x, float* y, const T* type) {
   const float p = __fmul_rn(b, si), q = __fmul_rn(b, -co);
@@ -124,8 +128,8 @@ __device__ __forceinline__ void pg_rot_pair(float a, float b, float co, float si
   const float s = __fsub_rn(__fmaf_rn(a, si, -q), __fmaf_rn(b, -co, -q));
   *x = r;
   *y = s;
-  const bool ok = fabsf(p) <= fabsf(r) * 0x1p20f && fabsf(q) <= fabsf(s) * 0x1p20f && pg_safe(r, type) && pg_safe(s, type);
-  if (!ok) {
+  const float most = fmaxf(fmaxf(fabsf(p), fabsf(q)), pg_least(type) * 0x1p20f);
+  if (!(fminf(fabsf(r), fabsf(s)) * 0x1p20f >= most && pg_off_midpoint(r, type) && pg_off_midpoint(s, type))) {
     *x = pg_rot_careful<T>(a, co, b, si);
     *y = pg_rot_careful<T>(a, si, b, -co);
   }
