@@ -3,7 +3,7 @@
 // Append: the runs, lanes and loads of the 16-bit append (k_paged_append.cu).  A lane has two vectors of 8 dims, D/2
 // apart in one head, so four neighbouring lanes hold two groups of 32 dims that share a scale: two shuffles
 // find a group's largest magnitude, and each lane's 8 codes make one 32-bit word.  The quotient x / s decides the code, and
-// ties are common (both have few bits): x (1 / s) is off by 2^-21, which a fused sum with 96 rounds off again (to
+// ties are common (both have few bits): x (1 / s), with 1 / s off by an ulp, is off by 2^-20, which a fused sum with 96 rounds off again (to
 // 2^-17: x / s is a tie, or 2^-13 away from one), and the sum of that with 1.5 2^23 goes to the whole number, ties to even.
 // 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 47 us, 3.8 TB/s; bound by the rotation's
 // and the codes' arithmetic (with a branch per component of a rotated pair, not per pair, 54 us, issue slots 62 % busy).  A step of 32
@@ -17,32 +17,49 @@
 namespace {
 
 // Code words of a lane's 8 dims x and of its 8 dims y, and their groups' scales, among four lanes.
-template <typename T>
 struct Held {
   uint32_t w0, w1;
   uint32_t s0, s1;        // e4m3 bits
 };
-__device__ __forceinline__ float pick_abs(float m, float x) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(m), "f"(fabsf(x)));
-  return y;
+// Of pairs; a NaN goes on.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, const __half*) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
-// e4m3 of top / 7, to nearest even, 448 at most (a NaN stays one)
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, const __nv_bfloat16*) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t top2(const uint4& v) {
+  const T* t = nullptr;
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  return max2(max2(v.x & kAbs, v.y & kAbs, t), max2(v.z & kAbs, v.w & kAbs, t), t);
+}
+// e4m3 of top / 7, to nearest even, 448 at most (a NaN stays one).  The quotient is right by one residual step: ties are common.
 __device__ __forceinline__ uint32_t scale_bits(float top) {
+  float x;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(top), "f"(4096.f));
+  constexpr float kInv = 1.f / 7.f;
+  const float q0 = x * kInv, q = __fmaf_rn(__fmaf_rn(-7.f, q0, x), kInv, q0);
   uint16_t b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(__fdiv_rn(top, 7.f)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(q));
   return b & 0xFFu;
 }
 template <typename T>
 __device__ __forceinline__ uint32_t code_word(const Vec<T>& x, uint32_t bits, float top) {
   const uint32_t h = pg4_e4m3x2(bits, (const __half*)nullptr);
   const float s = __half2float(*reinterpret_cast<const __half*>(&h));
-  if (s == 0.f) return 0x88888888u;
-  const float inv = __frcp_rn(s), most = 7.f * s;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  if (s == 0.f) inv = 0.f;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = to_f(x.e[i]);
   if (!(top < 7.5f * s)) {                         // (the scale is at its end, or has few bits: else nothing rounds past 7)
+    const float most = 7.f * s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -most), most);
   }
@@ -58,23 +75,18 @@ __device__ __forceinline__ uint32_t code_word(const Vec<T>& x, uint32_t bits, fl
   return w - magic;
 }
 template <typename T>
-__device__ __forceinline__ Held<T> hold(const Vec<T>& x, const Vec<T>& y) {
-  float m0 = 0.f, m1 = 0.f;
+__device__ __forceinline__ Held hold(const Vec<T>& x, const Vec<T>& y) {
+  const T* t = nullptr;
+  const uint32_t mx = top2<T>(x.u), my = top2<T>(y.u);
+  uint32_t m = max2(__byte_perm(mx, my, 0x5410), __byte_perm(mx, my, 0x7632), t);      // (x's, y's)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m0 = pick_abs(m0, to_f(x.e[i]));
-    m1 = pick_abs(m1, to_f(y.e[i]));
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    m0 = pick_abs(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-    m1 = pick_abs(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-  }
-  Held<T> r;
-  r.s0 = scale_bits(m0);
-  r.s1 = scale_bits(m1);
-  r.w0 = code_word(x, r.s0, m0);
-  r.w1 = code_word(y, r.s1, m1);
+  for (int o = 1; o < 4; o <<= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o), t);
+  const float2 top = pg4_floats(m, t);
+  Held r;
+  r.s0 = scale_bits(top.x);
+  r.s1 = scale_bits(top.y);
+  r.w0 = code_word(x, r.s0, top.x);
+  r.w1 = code_word(y, r.s1, top.y);
   return r;
 }
 
@@ -136,7 +148,7 @@ k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, 
     vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
     vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
     if (kAxes || a.rope != nullptr) turn<T>(x, y, cs, a.half);
-    const Held<T> hk = hold(x, y), hv = hold(vx, vy);
+    const Held hk = hold(x, y), hv = hold(vx, vy);
     if (!have) continue;
     const int s = p & (ps - 1);
     const int g0 = c >> 2, g1 = NX / 2 + (c >> 2);        // groups (and 16-byte pieces) of the two words
