@@ -5,12 +5,14 @@
 // find a group's largest magnitude, and each lane's 8 codes make one 32-bit word.  The quotient x / s decides the code, and
 // ties are common (both have few bits): x (1 / s), with 1 / s off by an ulp, is off by 2^-20, which a fused sum with 96 rounds off again (to
 // 2^-17: x / s is a tie, or 2^-13 away from one), and the sum of that with 1.5 2^23 goes to the whole number, ties to even.
-// 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 47 us, 3.8 TB/s; bound by the rotation's
-// and the codes' arithmetic (with a branch per component of a rotated pair, not per pair, 54 us, issue slots 62 % busy).  A step of 32
-// rows: 4.0 us replayed.
+// 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 38.3 us, 4.7 TB/s; bound by the rotation's
+// and the codes' instructions.  (With a branch per component of a rotated pair, not per pair, 54 us; with a longer test of a pair, codes by
+// correctly rounded quotients and no prefetch 47; with a division per scale and magnitudes one by one 40.)  A step of 32 rows: 3.1
+// us replayed.
 //
-// Read: a lane takes a word of 8 dims of the key and of the value, 4 + 1 bytes in and 16 bytes out each.  8288 tokens: 10.5 us, 4.1
-// TB/s; a step's 32: 2.2 us replayed.
+// Read: a lane takes a word of 8 dims of the key and of the value, 4 + 1 bytes in and 16 bytes out each, of four tokens at a
+// time.  8288 tokens: 7.5 us, 5.7 TB/s (one token at a time 10.5; 9360 tokens of 12 heads of 64, pages of 32: 7.4 for 6.9); a step's
+// 32: 2.2 us replayed.
 #include "paged4_internal.h"
 #include "paged_append.h"
 
@@ -209,16 +211,27 @@ k_paged4_read(const uint8_t* pool, T* __restrict__ k_out, T* __restrict__ v_out,
   if (col >= a.kv_cols) return;
   const int head = col / W, w = col % W;
   const uint8_t* rec = pool + ((int64_t)page * a.Hkv + head) * kvc_pg4_record(D, a.ps_log2);
-  for (int p = lo + warp / gw; p < hi; p += kWarps / gw) {
-    const int s = p & (ps - 1);
-    const int piece = (w >> 2) ^ ((s >> 2) & (NX - 1));
-    const uint32_t kw = (uint32_t)pg_ld(reinterpret_cast<const int32_t*>(rec + s * (D / 2) + 4 * w));
-    const uint32_t vw = (uint32_t)pg_ld(reinterpret_cast<const int32_t*>(rec + (ps + s) * (D / 2) + 16 * piece + 4 * (w & 3)));
-    const uint32_t ks = ld_byte(rec + ps * D + s * NX + (w >> 2));
-    const uint32_t vs = ld_byte(rec + ps * D + ps * NX + (w >> 2) * ps + s);
-    const int64_t dst = ((int64_t)(r.t0 + p - p0) * a.Hkv + head) * D + 8 * w;
-    if (k_out != nullptr) *reinterpret_cast<uint4*>(k_out + dst) = unheld<T>(kw, ks);
-    if (v_out != nullptr) *reinterpret_cast<uint4*>(v_out + dst) = unheld<T>(vw, vs);
+  const int stride = kWarps / gw;
+  constexpr int U = 4;                    // tokens whose loads are in flight together
+  for (int p = lo + warp / gw; p < hi; p += U * stride) {
+    uint32_t kw[U], vw[U], ks[U], vs[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (p + i * stride >= hi) break;
+      const int s = (p + i * stride) & (ps - 1);
+      const int piece = (w >> 2) ^ ((s >> 2) & (NX - 1));
+      kw[i] = (uint32_t)pg_ld(reinterpret_cast<const int32_t*>(rec + s * (D / 2) + 4 * w));
+      vw[i] = (uint32_t)pg_ld(reinterpret_cast<const int32_t*>(rec + (ps + s) * (D / 2) + 16 * piece + 4 * (w & 3)));
+      ks[i] = ld_byte(rec + ps * D + s * NX + (w >> 2));
+      vs[i] = ld_byte(rec + ps * D + ps * NX + (w >> 2) * ps + s);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (p + i * stride >= hi) break;
+      const int64_t dst = ((int64_t)(r.t0 + p + i * stride - p0) * a.Hkv + head) * D + 8 * w;
+      if (k_out != nullptr) *reinterpret_cast<uint4*>(k_out + dst) = unheld<T>(kw[i], ks[i]);
+      if (v_out != nullptr) *reinterpret_cast<uint4*>(v_out + dst) = unheld<T>(vw[i], vs[i]);
+    }
   }
 }
 

@@ -8,15 +8,15 @@
 // x[j + D/2]), or two vectors of pairs (x[2j], x[2j+1]).  A block's warps are divided between columns
 // (32 such lanes' worth of the keys' and values' heads, or of the queries') and tokens: few tokens to
 // a run, and all of them are on columns; many, and each takes every eighth token, some four in all,
-// so that a long page does not become a long chain.  One token of a warp is in flight, all its loads together
-// (eight 16-byte ones a lane, and 32 warps an SM: 5.6 TB/s for prompts, 0.83 of a copy; a decode step of 32 rows takes
+// so that a long page does not become a long chain.  One token of a warp is in flight, all its loads together, the next one's
+// on their way to L2 (eight 16-byte ones a lane, and 32 warps an SM: 5.6 TB/s for prompts, 0.83 of a copy; a decode step of 32 rows takes
 // 5 us replayed, of which the loads that wait for the page number, though only the stores need it, are a part).
 // A run's keys, after rounding, give the page's maximum and minimum in registers: no second pass, no
 // atomics.
 //
 // With positions of several axes (kAxes) each pair takes its angles from the row of its axis: by the same 16-byte loads where a
 // lane's pairs of a vector go by one axis (sections side by side), else pair by pair.  Two frames of 1560 tokens, 40 heads of 128:
-// 46 us, 4.2 TB/s, where slots as positions take 38 (the positions' load stands before the angles'; more registers to a
+// 42.5 us, 4.5 TB/s, where slots as positions take 34.6 (the positions' load stands before the angles'; more registers to a
 // thread, for no spills, cost more in warps: 65 us where this took 49).
 #include "paged_append.h"
 
