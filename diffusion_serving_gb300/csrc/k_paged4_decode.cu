@@ -4,7 +4,8 @@
 // Work goes to blocks as in the 16-bit streaming kernel (k_paged_decode.cu, paged_internal.h): a block takes one stretch
 // of the line of all rows' tiles, here of 128 slots, through a ring of shared-memory stages.  A page's slots of a head are
 // one record, so a tile arrives as one bulk copy per page.  Warps:
-//   consumers: sets of four, which take tiles in turn, 32 slots of a tile to a warp; three sets for up to 8 query rows, else two
+//   consumers: sets of four, 32 slots of a tile to a warp; three sets for up to 8 query rows, else two.  They take an item's tiles in
+//     turn, or, where there are many items of few tiles, an item each
 //   the last three: producers (page numbers, copies, every other record each) and between them a helper: the next items' queries and extents
 //
 // At a quarter of the 16-bit store's bytes a slot, instructions bound this kernel as much as HBM does, so the slots stand in M
@@ -24,10 +25,13 @@
 // rounded to fp16 once for the product with V (their sum takes them unrounded).
 //
 // Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 76 us, 3.8 TB/s of codes and scales,
-// 0.56 of a plain copy (the 16-bit kernel 171 us); 2 rows of 100001 and 131072 slots, pages of 64: 62 us, 4.1 TB/s.  Bound by the
+// 0.56 of a plain copy (the 16-bit kernel 171 us); 2 rows of 100001 and 131072 slots, pages of 64: 60 us, 4.2 TB/s.  Bound by the
 // consumers' instructions and their latency: 325 a warp for 16 slots of 128 dims, issue slots 58 % busy; of 67 us (32 rows of 8192) the
 // copies by themselves take 52, the products with K and with V 18 each, waits and work split 16.  More warps of fewer registers
 // (four sets: spills) took 94 us, fewer (two sets) 68; nine stages for six changed nothing.  One row of 490 slots: 8 us.
+// Items of few tiles cost a block their beginnings and ends, some 3.5 us one after another; in sets of their own 128 rows of 100 slots
+// take 17 us where they took 24, 512 of 300 68 for 96, 128 of 1000 47 for 51; but 128 of 2000, 16 tiles an item, 87 for 77, so it is
+// done up to a mean of 8.  (31 rows of 100 and one of 16000, whose item a set has for itself: 17 us for 16.)
 #include "paged4_internal.h"
 #include "paged_finish.h"
 #include "paged_ptx.h"
@@ -45,6 +49,8 @@ constexpr int kProducers = 3;                     // producer warps, which take 
 template <int R> constexpr int kThreads = (kWarps<R> + kProducers + 1) * 32;   // + helper
 constexpr int kPad = 8;                           // floats: rows of the warps' states on different banks
 constexpr int kMinTiles = 4, kItemCost = 2;       // fewest tiles for a block; an item's beginning and end, in tiles
+constexpr int kItems = 6;                         // items whose queries are kept
+constexpr int kBrief = 8;                         // tiles of a mean item up to which sets of consumers have items of their own
 constexpr float kBias = 8.f, kTop = 15.f;         // log2 of a weight at its reference, and of the largest taken
 
 template <int D> constexpr uint32_t kStageBytes = kTile * (D + D / 16);
@@ -54,21 +60,23 @@ template <typename T, int D, int R>
 struct Smem {
   uint8_t stage[kStages<D, R>][kStageBytes<D>];   // 128-byte aligned
   float acc[kWarps<R>][R][D + kPad];
-  __half q[2][R][D + 8];                          // an item's queries (+ 8: rows on different banks)
-  float q_scale[2][R];                            // of their scores, to log2 units
+  __half q[kItems][R][D + 8];                          // an item's queries (+ 8: rows on different banks)
+  float q_scale[kItems][R];                            // of their scores, to log2 units
   float2 ml[kWarps<R>][R];
-  int64_t at[2][R];                               // rows of the outputs
-  int limit[2][R];                                // where each query row's keys end (rows that are not there: all)
-  kvc_pg_end end[2];
-  int tiles[2];                                   // this block's tiles of the item; -1: there is none
-  int key0[2];                                    // position of the first one's first slot
-  int len[2], open[2];                            // where the row's slots end; below this every query row sees all
+  int64_t at[kItems][R];                               // rows of the outputs
+  int limit[kItems][R];                                // where each query row's keys end (rows that are not there: all)
+  kvc_pg_end end[kItems];
+  int tiles[kItems];                              // this block's tiles of the item; -1: there is none
+  int first[kItems];                              // tiles of this block before them
+  int key0[kItems];                                    // position of the first one's first slot
+  int len[kItems], open[kItems];                            // where the row's slots end; below this every query row sees all
   uint32_t bad[kStages<D, R>];                    // records of a stage that no page stands behind
+  int tile[kStages<D, R>];                        // the last one that a stage was given to
   uint64_t full[kStages<D, R>], empty[kStages<D, R>];
-  uint64_t q_full[2], item_empty[2];
+  uint64_t q_full[kItems], item_empty[2][kItems];  // (the second: of a set's own items)
   WaitCtl wc;
-  int flag;
-  int fail[2];                                    // a consumer's wait gave up: before an item, within it
+  int flag[kSets<R>];                             // (a set's, or the first for all)
+  int fail[kSets<R>][2];                          // a consumer's wait gave up: before an item, within it
 };
 
 __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
@@ -110,6 +118,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Until a stage has been given to tile u (false: as mbar_wait).
+__device__ __noinline__ bool await_tile(const volatile int* tile, int u, volatile WaitCtl* w) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if (*tile == u) return true;
+    if ((n & 63) == 0) {
+      if (w->abort) return false;
+      if (globaltimer() - t0 > (uint64_t)w->limit_ns) {
+        w->abort = 1;
+        return false;
+      }
+    }
+  }
+}
 // D / 32 words of codes at a shared address (16 or 8 bytes).
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* r) {
@@ -147,14 +169,16 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   if (threadIdx.x < S) {
     mbar_init(&sm.full[threadIdx.x], 1);             // its producer's first lane
     mbar_init(&sm.empty[threadIdx.x], 4);             // a set's warps
+    sm.tile[threadIdx.x] = -1;
   }
-  if (threadIdx.x >= 32 && threadIdx.x < 34) {
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + kItems) {
     mbar_init(&sm.q_full[threadIdx.x - 32], 32);
-    mbar_init(&sm.item_empty[threadIdx.x - 32], kW);
+    mbar_init(&sm.item_empty[0][threadIdx.x - 32], kW);
+    mbar_init(&sm.item_empty[1][threadIdx.x - 32], 4);
   }
   if (threadIdx.x == 64) {
     wait_init(&sm.wc, a.stall_ns);
-    sm.fail[0] = sm.fail[1] = 0;
+    for (int i = 0; i < kSets<R>; ++i) sm.fail[i][0] = sm.fail[i][1] = 0;
   }
   fence_mbar_init();
   __syncthreads();
@@ -162,6 +186,8 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   kvc_pdl_release();
   kvc_pg_sched<R, kTile> sch;
   sch.init(a, reinterpret_cast<uint8_t*>(&sm) + ((sizeof(Sm) + 15) & ~(size_t)15), kMinTiles, kMinTiles, kItemCost, gridDim.x);
+  // Many items of few tiles: sets take items of their own, each every kSets-th, so that one's beginning and end pass beside another's.
+  const bool own = sch.stride == 0 && sch.total - sch.n_items * sch.cost <= kBrief * sch.n_items;
   kvc_pg_item it;
   bool more = false;
   if (warp >= kW) more = sch.first(a, blockIdx.x, it);
@@ -207,6 +233,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         if (lane == 0) {
           if (want != good) atomicOr(a.err, KVC_DEV_BAD_PAGE);
           sm.bad[st] = want ^ good;
+          *(volatile int*)&sm.tile[st] = u;
           mbar_expect_tx(&sm.full[st], __popc(good) * record);
         }
         __syncwarp();
@@ -227,14 +254,16 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
   } else if (warp == kW + kProducers) {
     // ---------------- helper: queries of the items to come ----------------
     constexpr int VQ = D / 8;                               // 16-byte vectors of a query row
+    int first = 0, ends = own ? kSets<R> : 1;               // (each set comes to an end of its own)
     for (int n = 0;; ++n) {
-      const int b = n & 1;
-      if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.item_empty[b], (n / 2 - 1) & 1, wc))) break;
+      const int b = n % kItems;
+      if (n >= kItems && !__all_sync(0xffffffffu, mbar_wait(&sm.item_empty[own][b], (n / kItems - 1) & 1, wc))) break;
       if (!more) {
         if (lane == 0) sm.tiles[b] = -1;
         __syncwarp();
         mbar_arrive(&sm.q_full[b]);
-        break;
+        if (--ends == 0) break;
+        continue;
       }
       const kvc_pg_end e = pg_end(a, sch, it);
       int64_t at = 0;
@@ -251,6 +280,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
       if (lane == 0) {
         sm.end[b] = e;
         sm.tiles[b] = it.tile1 - it.tile0;
+        sm.first[b] = first;
         sm.key0[b] = it.tile0 * kTile;
         sm.len[b] = it.r.len;
         sm.open[b] = open;
@@ -273,6 +303,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         if (v % VQ == 0) sm.q_scale[b][v / VQ] = pg4_score_scale(f, a.scale_log2);
       }
       mbar_arrive(&sm.q_full[b]);
+      first += it.tile1 - it.tile0;
       more = sch.next(a, it);
     }
   } else {
@@ -294,16 +325,21 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     const int lr = lane & 7, l_slot = 4 * (lr >> 1) + (lr & 1) + 2 * (lane >> 3 & 1), l_piece = lane >> 4;
     const uint32_t v_off = rec_i * record + (ps + s0 + l_slot) * (D / 2);
     const int l_turn = (l_slot >> 2) & (W - 1);
-    auto bar = [] { named_bar<1>(kW * 32); };
-    int t = 0;                                              // tiles of this block before the item's
+    auto consume = [&](auto owned) {
+    // the warps that share an item: all of the consumers, or (kOwn) a set
+    constexpr bool kOwn = decltype(owned)::value;
+    constexpr int kN = kOwn ? 4 : kW, kApart = kOwn ? kSets<R> : 1;
+    constexpr int kStep = kOwn ? 1 : kSets<R>;              // from a tile of this warp to its next
+    const int mates = kOwn ? set : 0, w0 = 4 * mates;
+    auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + mates), "n"(kN * 32) : "memory"); };
     int u = set, st = set;                                  // this warp's next tile and its stage,
     uint32_t phase = 0;                                     // whose barrier's phase it is
-    for (int n = 0;; ++n) {
-      const int b = n & 1;
-      bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / 2) & 1, wc));
-      if (!ok) sm.fail[0] = 1;
+    for (int n = mates;; n += kApart) {
+      const int b = n % kItems;
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / kItems) & 1, wc));
+      if (!ok) sm.fail[mates][0] = 1;
       bar();                                                // (the last item's states have been read, too)
-      if (sm.fail[0]) break;                                // what ends the loop is the same for every consumer
+      if (sm.fail[mates][0]) break;                         // what ends the loop is the same for all that share an item
       const int tiles = sm.tiles[b];
       if (tiles < 0) break;
       uint32_t qb[NQ][2 * W][2];                            // B operands: query 8 x + g, this lane's dims
@@ -320,7 +356,12 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         qs[x][1] = sm.q_scale[b][8 * x + 2 * quad + 1];
       }
       const int len = sm.len[b], open = sm.open[b];
-      const int t_end = t + tiles;
+      const int t = sm.first[b], t_end = t + tiles;
+      if (kOwn) {
+        u = t;
+        st = u % S;
+        phase = (u / S) & 1;
+      }
       int key = sm.key0[b] + r0 + (u - t) * kTile;          // position of the warp's first slot
       float o[NQ][MT][4];
       float nm[NQ][2], l[NQ][2];                            // kBias less the references, sums of this lane's slots
@@ -331,8 +372,10 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         nm[x][0] = nm[x][1] = INFINITY;
         l[x][0] = l[x][1] = 0.f;
       }
-      for (; u < t_end; u += kSets<R>, key += kSets<R> * kTile) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], phase, wc));
+      for (; u < t_end; u += kStep, key += kStep * kTile) {
+        // (a set that has run ahead of the others may be rounds ahead of the ring, where a barrier's parity says nothing)
+        ok = !kOwn || *(volatile int*)&sm.tile[st] == u || await_tile(&sm.tile[st], u, wc);
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.full[st], phase, wc));
         if (!ok) break;
         const uint32_t base = smem_u32(sm.stage[st]);
         const uint32_t gone = sm.bad[st];
@@ -473,16 +516,15 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[st]);          // this warp is done with the stage
-        st += kSets<R>;
+        st += kStep;
         if (st >= S) {
           st -= S;
           phase ^= 1;
         }
       }
-      t = t_end;
 
       // ---- the item's end ----
-      if (!ok) sm.fail[1] = 1;
+      if (!ok) sm.fail[mates][1] = 1;
       const kvc_pg_end e = sm.end[b];
 #pragma unroll
       for (int x = 0; x < NQ; ++x) {
@@ -503,23 +545,23 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         }
       }
       bar();
-      if (sm.fail[1]) break;
+      if (sm.fail[mates][1]) break;
       pg_finish<T, D, R>(
-          a, e, out, &sm.flag, threadIdx.x, kW * 32, false,
+          a, e, out, &sm.flag[mates], threadIdx.x - 32 * w0, kN * 32, false,
           [&](int r, int d, float* Mp, float* Lp) {
-            float2 ml[kW];
+            float2 ml[kN];
             float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-              ml[w] = sm.ml[w][r];
+            for (int w = 0; w < kN; ++w) {
+              ml[w] = sm.ml[w0 + w][r];
               M = fmaxf(M, ml[w].x);
             }
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
+            for (int w = 0; w < kN; ++w) {
               const float wt = pg_weight(ml[w].x, M);
               L = fmaf(wt, ml[w].y, L);
-              pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w][r][d]));
+              pg_acc4(x, wt, *reinterpret_cast<const float4*>(&sm.acc[w0 + w][r][d]));
             }
             *Mp = M;
             *Lp = L;
@@ -527,9 +569,12 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
           },
           [](int, int, float2*, float4*) {}, [&](int r) { return sm.at[b][r]; }, bar);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[b]);
+      if (lane == 0) mbar_arrive(&sm.item_empty[kOwn][b]);
     }
-    if (threadIdx.x == 0 && wc->abort) atomicOr(a.err, KVC_DEV_TIMEOUT);
+    };
+    if (own) consume(std::true_type());
+    else consume(std::false_type());
+    if (threadIdx.x % 128 == 0 && wc->abort) atomicOr(a.err, KVC_DEV_TIMEOUT);
   }
 }
 

@@ -299,6 +299,7 @@ struct kvc_pg_sched {
   int* rows;             // [rows][3]
   int n_rows, T, lo;     // lo: where the rows' own keys begin (behind a shared prefix, or 0)
   bool causal;
+  int n_items;
   int total, per, stride, cost;   // stride: places between items' beginnings where they are padded, else 0
   int end;               // of this block's stretch
   int waves, wave, from; // waves of whole items (0: none), the one at hand, where the stretches begin on the line
@@ -373,6 +374,7 @@ struct kvc_pg_sched {
     items *= a.Hv;
     over = __any_sync(0xffffffffu, over) || tiles + items * item_cost > KVC_PG_LINE;
     cost = item_cost;
+    n_items = (int)items;
     waves = 0;
     if (over) {
       if (threadIdx.x == 0) atomicOr(a.err, KVC_DEV_OVERFLOW);

@@ -166,6 +166,39 @@ def test_a_batch_of_1024_rows():
             ref.check(out[rows], lse[rows], got, f"row {b}")
 
 
+@pytest.mark.parametrize("dtype,heads,dim,page", [(BF16, 8, 128, 16), (F16, 32, 128, 64), (F16, 8, 64, 32), (BF16, 32, 64, 128)])
+def test_many_short_rows_and_a_few_long_ones(dtype, heads, dim, page):
+    """Rows of a few tiles, which sets of warps take by themselves, and among them some of more tiles than are in flight at once."""
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(0, 400, 160)]
+    lens[7], lens[90], lens[91] = 3000, 1700, 2500
+    c, g, k, v = big(lens, heads, 2, dim, dtype, page, seed=8)
+    q = torch.randn(len(lens), heads, dim, device="cuda", generator=g).to(dtype)
+    out, lse = c.attend(q, lse=True)
+    for _ in range(3):                                    # the same bits again
+        again, lse2 = c.attend(q, lse=True)
+        assert torch.equal(bits(again), bits(out)) and torch.equal(bits(lse2), bits(lse))
+    assert c.get_error() == 0
+    for b, n in enumerate(lens):
+        kk, vv = to64(k[b]).reshape(-1, 2, dim), to64(v[b]).reshape(-1, 2, dim)
+        got = ref.attend_rows(to64(q[b:b + 1]), kk, vv, ref.visible_mask(n, 0, 1, n, False), dim ** -0.5, dtype)
+        got[2][:] += 2.0 ** -33 * np.repeat(np.abs(vv).sum(0), heads // 2, 0)               # (weights: 2^8 too large here)
+        ref.check(out[b:b + 1], lse[b:b + 1], got, f"row {b}")
+
+
+def test_a_wait_that_ran_out_among_short_rows():
+    c, g, _, _ = big([100] * 200, 8, 2, 128, BF16, 16, seed=42)
+    q = torch.randn(200, 8, 128, device="cuda", generator=g).to(BF16)
+    want = c.attend(q)
+    assert c.get_error() == 0
+    paged4.kvc_paged4_debug_stall_waits(c.handle, 200_000)
+    c.attend(q)
+    paged4.kvc_paged4_debug_stall_waits(c.handle, 0)
+    assert c.get_error() & paged.DEV_TIMEOUT
+    got = c.attend(q)
+    assert c.get_error() == 0 and torch.equal(bits(got), bits(want))
+
+
 @pytest.mark.parametrize("heads,kv_heads", [(96, 1), (22, 2), (33, 1)])
 @pytest.mark.parametrize("new", [1, 9])
 def test_large_and_odd_groups(heads, kv_heads, new):
