@@ -25,12 +25,12 @@
 // rounded to fp16 once for the product with V (their sum takes them unrounded).
 //
 // Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 76 us, 3.8 TB/s of codes and scales,
-// 0.56 of a plain copy (the 16-bit kernel 171 us); 2 rows of 100001 and 131072 slots, pages of 64: 60 us, 4.2 TB/s.  Bound by the
+// 0.56 of a plain copy (the 16-bit kernel 171 us); 2 rows of 100001 and 131072 slots, pages of 64: 61 us, 4.1 TB/s.  Bound by the
 // consumers' instructions and their latency: 325 a warp for 16 slots of 128 dims, issue slots 58 % busy; of 67 us (32 rows of 8192) the
 // copies by themselves take 52, the products with K and with V 18 each, waits and work split 16.  More warps of fewer registers
 // (four sets: spills) took 94 us, fewer (two sets) 68; nine stages for six changed nothing.  One row of 490 slots: 8 us.
 // Items of few tiles cost a block their beginnings and ends, some 3.5 us one after another; in sets of their own 128 rows of 100 slots
-// take 17 us where they took 24, 512 of 300 68 for 96, 128 of 1000 47 for 51; but 128 of 2000, 16 tiles an item, 87 for 77, so it is
+// take 17 us where they took 24, 512 of 300 69 for 96, 128 of 1000 45 for 51; but 128 of 2000, 16 tiles an item, 87 for 77, so it is
 // done up to a mean of 8.  (31 rows of 100 and one of 16000, whose item a set has for itself: 17 us for 16.)
 #include "paged4_internal.h"
 #include "paged_finish.h"
@@ -71,8 +71,9 @@ struct Smem {
   int key0[kItems];                                    // position of the first one's first slot
   int len[kItems], open[kItems];                            // where the row's slots end; below this every query row sees all
   uint32_t bad[kStages<D, R>];                    // records of a stage that no page stands behind
-  int tile[kStages<D, R>];                        // the last one that a stage was given to
-  uint64_t full[kStages<D, R>], empty[kStages<D, R>];
+  // A stage that is full, by the set whose own item its tile is of (the first, where they share items): a set that has run ahead of
+  // the others may be rounds ahead of the ring, where the parity of a barrier they shared would say nothing.
+  uint64_t full[kSets<R>][kStages<D, R>], empty[kStages<D, R>];
   uint64_t q_full[kItems], item_empty[2][kItems];  // (the second: of a set's own items)
   WaitCtl wc;
   int flag[kSets<R>];                             // (a set's, or the first for all)
@@ -118,20 +119,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Until a stage has been given to tile u (false: as mbar_wait).
-__device__ __noinline__ bool await_tile(const volatile int* tile, int u, volatile WaitCtl* w) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t n = 1;; ++n) {
-    if (*tile == u) return true;
-    if ((n & 63) == 0) {
-      if (w->abort) return false;
-      if (globaltimer() - t0 > (uint64_t)w->limit_ns) {
-        w->abort = 1;
-        return false;
-      }
-    }
-  }
-}
 // D / 32 words of codes at a shared address (16 or 8 bytes).
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* r) {
@@ -167,9 +154,8 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
 
   // set-up that touches no global memory runs before the wait for the previous kernel
   if (threadIdx.x < S) {
-    mbar_init(&sm.full[threadIdx.x], 1);             // its producer's first lane
+    for (int i = 0; i < kSets<R>; ++i) mbar_init(&sm.full[i][threadIdx.x], 1);   // its producer's first lane
     mbar_init(&sm.empty[threadIdx.x], 4);             // a set's warps
-    sm.tile[threadIdx.x] = -1;
   }
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kItems) {
     mbar_init(&sm.q_full[threadIdx.x - 32], 32);
@@ -207,6 +193,8 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     };
     int t = 0;                                              // tiles of this block before the item's
     int u = warp - kW, st = u, round = 0;                   // this warp's next tile, its stage, rounds of the ring before it
+    int owner = 0;                                          // the set whose own item this is
+    uint64_t used = 0;                                      // full barriers that this warp has used an odd number of times
     bool ok = true;
     int ahead = more ? window(it, it.tile0) : -1;
     for (; ok && more;) {
@@ -233,11 +221,11 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         if (lane == 0) {
           if (want != good) atomicOr(a.err, KVC_DEV_BAD_PAGE);
           sm.bad[st] = want ^ good;
-          *(volatile int*)&sm.tile[st] = u;
-          mbar_expect_tx(&sm.full[st], __popc(good) * record);
+          mbar_expect_tx(&sm.full[owner][st], __popc(good) * record);
         }
         __syncwarp();
-        if (fine) bulk_load(&sm.full[st], sm.stage[st] + lane * record, heads + (int64_t)page * a.Hkv * record, record);
+        if (fine) bulk_load(&sm.full[owner][st], sm.stage[st] + lane * record, heads + (int64_t)page * a.Hkv * record, record);
+        used ^= 1ull << (owner * S + st);
         st += kProducers;
         if (st >= S) {
           st -= S;
@@ -247,9 +235,11 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
       if (w0 + wide < tile1 && more) ahead = window(nx, nx.tile0);   // (the last window held no tile of this warp's)
       t += tile1 - tile0;
       it = nx;
+      if (own) owner = owner + 1 < kSets<R> ? owner + 1 : 0;
     }
     if (lane == 0) {   // every load issued here lands before the block releases its shared memory, consumers that gave up or not
-      for (int i = u - kProducers; i >= 0 && i >= u - S; i -= kProducers) mbar_wait(&sm.full[i % S], (i / S) & 1, wc, false);
+      for (int i = 0; i < kSets<R>; ++i)
+        for (int x = warp - kW; x < S; x += kProducers) mbar_wait(&sm.full[i][x], ~(uint32_t)(used >> (i * S + x)) & 1, wc, false);
     }
   } else if (warp == kW + kProducers) {
     // ---------------- helper: queries of the items to come ----------------
@@ -333,7 +323,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
     const int mates = kOwn ? set : 0, w0 = 4 * mates;
     auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + mates), "n"(kN * 32) : "memory"); };
     int u = set, st = set;                                  // this warp's next tile and its stage,
-    uint32_t phase = 0;                                     // whose barrier's phase it is
+    uint32_t phase = 0;                                     // whose barrier's phase it is (kOwn: those of all stages, a bit each)
     for (int n = mates;; n += kApart) {
       const int b = n % kItems;
       bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[b], (n / kItems) & 1, wc));
@@ -360,7 +350,6 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
       if (kOwn) {
         u = t;
         st = u % S;
-        phase = (u / S) & 1;
       }
       int key = sm.key0[b] + r0 + (u - t) * kTile;          // position of the warp's first slot
       float o[NQ][MT][4];
@@ -373,9 +362,7 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         l[x][0] = l[x][1] = 0.f;
       }
       for (; u < t_end; u += kStep, key += kStep * kTile) {
-        // (a set that has run ahead of the others may be rounds ahead of the ring, where a barrier's parity says nothing)
-        ok = !kOwn || *(volatile int*)&sm.tile[st] == u || await_tile(&sm.tile[st], u, wc);
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&sm.full[st], phase, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[mates][st], kOwn ? phase >> st & 1 : phase, wc));
         if (!ok) break;
         const uint32_t base = smem_u32(sm.stage[st]);
         const uint32_t gone = sm.bad[st];
@@ -516,10 +503,11 @@ k_paged4_decode(const uint8_t* pool, const T* q, T* __restrict__ out, kvc_pg_arg
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[st]);          // this warp is done with the stage
+        if (kOwn) phase ^= 1u << st;
         st += kStep;
         if (st >= S) {
           st -= S;
-          phase ^= 1;
+          if (!kOwn) phase ^= 1;
         }
       }
 
