@@ -10,7 +10,10 @@
 // a run, and all of them are on columns; many, and each takes every eighth token, some four in all,
 // so that a long page does not become a long chain.  One token of a warp is in flight, all its loads together, the next one's
 // on their way to L2 (eight 16-byte ones a lane, and 32 warps an SM: 5.6 TB/s for prompts, 0.83 of a copy; a decode step of 32 rows takes
-// 5 us replayed, of which the loads that wait for the page number, though only the stores need it, are a part).
+// 3.3 us replayed, of which the loads that wait for the page number, though only the stores need it, are a part).
+// Keys that are stored as they come (kTurn false) have instances of their own, without the rotation's registers and without the
+// prefetch, which only helps where arithmetic stands between the loads: 8 prompts of 8 heads, fp16, 7.9 us (9.2 in the instance
+// that can turn; with bounds 11.0 and 15.2), a step of 32 rows 2.0 (2.2).
 // A run's keys, after rounding, give the page's maximum and minimum in registers: no second pass, no
 // atomics.
 //
@@ -38,7 +41,7 @@ __device__ __forceinline__ float pick_min(float a, float b) {
 __device__ __forceinline__ __half pick_min(__half a, __half b) { return __hmin_nan(a, b); }
 __device__ __forceinline__ __nv_bfloat16 pick_min(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmin_nan(a, b); }
 
-template <typename T, int D, bool kBounds, int kAxes>
+template <typename T, int D, bool kBounds, bool kTurn, int kAxes>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
                T* q_out, T* __restrict__ bounds, AppendArgs a) {
@@ -57,12 +60,12 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   const int column = (p0 >> a.ps_log2) + j;
   const int lo = max(p0, column << a.ps_log2), hi = min(r.len, (column + 1) << a.ps_log2);
   if (lo >= hi) return;
-  const int end = !kAxes && a.rope != nullptr ? min(hi, a.rope_positions) : hi;
+  const int end = !kAxes && kTurn ? min(hi, a.rope_positions) : hi;
   if (end < hi && threadIdx.x == 0) atomicOr(a.err, KVC_DEV_BAD_POS);
   const int gw = a.groups_y;                        // column groups this block's warps divide into
   const int group = (int)blockIdx.y * gw + warp % gw;
   const int stride = kWarps / gw;
-  if (group >= a.kv_groups)
+  if (kTurn && group >= a.kv_groups)
     append_queries<T, D, kAxes>(a, r, q, q_out, group - a.kv_groups, lo + warp / gw, end, stride, p0);
   // ---- keys and values ----
   const int page = a.table[(int64_t)b * a.max_pages + column];
@@ -86,7 +89,7 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
       const int64_t off = (int64_t)(r.t0 + p - p0) * a.kv_stride + src0;
       x.u = pg_ld(reinterpret_cast<const uint4*>(k + off));
       y.u = pg_ld(reinterpret_cast<const uint4*>(k + off + D / 2));
-      if (p + stride < end) {
+      if (kTurn && p + stride < end) {
         const int64_t next = off + stride * a.kv_stride;
         ahead(k + next);
         ahead(k + next + D / 2);
@@ -95,14 +98,14 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
       }
       if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
       if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
-      else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+      else if (kTurn) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
       if (kAxes && !have) continue;
       vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
       vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
       const int64_t dst = (((int64_t)page << a.ps_log2) + (p & (ps - 1))) * dst_row + src0;
       *reinterpret_cast<uint4*>(vp + dst) = vx.u;
       *reinterpret_cast<uint4*>(vp + dst + D / 2) = vy.u;
-      if (kAxes || a.rope != nullptr) turn<T>(x, y, cs, a.half);
+      if (kTurn) turn<T>(x, y, cs, a.half);
       *reinterpret_cast<uint4*>(kp + dst) = x.u;
       *reinterpret_cast<uint4*>(kp + dst + D / 2) = y.u;
       if (kBounds) {
@@ -183,10 +186,11 @@ cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, vo
                           (T*)q_out, (T*)c->bounds, a);
   };
   const bool bounds = c->bounds != nullptr;
+  if (a.rope == nullptr) return bounds ? go(k_paged_append<T, D, true, false, kSlots>) : go(k_paged_append<T, D, false, false, kSlots>);
   switch (axes_kind(a, D, VL)) {
-    case kSlots: return bounds ? go(k_paged_append<T, D, true, kSlots>) : go(k_paged_append<T, D, false, kSlots>);
-    case kFlat: return bounds ? go(k_paged_append<T, D, true, kFlat>) : go(k_paged_append<T, D, false, kFlat>);
-    default: return bounds ? go(k_paged_append<T, D, true, kAny>) : go(k_paged_append<T, D, false, kAny>);
+    case kSlots: return bounds ? go(k_paged_append<T, D, true, true, kSlots>) : go(k_paged_append<T, D, false, true, kSlots>);
+    case kFlat: return bounds ? go(k_paged_append<T, D, true, true, kFlat>) : go(k_paged_append<T, D, false, true, kFlat>);
+    default: return bounds ? go(k_paged_append<T, D, true, true, kAny>) : go(k_paged_append<T, D, false, true, kAny>);
   }
 }
 

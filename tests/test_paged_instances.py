@@ -1,0 +1,21 @@
+"""Which instance of a paged kernel a call runs, and what its warps do there (static checks, no GPU): what costs time without
+changing a result."""
+import os
+import re
+
+from tests.test_kernel_source import CSRC, block_from, code
+
+
+def kernel(text, name):
+    """The body of kernel `name`."""
+    m = re.search(r"__global__[^{;]*\b%s\s*\(" % name, text)
+    return block_from(text, m.start())
+
+
+def test_keys_stored_as_they_come_have_instances_of_their_own():
+    """Registers, spills and prefetches that only a rotation needs slow a plain copy down by 10 to 18 % where one instance does
+    both: whether keys are turned is decided at the launch, not in the kernel."""
+    text = code(os.path.join(CSRC, "k_paged_append.cu"))
+    assert not re.search(r"a\.rope\s*[!=]=", kernel(text, "k_paged_append"))
+    launch = block_from(text, text.index("cudaError_t launch("))
+    assert re.search(r"if \(a\.rope == nullptr\) return .*k_paged_append<T, D, true, false, kSlots>", launch)
