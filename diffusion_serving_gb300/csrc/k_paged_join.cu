@@ -14,16 +14,18 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRowBlocks = 8;             // blocks per split item
 
 // Block (c, y) joins rows y * 8 + warp, ... of the item that begins in block c of k_paged_tc (or k_paged4_tc) and goes on behind
-// it, if there is one.
-template <typename T, int D>
+// it, if there is one.  kWaves: that kernel may have taken whole items in waves first, so the shares are worked out as it did; an
+// instance of its own, as the sums that this takes make any other call 1 us longer (40 tokens over 2000 slots, 32 heads over 8,
+// 16-bit store: 25.1 us, 26.1 with them).
+template <typename T, int D, bool kWaves>
 __global__ void __launch_bounds__(kThreads)
 k_paged_join(T* __restrict__ out, kvc_pg_args a) {
   constexpr int R = KVC_PG_TC_ROWS;
   extern __shared__ __align__(16) uint8_t smem[];
-  kvc_pg_sched<R, KVC_PG_TC_TILE, true> sch;
+  kvc_pg_sched<R, KVC_PG_TC_TILE, kWaves> sch;
   sch.init(a, smem, KVC_PG_TC_MIN, KVC_PG_TC_WHOLE, KVC_PG_TC_COST, KVC_PG_GRID);
   // the item at the end of the block's stretch
-  const bool waves = sch.waves > 0;
+  const bool waves = kWaves && sch.waves > 0;
   const long long end = waves ? sch.from + sch.cut[blockIdx.x + 1] : (long long)(blockIdx.x + 1) * sch.per;
   const bool any = end < sch.total && (!waves || sch.cut[blockIdx.x] < sch.cut[blockIdx.x + 1]);
   kvc_pg_item it;
@@ -105,8 +107,10 @@ cudaError_t launch_prefix(const kvc_pg_args& a, int R, int TS, int cost, int gri
 
 template <typename T, int D>
 cudaError_t launch(const kvc_pg_args& a, void* out, cudaStream_t s) {
-  return kvc_launch_pdl(k_paged_join<T, D>, dim3(KVC_PG_GRID, kRowBlocks), dim3(kThreads), pg_sched_bytes(a.B, true), s,
-                        (T*)out, a);
+  auto go = [&](auto kernel) {
+    return kvc_launch_pdl(kernel, dim3(KVC_PG_GRID, kRowBlocks), dim3(kThreads), pg_sched_bytes(a.B, a.waves), s, (T*)out, a);
+  };
+  return a.waves ? go(k_paged_join<T, D, true>) : go(k_paged_join<T, D, false>);
 }
 
 }  // namespace

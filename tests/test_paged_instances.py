@@ -19,3 +19,11 @@ def test_keys_stored_as_they_come_have_instances_of_their_own():
     assert not re.search(r"a\.rope\s*[!=]=", kernel(text, "k_paged_append"))
     launch = block_from(text, text.index("cudaError_t launch("))
     assert re.search(r"if \(a\.rope == nullptr\) return .*k_paged_append<T, D, true, false, kSlots>", launch)
+
+
+def test_joins_work_out_waves_only_where_there_may_be_some():
+    """The sums over whole items taken in waves make a join 1 us longer: calls that take none run an instance without them."""
+    text = code(os.path.join(CSRC, "k_paged_join.cu"))
+    assert "kvc_pg_sched<R, KVC_PG_TC_TILE, kWaves> sch;" in kernel(text, "k_paged_join")
+    assert re.search(r"return a\.waves \? go\(k_paged_join<T, D, true>\) : go\(k_paged_join<T, D, false>\);", text)
+    assert "pg_sched_bytes(a.B, a.waves)" in text
