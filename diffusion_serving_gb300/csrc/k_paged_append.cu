@@ -19,8 +19,9 @@
 //
 // With positions of several axes (kAxes) each pair takes its angles from the row of its axis: by the same 16-byte loads where a
 // lane's pairs of a vector go by one axis (sections side by side), else pair by pair.  Two frames of 1560 tokens, 40 heads of 128:
-// 42.5 us, 4.5 TB/s, where slots as positions take 34.6 (the positions' load stands before the angles'; more registers to a
-// thread, for no spills, cost more in warps: 65 us where this took 49).
+// 39.4 us, 4.9 TB/s, where slots as positions take 34.3: a position is loaded before its angles (eight tokens' at a time), and the
+// shuffles that hand positions on keep warps whole.  More registers to a thread, for no spills, cost more in warps (65 us where this
+// took 49); query warps that went through the keys' loop as well, to no end, cost 3.6 us.
 #include "paged_append.h"
 
 namespace {
@@ -80,7 +81,7 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   const int64_t dst_row = (int64_t)a.Hkv * D;
   Vec<T> mx0, mx1, mn0, mn1;
   bool any = false;
-  if (kAxes || have) {                              // (with axes a warp stays whole)
+  if (kAxes ? group < a.kv_groups : have) {         // (with axes a warp stays whole; those of queries alone leave the keys out)
     const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
     Places places;
     for (int p = lo + warp / gw; p < end; p += stride) {

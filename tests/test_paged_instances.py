@@ -27,3 +27,15 @@ def test_joins_work_out_waves_only_where_there_may_be_some():
     assert "kvc_pg_sched<R, KVC_PG_TC_TILE, kWaves> sch;" in kernel(text, "k_paged_join")
     assert re.search(r"return a\.waves \? go\(k_paged_join<T, D, true>\) : go\(k_paged_join<T, D, false>\);", text)
     assert "pg_sched_bytes(a.B, a.waves)" in text
+
+
+def test_warps_of_queries_alone_leave_the_keys_loop_out():
+    """With several axes a warp that has keys goes through their loop whole (its lanes exchange positions), but one that has none
+    must not: it would load head 0's keys, positions and angles for every token and store nothing."""
+    body = kernel(code(os.path.join(CSRC, "k_paged_append.cu")), "k_paged_append")
+    keys = body[body.index("const int page ="):]
+    loop = keys.index("for (int p = lo + warp / gw; p < end; p += stride)")
+    guard = re.findall(r"if \(([^\n]*)\) \{", keys[:loop])[-1]
+    assert guard == "kAxes ? group < a.kv_groups : have", guard
+    other = kernel(code(os.path.join(CSRC, "k_paged4_append.cu")), "k_paged4_append")
+    assert re.search(r"if \(group >= a\.kv_groups\) \{\s*append_queries[^}]*return;\s*\}", other)
