@@ -40,6 +40,7 @@ class kvc_paged_config(ctypes.Structure):
 
 class kvc_rope_axes(ctypes.Structure):
     _fields_ = [("n_axes", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * 64)]
+    pairs = None                                           # rope_axes: how many were given; else all of a head's are meant
 
 
 def rope_axes(pair_axis, n_axes=None) -> kvc_rope_axes:
@@ -51,7 +52,7 @@ def rope_axes(pair_axis, n_axes=None) -> kvc_rope_axes:
         raise ValueError(f"kvc: rope_axes takes an axis from 0 to {n - 1} (at most 4 axes) for each of up to 64 pairs")
     a = kvc_rope_axes(n_axes=n)
     a.pair_axis[:len(pair_axis)] = pair_axis
-    a.pairs, a.ref = len(pair_axis), ctypes.byref(a)
+    a.pairs = len(pair_axis)
     return a
 
 
@@ -334,7 +335,9 @@ class PagedKVCache:
     def _positions(self, positions, axes, n, rope):
         if axes is None:
             axes = self._one_axis
-        if axes.pairs != self.head_dim // 2:
+        elif not isinstance(axes, kvc_rope_axes):
+            raise ValueError(f"kvc: axes are made by rope_axes, got {type(axes).__name__}")
+        if axes.pairs not in (None, self.head_dim // 2):
             raise ValueError(f"kvc: axes must name an axis for each of the {self.head_dim // 2} pairs of a head, got {axes.pairs}")
         s = positions.shape
         if positions.dtype is not torch.int32 or positions.get_device() != self._index or not positions.is_contiguous() or \
@@ -344,7 +347,7 @@ class PagedKVCache:
                              f"on {self.device}, got {list(s)} {positions.dtype} on {positions.device}")
         if rope is None:
             raise ValueError("kvc: positions without rope")
-        return axes.ref, positions.data_ptr()
+        return axes, positions.data_ptr()
 
     @functools.cached_property
     def _one_axis(self):
