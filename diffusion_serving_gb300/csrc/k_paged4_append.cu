@@ -40,7 +40,10 @@ __device__ __forceinline__ uint32_t top2(const uint4& v) {
   constexpr uint32_t kAbs = 0x7FFF7FFFu;
   return max2(max2(v.x & kAbs, v.y & kAbs, t), max2(v.z & kAbs, v.w & kAbs, t), t);
 }
-// e4m3 of top / 7, to nearest even, 448 at most (a NaN stays one).  The quotient is right by one residual step: ties are common.
+// e4m3 of top / 7, to nearest even, 448 at most (a NaN stays one).  Ties are common (top = 7 m with five bits in m), so the quotient
+// has to be the rounded exact one: q0 = x y with y = 1/7 rounded, its residual x - 7 q0, exact in a fused multiply-add, and q0 plus the
+// residual times y (Markstein's correction: P. W. Markstein, Computation of elementary functions on the IBM RISC System/6000 processor,
+// IBM J. Res. Dev. 34, 1990).  A test goes through every magnitude of both 16-bit types.
 __device__ __forceinline__ uint32_t scale_bits(float top) {
   float x;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(top), "f"(4096.f));
