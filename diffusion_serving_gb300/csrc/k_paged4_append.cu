@@ -5,8 +5,8 @@
 // find a group's largest magnitude, and each lane's 8 codes make one 32-bit word.  The quotient x / s decides the code, and
 // ties are common (both have few bits): x (1 / s), with 1 / s off by an ulp, is off by 2^-20, which a fused sum with 96 rounds off again (to
 // 2^-17: x / s is a tie, or 2^-13 away from one), and the sum of that with 1.5 2^23 goes to the whole number, ties to even.
-// 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 38.3 us, 4.7 TB/s; bound by the rotation's
-// and the codes' instructions.  (With a branch per component of a rotated pair, not per pair, 54 us; with a longer test of a pair, codes by
+// 8 prompts of 512 .. 1560 tokens, 32 heads over 8 of 128, queries turned beside them: 38.4 us, 4.7 TB/s; issue slots are 66 % busy with the
+// rotation and the codes, and the rest is loads waited for by the 27 warps that an SM holds at 64 registers (28 to 60 bytes spilled).  (With a branch per component of a rotated pair, not per pair, 54 us; with a longer test of a pair, codes by
 // correctly rounded quotients and no prefetch 47; with a division per scale and magnitudes one by one 40.)  A step of 32 rows: 3.1
 // us replayed.
 //

@@ -6,7 +6,8 @@
 // one record, so a tile arrives as one bulk copy per page.  Warps:
 //   consumers: sets of four, 32 slots of a tile to a warp; three sets for up to 8 query rows, else two.  They take an item's tiles in
 //     turn, or, where there are many items of few tiles, an item each
-//   the last three: producers (page numbers, copies, every other record each) and between them a helper: the next items' queries and extents
+//   behind them three producers: page numbers and copies, a tile each in turn
+//   the last: a helper, the next items' queries and extents
 //
 // At a quarter of the 16-bit store's bytes a slot, instructions bound this kernel as much as HBM does, so the slots stand in M
 // of the m16n8k16 MMAs and the up to 8 (16: two MMAs) query rows in N: an MMA takes 16 slots x 16 dims of codes, twice what it
@@ -26,12 +27,17 @@
 //
 // Measured: 32 rows of 234 .. 16384 slots, 8 kv heads of 128, 32 heads, bf16, pages of 16: 76 us, 3.8 TB/s of codes and scales,
 // 0.56 of a plain copy (the 16-bit kernel 171 us); 2 rows of 100001 and 131072 slots, pages of 64: 61 us, 4.1 TB/s.  Bound by the
-// consumers' instructions and their latency: 325 a warp for 16 slots of 128 dims, issue slots 58 % busy; of 67 us (32 rows of 8192) the
-// copies by themselves take 52, the products with K and with V 18 each, waits and work split 16.  More warps of fewer registers
+// consumers' instructions and their latency: 324 a warp for 16 slots of 128 dims, issue slots 55 to 58 % busy; of 67 us (32 rows of 8192)
+// the copies by themselves take 52, the products with K and with V 18 each, waits and work split 16.  More warps of fewer registers
 // (four sets: spills) took 94 us, fewer (two sets) 68; nine stages for six changed nothing.  One row of 490 slots: 8 us.
 // Items of few tiles cost a block their beginnings and ends, some 3.5 us one after another; in sets of their own 128 rows of 100 slots
 // take 17 us where they took 24, 512 of 300 69 for 96, 128 of 1000 45 for 51; but 128 of 2000, 16 tiles an item, 87 for 77, so it is
-// done up to a mean of 8.  (31 rows of 100 and one of 16000, whose item a set has for itself: 17 us for 16.)
+// done up to a mean of 8.  A long row among many short ones, whose parts in a block one set then has for itself, is faster for it too:
+// one of 131072 slots with 200 of 100 take 72 us (83 shared by all consumers; 36 and 23 in calls of their own), 8 of 32768 with 512 of
+// 100 147 (179), 8 of 8000 with 120 of 100 42 (47); but one of 16000 with 31 of 100 16.5 (15.6).
+// Up to 16 query rows (two tiles of 8, sets of four warps at 168 registers; heads of 128 spill 176 bytes): 4 tokens of 32 heads over 8,
+// heads of 128 and of 64, 1 row of 8000 slots 15 and 10 us, 8 of them 34 and 21, 32 of them 99 and 57 (one token: 10 and 9, 23 and 17,
+// 63 and 43); 16 heads over 1, one token: 14 and 9, 15 and 10, 22 and 15.
 #include "paged4_internal.h"
 #include "paged_finish.h"
 #include "paged_ptx.h"

@@ -17,7 +17,8 @@
 // taken 2^6 too large, so that fp16 holds them with full precision down to 2^-20 of the reference.
 //
 // Measured: chunks of 700 and 1024 tokens over 9000 and 16384 slots, causal, 32 heads over 8 kv heads of 128, bf16: 356 us, 1.03
-// PFLOP/s of visible pairs (the 16-bit kernel 288); 1560 tokens over 32760 slots, 12 heads: 342 us.  Bound by what a tile of some 2000 cycles
+// PFLOP/s of visible pairs, 352 replayed (the 16-bit kernel 286 to 292, 266 replayed); 1560 tokens over 32760 slots, 12 heads: 340 us, 330
+// replayed (the 16-bit kernel 390).  Bound by what a tile of some 2000 cycles
 // (the products' own 1024) asks of each scheduler's four warps: 1390 instructions, and of shared memory, 73 % busy: the MMAs' 96 KB,
 // 64 KB of expanded operands, 35 KB of records.  1024 tokens over 16384 slots take 262 us; without the expansion 207, without the
 // weights 211, without the products 243.  With four expanding warps 277, with sixteen (24 warps) 285, with two softmax warps to 32 rows

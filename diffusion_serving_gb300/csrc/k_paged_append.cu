@@ -9,7 +9,7 @@
 // (32 such lanes' worth of the keys' and values' heads, or of the queries') and tokens: few tokens to
 // a run, and all of them are on columns; many, and each takes every eighth token, some four in all,
 // so that a long page does not become a long chain.  One token of a warp is in flight, all its loads together, the next one's
-// on their way to L2 (eight 16-byte ones a lane, and 32 warps an SM: 5.6 TB/s for prompts, 0.83 of a copy; a decode step of 32 rows takes
+// on their way to L2 (eight 16-byte ones a lane, and 32 warps an SM: 6.4 TB/s for prompts, 0.94 of a copy; a decode step of 32 rows takes
 // 3.3 us replayed, of which the loads that wait for the page number, though only the stores need it, are a part).
 // Keys that are stored as they come (kTurn false) have instances of their own, without the rotation's registers and without the
 // prefetch, which only helps where arithmetic stands between the loads: 8 prompts of 8 heads, fp16, 7.9 us (9.2 in the instance

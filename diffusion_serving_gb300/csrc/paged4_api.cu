@@ -36,7 +36,8 @@ kvc_pg4_layout workspace_of(const kvc_paged_config& g) {
 // them, for heads of 128 or 64).  32 heads over 8, streaming and tensor-core kernel: 32 rows a group, heads of 128: 18 and 24 us
 // for a batch of 1 over 8000 slots, 21 and 29 for 8 over 2000, but 38 and 27 for 32 over 600, 183 and 165 for 32 over 8000; heads of
 // 64: 32 and 50 for 8 over 8000, 102 and 141 for 32 over 8000; 64 rows: 12 and 22 for 1 over 8000 of 64 dims, 25 and 16 for 8 over 600 of
-// 128.  Lengths are on the device: the slots are those that the table has columns for.
+// 128.  Lengths are on the device: the slots are those that the table has columns for, so with a table far wider than its rows several
+// passes are not taken (16 rows of 900 .. 9000 slots, 1 to 5 tokens, 40 heads over 8 of 64: 33 us, and 54 under a table of 131072 slots).
 bool few_rows(const kvc_pg_args& a, int head_dim) {
   const int T = 16 / a.Gv;                             // tokens to an item
   const int64_t passes = ((int64_t)a.max_q + T - 1) / T, items = a.B * (int64_t)a.Hv * passes;

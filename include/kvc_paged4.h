@@ -10,6 +10,8 @@
  *   code  c = 8 + x / s, rounded to a whole number (ties to even) and limited to 1 .. 15; 8 where s is 0.
  * The slot then holds (c - 8) s, which both 16-bit types represent exactly.  Values of up to 3136 are held within s / 2 or
  * 7 * 2^-10 of themselves, whichever is more (groups of magnitudes up to that as zeros), larger ones, infinity too, as 3136.
+ * So values should not be small: N(0, 1) keys and values, scaled down by 20 or less, are held within 10 % (rms), by 100 within 12 %,
+ * by 500 not at all.
  * A group with a NaN is held as NaN throughout.
  *
  * Store.  One pool [n_pages][Hkv] of records of page_size * (D + D / 16) bytes, each:
@@ -59,6 +61,9 @@ int kvc_paged4_read(kvc_paged4* c, void* k_out, void* v_out, int32_t n_tokens, c
 /* out = softmax(scale q k^T) v of every token over the values held of its row's slots [0, kv_len), as kvc_paged_attend
  * (with whose results over the same values it agrees but for rounding; flags: KVC_CAUSAL alone).  Slots behind a row's length
  * may hold any bits.  Weights are rounded to fp16 before their product with the values, whichever the 16-bit type.
+ *  max_q, the batch and the columns of the table choose the kernel (lengths are on the device), and with it the last bits: more than
+ *  16 query rows a group (tokens x heads / kv_heads) take the streaming kernel, in up to four passes, only where few items and the
+ *  table's slots over them make that faster; a table sized for far longer rows sends drafted tokens to the chunks' kernel.
  *  Errors: KVC_ERR_ARG, KVC_ERR_CUDA. */
 int kvc_paged4_attend(kvc_paged4* c, const void* q, void* out, float* d_lse, int32_t n_tokens, const int32_t* d_cu,
                       int32_t max_q, uint32_t flags, void* stream);
