@@ -97,7 +97,7 @@ __device__ __forceinline__ Held hold(const Vec<T>& x, const Vec<T>& y) {
 
 template <typename T, int D, int kAxes>
 __global__ void __launch_bounds__(kThreads, 4)
-k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, T* q_out, AppendArgs a) {
+k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, T* q_out, ArgsOf<T, kAxes> a) {
   constexpr int VL = 8;
   constexpr int PH = D / 2 / VL;          // vector pairs of a head
   constexpr int NX = D / 32;              // groups of a head
@@ -132,7 +132,8 @@ k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, 
   const int head = have ? col / PH : 0, c = col % PH;     // (lanes past the last head take part in the shuffles)
   const int64_t src0 = (int64_t)head * D + c * VL;
   uint8_t* rec = pool + ((int64_t)page * a.Hkv + head) * kvc_pg4_record(D, a.ps_log2);
-  const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
+  uint32_t axes = 0;
+  if constexpr (kAxes != kSlots) axes = lane_axes<T, D>(a, c, a.half);
   Places places;
   for (int p = lo + warp / gw; p < end; p += stride) {
     Vec<T> x, y, vx, vy;
@@ -147,9 +148,12 @@ k_paged4_append(const T* k, const T* v, const T* q, uint8_t* __restrict__ pool, 
       ahead(v + next);
       ahead(v + next + D / 2);
     }
-    if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;        // (the same for the whole warp)
-    if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
-    else if (a.rope != nullptr) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+    if constexpr (kAxes != kSlots) {
+      if (!places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;               // (the same for the whole warp)
+      load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
+    } else if (a.rope != nullptr) {
+      load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+    }
     vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
     vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
     if (kAxes || a.rope != nullptr) turn<T>(x, y, cs, a.half);
@@ -238,9 +242,9 @@ k_paged4_read(const uint8_t* pool, T* __restrict__ k_out, T* __restrict__ v_out,
   }
 }
 
-AppendArgs base_args(const kvc_paged4* c, int n_tokens, const int32_t* cu) {
+AxesArgs base_args(const kvc_paged4* c, int n_tokens, const int32_t* cu) {
   const kvc_paged_config& g = c->cfg;
-  AppendArgs a{};
+  AxesArgs a{};
   a.table = c->table;
   a.kv_len = c->kv_len;
   a.cu = cu;
@@ -256,7 +260,7 @@ AppendArgs base_args(const kvc_paged4* c, int n_tokens, const int32_t* cu) {
 }
 
 template <typename T, int D>
-cudaError_t launch(kvc_paged4* c, const void* k, const void* v, const void* q, void* q_out, AppendArgs a, cudaStream_t s) {
+cudaError_t launch(kvc_paged4* c, const void* k, const void* v, const void* q, void* q_out, AxesArgs a, cudaStream_t s) {
   a.kv_cols = a.Hkv * (D / 16);
   a.q_cols = q != nullptr ? a.H * (D / 16) : 0;
   a.kv_groups = (a.kv_cols + 31) / 32;
@@ -283,7 +287,7 @@ cudaError_t kvc_pg4_launch_append(kvc_paged4* c, const void* k, const void* v, i
                                   int64_t q_stride, void* q_out, int n_tokens, const int32_t* cu, const float* rope,
                                   int rope_positions, const kvc_rope_axes* axes, const int32_t* positions, bool half,
                                   cudaStream_t s) {
-  AppendArgs a = base_args(c, n_tokens, cu);
+  AxesArgs a = base_args(c, n_tokens, cu);
   a.rope = reinterpret_cast<const float2*>(rope);
   a.rope_positions = rope_positions;
   a.kv_stride = kv_stride;

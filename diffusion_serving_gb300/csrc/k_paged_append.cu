@@ -45,7 +45,7 @@ __device__ __forceinline__ __nv_bfloat16 pick_min(__nv_bfloat16 a, __nv_bfloat16
 template <typename T, int D, bool kBounds, bool kTurn, int kAxes>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __restrict__ vp,
-               T* q_out, T* __restrict__ bounds, AppendArgs a) {
+               T* q_out, T* __restrict__ bounds, ArgsOf<T, kAxes> a) {
   constexpr int VL = Vec<T>::N;
   constexpr int PH = D / 2 / VL;          // vector pairs of a head
   __shared__ uint4 s_red[kBounds ? kWarps : 1][4][32];
@@ -82,7 +82,8 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
   Vec<T> mx0, mx1, mn0, mn1;
   bool any = false;
   if (kAxes ? group < a.kv_groups : have) {         // (with axes a warp stays whole; those of queries alone leave the keys out)
-    const uint32_t axes = kAxes ? lane_axes<T, D>(a, c, a.half) : 0;
+    uint32_t axes = 0;
+    if constexpr (kAxes != kSlots) axes = lane_axes<T, D>(a, c, a.half);
     Places places;
     for (int p = lo + warp / gw; p < end; p += stride) {
       Vec<T> x, y, vx, vy;
@@ -97,10 +98,13 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
         ahead(v + next);
         ahead(v + next + D / 2);
       }
-      if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
-      if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
-      else if (kTurn) load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
-      if (kAxes && !have) continue;
+      if constexpr (kAxes != kSlots) {
+        if (!places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
+        load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, c, a.half);
+        if (!have) continue;
+      } else if (kTurn) {
+        load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), c, a.half);
+      }
       vx.u = pg_ld(reinterpret_cast<const uint4*>(v + off));
       vy.u = pg_ld(reinterpret_cast<const uint4*>(v + off + D / 2));
       const int64_t dst = (((int64_t)page << a.ps_log2) + (p & (ps - 1))) * dst_row + src0;
@@ -174,7 +178,7 @@ k_paged_append(const T* k, const T* v, const T* q, T* __restrict__ kp, T* __rest
 }
 
 template <typename T, int D>
-cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, void* q_out, AppendArgs a,
+cudaError_t launch(kvc_paged* c, const void* k, const void* v, const void* q, void* q_out, AxesArgs a,
                    cudaStream_t s) {
   constexpr int VL = Vec<T>::N;
   a.kv_cols = a.Hkv * (D / 2 / VL);
@@ -202,7 +206,7 @@ cudaError_t kvc_pg_launch_append(kvc_paged* c, const void* k, const void* v, int
                                  int rope_positions, const kvc_rope_axes* axes, const int32_t* positions, bool half,
                                  cudaStream_t s) {
   const kvc_paged_config& g = c->cfg;
-  AppendArgs a{};
+  AxesArgs a{};
   a.table = c->table;
   a.kv_len = c->kv_len;
   a.cu = cu;

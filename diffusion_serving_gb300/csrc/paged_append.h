@@ -5,6 +5,8 @@
 #include "paged_internal.h"
 #include "paged_rope.h"
 
+#include <type_traits>
+
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
@@ -37,10 +39,21 @@ struct AppendArgs {
   int kv_groups;              // column groups of the keys; those of the queries follow
   int H, Hkv;
   int half;
-  const int32_t* pos;         // [n_tokens][n_axes], with axes
+};
+// With positions of several axes.
+struct AxesArgs : AppendArgs {
+  const int32_t* pos;         // [n_tokens][n_axes]; null: slots are the positions
   int n_axes;
   uint32_t pair_axis[4];      // two bits a pair
 };
+// How positions are given: slots; several axes, with each lane's VL / 2 pairs of a vector on one of them (kFlat: sections side by
+// side); several axes in any order.
+enum { kSlots = 0, kFlat = 1, kAny = 2 };
+// What a kernel is told.  Launch parameters that it has no use for cost an fp32 step of 32 rows 0.1 us (2.64 and 2.76 us replayed, with
+// bounds 3.15 and 3.28) and 8 prompts 1 %.  16-bit rotations are short of registers and get them all the same: with fewer parameters the
+// compiler keeps more of them in registers and spills 12 to 24 bytes more (8 prompts into 4 bits 79.9 and 81.5 us, 40 heads, a step 3.2 and 3.0).
+template <typename T, int kAxes>
+using ArgsOf = std::conditional_t<kAxes != kSlots || sizeof(T) == 2, AxesArgs, AppendArgs>;
 
 // Turns the two vectors x (elements c VL ..) and y (D/2 further) of a head by the row `cs` of the table.
 template <typename T>
@@ -66,7 +79,7 @@ struct Places {
   __device__ __forceinline__ Places() : v(0), i(-1), bad(0) {}
   // The next token's, `token` of the call; its warp's others follow it `stride` apart and end before `end`.  A whole warp calls it;
   // false, and the error bit, if one is outside the table.
-  __device__ __forceinline__ bool next(const AppendArgs& a, int token, int stride, int end) {
+  __device__ __forceinline__ bool next(const AxesArgs& a, int token, int stride, int end) {
     const int lane = threadIdx.x & 31;
     if ((++i & 7) == 0) {
       const int t = token + (lane >> 2) * stride;
@@ -80,12 +93,9 @@ struct Places {
   // The token's position on an axis of the lane's own.
   __device__ __forceinline__ int of(int axis) const { return __shfl_sync(0xffffffffu, v, 4 * (i & 7) + axis); }
 };
-// How positions are given: slots; several axes, with each lane's VL / 2 pairs of a vector on one of them (kFlat: sections side by
-// side); several axes in any order.
-enum { kSlots = 0, kFlat = 1, kAny = 2 };
 // The axes of a lane's pairs, two bits each: VL / 2 pairs from `first`, for both w.
 template <typename T, int D>
-__device__ __forceinline__ uint32_t lane_axes(const AppendArgs& a, int c, bool half) {
+__device__ __forceinline__ uint32_t lane_axes(const AxesArgs& a, int c, bool half) {
   constexpr int VL = Vec<T>::N;
   uint32_t bits = 0;
 #pragma unroll
@@ -219,7 +229,7 @@ __device__ __forceinline__ bool find_run(const AppendArgs& a, int& b, int& j) {
 
 // Column group `group` of the queries of tokens at slots [p, end), every `stride`th.
 template <typename T, int D, int kAxes>
-__device__ __forceinline__ void append_queries(const AppendArgs& a, const Row& r, const T* q, T* q_out, int group, int p, int end,
+__device__ __forceinline__ void append_queries(const ArgsOf<T, kAxes>& a, const Row& r, const T* q, T* q_out, int group, int p, int end,
                                                int stride, int p0) {
   constexpr int VL = Vec<T>::N;
   constexpr int PH = D / 2 / VL;          // vector pairs of a head
@@ -227,7 +237,8 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const Row& r
   const bool have = col < a.q_cols;
   if (!kAxes && !have) return;            // (with axes a warp stays whole)
   const int64_t off = (int64_t)(col / PH) * D + (col % PH) * VL;
-  const uint32_t axes = kAxes ? lane_axes<T, D>(a, col % PH, a.half) : 0;
+  uint32_t axes = 0;
+  if constexpr (kAxes != kSlots) axes = lane_axes<T, D>(a, col % PH, a.half);
   Places places;
   for (; p < end; p += stride) {
     Vec<T> x, y;
@@ -241,10 +252,13 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, const Row& r
         ahead(src + stride * a.q_stride + D / 2);
       }
     }
-    if (kAxes && !places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
-    if (kAxes) load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, col % PH, a.half);
-    else load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), col % PH, a.half);
-    if (kAxes && !have) continue;
+    if constexpr (kAxes != kSlots) {
+      if (!places.next(a, r.t0 + p - p0, stride, r.t0 + end - p0)) continue;
+      load_turn_axes<T, D, kAxes>(cs, a.rope, places, axes, col % PH, a.half);
+      if (!have) continue;
+    } else {
+      load_turn<T, D>(cs, a.rope + (int64_t)p * (D / 2), col % PH, a.half);
+    }
     turn<T>(x, y, cs, a.half);
     T* dst = q_out + (int64_t)(r.t0 + p - p0) * a.H * D + off;
     *reinterpret_cast<uint4*>(dst) = x.u;
@@ -264,13 +278,13 @@ inline dim3 run_grid(AppendArgs& a, int groups) {
                                        : (int64_t)a.n_tokens / ps + 2 * (int64_t)a.B;
   return dim3((unsigned)runs, gy);
 }
-inline void set_axes(AppendArgs& a, const kvc_rope_axes& axes, const int32_t* positions, int head_dim) {
+inline void set_axes(AxesArgs& a, const kvc_rope_axes& axes, const int32_t* positions, int head_dim) {
   a.pos = positions;
   a.n_axes = axes.n_axes;
   for (int j = 0; j < head_dim / 2; ++j) a.pair_axis[j >> 4] |= (uint32_t)axes.pair_axis[j] << (2 * (j & 15));
 }
 // The kind of an append: kSlots, kFlat or kAny, for vectors of `vl` elements.
-inline int axes_kind(const AppendArgs& a, int head_dim, int vl) {
+inline int axes_kind(const AxesArgs& a, int head_dim, int vl) {
   if (a.pos == nullptr) return kSlots;
   auto axis = [&](int j) { return a.pair_axis[j >> 4] >> (2 * (j & 15)) & 3; };
   for (int j = 0; j < head_dim / 2; ++j)
